@@ -1,7 +1,7 @@
 /*
  * i2s.h - C ABI of libi2s.so: the I2_S ternary-weight x INT8-activation
- * matmul and the I8_S x I8_S fused mul_mat_add(_relu), on NVIDIA GB300
- * (sm_103a).
+ * matmul and the I8_S x I8_S fused mul_mat_add(_relu), with the 8-bit KV cache
+ * and the attention over it, on NVIDIA GB300 (sm_103a).
  *
  * Sources, cited by page title and section:
  *   [P1] "ggml: additive INT8/ternary types, fused CPU ops, and kernels for
@@ -569,6 +569,159 @@ typedef struct w8a8_problem {
 size_t w8a8_mul_mat_grouped_workspace(const w8a8_problem* probs, int count, int64_t M);
 int w8a8_mul_mat_grouped(const w8a8_problem* probs, int count, int64_t M, void* ws, size_t ws_bytes,
                          i2s_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * 8-bit KV cache: the operators between a decoder's q/k/v projections and its
+ * output projection. Keys and values are held as int8 codes with one F32 scale
+ * for each block of KV8_BLOCK tokens and head; kv8_norm_rope prepares queries
+ * and keys, kv8_write quantizes tokens into the cache, kv8_read gives them
+ * back, kv8_attention attends over them.
+ *
+ * Cache. A pool of n_pages pages of page_tokens tokens (16, 32, 64, 128 or
+ * 256), kv8_page_bytes() each. A page is `heads` slabs, one per KV head, of
+ *   page_tokens x head_dim int8 K codes (token-major),
+ *   page_tokens x head_dim int8 V codes,
+ *   page_tokens/16 F32 K scales, page_tokens/16 F32 V scales,
+ *   zero to 31 bytes up to a multiple of 32 (never read or written).
+ * A value is code * scale. Token t of a sequence lies in the page
+ * page_table[s*table_width + t/page_tokens], at token t % page_tokens. No code
+ * or scale of a token at or past a sequence's length is ever used, so a pool
+ * needs no clearing.
+ *
+ * Batch. `rows` rows of new tokens, sequence by sequence: sequence s has the
+ * n = row_start[s+1] - row_start[s] rows from row_start[s], n >= 0, and row i
+ * of them is the token at position kv_len[s] - n + i, so kv_len[s] counts the
+ * batch's own tokens. Rows at and past row_start[seqs] belong to no sequence:
+ * no operator reads them or writes their outputs.
+ * row_start (seqs + 1), kv_len (seqs) and page_table are device int32, read by
+ * the kernels, so a captured graph may be replayed after they change. The
+ * kernels check them: a row_start that decreases or leaves [0, rows], a
+ * sequence of more than max_rows rows, a kv_len below zero or past
+ * table_width*page_tokens, and a page outside [0, n_pages) set a bit of *status
+ * (device int32, KV8_BAD_*; set, never cleared) and the rows, lengths or
+ * tokens concerned are cut to what is valid, so nothing outside the pool, the
+ * table or the row tensors is touched. kv8_read_status reports the word.
+ * Sequences may share pages that they only read; a block that a kv8_write
+ * writes must belong to one sequence of its batch.
+ *
+ * Row tensors. kv8_rows: element (row, head, d) at data[row*row_stride +
+ * head*head_stride + d], strides in elements, of KV8_F32, KV8_F16 or KV8_BF16;
+ * data 16-byte aligned and both strides a multiple of 16 bytes (so a slice of
+ * a fused q/k/v projection works). Strides are not negative, and an output's
+ * elements are distinct.
+ *
+ * Limits: head_dim 64 or 128, 1 <= heads <= 1024, 1 <= seqs <= KV8_MAX_SEQS,
+ * 1 <= max_rows <= rows < 2^31, table_width*page_tokens < 2^31. Errors of every
+ * call: BAD_SHAPE, NULL_PTR, MISALIGNED, BAD_ARG (an unknown dtype or flag, or
+ * an output that overlaps another operand), UNSUPPORTED_DEVICE, CUDA.
+ * ------------------------------------------------------------------------- */
+#define KV8_BLOCK 16
+#define KV8_MAX_SEQS 4096
+enum { KV8_F32 = 0, KV8_F16 = 1, KV8_BF16 = 2 };
+enum {                      /* bits of kv8_batch::status */
+    KV8_TIMEOUT = 1,        /* a kernel gave up a bounded wait */
+    KV8_BAD_ROWS = 2,
+    KV8_BAD_LENGTH = 4,
+    KV8_BAD_PAGE = 8
+};
+
+typedef struct kv8_cache {
+    void* pages;            /* device, n_pages * kv8_page_bytes() bytes, 16-byte aligned */
+    int64_t n_pages;
+    int heads;              /* KV heads */
+    int head_dim;
+    int page_tokens;
+} kv8_cache;
+
+typedef struct kv8_batch {
+    const int32_t* row_start;
+    const int32_t* kv_len;
+    const int32_t* page_table;
+    int32_t* status;
+    int64_t rows;           /* rows of the row tensors */
+    int64_t table_width;    /* entries of page_table per sequence */
+    int seqs;
+    int max_rows;           /* host bound on the rows of one sequence */
+} kv8_batch;
+
+typedef struct kv8_rows {
+    void* data;
+    int64_t row_stride;
+    int64_t head_stride;
+    int dtype;
+} kv8_rows;
+
+/* Host only; 0 for invalid sizes. */
+size_t kv8_page_bytes(int heads, int head_dim, int page_tokens);
+
+/* Quantizes the batch's keys and values (rows x cache->heads x head_dim) into
+ * the cache. A block's scale is max(amax, 1e-5)/127 over its values of this
+ * batch; if the block holds older tokens of the sequence (a position before
+ * the batch's first), the larger of that and the scale it has, and if that
+ * grows, the older codes are requantized from their values code*scale. A code
+ * is clamp(round(x * (1/scale)), -127, 127), halfway cases away from zero, each
+ * step one binary32 operation. An infinity or NaN among the values makes the
+ * block's scale NaN and its new codes zero: it reads back as NaN, and stays so
+ * until the block is written from its first token. Tokens at negative
+ * positions (n > kv_len) are skipped (KV8_BAD_LENGTH), as are those of a bad page.
+ * k and v have the same dtype. Writing the same tokens again changes nothing. */
+int kv8_write(const kv8_cache* cache, const kv8_batch* batch, const kv8_rows* k, const kv8_rows* v,
+              i2s_stream_t stream);
+
+/* The values code*scale of the batch's tokens (the last n of each sequence,
+ * n = kv_len for all of it) into k and v, rounded once to their dtype. Rows of
+ * negative positions and of bad pages are left as they were. */
+int kv8_read(const kv8_cache* cache, const kv8_batch* batch, const kv8_rows* k, const kv8_rows* v,
+             i2s_stream_t stream);
+
+/* RMS norm of each head of the queries and keys, and the position rotation, in
+ * one pass: y = x * (1/sqrt(mean(x^2) + eps)) * gamma[d] (gamma_q, gamma_k:
+ * device F32 [head_dim], or NULL for no norm of that tensor), then pair i of
+ * the first rot_dim values turns by the angle 2*pi*frac(position * turns[i] /
+ * 2^64): (a, b) -> (a cos - b sin, b cos + a sin). Pairs are (i, i + rot_dim/2),
+ * or with KV8_PAIRS_NEXT (2i, 2i + 1). The product is taken modulo 2^64, so the
+ * angle of a far position loses nothing; sums are binary32, one rounding to
+ * the dtype at the end.
+ * turns      device uint64 [rot_dim/2]; kv8_rope_turns_host fills base^(-2i/rot_dim)
+ *            radians per position, other frequency schemes fill their own.
+ * positions  device int32 [rows], any value. Every one of the `rows` rows is read
+ *            and written.
+ * q, k       inputs; q_heads or k_heads may be 0 (that tensor's arguments are
+ *            then ignored). Outputs may be the inputs themselves, both in
+ *            place, or else overlap no operand. All four have one dtype.
+ * rot_dim    a multiple of 8, 0 (no rotation; turns and positions unused) to head_dim.
+ * eps >= 0; with eps = 0 an all-zero head is undefined (0 * inf). */
+#define KV8_PAIRS_NEXT 1u
+int kv8_rope_turns_host(double base, int rot_dim, uint64_t* turns);
+int kv8_norm_rope(const kv8_rows* q, const kv8_rows* q_out, int q_heads, const float* gamma_q, const kv8_rows* k,
+                  const kv8_rows* k_out, int k_heads, const float* gamma_k, int64_t rows, int head_dim, float eps,
+                  const int32_t* positions, const uint64_t* turns, int rot_dim, unsigned flags, i2s_stream_t stream);
+
+/* Attention of the batch's queries over the cache: for query row i of sequence
+ * s and head h, out = sum_j p_j V_j with p = softmax_j(softmax_scale * q . K_j)
+ * over the sequence's tokens j < kv_len[s], of KV head h / (q_heads / heads).
+ * With KV8_CAUSAL only j <= the row's position, and with window > 0 (KV8_CAUSAL
+ * only) j > position - window. A row that sees no token has a zero output.
+ * Softmax statistics and sums are binary32; F32 queries and probabilities
+ * enter the tensor cores as two f16 parts each, 16-bit ones as one.
+ * q, out    rows x q_heads x head_dim, one dtype; q_heads a multiple of
+ *           cache->heads, at most 64 times it. out overlaps no other operand.
+ * lse       device F32 [rows x q_heads] or NULL: log(sum_j exp(softmax_scale *
+ *           q . K_j)), -infinity for a row that sees no token.
+ * ws        device workspace of at least kv8_attention_workspace() bytes, 256-byte
+ *           aligned, not preserved; calls sharing one are ordered on one stream.
+ * More errors: WORKSPACE_TOO_SMALL, BAD_ARG for a window without KV8_CAUSAL or
+ * a softmax_scale that is not finite. */
+#define KV8_CAUSAL 1u
+size_t kv8_attention_workspace(const kv8_cache* cache, const kv8_batch* batch, int q_heads);
+int kv8_attention(const kv8_cache* cache, const kv8_batch* batch, const kv8_rows* q, int q_heads, const kv8_rows* out,
+                  float softmax_scale, unsigned flags, int window, float* lse, void* ws, size_t ws_bytes,
+                  i2s_stream_t stream);
+
+/* Synchronizes `stream`, reads and clears a batch's status word, and returns
+ * I2S_OK, I2S_E_DEVICE_TIMEOUT (KV8_TIMEOUT) or I2S_E_BAD_ARG (another bit);
+ * *bits, if not NULL, gets the word. Errors: NULL_PTR, CUDA. */
+int kv8_read_status(int32_t* status, int32_t* bits, i2s_stream_t stream);
 
 /* ---------------------------------------------------------------------------
  * Device status. Kernels with bounded waits (the tensor-core pipelines) never

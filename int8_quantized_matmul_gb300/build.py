@@ -2,7 +2,7 @@
 
 Each translation unit under csrc/ is compiled by nvcc in parallel, then linked
 into int8_quantized_matmul_gb300/_lib/libi2s.so with the CUDA runtime linked
-statically and only the i2s_* / i8s_* symbols exported (so the library's own
+statically and only the i2s_* / i8s_* / w8a8_* / kv8_* symbols exported (so the library's own
 runtime never interposes on another copy loaded in the same process).
 """
 
@@ -20,7 +20,7 @@ LIB = os.path.join(LIBDIR, "libi2s.so")
 BUILD = os.path.join(HERE, "_build")
 
 SOURCES = ["abi.cu", "quant.cu", "gemv_tc.cu", "gemm_tc.cu", "i8s.cu", "i8s_tc.cu", "i8s_elt.cu",
-           "noalloc.cu"]
+           "noalloc.cu", "kv8.cu", "kv8_attn.cu"]
 NVCC = os.environ.get("NVCC", "nvcc")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-fmad=false", "-Xcompiler", "-fPIC,-fvisibility=hidden",

@@ -90,6 +90,8 @@ bool i2s_shape_ok(int64_t N, int64_t K, int64_t M) {
 
 }  // namespace
 
+int check_current_device() { return check_device(); }
+
 int device_sm_count() {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 152;

@@ -298,5 +298,6 @@ cudaError_t launch_requant(const float* y, int64_t n, const unsigned int* amax_b
                            cudaStream_t s);
 
 int device_sm_count();
+int check_current_device();   // I2S_OK if the current device is sm_103, else a status
 
 }  // namespace i2s

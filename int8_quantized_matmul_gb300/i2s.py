@@ -47,6 +47,21 @@ class w8a8_problem(ctypes.Structure):
     _fields_ = [("packed", _p), ("bscale", _p), ("N", _i64), ("K", _i64), ("x", _p), ("d", _p)]
 
 
+class kv8_cache(ctypes.Structure):
+    _fields_ = [("pages", _p), ("n_pages", _i64), ("heads", _int), ("head_dim", _int), ("page_tokens", _int)]
+
+
+class kv8_batch(ctypes.Structure):
+    _fields_ = [("row_start", _p), ("kv_len", _p), ("page_table", _p), ("status", _p), ("rows", _i64),
+                ("table_width", _i64), ("seqs", _int), ("max_rows", _int)]
+
+
+class kv8_rows(ctypes.Structure):
+    _fields_ = [("data", _p), ("row_stride", _i64), ("head_stride", _i64), ("dtype", _int)]
+
+
+_cache_p, _batch_p, _rows_p = (ctypes.POINTER(t) for t in (kv8_cache, kv8_batch, kv8_rows))
+
 _SIGS = {
     "i2s_status_string": (ctypes.c_char_p, [_int]),
     "i2s_version": (_int, []),
@@ -102,6 +117,15 @@ _SIGS = {
     "w8a8_mul_mat_packed": (_int, [_p, _p, _i64, _i64, _p, _i64, _p, _p, _sz, _p]),
     "w8a8_mul_mat_grouped_workspace": (_sz, [ctypes.POINTER(w8a8_problem), _int, _i64]),
     "w8a8_mul_mat_grouped": (_int, [ctypes.POINTER(w8a8_problem), _int, _i64, _p, _sz, _p]),
+    "kv8_page_bytes": (_sz, [_int, _int, _int]),
+    "kv8_write": (_int, [_cache_p, _batch_p, _rows_p, _rows_p, _p]),
+    "kv8_read": (_int, [_cache_p, _batch_p, _rows_p, _rows_p, _p]),
+    "kv8_rope_turns_host": (_int, [ctypes.c_double, _int, _p]),
+    "kv8_norm_rope": (_int, [_rows_p, _rows_p, _int, _p, _rows_p, _rows_p, _int, _p, _i64, _int, _f32, _p, _p, _int,
+                             ctypes.c_uint, _p]),
+    "kv8_attention_workspace": (_sz, [_cache_p, _batch_p, _int]),
+    "kv8_attention": (_int, [_cache_p, _batch_p, _rows_p, _int, _rows_p, _f32, ctypes.c_uint, _int, _p, _p, _sz, _p]),
+    "kv8_read_status": (_int, [_p, ctypes.POINTER(ctypes.c_int32), _p]),
 }
 for _name, (_res, _args) in _SIGS.items():
     _fn = getattr(_L, _name)
@@ -636,6 +660,229 @@ class W8A8Group:
     def __call__(self):
         _check("w8a8_mul_mat_grouped", _L.w8a8_mul_mat_grouped(self._arr, len(self.problems), self.M,
                                                                _dptr(self.ws), self.ws.numel(), _stream()))
+
+
+# -- 8-bit KV cache ---------------------------------------------------------------
+
+KV8_BLOCK = 16
+KV8_MAX_SEQS = 4096
+KV8_CAUSAL = 1
+KV8_PAIRS_NEXT = 1
+KV8_TIMEOUT, KV8_BAD_ROWS, KV8_BAD_LENGTH, KV8_BAD_PAGE = 1, 2, 4, 8
+
+
+def kv8_page_bytes(heads: int, head_dim: int, page_tokens: int) -> int:
+    return int(_L.kv8_page_bytes(heads, head_dim, page_tokens))
+
+
+def _kv8_rows(t):
+    """kv8_rows of a rows x heads x head_dim CUDA tensor, whose last dimension
+    is contiguous (the others may be strided, as slices of a fused projection are)."""
+    torch = _torch()
+    dtypes = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
+    if not t.is_cuda:
+        raise ValueError("expected a CUDA tensor")
+    if t.dim() != 3 or t.stride(2) != 1:
+        raise ValueError("expected rows x heads x head_dim with contiguous values")
+    if t.dtype not in dtypes:
+        raise ValueError(f"expected float32, float16 or bfloat16, got {t.dtype}")
+    return kv8_rows(t.data_ptr(), t.stride(0), t.stride(1), dtypes[t.dtype])
+
+
+def _kv8_same(cache, t, rows, heads, what):
+    if tuple(t.shape) != (rows, heads, cache.head_dim):
+        raise ValueError(f"{what}: expected shape {(rows, heads, cache.head_dim)}, got {tuple(t.shape)}")
+    if t.device != cache.device:
+        raise ValueError(f"{what}: on {t.device}, the cache is on {cache.device}")
+    return _kv8_rows(t)
+
+
+class _Kv8Call:
+    """A call marshalled once, for repeated use and CUDA graph capture. It runs
+    on torch's current stream of its tensors' device, which has to be the
+    current device. Its tensors are kept alive, not copied."""
+
+    def _bind(self, name, device, *args):
+        self._name, self._fn, self._args, self._index = name, getattr(_L, name), args, device.index
+        self._cuda = _torch().cuda
+
+    def __call__(self):
+        if self._cuda.current_device() != self._index:
+            raise ValueError(f"{self._name}: its tensors are on cuda:{self._index}, not on the current device")
+        rc = self._fn(*self._args, self._cuda.current_stream().cuda_stream)
+        if rc != 0:
+            raise I2SError(self._name, rc)
+
+
+class Kv8Cache:
+    """A pool of n_pages pages of an 8-bit KV cache; `data` is its uint8 device
+    tensor of n_pages x kv8_page_bytes (one is made if not given; it needs no
+    clearing)."""
+
+    def __init__(self, n_pages: int, heads: int, head_dim: int, page_tokens: int, data=None, device="cuda"):
+        nbytes = kv8_page_bytes(heads, head_dim, page_tokens)
+        if nbytes == 0 or n_pages < 1:
+            raise I2SError("kv8_page_bytes", -1)
+        torch = _torch()
+        if data is None:
+            data = torch.empty((n_pages, nbytes), dtype=torch.uint8, device=device)
+        if data.dtype != torch.uint8 or data.numel() < n_pages * nbytes:
+            raise ValueError(f"expected {n_pages * nbytes} bytes of uint8")
+        self.data, self.n_pages, self.heads, self.head_dim = data, n_pages, heads, head_dim
+        self.page_tokens, self.device = page_tokens, data.device
+        self.struct = kv8_cache(_dptr(data), n_pages, heads, head_dim, page_tokens)
+
+
+class Kv8Batch:
+    """Which rows belong to which sequence, and where its tokens lie: row_start
+    (seqs + 1), kv_len (seqs) and page_table (seqs x table_width), int32 device
+    tensors whose values may change between calls. rows: rows of the row
+    tensors; max_rows: a bound on the rows of one sequence (default: rows).
+    status() is the kernels' word (KV8_BAD_*), cleared by reading it; check()
+    raises if it is not zero."""
+
+    def __init__(self, row_start, kv_len, page_table, rows: int, max_rows=None):
+        torch = _torch()
+        if page_table.dim() != 2:
+            raise ValueError("page_table: expected seqs x table_width")
+        seqs, width = page_table.shape
+        for name, t, n in (("row_start", row_start, seqs + 1), ("kv_len", kv_len, seqs),
+                           ("page_table", page_table, seqs * width)):
+            if t.dtype != torch.int32 or t.numel() != n or t.device != page_table.device:
+                raise ValueError(f"{name}: expected {n} int32 values on {page_table.device}")
+        self.row_start, self.kv_len, self.page_table = row_start, kv_len, page_table
+        self.seqs, self.rows, self.device = seqs, int(rows), page_table.device
+        self.max_rows = int(max_rows if max_rows is not None else rows)
+        self.word = torch.zeros(1, dtype=torch.int32, device=page_table.device)
+        self.struct = kv8_batch(_dptr(row_start), _dptr(kv_len), _dptr(page_table), _dptr(self.word), self.rows, width,
+                                seqs, self.max_rows)
+
+    def _read(self):
+        bits = ctypes.c_int32(0)
+        return int(_L.kv8_read_status(_dptr(self.word), ctypes.byref(bits), _stream())), bits.value
+
+    def status(self) -> int:
+        rc, bits = self._read()
+        if rc == -5:
+            raise I2SError("kv8_read_status", rc)
+        return bits
+
+    def check(self):
+        _check("kv8_read_status", self._read()[0])
+
+
+class Kv8Write(_Kv8Call):
+    """kv8_write of k and v (rows x heads x head_dim) into the cache."""
+
+    def __init__(self, cache, batch, k, v):
+        self._keep = (cache, batch, k, v)
+        kr, vr = (_kv8_same(cache, t, batch.rows, cache.heads, name) for name, t in (("k", k), ("v", v)))
+        self._bind("kv8_write", cache.device, cache.struct, batch.struct, kr, vr)
+
+
+class Kv8Read(_Kv8Call):
+    """kv8_read of the batch's tokens into k and v (rows x heads x head_dim)."""
+
+    def __init__(self, cache, batch, k, v):
+        self._keep = (cache, batch, k, v)
+        kr, vr = (_kv8_same(cache, t, batch.rows, cache.heads, name) for name, t in (("k", k), ("v", v)))
+        self._bind("kv8_read", cache.device, cache.struct, batch.struct, kr, vr)
+
+
+class Kv8NormRope(_Kv8Call):
+    """kv8_norm_rope of q and k (rows x heads x head_dim; one may be None) into
+    q_out and k_out (new contiguous tensors if not given; the inputs themselves
+    for in place). turns: int64 device tensor of rot_dim/2 (kv8_rope_turns), or
+    None for no rotation."""
+
+    def __init__(self, q, k, positions=None, turns=None, gamma_q=None, gamma_k=None, eps: float = 1e-6,
+                 interleaved: bool = False, q_out=None, k_out=None):
+        torch = _torch()
+        some = q if q is not None else k
+        rows, _, dim = some.shape
+        outs = []
+        for t, o in ((q, q_out), (k, k_out)):
+            if t is not None and o is None:
+                o = torch.empty(tuple(t.shape), dtype=t.dtype, device=t.device)
+            if t is not None and (t.shape[0] != rows or t.shape[2] != dim or t.device != some.device or
+                                  o.shape != t.shape or o.device != t.device):
+                raise ValueError("q, k and their outputs have the same rows, head_dim and device")
+            outs.append(o)
+        self.q_out, self.k_out = outs
+        for name, t, dtype, n in (("gamma_q", gamma_q, torch.float32, dim), ("gamma_k", gamma_k, torch.float32, dim),
+                                  ("positions", positions, torch.int32, rows), ("turns", turns, torch.int64, None)):
+            if t is not None and (t.dtype != dtype or t.device != some.device or n not in (None, t.numel())):
+                raise ValueError(f"{name}: expected {n if n is not None else 'rot_dim/2'} values of {dtype} on {some.device}")
+        if turns is not None and positions is None:
+            raise ValueError("a rotation needs positions")
+        self._keep = (q, k, positions, turns, gamma_q, gamma_k)
+        parts = []
+        for t, o, g in ((q, self.q_out, gamma_q), (k, self.k_out, gamma_k)):
+            parts += [None, None, 0, None] if t is None else [_kv8_rows(t), _kv8_rows(o), t.shape[1], _dptr(g)]
+        self._bind("kv8_norm_rope", some.device, *parts, rows, dim, float(eps), _dptr(positions), _dptr(turns),
+                   0 if turns is None else 2 * turns.numel(), KV8_PAIRS_NEXT if interleaved else 0)
+
+
+class Kv8Attention(_Kv8Call):
+    """kv8_attention of q (rows x q_heads x head_dim) over the cache into out (a
+    new tensor if not given); scale defaults to head_dim**-0.5. lse: an F32 rows x
+    q_heads tensor, or None."""
+
+    def __init__(self, cache, batch, q, out=None, scale=None, causal: bool = True, window: int = 0, lse=None, ws=None):
+        torch = _torch()
+        heads = q.shape[1]
+        if out is None:
+            out = torch.empty(tuple(q.shape), dtype=q.dtype, device=q.device)
+        qr, orows = (_kv8_same(cache, t, batch.rows, heads, name) for name, t in (("q", q), ("out", out)))
+        if lse is not None and (lse.dtype != torch.float32 or tuple(lse.shape) != (batch.rows, heads) or
+                                lse.device != cache.device):
+            raise ValueError(f"lse: expected float32 {(batch.rows, heads)} on {cache.device}")
+        need = int(_L.kv8_attention_workspace(cache.struct, batch.struct, heads))
+        if need == 0:
+            raise I2SError("kv8_attention_workspace", -1)
+        self.out, self.lse, self.ws = out, lse, ws if ws is not None else _ws(need, cache.device)
+        self._keep = (cache, batch, q)
+        self._bind("kv8_attention", cache.device, cache.struct, batch.struct, qr, heads, orows,
+                   float(scale if scale is not None else cache.head_dim ** -0.5), KV8_CAUSAL if causal else 0,
+                   int(window), _dptr(lse), _dptr(self.ws), self.ws.numel())
+
+
+def kv8_write(cache, batch, k, v):
+    """Quantizes the batch's keys and values into the cache."""
+    Kv8Write(cache, batch, k, v)()
+
+
+def kv8_read(cache, batch, k=None, v=None, dtype=None):
+    """The values of the batch's tokens: (k, v), rows x heads x head_dim."""
+    torch = _torch()
+    shape = (batch.rows, cache.heads, cache.head_dim)
+    if k is None:
+        k = torch.empty(shape, dtype=dtype or torch.float32, device=cache.device)
+    if v is None:
+        v = torch.empty(shape, dtype=dtype or torch.float32, device=cache.device)
+    Kv8Read(cache, batch, k, v)()
+    return k, v
+
+
+def kv8_rope_turns(base: float, rot_dim: int, device="cuda"):
+    """int64 device tensor of rot_dim/2: base^(-2i/rot_dim) radians per position, in 2^-64 turns."""
+    turns = np.zeros(max(rot_dim // 2, 1), dtype=np.uint64)
+    _check("kv8_rope_turns_host", _L.kv8_rope_turns_host(float(base), rot_dim, turns.ctypes.data))
+    return _torch().from_numpy(turns.view(np.int64)).to(device)
+
+
+def kv8_norm_rope(q, k, positions=None, turns=None, **kw):
+    """(q, k) normed and rotated; arguments as Kv8NormRope."""
+    call = Kv8NormRope(q, k, positions, turns, **kw)
+    call()
+    return call.q_out, call.k_out
+
+
+def kv8_attention(cache, batch, q, **kw):
+    """Attention of q over the cache; arguments as Kv8Attention."""
+    call = Kv8Attention(cache, batch, q, **kw)
+    call()
+    return call.out
 
 
 def read_status(ws) -> int:

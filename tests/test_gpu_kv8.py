@@ -1,0 +1,518 @@
+"""The 8-bit KV cache operators on the GPU against their definitions.
+
+kv8_write and kv8_read are defined step by step in binary32, so pools and values
+are compared bit for bit. kv8_norm_rope and kv8_attention are compared with 64
+bits, within bounds from the number of roundings:
+
+norm and rotation: the square sum of up to 128 terms (8 sequential additions of
+  one lane's terms and of the 5 exchanges: relative 10 * 2^-24), the mean, eps,
+  root, reciprocal and two products (7 more roundings), cosine and sine (their
+  argument and the function: within 2^-22), two products and one sum: together
+  below 2^-19 of the larger of a pair's values; plus half a step of the dtype.
+attention: with A the largest sum |q||k| * scale that the row sees, a logit is
+  within A * 2^-18 (two f16 parts of q and up to 16 tensor-core steps of 2^-22
+  each, then the scales), its exponential within 2^-18 * (A + 1) of itself, the
+  sums over n tokens within (n/16 + 16) * 2^-22; twice that for the quotient.
+  Probabilities of 16-bit rows are rounded to f16, 2^-12 relative, or absolutely
+  2^-25 of the largest of the row's running tile, both below 2^-11 of
+  sum p|v| with the largest |v|; plus half a step of the dtype.
+"""
+
+import numpy as np
+import pytest
+
+from tests import kv8_reference as ref
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+DTYPES = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
+ALL = ["f32", "f16", "bf16"]
+
+
+@pytest.fixture(scope="module")
+def i2s():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from int8_quantized_matmul_gb300 import build as libbuild
+    libbuild.build()
+    from int8_quantized_matmul_gb300 import i2s as mod
+    assert mod.device_supported() == 1
+    return mod
+
+
+class Setup:
+    """A pool in use, with garbage wherever no token lies, and a batch over it."""
+
+    def __init__(self, i2s, kv, dim, page, lens, news, seed=0, pad_rows=0, max_rows=None, extra_width=0, first_page=0):
+        rng = np.random.default_rng(seed)
+        self.kv, self.dim, self.page, self.lens, self.news = kv, dim, page, lens, news
+        used = [-(-n // page) for n in lens]
+        n_pages = sum(used) + 2
+        width = max(1, max(used)) + extra_width
+        raw = rng.integers(0, 256, n_pages * kv * ref.slab_bytes(dim, page), dtype=np.uint8)
+        pool = ref.Pool(raw, kv, dim, page)
+        pool.codes = np.clip(np.rint(rng.normal(0, 40, pool.codes.shape)), -127, 127).astype(np.int8)
+        # blocks that no token lies in hold NaN and infinite scales
+        pool.scales = rng.choice(np.array([np.nan, np.inf, -np.inf, 3e38], np.float32), pool.scales.shape)
+        order = rng.permutation(n_pages)
+        table = np.full((len(lens), width), -7, np.int32)
+        at = 0
+        for s, n in enumerate(used):
+            table[s, :n] = order[at:at + n]
+            for i in range(-(-lens[s] // 16)):
+                p = order[at + i * 16 // page]
+                pool.scales[p, :, :, i * 16 % page // 16] = np.exp(rng.normal(0, 0.7, (kv, 2))) * 0.02
+            at += n
+        self.pool, self.table = ref.Pool(pool.bytes(), kv, dim, page), table
+        self.row_start = np.concatenate([[0], np.cumsum(news)]).astype(np.int32)
+        self.rows = int(self.row_start[-1]) + pad_rows
+        self.first_page = first_page
+        if first_page:   # the pages lie far into a larger pool
+            self.data = torch.empty((first_page + n_pages, kv * ref.slab_bytes(dim, page)), dtype=torch.uint8, device="cuda")
+            self.data[first_page:].view(-1).copy_(torch.from_numpy(self.pool.bytes()))
+        else:
+            self.data = torch.from_numpy(self.pool.bytes()).cuda().view(n_pages, -1)
+        self.cache = i2s.Kv8Cache(first_page + n_pages, kv, dim, page, data=self.data)
+        dev = np.where(table >= 0, table + first_page, table).astype(np.int32)
+        self.batch = i2s.Kv8Batch(torch.from_numpy(self.row_start).cuda(),
+                                  torch.tensor(lens, dtype=torch.int32, device="cuda"), torch.from_numpy(dev).cuda(),
+                                  rows=self.rows, max_rows=max_rows or max(1, max(news)))
+
+    def pool_now(self):
+        return self.data[self.first_page:].cpu().numpy().reshape(-1)
+
+
+def rows_tensor(rng, rows, heads, dim, dtype, layout="packed", std=1.0):
+    """(tensor, its values as float32)."""
+    x = torch.from_numpy((rng.standard_normal((rows, heads, dim)) * std).astype(np.float32)).to(DTYPES[dtype]).cuda()
+    if layout == "heads first":
+        x = x.transpose(0, 1).contiguous().transpose(0, 1)
+    elif layout == "slice":
+        big = torch.full((rows, heads + 3, dim), float("nan"), dtype=x.dtype, device="cuda")
+        big[:, 1:1 + heads] = x
+        x = big[:, 1:1 + heads]
+    return x, x.float().cpu().numpy()
+
+
+def same_bits(a, b):
+    a, b = np.ascontiguousarray(a), np.ascontiguousarray(b)
+    np.testing.assert_array_equal(a.view(np.uint8), b.view(np.uint8))
+
+
+# -- write and read -------------------------------------------------------------------------------
+
+WRITES = [
+    # kv, dim, page, lens, news
+    (1, 128, 16, [1], [1]),
+    (2, 128, 64, [17, 16, 15, 33], [1, 1, 1, 1]),
+    (8, 128, 64, [100, 0, 64, 65, 2], [1, 0, 64, 2, 2]),
+    (3, 64, 32, [50, 31, 32, 129], [37, 31, 1, 100]),
+    (1, 64, 256, [300, 700], [299, 45]),
+    (2, 128, 128, [130, 1000], [5, 1000]),
+]
+
+
+@pytest.mark.parametrize("dtype", ALL)
+@pytest.mark.parametrize("layout", ["packed", "heads first", "slice"])
+@pytest.mark.parametrize("case", WRITES)
+def test_write_is_bit_exact(i2s, case, layout, dtype):
+    kv, dim, page, lens, news = case
+    st = Setup(i2s, kv, dim, page, lens, news, seed=len(lens) + dim, pad_rows=5)
+    rng = np.random.default_rng(7)
+    # a spread of sizes: some blocks' scales grow, some keep the one they have
+    k, kf = rows_tensor(rng, st.rows, kv, dim, dtype, layout, std=3.0)
+    v, vf = rows_tensor(rng, st.rows, kv, dim, dtype, layout, std=0.2)
+    i2s.kv8_write(st.cache, st.batch, k, v)
+    ref.write(st.pool, st.table, lens, st.row_start, kf, vf)
+    assert st.batch.status() == 0
+    same_bits(st.pool_now(), st.pool.bytes())
+    i2s.kv8_write(st.cache, st.batch, k, v)   # the same tokens again change nothing
+    same_bits(st.pool_now(), st.pool.bytes())
+
+
+@pytest.mark.parametrize("dtype", ALL)
+@pytest.mark.parametrize("layout", ["packed", "heads first", "slice"])
+@pytest.mark.parametrize("case", WRITES)
+def test_read_is_the_codes_times_the_scales(i2s, case, layout, dtype):
+    kv, dim, page, lens, news = case
+    st = Setup(i2s, kv, dim, page, lens, news, seed=3, pad_rows=4)
+    rng = np.random.default_rng(8)
+    k, kf = rows_tensor(rng, st.rows, kv, dim, dtype, layout)
+    v, vf = rows_tensor(rng, st.rows, kv, dim, dtype, layout)
+    i2s.kv8_read(st.cache, st.batch, k, v)
+    for which, (got, before) in enumerate(((k, kf), (v, vf))):
+        want = before.copy()   # rows behind the last sequence stay as they were
+        for s, n in enumerate(news):
+            x, _ = ref.cached(st.pool, st.table, s, lens[s], which)
+            want[st.row_start[s]:st.row_start[s + 1]] = x[lens[s] - n:].astype(np.float32)
+        want = torch.from_numpy(want).to(DTYPES[dtype])
+        assert torch.equal(got.cpu(), want)
+    assert st.batch.status() == 0
+
+
+def test_tokens_appended_one_by_one_match_the_definition(i2s):
+    """40 single-token appends: every block grows through all its fill levels."""
+    kv, dim, page, total = 2, 128, 32, 40
+    st = Setup(i2s, kv, dim, page, [total], [1], seed=11)
+    rng = np.random.default_rng(12)
+    for n in range(1, total + 1):
+        st.batch.kv_len.fill_(n)
+        k, kf = rows_tensor(rng, 1, kv, dim, "f32", std=float(np.exp(rng.normal(0, 1))))
+        v, vf = rows_tensor(rng, 1, kv, dim, "f32", std=0.01 * n)
+        i2s.kv8_write(st.cache, st.batch, k, v)
+        ref.write(st.pool, st.table, [n], st.row_start, kf, vf)
+    same_bits(st.pool_now(), st.pool.bytes())
+
+
+def test_a_block_with_nan_or_infinity_reads_as_nan_until_rewritten(i2s):
+    st = Setup(i2s, 1, 64, 16, [20, 20, 20], [6, 6, 6], seed=2)
+    rng = np.random.default_rng(1)
+    k, kf = rows_tensor(rng, 18, 1, 64, "f32")
+    v, vf = rows_tensor(rng, 18, 1, 64, "f32")
+    k[3, 0, 5], kf[3, 0, 5] = float("nan"), np.nan        # position 17 of sequence 0
+    v[7, 0, 0], vf[7, 0, 0] = float("-inf"), -np.inf      # position 15 of sequence 1
+    i2s.kv8_write(st.cache, st.batch, k, v)
+    ref.write(st.pool, st.table, st.lens, st.row_start, kf, vf)
+    same_bits(st.pool_now(), st.pool.bytes())
+    back_k, back_v = i2s.kv8_read(st.cache, st.batch)
+    bad_k, bad_v = back_k.isnan().any(-1)[:, 0].tolist(), back_v.isnan().any(-1)[:, 0].tolist()
+    assert bad_k == [False, False, True, True, True, True] + 12 * [False]     # block 16.. of sequence 0
+    assert bad_v == 6 * [False] + [True, True, False, False, False, False] + 6 * [False]
+    st.batch.kv_len[0] = 21                                # a finite token more: the block stays NaN
+    k2, v2 = torch.ones_like(k), torch.ones_like(v)
+    i2s.kv8_write(st.cache, st.batch, k2, v2)              # positions 15..20: block 1 from its first token
+    assert not i2s.kv8_read(st.cache, st.batch)[0].isnan().any()
+
+
+def test_write_and_read_beyond_four_gigabytes(i2s):
+    """Pages whose byte offset passes 32 bits."""
+    page_bytes = 8 * ref.slab_bytes(128, 64)
+    first = (1 << 32) // page_bytes + 5
+    st = Setup(i2s, 8, 128, 64, [70, 200], [70, 3], seed=4, first_page=first)
+    rng = np.random.default_rng(5)
+    k, kf = rows_tensor(rng, st.rows, 8, 128, "f32")
+    v, vf = rows_tensor(rng, st.rows, 8, 128, "f32")
+    i2s.kv8_write(st.cache, st.batch, k, v)
+    ref.write(st.pool, st.table, st.lens, st.row_start, kf, vf)
+    same_bits(st.pool_now(), st.pool.bytes())
+    q, qf = rows_tensor(rng, st.rows, 16, 128, "f32")
+    check_attention(i2s, st, q, qf, "f32")
+
+
+# -- norm and rotation ------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", ALL)
+@pytest.mark.parametrize("dim,rot,interleaved,norm", [
+    (128, 128, False, True), (128, 128, True, True), (128, 32, False, False), (128, 8, False, True),
+    (128, 40, True, False), (64, 64, False, True), (64, 64, True, False), (64, 24, False, True), (64, 0, False, True),
+    (128, 104, False, True)])
+@pytest.mark.parametrize("rows,qh,kh", [(1, 1, 1), (7, 12, 2), (33, 5, 0), (130, 0, 3)])
+def test_norm_rope(i2s, dtype, dim, rot, interleaved, norm, rows, qh, kh):
+    rng = np.random.default_rng(rows + dim + rot)
+    base = 1000000.0
+    turns = i2s.kv8_rope_turns(base, rot) if rot else None
+    pos = rng.integers(-5, 1 << 31, rows).astype(np.int32)
+    pos[0] = (1 << 31) - 1
+    dpos = torch.from_numpy(pos).cuda()
+    q, qf = rows_tensor(rng, rows, qh, dim, dtype, "slice", std=2.0) if qh else (None, None)
+    k, kf = rows_tensor(rng, rows, kh, dim, dtype, "heads first", std=0.01) if kh else (None, None)
+    gq, gk = (torch.from_numpy((1 + 0.3 * rng.standard_normal(dim)).astype(np.float32)).cuda() for _ in range(2))
+    got = i2s.kv8_norm_rope(q, k, dpos, turns, gamma_q=gq if norm else None, gamma_k=gk if norm else None, eps=1e-6,
+                            interleaved=interleaved)
+    integers = [int(t) % (1 << 64) for t in turns.tolist()] if rot else []
+    for x, y, g in ((qf, got[0], gq), (kf, got[1], gk)):
+        if x is None:
+            assert y is None
+            continue
+        want = ref.norm_rope(x, g.cpu().numpy() if norm else None, 1e-6, pos, integers, interleaved)
+        y = y.float().cpu().numpy().astype(np.float64)
+        # the larger of a pair bounds the rounding of both
+        size = np.abs(ref.norm_rope(x, g.cpu().numpy() if norm else None, 1e-6, pos, [], interleaved))
+        if rot:
+            a, b = ((slice(0, rot, 2), slice(1, rot, 2)) if interleaved else
+                    (slice(0, rot // 2), slice(rot // 2, rot)))
+            both = size[..., a] + size[..., b]
+            size[..., a], size[..., b] = both, both
+        eps = torch.finfo(DTYPES[dtype]).eps / 2 if dtype != "f32" else 0.0
+        tiny = 2.0 ** -25 if dtype == "f16" else 0.0   # half a step of f16's subnormals
+        assert (np.abs(y - want) <= size * 2.0 ** -19 + np.abs(want) * eps * (1 + 2.0 ** -9) + tiny).all()
+
+
+def test_norm_rope_in_place_in_a_fused_row(i2s):
+    rng = np.random.default_rng(3)
+    rows, qh, kh, dim = 9, 4, 2, 128
+    fused, f = rows_tensor(rng, rows, qh + 2 * kh, dim, "f32")
+    turns = i2s.kv8_rope_turns(10000.0, dim)
+    pos = torch.arange(100, 100 + rows, dtype=torch.int32, device="cuda")
+    q, k = fused[:, :qh], fused[:, qh:qh + kh]
+    want = i2s.kv8_norm_rope(q, k, pos, turns)
+    values = fused[:, qh + kh:].clone()
+    i2s.kv8_norm_rope(q, k, pos, turns, q_out=q, k_out=k)
+    assert torch.equal(q, want[0]) and torch.equal(k, want[1]) and torch.equal(fused[:, qh + kh:], values)
+
+
+def test_norm_rope_zero_head_and_zero_position(i2s):
+    x = torch.zeros((2, 1, 64), device="cuda")
+    x[1] = torch.randn((1, 64), device="cuda")
+    pos = torch.zeros(2, dtype=torch.int32, device="cuda")
+    out, _ = i2s.kv8_norm_rope(x, None, pos, i2s.kv8_rope_turns(10000.0, 64))
+    assert torch.equal(out, x)   # position 0 turns nothing
+    out, _ = i2s.kv8_norm_rope(x, None, pos, None, gamma_q=torch.ones(64, device="cuda"), eps=1e-6)
+    assert torch.equal(out[0], torch.zeros_like(out[0]))
+
+
+# -- attention ----------------------------------------------------------------------------------------
+
+def check_attention(i2s, st, q, qf, dtype, causal=True, window=0, scale=None, out=None, with_lse=True, ws=None):
+    heads = qf.shape[1]
+    scale = st.dim ** -0.5 if scale is None else scale
+    lse = torch.full((st.rows, heads), 99.0, device="cuda") if with_lse else None
+    if out is None:
+        out = torch.full((st.rows, heads, st.dim), 7.0, dtype=DTYPES[dtype], device="cuda")
+    before = out.float().cpu().numpy().copy()
+    i2s.kv8_attention(st.cache, st.batch, q, out=out, scale=scale, causal=causal, window=window, lse=lse, ws=ws)
+    torch.cuda.synchronize()
+    compare_attention(st, qf, dtype, causal, window, scale, out, lse, before)
+
+
+def compare_attention(st, qf, dtype, causal, window, scale, out, lse, before):
+    want, want_lse, weight, size = ref.attention(st.pool, st.table, st.lens, st.row_start, qf, float(np.float32(scale)),
+                                                 causal, window)
+    got = out.float().cpu().numpy().astype(np.float64)
+    last = st.row_start[-1]
+    np.testing.assert_array_equal(got[last:], before[last:])   # rows behind the last sequence
+    got, want, weight, size, want_lse = got[:last], want[:last], weight[:last], size[:last], want_lse[:last]
+    n = max(st.lens + [1])
+    rel = 2 * (2.0 ** -18 * (size + 1) * 2 + (n / 16 + 16) * 2.0 ** -22)
+    tol = weight * rel[..., None]
+    if dtype != "f32":
+        tol += weight.max(-1, keepdims=True) * 2.0 ** -11 + np.abs(want) * torch.finfo(DTYPES[dtype]).eps / 2 * 1.01 + 2.0 ** -24
+    worst = np.abs(got - want) - tol
+    assert (worst <= 0).all(), (float(worst.max()), np.unravel_index(worst.argmax(), worst.shape))
+    if lse is not None:
+        got_lse = lse.cpu().numpy().astype(np.float64)
+        assert (got_lse[last:] == 99.0).all()
+        got_lse = got_lse[:last]
+        np.testing.assert_array_equal(np.isneginf(got_lse), np.isneginf(want_lse))
+        fine = ~np.isneginf(want_lse)
+        assert (np.abs(got_lse - want_lse)[fine] <= (rel + 2.0 ** -22 * np.abs(np.where(fine, want_lse, 0)))[fine]).all()
+
+
+ATTENTION = [
+    # kv, group, dim, page, lens, news, causal, window
+    (1, 1, 128, 16, [1], [1], True, 0),
+    (2, 6, 128, 64, [75], [1], True, 0),
+    (2, 6, 128, 16, [15, 16, 17, 1, 400], [1, 1, 1, 1, 1], True, 0),
+    (8, 2, 128, 64, [300, 0, 64, 1037], [1, 0, 1, 1], True, 0),
+    (1, 8, 64, 32, [513, 31], [1, 1], True, 0),
+    (3, 5, 64, 128, [129, 255, 2000], [1, 1, 1], True, 100),
+    (2, 7, 128, 256, [4096], [1], True, 0),
+    (1, 16, 128, 64, [777, 20], [1, 1], True, 0),
+    (2, 6, 128, 16, [90, 33, 5, 700], [3, 6, 5, 1], True, 0),         # drafts
+    (2, 6, 128, 16, [90, 33, 5, 700], [3, 6, 5, 1], True, 20),
+    (4, 4, 64, 64, [100, 64, 1], [8, 64, 1], True, 0),
+    (1, 2, 128, 32, [333], [333], True, 0),                           # a prompt
+    (2, 3, 128, 64, [500, 130, 129], [257, 130, 64], True, 0),        # chunks
+    (2, 3, 128, 64, [500, 130, 129], [257, 130, 64], True, 33),
+    (2, 2, 64, 32, [400, 65], [128, 65], True, 1),                    # each row sees itself alone
+    (1, 4, 128, 64, [10, 100], [20, 100], True, 0),                   # rows before position 0 see nothing
+    (2, 4, 128, 64, [0, 40], [3, 3], True, 0),                        # an empty cache
+    (2, 4, 128, 64, [200, 40], [70, 3], False, 0),                    # every row sees all tokens
+    (2, 1, 64, 16, [40, 3], [1, 2], False, 0),
+    (1, 64, 128, 64, [200], [5], True, 0),
+    (1, 13, 64, 64, [200, 100, 47], [9, 21, 2], True, 0),
+]
+
+
+@pytest.mark.parametrize("dtype", ALL)
+@pytest.mark.parametrize("case", range(len(ATTENTION)))
+def test_attention(i2s, case, dtype):
+    kv, group, dim, page, lens, news, causal, window = ATTENTION[case]
+    st = Setup(i2s, kv, dim, page, lens, news, seed=case, pad_rows=3, extra_width=2)
+    rng = np.random.default_rng(case + 100)
+    q, qf = rows_tensor(rng, st.rows, kv * group, dim, dtype, std=1.5)
+    check_attention(i2s, st, q, qf, dtype, causal, window)
+    assert st.batch.status() == 0
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("new", [1, 4, 70])
+def test_attention_strides(i2s, dtype, new):
+    st = Setup(i2s, 2, 128, 32, [150, 90], [new, new], seed=1)
+    rng = np.random.default_rng(2)
+    q, qf = rows_tensor(rng, st.rows, 6, 128, dtype, "slice")
+    out = torch.full((6, st.rows, 128), 5.0, dtype=DTYPES[dtype], device="cuda").transpose(0, 1)
+    check_attention(i2s, st, q, qf, dtype, out=out, with_lse=False)
+
+
+@pytest.mark.parametrize("new", [1, 40])
+@pytest.mark.parametrize("size", [1e-30, 1e-5, 300.0, 1e20])
+def test_attention_of_small_and_large_queries(i2s, size, new):
+    """Queries outside f16's range, with a scale that brings the logits back."""
+    st = Setup(i2s, 1, 128, 64, [200], [new], seed=6)
+    rng = np.random.default_rng(9)
+    q, qf = rows_tensor(rng, st.rows, 4, 128, "f32", std=size)
+    check_attention(i2s, st, q, qf, "f32", scale=128 ** -0.5 / size)
+
+
+@pytest.mark.parametrize("new", [1, 40])
+def test_attention_with_scales_far_apart(i2s, new):
+    """Value scales from 1e-7 to 1e4 from block to block, and sharp logits."""
+    st = Setup(i2s, 2, 128, 64, [350], [new], seed=21)
+    rng = np.random.default_rng(22)
+    for p in st.table[0][st.table[0] >= 0]:
+        st.pool.scales[p, :, 1] = np.exp(rng.uniform(np.log(1e-7), np.log(1e4), st.pool.scales[p, :, 1].shape))
+        st.pool.scales[p, :, 0] = np.where(np.isfinite(st.pool.scales[p, :, 0]), 0.05, np.nan)
+    st.data.view(-1).copy_(torch.from_numpy(st.pool.bytes()))
+    st.pool = ref.Pool(st.pool.bytes(), 2, 128, 64)
+    q, qf = rows_tensor(rng, st.rows, 4, 128, "f32", std=3.0)
+    check_attention(i2s, st, q, qf, "f32")
+
+
+@pytest.mark.parametrize("new", [1, 40])
+def test_a_nan_block_is_nan_where_it_is_seen_and_nowhere_else(i2s, new):
+    st = Setup(i2s, 1, 128, 64, [100, 100], [new, new], seed=5)
+    p = st.table[0][0]
+    st.pool.scales[p, 0, 0, 1] = np.nan   # tokens 16..31 of sequence 0
+    st.data.view(-1).copy_(torch.from_numpy(st.pool.bytes()))
+    q, _ = rows_tensor(np.random.default_rng(1), st.rows, 2, 128, "f32")
+    out = i2s.kv8_attention(st.cache, st.batch, q)
+    assert out[:new].isnan().all() and not out[new:].isnan().any()
+    out = i2s.kv8_attention(st.cache, st.batch, q, window=20)   # behind every row's window
+    assert not out.isnan().any()
+
+
+@pytest.mark.parametrize("new", [1, 3, 50])
+def test_bad_pages_lengths_and_rows_are_cut_and_reported(i2s, new):
+    st = Setup(i2s, 2, 128, 32, [130, 64, 80], [new] * 3, seed=13)
+    rng = np.random.default_rng(3)
+    q, qf = rows_tensor(rng, st.rows, 4, 128, "f32")
+    k, kf = rows_tensor(rng, st.rows, 2, 128, "f32")
+    for bad in (-1, st.cache.n_pages, 1 << 30):
+        st.batch.page_table[0, 1] = bad        # tokens 32..63 of sequence 0
+        st.table[0, 1] = -1
+        check_attention(i2s, st, q, qf, "f32")
+        assert st.batch.status() == i2s.KV8_BAD_PAGE
+        assert st.batch.status() == 0
+    # a page that a write and a read need: nothing else changes
+    st.batch.page_table[0, 4] = -3
+    st.table[0, 4] = -1
+    i2s.kv8_write(st.cache, st.batch, k, k)
+    assert st.batch.status() == i2s.KV8_BAD_PAGE
+    ref.write(st.pool, st.table, st.lens, st.row_start, kf, kf)
+    same_bits(st.pool_now(), st.pool.bytes())
+    i2s.kv8_read(st.cache, st.batch)
+    with pytest.raises(i2s.I2SError):
+        st.batch.check()
+    # a length past the table, and one below zero
+    st.batch.kv_len[1] = 1 << 30
+    st.batch.kv_len[2] = -5
+    out = i2s.kv8_attention(st.cache, st.batch, q)
+    assert st.batch.status() & i2s.KV8_BAD_LENGTH
+    assert torch.equal(out[2 * new:], torch.zeros_like(out[2 * new:]))
+    # row starts that go backwards or leave the tensor
+    st.batch.kv_len.copy_(torch.tensor(st.lens, dtype=torch.int32))
+    for starts in ([0, 2 * new, new, 3 * new], [0, new, 2 * new, 1 << 30], [-4, new, 2 * new, 3 * new]):
+        st.batch.row_start.copy_(torch.tensor(starts, dtype=torch.int32))
+        i2s.kv8_attention(st.cache, st.batch, q)
+        i2s.kv8_write(st.cache, st.batch, k, k)
+        i2s.kv8_read(st.cache, st.batch)
+        assert st.batch.status() & i2s.KV8_BAD_ROWS
+
+
+@pytest.mark.parametrize("new", [1, 30])
+def test_attention_replayed_from_a_graph_after_the_lengths_change(i2s, new):
+    st = Setup(i2s, 2, 128, 64, [300, 150], [new, new], seed=17)
+    rng = np.random.default_rng(4)
+    q, qf = rows_tensor(rng, st.rows, 6, 128, "f32")
+    lse = torch.empty((st.rows, 6), device="cuda")
+    one = i2s.Kv8Attention(st.cache, st.batch, q, lse=lse)
+    two = i2s.Kv8Attention(st.cache, st.batch, q, ws=one.ws)   # another graph with the same workspace
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graphs = []
+    with torch.cuda.stream(side):
+        one()
+        two()
+        for call in (one, two):
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g, stream=side):
+                call()
+            graphs.append(g)
+    torch.cuda.current_stream().wait_stream(side)
+    for lens in ([300, 150], [77, 149], [new, new]):
+        st.lens = lens
+        st.batch.kv_len.copy_(torch.tensor(lens, dtype=torch.int32))
+        one.out.zero_()
+        for g in graphs + graphs[:1]:
+            g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(one.out, two.out)
+        compare_attention(st, qf, "f32", True, 0, 128 ** -0.5, one.out, lse, one.out.cpu().numpy())
+
+
+def test_attention_is_the_same_every_time(i2s):
+    for news in ([1, 1, 1], [40, 3, 99]):
+        st = Setup(i2s, 2, 128, 64, [3000, 150, 700], news, seed=23)
+        q, _ = rows_tensor(np.random.default_rng(4), st.rows, 8, 128, "f32")
+        call = i2s.Kv8Attention(st.cache, st.batch, q)
+        call()
+        first = call.out.clone()
+        for _ in range(5):
+            call.ws.fill_(255)
+            call()
+            assert torch.equal(first, call.out)
+
+
+# -- a decoder layer's run of them ----------------------------------------------------------------------
+
+@pytest.mark.parametrize("new", [1, 24])
+def test_projections_norm_rope_write_attention_together(i2s, new):
+    """W8A8 q, k, v -> kv8_norm_rope -> kv8_write -> kv8_attention -> W8A8 o on one stream, in a captured graph: the
+    attention equals the definition on what the cache then holds."""
+    hidden, qh, kv, dim, page = 256, 4, 2, 64, 32
+    lens, seqs = [40 + new, new], 2
+    st = Setup(i2s, kv, dim, page, lens, [new] * seqs, seed=31)
+    M = st.rows
+    g = torch.Generator(device="cuda").manual_seed(5)
+    x = torch.randn((M, hidden), generator=g, device="cuda")
+    qkv = torch.empty((M, (qh + 2 * kv) * dim), device="cuda")
+
+    def packed(n, k):
+        wq, bs = i2s.w8a8_quantize_weights(torch.randn((n, k), generator=g, device="cuda") * k ** -0.5)
+        return i2s.w8a8_pack_weights(wq), bs
+    w, bs = packed(qkv.shape[1], hidden)
+    wo, bo = packed(hidden, qh * dim)
+    q, k, v = qkv.view(M, -1, dim).split([qh, kv, kv], 1)
+    out = torch.empty((M, qh, dim), device="cuda")
+    y = torch.empty((M, hidden), device="cuda")
+    pos = torch.cat([torch.arange(n - new, n) for n in lens]).to(torch.int32).cuda()
+    gamma = torch.full((dim,), 1.5, device="cuda")
+    steps = [i2s.W8A8Group([(w, bs, qkv.shape[1], hidden, x, qkv)], M),
+             i2s.Kv8NormRope(q, k, pos, i2s.kv8_rope_turns(1e6, dim), gamma_q=gamma, gamma_k=gamma, q_out=q, k_out=k),
+             i2s.Kv8Write(st.cache, st.batch, k, v), i2s.Kv8Attention(st.cache, st.batch, q, out=out),
+             i2s.W8A8Group([(wo, bo, hidden, qh * dim, out.view(M, -1), y)], M)]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for step in steps:
+            step()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            for step in steps:
+                step()
+    side.synchronize()
+    x.copy_(torch.randn(x.shape, generator=g, device="cuda"))
+    graph.replay()
+    torch.cuda.synchronize()
+    assert st.batch.status() == 0
+    st.pool = ref.Pool(st.pool_now(), kv, dim, page)
+    qf = q.float().cpu().numpy()
+    compare_attention(st, qf, "f32", True, 0, dim ** -0.5, out, None, out.cpu().numpy())
+    # what the cache holds is the normed, rotated keys within half a step of the block's scale
+    kept, _ = i2s.kv8_read(st.cache, st.batch)
+    step = k.abs().amax().item() / 127
+    assert (kept - k).abs().max().item() <= 1.01 * step
+    want = i2s.w8a8_mul_mat_packed(wo, bo, hidden, qh * dim, out.view(M, -1))[0]
+    assert torch.equal(y, want)
