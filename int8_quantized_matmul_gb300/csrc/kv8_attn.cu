@@ -1,8 +1,12 @@
 // Attention over the 8-bit KV cache (include/i2s.h, kv8_attention).
 
+#include <algorithm>
+#include <atomic>
+
 #include "common.cuh"
 #include "internal.h"
 #include "kv8.cuh"
+#include "kv8_decode.cuh"
 
 namespace i2s {
 
@@ -61,20 +65,53 @@ __global__ void __launch_bounds__(128) k_kv8_attn(const __grid_constant__ Kv8Att
 
 }  // namespace
 
-size_t kv8_attention_ws(int heads, int dim, int q_heads, int seqs, int max_rows, long long rows) { return 256; }
+// Rows of an item (query rows of one sequence and KV head).
+static bool is_decode(int heads, int q_heads, int max_rows) {
+    return (long long)max_rows * (q_heads / heads) <= kvd::kRows;
+}
+
+static size_t plan_bytes(int heads, int seqs) { return ((size_t)heads * seqs * sizeof(Kv8Plan) + 255) / 256 * 256; }
+
+size_t kv8_attention_ws(int heads, int dim, int q_heads, int seqs, int max_rows, long long rows) {
+    if (!is_decode(heads, q_heads, max_rows)) return 256;
+    return plan_bytes(heads, seqs) + (size_t)2 * kvd::kMaxCtas * kvd::kRows * (dim + 2) * sizeof(float);
+}
+
+template <int DT, int D>
+static cudaError_t launch_dt(const Kv8AttnArgs& a, void* ws, cudaStream_t s) {
+    if (!is_decode(a.c.heads, a.q_heads, a.c.max_rows)) {
+        k_kv8_attn<DT, D><<<(unsigned)((a.c.rows * a.q_heads + 3) / 4), 128, 0, s>>>(a);
+        return cudaGetLastError();
+    }
+    Kv8Plan* plan = static_cast<Kv8Plan*>(ws);
+    float* slots = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + plan_bytes(a.c.heads, a.c.seqs));
+    constexpr int bytes = kvd::ring_bytes<D>();
+    static std::atomic<unsigned long long> ready{0};   // a bit per device
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (!(ready.load(std::memory_order_acquire) >> (dev & 63) & 1)) {
+        e = cudaFuncSetAttribute(k_kv8_decode<DT, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e != cudaSuccess) return e;
+        ready.fetch_or(1ull << (dev & 63), std::memory_order_release);
+    }
+    const int ctas = std::min(kvd::kMaxCtas, kvd::kCtasPerSm * device_sm_count());
+    k_kv8_decode<DT, D><<<ctas, kvd::kThreads, bytes, s>>>(a, slots, plan);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    const dim3 grid((unsigned)(a.c.seqs * a.c.heads), (unsigned)(a.c.max_rows * (a.q_heads / a.c.heads)));
+    return launch_pdl(k_kv8_join<DT, D>, grid, dim3(kJoinWarps * 32), 0, s, a, slots, plan);
+}
 
 template <int D>
-static void launch_d(const Kv8AttnArgs& a, cudaStream_t s) {
-    const unsigned grid = (unsigned)((a.c.rows * a.q_heads + 3) / 4);
-    if (a.dtype == kKvF32) k_kv8_attn<kKvF32, D><<<grid, 128, 0, s>>>(a);
-    else if (a.dtype == kKvF16) k_kv8_attn<kKvF16, D><<<grid, 128, 0, s>>>(a);
-    else k_kv8_attn<kKvBf16, D><<<grid, 128, 0, s>>>(a);
+static cudaError_t launch_d(const Kv8AttnArgs& a, void* ws, cudaStream_t s) {
+    if (a.dtype == kKvF32) return launch_dt<kKvF32, D>(a, ws, s);
+    if (a.dtype == kKvF16) return launch_dt<kKvF16, D>(a, ws, s);
+    return launch_dt<kKvBf16, D>(a, ws, s);
 }
 
 cudaError_t launch_kv8_attention(const Kv8AttnArgs& a, void* ws, cudaStream_t s) {
-    if (a.c.dim == 64) launch_d<64>(a, s);
-    else launch_d<128>(a, s);
-    return cudaGetLastError();
+    return a.c.dim == 64 ? launch_d<64>(a, ws, s) : launch_d<128>(a, ws, s);
 }
 
 }  // namespace i2s

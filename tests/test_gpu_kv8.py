@@ -383,6 +383,20 @@ def test_a_nan_block_is_nan_where_it_is_seen_and_nowhere_else(i2s, new):
     assert not out.isnan().any()
 
 
+@pytest.mark.parametrize("new", [2, 40])
+def test_a_nan_block_that_one_row_sees_does_not_reach_the_others(i2s, new):
+    st = Setup(i2s, 1, 128, 64, [100], [new], seed=5)
+    first = 100 - new   # row 0 sees tokens 31..first, row 1 32..first + 1
+    for which in (0, 1):
+        page = st.pool.raw.copy()
+        st.pool.scales[st.table[0][0], 0, which, 1] = np.nan   # tokens 16..31
+        st.data.view(-1).copy_(torch.from_numpy(st.pool.bytes()))
+        q, _ = rows_tensor(np.random.default_rng(1), st.rows, 2, 128, "f32")
+        out = i2s.kv8_attention(st.cache, st.batch, q, window=first - 31 + 1)
+        assert out[0].isnan().all() and not out[1:].isnan().any()
+        st.pool = ref.Pool(page.reshape(-1), 1, 128, 64)
+
+
 @pytest.mark.parametrize("new", [1, 3, 50])
 def test_bad_pages_lengths_and_rows_are_cut_and_reported(i2s, new):
     st = Setup(i2s, 2, 128, 32, [130, 64, 80], [new] * 3, seed=13)
