@@ -315,32 +315,39 @@ int64_t slab_bytes(int dim, int page_tokens) {
     return 2 * (int64_t)page_tokens * dim + (page_tokens / kKvBlock * 8 + 31) / 32 * 32;
 }
 
+// Checks the sizes of a cache and a batch and fills them into the kernels' view.
+int check_sizes(const kv8_cache& c, const kv8_batch& b, Kv8View& w) {
+    if (!cache_shape_ok(c.heads, c.head_dim, c.page_tokens)) return I2S_E_BAD_SHAPE;
+    if (c.n_pages < 1 || c.n_pages >= ((int64_t)1 << 31)) return I2S_E_BAD_SHAPE;
+    if (b.seqs < 1 || b.seqs > KV8_MAX_SEQS || b.rows < 1 || b.rows >= ((int64_t)1 << 31) || b.max_rows < 1 ||
+        b.max_rows > b.rows)
+        return I2S_E_BAD_SHAPE;
+    if (b.table_width < 1 || b.table_width >= ((int64_t)1 << 31) / c.page_tokens) return I2S_E_BAD_SHAPE;
+    w.n_pages = c.n_pages;
+    w.rows = b.rows;
+    w.width = b.table_width;
+    w.seqs = b.seqs;
+    w.max_rows = b.max_rows;
+    w.heads = c.heads;
+    w.dim = c.head_dim;
+    w.page_shift = __builtin_ctz((unsigned)c.page_tokens);
+    w.slab = (int)slab_bytes(c.head_dim, c.page_tokens);
+    return I2S_OK;
+}
+
 // Checks a cache and a batch; fills the kernels' view and the pool's bytes.
 int check_batch(const kv8_cache* c, const kv8_batch* b, Kv8View& w, Range& pool) {
     if (!c || !b || !c->pages || !b->row_start || !b->kv_len || !b->page_table || !b->status) return I2S_E_NULL_PTR;
-    if (!cache_shape_ok(c->heads, c->head_dim, c->page_tokens)) return I2S_E_BAD_SHAPE;
-    if (c->n_pages < 1 || c->n_pages >= ((int64_t)1 << 31)) return I2S_E_BAD_SHAPE;
-    if (b->seqs < 1 || b->seqs > KV8_MAX_SEQS || b->rows < 1 || b->rows >= ((int64_t)1 << 31) || b->max_rows < 1 ||
-        b->max_rows > b->rows)
-        return I2S_E_BAD_SHAPE;
-    if (b->table_width < 1 || b->table_width >= ((int64_t)1 << 31) / c->page_tokens) return I2S_E_BAD_SHAPE;
+    const int r = check_sizes(*c, *b, w);
+    if (r) return r;
     if (!aligned16(c->pages) || ((uintptr_t)b->row_start & 3) || ((uintptr_t)b->kv_len & 3) ||
         ((uintptr_t)b->page_table & 3) || ((uintptr_t)b->status & 3))
         return I2S_E_MISALIGNED;
     w.pages = static_cast<uint8_t*>(c->pages);
-    w.n_pages = c->n_pages;
     w.row_start = b->row_start;
     w.kv_len = b->kv_len;
     w.table = b->page_table;
     w.status = b->status;
-    w.rows = b->rows;
-    w.width = b->table_width;
-    w.seqs = b->seqs;
-    w.max_rows = b->max_rows;
-    w.heads = c->heads;
-    w.dim = c->head_dim;
-    w.page_shift = __builtin_ctz((unsigned)c->page_tokens);
-    w.slab = (int)slab_bytes(c->head_dim, c->page_tokens);
     pool = bytes_at(c->pages, (size_t)c->n_pages * c->heads * w.slab);
     return I2S_OK;
 }
@@ -508,12 +515,10 @@ int kv8_norm_rope(const kv8_rows* q, const kv8_rows* q_out, int q_heads, const f
 }
 
 size_t kv8_attention_workspace(const kv8_cache* cache, const kv8_batch* batch, int q_heads) {
-    if (!cache || !batch || !cache_shape_ok(cache->heads, cache->head_dim, cache->page_tokens)) return 0;
-    if (batch->seqs < 1 || batch->seqs > KV8_MAX_SEQS || batch->rows < 1 || batch->rows >= ((int64_t)1 << 31) ||
-        batch->max_rows < 1 || batch->max_rows > batch->rows)
-        return 0;
-    if (q_heads < 1 || q_heads % cache->heads || q_heads / cache->heads > 64) return 0;
-    return kv8_attention_ws(cache->heads, cache->head_dim, q_heads, batch->seqs, batch->max_rows, batch->rows);
+    Kv8View c;
+    if (!cache || !batch || check_sizes(*cache, *batch, c) != I2S_OK) return 0;
+    if (q_heads < 1 || q_heads % c.heads || q_heads / c.heads > 64) return 0;
+    return kv8_attention_ws(c, q_heads);
 }
 
 int kv8_attention(const kv8_cache* cache, const kv8_batch* batch, const kv8_rows* q, int q_heads, const kv8_rows* out,

@@ -135,7 +135,7 @@ struct Kv8AttnArgs {
     bool causal;
     int window;          // 0: none
 };
-size_t kv8_attention_ws(int heads, int dim, int q_heads, int seqs, int max_rows, long long rows);
+size_t kv8_attention_ws(const Kv8View& c, int q_heads);   // sizes only
 cudaError_t launch_kv8_attention(const Kv8AttnArgs& a, void* ws, cudaStream_t s);
 
 }  // namespace i2s

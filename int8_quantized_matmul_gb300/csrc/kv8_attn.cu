@@ -7,63 +7,9 @@
 #include "internal.h"
 #include "kv8.cuh"
 #include "kv8_decode.cuh"
+#include "kv8_tile.cuh"
 
 namespace i2s {
-
-namespace {
-
-// One warp per (row, query head), one token at a time with a running maximum
-// and sum.
-template <int DT, int D>
-__global__ void __launch_bounds__(128) k_kv8_attn(const __grid_constant__ Kv8AttnArgs a) {
-    using T = typename Kv8T<DT>::type;
-    constexpr int VPL = D / 32;
-    const Kv8View& c = a.c;
-    const int lane = threadIdx.x & 31;
-    const long long unit = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
-    const long long row = unit / a.q_heads;
-    const int head = (int)(unit - row * a.q_heads), kv = head / (a.q_heads / c.heads);
-    if (row >= c.rows) return;
-    const int s = kv8_seq_of_row(c, row);
-    if (s < 0) return;
-    const Kv8Seq sq = kv8_seq(c, s);
-    const long long i = row - sq.row0;
-    if (i < 0 || i >= sq.n) return;
-    const int pos = (int)((long long)sq.len - sq.n + i);
-    const int last = a.causal ? min(sq.len, pos + 1) : sq.len;
-    const int first = a.window ? max(0, pos - a.window + 1) : 0;
-    float q[VPL], o[VPL] = {}, m = -INFINITY, l = 0.0f;
-    kv8_load<T, VPL>(static_cast<const T*>(a.q.data) + row * a.q.row_stride + head * a.q.head_stride + VPL * lane, q);
-    const int mask = (1 << c.page_shift) - 1;
-    for (int t = first; t < last; ++t) {
-        const uint8_t* slab = kv8_slab(c, s, t, kv);
-        if (slab == nullptr) continue;
-        const int in = t & mask;
-        const Kv8Vec<int8_t, VPL> kc = *reinterpret_cast<const Kv8Vec<int8_t, VPL>*>(slab + kv8_code_off(c, 0, in) + VPL * lane);
-        const Kv8Vec<int8_t, VPL> vc = *reinterpret_cast<const Kv8Vec<int8_t, VPL>*>(slab + kv8_code_off(c, 1, in) + VPL * lane);
-        const float ks = *reinterpret_cast<const float*>(slab + kv8_scale_off(c, 0, in));
-        const float vs = *reinterpret_cast<const float*>(slab + kv8_scale_off(c, 1, in));
-        float dot = 0.0f;
-#pragma unroll
-        for (int j = 0; j < VPL; ++j) dot = fmaf(q[j], (float)kc.v[j], dot);
-#pragma unroll
-        for (int w = 16; w > 0; w >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, w);
-        const float x = dot * ks * a.scale;
-        const float nm = fmaxf(m, x);
-        const float keep = __expf(m - nm), p = __expf(x - nm);
-        l = fmaf(l, keep, p);
-#pragma unroll
-        for (int j = 0; j < VPL; ++j) o[j] = fmaf(o[j], keep, p * vs * (float)vc.v[j]);
-        m = nm;
-    }
-    const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
-#pragma unroll
-    for (int j = 0; j < VPL; ++j) o[j] *= inv;
-    kv8_store<T, VPL>(static_cast<T*>(a.out.data) + row * a.out.row_stride + head * a.out.head_stride + VPL * lane, o);
-    if (a.lse != nullptr && lane == 0) a.lse[row * a.q_heads + head] = m + logf(l);
-}
-
-}  // namespace
 
 // Rows of an item (query rows of one sequence and KV head).
 static bool is_decode(int heads, int q_heads, int max_rows) {
@@ -72,35 +18,95 @@ static bool is_decode(int heads, int q_heads, int max_rows) {
 
 static size_t plan_bytes(int heads, int seqs) { return ((size_t)heads * seqs * sizeof(Kv8Plan) + 255) / 256 * 256; }
 
-size_t kv8_attention_ws(int heads, int dim, int q_heads, int seqs, int max_rows, long long rows) {
-    if (!is_decode(heads, q_heads, max_rows)) return 256;
-    return plan_bytes(heads, seqs) + (size_t)2 * kvd::kMaxCtas * kvd::kRows * (dim + 2) * sizeof(float);
+// How the tile kernel cuts its work. Two query tiles per CTA read the cache half
+// as often and overlap each other's softmax and MMAs, but leave SMs idle where
+// there are too few of them; so do long caches under few rows, whose tiles are
+// then split between CTAs (as many as fill the SMs, two tiles of the cache at least each).
+struct TileCut {
+    int query_tiles;   // of a CTA
+    int items;         // grid: heads times a bound on the row tiles
+    int splits;
+};
+constexpr int kSms = 152;
+
+static TileCut tile_cut(int heads, int q_heads, int seqs, int max_rows, long long rows, long long tokens, int window) {
+    const long long rows_head = rows * (q_heads / heads);
+    const int some = (int)std::min<long long>(seqs, rows);   // sequences that may have rows
+    TileCut t;
+    t.query_tiles = heads * ((rows_head + 255) / 256) >= kSms ? 2 : 1;
+    const int per = t.query_tiles * kvt::kTileQ;
+    t.items = (int)(heads * (rows_head / per + some));
+    const long long likely = heads * std::max<long long>((rows_head + per - 1) / per, some);
+    if (window) tokens = std::min<long long>(tokens, (long long)window + max_rows);
+    const long long tiles = (tokens + kvt::kTileKv - 1) / kvt::kTileKv;
+    t.splits = (int)std::max<long long>(1, std::min<long long>(kSms / likely, tiles / 2));
+    return t;
+}
+
+static size_t up256(size_t n) { return (n + 255) / 256 * 256; }
+
+size_t kv8_attention_ws(const Kv8View& c, int q_heads) {
+    if (is_decode(c.heads, q_heads, c.max_rows))
+        return plan_bytes(c.heads, c.seqs) + (size_t)2 * kvd::kMaxCtas * kvd::kRows * (c.dim + 2) * sizeof(float);
+    const TileCut t = tile_cut(c.heads, q_heads, c.seqs, c.max_rows, c.rows, c.width << c.page_shift, 0);
+    if (t.splits == 1) return 256;
+    const size_t units = (size_t)t.splits * c.rows * q_heads;
+    return up256(units * c.dim * sizeof(float)) + 2 * up256(units * sizeof(float));
+}
+
+// Sets a kernel's shared memory once per device.
+template <typename K>
+static cudaError_t allow_smem(K kernel, int bytes, std::atomic<unsigned long long>& ready) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || (ready.load(std::memory_order_acquire) >> (dev & 63) & 1)) return e;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) ready.fetch_or(1ull << (dev & 63), std::memory_order_release);
+    return e;
+}
+
+template <int DT, int D, int MT>
+static cudaError_t launch_tile(const Kv8AttnArgs& a, const TileCut& t, const Kv8Parts& parts, cudaStream_t s) {
+    constexpr int bytes = kvt::smem_bytes<D, DT == kKvF32 ? 2 : 1>();
+    static_assert(bytes <= 232448, "shared memory");
+    static std::atomic<unsigned long long> ready{0};   // a bit per device
+    const cudaError_t e = allow_smem(k_kv8_tile<DT, D, MT>, bytes, ready);
+    if (e != cudaSuccess) return e;
+    k_kv8_tile<DT, D, MT><<<dim3((unsigned)t.items, (unsigned)t.splits), kvt::kThreads, bytes, s>>>(a, parts);
+    return cudaGetLastError();
 }
 
 template <int DT, int D>
-static cudaError_t launch_dt(const Kv8AttnArgs& a, void* ws, cudaStream_t s) {
-    if (!is_decode(a.c.heads, a.q_heads, a.c.max_rows)) {
-        k_kv8_attn<DT, D><<<(unsigned)((a.c.rows * a.q_heads + 3) / 4), 128, 0, s>>>(a);
-        return cudaGetLastError();
-    }
+static cudaError_t launch_decode(const Kv8AttnArgs& a, void* ws, cudaStream_t s) {
     Kv8Plan* plan = static_cast<Kv8Plan*>(ws);
     float* slots = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + plan_bytes(a.c.heads, a.c.seqs));
     constexpr int bytes = kvd::ring_bytes<D>();
-    static std::atomic<unsigned long long> ready{0};   // a bit per device
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
+    static std::atomic<unsigned long long> ready{0};
+    cudaError_t e = allow_smem(k_kv8_decode<DT, D>, bytes, ready);
     if (e != cudaSuccess) return e;
-    if (!(ready.load(std::memory_order_acquire) >> (dev & 63) & 1)) {
-        e = cudaFuncSetAttribute(k_kv8_decode<DT, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-        if (e != cudaSuccess) return e;
-        ready.fetch_or(1ull << (dev & 63), std::memory_order_release);
-    }
     const int ctas = std::min(kvd::kMaxCtas, kvd::kCtasPerSm * device_sm_count());
     k_kv8_decode<DT, D><<<ctas, kvd::kThreads, bytes, s>>>(a, slots, plan);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     const dim3 grid((unsigned)(a.c.seqs * a.c.heads), (unsigned)(a.c.max_rows * (a.q_heads / a.c.heads)));
     return launch_pdl(k_kv8_join<DT, D>, grid, dim3(kJoinWarps * 32), 0, s, a, slots, plan);
+}
+
+template <int DT, int D>
+static cudaError_t launch_dt(const Kv8AttnArgs& a, void* ws, cudaStream_t s) {
+    if (is_decode(a.c.heads, a.q_heads, a.c.max_rows)) return launch_decode<DT, D>(a, ws, s);
+    const TileCut t = tile_cut(a.c.heads, a.q_heads, a.c.seqs, a.c.max_rows, a.c.rows, a.c.width << a.c.page_shift, a.window);
+    Kv8Parts parts = {nullptr, nullptr, nullptr};
+    const size_t units = (size_t)t.splits * a.c.rows * a.q_heads;
+    if (t.splits > 1) {
+        parts.o = static_cast<float*>(ws);
+        parts.m = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + up256(units * D * sizeof(float)));
+        parts.l = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(parts.m) + up256(units * sizeof(float)));
+    }
+    const cudaError_t e = t.query_tiles == 2 ? launch_tile<DT, D, 2>(a, t, parts, s) : launch_tile<DT, D, 1>(a, t, parts, s);
+    if (e != cudaSuccess || t.splits == 1) return e;
+    const dim3 grid((unsigned)((a.c.rows * a.q_heads + 7) / 8));
+    return launch_pdl(k_kv8_join_splits<DT, D>, grid, dim3(256), 0, s, a, parts, t.splits);
 }
 
 template <int D>

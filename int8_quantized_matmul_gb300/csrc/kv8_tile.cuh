@@ -1,0 +1,619 @@
+// Attention of many query rows over the 8-bit KV cache on the 5th-generation
+// tensor cores: the tile kernel of kv8_attn.cu.
+//
+// An item is (sequence, KV head, up to MT * 128 query rows): the sequence's
+// new tokens times the query heads of the KV head, token by token, are cut
+// into tiles of 128 rows, and a CTA takes MT (1 or 2) neighbouring ones, so
+// each 128-token tile of the cache is read and converted once for all of them.
+//
+// Mathematics. With x_j = softmax_scale * log2(e) * q.K_j, and the values
+// V_j = v_b code_j of block b (16 tokens, one scale v_b),
+//   w_j = 2^(x_j + log2(v_b) - m + kBias),  O = sum_j w_j code_j,
+//   l = sum_b (sum_j w_j) / v_b,  out = O / l,
+// m the running maximum of x_j + log2(v_b): the scales enter as one addend of
+// the exponent and one product per block and row, and the weights that are
+// rounded to f16 stay in (0, 2^14]. log2(v_b) is rounded at 2^-22, the size of
+// the exponential's own error.
+//
+// Precision. Codes are exact in f16. F32 queries are scaled by a power of two
+// per row and split into two f16 parts (22 bits), and so are the weights: two
+// MMAs each into the same accumulator (PARTS = 2). 16-bit queries are exact in
+// one part after the scaling (f16's 11 bits hold bf16's 8), and their weights
+// are rounded once to f16, 2^-12, below the half step of the output.
+//
+// Roles (14 warps, one CTA per SM):
+//   warps 0-3, 4-7   softmax of query tile 0, 1: one thread per row (TMEM lane);
+//                    they also stage Q, rescale O and write the output
+//   warps 8-11       producer: int8 K and V from global memory, a tile ahead in
+//                    registers, to f16 in 128-byte-swizzled shared memory
+//   warps 12, 13     one thread issues the MMAs of query tile 0, 1
+// TMEM (512 columns): S of each query tile (128 columns of f32), overwritten in
+// place by the weights (32 columns of S become 16 of high and 16 of low
+// parts), and O of each (D columns). With two query tiles one's softmax runs
+// while the other's MMAs do. K is the K-major operand [token][d]; V with the
+// same bytes is the MN-major operand.
+//
+// A slot of the ring holds K or V of one tile, in the order K0 V0 K1 V1 ...
+// full[] counts the 128 producer threads, empty[] the query tiles' commits.
+// Every wait is bounded; one that runs out sets KV8_TIMEOUT.
+#pragma once
+
+#include "kv8_decode.cuh"
+#include "tc.cuh"
+
+namespace i2s {
+
+namespace kvt {
+
+constexpr int kTileQ = 128;
+constexpr int kTileKv = 128;
+constexpr int kBlocks = kTileKv / kKvBlock;
+constexpr int kThreads = 14 * 32;
+constexpr int kProducerWarp = 8;
+constexpr int kIssueWarp = 12;
+constexpr float kBias = 8.0f;
+constexpr float kSlack = 6.0f;
+constexpr long long kWait = 2000000000LL;
+constexpr int kConsts = 4;           // tiles whose scales are kept: the producer is at most two ahead
+constexpr int kHalf = kTileKv * 128; // bytes of 64 columns of 128 rows of f16
+
+template <int D>
+__host__ __device__ constexpr int operand_bytes() { return kTileKv * D * 2; }
+template <int D, int PARTS>
+__host__ __device__ constexpr int slots_of() { return D == 128 ? (PARTS == 2 ? 3 : 4) : 6; }
+
+struct Shared {
+    uint64_t full[6], empty[6], cfull[kConsts];
+    uint64_t q_ready[2], s_full[2], p_ready[2], pv_done[2], drained[2];
+    float ks[kConsts][kBlocks], lv[kConsts][kBlocks], iv[kConsts][kBlocks];
+    float mul[2][kTileQ];
+    uint32_t tmem;
+    int abort;
+    int scan[kThreads / 32];
+    int item[2];   // sequence, first row of the item in it
+};
+
+template <int D, int PARTS>
+__host__ __device__ constexpr int smem_bytes() {
+    return 1024 + (2 * PARTS + slots_of<D, PARTS>()) * operand_bytes<D>() + (int)sizeof(Shared);
+}
+
+// MN-major operand in the 128-byte-swizzled canonical layout: rows (k) of 64
+// elements, 8-row atoms of 1024 bytes, the next 64 columns kHalf bytes on.
+__device__ __forceinline__ uint64_t sdesc_sw128_mnmajor(uint32_t saddr) {
+    uint64_t d = 0;
+    d |= (uint64_t)((saddr >> 4) & 0x3FFFu);
+    d |= (uint64_t)(kHalf >> 4) << 16;
+    d |= (uint64_t)(1024u >> 4) << 32;
+    d |= (uint64_t)1 << 46;
+    d |= (uint64_t)2 << 61;
+    return d;
+}
+constexpr uint32_t kTransposeB = 1u << 16;   // B is MN-major (instruction descriptor)
+
+__device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
+
+}  // namespace kvt
+
+// Where a split's parts go: [split][row][head] of D sums, then the maxima and
+// the l of all of them.
+struct Kv8Parts {
+    float* o;
+    float* m;
+    float* l;
+};
+
+template <int DT, int D, int MT>
+__global__ void __launch_bounds__(kvt::kThreads, 1)
+    k_kv8_tile(const __grid_constant__ Kv8AttnArgs a, Kv8Parts parts) {
+    using namespace kvt;
+    using kvd::ex2;
+    using T = typename Kv8T<DT>::type;
+    constexpr int PARTS = DT == kKvF32 ? 2 : 1;
+    constexpr int kSlots = slots_of<D, PARTS>();
+    constexpr int kOp = operand_bytes<D>();
+    constexpr int kKSteps = D / 16, kVSteps = kTileKv / 16;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+    uint8_t* sQ = smem;                                  // [query tile][part]
+    uint8_t* sKV = smem + 2 * PARTS * kOp;               // ring
+    Shared& S = *reinterpret_cast<Shared*>(sKV + kSlots * kOp);
+
+    const Kv8View& c = a.c;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int group = a.q_heads / c.heads;
+    constexpr int kRowsItem = MT * kTileQ;
+
+    // The item: heads vary fastest, the last rows of the last sequence come
+    // first (under a causal mask they see the most).
+    {
+        const int per = (c.seqs + kThreads - 1) / kThreads;
+        int mine = 0;
+        for (int i = 0; i < per; ++i) {
+            const int s = tid * per + i;
+            if (s < c.seqs) mine += (int)(((long long)kv8_seq(c, s).n * group + kRowsItem - 1) / kRowsItem);
+        }
+        int upto = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += v;
+        }
+        if (lane == 31) S.scan[warp] = upto;
+        __syncthreads();
+        int base = upto - mine, all = 0;
+        for (int w = 0; w < kThreads / 32; ++w) {
+            if (w < warp) base += S.scan[w];
+            all += S.scan[w];
+        }
+        const int at = all - 1 - (int)(blockIdx.x / c.heads);
+        if (at < 0) return;   // uniform: every thread has the same `all`
+        if (mine > 0 && base <= at && at < base + mine) {
+            int s = tid * per;
+            for (; s + 1 < c.seqs; ++s) {
+                const int n = (int)(((long long)kv8_seq(c, s).n * group + kRowsItem - 1) / kRowsItem);
+                if (at < base + n) break;
+                base += n;
+            }
+            S.item[0] = s;
+            S.item[1] = (at - base) * kRowsItem;
+        }
+    }
+    if (tid == 0) {
+        for (int i = 0; i < kSlots; ++i) {
+            tc::mbar_init(&S.full[i], 128);
+            tc::mbar_init(&S.empty[i], MT);
+        }
+        for (int i = 0; i < kConsts; ++i) tc::mbar_init(&S.cfull[i], 32);
+        for (int i = 0; i < 2; ++i) {
+            tc::mbar_init(&S.q_ready[i], 128);
+            tc::mbar_init(&S.s_full[i], 1);
+            tc::mbar_init(&S.p_ready[i], 128);
+            tc::mbar_init(&S.pv_done[i], 1);
+            tc::mbar_init(&S.drained[i], 1);
+        }
+        S.abort = 0;
+        tc::fence_mbar_init();
+    }
+    if (warp == kIssueWarp) {
+        tc::tmem_alloc(&S.tmem, 512);
+        tc::tmem_relinquish();
+    }
+    tc::tc_fence_before();
+    __syncthreads();
+    tc::tc_fence_after();
+    const uint32_t tmem = S.tmem;
+    const int s = S.item[0];
+    const int head = blockIdx.x % c.heads;
+    const Kv8Seq sq = kv8_seq(c, s);
+    const int row_lo = S.item[1];                                   // rows of the sequence's n * group
+    const int row_hi = (int)min((long long)row_lo + kRowsItem, (long long)sq.n * group);
+
+    // The tiles that rows [lo, hi) see, then this split's share of the item's,
+    // and how many of those each query tile needs.
+    auto last_seen = [&](int row) {   // tokens that a row sees end here
+        if (!a.causal) return (long long)sq.len;
+        return max(0LL, min((long long)sq.len, (long long)sq.len - sq.n + row / group + 1));
+    };
+    int t_lo = 0;
+    if (a.window) t_lo = (int)(max(0LL, (long long)sq.len - sq.n + row_lo / group - a.window + 1) / kTileKv);
+    const int t_hi = (int)((last_seen(row_hi - 1) + kTileKv - 1) / kTileKv);
+    const int tiles = max(0, t_hi - t_lo);
+    const int from = t_lo + (int)((long long)tiles * blockIdx.y / gridDim.y);
+    const int to = t_lo + (int)((long long)tiles * (blockIdx.y + 1) / gridDim.y);
+    const int steps = to - from;
+    auto steps_of = [&](int qt) {
+        const int lo = row_lo + qt * kTileQ, hi = min(row_hi, lo + kTileQ);
+        if (lo >= hi) return 0;
+        return max(0, min(steps, (int)((last_seen(hi - 1) + kTileKv - 1) / kTileKv) - from));
+    };
+    volatile int* abort_flag = &S.abort;
+    auto fail = [&]() {
+        *abort_flag = 1;
+        atomicOr(c.status, kKvTimeout);
+    };
+
+    if (warp < 4 * MT) {
+        // ------------------------------------------------------------ softmax
+        const int qt = warp >> 2, r = tid & 127;
+        const int n = steps_of(qt);
+        const int tile_row = row_lo + qt * kTileQ;
+        if (n > 0) {
+            // Q: each warp its 32 rows, a lane 4 (D = 128) or 2 consecutive values
+            constexpr int VPL = D / 32;
+            uint8_t* q0 = sQ + qt * PARTS * kOp;
+            constexpr int kBatch = 8;
+#pragma unroll 1
+            for (int i0 = 0; i0 < 32; i0 += kBatch) {
+                float x[kBatch][VPL];
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i) {
+                    const int row = tile_row + (warp & 3) * 32 + i0 + i;
+                    if (row < row_hi) {
+                        const int ti = row / group, hh = head * group + row - ti * group;
+                        kv8_load<T, VPL>(static_cast<const T*>(a.q.data) + (sq.row0 + ti) * a.q.row_stride +
+                                             hh * a.q.head_stride + VPL * lane, x[i]);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < VPL; ++j) x[i][j] = 0.0f;
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i) {
+                    const int rr = (warp & 3) * 32 + i0 + i;
+                    uint32_t top = 0;
+#pragma unroll
+                    for (int j = 0; j < VPL; ++j) top = max(top, __float_as_uint(x[i][j]) & 0x7fffffffu);
+                    top = __reduce_max_sync(0xffffffffu, top);
+                    float up, down;
+                    kvd::row_scale(top, up, down);
+                    // mul is not negative, so the largest S of a block is the largest logit
+                    if (lane == 0) S.mul[qt][rr] = down * (fabsf(a.scale) * 1.44269504088896340736f);
+                    if (a.scale < 0.0f) up = -up;
+                    uint32_t hi[VPL / 2], lo[VPL / 2];
+#pragma unroll
+                    for (int j = 0; j < VPL; j += 2) kvd::split2(x[i][j] * up, x[i][j + 1] * up, hi[j / 2], lo[j / 2]);
+                    const int byte = 2 * VPL * lane;   // in the row of D f16
+                    const uint32_t off = (byte >> 7) * kHalf + rr * 128 + ((((byte & 127) >> 4) ^ (rr & 7)) << 4) + (byte & 15);
+                    if (VPL == 4) {
+                        *reinterpret_cast<uint2*>(q0 + off) = make_uint2(hi[0], hi[VPL / 2 - 1]);
+                        if (PARTS == 2) *reinterpret_cast<uint2*>(q0 + kOp + off) = make_uint2(lo[0], lo[VPL / 2 - 1]);
+                    } else {
+                        *reinterpret_cast<uint32_t*>(q0 + off) = hi[0];
+                        if (PARTS == 2) *reinterpret_cast<uint32_t*>(q0 + kOp + off) = lo[0];
+                    }
+                }
+            }
+            tc::fence_proxy_async_smem();
+            __syncwarp();
+            tc::mbar_arrive(&S.q_ready[qt]);
+        }
+        const int row = tile_row + r;
+        const bool live = row < row_hi;
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t ts = tmem + lanes + (uint32_t)qt * kTileKv;
+        const uint32_t to_ = tmem + lanes + (uint32_t)(MT * kTileKv + qt * D);
+        int see_lo = 0, see_hi = 0;
+        if (live) {
+            see_hi = (int)last_seen(row);
+            if (a.window) see_lo = (int)max(0LL, (long long)sq.len - sq.n + row / group - a.window + 1);
+        }
+        const int all_lo = __reduce_max_sync(0xffffffffu, live ? see_lo : 0);
+        const int all_hi = __reduce_min_sync(0xffffffffu, live ? see_hi : 0x7fffffff);
+        const float mul = n > 0 ? S.mul[qt][r] : 0.0f;   // written by this warp
+        float m = -INFINITY, l = 0.0f;
+        bool ok = true;
+        for (int j = 0; j < n; ++j) {
+            const int cs = j % kConsts;
+            if (!tc::mbar_wait(&S.cfull[cs], (j / kConsts) & 1, abort_flag, kWait) ||
+                !tc::mbar_wait(&S.s_full[qt], j & 1, abort_flag, kWait)) { fail(); ok = false; }
+            if (__any_sync(0xffffffffu, !ok)) { ok = false; break; }
+            tc::tc_fence_after();
+            const int tok = (from + j) * kTileKv;
+            const bool masked = tok < all_lo || tok + kTileKv > all_hi;   // for some row of the warp
+            const int lo = see_lo - tok, hi = see_hi - tok;
+            float top = -INFINITY;
+#pragma unroll
+            for (int ch = 0; ch < 4; ++ch) {
+                uint32_t v[32];
+                tc::tmem_ld_32x32b_x32(ts + 32u * ch, v);
+                tc::tmem_ld_wait();
+                if (masked) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        if (32 * ch + i < lo || 32 * ch + i >= hi) v[i] = 0xff800000u;   // -infinity
+                }
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    float t0 = -INFINITY, t1 = -INFINITY;
+#pragma unroll
+                    for (int i = 0; i < 16; i += 4) {
+                        t0 = max3(t0, __uint_as_float(v[16 * b + i]), __uint_as_float(v[16 * b + i + 1]));
+                        t1 = max3(t1, __uint_as_float(v[16 * b + i + 2]), __uint_as_float(v[16 * b + i + 3]));
+                    }
+                    t0 = fmaxf(t0, t1);
+                    // a zero scale times -infinity would be NaN, which the maximum ignores
+                    top = fmaxf(top, fmaf(t0, mul * S.ks[cs][2 * ch + b], S.lv[cs][2 * ch + b]));
+                }
+            }
+            if (__any_sync(0xffffffffu, top > m + kSlack)) {
+                const float nm = fmaxf(m, top);
+                const float keep = nm == -INFINITY ? 1.0f : ex2(m - nm);
+                m = nm;
+                l *= keep;
+                if (j > 0) {   // the MMAs into O are done: S came after them
+#pragma unroll 1
+                    for (int ch = 0; ch < D / 32; ++ch) {
+                        uint32_t v[32];
+                        tc::tmem_ld_32x32b_x32(to_ + 32u * ch, v);
+                        tc::tmem_ld_wait();
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * keep);
+                        tc::tmem_st_32x32b_x32(to_ + 32u * ch, v);
+                    }
+                }
+            }
+            const float sub = m == -INFINITY ? 0.0f : m - kBias;
+#pragma unroll
+            for (int ch = 0; ch < 4; ++ch) {
+                uint32_t v[32];
+                tc::tmem_ld_32x32b_x32(ts + 32u * ch, v);
+                tc::tmem_ld_wait();
+                uint32_t hi16[16], lo16[16];
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    const float xm = mul * S.ks[cs][2 * ch + b], add = S.lv[cs][2 * ch + b] - sub;
+                    float sum0 = 0.0f, sum1 = 0.0f;
+#pragma unroll
+                    for (int i = 0; i < 16; i += 2) {
+                        const int k = 16 * b + i;
+                        float w0 = ex2(fmaf(__uint_as_float(v[k]), xm, add));
+                        float w1 = ex2(fmaf(__uint_as_float(v[k + 1]), xm, add));
+                        if (masked) {
+                            if (32 * ch + k < lo || 32 * ch + k >= hi) w0 = 0.0f;
+                            if (32 * ch + k + 1 < lo || 32 * ch + k + 1 >= hi) w1 = 0.0f;
+                        }
+                        sum0 += w0;
+                        sum1 += w1;
+                        if (PARTS == 2) kvd::split2(w0, w1, hi16[k / 2], lo16[k / 2]);
+                        else hi16[k / 2] = kvd::pack2(w0, w1);
+                    }
+                    l = fmaf(sum0 + sum1, S.iv[cs][2 * ch + b], l);
+                }
+                tc::tmem_st_32x32b_x16(ts + 32u * ch, hi16);
+                if (PARTS == 2) tc::tmem_st_32x32b_x16(ts + 32u * ch + 16u, lo16);
+            }
+            tc::tmem_st_wait();
+            tc::tc_fence_before();
+            tc::mbar_arrive(&S.p_ready[qt]);
+        }
+        if (n > 0 && ok) {
+            if (!tc::mbar_wait(&S.pv_done[qt], (n - 1) & 1, abort_flag, kWait)) { fail(); ok = false; }
+            ok = !__any_sync(0xffffffffu, !ok);
+            tc::tc_fence_after();
+        }
+        if (ok) {
+            const int ti = row / group, hh = head * group + row - ti * group;
+            const long long grow = sq.row0 + ti;
+            const bool split = gridDim.y > 1;
+            const long long part = ((long long)blockIdx.y * c.rows + grow) * a.q_heads + hh;
+            const float inv = split ? 1.0f : (l == 0.0f ? 0.0f : __fdiv_rn(1.0f, l));
+            if (live) {
+                if (split) {
+                    parts.m[part] = m;
+                    parts.l[part] = l;
+                } else if (a.lse != nullptr) {
+                    a.lse[grow * a.q_heads + hh] =
+                        l == 0.0f ? -INFINITY : (log2f(l) + (m - kBias)) * 0.69314718055994530942f;
+                }
+            }
+            if (!split || n > 0) {
+#pragma unroll 1
+                for (int ch = 0; ch < D / 32; ++ch) {
+                    uint32_t v[32];
+                    if (n > 0) {
+                        tc::tmem_ld_32x32b_x32(to_ + 32u * ch, v);
+                        tc::tmem_ld_wait();
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[i] = 0u;
+                    }
+                    if (live && split) {
+                        float* dst = parts.o + part * D + 32 * ch;
+#pragma unroll
+                        for (int i = 0; i < 32; i += 4)
+                            *reinterpret_cast<uint4*>(dst + i) = make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+                    } else if (live) {
+                        T* dst = static_cast<T*>(a.out.data) + grow * a.out.row_stride + hh * a.out.head_stride + 32 * ch;
+                        constexpr int W = 16 / sizeof(T);
+#pragma unroll
+                        for (int i = 0; i < 32; i += W) {
+                            float x[W];
+#pragma unroll
+                            for (int k = 0; k < W; ++k) x[k] = __uint_as_float(v[i + k]) * inv;
+                            kv8_store<T, W>(dst + i, x);
+                        }
+                    }
+                    __syncwarp();
+                }
+            }
+        }
+        tc::tc_fence_before();
+    } else if (warp >= kProducerWarp && warp < kIssueWarp) {
+        // ----------------------------------------------------------- producer
+        const int p = tid - kProducerWarp * 32;
+        constexpr int kChunks = D / 16;          // 16-byte chunks of a token's codes
+        constexpr int kLoads = kChunks;          // per thread and operand: 128 * kChunks / 128
+        const int* table = c.table + (long long)s * c.width;
+        uint4 reg[kLoads];
+        int pages = -1;   // lane i < 8: the page of block i of the current tile, -1: none
+        auto fetch_pages = [&](int j) {
+            pages = -1;
+            const long long tok = (long long)(from + j) * kTileKv + (lane & 7) * kKvBlock;
+            if (j < steps && tok < sq.len) {
+                pages = table[tok >> c.page_shift];
+                if (pages < 0 || pages >= c.n_pages) {
+                    if (warp == kProducerWarp) atomicOr(c.status, kKvBadPage);
+                    pages = -1;
+                }
+            }
+        };
+        auto load = [&](int j, int which) {
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) {
+                const int idx = i * 128 + p, r = idx / kChunks, cc = idx % kChunks;
+                const int page = __shfl_sync(0xffffffffu, pages, r >> 4);
+                if (page >= 0) {
+                    const int tok = ((from + j) * kTileKv + r) & ((1 << c.page_shift) - 1);
+                    reg[i] = *reinterpret_cast<const uint4*>(c.pages + ((long long)page * c.heads + head) * c.slab +
+                                                             kv8_code_off(c, which, tok) + 16 * cc);
+                } else {
+                    reg[i] = make_uint4(0u, 0u, 0u, 0u);
+                }
+            }
+        };
+        auto scales = [&](int j) {   // the first producer warp, lane i < 8: block i
+            const int cs = j % kConsts;
+            if (lane < kBlocks) {
+                float k = 0.0f, lv = -INFINITY, iv = 0.0f;
+                if (pages >= 0) {
+                    const int tok = ((from + j) * kTileKv + lane * kKvBlock) & ((1 << c.page_shift) - 1);
+                    const uint8_t* slab = c.pages + ((long long)pages * c.heads + head) * c.slab;
+                    k = *reinterpret_cast<const float*>(slab + kv8_scale_off(c, 0, tok));
+                    const float v = *reinterpret_cast<const float*>(slab + kv8_scale_off(c, 1, tok));
+                    // a scale that no written block has (0 among them) counts as 2^-40
+                    const float some = v < 0x1p-40f ? 0x1p-40f : v;
+                    lv = log2f(some);
+                    // NaN weights make l NaN for the rows that see the block; the others add 0 * 1
+                    iv = v == v ? __fdiv_rn(1.0f, some) : 1.0f;
+                }
+                S.ks[cs][lane] = k;
+                S.lv[cs][lane] = lv;
+                S.iv[cs][lane] = iv;
+            }
+            tc::mbar_arrive(&S.cfull[cs]);
+        };
+        bool ok = true;
+        fetch_pages(0);
+        if (steps > 0) load(0, 0);
+        for (int i = 0; i < 2 * steps && ok; ++i) {
+            const int slot = i % kSlots, use = i / kSlots, which = i & 1;
+            if (!tc::mbar_wait_idle(&S.empty[slot], (use & 1) ^ 1, abort_flag, kWait)) { fail(); ok = false; break; }
+            if (which == 0 && warp == kProducerWarp) scales(i >> 1);
+            uint8_t* dst = sKV + slot * kOp;
+#pragma unroll
+            for (int q = 0; q < kLoads; ++q) {
+                const int idx = q * 128 + p, r = idx / kChunks, cc = idx % kChunks;
+                const uint32_t w[4] = {reg[q].x ^ 0x80808080u, reg[q].y ^ 0x80808080u, reg[q].z ^ 0x80808080u,
+                                       reg[q].w ^ 0x80808080u};
+                uint4 h[2];
+                h[0] = make_uint4(kvd::codes2<0x4140>(w[0]), kvd::codes2<0x4342>(w[0]), kvd::codes2<0x4140>(w[1]),
+                                  kvd::codes2<0x4342>(w[1]));
+                h[1] = make_uint4(kvd::codes2<0x4140>(w[2]), kvd::codes2<0x4342>(w[2]), kvd::codes2<0x4140>(w[3]),
+                                  kvd::codes2<0x4342>(w[3]));
+                // the lanes of the second half of a row store their two chunks
+                // in the other order: different banks at the same time
+                const int flip = (cc >> 2) & 1;
+                uint8_t* base = dst + (cc >> 2) * kHalf + r * 128;
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const int ch = 2 * (cc & 3) + (k ^ flip);
+                    *reinterpret_cast<uint4*>(base + ((ch ^ (r & 7)) << 4)) = (k ^ flip) ? h[1] : h[0];
+                }
+            }
+            tc::fence_proxy_async_smem();
+            tc::mbar_arrive(&S.full[slot]);
+            if (i + 1 < 2 * steps) {
+                if (which == 1) fetch_pages((i + 1) >> 1);
+                load((i + 1) >> 1, which ^ 1);
+            }
+        }
+    } else if (warp >= kIssueWarp && warp < kIssueWarp + MT) {
+        // ---------------------------------------------------------- MMA issue
+        if (lane == 0) {
+            const int qt = warp - kIssueWarp;
+            const int n = steps_of(qt);
+            constexpr uint32_t idesc_qk = tc::idesc_f16_f32(kTileQ, kTileKv);
+            constexpr uint32_t idesc_pv = tc::idesc_f16_f32(kTileQ, D) | kTransposeB;
+            const uint32_t ts = tmem + (uint32_t)qt * kTileKv;
+            const uint32_t to_ = tmem + (uint32_t)(MT * kTileKv + qt * D);
+            const uint64_t qd = tc::sdesc_sw128_kmajor(tc::smem_u32(sQ + qt * PARTS * kOp));
+            bool ok = true;
+            auto qk = [&](int j) {
+                const int i = 2 * j, slot = i % kSlots;
+                if (!tc::mbar_wait_spin(&S.full[slot], (i / kSlots) & 1, abort_flag, kWait)) return false;
+                tc::tc_fence_after();
+                const uint64_t kd = tc::sdesc_sw128_kmajor(tc::smem_u32(sKV + slot * kOp));
+#pragma unroll
+                for (int pt = 0; pt < PARTS; ++pt)
+#pragma unroll
+                    for (int k = 0; k < kKSteps; ++k) {
+                        const uint64_t off = (uint64_t)((k >> 2) * (kHalf >> 4) + 2 * (k & 3));
+                        tc::umma_f16(ts, qd + (uint64_t)(pt * (kOp >> 4)) + off, kd + off, idesc_qk, pt + k > 0);
+                    }
+                tc::umma_commit(&S.empty[slot]);
+                tc::umma_commit(&S.s_full[qt]);
+                return true;
+            };
+            if (n > 0) {
+                ok = tc::mbar_wait_spin(&S.q_ready[qt], 0, abort_flag, kWait);
+                tc::tc_fence_after();
+                ok = ok && qk(0);
+            }
+            for (int j = 0; ok && j < n; ++j) {
+                const int i = 2 * j + 1, slot = i % kSlots;
+                ok = tc::mbar_wait_spin(&S.full[slot], (i / kSlots) & 1, abort_flag, kWait) &&
+                     tc::mbar_wait_spin(&S.p_ready[qt], j & 1, abort_flag, kWait);
+                if (!ok) break;
+                tc::tc_fence_after();
+                const uint64_t vd = sdesc_sw128_mnmajor(tc::smem_u32(sKV + slot * kOp));
+#pragma unroll
+                for (int k = 0; k < kVSteps; ++k)
+#pragma unroll
+                    for (int pt = 0; pt < PARTS; ++pt)
+                        tc::umma_f16_tmem_a(to_, ts + (uint32_t)(32 * (k >> 1) + 16 * pt + 8 * (k & 1)),
+                                            vd + (uint64_t)(k * (2048 >> 4)), idesc_pv, (j > 0) || (pt + k > 0));
+                tc::umma_commit(&S.empty[slot]);
+                tc::umma_commit(&S.pv_done[qt]);
+                if (j + 1 < n) {
+                    // S takes the place of the weights that these MMAs read
+                    ok = tc::mbar_wait_spin(&S.pv_done[qt], j & 1, abort_flag, kWait) && qk(j + 1);
+                }
+            }
+            // tiles that only the other query tile sees
+            for (int i = 2 * n; ok && i < 2 * steps; ++i) {
+                const int slot = i % kSlots;
+                ok = tc::mbar_wait(&S.full[slot], (i / kSlots) & 1, abort_flag, kWait);
+                if (ok) tc::mbar_arrive(&S.empty[slot]);
+            }
+            if (!ok) fail();
+            // every MMA issued is done before TMEM and shared memory are left
+            tc::umma_commit(&S.drained[qt]);
+            tc::mbar_wait_drain(&S.drained[qt], 0, kWait / 8);
+        }
+        __syncwarp();
+    }
+    __syncthreads();
+    tc::tc_fence_after();
+    if (warp == kIssueWarp) tc::tmem_dealloc(tmem, 512);
+}
+
+// Joins the splits of every row that belongs to a sequence: one warp per (row, query head).
+template <int DT, int D>
+__global__ void __launch_bounds__(256) k_kv8_join_splits(const __grid_constant__ Kv8AttnArgs a, Kv8Parts parts, int splits) {
+    using T = typename Kv8T<DT>::type;
+    constexpr int VPL = D / 32;
+    const Kv8View& c = a.c;
+    const int lane = threadIdx.x & 31;
+    const long long unit = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+    const long long row = unit / a.q_heads;
+    if (row >= c.rows) return;
+    const int s = kv8_seq_of_row(c, row);
+    if (s < 0) return;
+    const Kv8Seq sq = kv8_seq(c, s);
+    if (row < sq.row0 || row >= sq.row0 + sq.n) return;
+    const int hh = (int)(unit - row * a.q_heads);
+    pdl_wait();
+    const long long step = c.rows * a.q_heads;
+    float m = -INFINITY;
+    for (int i = 0; i < splits; ++i) m = fmaxf(m, parts.m[i * step + unit]);
+    float l = 0.0f, o[VPL] = {};
+    for (int i = 0; i < splits; ++i) {
+        const float pm = parts.m[i * step + unit], pl = parts.l[i * step + unit];
+        if (pl == 0.0f) continue;   // a split that holds nothing the row sees has written no sums
+        const float k = pm == -INFINITY ? 1.0f : kvd::ex2(pm - m);   // -infinity with a sum: NaN
+        float v[VPL];
+        kv8_load<float, VPL>(parts.o + (i * step + unit) * D + VPL * lane, v);
+#pragma unroll
+        for (int j = 0; j < VPL; ++j) o[j] = fmaf(v[j], k, o[j]);
+        l = fmaf(pl, k, l);
+    }
+    const float inv = l == 0.0f ? 0.0f : __fdiv_rn(1.0f, l);
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) o[j] *= inv;
+    kv8_store<T, VPL>(static_cast<T*>(a.out.data) + row * a.out.row_stride + hh * a.out.head_stride + VPL * lane, o);
+    if (a.lse != nullptr && lane == 0)
+        a.lse[row * a.q_heads + hh] = l == 0.0f ? -INFINITY : (log2f(l) + (m - kvt::kBias)) * 0.69314718055994530942f;
+}
+
+}  // namespace i2s

@@ -84,11 +84,12 @@ def cached(pool, table, s, length, which):
 
 
 def attention(pool, table, kv_len, row_start, q, scale, causal, window):
-    """(out, lse, sum p|v|, largest sum |q||k| * scale) for each row and head, in 64 bits; rows of no sequence NaN."""
+    """(out, lse, sum p|v|, largest sum |q||k| * scale, tokens seen times the largest value that a block seen can hold)
+    for each row and head, in 64 bits; rows of no sequence NaN."""
     rows, heads, dim = q.shape
     group = heads // pool.heads
     out, lse = np.full((rows, heads, dim), np.nan), np.full((rows, heads), np.nan)
-    weight, size = np.zeros((rows, heads, dim)), np.zeros((rows, heads))
+    weight, size, reach = np.zeros((rows, heads, dim)), np.zeros((rows, heads)), np.zeros((rows, heads))
     for s, length in enumerate(kv_len):
         n = row_start[s + 1] - row_start[s]
         if n == 0:
@@ -97,6 +98,8 @@ def attention(pool, table, kv_len, row_start, q, scale, causal, window):
         v, _ = cached(pool, table, s, length, 1)
         pos = np.arange(length - n, length)[:, None]
         key = np.arange(length)
+        page = np.where(there, np.asarray(table[s])[key // pool.page], 0)
+        holds = 127.0 * pool.scales[page, :, 1, key % pool.page // BLOCK]
         seen = np.broadcast_to(there, (n, length)).copy()
         if causal:
             seen &= key <= pos
@@ -119,8 +122,9 @@ def attention(pool, table, kv_len, row_start, q, scale, causal, window):
                 p = np.where(total > 0, p / total, 0)
             out[at, h] = p @ vh
             weight[at, h] = p @ np.abs(vh)
+            reach[at, h] = seen.sum(1) * np.where(seen, holds[:, h // group], 0).max(1)
             size[at, h] = np.where(seen, np.abs(x) @ np.abs(kh).T * abs(scale), 0).max(1)
-    return out, lse, weight, size
+    return out, lse, weight, size, reach
 
 
 def norm_rope(x, gamma, eps, positions, turns, interleaved):

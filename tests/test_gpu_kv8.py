@@ -13,6 +13,9 @@ attention: with A the largest sum |q||k| * scale that the row sees, a logit is
   within A * 2^-18 (two f16 parts of q and up to 16 tensor-core steps of 2^-22
   each, then the scales), its exponential within 2^-18 * (A + 1) of itself, the
   sums over n tokens within (n/16 + 16) * 2^-22; twice that for the quotient.
+  The low f16 part of a weight is rounded to steps of 2^-24 at the finest, an
+  error of 2^-25 where the row's largest weight is at least 2^8: with n tokens
+  seen, n * 2^-33 of the largest value that a block seen can hold.
   Probabilities of 16-bit rows are rounded to f16, 2^-12 relative, or absolutely
   2^-25 of the largest of the row's running tile, both below 2^-11 of
   sum p|v| with the largest |v|; plus half a step of the dtype.
@@ -277,15 +280,15 @@ def check_attention(i2s, st, q, qf, dtype, causal=True, window=0, scale=None, ou
 
 
 def compare_attention(st, qf, dtype, causal, window, scale, out, lse, before):
-    want, want_lse, weight, size = ref.attention(st.pool, st.table, st.lens, st.row_start, qf, float(np.float32(scale)),
+    want, want_lse, weight, size, reach = ref.attention(st.pool, st.table, st.lens, st.row_start, qf, float(np.float32(scale)),
                                                  causal, window)
     got = out.float().cpu().numpy().astype(np.float64)
     last = st.row_start[-1]
     np.testing.assert_array_equal(got[last:], before[last:])   # rows behind the last sequence
-    got, want, weight, size, want_lse = got[:last], want[:last], weight[:last], size[:last], want_lse[:last]
+    got, want, weight, size, want_lse, reach = (x[:last] for x in (got, want, weight, size, want_lse, reach))
     n = max(st.lens + [1])
     rel = 2 * (2.0 ** -18 * (size + 1) * 2 + (n / 16 + 16) * 2.0 ** -22)
-    tol = weight * rel[..., None]
+    tol = weight * rel[..., None] + reach[..., None] * 2.0 ** -33
     if dtype != "f32":
         tol += weight.max(-1, keepdims=True) * 2.0 ** -11 + np.abs(want) * torch.finfo(DTYPES[dtype]).eps / 2 * 1.01 + 2.0 ** -24
     worst = np.abs(got - want) - tol
