@@ -29,11 +29,11 @@ struct TileCut {
 };
 constexpr int kSms = 152;
 
-static TileCut tile_cut(int heads, int q_heads, int seqs, int max_rows, long long rows, long long tokens, int window) {
+static TileCut tile_cut(int dtype, int heads, int q_heads, int seqs, int max_rows, long long rows, long long tokens, int window) {
     const long long rows_head = rows * (q_heads / heads);
     const int some = (int)std::min<long long>(seqs, rows);   // sequences that may have rows
     TileCut t;
-    t.query_tiles = heads * ((rows_head + 255) / 256) >= kSms ? 2 : 1;
+    t.query_tiles = dtype != kKvF32 && heads * ((rows_head + 255) / 256) >= kSms ? 2 : 1;
     const int per = t.query_tiles * kvt::kTileQ;
     t.items = (int)(heads * (rows_head / per + some));
     const long long likely = heads * std::max<long long>((rows_head + per - 1) / per, some);
@@ -48,10 +48,13 @@ static size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 size_t kv8_attention_ws(const Kv8View& c, int q_heads) {
     if (is_decode(c.heads, q_heads, c.max_rows))
         return plan_bytes(c.heads, c.seqs) + (size_t)2 * kvd::kMaxCtas * kvd::kRows * (c.dim + 2) * sizeof(float);
-    const TileCut t = tile_cut(c.heads, q_heads, c.seqs, c.max_rows, c.rows, c.width << c.page_shift, 0);
-    if (t.splits == 1) return 256;
-    const size_t units = (size_t)t.splits * c.rows * q_heads;
-    return up256(units * c.dim * sizeof(float)) + 2 * up256(units * sizeof(float));
+    size_t need = 256;   // for either dtype
+    for (int dtype : {kKvF32, kKvF16}) {
+        const TileCut t = tile_cut(dtype, c.heads, q_heads, c.seqs, c.max_rows, c.rows, c.width << c.page_shift, 0);
+        const size_t units = (size_t)t.splits * c.rows * q_heads;
+        if (t.splits > 1) need = std::max(need, up256(units * c.dim * sizeof(float)) + 2 * up256(units * sizeof(float)));
+    }
+    return need;
 }
 
 // Sets a kernel's shared memory once per device.
@@ -67,7 +70,7 @@ static cudaError_t allow_smem(K kernel, int bytes, std::atomic<unsigned long lon
 
 template <int DT, int D, int MT>
 static cudaError_t launch_tile(const Kv8AttnArgs& a, const TileCut& t, const Kv8Parts& parts, cudaStream_t s) {
-    constexpr int bytes = kvt::smem_bytes<D, DT == kKvF32 ? 2 : 1>();
+    constexpr int bytes = kvt::smem_bytes<D, DT == kKvF32 ? 2 : 1, MT>();
     static_assert(bytes <= 232448, "shared memory");
     static std::atomic<unsigned long long> ready{0};   // a bit per device
     const cudaError_t e = allow_smem(k_kv8_tile<DT, D, MT>, bytes, ready);
@@ -95,7 +98,7 @@ static cudaError_t launch_decode(const Kv8AttnArgs& a, void* ws, cudaStream_t s)
 template <int DT, int D>
 static cudaError_t launch_dt(const Kv8AttnArgs& a, void* ws, cudaStream_t s) {
     if (is_decode(a.c.heads, a.q_heads, a.c.max_rows)) return launch_decode<DT, D>(a, ws, s);
-    const TileCut t = tile_cut(a.c.heads, a.q_heads, a.c.seqs, a.c.max_rows, a.c.rows, a.c.width << a.c.page_shift, a.window);
+    const TileCut t = tile_cut(DT, a.c.heads, a.q_heads, a.c.seqs, a.c.max_rows, a.c.rows, a.c.width << a.c.page_shift, a.window);
     Kv8Parts parts = {nullptr, nullptr, nullptr};
     const size_t units = (size_t)t.splits * a.c.rows * a.q_heads;
     if (t.splits > 1) {
@@ -103,7 +106,9 @@ static cudaError_t launch_dt(const Kv8AttnArgs& a, void* ws, cudaStream_t s) {
         parts.m = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + up256(units * D * sizeof(float)));
         parts.l = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(parts.m) + up256(units * sizeof(float)));
     }
-    const cudaError_t e = t.query_tiles == 2 ? launch_tile<DT, D, 2>(a, t, parts, s) : launch_tile<DT, D, 1>(a, t, parts, s);
+    cudaError_t e;
+    if constexpr (DT == kKvF32) e = launch_tile<DT, D, 1>(a, t, parts, s);
+    else e = t.query_tiles == 2 ? launch_tile<DT, D, 2>(a, t, parts, s) : launch_tile<DT, D, 1>(a, t, parts, s);
     if (e != cudaSuccess || t.splits == 1) return e;
     const dim3 grid((unsigned)((a.c.rows * a.q_heads + 7) / 8));
     return launch_pdl(k_kv8_join_splits<DT, D>, grid, dim3(256), 0, s, a, parts, t.splits);

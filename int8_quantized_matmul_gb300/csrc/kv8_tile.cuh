@@ -21,21 +21,34 @@
 // one part after the scaling (f16's 11 bits hold bf16's 8), and their weights
 // are rounded once to f16, 2^-12, below the half step of the output.
 //
-// Roles (14 warps, one CTA per SM):
-//   warps 0-3, 4-7   softmax of query tile 0, 1: one thread per row (TMEM lane);
-//                    they also stage Q, rescale O and write the output
-//   warps 8-11       producer: int8 K and V from global memory, a tile ahead in
-//                    registers, to f16 in 128-byte-swizzled shared memory
-//   warps 12, 13     one thread issues the MMAs of query tile 0, 1
-// TMEM (512 columns): S of each query tile (128 columns of f32), overwritten in
-// place by the weights (32 columns of S become 16 of high and 16 of low
-// parts), and O of each (D columns). With two query tiles one's softmax runs
-// while the other's MMAs do. K is the K-major operand [token][d]; V with the
-// same bytes is the MN-major operand.
+// Accumulation. The tensor core cuts each MMA's sum off below 2^-24 of the
+// accumulator, always towards zero, so a long chain loses: over 4000 tokens
+// 9e-6 of O was measured. For F32 rows O is therefore moved every kChain tiles
+// into a running sum that is added to with rounding (1e-6).
+//
+// Two shapes. MT = 2 (16-bit rows, where there are enough of them): two query
+// tiles per CTA share each converted tile of the cache, one's softmax runs while
+// the other's MMAs do; a thread has a whole row. MT = 1: one query tile, two S
+// buffers, so that Q K^T of the next tile runs during the softmax; a row's 128
+// columns belong to two threads, which exchange their maxima.
+//
+// Roles (16 warps, one CTA per SM):
+//   warps 0-7    softmax (MT = 2: 0-3 query tile 0, 4-7 tile 1; MT = 1: 0-3 the
+//                first 64 tokens of a tile, 4-7 the others); they also stage Q,
+//                rescale O and write the output
+//   warps 8-11   producer: int8 K and V by cp.async, kStages operands ahead, each
+//                thread its own chunks, to f16 in 128-byte-swizzled shared memory
+//   warps 12, 13 one thread each issues MMAs (MT = 2: of query tile 0, 1; MT = 1:
+//                Q K^T, P V)
+// TMEM (512 columns): S (2 x 128 columns of f32), overwritten in place by the
+// weights (32 columns of S become 16 of high and 16 of low parts), and O (MT x D,
+// for F32 rows and the running sum). K is the K-major operand [token][d]; V with
+// the same bytes is the MN-major operand.
 //
 // A slot of the ring holds K or V of one tile, in the order K0 V0 K1 V1 ...
-// full[] counts the 128 producer threads, empty[] the query tiles' commits.
-// Every wait is bounded; one that runs out sets KV8_TIMEOUT.
+// full[] counts the 128 producer threads, empty[] the commits of the MMAs that
+// read it. Barriers that two steps could reach at once exist twice, used by
+// turns. Every wait is bounded; one that runs out sets KV8_TIMEOUT.
 #pragma once
 
 #include "kv8_decode.cuh"
@@ -48,34 +61,40 @@ namespace kvt {
 constexpr int kTileQ = 128;
 constexpr int kTileKv = 128;
 constexpr int kBlocks = kTileKv / kKvBlock;
-constexpr int kThreads = 14 * 32;
+constexpr int kThreads = 512;
 constexpr int kProducerWarp = 8;
 constexpr int kIssueWarp = 12;
 constexpr float kBias = 8.0f;
 constexpr float kSlack = 6.0f;
 constexpr long long kWait = 2000000000LL;
-constexpr int kConsts = 4;           // tiles whose scales are kept: the producer is at most two ahead
+constexpr int kChain = 4;            // tiles summed in one accumulator (F32 rows)
+constexpr int kSlots = 3;            // operands of the ring
+constexpr int kStages = 3;           // int8 operands on their way
+constexpr int kConsts = 8;           // tiles whose scales are kept: fewer than that are under way
 constexpr int kHalf = kTileKv * 128; // bytes of 64 columns of 128 rows of f16
+// Registers of a thread after the split (of the 128 at launch): softmax,
+// producer, issue. 256 * 168 + 128 * 96 + 128 * 64 <= 512 * 128.
+constexpr int kRegsSoftmax = 168, kRegsProducer = 96, kRegsIssue = 64;
 
 template <int D>
 __host__ __device__ constexpr int operand_bytes() { return kTileKv * D * 2; }
-template <int D, int PARTS>
-__host__ __device__ constexpr int slots_of() { return D == 128 ? (PARTS == 2 ? 3 : 4) : 6; }
 
 struct Shared {
-    uint64_t full[6], empty[6], cfull[kConsts];
-    uint64_t q_ready[2], s_full[2], p_ready[2], pv_done[2], drained[2];
+    uint64_t full[kSlots], empty[kSlots], cfull[kConsts];
+    uint64_t q_ready[2], s_full[2], p_ready[2], pv_done[2], drained[2], x_ready[2], l_ready;
     float ks[kConsts][kBlocks], lv[kConsts][kBlocks], iv[kConsts][kBlocks];
-    float mul[2][kTileQ];
+    float raw[kConsts][2 * kBlocks];
+    float mul[2 * kTileQ];
+    float top[2][2][kTileQ], lsum[2][kTileQ];
     uint32_t tmem;
     int abort;
     int scan[kThreads / 32];
     int item[2];   // sequence, first row of the item in it
 };
 
-template <int D, int PARTS>
+template <int D, int PARTS, int MT>
 __host__ __device__ constexpr int smem_bytes() {
-    return 1024 + (2 * PARTS + slots_of<D, PARTS>()) * operand_bytes<D>() + (int)sizeof(Shared);
+    return 1024 + (MT * PARTS + kSlots) * operand_bytes<D>() + kStages * operand_bytes<D>() / 2 + (int)sizeof(Shared);
 }
 
 // MN-major operand in the 128-byte-swizzled canonical layout: rows (k) of 64
@@ -92,6 +111,27 @@ __device__ __forceinline__ uint64_t sdesc_sw128_mnmajor(uint32_t saddr) {
 constexpr uint32_t kTransposeB = 1u << 16;   // B is MN-major (instruction descriptor)
 
 __device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
+// 16 bytes, or zeros.
+__device__ __forceinline__ void cp16z(uint32_t dst, const void* src, bool there) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+
+// A thread's share of one tile of S: COLS columns from `ts`, in pieces of 32.
+// fetch(piece) loads one (once, if it is kept).
+template <int COLS, bool KEEP>
+struct Scores {
+    uint32_t v[KEEP ? COLS : 32];
+    __device__ __forceinline__ void fetch(uint32_t ts, int piece) {
+        uint32_t(&w)[32] = *reinterpret_cast<uint32_t(*)[32]>(&v[KEEP ? 32 * piece : 0]);
+        tc::tmem_ld_32x32b_x32(ts + 32u * piece, w);
+    }
+    __device__ __forceinline__ float at(int i) const { return __uint_as_float(v[KEEP ? i : i & 31]); }
+    __device__ __forceinline__ void hide(int i) { v[KEEP ? i : i & 31] = 0xff800000u; }
+};
 
 }  // namespace kvt
 
@@ -110,14 +150,16 @@ __global__ void __launch_bounds__(kvt::kThreads, 1)
     using kvd::ex2;
     using T = typename Kv8T<DT>::type;
     constexpr int PARTS = DT == kKvF32 ? 2 : 1;
-    constexpr int kSlots = slots_of<D, PARTS>();
+    static_assert(MT == 1 || PARTS == 1, "F32 rows need the columns of the second tile for their running sum");
+    constexpr bool kChained = PARTS == 2;
     constexpr int kOp = operand_bytes<D>();
     constexpr int kKSteps = D / 16, kVSteps = kTileKv / 16;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     uint8_t* sQ = smem;                                  // [query tile][part]
-    uint8_t* sKV = smem + 2 * PARTS * kOp;               // ring
-    Shared& S = *reinterpret_cast<Shared*>(sKV + kSlots * kOp);
+    uint8_t* sKV = smem + MT * PARTS * kOp;              // ring of f16 operands
+    uint8_t* sRaw = sKV + kSlots * kOp;                  // ring of int8 operands
+    Shared& S = *reinterpret_cast<Shared*>(sRaw + kStages * kOp / 2);
 
     const Kv8View& c = a.c;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -166,12 +208,14 @@ __global__ void __launch_bounds__(kvt::kThreads, 1)
         }
         for (int i = 0; i < kConsts; ++i) tc::mbar_init(&S.cfull[i], 32);
         for (int i = 0; i < 2; ++i) {
-            tc::mbar_init(&S.q_ready[i], 128);
+            tc::mbar_init(&S.q_ready[i], 256 / MT);
             tc::mbar_init(&S.s_full[i], 1);
-            tc::mbar_init(&S.p_ready[i], 128);
+            tc::mbar_init(&S.p_ready[i], 256 / MT);
             tc::mbar_init(&S.pv_done[i], 1);
             tc::mbar_init(&S.drained[i], 1);
+            tc::mbar_init(&S.x_ready[i], 256);
         }
+        tc::mbar_init(&S.l_ready, 256);
         S.abort = 0;
         tc::fence_mbar_init();
     }
@@ -213,22 +257,30 @@ __global__ void __launch_bounds__(kvt::kThreads, 1)
         atomicOr(c.status, kKvTimeout);
     };
 
-    if (warp < 4 * MT) {
+    constexpr uint32_t kColO = 2 * kTileKv, kColRun = kColO + D;   // O of tile 0, running sum (or O of tile 1)
+
+    if (warp < 8) {
         // ------------------------------------------------------------ softmax
-        const int qt = warp >> 2, r = tid & 127;
+        regs_up<kRegsSoftmax>();
+        // qt: the query tile; h: which half of a row's columns (MT = 1)
+        const int qt = MT == 2 ? warp >> 2 : 0, h = MT == 1 ? warp >> 2 : 0, r = tid & 127;
         const int n = steps_of(qt);
         const int tile_row = row_lo + qt * kTileQ;
+        constexpr int COLS = MT == 2 ? kTileKv : kTileKv / 2;
+        constexpr int OC = MT == 2 ? D : D / 2;   // columns of O that a thread has
         if (n > 0) {
-            // Q: each warp its 32 rows, a lane 4 (D = 128) or 2 consecutive values
+            // Q: each warp 32 (MT = 2) or 16 of the rows, a lane 4 (D = 128) or 2 consecutive values
             constexpr int VPL = D / 32;
+            constexpr int kWarpRows = MT == 2 ? 32 : 16;
+            const int r0 = (MT == 2 ? warp & 3 : warp) * kWarpRows;
             uint8_t* q0 = sQ + qt * PARTS * kOp;
             constexpr int kBatch = 8;
 #pragma unroll 1
-            for (int i0 = 0; i0 < 32; i0 += kBatch) {
+            for (int i0 = 0; i0 < kWarpRows; i0 += kBatch) {
                 float x[kBatch][VPL];
 #pragma unroll
                 for (int i = 0; i < kBatch; ++i) {
-                    const int row = tile_row + (warp & 3) * 32 + i0 + i;
+                    const int row = tile_row + r0 + i0 + i;
                     if (row < row_hi) {
                         const int ti = row / group, hh = head * group + row - ti * group;
                         kv8_load<T, VPL>(static_cast<const T*>(a.q.data) + (sq.row0 + ti) * a.q.row_stride +
@@ -240,7 +292,7 @@ __global__ void __launch_bounds__(kvt::kThreads, 1)
                 }
 #pragma unroll
                 for (int i = 0; i < kBatch; ++i) {
-                    const int rr = (warp & 3) * 32 + i0 + i;
+                    const int rr = r0 + i0 + i;
                     uint32_t top = 0;
 #pragma unroll
                     for (int j = 0; j < VPL; ++j) top = max(top, __float_as_uint(x[i][j]) & 0x7fffffffu);
@@ -248,7 +300,7 @@ __global__ void __launch_bounds__(kvt::kThreads, 1)
                     float up, down;
                     kvd::row_scale(top, up, down);
                     // mul is not negative, so the largest S of a block is the largest logit
-                    if (lane == 0) S.mul[qt][rr] = down * (fabsf(a.scale) * 1.44269504088896340736f);
+                    if (lane == 0) S.mul[qt * kTileQ + rr] = down * (fabsf(a.scale) * 1.44269504088896340736f);
                     if (a.scale < 0.0f) up = -up;
                     uint32_t hi[VPL / 2], lo[VPL / 2];
 #pragma unroll
@@ -265,14 +317,13 @@ __global__ void __launch_bounds__(kvt::kThreads, 1)
                 }
             }
             tc::fence_proxy_async_smem();
-            __syncwarp();
             tc::mbar_arrive(&S.q_ready[qt]);
         }
         const int row = tile_row + r;
         const bool live = row < row_hi;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-        const uint32_t ts = tmem + lanes + (uint32_t)qt * kTileKv;
-        const uint32_t to_ = tmem + lanes + (uint32_t)(MT * kTileKv + qt * D);
+        const uint32_t to_ = tmem + lanes + kColO + (uint32_t)(qt * D + h * OC);
+        const uint32_t tr = tmem + lanes + kColRun + (uint32_t)(h * OC);
         int see_lo = 0, see_hi = 0;
         if (live) {
             see_hi = (int)last_seen(row);
@@ -280,96 +331,155 @@ __global__ void __launch_bounds__(kvt::kThreads, 1)
         }
         const int all_lo = __reduce_max_sync(0xffffffffu, live ? see_lo : 0);
         const int all_hi = __reduce_min_sync(0xffffffffu, live ? see_hi : 0x7fffffff);
-        const float mul = n > 0 ? S.mul[qt][r] : 0.0f;   // written by this warp
-        float m = -INFINITY, l = 0.0f;
         bool ok = true;
-        for (int j = 0; j < n; ++j) {
+        // a wait that every lane of the warp takes, and gives up together
+        auto wait = [&](uint64_t* bar, int parity) {
+            if (!tc::mbar_wait(bar, (uint32_t)parity, abort_flag, kWait)) { fail(); ok = false; }
+            ok = !__any_sync(0xffffffffu, !ok);
+            return ok;
+        };
+        float mul = 0.0f;
+        if (n > 0 && wait(&S.q_ready[qt], 0)) mul = S.mul[qt * kTileQ + r];
+        float m = -INFINITY, l = 0.0f, m_run = -INFINITY;
+        for (int j = 0; ok && j < n; ++j) {
             const int cs = j % kConsts;
-            if (!tc::mbar_wait(&S.cfull[cs], (j / kConsts) & 1, abort_flag, kWait) ||
-                !tc::mbar_wait(&S.s_full[qt], j & 1, abort_flag, kWait)) { fail(); ok = false; }
-            if (__any_sync(0xffffffffu, !ok)) { ok = false; break; }
+            const int bf = MT == 2 ? qt : j & 1, ph = MT == 2 ? j & 1 : (j >> 1) & 1;
+            if (!wait(&S.cfull[cs], (j / kConsts) & 1) || !wait(&S.s_full[bf], ph)) break;
             tc::tc_fence_after();
+            const uint32_t ts = tmem + lanes + (uint32_t)(bf * kTileKv + h * COLS);
             const int tok = (from + j) * kTileKv;
             const bool masked = tok < all_lo || tok + kTileKv > all_hi;   // for some row of the warp
-            const int lo = see_lo - tok, hi = see_hi - tok;
+            const int lo = see_lo - tok - h * COLS, hi = see_hi - tok - h * COLS;
+            const float* ks = &S.ks[cs][h * (COLS / kKvBlock)];
+            const float* lv = &S.lv[cs][h * (COLS / kKvBlock)];
+            const float* iv = &S.iv[cs][h * (COLS / kKvBlock)];
+            Scores<COLS, MT == 1> x;
             float top = -INFINITY;
+            if (MT == 1) {
 #pragma unroll
-            for (int ch = 0; ch < 4; ++ch) {
-                uint32_t v[32];
-                tc::tmem_ld_32x32b_x32(ts + 32u * ch, v);
+                for (int ch = 0; ch < COLS / 32; ++ch) x.fetch(ts, ch);
                 tc::tmem_ld_wait();
+            }
+#pragma unroll
+            for (int ch = 0; ch < COLS / 32; ++ch) {
+                if (MT == 2) {
+                    x.fetch(ts, ch);
+                    tc::tmem_ld_wait();
+                }
                 if (masked) {
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        if (32 * ch + i < lo || 32 * ch + i >= hi) v[i] = 0xff800000u;   // -infinity
+                    for (int i = 32 * ch; i < 32 * ch + 32; ++i)
+                        if (i < lo || i >= hi) x.hide(i);
                 }
 #pragma unroll
-                for (int b = 0; b < 2; ++b) {
+                for (int b = 2 * ch; b < 2 * ch + 2; ++b) {
                     float t0 = -INFINITY, t1 = -INFINITY;
 #pragma unroll
-                    for (int i = 0; i < 16; i += 4) {
-                        t0 = max3(t0, __uint_as_float(v[16 * b + i]), __uint_as_float(v[16 * b + i + 1]));
-                        t1 = max3(t1, __uint_as_float(v[16 * b + i + 2]), __uint_as_float(v[16 * b + i + 3]));
+                    for (int i = 16 * b; i < 16 * b + 16; i += 4) {
+                        t0 = max3(t0, x.at(i), x.at(i + 1));
+                        t1 = max3(t1, x.at(i + 2), x.at(i + 3));
                     }
-                    t0 = fmaxf(t0, t1);
                     // a zero scale times -infinity would be NaN, which the maximum ignores
-                    top = fmaxf(top, fmaf(t0, mul * S.ks[cs][2 * ch + b], S.lv[cs][2 * ch + b]));
+                    top = fmaxf(top, fmaf(fmaxf(t0, t1), mul * ks[b], lv[b]));
                 }
             }
-            if (__any_sync(0xffffffffu, top > m + kSlack)) {
+            if (MT == 1) {   // the row's other half
+                S.top[bf][h][r] = top;
+                tc::mbar_arrive(&S.x_ready[bf]);
+                if (!wait(&S.x_ready[bf], ph)) break;
+                top = fmaxf(top, S.top[bf][h ^ 1][r]);
+            }
+            const bool grown = __any_sync(0xffffffffu, top > m + kSlack);
+            const bool flush = kChained && j > 0 && j % kChain == 0;
+            float keep = 1.0f;
+            if (grown) {
                 const float nm = fmaxf(m, top);
-                const float keep = nm == -INFINITY ? 1.0f : ex2(m - nm);
+                keep = nm == -INFINITY ? 1.0f : ex2(m - nm);
                 m = nm;
                 l *= keep;
-                if (j > 0) {   // the MMAs into O are done: S came after them
+            }
+            if ((grown && j > 0) || flush) {
+                // O holds the tiles before this one; with two S buffers their MMAs may still run
+                if (MT == 1) {
+                    if (!wait(&S.pv_done[(j - 1) & 1], ((j - 1) >> 1) & 1)) break;
+                    tc::tc_fence_after();
+                }
+                if (flush) {
+                    const bool first = j == kChain;
+                    const float keep_run = m == -INFINITY ? 1.0f : ex2(m_run - m);
+                    m_run = m;
 #pragma unroll 1
-                    for (int ch = 0; ch < D / 32; ++ch) {
-                        uint32_t v[32];
-                        tc::tmem_ld_32x32b_x32(to_ + 32u * ch, v);
+                    for (int ch = 0; ch < OC / 16; ++ch) {
+                        uint32_t o[16], v[16];
+                        tc::tmem_ld_32x32b_x16(to_ + 16u * ch, o);
+                        if (!first) tc::tmem_ld_32x32b_x16(tr + 16u * ch, v);
                         tc::tmem_ld_wait();
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * keep);
-                        tc::tmem_st_32x32b_x32(to_ + 32u * ch, v);
+                        for (int i = 0; i < 16; ++i) {
+                            const float y = __uint_as_float(o[i]) * keep;
+                            v[i] = __float_as_uint(first ? y : fmaf(__uint_as_float(v[i]), keep_run, y));
+                        }
+                        tc::tmem_st_32x32b_x16(tr + 16u * ch, v);
+                    }
+                } else {
+#pragma unroll 1
+                    for (int ch = 0; ch < OC / 16; ++ch) {
+                        uint32_t v[16];
+                        tc::tmem_ld_32x32b_x16(to_ + 16u * ch, v);
+                        tc::tmem_ld_wait();
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * keep);
+                        tc::tmem_st_32x32b_x16(to_ + 16u * ch, v);
                     }
                 }
             }
             const float sub = m == -INFINITY ? 0.0f : m - kBias;
 #pragma unroll
-            for (int ch = 0; ch < 4; ++ch) {
-                uint32_t v[32];
-                tc::tmem_ld_32x32b_x32(ts + 32u * ch, v);
-                tc::tmem_ld_wait();
+            for (int ch = 0; ch < COLS / 32; ++ch) {
+                if (MT == 2) {
+                    x.fetch(ts, ch);
+                    tc::tmem_ld_wait();
+                    if (masked) {
+#pragma unroll
+                        for (int i = 32 * ch; i < 32 * ch + 32; ++i)
+                            if (i < lo || i >= hi) x.hide(i);
+                    }
+                }
                 uint32_t hi16[16], lo16[16];
 #pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                    const float xm = mul * S.ks[cs][2 * ch + b], add = S.lv[cs][2 * ch + b] - sub;
+                for (int b = 2 * ch; b < 2 * ch + 2; ++b) {
+                    const float xm = mul * ks[b], add = lv[b] - sub;
                     float sum0 = 0.0f, sum1 = 0.0f;
 #pragma unroll
-                    for (int i = 0; i < 16; i += 2) {
-                        const int k = 16 * b + i;
-                        float w0 = ex2(fmaf(__uint_as_float(v[k]), xm, add));
-                        float w1 = ex2(fmaf(__uint_as_float(v[k + 1]), xm, add));
-                        if (masked) {
-                            if (32 * ch + k < lo || 32 * ch + k >= hi) w0 = 0.0f;
-                            if (32 * ch + k + 1 < lo || 32 * ch + k + 1 >= hi) w1 = 0.0f;
+                    for (int i = 16 * b; i < 16 * b + 16; i += 2) {
+                        float w0 = ex2(fmaf(x.at(i), xm, add)), w1 = ex2(fmaf(x.at(i + 1), xm, add));
+                        if (masked) {   // also where the block's scale is NaN
+                            if (i < lo || i >= hi) w0 = 0.0f;
+                            if (i + 1 < lo || i + 1 >= hi) w1 = 0.0f;
                         }
                         sum0 += w0;
                         sum1 += w1;
-                        if (PARTS == 2) kvd::split2(w0, w1, hi16[k / 2], lo16[k / 2]);
-                        else hi16[k / 2] = kvd::pack2(w0, w1);
+                        const int p = (i & 31) / 2;
+                        if (PARTS == 2) kvd::split2(w0, w1, hi16[p], lo16[p]);
+                        else hi16[p] = kvd::pack2(w0, w1);
                     }
-                    l = fmaf(sum0 + sum1, S.iv[cs][2 * ch + b], l);
+                    l = fmaf(sum0 + sum1, iv[b], l);
                 }
                 tc::tmem_st_32x32b_x16(ts + 32u * ch, hi16);
                 if (PARTS == 2) tc::tmem_st_32x32b_x16(ts + 32u * ch + 16u, lo16);
             }
             tc::tmem_st_wait();
             tc::tc_fence_before();
-            tc::mbar_arrive(&S.p_ready[qt]);
+            tc::mbar_arrive(&S.p_ready[bf]);
         }
-        if (n > 0 && ok) {
-            if (!tc::mbar_wait(&S.pv_done[qt], (n - 1) & 1, abort_flag, kWait)) { fail(); ok = false; }
-            ok = !__any_sync(0xffffffffu, !ok);
+        if (MT == 1 && ok) {   // l of both halves
+            S.lsum[h][r] = l;
+            tc::mbar_arrive(&S.l_ready);
+            if (wait(&S.l_ready, 0)) l += S.lsum[h ^ 1][r];
+        }
+        if (ok && n > 0) {
+            const int last = n - 1;
+            wait(&S.pv_done[MT == 2 ? qt : last & 1], MT == 2 ? last & 1 : (last >> 1) & 1);
             tc::tc_fence_after();
         }
         if (ok) {
@@ -378,7 +488,9 @@ __global__ void __launch_bounds__(kvt::kThreads, 1)
             const bool split = gridDim.y > 1;
             const long long part = ((long long)blockIdx.y * c.rows + grow) * a.q_heads + hh;
             const float inv = split ? 1.0f : (l == 0.0f ? 0.0f : __fdiv_rn(1.0f, l));
-            if (live) {
+            const bool ran = kChained && n > kChain;
+            const float keep_run = m == -INFINITY ? 1.0f : ex2(m_run - m);
+            if (live && h == 0) {
                 if (split) {
                     parts.m[part] = m;
                     parts.l[part] = l;
@@ -389,29 +501,38 @@ __global__ void __launch_bounds__(kvt::kThreads, 1)
             }
             if (!split || n > 0) {
 #pragma unroll 1
-                for (int ch = 0; ch < D / 32; ++ch) {
+                for (int ch = 0; ch < OC / 32; ++ch) {
                     uint32_t v[32];
                     if (n > 0) {
                         tc::tmem_ld_32x32b_x32(to_ + 32u * ch, v);
                         tc::tmem_ld_wait();
+                        if (ran) {
+                            uint32_t w[32];
+                            tc::tmem_ld_32x32b_x32(tr + 32u * ch, w);
+                            tc::tmem_ld_wait();
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                v[i] = __float_as_uint(fmaf(__uint_as_float(w[i]), keep_run, __uint_as_float(v[i])));
+                        }
                     } else {
 #pragma unroll
                         for (int i = 0; i < 32; ++i) v[i] = 0u;
                     }
+                    const int d0 = h * OC + 32 * ch;
                     if (live && split) {
-                        float* dst = parts.o + part * D + 32 * ch;
+                        float* dst = parts.o + part * D + d0;
 #pragma unroll
                         for (int i = 0; i < 32; i += 4)
                             *reinterpret_cast<uint4*>(dst + i) = make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
                     } else if (live) {
-                        T* dst = static_cast<T*>(a.out.data) + grow * a.out.row_stride + hh * a.out.head_stride + 32 * ch;
+                        T* dst = static_cast<T*>(a.out.data) + grow * a.out.row_stride + hh * a.out.head_stride + d0;
                         constexpr int W = 16 / sizeof(T);
 #pragma unroll
                         for (int i = 0; i < 32; i += W) {
-                            float x[W];
+                            float y[W];
 #pragma unroll
-                            for (int k = 0; k < W; ++k) x[k] = __uint_as_float(v[i + k]) * inv;
-                            kv8_store<T, W>(dst + i, x);
+                            for (int k = 0; k < W; ++k) y[k] = __uint_as_float(v[i + k]) * inv;
+                            kv8_store<T, W>(dst + i, y);
                         }
                     }
                     __syncwarp();
@@ -419,77 +540,96 @@ __global__ void __launch_bounds__(kvt::kThreads, 1)
             }
         }
         tc::tc_fence_before();
-    } else if (warp >= kProducerWarp && warp < kIssueWarp) {
+    } else if (warp < kIssueWarp) {
         // ----------------------------------------------------------- producer
+        regs_down<kRegsProducer>();
         const int p = tid - kProducerWarp * 32;
-        constexpr int kChunks = D / 16;          // 16-byte chunks of a token's codes
-        constexpr int kLoads = kChunks;          // per thread and operand: 128 * kChunks / 128
+        constexpr int kChunks = D / 16;          // 16-byte chunks of a token's codes, and loads per thread and operand
         const int* table = c.table + (long long)s * c.width;
-        uint4 reg[kLoads];
-        int pages = -1;   // lane i < 8: the page of block i of the current tile, -1: none
+        const uint32_t raw = kvd::smem_addr(sRaw) + 16 * p;
+        // lane i < 8 of each warp: the page of block i of tile j, -1: none
         auto fetch_pages = [&](int j) {
-            pages = -1;
+            int page = -1;
             const long long tok = (long long)(from + j) * kTileKv + (lane & 7) * kKvBlock;
             if (j < steps && tok < sq.len) {
-                pages = table[tok >> c.page_shift];
-                if (pages < 0 || pages >= c.n_pages) {
+                page = table[tok >> c.page_shift];
+                if (page < 0 || page >= c.n_pages) {
                     if (warp == kProducerWarp) atomicOr(c.status, kKvBadPage);
-                    pages = -1;
+                    page = -1;
                 }
             }
+            return page;
         };
-        auto load = [&](int j, int which) {
+        int pages = fetch_pages(0), pages_next = fetch_pages(1);
+        unsigned present = 0;   // bit j % kConsts: this lane's block of tile j is there
+        auto issue = [&](int i) {   // operand i: K or V of tile i / 2
+            if (i < 2 * steps) {
+                const int j = i >> 1, which = i & 1;
+                const uint32_t dst = raw + (uint32_t)(i % kStages) * (kOp / 2);
 #pragma unroll
-            for (int i = 0; i < kLoads; ++i) {
-                const int idx = i * 128 + p, r = idx / kChunks, cc = idx % kChunks;
-                const int page = __shfl_sync(0xffffffffu, pages, r >> 4);
-                if (page >= 0) {
+                for (int q = 0; q < kChunks; ++q) {
+                    const int idx = q * 128 + p, r = idx / kChunks, cc = idx % kChunks;
+                    const int page = __shfl_sync(0xffffffffu, pages, r >> 4);
                     const int tok = ((from + j) * kTileKv + r) & ((1 << c.page_shift) - 1);
-                    reg[i] = *reinterpret_cast<const uint4*>(c.pages + ((long long)page * c.heads + head) * c.slab +
-                                                             kv8_code_off(c, which, tok) + 16 * cc);
+                    const uint8_t* src = c.pages;
+                    if (page >= 0) src += ((long long)page * c.heads + head) * c.slab + kv8_code_off(c, which, tok) + 16 * cc;
+                    cp16z(dst + 2048u * q, src, page >= 0);
+                }
+                if (which == 0) {
+                    const int cs = j % kConsts;
+                    present &= ~(1u << cs);
+                    if (warp == kProducerWarp && lane < kBlocks && pages >= 0) {
+                        present |= 1u << cs;
+                        const int tok = ((from + j) * kTileKv + lane * kKvBlock) & ((1 << c.page_shift) - 1);
+                        const uint8_t* slab = c.pages + ((long long)pages * c.heads + head) * c.slab;
+                        kvd::cp4(kvd::smem_addr(&S.raw[cs][lane]), slab + kv8_scale_off(c, 0, tok));
+                        kvd::cp4(kvd::smem_addr(&S.raw[cs][kBlocks + lane]), slab + kv8_scale_off(c, 1, tok));
+                    }
                 } else {
-                    reg[i] = make_uint4(0u, 0u, 0u, 0u);
+                    pages = pages_next;
+                    pages_next = fetch_pages(j + 2);
                 }
             }
+            kvd::cp_commit();
         };
-        auto scales = [&](int j) {   // the first producer warp, lane i < 8: block i
-            const int cs = j % kConsts;
-            if (lane < kBlocks) {
-                float k = 0.0f, lv = -INFINITY, iv = 0.0f;
-                if (pages >= 0) {
-                    const int tok = ((from + j) * kTileKv + lane * kKvBlock) & ((1 << c.page_shift) - 1);
-                    const uint8_t* slab = c.pages + ((long long)pages * c.heads + head) * c.slab;
-                    k = *reinterpret_cast<const float*>(slab + kv8_scale_off(c, 0, tok));
-                    const float v = *reinterpret_cast<const float*>(slab + kv8_scale_off(c, 1, tok));
-                    // a scale that no written block has (0 among them) counts as 2^-40
-                    const float some = v < 0x1p-40f ? 0x1p-40f : v;
-                    lv = log2f(some);
-                    // NaN weights make l NaN for the rows that see the block; the others add 0 * 1
-                    iv = v == v ? __fdiv_rn(1.0f, some) : 1.0f;
-                }
-                S.ks[cs][lane] = k;
-                S.lv[cs][lane] = lv;
-                S.iv[cs][lane] = iv;
-            }
-            tc::mbar_arrive(&S.cfull[cs]);
-        };
-        bool ok = true;
-        fetch_pages(0);
-        if (steps > 0) load(0, 0);
-        for (int i = 0; i < 2 * steps && ok; ++i) {
+#pragma unroll 1
+        for (int i = 0; i < kStages - 1; ++i) issue(i);
+        for (int i = 0; i < 2 * steps; ++i) {
             const int slot = i % kSlots, use = i / kSlots, which = i & 1;
-            if (!tc::mbar_wait_idle(&S.empty[slot], (use & 1) ^ 1, abort_flag, kWait)) { fail(); ok = false; break; }
-            if (which == 0 && warp == kProducerWarp) scales(i >> 1);
+            bool ok = tc::mbar_wait_idle(&S.empty[slot], (use & 1) ^ 1, abort_flag, kWait);
+            if (!ok) fail();
+            if (__any_sync(0xffffffffu, !ok)) break;
+            kvd::cp_wait<kStages - 2>();   // this thread's chunks of operand i are here
+            if (which == 0 && warp == kProducerWarp) {
+                const int j = i >> 1, cs = j % kConsts;
+                if (lane < kBlocks) {
+                    float k = 0.0f, lv = -INFINITY, iv = 0.0f;
+                    if (present >> cs & 1) {
+                        k = S.raw[cs][lane];
+                        const float v = S.raw[cs][kBlocks + lane];
+                        // a scale that no written block has (0 among them) counts as 2^-40
+                        const float some = v < 0x1p-40f ? 0x1p-40f : v;
+                        lv = log2f(some);
+                        // NaN weights make l NaN for the rows that see the block; the others add 0 * 1
+                        iv = v == v ? __fdiv_rn(1.0f, some) : 1.0f;
+                    }
+                    S.ks[cs][lane] = k;
+                    S.lv[cs][lane] = lv;
+                    S.iv[cs][lane] = iv;
+                }
+                tc::mbar_arrive(&S.cfull[cs]);
+            }
+            const uint8_t* src = sRaw + (i % kStages) * (kOp / 2) + 16 * p;
             uint8_t* dst = sKV + slot * kOp;
 #pragma unroll
-            for (int q = 0; q < kLoads; ++q) {
+            for (int q = 0; q < kChunks; ++q) {
                 const int idx = q * 128 + p, r = idx / kChunks, cc = idx % kChunks;
-                const uint32_t w[4] = {reg[q].x ^ 0x80808080u, reg[q].y ^ 0x80808080u, reg[q].z ^ 0x80808080u,
-                                       reg[q].w ^ 0x80808080u};
-                uint4 h[2];
-                h[0] = make_uint4(kvd::codes2<0x4140>(w[0]), kvd::codes2<0x4342>(w[0]), kvd::codes2<0x4140>(w[1]),
+                const uint4 x = *reinterpret_cast<const uint4*>(src + 2048 * q);
+                const uint32_t w[4] = {x.x ^ 0x80808080u, x.y ^ 0x80808080u, x.z ^ 0x80808080u, x.w ^ 0x80808080u};
+                uint4 f[2];
+                f[0] = make_uint4(kvd::codes2<0x4140>(w[0]), kvd::codes2<0x4342>(w[0]), kvd::codes2<0x4140>(w[1]),
                                   kvd::codes2<0x4342>(w[1]));
-                h[1] = make_uint4(kvd::codes2<0x4140>(w[2]), kvd::codes2<0x4342>(w[2]), kvd::codes2<0x4140>(w[3]),
+                f[1] = make_uint4(kvd::codes2<0x4140>(w[2]), kvd::codes2<0x4342>(w[2]), kvd::codes2<0x4140>(w[3]),
                                   kvd::codes2<0x4342>(w[3]));
                 // the lanes of the second half of a row store their two chunks
                 // in the other order: different banks at the same time
@@ -498,32 +638,35 @@ __global__ void __launch_bounds__(kvt::kThreads, 1)
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     const int ch = 2 * (cc & 3) + (k ^ flip);
-                    *reinterpret_cast<uint4*>(base + ((ch ^ (r & 7)) << 4)) = (k ^ flip) ? h[1] : h[0];
+                    *reinterpret_cast<uint4*>(base + ((ch ^ (r & 7)) << 4)) = (k ^ flip) ? f[1] : f[0];
                 }
             }
             tc::fence_proxy_async_smem();
             tc::mbar_arrive(&S.full[slot]);
-            if (i + 1 < 2 * steps) {
-                if (which == 1) fetch_pages((i + 1) >> 1);
-                load((i + 1) >> 1, which ^ 1);
-            }
+            issue(i + kStages - 1);   // into the stage of operand i - 1, which this thread has read
         }
-    } else if (warp >= kIssueWarp && warp < kIssueWarp + MT) {
+        kvd::cp_wait<0>();
+    } else {
         // ---------------------------------------------------------- MMA issue
-        if (lane == 0) {
-            const int qt = warp - kIssueWarp;
+        regs_down<kRegsIssue>();
+        if (lane == 0 && warp < kIssueWarp + 2) {
+            const int me = warp - kIssueWarp;
+            const int qt = MT == 2 ? me : 0;
             const int n = steps_of(qt);
             constexpr uint32_t idesc_qk = tc::idesc_f16_f32(kTileQ, kTileKv);
             constexpr uint32_t idesc_pv = tc::idesc_f16_f32(kTileQ, D) | kTransposeB;
-            const uint32_t ts = tmem + (uint32_t)qt * kTileKv;
-            const uint32_t to_ = tmem + (uint32_t)(MT * kTileKv + qt * D);
+            const uint32_t to_ = tmem + kColO + (uint32_t)(qt * D);
             const uint64_t qd = tc::sdesc_sw128_kmajor(tc::smem_u32(sQ + qt * PARTS * kOp));
-            bool ok = true;
-            auto qk = [&](int j) {
+            auto wait = [&](uint64_t* bar, int parity) {
+                return tc::mbar_wait_spin(bar, (uint32_t)parity, abort_flag, kWait);
+            };
+            // S of step j, into buffer bf
+            auto qk = [&](int j, int bf) {
                 const int i = 2 * j, slot = i % kSlots;
-                if (!tc::mbar_wait_spin(&S.full[slot], (i / kSlots) & 1, abort_flag, kWait)) return false;
+                if (!wait(&S.full[slot], (i / kSlots) & 1)) return false;
                 tc::tc_fence_after();
                 const uint64_t kd = tc::sdesc_sw128_kmajor(tc::smem_u32(sKV + slot * kOp));
+                const uint32_t ts = tmem + (uint32_t)(bf * kTileKv);
 #pragma unroll
                 for (int pt = 0; pt < PARTS; ++pt)
 #pragma unroll
@@ -532,44 +675,65 @@ __global__ void __launch_bounds__(kvt::kThreads, 1)
                         tc::umma_f16(ts, qd + (uint64_t)(pt * (kOp >> 4)) + off, kd + off, idesc_qk, pt + k > 0);
                     }
                 tc::umma_commit(&S.empty[slot]);
-                tc::umma_commit(&S.s_full[qt]);
+                tc::umma_commit(&S.s_full[bf]);
                 return true;
             };
-            if (n > 0) {
-                ok = tc::mbar_wait_spin(&S.q_ready[qt], 0, abort_flag, kWait);
-                tc::tc_fence_after();
-                ok = ok && qk(0);
-            }
-            for (int j = 0; ok && j < n; ++j) {
+            // O of step j from the weights in buffer bf, ready in phase ph
+            auto pv = [&](int j, int bf, int ph) {
                 const int i = 2 * j + 1, slot = i % kSlots;
-                ok = tc::mbar_wait_spin(&S.full[slot], (i / kSlots) & 1, abort_flag, kWait) &&
-                     tc::mbar_wait_spin(&S.p_ready[qt], j & 1, abort_flag, kWait);
-                if (!ok) break;
+                if (!wait(&S.full[slot], (i / kSlots) & 1) || !wait(&S.p_ready[bf], ph)) return false;
                 tc::tc_fence_after();
                 const uint64_t vd = sdesc_sw128_mnmajor(tc::smem_u32(sKV + slot * kOp));
+                const uint32_t ts = tmem + (uint32_t)(bf * kTileKv);
+                const bool first = kChained ? j % kChain == 0 : j == 0;
 #pragma unroll
                 for (int k = 0; k < kVSteps; ++k)
 #pragma unroll
                     for (int pt = 0; pt < PARTS; ++pt)
                         tc::umma_f16_tmem_a(to_, ts + (uint32_t)(32 * (k >> 1) + 16 * pt + 8 * (k & 1)),
-                                            vd + (uint64_t)(k * (2048 >> 4)), idesc_pv, (j > 0) || (pt + k > 0));
+                                            vd + (uint64_t)(k * (2048 >> 4)), idesc_pv, !first || (pt + k > 0));
                 tc::umma_commit(&S.empty[slot]);
-                tc::umma_commit(&S.pv_done[qt]);
-                if (j + 1 < n) {
-                    // S takes the place of the weights that these MMAs read
-                    ok = tc::mbar_wait_spin(&S.pv_done[qt], j & 1, abort_flag, kWait) && qk(j + 1);
-                }
+                tc::umma_commit(&S.pv_done[bf]);
+                return true;
+            };
+            bool ok = true;
+            if (n > 0 && (MT == 2 || me == 0)) {
+                ok = wait(&S.q_ready[qt], 0);
+                tc::tc_fence_after();
             }
-            // tiles that only the other query tile sees
-            for (int i = 2 * n; ok && i < 2 * steps; ++i) {
-                const int slot = i % kSlots;
-                ok = tc::mbar_wait(&S.full[slot], (i / kSlots) & 1, abort_flag, kWait);
-                if (ok) tc::mbar_arrive(&S.empty[slot]);
+            if (MT == 1) {
+                for (int j = 0; ok && j < n; ++j) {
+                    const int bf = j & 1;
+                    if (me == 0) {   // the buffer's weights of step j - 2 have been used
+                        if (j >= 2) ok = wait(&S.pv_done[bf], ((j - 2) >> 1) & 1);
+                        if (ok) tc::tc_fence_after();
+                        ok = ok && qk(j, bf);
+                    } else {
+                        ok = pv(j, bf, (j >> 1) & 1);
+                    }
+                }
+            } else {
+                if (n > 0) ok = ok && qk(0, qt);
+                for (int j = 0; ok && j < n; ++j) {
+                    ok = pv(j, qt, j & 1);
+                    // S takes the place of the weights that these MMAs read
+                    if (ok && j + 1 < n) {
+                        ok = wait(&S.pv_done[qt], j & 1);
+                        if (ok) tc::tc_fence_after();
+                        ok = ok && qk(j + 1, qt);
+                    }
+                }
+                // tiles that only the other query tile sees
+                for (int i = 2 * n; ok && i < 2 * steps; ++i) {
+                    const int slot = i % kSlots;
+                    ok = tc::mbar_wait(&S.full[slot], (i / kSlots) & 1, abort_flag, kWait);
+                    if (ok) tc::mbar_arrive(&S.empty[slot]);
+                }
             }
             if (!ok) fail();
             // every MMA issued is done before TMEM and shared memory are left
-            tc::umma_commit(&S.drained[qt]);
-            tc::mbar_wait_drain(&S.drained[qt], 0, kWait / 8);
+            tc::umma_commit(&S.drained[me]);
+            tc::mbar_wait_drain(&S.drained[me], 0, kWait / 8);
         }
         __syncwarp();
     }
