@@ -26,20 +26,21 @@
 // 9e-6 of O was measured. For F32 rows O is therefore moved every kChain tiles
 // into a running sum that is added to with rounding (1e-6).
 //
-// Two shapes. MT = 2 (16-bit rows, where there are enough of them): two query
-// tiles per CTA share each converted tile of the cache, one's softmax runs while
-// the other's MMAs do; a thread has a whole row. MT = 1: one query tile, two S
-// buffers, so that Q K^T of the next tile runs during the softmax; a row's 128
-// columns belong to two threads, which exchange their maxima.
+// Two shapes, each with two warpgroups of softmax threads, one thread per row
+// (TMEM lane), that run out of step, so that one's work fills the other's waits
+// and the MMAs of one's tile run during the other's softmax. MT = 2 (16-bit
+// rows, where there are enough of them): two query tiles share each converted
+// tile of the cache, a warpgroup each. MT = 1: the warpgroups take the tiles of
+// the cache by turns; the running maximum goes from one to the other through
+// shared memory, between the maximum and the weights of a tile.
 //
 // Roles (16 warps, one CTA per SM):
-//   warps 0-7    softmax (MT = 2: 0-3 query tile 0, 4-7 tile 1; MT = 1: 0-3 the
-//                first 64 tokens of a tile, 4-7 the others); they also stage Q,
-//                rescale O and write the output
-//   warps 8-11   producer: int8 K and V by cp.async, kStages operands ahead, each
-//                thread its own chunks, to f16 in 128-byte-swizzled shared memory
-//   warps 12, 13 one thread each issues MMAs (MT = 2: of query tile 0, 1; MT = 1:
-//                Q K^T, P V)
+//   warps 0-3, 4-7  softmax; they also stage Q, rescale O and write the output
+//   warps 8-11      producer: int8 K and V by cp.async, kStages operands ahead,
+//                   each thread its own chunks, to f16 in 128-byte-swizzled
+//                   shared memory
+//   warps 12, 13    one thread each issues MMAs (MT = 2: of query tile 0, 1;
+//                   MT = 1: Q K^T, P V)
 // TMEM (512 columns): S (2 x 128 columns of f32), overwritten in place by the
 // weights (32 columns of S become 16 of high and 16 of low parts), and O (MT x D,
 // for F32 rows and the running sum). K is the K-major operand [token][d]; V with
@@ -81,11 +82,11 @@ __host__ __device__ constexpr int operand_bytes() { return kTileKv * D * 2; }
 
 struct Shared {
     uint64_t full[kSlots], empty[kSlots], cfull[kConsts];
-    uint64_t q_ready[2], s_full[2], p_ready[2], pv_done[2], drained[2], x_ready[2], l_ready;
-    float ks[kConsts][kBlocks], lv[kConsts][kBlocks], iv[kConsts][kBlocks];
+    uint64_t q_ready[2], s_full[2], p_ready[2], pv_done[2], drained[2], m_ready[2], l_ready;
+    float4 cst[kConsts][kBlocks];   // K scale, log2 of the V scale, its inverse
     float raw[kConsts][2 * kBlocks];
     float mul[2 * kTileQ];
-    float top[2][2][kTileQ], lsum[2][kTileQ];
+    float m[2][kTileQ], l[2][kTileQ], m_run[kTileQ];
     uint32_t tmem;
     int abort;
     int scan[kThreads / 32];
@@ -120,18 +121,128 @@ __device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.al
 template <int N>
 __device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 
-// A thread's share of one tile of S: COLS columns from `ts`, in pieces of 32.
-// fetch(piece) loads one (once, if it is kept).
-template <int COLS, bool KEEP>
-struct Scores {
-    uint32_t v[KEEP ? COLS : 32];
-    __device__ __forceinline__ void fetch(uint32_t ts, int piece) {
-        uint32_t(&w)[32] = *reinterpret_cast<uint32_t(*)[32]>(&v[KEEP ? 32 * piece : 0]);
-        tc::tmem_ld_32x32b_x32(ts + 32u * piece, w);
+// a * b + c of two values at once.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n.reg .b64 ra, rb, rc, rd;\nmov.b64 ra, {%2, %3};\nmov.b64 rb, {%4, %5};\nmov.b64 rc, {%6, %7};\n"
+        "fma.rn.f32x2 rd, ra, rb, rc;\nmov.b64 {%0, %1}, rd;\n}\n"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n.reg .b64 ra, rb, rd;\nmov.b64 ra, {%2, %3};\nmov.b64 rb, {%4, %5};\n"
+        "add.rn.f32x2 rd, ra, rb;\nmov.b64 {%0, %1}, rd;\n}\n"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+
+// The columns [0, 32) of a piece that a row does not see, as -infinity.
+__device__ __forceinline__ void hide(uint32_t (&v)[32], int lo, int hi) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+        if (i < lo || i >= hi) v[i] = 0xff800000u;
+}
+
+// The largest logit (with the V scale's log2) of 32 columns of S.
+template <bool MASKED>
+__device__ __forceinline__ float piece_top(uint32_t (&v)[32], float mul, const float4* cst, int lo, int hi) {
+    if (MASKED) hide(v, lo, hi);
+    float top = -INFINITY;
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+        float t0 = -INFINITY, t1 = -INFINITY;
+#pragma unroll
+        for (int i = 16 * b; i < 16 * b + 16; i += 4) {
+            t0 = max3(t0, __uint_as_float(v[i]), __uint_as_float(v[i + 1]));
+            t1 = max3(t1, __uint_as_float(v[i + 2]), __uint_as_float(v[i + 3]));
+        }
+        const float2 k = *reinterpret_cast<const float2*>(&cst[b]);
+        // a zero scale times -infinity would be NaN, which the maximum ignores
+        top = fmaxf(top, fmaf(fmaxf(t0, t1), mul * k.x, k.y));
     }
-    __device__ __forceinline__ float at(int i) const { return __uint_as_float(v[KEEP ? i : i & 31]); }
-    __device__ __forceinline__ void hide(int i) { v[KEEP ? i : i & 31] = 0xff800000u; }
-};
+    return top;
+}
+
+// The weights of 32 columns, as f16 (parts), and their share of l.
+template <bool MASKED, int PARTS>
+__device__ __forceinline__ void piece_weights(uint32_t (&v)[32], float mul, float sub, const float4* cst, int lo, int hi,
+                                              float& l, uint32_t (&hi16)[16], uint32_t (&lo16)[16]) {
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+        const float4 k = cst[b];
+        const float xm = mul * k.x, add = k.y - sub;
+        float2 sum = make_float2(0.0f, 0.0f);
+#pragma unroll
+        for (int i = 16 * b; i < 16 * b + 16; i += 2) {
+            float2 w = fma2(make_float2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), make_float2(xm, xm),
+                            make_float2(add, add));
+            w.x = kvd::ex2(w.x);
+            w.y = kvd::ex2(w.y);
+            if (MASKED) {   // zero, also where the block's scale is NaN
+                if (i < lo || i >= hi) w.x = 0.0f;
+                if (i + 1 < lo || i + 1 >= hi) w.y = 0.0f;
+            }
+            sum = add2(sum, w);
+            const __half2 h = __floats2half2_rn(w.x, w.y);
+            hi16[i / 2] = *reinterpret_cast<const uint32_t*>(&h);
+            if (PARTS == 2) {
+                const float2 f = __half22float2(h);
+                const float2 rest = fma2(f, make_float2(-1.0f, -1.0f), w);
+                lo16[i / 2] = kvd::pack2(rest.x, rest.y);
+            }
+        }
+        l = fmaf(sum.x + sum.y, k.z, l);
+    }
+}
+
+// One tile of S at `ts` (128 columns of the thread's row): its largest logit.
+template <bool MASKED>
+__device__ __forceinline__ float tile_top(uint32_t ts, float mul, const float4* cst, int lo, int hi) {
+    uint32_t a[32], b[32];
+    float top = -INFINITY;
+    tc::tmem_ld_32x32b_x32(ts, a);
+    tc::tmem_ld_wait();
+    tc::tmem_ld_32x32b_x32(ts + 32u, b);
+    top = fmaxf(top, piece_top<MASKED>(a, mul, cst, lo, hi));
+    tc::tmem_ld_wait();
+    tc::tmem_ld_32x32b_x32(ts + 64u, a);
+    top = fmaxf(top, piece_top<MASKED>(b, mul, cst + 2, lo - 32, hi - 32));
+    tc::tmem_ld_wait();
+    tc::tmem_ld_32x32b_x32(ts + 96u, b);
+    top = fmaxf(top, piece_top<MASKED>(a, mul, cst + 4, lo - 64, hi - 64));
+    tc::tmem_ld_wait();
+    return fmaxf(top, piece_top<MASKED>(b, mul, cst + 6, lo - 96, hi - 96));
+}
+
+// The tile's weights in place of its S.
+template <bool MASKED, int PARTS>
+__device__ __forceinline__ void tile_weights(uint32_t ts, float mul, float sub, const float4* cst, int lo, int hi, float& l) {
+    uint32_t a[32], b[32], hi16[16], lo16[16];
+    auto store = [&](uint32_t at) {
+        tc::tmem_st_32x32b_x16(at, hi16);
+        if (PARTS == 2) tc::tmem_st_32x32b_x16(at + 16u, lo16);
+    };
+    tc::tmem_ld_32x32b_x32(ts, a);
+    tc::tmem_ld_wait();
+    tc::tmem_ld_32x32b_x32(ts + 32u, b);
+    piece_weights<MASKED, PARTS>(a, mul, sub, cst, lo, hi, l, hi16, lo16);
+    store(ts);
+    tc::tmem_ld_wait();
+    tc::tmem_ld_32x32b_x32(ts + 64u, a);
+    piece_weights<MASKED, PARTS>(b, mul, sub, cst + 2, lo - 32, hi - 32, l, hi16, lo16);
+    store(ts + 32u);
+    tc::tmem_ld_wait();
+    tc::tmem_ld_32x32b_x32(ts + 96u, b);
+    piece_weights<MASKED, PARTS>(a, mul, sub, cst + 4, lo - 64, hi - 64, l, hi16, lo16);
+    store(ts + 64u);
+    tc::tmem_ld_wait();
+    piece_weights<MASKED, PARTS>(b, mul, sub, cst + 6, lo - 96, hi - 96, l, hi16, lo16);
+    store(ts + 96u);
+    tc::tmem_st_wait();
+}
 
 }  // namespace kvt
 
@@ -210,10 +321,10 @@ __global__ void __launch_bounds__(kvt::kThreads, 1)
         for (int i = 0; i < 2; ++i) {
             tc::mbar_init(&S.q_ready[i], 256 / MT);
             tc::mbar_init(&S.s_full[i], 1);
-            tc::mbar_init(&S.p_ready[i], 256 / MT);
+            tc::mbar_init(&S.p_ready[i], 128);
             tc::mbar_init(&S.pv_done[i], 1);
             tc::mbar_init(&S.drained[i], 1);
-            tc::mbar_init(&S.x_ready[i], 256);
+            tc::mbar_init(&S.m_ready[i], 128);
         }
         tc::mbar_init(&S.l_ready, 256);
         S.abort = 0;
@@ -262,12 +373,10 @@ __global__ void __launch_bounds__(kvt::kThreads, 1)
     if (warp < 8) {
         // ------------------------------------------------------------ softmax
         regs_up<kRegsSoftmax>();
-        // qt: the query tile; h: which half of a row's columns (MT = 1)
+        // qt: the query tile; h: which of the warpgroups that share one (MT = 1)
         const int qt = MT == 2 ? warp >> 2 : 0, h = MT == 1 ? warp >> 2 : 0, r = tid & 127;
         const int n = steps_of(qt);
         const int tile_row = row_lo + qt * kTileQ;
-        constexpr int COLS = MT == 2 ? kTileKv : kTileKv / 2;
-        constexpr int OC = MT == 2 ? D : D / 2;   // columns of O that a thread has
         if (n > 0) {
             // Q: each warp 32 (MT = 2) or 16 of the rows, a lane 4 (D = 128) or 2 consecutive values
             constexpr int VPL = D / 32;
@@ -322,8 +431,8 @@ __global__ void __launch_bounds__(kvt::kThreads, 1)
         const int row = tile_row + r;
         const bool live = row < row_hi;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-        const uint32_t to_ = tmem + lanes + kColO + (uint32_t)(qt * D + h * OC);
-        const uint32_t tr = tmem + lanes + kColRun + (uint32_t)(h * OC);
+        const uint32_t to_ = tmem + lanes + kColO + (uint32_t)(qt * D);
+        const uint32_t tr = tmem + lanes + kColRun;
         int see_lo = 0, see_hi = 0;
         if (live) {
             see_hi = (int)last_seen(row);
@@ -341,62 +450,34 @@ __global__ void __launch_bounds__(kvt::kThreads, 1)
         float mul = 0.0f;
         if (n > 0 && wait(&S.q_ready[qt], 0)) mul = S.mul[qt * kTileQ + r];
         float m = -INFINITY, l = 0.0f, m_run = -INFINITY;
-        for (int j = 0; ok && j < n; ++j) {
+        for (int j = h; ok && j < n; j += 3 - MT) {
             const int cs = j % kConsts;
             const int bf = MT == 2 ? qt : j & 1, ph = MT == 2 ? j & 1 : (j >> 1) & 1;
             if (!wait(&S.cfull[cs], (j / kConsts) & 1) || !wait(&S.s_full[bf], ph)) break;
             tc::tc_fence_after();
-            const uint32_t ts = tmem + lanes + (uint32_t)(bf * kTileKv + h * COLS);
+            const uint32_t ts = tmem + lanes + (uint32_t)(bf * kTileKv);
             const int tok = (from + j) * kTileKv;
             const bool masked = tok < all_lo || tok + kTileKv > all_hi;   // for some row of the warp
-            const int lo = see_lo - tok - h * COLS, hi = see_hi - tok - h * COLS;
-            const float* ks = &S.ks[cs][h * (COLS / kKvBlock)];
-            const float* lv = &S.lv[cs][h * (COLS / kKvBlock)];
-            const float* iv = &S.iv[cs][h * (COLS / kKvBlock)];
-            Scores<COLS, MT == 1> x;
-            float top = -INFINITY;
-            if (MT == 1) {
-#pragma unroll
-                for (int ch = 0; ch < COLS / 32; ++ch) x.fetch(ts, ch);
-                tc::tmem_ld_wait();
+            const int lo = see_lo - tok, hi = see_hi - tok;
+            const float top = masked ? tile_top<true>(ts, mul, S.cst[cs], lo, hi) : tile_top<false>(ts, mul, S.cst[cs], lo, hi);
+            float before = m;
+            if (MT == 1 && j > 0) {   // the maximum up to the tile before, of the other warpgroup
+                if (!wait(&S.m_ready[bf ^ 1], ((j - 1) >> 1) & 1)) break;
+                before = S.m[bf ^ 1][r];
+                if (before != m) l *= m == -INFINITY ? 0.0f : ex2(m - before);
             }
-#pragma unroll
-            for (int ch = 0; ch < COLS / 32; ++ch) {
-                if (MT == 2) {
-                    x.fetch(ts, ch);
-                    tc::tmem_ld_wait();
-                }
-                if (masked) {
-#pragma unroll
-                    for (int i = 32 * ch; i < 32 * ch + 32; ++i)
-                        if (i < lo || i >= hi) x.hide(i);
-                }
-#pragma unroll
-                for (int b = 2 * ch; b < 2 * ch + 2; ++b) {
-                    float t0 = -INFINITY, t1 = -INFINITY;
-#pragma unroll
-                    for (int i = 16 * b; i < 16 * b + 16; i += 4) {
-                        t0 = max3(t0, x.at(i), x.at(i + 1));
-                        t1 = max3(t1, x.at(i + 2), x.at(i + 3));
-                    }
-                    // a zero scale times -infinity would be NaN, which the maximum ignores
-                    top = fmaxf(top, fmaf(fmaxf(t0, t1), mul * ks[b], lv[b]));
-                }
-            }
-            if (MT == 1) {   // the row's other half
-                S.top[bf][h][r] = top;
-                tc::mbar_arrive(&S.x_ready[bf]);
-                if (!wait(&S.x_ready[bf], ph)) break;
-                top = fmaxf(top, S.top[bf][h ^ 1][r]);
-            }
-            const bool grown = __any_sync(0xffffffffu, top > m + kSlack);
+            const bool grown = __any_sync(0xffffffffu, top > before + kSlack);
             const bool flush = kChained && j > 0 && j % kChain == 0;
             float keep = 1.0f;
+            m = before;
             if (grown) {
-                const float nm = fmaxf(m, top);
-                keep = nm == -INFINITY ? 1.0f : ex2(m - nm);
-                m = nm;
+                m = fmaxf(before, top);
+                keep = m == -INFINITY ? 1.0f : ex2(before - m);
                 l *= keep;
+            }
+            if (MT == 1) {
+                S.m[bf][r] = m;
+                tc::mbar_arrive(&S.m_ready[bf]);
             }
             if ((grown && j > 0) || flush) {
                 // O holds the tiles before this one; with two S buffers their MMAs may still run
@@ -409,79 +490,58 @@ __global__ void __launch_bounds__(kvt::kThreads, 1)
                     const float keep_run = m == -INFINITY ? 1.0f : ex2(m_run - m);
                     m_run = m;
 #pragma unroll 1
-                    for (int ch = 0; ch < OC / 16; ++ch) {
-                        uint32_t o[16], v[16];
-                        tc::tmem_ld_32x32b_x16(to_ + 16u * ch, o);
-                        if (!first) tc::tmem_ld_32x32b_x16(tr + 16u * ch, v);
+                    for (int ch = 0; ch < D / 32; ++ch) {
+                        uint32_t o[32], v[32];
+                        tc::tmem_ld_32x32b_x32(to_ + 32u * ch, o);
+                        if (!first) tc::tmem_ld_32x32b_x32(tr + 32u * ch, v);
                         tc::tmem_ld_wait();
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) {
+                        for (int i = 0; i < 32; ++i) {
                             const float y = __uint_as_float(o[i]) * keep;
                             v[i] = __float_as_uint(first ? y : fmaf(__uint_as_float(v[i]), keep_run, y));
                         }
-                        tc::tmem_st_32x32b_x16(tr + 16u * ch, v);
+                        tc::tmem_st_32x32b_x32(tr + 32u * ch, v);
                     }
                 } else {
 #pragma unroll 1
-                    for (int ch = 0; ch < OC / 16; ++ch) {
-                        uint32_t v[16];
-                        tc::tmem_ld_32x32b_x16(to_ + 16u * ch, v);
+                    for (int ch = 0; ch < D / 32; ++ch) {
+                        uint32_t v[32];
+                        tc::tmem_ld_32x32b_x32(to_ + 32u * ch, v);
                         tc::tmem_ld_wait();
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * keep);
-                        tc::tmem_st_32x32b_x16(to_ + 16u * ch, v);
+                        for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * keep);
+                        tc::tmem_st_32x32b_x32(to_ + 32u * ch, v);
                     }
                 }
             }
             const float sub = m == -INFINITY ? 0.0f : m - kBias;
-#pragma unroll
-            for (int ch = 0; ch < COLS / 32; ++ch) {
-                if (MT == 2) {
-                    x.fetch(ts, ch);
-                    tc::tmem_ld_wait();
-                    if (masked) {
-#pragma unroll
-                        for (int i = 32 * ch; i < 32 * ch + 32; ++i)
-                            if (i < lo || i >= hi) x.hide(i);
-                    }
-                }
-                uint32_t hi16[16], lo16[16];
-#pragma unroll
-                for (int b = 2 * ch; b < 2 * ch + 2; ++b) {
-                    const float xm = mul * ks[b], add = lv[b] - sub;
-                    float sum0 = 0.0f, sum1 = 0.0f;
-#pragma unroll
-                    for (int i = 16 * b; i < 16 * b + 16; i += 2) {
-                        float w0 = ex2(fmaf(x.at(i), xm, add)), w1 = ex2(fmaf(x.at(i + 1), xm, add));
-                        if (masked) {   // also where the block's scale is NaN
-                            if (i < lo || i >= hi) w0 = 0.0f;
-                            if (i + 1 < lo || i + 1 >= hi) w1 = 0.0f;
-                        }
-                        sum0 += w0;
-                        sum1 += w1;
-                        const int p = (i & 31) / 2;
-                        if (PARTS == 2) kvd::split2(w0, w1, hi16[p], lo16[p]);
-                        else hi16[p] = kvd::pack2(w0, w1);
-                    }
-                    l = fmaf(sum0 + sum1, iv[b], l);
-                }
-                tc::tmem_st_32x32b_x16(ts + 32u * ch, hi16);
-                if (PARTS == 2) tc::tmem_st_32x32b_x16(ts + 32u * ch + 16u, lo16);
-            }
-            tc::tmem_st_wait();
+            if (masked) tile_weights<true, PARTS>(ts, mul, sub, S.cst[cs], lo, hi, l);
+            else tile_weights<false, PARTS>(ts, mul, sub, S.cst[cs], lo, hi, l);
             tc::tc_fence_before();
             tc::mbar_arrive(&S.p_ready[bf]);
         }
-        if (MT == 1 && ok) {   // l of both halves
-            S.lsum[h][r] = l;
-            tc::mbar_arrive(&S.l_ready);
-            if (wait(&S.l_ready, 0)) l += S.lsum[h ^ 1][r];
-        }
         if (ok && n > 0) {
             const int last = n - 1;
-            wait(&S.pv_done[MT == 2 ? qt : last & 1], MT == 2 ? last & 1 : (last >> 1) & 1);
+            if (MT == 1) {
+                // the maximum of all tiles, l of both warpgroups, and what the
+                // running sum refers to (the first warpgroup moves O)
+                if (wait(&S.m_ready[last & 1], (last >> 1) & 1)) {
+                    const float all = S.m[last & 1][r];
+                    if (all != m) l *= m == -INFINITY ? 0.0f : ex2(m - all);
+                    m = all;
+                    S.l[h][r] = l;
+                    if (h == 0) S.m_run[r] = m_run;
+                    tc::mbar_arrive(&S.l_ready);
+                    if (wait(&S.l_ready, 0)) {
+                        l += S.l[h ^ 1][r];
+                        m_run = S.m_run[r];
+                    }
+                }
+            }
+            if (ok) wait(&S.pv_done[MT == 2 ? qt : last & 1], MT == 2 ? last & 1 : (last >> 1) & 1);
             tc::tc_fence_after();
         }
+        constexpr int OC = MT == 2 ? D : D / 2;   // columns of O that a thread writes
         if (ok) {
             const int ti = row / group, hh = head * group + row - ti * group;
             const long long grow = sq.row0 + ti;
@@ -504,11 +564,11 @@ __global__ void __launch_bounds__(kvt::kThreads, 1)
                 for (int ch = 0; ch < OC / 32; ++ch) {
                     uint32_t v[32];
                     if (n > 0) {
-                        tc::tmem_ld_32x32b_x32(to_ + 32u * ch, v);
+                        tc::tmem_ld_32x32b_x32(to_ + (uint32_t)(h * OC + 32 * ch), v);
                         tc::tmem_ld_wait();
                         if (ran) {
                             uint32_t w[32];
-                            tc::tmem_ld_32x32b_x32(tr + 32u * ch, w);
+                            tc::tmem_ld_32x32b_x32(tr + (uint32_t)(h * OC + 32 * ch), w);
                             tc::tmem_ld_wait();
 #pragma unroll
                             for (int i = 0; i < 32; ++i)
@@ -547,6 +607,12 @@ __global__ void __launch_bounds__(kvt::kThreads, 1)
         constexpr int kChunks = D / 16;          // 16-byte chunks of a token's codes, and loads per thread and operand
         const int* table = c.table + (long long)s * c.width;
         const uint32_t raw = kvd::smem_addr(sRaw) + 16 * p;
+        // Load q of a thread: four lanes have 64 codes of a token row (one swizzle
+        // atom), eight lanes two rows of it, whose f16 chunks lie in different banks.
+        auto row_at = [&](int q) { return (D == 128 ? q >> 1 : q) * 32 + (p >> 2); };
+        auto chunk_at = [&](int q) { return (p & 3) + (D == 128 ? 4 * (q & 1) : 0); };
+        const int sw = (p >> 2) & 7;
+        const int at0 = ((2 * (p & 3)) ^ sw) << 4, at1 = ((2 * (p & 3) + 1) ^ sw) << 4;
         // lane i < 8 of each warp: the page of block i of tile j, -1: none
         auto fetch_pages = [&](int j) {
             int page = -1;
@@ -568,7 +634,7 @@ __global__ void __launch_bounds__(kvt::kThreads, 1)
                 const uint32_t dst = raw + (uint32_t)(i % kStages) * (kOp / 2);
 #pragma unroll
                 for (int q = 0; q < kChunks; ++q) {
-                    const int idx = q * 128 + p, r = idx / kChunks, cc = idx % kChunks;
+                    const int r = row_at(q), cc = chunk_at(q);
                     const int page = __shfl_sync(0xffffffffu, pages, r >> 4);
                     const int tok = ((from + j) * kTileKv + r) & ((1 << c.page_shift) - 1);
                     const uint8_t* src = c.pages;
@@ -613,9 +679,7 @@ __global__ void __launch_bounds__(kvt::kThreads, 1)
                         // NaN weights make l NaN for the rows that see the block; the others add 0 * 1
                         iv = v == v ? __fdiv_rn(1.0f, some) : 1.0f;
                     }
-                    S.ks[cs][lane] = k;
-                    S.lv[cs][lane] = lv;
-                    S.iv[cs][lane] = iv;
+                    S.cst[cs][lane] = make_float4(k, lv, iv, 0.0f);
                 }
                 tc::mbar_arrive(&S.cfull[cs]);
             }
@@ -623,23 +687,13 @@ __global__ void __launch_bounds__(kvt::kThreads, 1)
             uint8_t* dst = sKV + slot * kOp;
 #pragma unroll
             for (int q = 0; q < kChunks; ++q) {
-                const int idx = q * 128 + p, r = idx / kChunks, cc = idx % kChunks;
                 const uint4 x = *reinterpret_cast<const uint4*>(src + 2048 * q);
                 const uint32_t w[4] = {x.x ^ 0x80808080u, x.y ^ 0x80808080u, x.z ^ 0x80808080u, x.w ^ 0x80808080u};
-                uint4 f[2];
-                f[0] = make_uint4(kvd::codes2<0x4140>(w[0]), kvd::codes2<0x4342>(w[0]), kvd::codes2<0x4140>(w[1]),
-                                  kvd::codes2<0x4342>(w[1]));
-                f[1] = make_uint4(kvd::codes2<0x4140>(w[2]), kvd::codes2<0x4342>(w[2]), kvd::codes2<0x4140>(w[3]),
-                                  kvd::codes2<0x4342>(w[3]));
-                // the lanes of the second half of a row store their two chunks
-                // in the other order: different banks at the same time
-                const int flip = (cc >> 2) & 1;
-                uint8_t* base = dst + (cc >> 2) * kHalf + r * 128;
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const int ch = 2 * (cc & 3) + (k ^ flip);
-                    *reinterpret_cast<uint4*>(base + ((ch ^ (r & 7)) << 4)) = (k ^ flip) ? f[1] : f[0];
-                }
+                uint8_t* base = dst + (chunk_at(q) >> 2) * kHalf + row_at(q) * 128;
+                *reinterpret_cast<uint4*>(base + at0) = make_uint4(kvd::codes2<0x4140>(w[0]), kvd::codes2<0x4342>(w[0]),
+                                                                   kvd::codes2<0x4140>(w[1]), kvd::codes2<0x4342>(w[1]));
+                *reinterpret_cast<uint4*>(base + at1) = make_uint4(kvd::codes2<0x4140>(w[2]), kvd::codes2<0x4342>(w[2]),
+                                                                   kvd::codes2<0x4140>(w[3]), kvd::codes2<0x4342>(w[3]));
             }
             tc::fence_proxy_async_smem();
             tc::mbar_arrive(&S.full[slot]);
@@ -658,7 +712,7 @@ __global__ void __launch_bounds__(kvt::kThreads, 1)
             const uint32_t to_ = tmem + kColO + (uint32_t)(qt * D);
             const uint64_t qd = tc::sdesc_sw128_kmajor(tc::smem_u32(sQ + qt * PARTS * kOp));
             auto wait = [&](uint64_t* bar, int parity) {
-                return tc::mbar_wait_spin(bar, (uint32_t)parity, abort_flag, kWait);
+                return tc::mbar_wait(bar, (uint32_t)parity, abort_flag, kWait);
             };
             // S of step j, into buffer bf
             auto qk = [&](int j, int bf) {
@@ -668,11 +722,11 @@ __global__ void __launch_bounds__(kvt::kThreads, 1)
                 const uint64_t kd = tc::sdesc_sw128_kmajor(tc::smem_u32(sKV + slot * kOp));
                 const uint32_t ts = tmem + (uint32_t)(bf * kTileKv);
 #pragma unroll
-                for (int pt = 0; pt < PARTS; ++pt)
+                for (int pt = PARTS - 1; pt >= 0; --pt)   // the small parts first, while the sum is small
 #pragma unroll
                     for (int k = 0; k < kKSteps; ++k) {
                         const uint64_t off = (uint64_t)((k >> 2) * (kHalf >> 4) + 2 * (k & 3));
-                        tc::umma_f16(ts, qd + (uint64_t)(pt * (kOp >> 4)) + off, kd + off, idesc_qk, pt + k > 0);
+                        tc::umma_f16(ts, qd + (uint64_t)(pt * (kOp >> 4)) + off, kd + off, idesc_qk, pt != PARTS - 1 || k > 0);
                     }
                 tc::umma_commit(&S.empty[slot]);
                 tc::umma_commit(&S.s_full[bf]);
@@ -687,11 +741,11 @@ __global__ void __launch_bounds__(kvt::kThreads, 1)
                 const uint32_t ts = tmem + (uint32_t)(bf * kTileKv);
                 const bool first = kChained ? j % kChain == 0 : j == 0;
 #pragma unroll
-                for (int k = 0; k < kVSteps; ++k)
+                for (int pt = PARTS - 1; pt >= 0; --pt)
 #pragma unroll
-                    for (int pt = 0; pt < PARTS; ++pt)
+                    for (int k = 0; k < kVSteps; ++k)
                         tc::umma_f16_tmem_a(to_, ts + (uint32_t)(32 * (k >> 1) + 16 * pt + 8 * (k & 1)),
-                                            vd + (uint64_t)(k * (2048 >> 4)), idesc_pv, !first || (pt + k > 0));
+                                            vd + (uint64_t)(k * (2048 >> 4)), idesc_pv, !first || pt != PARTS - 1 || k > 0);
                 tc::umma_commit(&S.empty[slot]);
                 tc::umma_commit(&S.pv_done[bf]);
                 return true;
