@@ -36,8 +36,8 @@
 //
 // Roles (16 warps, one CTA per SM):
 //   warps 0-3, 4-7  softmax; they also stage Q, rescale O and write the output
-//   warps 8-11      producer: int8 K and V by cp.async, kStages operands ahead,
-//                   each thread its own chunks, to f16 in 128-byte-swizzled
+//   warps 8-11      producer: int8 K and V by cp.async, an operand ahead, each
+//                   thread its own chunks, to f16 in 128-byte-swizzled
 //                   shared memory
 //   warps 12, 13    one thread each issues MMAs (MT = 2: of query tile 0, 1;
 //                   MT = 1: Q K^T, P V)
@@ -69,9 +69,11 @@ constexpr float kBias = 8.0f;
 constexpr float kSlack = 6.0f;
 constexpr long long kWait = 2000000000LL;
 constexpr int kChain = 4;            // tiles summed in one accumulator (F32 rows)
-constexpr int kSlots = 3;            // operands of the ring
-constexpr int kStages = 3;           // int8 operands on their way
-constexpr int kConsts = 8;           // tiles whose scales are kept: fewer than that are under way
+constexpr int kSlots = 4;            // operands of the ring: K of a tile takes the place of K two tiles before,
+                                     // free since that tile's S, not that of a V, free only after its weights
+constexpr int kStages = 2;           // int8 operands on their way
+constexpr int kConsts = 4;           // tiles whose scales are kept: K of a tile is stored when S of the
+                                     // tile two before is done, so when the weights of four before were used
 constexpr int kHalf = kTileKv * 128; // bytes of 64 columns of 128 rows of f16
 // Registers of a thread after the split (of the 128 at launch): softmax,
 // producer, issue. 256 * 168 + 128 * 96 + 128 * 64 <= 512 * 128.
@@ -82,11 +84,10 @@ __host__ __device__ constexpr int operand_bytes() { return kTileKv * D * 2; }
 
 struct Shared {
     uint64_t full[kSlots], empty[kSlots], cfull[kConsts];
-    uint64_t q_ready[2], s_full[2], p_ready[2], pv_done[2], drained[2], m_ready[2], l_ready;
+    uint64_t q_ready[2], s_full[2], p_ready[2][2], pv_done[2], drained[2], m_ready[2], l_ready;
     float4 cst[kConsts][kBlocks];   // K scale, log2 of the V scale, its inverse
     float raw[kConsts][2 * kBlocks];
-    float mul[2 * kTileQ];
-    float m[2][kTileQ], l[2][kTileQ], m_run[kTileQ];
+    float rows[3 * kTileQ];   // each row's factor (of MT tiles), then for MT = 1 its maximum after the even and the odd tiles
     uint32_t tmem;
     int abort;
     int scan[kThreads / 32];
@@ -95,7 +96,7 @@ struct Shared {
 
 template <int D, int PARTS, int MT>
 __host__ __device__ constexpr int smem_bytes() {
-    return 1024 + (MT * PARTS + kSlots) * operand_bytes<D>() + kStages * operand_bytes<D>() / 2 + (int)sizeof(Shared);
+    return (MT * PARTS + kSlots) * operand_bytes<D>() + kStages * operand_bytes<D>() / 2 + (int)sizeof(Shared);
 }
 
 // MN-major operand in the 128-byte-swizzled canonical layout: rows (k) of 64
@@ -217,13 +218,19 @@ __device__ __forceinline__ float tile_top(uint32_t ts, float mul, const float4* 
     return fmaxf(top, piece_top<MASKED>(b, mul, cst + 6, lo - 96, hi - 96));
 }
 
-// The tile's weights in place of its S.
+// The tile's weights in place of its S; each half of them is handed on as soon as it is there.
 template <bool MASKED, int PARTS>
-__device__ __forceinline__ void tile_weights(uint32_t ts, float mul, float sub, const float4* cst, int lo, int hi, float& l) {
+__device__ __forceinline__ void tile_weights(uint32_t ts, float mul, float sub, const float4* cst, int lo, int hi, float& l,
+                                             uint64_t* ready) {
     uint32_t a[32], b[32], hi16[16], lo16[16];
     auto store = [&](uint32_t at) {
         tc::tmem_st_32x32b_x16(at, hi16);
         if (PARTS == 2) tc::tmem_st_32x32b_x16(at + 16u, lo16);
+    };
+    auto hand_on = [&](int half) {
+        tc::tmem_st_wait();
+        tc::tc_fence_before();
+        tc::mbar_arrive(&ready[half]);
     };
     tc::tmem_ld_32x32b_x32(ts, a);
     tc::tmem_ld_wait();
@@ -235,13 +242,51 @@ __device__ __forceinline__ void tile_weights(uint32_t ts, float mul, float sub, 
     piece_weights<MASKED, PARTS>(b, mul, sub, cst + 2, lo - 32, hi - 32, l, hi16, lo16);
     store(ts + 32u);
     tc::tmem_ld_wait();
+    hand_on(0);
     tc::tmem_ld_32x32b_x32(ts + 96u, b);
     piece_weights<MASKED, PARTS>(a, mul, sub, cst + 4, lo - 64, hi - 64, l, hi16, lo16);
     store(ts + 64u);
     tc::tmem_ld_wait();
     piece_weights<MASKED, PARTS>(b, mul, sub, cst + 6, lo - 96, hi - 96, l, hi16, lo16);
     store(ts + 96u);
-    tc::tmem_st_wait();
+    hand_on(1);
+}
+
+// The MMA wrappers of tc.cuh for a warp whose control flow stays uniform (the
+// operands then live in uniform registers, where an MMA inside a branch of one
+// lane takes about 90 cycles to issue): `lead` is not zero in one lane.
+__device__ __forceinline__ void umma_ss(uint32_t lead, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                        uint32_t accumulate) {
+    asm volatile(
+        "{\n"
+        ".reg .pred p, q;\n"
+        "setp.ne.b32 p, %4, 0;\n"
+        "setp.ne.b32 q, %5, 0;\n"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n"
+        "}\n" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(lead)
+        : "memory");
+}
+__device__ __forceinline__ void umma_ts(uint32_t lead, uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                        uint32_t accumulate) {
+    asm volatile(
+        "{\n"
+        ".reg .pred p, q;\n"
+        "setp.ne.b32 p, %4, 0;\n"
+        "setp.ne.b32 q, %5, 0;\n"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n"
+        "}\n" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(lead)
+        : "memory");
+}
+__device__ __forceinline__ void commit(uint32_t lead, uint64_t* bar) {
+    asm volatile(
+        "{\n"
+        ".reg .pred q;\n"
+        "setp.ne.b32 q, %1, 0;\n"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n"
+        "}\n" ::"r"(tc::smem_u32(bar)), "r"(lead)
+        : "memory");
 }
 
 }  // namespace kvt
@@ -265,10 +310,9 @@ __global__ void __launch_bounds__(kvt::kThreads, 1)
     constexpr bool kChained = PARTS == 2;
     constexpr int kOp = operand_bytes<D>();
     constexpr int kKSteps = D / 16, kVSteps = kTileKv / 16;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-    uint8_t* sQ = smem;                                  // [query tile][part]
-    uint8_t* sKV = smem + MT * PARTS * kOp;              // ring of f16 operands
+    extern __shared__ __align__(1024) uint8_t smem_tile[];
+    uint8_t* sQ = smem_tile;                                  // [query tile][part]
+    uint8_t* sKV = sQ + MT * PARTS * kOp;              // ring of f16 operands
     uint8_t* sRaw = sKV + kSlots * kOp;                  // ring of int8 operands
     Shared& S = *reinterpret_cast<Shared*>(sRaw + kStages * kOp / 2);
 
@@ -321,7 +365,8 @@ __global__ void __launch_bounds__(kvt::kThreads, 1)
         for (int i = 0; i < 2; ++i) {
             tc::mbar_init(&S.q_ready[i], 256 / MT);
             tc::mbar_init(&S.s_full[i], 1);
-            tc::mbar_init(&S.p_ready[i], 128);
+            tc::mbar_init(&S.p_ready[i][0], 128);
+            tc::mbar_init(&S.p_ready[i][1], 128);
             tc::mbar_init(&S.pv_done[i], 1);
             tc::mbar_init(&S.drained[i], 1);
             tc::mbar_init(&S.m_ready[i], 128);
@@ -378,42 +423,46 @@ __global__ void __launch_bounds__(kvt::kThreads, 1)
         const int n = steps_of(qt);
         const int tile_row = row_lo + qt * kTileQ;
         if (n > 0) {
-            // Q: each warp 32 (MT = 2) or 16 of the rows, a lane 4 (D = 128) or 2 consecutive values
+            // Q: each warp 32 (MT = 2) or 16 of the rows, 16 at a time, a lane 4
+            // (D = 128) or 2 consecutive values. Rows past the last are copies of it.
             constexpr int VPL = D / 32;
             constexpr int kWarpRows = MT == 2 ? 32 : 16;
             const int r0 = (MT == 2 ? warp & 3 : warp) * kWarpRows;
             uint8_t* q0 = sQ + qt * PARTS * kOp;
-            constexpr int kBatch = 8;
 #pragma unroll 1
-            for (int i0 = 0; i0 < kWarpRows; i0 += kBatch) {
-                float x[kBatch][VPL];
+            for (int i0 = 0; i0 < kWarpRows; i0 += 16) {
+                Kv8Vec<T, VPL> raw[16];
+                const int row = min(tile_row + r0 + i0, row_hi - 1);
+                int ti = row / group, g = row - ti * group, left = row_hi - 1 - row;
+                const T* q_at = static_cast<const T*>(a.q.data) + VPL * lane + (long long)head * group * a.q.head_stride;
 #pragma unroll
-                for (int i = 0; i < kBatch; ++i) {
-                    const int row = tile_row + r0 + i0 + i;
-                    if (row < row_hi) {
-                        const int ti = row / group, hh = head * group + row - ti * group;
-                        kv8_load<T, VPL>(static_cast<const T*>(a.q.data) + (sq.row0 + ti) * a.q.row_stride +
-                                             hh * a.q.head_stride + VPL * lane, x[i]);
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < VPL; ++j) x[i][j] = 0.0f;
+                for (int i = 0; i < 16; ++i) {
+                    raw[i] = *reinterpret_cast<const Kv8Vec<T, VPL>*>(q_at + (sq.row0 + ti) * a.q.row_stride +
+                                                                       g * a.q.head_stride);
+                    if (left > 0) {
+                        --left;
+                        if (++g == group) g = 0, ++ti;
                     }
                 }
 #pragma unroll
-                for (int i = 0; i < kBatch; ++i) {
+                for (int i = 0; i < 16; ++i) {
                     const int rr = r0 + i0 + i;
+                    float x[VPL];
                     uint32_t top = 0;
 #pragma unroll
-                    for (int j = 0; j < VPL; ++j) top = max(top, __float_as_uint(x[i][j]) & 0x7fffffffu);
+                    for (int j = 0; j < VPL; ++j) {
+                        x[j] = kv8_f(raw[i].v[j]);
+                        top = max(top, __float_as_uint(x[j]) & 0x7fffffffu);
+                    }
                     top = __reduce_max_sync(0xffffffffu, top);
                     float up, down;
                     kvd::row_scale(top, up, down);
                     // mul is not negative, so the largest S of a block is the largest logit
-                    if (lane == 0) S.mul[qt * kTileQ + rr] = down * (fabsf(a.scale) * 1.44269504088896340736f);
+                    if (lane == 0) S.rows[qt * kTileQ + rr] = down * (fabsf(a.scale) * 1.44269504088896340736f);
                     if (a.scale < 0.0f) up = -up;
                     uint32_t hi[VPL / 2], lo[VPL / 2];
 #pragma unroll
-                    for (int j = 0; j < VPL; j += 2) kvd::split2(x[i][j] * up, x[i][j + 1] * up, hi[j / 2], lo[j / 2]);
+                    for (int j = 0; j < VPL; j += 2) kvd::split2(x[j] * up, x[j + 1] * up, hi[j / 2], lo[j / 2]);
                     const int byte = 2 * VPL * lane;   // in the row of D f16
                     const uint32_t off = (byte >> 7) * kHalf + rr * 128 + ((((byte & 127) >> 4) ^ (rr & 7)) << 4) + (byte & 15);
                     if (VPL == 4) {
@@ -448,7 +497,8 @@ __global__ void __launch_bounds__(kvt::kThreads, 1)
             return ok;
         };
         float mul = 0.0f;
-        if (n > 0 && wait(&S.q_ready[qt], 0)) mul = S.mul[qt * kTileQ + r];
+        if (n > 0 && wait(&S.q_ready[qt], 0)) mul = S.rows[qt * kTileQ + r];
+        float* const s_m = &S.rows[kTileQ];   // [step & 1][row] (MT = 1)
         float m = -INFINITY, l = 0.0f, m_run = -INFINITY;
         for (int j = h; ok && j < n; j += 3 - MT) {
             const int cs = j % kConsts;
@@ -463,7 +513,7 @@ __global__ void __launch_bounds__(kvt::kThreads, 1)
             float before = m;
             if (MT == 1 && j > 0) {   // the maximum up to the tile before, of the other warpgroup
                 if (!wait(&S.m_ready[bf ^ 1], ((j - 1) >> 1) & 1)) break;
-                before = S.m[bf ^ 1][r];
+                before = s_m[(bf ^ 1) * kTileQ + r];
                 if (before != m) l *= m == -INFINITY ? 0.0f : ex2(m - before);
             }
             const bool grown = __any_sync(0xffffffffu, top > before + kSlack);
@@ -476,7 +526,7 @@ __global__ void __launch_bounds__(kvt::kThreads, 1)
                 l *= keep;
             }
             if (MT == 1) {
-                S.m[bf][r] = m;
+                s_m[bf * kTileQ + r] = m;
                 tc::mbar_arrive(&S.m_ready[bf]);
             }
             if ((grown && j > 0) || flush) {
@@ -515,30 +565,28 @@ __global__ void __launch_bounds__(kvt::kThreads, 1)
                 }
             }
             const float sub = m == -INFINITY ? 0.0f : m - kBias;
-            if (masked) tile_weights<true, PARTS>(ts, mul, sub, S.cst[cs], lo, hi, l);
-            else tile_weights<false, PARTS>(ts, mul, sub, S.cst[cs], lo, hi, l);
-            tc::tc_fence_before();
-            tc::mbar_arrive(&S.p_ready[bf]);
+            if (masked) tile_weights<true, PARTS>(ts, mul, sub, S.cst[cs], lo, hi, l, S.p_ready[bf]);
+            else tile_weights<false, PARTS>(ts, mul, sub, S.cst[cs], lo, hi, l, S.p_ready[bf]);
         }
         if (ok && n > 0) {
             const int last = n - 1;
-            if (MT == 1) {
+            if (wait(&S.pv_done[MT == 2 ? qt : last & 1], MT == 2 ? last & 1 : (last >> 1) & 1) && MT == 1 &&
+                wait(&S.m_ready[last & 1], (last >> 1) & 1)) {
                 // the maximum of all tiles, l of both warpgroups, and what the
-                // running sum refers to (the first warpgroup moves O)
-                if (wait(&S.m_ready[last & 1], (last >> 1) & 1)) {
-                    const float all = S.m[last & 1][r];
-                    if (all != m) l *= m == -INFINITY ? 0.0f : ex2(m - all);
-                    m = all;
-                    S.l[h][r] = l;
-                    if (h == 0) S.m_run[r] = m_run;
-                    tc::mbar_arrive(&S.l_ready);
-                    if (wait(&S.l_ready, 0)) {
-                        l += S.l[h ^ 1][r];
-                        m_run = S.m_run[r];
-                    }
+                // running sum refers to (the first warpgroup moves O), through
+                // the memory of Q, which nothing reads any more
+                float* const ex = reinterpret_cast<float*>(sQ);
+                const float all = s_m[(last & 1) * kTileQ + r];
+                if (all != m) l *= m == -INFINITY ? 0.0f : ex2(m - all);
+                m = all;
+                ex[h * kTileQ + r] = l;
+                if (h == 0) ex[2 * kTileQ + r] = m_run;
+                tc::mbar_arrive(&S.l_ready);
+                if (wait(&S.l_ready, 0)) {
+                    l += ex[(h ^ 1) * kTileQ + r];
+                    m_run = ex[2 * kTileQ + r];
                 }
             }
-            if (ok) wait(&S.pv_done[MT == 2 ? qt : last & 1], MT == 2 ? last & 1 : (last >> 1) & 1);
             tc::tc_fence_after();
         }
         constexpr int OC = MT == 2 ? D : D / 2;   // columns of O that a thread writes
@@ -658,14 +706,14 @@ __global__ void __launch_bounds__(kvt::kThreads, 1)
             }
             kvd::cp_commit();
         };
-#pragma unroll 1
-        for (int i = 0; i < kStages - 1; ++i) issue(i);
+        issue(0);
         for (int i = 0; i < 2 * steps; ++i) {
             const int slot = i % kSlots, use = i / kSlots, which = i & 1;
             bool ok = tc::mbar_wait_idle(&S.empty[slot], (use & 1) ^ 1, abort_flag, kWait);
             if (!ok) fail();
             if (__any_sync(0xffffffffu, !ok)) break;
-            kvd::cp_wait<kStages - 2>();   // this thread's chunks of operand i are here
+            kvd::cp_wait<0>();   // this thread's chunks of operand i are here
+            issue(i + 1);        // into the stage of operand i - 1, which this thread has read
             if (which == 0 && warp == kProducerWarp) {
                 const int j = i >> 1, cs = j % kConsts;
                 if (lane < kBlocks) {
@@ -697,13 +745,13 @@ __global__ void __launch_bounds__(kvt::kThreads, 1)
             }
             tc::fence_proxy_async_smem();
             tc::mbar_arrive(&S.full[slot]);
-            issue(i + kStages - 1);   // into the stage of operand i - 1, which this thread has read
         }
         kvd::cp_wait<0>();
     } else {
         // ---------------------------------------------------------- MMA issue
         regs_down<kRegsIssue>();
-        if (lane == 0 && warp < kIssueWarp + 2) {
+        if (warp < kIssueWarp + 2) {
+            const uint32_t lead = lane == 0;
             const int me = warp - kIssueWarp;
             const int qt = MT == 2 ? me : 0;
             const int n = steps_of(qt);
@@ -712,7 +760,8 @@ __global__ void __launch_bounds__(kvt::kThreads, 1)
             const uint32_t to_ = tmem + kColO + (uint32_t)(qt * D);
             const uint64_t qd = tc::sdesc_sw128_kmajor(tc::smem_u32(sQ + qt * PARTS * kOp));
             auto wait = [&](uint64_t* bar, int parity) {
-                return tc::mbar_wait(bar, (uint32_t)parity, abort_flag, kWait);
+                const bool got = tc::mbar_wait(bar, (uint32_t)parity, abort_flag, kWait);
+                return __all_sync(0xffffffffu, got) != 0;
             };
             // S of step j, into buffer bf
             auto qk = [&](int j, int bf) {
@@ -726,28 +775,32 @@ __global__ void __launch_bounds__(kvt::kThreads, 1)
 #pragma unroll
                     for (int k = 0; k < kKSteps; ++k) {
                         const uint64_t off = (uint64_t)((k >> 2) * (kHalf >> 4) + 2 * (k & 3));
-                        tc::umma_f16(ts, qd + (uint64_t)(pt * (kOp >> 4)) + off, kd + off, idesc_qk, pt != PARTS - 1 || k > 0);
+                        umma_ss(lead, ts, qd + (uint64_t)(pt * (kOp >> 4)) + off, kd + off, idesc_qk, pt != PARTS - 1 || k > 0);
                     }
-                tc::umma_commit(&S.empty[slot]);
-                tc::umma_commit(&S.s_full[bf]);
+                commit(lead, &S.empty[slot]);
+                commit(lead, &S.s_full[bf]);
                 return true;
             };
             // O of step j from the weights in buffer bf, ready in phase ph
             auto pv = [&](int j, int bf, int ph) {
                 const int i = 2 * j + 1, slot = i % kSlots;
-                if (!wait(&S.full[slot], (i / kSlots) & 1) || !wait(&S.p_ready[bf], ph)) return false;
-                tc::tc_fence_after();
+                if (!wait(&S.full[slot], (i / kSlots) & 1)) return false;
                 const uint64_t vd = sdesc_sw128_mnmajor(tc::smem_u32(sKV + slot * kOp));
                 const uint32_t ts = tmem + (uint32_t)(bf * kTileKv);
                 const bool first = kChained ? j % kChain == 0 : j == 0;
 #pragma unroll
-                for (int pt = PARTS - 1; pt >= 0; --pt)
+                for (int half = 0; half < 2; ++half) {
+                    if (!wait(&S.p_ready[bf][half], ph)) return false;
+                    tc::tc_fence_after();
 #pragma unroll
-                    for (int k = 0; k < kVSteps; ++k)
-                        tc::umma_f16_tmem_a(to_, ts + (uint32_t)(32 * (k >> 1) + 16 * pt + 8 * (k & 1)),
-                                            vd + (uint64_t)(k * (2048 >> 4)), idesc_pv, !first || pt != PARTS - 1 || k > 0);
-                tc::umma_commit(&S.empty[slot]);
-                tc::umma_commit(&S.pv_done[bf]);
+                    for (int pt = PARTS - 1; pt >= 0; --pt)
+#pragma unroll
+                        for (int k = half * kVSteps / 2; k < (half + 1) * kVSteps / 2; ++k)
+                            umma_ts(lead, to_, ts + (uint32_t)(32 * (k >> 1) + 16 * pt + 8 * (k & 1)),
+                                    vd + (uint64_t)(k * (2048 >> 4)), idesc_pv, !first || pt != PARTS - 1 || k > 0);
+                }
+                commit(lead, &S.empty[slot]);
+                commit(lead, &S.pv_done[bf]);
                 return true;
             };
             bool ok = true;
@@ -780,13 +833,13 @@ __global__ void __launch_bounds__(kvt::kThreads, 1)
                 // tiles that only the other query tile sees
                 for (int i = 2 * n; ok && i < 2 * steps; ++i) {
                     const int slot = i % kSlots;
-                    ok = tc::mbar_wait(&S.full[slot], (i / kSlots) & 1, abort_flag, kWait);
-                    if (ok) tc::mbar_arrive(&S.empty[slot]);
+                    ok = wait(&S.full[slot], (i / kSlots) & 1);
+                    if (ok && lead) tc::mbar_arrive(&S.empty[slot]);
                 }
             }
-            if (!ok) fail();
+            if (!ok && lead) fail();
             // every MMA issued is done before TMEM and shared memory are left
-            tc::umma_commit(&S.drained[me]);
+            commit(lead, &S.drained[me]);
             tc::mbar_wait_drain(&S.drained[me], 0, kWait / 8);
         }
         __syncwarp();
