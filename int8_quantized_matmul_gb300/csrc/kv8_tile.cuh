@@ -36,11 +36,12 @@
 //
 // Roles (16 warps, one CTA per SM):
 //   warps 0-3, 4-7  softmax; they also stage Q, rescale O and write the output
-//   warps 8-11      producer: int8 K and V by cp.async, an operand ahead, each
+//   warps 8-11      producer: int8 K and V by cp.async, a tile ahead, each
 //                   thread its own chunks, to f16 in 128-byte-swizzled
 //                   shared memory
 //   warps 12, 13    one thread each issues MMAs (MT = 2: of query tile 0, 1;
 //                   MT = 1: Q K^T, P V)
+//   warp 14         looks up the pages and the scales of the tiles to come
 // TMEM (512 columns): S (2 x 128 columns of f32), overwritten in place by the
 // weights (32 columns of S become 16 of high and 16 of low parts), and O (MT x D,
 // for F32 rows and the running sum). K is the K-major operand [token][d]; V with
@@ -71,7 +72,7 @@ constexpr long long kWait = 2000000000LL;
 constexpr int kChain = 4;            // tiles summed in one accumulator (F32 rows)
 constexpr int kSlots = 4;            // operands of the ring: K of a tile takes the place of K two tiles before,
                                      // free since that tile's S, not that of a V, free only after its weights
-constexpr int kStages = 2;           // int8 operands on their way
+constexpr int kStages = 2;           // int8 operands on their way: K and V of a tile
 constexpr int kConsts = 4;           // tiles whose scales are kept: K of a tile is stored when S of the
                                      // tile two before is done, so when the weights of four before were used
 constexpr int kHalf = kTileKv * 128; // bytes of 64 columns of 128 rows of f16
@@ -83,10 +84,10 @@ template <int D>
 __host__ __device__ constexpr int operand_bytes() { return kTileKv * D * 2; }
 
 struct Shared {
-    uint64_t full[kSlots], empty[kSlots], cfull[kConsts];
+    uint64_t full[kSlots], empty[kSlots], cfull[kConsts], bfull[kConsts];
     uint64_t q_ready[2], s_full[2], p_ready[2][2], pv_done[2], drained[2], m_ready[2], l_ready;
     float4 cst[kConsts][kBlocks];   // K scale, log2 of the V scale, its inverse
-    float raw[kConsts][2 * kBlocks];
+    const uint8_t* block[kConsts][kBlocks];   // K codes of a tile's blocks, null where there is none
     float rows[3 * kTileQ];   // each row's factor (of MT tiles), then for MT = 1 its maximum after the even and the odd tiles
     uint32_t tmem;
     int abort;
@@ -317,7 +318,8 @@ __global__ void __launch_bounds__(kvt::kThreads, 1)
     Shared& S = *reinterpret_cast<Shared*>(sRaw + kStages * kOp / 2);
 
     const Kv8View& c = a.c;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    // (the shuffle tells the compiler that a warp's index is the same in all its lanes)
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const int group = a.q_heads / c.heads;
     constexpr int kRowsItem = MT * kTileQ;
 
@@ -361,7 +363,10 @@ __global__ void __launch_bounds__(kvt::kThreads, 1)
             tc::mbar_init(&S.full[i], 128);
             tc::mbar_init(&S.empty[i], MT);
         }
-        for (int i = 0; i < kConsts; ++i) tc::mbar_init(&S.cfull[i], 32);
+        for (int i = 0; i < kConsts; ++i) {
+            tc::mbar_init(&S.cfull[i], 32);
+            tc::mbar_init(&S.bfull[i], 32);
+        }
         for (int i = 0; i < 2; ++i) {
             tc::mbar_init(&S.q_ready[i], 256 / MT);
             tc::mbar_init(&S.s_full[i], 1);
@@ -653,7 +658,6 @@ __global__ void __launch_bounds__(kvt::kThreads, 1)
         regs_down<kRegsProducer>();
         const int p = tid - kProducerWarp * 32;
         constexpr int kChunks = D / 16;          // 16-byte chunks of a token's codes, and loads per thread and operand
-        const int* table = c.table + (long long)s * c.width;
         const uint32_t raw = kvd::smem_addr(sRaw) + 16 * p;
         // Load q of a thread: four lanes have 64 codes of a token row (one swizzle
         // atom), eight lanes two rows of it, whose f16 chunks lie in different banks.
@@ -661,88 +665,60 @@ __global__ void __launch_bounds__(kvt::kThreads, 1)
         auto chunk_at = [&](int q) { return (p & 3) + (D == 128 ? 4 * (q & 1) : 0); };
         const int sw = (p >> 2) & 7;
         const int at0 = ((2 * (p & 3)) ^ sw) << 4, at1 = ((2 * (p & 3) + 1) ^ sw) << 4;
-        // lane i < 8 of each warp: the page of block i of tile j, -1: none
-        auto fetch_pages = [&](int j) {
-            int page = -1;
-            const long long tok = (long long)(from + j) * kTileKv + (lane & 7) * kKvBlock;
-            if (j < steps && tok < sq.len) {
-                page = table[tok >> c.page_shift];
-                if (page < 0 || page >= c.n_pages) {
-                    if (warp == kProducerWarp) atomicOr(c.status, kKvBadPage);
-                    page = -1;
-                }
-            }
-            return page;
+        // This thread's rows of a tile: where their K codes lie (null: nowhere),
+        // V's being `plane` further on.
+        constexpr int kRows = 4, kPerRow = kChunks / kRows;   // loads q of a row: kPerRow
+        const uint8_t* src[kRows];
+        const int plane = c.dim << c.page_shift;
+        const int in_row = (row_at(0) & (kKvBlock - 1)) * D + 16 * (p & 3);
+        bool ok = true;
+        auto wait = [&](uint64_t* bar, int parity) {
+            if (!tc::mbar_wait_idle(bar, (uint32_t)parity, abort_flag, kWait)) { fail(); ok = false; }
+            ok = !__any_sync(0xffffffffu, !ok);
+            return ok;
         };
-        int pages = fetch_pages(0), pages_next = fetch_pages(1);
-        unsigned present = 0;   // bit j % kConsts: this lane's block of tile j is there
-        auto issue = [&](int i) {   // operand i: K or V of tile i / 2
-            if (i < 2 * steps) {
-                const int j = i >> 1, which = i & 1;
-                const uint32_t dst = raw + (uint32_t)(i % kStages) * (kOp / 2);
+        auto start_tile = [&](int j) {
+            if (!wait(&S.bfull[j % kConsts], (j / kConsts) & 1)) return;
 #pragma unroll
-                for (int q = 0; q < kChunks; ++q) {
-                    const int r = row_at(q), cc = chunk_at(q);
-                    const int page = __shfl_sync(0xffffffffu, pages, r >> 4);
-                    const int tok = ((from + j) * kTileKv + r) & ((1 << c.page_shift) - 1);
-                    const uint8_t* src = c.pages;
-                    if (page >= 0) src += ((long long)page * c.heads + head) * c.slab + kv8_code_off(c, which, tok) + 16 * cc;
-                    cp16z(dst + 2048u * q, src, page >= 0);
-                }
-                if (which == 0) {
-                    const int cs = j % kConsts;
-                    present &= ~(1u << cs);
-                    if (warp == kProducerWarp && lane < kBlocks && pages >= 0) {
-                        present |= 1u << cs;
-                        const int tok = ((from + j) * kTileKv + lane * kKvBlock) & ((1 << c.page_shift) - 1);
-                        const uint8_t* slab = c.pages + ((long long)pages * c.heads + head) * c.slab;
-                        kvd::cp4(kvd::smem_addr(&S.raw[cs][lane]), slab + kv8_scale_off(c, 0, tok));
-                        kvd::cp4(kvd::smem_addr(&S.raw[cs][kBlocks + lane]), slab + kv8_scale_off(c, 1, tok));
-                    }
-                } else {
-                    pages = pages_next;
-                    pages_next = fetch_pages(j + 2);
-                }
+            for (int k = 0; k < kRows; ++k) {
+                src[k] = S.block[j % kConsts][row_at(k * kPerRow) / kKvBlock];
+                if (src[k] != nullptr) src[k] += in_row;
             }
-            kvd::cp_commit();
         };
-        issue(0);
-        for (int i = 0; i < 2 * steps; ++i) {
-            const int slot = i % kSlots, use = i / kSlots, which = i & 1;
-            bool ok = tc::mbar_wait_idle(&S.empty[slot], (use & 1) ^ 1, abort_flag, kWait);
-            if (!ok) fail();
-            if (__any_sync(0xffffffffu, !ok)) break;
-            kvd::cp_wait<0>();   // this thread's chunks of operand i are here
-            issue(i + 1);        // into the stage of operand i - 1, which this thread has read
-            if (which == 0 && warp == kProducerWarp) {
-                const int j = i >> 1, cs = j % kConsts;
-                if (lane < kBlocks) {
-                    float k = 0.0f, lv = -INFINITY, iv = 0.0f;
-                    if (present >> cs & 1) {
-                        k = S.raw[cs][lane];
-                        const float v = S.raw[cs][kBlocks + lane];
-                        // a scale that no written block has (0 among them) counts as 2^-40
-                        const float some = v < 0x1p-40f ? 0x1p-40f : v;
-                        lv = log2f(some);
-                        // NaN weights make l NaN for the rows that see the block; the others add 0 * 1
-                        iv = v == v ? __fdiv_rn(1.0f, some) : 1.0f;
-                    }
-                    S.cst[cs][lane] = make_float4(k, lv, iv, 0.0f);
-                }
-                tc::mbar_arrive(&S.cfull[cs]);
-            }
-            const uint8_t* src = sRaw + (i % kStages) * (kOp / 2) + 16 * p;
+        auto copy = [&](int q, int stage, int which) {
+            const uint8_t* at = src[q / kPerRow];
+            cp16z(raw + (uint32_t)(stage * (kOp / 2) + 2048 * q),
+                  at == nullptr ? c.pages : at + (which ? plane : 0) + 64 * (q % kPerRow), at != nullptr);
+        };
+        if (steps > 0) start_tile(0);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            if (steps > 0 && ok)
+#pragma unroll
+                for (int q = 0; q < kChunks; ++q) copy(q, i, i);
+            kvd::cp_commit();
+        }
+        for (int i = 0; ok && i < 2 * steps; ++i) {
+            const int slot = i % kSlots, use = i / kSlots, which = i & 1, stage = i & 1;
+            const bool more = i + 2 < 2 * steps;
+            if (which == 0 && more) start_tile((i >> 1) + 1);
+            if (!ok || !wait(&S.empty[slot], (use & 1) ^ 1)) break;
+            kvd::cp_wait<1>();   // this thread's chunks of operand i are here, those of the next may not be
+            const uint8_t* from_raw = sRaw + stage * (kOp / 2) + 16 * p;
             uint8_t* dst = sKV + slot * kOp;
 #pragma unroll
             for (int q = 0; q < kChunks; ++q) {
-                const uint4 x = *reinterpret_cast<const uint4*>(src + 2048 * q);
+                const uint4 x = *reinterpret_cast<const uint4*>(from_raw + 2048 * q);
                 const uint32_t w[4] = {x.x ^ 0x80808080u, x.y ^ 0x80808080u, x.z ^ 0x80808080u, x.w ^ 0x80808080u};
                 uint8_t* base = dst + (chunk_at(q) >> 2) * kHalf + row_at(q) * 128;
                 *reinterpret_cast<uint4*>(base + at0) = make_uint4(kvd::codes2<0x4140>(w[0]), kvd::codes2<0x4342>(w[0]),
                                                                    kvd::codes2<0x4140>(w[1]), kvd::codes2<0x4342>(w[1]));
                 *reinterpret_cast<uint4*>(base + at1) = make_uint4(kvd::codes2<0x4140>(w[2]), kvd::codes2<0x4342>(w[2]),
                                                                    kvd::codes2<0x4140>(w[3]), kvd::codes2<0x4342>(w[3]));
+                // the chunk is read: the one of the same operand of the next tile takes its place
+                if (more) copy(q, stage, which);
             }
+            kvd::cp_commit();
             tc::fence_proxy_async_smem();
             tc::mbar_arrive(&S.full[slot]);
         }
@@ -754,10 +730,11 @@ __global__ void __launch_bounds__(kvt::kThreads, 1)
             const uint32_t lead = lane == 0;
             const int me = warp - kIssueWarp;
             const int qt = MT == 2 ? me : 0;
-            const int n = steps_of(qt);
+            const int n = __shfl_sync(0xffffffffu, steps_of(qt), 0);
+            const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
             constexpr uint32_t idesc_qk = tc::idesc_f16_f32(kTileQ, kTileKv);
             constexpr uint32_t idesc_pv = tc::idesc_f16_f32(kTileQ, D) | kTransposeB;
-            const uint32_t to_ = tmem + kColO + (uint32_t)(qt * D);
+            const uint32_t to_ = tm + kColO + (uint32_t)(qt * D);
             const uint64_t qd = tc::sdesc_sw128_kmajor(tc::smem_u32(sQ + qt * PARTS * kOp));
             auto wait = [&](uint64_t* bar, int parity) {
                 const bool got = tc::mbar_wait(bar, (uint32_t)parity, abort_flag, kWait);
@@ -769,7 +746,7 @@ __global__ void __launch_bounds__(kvt::kThreads, 1)
                 if (!wait(&S.full[slot], (i / kSlots) & 1)) return false;
                 tc::tc_fence_after();
                 const uint64_t kd = tc::sdesc_sw128_kmajor(tc::smem_u32(sKV + slot * kOp));
-                const uint32_t ts = tmem + (uint32_t)(bf * kTileKv);
+                const uint32_t ts = tm + (uint32_t)(bf * kTileKv);
 #pragma unroll
                 for (int pt = PARTS - 1; pt >= 0; --pt)   // the small parts first, while the sum is small
 #pragma unroll
@@ -786,7 +763,7 @@ __global__ void __launch_bounds__(kvt::kThreads, 1)
                 const int i = 2 * j + 1, slot = i % kSlots;
                 if (!wait(&S.full[slot], (i / kSlots) & 1)) return false;
                 const uint64_t vd = sdesc_sw128_mnmajor(tc::smem_u32(sKV + slot * kOp));
-                const uint32_t ts = tmem + (uint32_t)(bf * kTileKv);
+                const uint32_t ts = tm + (uint32_t)(bf * kTileKv);
                 const bool first = kChained ? j % kChain == 0 : j == 0;
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
@@ -841,6 +818,57 @@ __global__ void __launch_bounds__(kvt::kThreads, 1)
             // every MMA issued is done before TMEM and shared memory are left
             commit(lead, &S.drained[me]);
             tc::mbar_wait_drain(&S.drained[me], 0, kWait / 8);
+        } else if (warp == kIssueWarp + 2) {
+            // ------------------------------------------- pages and scales
+            // Lane i < 8: block i of a tile. The table entries are read two tiles
+            // before the pointers are due, the scales when they are.
+            const int* table = c.table + (long long)s * c.width;
+            constexpr int kNoBlock = -1 << 31;   // past the last token: no page, and no bad one
+            auto fetch_page = [&](int j) {
+                const long long tok = (long long)(from + j) * kTileKv + lane * kKvBlock;
+                return lane < kBlocks && j < steps && tok < sq.len ? table[tok >> c.page_shift] : kNoBlock;
+            };
+            auto hand_block = [&](int j, int page) {   // returns (K scale, V scale; negative: no block)
+                float2 sc = make_float2(0.0f, -1.0f);
+                if (lane < kBlocks) {
+                    const uint8_t* at = nullptr;
+                    if (page >= 0 && page < c.n_pages) {
+                        const int tok = ((from + j) * kTileKv + lane * kKvBlock) & ((1 << c.page_shift) - 1);
+                        const uint8_t* slab = c.pages + ((long long)page * c.heads + head) * c.slab;
+                        at = slab + kv8_code_off(c, 0, tok);
+                        sc.x = *reinterpret_cast<const float*>(slab + kv8_scale_off(c, 0, tok));
+                        sc.y = *reinterpret_cast<const float*>(slab + kv8_scale_off(c, 1, tok));
+                        if (sc.y < 0x1p-40f) sc.y = 0x1p-40f;   // a scale that no written block has (0 among them)
+                    } else if (page != kNoBlock) {
+                        atomicOr(c.status, kKvBadPage);
+                    }
+                    S.block[j % kConsts][lane] = at;
+                }
+                tc::mbar_arrive(&S.bfull[j % kConsts]);
+                return sc;
+            };
+            int page0 = fetch_page(0), page1 = fetch_page(1), page2 = fetch_page(2);
+            float2 sc0 = hand_block(0, page0), sc1 = hand_block(1, page1);
+            bool ok = true;
+            for (int j = 0; ok && j < steps; ++j) {
+                const int page3 = fetch_page(j + 3);
+                const int i = 2 * j;   // the scales of four tiles before are done with when K's slot is free
+                ok = tc::mbar_wait(&S.empty[i % kSlots], ((i / kSlots) & 1) ^ 1, abort_flag, kWait);
+                if (!ok) fail();
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                if (lane < kBlocks) {
+                    const float k = sc0.x, v = sc0.y;
+                    // NaN weights make l NaN for the rows that see the block; the others add 0 * 1
+                    S.cst[j % kConsts][lane] = v < 0.0f ? make_float4(0.0f, -INFINITY, 0.0f, 0.0f)
+                                                        : make_float4(k, log2f(v), v == v ? __fdiv_rn(1.0f, v) : 1.0f, 0.0f);
+                }
+                tc::mbar_arrive(&S.cfull[j % kConsts]);
+                sc0 = sc1;
+                // the pointers of tile j - 2, in the same place, were read before K of tile j - 2 was stored
+                if (j + 2 < steps) sc1 = hand_block(j + 2, page2);
+                page2 = page3;
+            }
         }
         __syncwarp();
     }
