@@ -611,8 +611,8 @@ int w8a8_mul_mat_grouped(const w8a8_problem* probs, int count, int64_t M, void* 
  * elements are distinct.
  *
  * Limits: head_dim 64 or 128, 1 <= heads <= 1024, 1 <= seqs <= KV8_MAX_SEQS,
- * 1 <= max_rows <= rows < 2^31, table_width*page_tokens < 2^31. Errors of every
- * call: BAD_SHAPE, NULL_PTR, MISALIGNED, BAD_ARG (an unknown dtype or flag, or
+ * 1 <= max_rows <= rows < 2^31, table_width*page_tokens < 2^31,
+ * seqs*heads*table_width*page_tokens < 2^35. Errors of every call: BAD_SHAPE, NULL_PTR, MISALIGNED, BAD_ARG (an unknown dtype or flag, or
  * an output that overlaps another operand), UNSUPPORTED_DEVICE, CUDA.
  * ------------------------------------------------------------------------- */
 #define KV8_BLOCK 16

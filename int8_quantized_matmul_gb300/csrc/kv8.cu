@@ -323,6 +323,8 @@ int check_sizes(const kv8_cache& c, const kv8_batch& b, Kv8View& w) {
         b.max_rows > b.rows)
         return I2S_E_BAD_SHAPE;
     if (b.table_width < 1 || b.table_width >= ((int64_t)1 << 31) / c.page_tokens) return I2S_E_BAD_SHAPE;
+    // blocks of all sequences and heads are counted in 32 bits
+    if (b.table_width * (c.page_tokens / kKvBlock) >= ((int64_t)1 << 31) / ((int64_t)b.seqs * c.heads)) return I2S_E_BAD_SHAPE;
     w.n_pages = c.n_pages;
     w.rows = b.rows;
     w.width = b.table_width;

@@ -31,10 +31,11 @@
 // for two codes) and subtracting 1152.
 //
 // Work split. The blocks of all items, item by item, are cut into equal
-// contiguous ranges, one per CTA (kDecodeCtas resident at once), so ragged
-// lengths leave no SM idle. The four warps of a CTA take the blocks of a range
-// in turn, each with its own ring of kStages blocks filled by cp.async and its
-// own running maximum, and join through shared memory. An item cut between
+// contiguous ranges, one per CTA, so ragged lengths leave no SM idle; kRounds
+// times as many CTAs as fit at once, so the SMs that memory serves faster take
+// more of them. The four warps of a CTA take the blocks of a range
+// in turn, two at a time, each with its own ring filled by cp.async a pair ahead
+// and its own running maximum, and join through shared memory. An item cut between
 // CTAs leaves its parts (O, m, l in F32) in the workspace for k_kv8_join.
 #pragma once
 
@@ -46,23 +47,28 @@ namespace kvd {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-constexpr int kStages = 4;
+constexpr int kStages = 2;           // pairs of blocks in a warp's ring
 constexpr int kRows = 8;             // query rows of an item
 constexpr int kCtasPerSm = 3;
-constexpr int kMaxCtas = 152 * kCtasPerSm;
-constexpr int kGrain = 2 * kWarps;   // blocks a CTA takes at least: below, a join costs more than it saves
+constexpr int kMaxCtas = 152 * kCtasPerSm;   // two or three times as many, each with less: 2 to 13 % slower (64 sequences)
+constexpr int kStart = 14;            // blocks that an item's start counts for
+constexpr int kGrain = kStart + 2 * kWarps;   // places (of the order below) that a CTA takes at least: below, a join costs more than it saves
 constexpr float kBias = 8.0f;
 constexpr float kSlack = 6.0f;       // m follows the maximum only when it grows by more
+constexpr int kNoBlock = -0x7fffffff - 1;    // in the place of a page: past the part's blocks
 constexpr int kExpLo = -40, kExpHi = 86;
 
 template <int D>
-__host__ __device__ constexpr int stage_bytes() { return 2 * kKvBlock * D + 16; }
+__host__ __device__ constexpr int block_bytes() { return 2 * kKvBlock * D + 16; }   // codes, the two scales
 template <int D>
-__host__ __device__ constexpr int ring_bytes() { return kWarps * kStages * stage_bytes<D>(); }
+__host__ __device__ constexpr int ring_bytes() { return kWarps * kStages * 2 * block_bytes<D>(); }
 
 // The blocks [lo, hi) that any row of a sequence sees.
 struct Span {
     int lo, hi;
+    // its length in the order that is cut into ranges: starting an item costs as
+    // much time as some blocks do
+    __device__ __forceinline__ int cost() const { return lo == hi ? 0 : hi - lo + kStart; }
 };
 __device__ __forceinline__ Span span_of(const Kv8AttnArgs& a, const Kv8Seq& q) {
     if (q.n == 0 || q.len == 0) return {0, 0};
@@ -151,11 +157,14 @@ __global__ void __launch_bounds__(kvd::kThreads, kvd::kCtasPerSm)
     using T = typename Kv8T<DT>::type;
     constexpr int kSteps = D / 16;    // k steps of Q K^T
     constexpr int kTiles = D / 8;     // n tiles of P V
-    constexpr int kStage = stage_bytes<D>();
+    constexpr int kBlk = block_bytes<D>(), kRing = kStages * 2 * kBlk;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int s_scan[kWarps];
-    __shared__ long long s_total;
     __shared__ int s_at[2];
+    __shared__ volatile struct {
+        long long row0;
+        int seq, head, item_x, b_at, blocks, count, rows, x, x_seq;
+    } s_part;
     __shared__ float s_m[kWarps][kRows], s_l[kWarps][kRows];
 
     const Kv8View& c = a.c;
@@ -169,8 +178,7 @@ __global__ void __launch_bounds__(kvd::kThreads, kvd::kCtasPerSm)
     for (int i = 0; i < per; ++i) {
         const int s = tid * per + i;
         if (s < c.seqs) {
-            const Span p = span_of(a, kv8_seq(c, s));
-            mine += p.hi - p.lo;
+            mine += span_of(a, kv8_seq(c, s)).cost();
         }
     }
     int before = mine;
@@ -181,116 +189,139 @@ __global__ void __launch_bounds__(kvd::kThreads, kvd::kCtasPerSm)
     }
     if (lane == 31) s_scan[warp] = before;
     __syncthreads();
-    long long base = before - mine, all = 0;
+    int base = before - mine, all = 0;
     for (int w = 0; w < kWarps; ++w) {
         if (w < warp) base += s_scan[w];
         all += s_scan[w];
     }
+    // CTA i takes [start(i), start(i + 1)) of `all` (below 2^31); an item is
+    // kStart places that hold nothing and then its blocks
     all *= c.heads;
-    const long long ctas = min((long long)gridDim.x, (all + kGrain - 1) / kGrain);
-    if (blockIdx.x >= ctas) return;
-    long long x = all * blockIdx.x / ctas;
-    const long long x_end = all * (blockIdx.x + 1) / ctas;
+    const int ctas = min((int)gridDim.x, (all + kGrain - 1) / kGrain);
+    const int cta = blockIdx.x;
+    if (cta >= ctas) return;
+    const int each = all / ctas, more = all - each * ctas;
+    int x = cta * each + min(cta, more);
+    const int x_end = x + each + (cta < more);
     if (mine > 0 && base * c.heads <= x && x < (base + mine) * c.heads) {
         int s = tid * per;
-        long long at = base;
+        int at = base;
         for (; s + 1 < c.seqs; ++s) {
-            const Span p = span_of(a, kv8_seq(c, s));
-            if (x < (at + p.hi - p.lo) * c.heads) break;
-            at += p.hi - p.lo;
+            const int cost = span_of(a, kv8_seq(c, s)).cost();
+            if (x < (at + cost) * c.heads) break;
+            at += cost;
         }
         s_at[0] = s;
-        s_total = at * c.heads;
+        s_at[1] = at * c.heads;
     }
     __syncthreads();
     int s = s_at[0];
-    long long x_seq = s_total;   // the sequence's first block in the whole order
+    int x_seq = s_at[1];   // the sequence's first block in the whole order
 
-    const uint32_t ring = smem_addr(smem) + warp * kStages * kStage;
-    uint8_t* ring_p = smem + warp * kStages * kStage;
+    const uint32_t ring = smem_addr(smem) + warp * kRing;
+    uint8_t* ring_p = smem + warp * kRing;
 
     while (x < x_end) {
+        // The part of [x, x_end) that lies in one item.
         Kv8Seq sq = kv8_seq(c, s);
         Span sp = span_of(a, sq);
-        while (s + 1 < c.seqs && x >= x_seq + (long long)(sp.hi - sp.lo) * c.heads) {
-            x_seq += (long long)(sp.hi - sp.lo) * c.heads;
+        while (s + 1 < c.seqs && x >= x_seq + sp.cost() * c.heads) {
+            x_seq += sp.cost() * c.heads;
             ++s;
             sq = kv8_seq(c, s);
             sp = span_of(a, sq);
         }
-        const int blocks = sp.hi - sp.lo;
-        const int head = (int)((x - x_seq) / blocks);
-        const int b_at = (int)((x - x_seq) - (long long)head * blocks);
-        const int b_lo = sp.lo + b_at;
-        const int count = (int)min((long long)(blocks - b_at), x_end - x);
-        const long long item_x = x - b_at;
-        x += count;
+        const int cost = sp.cost(), blocks = sp.hi - sp.lo;
+        const int head = (x - x_seq) / cost;
+        const int item_x = x_seq + head * cost;
+        const int b_at = max(x - item_x - kStart, 0), count = min(cost, x_end - item_x) - kStart - b_at;
+        const int x_next = min(item_x + cost, x_end);
+        if (count <= 0) {   // only places before the blocks
+            x = x_next;
+            continue;
+        }
+        const int b_lo = sp.lo + b_at, rows = min(sq.n * group, kRows);
+        // What only the join and the next part need waits in shared memory: the
+        // registers are the accumulators'.
+        if (tid == 0) {
+            s_part.seq = s, s_part.head = head, s_part.item_x = item_x, s_part.b_at = b_at, s_part.blocks = blocks;
+            s_part.count = count, s_part.rows = rows, s_part.row0 = sq.row0;
+            s_part.x = x_next, s_part.x_seq = x_seq;
+        }
 
-        // The warp's blocks: b_lo + warp + kWarps * i. Lane l holds the page of
-        // its l-th block of the current 32.
-        const int own = count > warp ? (count - warp + kWarps - 1) / kWarps : 0;
+        // Query row g of the item, on its way while the pages are looked up.
+        const bool live = g < rows;
+        Kv8Vec<T, 4> q_raw[kSteps];
+        {
+            const int ti = live ? g / group : 0;
+            const int hh = head * group + (live ? g - ti * group : 0);
+            const T* src = static_cast<const T*>(a.q.data) + (sq.row0 + ti) * a.q.row_stride + hh * a.q.head_stride;
+#pragma unroll
+            for (int k = 0; k < kSteps; ++k)
+                q_raw[k] = *reinterpret_cast<const Kv8Vec<T, 4>*>(src + (k >> 2) * 64 + 16 * t + 4 * (k & 3));
+        }
+        // The warp's pairs of blocks: b_lo + 2 (warp + kWarps * i) and the one
+        // after. Lane l holds the page of block l & 1 of its (l / 2)-th pair of
+        // the current 16.
+        const int pairs = (count + 1) / 2;
+        const int own = pairs > warp ? (pairs - warp + kWarps - 1) / kWarps : 0;
         const int* table = c.table + (long long)s * c.width;
-        int pages = -1;
+        int pages;
         auto fetch_pages = [&](int i0) {
             pages = -1;
-            if (i0 + lane < own) {
-                const int b = b_lo + warp + kWarps * (i0 + lane);
-                pages = table[(long long)b * kKvBlock >> c.page_shift];
-                if (pages < 0 || pages >= c.n_pages) {
-                    atomicOr(c.status, kKvBadPage);
-                    pages = -1;
-                }
-            }
+            const int at = 2 * (warp + kWarps * (i0 + (lane >> 1))) + (lane & 1);
+            if (at < count) pages = table[(long long)(b_lo + at) * kKvBlock >> c.page_shift];
+            else pages = kNoBlock;
         };
-        int issued = 0;
-        unsigned present = 0;   // stages that hold a block
-        auto issue = [&]() {
-            if (issued < own) {
-                if ((issued & 31) == 0) fetch_pages(issued);
-                const int page = __shfl_sync(0xffffffffu, pages, issued & 31);
-                const int stage = issued % kStages;
-                present &= ~(1u << stage);
-                if (page >= 0) {
-                    present |= 1u << stage;
-                    const int tok = (b_lo + warp + kWarps * issued) * kKvBlock & ((1 << c.page_shift) - 1);
-                    const uint8_t* slab = c.pages + ((long long)page * c.heads + head) * c.slab;
-                    const uint8_t* kp = slab + kv8_code_off(c, 0, tok);
-                    const uint8_t* vp = slab + kv8_code_off(c, 1, tok);
-                    const uint32_t dst = ring + stage * kStage;
-                    constexpr int kChunks = D;   // 16-byte chunks of a block's K codes: 16 * D / 16
-#pragma unroll
-                    for (int i = 0; i < kChunks / 32; ++i) {
-                        const int ch = i * 32 + lane, r = ch / (D / 16), cc = ch % (D / 16);
-                        cp16(dst + k_off<D>(r, cc), kp + ch * 16);
-                        cp16(dst + kKvBlock * D + v_off<D>(r, cc), vp + ch * 16);
+        unsigned present = 0;   // bit 2 * stage + b: block b of the stage's pair is there
+        auto issue = [&](int i) {
+            if (i < own) {
+                if ((i & 15) == 0) {
+                    fetch_pages(i);
+                    if (pages < 0 || pages >= c.n_pages) {
+                        if (pages != kNoBlock) atomicOr(c.status, kKvBadPage);
+                        pages = -1;
                     }
-                    if (lane < 2) cp4(dst + 2 * kKvBlock * D + 4 * lane, slab + kv8_scale_off(c, lane, tok));
                 }
-                ++issued;
+                const int stage = i & 1;
+                present &= ~(3u << (2 * stage));
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    const int page = __shfl_sync(0xffffffffu, pages, 2 * (i & 15) + b);
+                    if (page >= 0) {
+                        present |= 1u << (2 * stage + b);
+                        const int tok = (b_lo + 2 * (warp + kWarps * i) + b) * kKvBlock & ((1 << c.page_shift) - 1);
+                        const uint8_t* slab = c.pages + ((long long)page * c.heads + head) * c.slab;
+                        const uint8_t* kp = slab + kv8_code_off(c, 0, tok) + 16 * lane;
+                        const uint8_t* vp = slab + kv8_code_off(c, 1, tok) + 16 * lane;
+                        const uint32_t dst = ring + (2 * stage + b) * kBlk;
+                        constexpr int kChunks = D;   // 16-byte chunks of a block's K codes: 16 * D / 16
+#pragma unroll
+                        for (int k = 0; k < kChunks / 32; ++k) {
+                            const int ch = k * 32 + lane, r = ch / (D / 16), cc = ch % (D / 16);
+                            cp16(dst + k_off<D>(r, cc), kp + k * 512);
+                            cp16(dst + kKvBlock * D + v_off<D>(r, cc), vp + k * 512);
+                        }
+                        if (lane < 2) cp4(dst + 2 * kKvBlock * D + 4 * lane, slab + kv8_scale_off(c, lane, tok));
+                    }
+                }
             }
             cp_commit();
         };
-#pragma unroll
-        for (int i = 0; i < kStages - 1; ++i) issue();
+        issue(0);
 
-        // Query fragments of row g: hi parts as rows 0-7, lo parts as rows 8-15.
-        const int rows = min(sq.n * group, kRows);
-        const bool live = g < rows;
-        const int tok_i = live ? g / group : 0;
-        const int q_head = head * group + (live ? g - tok_i * group : 0);
-        const long long q_row = sq.row0 + tok_i;
         uint32_t qa[kSteps][4];
         float mul;
         {
             float q[kSteps][4];
             uint32_t top = 0;
-            const T* src = static_cast<const T*>(a.q.data) + q_row * a.q.row_stride + q_head * a.q.head_stride;
 #pragma unroll
             for (int k = 0; k < kSteps; ++k) {
-                if (live) kv8_load<T, 4>(src + (k >> 2) * 64 + 16 * t + 4 * (k & 3), q[k]);
-                else q[k][0] = q[k][1] = q[k][2] = q[k][3] = 0.0f;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) top = max(top, __float_as_uint(q[k][j]) & 0x7fffffffu);
+                for (int j = 0; j < 4; ++j) {
+                    q[k][j] = live ? kv8_f(q_raw[k].v[j]) : 0.0f;
+                    top = max(top, __float_as_uint(q[k][j]) & 0x7fffffffu);
+                }
             }
             top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
             top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
@@ -306,7 +337,7 @@ __global__ void __launch_bounds__(kvd::kThreads, kvd::kCtasPerSm)
         // The tokens row g sees: [see_lo, see_hi). Those of unused rows, all.
         int see_lo = 0, see_hi = sq.len;
         if (live && a.causal) {
-            const int pos = (int)((long long)sq.len - sq.n + tok_i);
+            const int pos = (int)((long long)sq.len - sq.n + g / group);
             see_hi = min(sq.len, pos + 1);
             if (a.window) see_lo = max(0, pos - a.window + 1);
         }
@@ -323,39 +354,55 @@ __global__ void __launch_bounds__(kvd::kThreads, kvd::kCtasPerSm)
         for (int i = 0; i < kTiles; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
 
         for (int it = 0; it < own; ++it) {
-            cp_wait<kStages - 2>();
-            __syncwarp();   // this block is here, and every lane is done with the one before, whose stage is filled next
-            issue();
-            const int stage = it % kStages;
-            const uint8_t* st = ring_p + stage * kStage;
-            if (present >> stage & 1) {
-                const float ks = *reinterpret_cast<const float*>(st + 2 * kKvBlock * D);
-                const float vs = *reinterpret_cast<const float*>(st + 2 * kKvBlock * D + 4);
-                float sc[2][4] = {};
+            cp_wait<0>();
+            __syncwarp();   // this pair is here, and every lane is done with the one before, whose stage is filled next
+            issue(it + 1);
+            const int stage = it & 1;
+            const uint8_t* st = ring_p + 2 * stage * kBlk;
+            const unsigned there = present >> (2 * stage) & 3;
+            if (there != 0) {
+                // The two blocks' chains are independent: each fills the other's
+                // waits. One that is not there is computed from what the stage
+                // holds, and hidden.
+                float sc[2][2][4] = {};   // [block][half of its tokens]
 #pragma unroll
                 for (int cc = 0; cc < D / 64; ++cc) {
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const uint4 w = *reinterpret_cast<const uint4*>(st + k_off<D>(4 * (g >> 1) + 2 * j + (g & 1), 4 * cc + t));
-                        const uint32_t kw[4] = {w.x ^ 0x80808080u, w.y ^ 0x80808080u, w.z ^ 0x80808080u, w.w ^ 0x80808080u};
+                    for (int b = 0; b < 2; ++b) {
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            mma16816(sc[j], qa[4 * cc + k], codes2<0x4140>(kw[k]), codes2<0x4342>(kw[k]));
+                        for (int j = 0; j < 2; ++j) {
+                            const uint4 w = *reinterpret_cast<const uint4*>(
+                                st + b * kBlk + k_off<D>(4 * (g >> 1) + 2 * j + (g & 1), 4 * cc + t));
+                            const uint32_t kw[4] = {w.x ^ 0x80808080u, w.y ^ 0x80808080u, w.z ^ 0x80808080u, w.w ^ 0x80808080u};
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                mma16816(sc[b][j], qa[4 * cc + k], codes2<0x4140>(kw[k]), codes2<0x4342>(kw[k]));
+                        }
                     }
                 }
-                const int e = min(max((int)(__float_as_uint(vs) >> 23 & 255) - 127, kExpLo), kExpHi);
-                const float f = vs * __int_as_float((127 - e) << 23);
-                const float xm = mul * ks, ef = (float)e;
-                float y[4];
+                const int tok = (b_lo + 2 * (warp + kWarps * it)) * kKvBlock;
+                const bool masked = tok < all_lo || tok + 2 * kKvBlock > all_hi || there != 3;
+                float y[2][4], f[2], un[2];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) y[j] = fmaf(sc[j >> 1][j & 1] + sc[j >> 1][2 + (j & 1)], xm, ef);
-                const int tok = (b_lo + warp + kWarps * it) * kKvBlock;
-                if (tok < all_lo || tok + kKvBlock > all_hi) {
+                for (int b = 0; b < 2; ++b) {
+                    const float2 kv = *reinterpret_cast<const float2*>(st + b * kBlk + 2 * kKvBlock * D);   // the two scales
+                    const int e = min(max((int)(__float_as_uint(kv.y) >> 23 & 255) - 127, kExpLo), kExpHi);
+                    un[b] = __int_as_float((127 - e) << 23);
+                    f[b] = kv.y * un[b];
+                    const float xm = mul * kv.x, ef = (float)e;
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
-                        if (tok + 4 * t + j < see_lo || tok + 4 * t + j >= see_hi) y[j] = -INFINITY;
+                        y[b][j] = fmaf(sc[b][j >> 1][j & 1] + sc[b][j >> 1][2 + (j & 1)], xm, ef);
+                    if (masked) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const int at = tok + b * kKvBlock + 4 * t + j;
+                            if (at < see_lo || at >= see_hi || !(there >> b & 1)) y[b][j] = -INFINITY;
+                        }
+                    }
                 }
-                float top = fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3]));
+                float top = fmaxf(fmaxf(fmaxf(y[0][0], y[0][1]), fmaxf(y[0][2], y[0][3])),
+                                  fmaxf(fmaxf(y[1][0], y[1][1]), fmaxf(y[1][2], y[1][3])));
                 if (__any_sync(0xffffffffu, top > m + kSlack)) {   // also the first block: m is -infinity
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
@@ -369,37 +416,43 @@ __global__ void __launch_bounds__(kvd::kThreads, kvd::kCtasPerSm)
                         for (int j = 0; j < 4; ++j) o[i][j] *= keep;
                 }
                 const float sub = m == -INFINITY ? 0.0f : m - kBias;
-                float p[4];
+                uint32_t pa[2][4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) p[j] = ex2(y[j] - sub);
-                l = fmaf(p[0] + p[1] + (p[2] + p[3]), __int_as_float((127 - e) << 23), l);
-                uint32_t pa[4];
-                float pf[4];   // a token that the row does not see is zero even where the block's scale is NaN
+                for (int b = 0; b < 2; ++b) {
+                    float p[4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) pf[j] = y[j] == -INFINITY ? 0.0f : p[j] * f;
-                split2(pf[0], pf[1], pa[0], pa[1]);
-                split2(pf[2], pf[3], pa[2], pa[3]);
-                uint32_t vw[4][D / 32];   // [token 4t + r][words of 4 d]
+                    for (int j = 0; j < 4; ++j) p[j] = ex2(y[b][j] - sub);
+                    l = fmaf(p[0] + p[1] + (p[2] + p[3]), un[b], l);
+                    // a token that the row does not see is zero even where the block's scale is NaN
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const uint8_t* vr = st + kKvBlock * D;
-                    if (D == 128) {
-                        const uint4 w = *reinterpret_cast<const uint4*>(vr + v_off<D>(4 * t + r, g));
-                        vw[r][0] = w.x ^ 0x80808080u, vw[r][1] = w.y ^ 0x80808080u;
-                        vw[r][D / 32 - 2] = w.z ^ 0x80808080u, vw[r][D / 32 - 1] = w.w ^ 0x80808080u;
-                    } else {
-                        const uint2 w = *reinterpret_cast<const uint2*>(vr + v_off<D>(4 * t + r, g >> 1) + 8 * (g & 1));
-                        vw[r][0] = w.x ^ 0x80808080u, vw[r][1] = w.y ^ 0x80808080u;
-                    }
+                    for (int j = 0; j < 4; ++j) p[j] = masked && y[b][j] == -INFINITY ? 0.0f : p[j] * f[b];
+                    split2(p[0], p[1], pa[b][0], pa[b][1]);
+                    split2(p[2], p[3], pa[b][2], pa[b][3]);
                 }
 #pragma unroll
-                for (int w = 0; w < D / 32; ++w) {
-                    const uint32_t a0 = __byte_perm(vw[0][w], vw[1][w], 0x5140), a1 = __byte_perm(vw[0][w], vw[1][w], 0x7362);
-                    const uint32_t b0 = __byte_perm(vw[2][w], vw[3][w], 0x5140), b1 = __byte_perm(vw[2][w], vw[3][w], 0x7362);
-                    mma16816(o[4 * w], pa, codes2<0x4140>(a0), codes2<0x4140>(b0));
-                    mma16816(o[4 * w + 1], pa, codes2<0x4342>(a0), codes2<0x4342>(b0));
-                    mma16816(o[4 * w + 2], pa, codes2<0x4140>(a1), codes2<0x4140>(b1));
-                    mma16816(o[4 * w + 3], pa, codes2<0x4342>(a1), codes2<0x4342>(b1));
+                for (int b = 0; b < 2; ++b) {
+                    uint32_t vw[4][D / 32];   // [token 4t + r][words of 4 d]
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const uint8_t* vr = st + b * kBlk + kKvBlock * D;
+                        if (D == 128) {
+                            const uint4 w = *reinterpret_cast<const uint4*>(vr + v_off<D>(4 * t + r, g));
+                            vw[r][0] = w.x ^ 0x80808080u, vw[r][1] = w.y ^ 0x80808080u;
+                            vw[r][D / 32 - 2] = w.z ^ 0x80808080u, vw[r][D / 32 - 1] = w.w ^ 0x80808080u;
+                        } else {
+                            const uint2 w = *reinterpret_cast<const uint2*>(vr + v_off<D>(4 * t + r, g >> 1) + 8 * (g & 1));
+                            vw[r][0] = w.x ^ 0x80808080u, vw[r][1] = w.y ^ 0x80808080u;
+                        }
+                    }
+#pragma unroll
+                    for (int w = 0; w < D / 32; ++w) {
+                        const uint32_t a0 = __byte_perm(vw[0][w], vw[1][w], 0x5140), a1 = __byte_perm(vw[0][w], vw[1][w], 0x7362);
+                        const uint32_t b0 = __byte_perm(vw[2][w], vw[3][w], 0x5140), b1 = __byte_perm(vw[2][w], vw[3][w], 0x7362);
+                        mma16816(o[4 * w], pa[b], codes2<0x4140>(a0), codes2<0x4140>(b0));
+                        mma16816(o[4 * w + 1], pa[b], codes2<0x4342>(a0), codes2<0x4342>(b0));
+                        mma16816(o[4 * w + 2], pa[b], codes2<0x4140>(a1), codes2<0x4140>(b1));
+                        mma16816(o[4 * w + 3], pa[b], codes2<0x4342>(a1), codes2<0x4342>(b1));
+                    }
                 }
             }
         }
@@ -408,9 +461,11 @@ __global__ void __launch_bounds__(kvd::kThreads, kvd::kCtasPerSm)
         l += __shfl_xor_sync(0xffffffffu, l, 2);
 
         // Join the warps. Row g's values 2 D/8 t .. are in this thread: tile i
-        // has columns 2t and 2t + 1, which stand for d = (D/8)(2t) + i and (D/8)(2t + 1) + i.
-        float* join = reinterpret_cast<float*>(ring_p);   // kRows x D, in this warp's own ring
+        // has columns 2t and 2t + 1, which stand for d = (D/8)(2t) + i and
+        // (D/8)(2t + 1) + i. (The next part's first loads started before this,
+        // with the registers that takes: 5 % slower.)
         __syncwarp();
+        float* join = reinterpret_cast<float*>(ring_p);   // kRows x D
 #pragma unroll
         for (int i = 0; i < kTiles; i += 4) {
             float4 lo4, hi4;
@@ -430,10 +485,9 @@ __global__ void __launch_bounds__(kvd::kThreads, kvd::kCtasPerSm)
             s_l[warp][g] = l;
         }
         __syncthreads();
-        const bool whole = b_at == 0 && count == blocks;
-        const int cta = blockIdx.x;
-        float* slot = slots + (long long)(2 * cta + (b_at == 0 ? 1 : 0)) * slot_floats<D>();
-        for (int i = tid; i < rows * (D / 4); i += kThreads) {
+        const bool whole = s_part.count == s_part.blocks;
+        float* slot = slots + (long long)(2 * cta + (s_part.b_at == 0 ? 1 : 0)) * slot_floats<D>();
+        for (int i = tid; i < s_part.rows * (D / 4); i += kThreads) {
             const int r = i / (D / 4), q4 = i % (D / 4);
             float top = s_m[0][r];
 #pragma unroll
@@ -445,8 +499,8 @@ __global__ void __launch_bounds__(kvd::kThreads, kvd::kCtasPerSm)
             for (int w = 0; w < kWarps; ++w) {
                 const float mw = s_m[w][r];
                 const float k = mw == -INFINITY ? 0.0f : ex2(mw - top);
-                const float4 v = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(smem + w * kStages * kStage) +
-                                                                 r * D + 4 * (q4 ^ tq));
+                const float4 v = *reinterpret_cast<const float4*>(
+                    reinterpret_cast<const float*>(smem + w * kRing) + r * D + 4 * (q4 ^ tq));
                 const float lw = s_l[w][r];
                 // a warp without a visible token has zeros, or NaN where a NaN scale met nothing else
                 sum.x = fmaf(v.x, k, sum.x), sum.y = fmaf(v.y, k, sum.y);
@@ -455,8 +509,8 @@ __global__ void __launch_bounds__(kvd::kThreads, kvd::kCtasPerSm)
             }
             if (whole) {
                 const float inv = total == 0.0f ? 0.0f : __fdiv_rn(1.0f, total);
-                const int ti = r / group, hh = head * group + r - ti * group;
-                const long long row = sq.row0 + ti;
+                const int ti = r / group, hh = s_part.head * group + r - ti * group;
+                const long long row = s_part.row0 + ti;
                 const float out[4] = {sum.x * inv, sum.y * inv, sum.z * inv, sum.w * inv};
                 kv8_store<T, 4>(static_cast<T*>(a.out.data) + row * a.out.row_stride + hh * a.out.head_stride + 4 * q4, out);
                 if (a.lse != nullptr && q4 == 0)
@@ -470,21 +524,25 @@ __global__ void __launch_bounds__(kvd::kThreads, kvd::kCtasPerSm)
                 }
             }
         }
-        if (tid == 0 && b_at == 0) {
+        if (tid == 0 && s_part.b_at == 0) {
             // the CTA that holds the item's last block
-            const long long last = item_x + blocks - 1;
-            int to = (int)(last * ctas / all);
-            while (all * (to + 1) / ctas <= last) ++to;
-            while (all * to / ctas > last) --to;
-            plan[(long long)s * c.heads + head] = {cta, to};
+            const int last = s_part.item_x + kStart + s_part.blocks - 1, long_ones = more * (each + 1);
+            const int to = last < long_ones ? last / (each + 1) : more + (last - long_ones) / each;
+            plan[(long long)s_part.seq * c.heads + s_part.head] = {cta, to};
         }
+        s = s_part.seq;
+        x = s_part.x;
+        x_seq = s_part.x_seq;
         __syncthreads();
     }
 }
 
 // Joins the parts of the items that were cut, and writes the rows of those that
-// see no block. One CTA per (item, query row); each warp sums every eighth part.
-constexpr int kJoinWarps = 8;
+// see no block. One CTA per (item, query row). The parts' maxima and l are read
+// at once, a thread each; then the warps sum the parts' rows by turns, eight
+// loads at a time. CTAs of kJoinWarps warps where there are few of them (an
+// item may then have hundreds of parts), else of a quarter of that.
+constexpr int kJoinWarps = 32;
 
 template <int DT, int D>
 __global__ void __launch_bounds__(kJoinWarps * 32)
@@ -493,9 +551,10 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
     using T = typename Kv8T<DT>::type;
     constexpr int VPL = D / 32;
     __shared__ float s_o[kJoinWarps][D];
-    __shared__ float s_m[kJoinWarps], s_l[kJoinWarps];
+    __shared__ float s_k[kMaxCtas], s_pl[kMaxCtas];   // each part's factor, and its l
+    __shared__ float s_red[2][kJoinWarps];
     const Kv8View& c = a.c;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, warps = blockDim.x >> 5;
     const int s = blockIdx.x / c.heads, head = blockIdx.x - s * c.heads;
     const int group = a.q_heads / c.heads, r = blockIdx.y;
     const Kv8Seq sq = kv8_seq(c, s);
@@ -507,42 +566,62 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
     if (sp.lo == sp.hi) {
         const float zero[VPL] = {};
         if (warp == 0) kv8_store<T, VPL>(out, zero);
-        if (a.lse != nullptr && threadIdx.x == 0) a.lse[row * a.q_heads + hh] = -INFINITY;
+        if (a.lse != nullptr && tid == 0) a.lse[row * a.q_heads + hh] = -INFINITY;
         return;
     }
     pdl_wait();   // the parts and the plan are written by the launch before
     const Kv8Plan p = plan[blockIdx.x];
-    if (p.first >= p.last) return;
-    float m = -INFINITY, l = 0.0f, o[VPL] = {};
-    for (int i = p.first + warp; i <= p.last; i += kJoinWarps) {
-        const float* slot = slots + (long long)(2 * i + (i == p.first ? 1 : 0)) * slot_floats<D>();
-        const float pm = slot[kRows * D + r], pl = slot[kRows * (D + 1) + r];
-        float v[VPL];
-        kv8_load<float, VPL>(slot + r * D + VPL * lane, v);
-        const float nm = fmaxf(m, pm);
-        const float k0 = m == -INFINITY ? 0.0f : ex2(m - nm), k1 = pm == -INFINITY ? 0.0f : ex2(pm - nm);
+    const int parts = p.last - p.first + 1;
+    if (parts <= 1) return;
+    // part i: slot 2 (first + i), the first part's 2 first + 1
+    const float* first = slots + (long long)2 * p.first * slot_floats<D>();
+    auto at = [&](int i) { return first + (long long)(2 * i + (i == 0)) * slot_floats<D>(); };
+    constexpr int kBatch = 8;
+    float v[kBatch][VPL];
+    auto fetch = [&](int i0) {   // on its way while the factors are made
 #pragma unroll
-        for (int j = 0; j < VPL; ++j) o[j] = fmaf(v[j], k1, o[j] * k0);
-        l = fmaf(pl, k1, l * k0);
-        m = nm;
+        for (int b = 0; b < kBatch; ++b)
+            kv8_load<float, VPL>(at(min(i0 + b * warps, parts - 1)) + r * D + VPL * lane, v[b]);
+    };
+    fetch(warp);
+    float top = -INFINITY;
+    for (int i = tid; i < parts; i += blockDim.x) {
+        s_k[i] = at(i)[kRows * D + r];
+        s_pl[i] = at(i)[kRows * (D + 1) + r];
+        top = fmaxf(top, s_k[i]);
+    }
+    top = warp_max(top);
+    if (lane == 0) s_red[0][warp] = top;
+    __syncthreads();
+    top = s_red[0][0];
+    for (int w = 1; w < warps; ++w) top = fmaxf(top, s_red[0][w]);
+    float l = 0.0f;
+    for (int i = tid; i < parts; i += blockDim.x) {
+        // a part without a visible token has zeros, or NaN where a NaN scale met nothing else
+        s_k[i] = s_k[i] == -INFINITY ? 0.0f : ex2(s_k[i] - top);
+        l = fmaf(s_pl[i], s_k[i], l);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    if (lane == 0) s_red[1][warp] = l;
+    __syncthreads();
+    float o[VPL] = {};
+    for (int i0 = warp; i0 < parts; i0 += kBatch * warps) {
+        if (i0 != warp) fetch(i0);
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b)
+            if (i0 + b * warps < parts)
+#pragma unroll
+                for (int j = 0; j < VPL; ++j) o[j] = fmaf(v[b][j], s_k[i0 + b * warps], o[j]);
     }
     kv8_store<float, VPL>(&s_o[warp][VPL * lane], o);
-    if (lane == 0) {
-        s_m[warp] = m;
-        s_l[warp] = l;
-    }
     __syncthreads();
     if (warp != 0) return;
-    float top = s_m[0];
-#pragma unroll
-    for (int w = 1; w < kJoinWarps; ++w) top = fmaxf(top, s_m[w]);
     float total = 0.0f, sum[VPL] = {};
+    for (int w = 0; w < warps; ++w) {
+        total += s_red[1][w];
 #pragma unroll
-    for (int w = 0; w < kJoinWarps; ++w) {
-        const float k = s_m[w] == -INFINITY ? 0.0f : ex2(s_m[w] - top);
-        total = fmaf(s_l[w], k, total);
-#pragma unroll
-        for (int j = 0; j < VPL; ++j) sum[j] = fmaf(s_o[w][VPL * lane + j], k, sum[j]);
+        for (int j = 0; j < VPL; ++j) sum[j] += s_o[w][VPL * lane + j];
     }
     const float inv = total == 0.0f ? 0.0f : __fdiv_rn(1.0f, total);
 #pragma unroll

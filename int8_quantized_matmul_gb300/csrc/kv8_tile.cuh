@@ -823,7 +823,7 @@ __global__ void __launch_bounds__(kvt::kThreads, 1)
             // Lane i < 8: block i of a tile. The table entries are read two tiles
             // before the pointers are due, the scales when they are.
             const int* table = c.table + (long long)s * c.width;
-            constexpr int kNoBlock = -1 << 31;   // past the last token: no page, and no bad one
+            constexpr int kNoBlock = -0x7fffffff - 1;   // past the last token: no page, and no bad one
             auto fetch_page = [&](int j) {
                 const long long tok = (long long)(from + j) * kTileKv + lane * kKvBlock;
                 return lane < kBlocks && j < steps && tok < sq.len ? table[tok >> c.page_shift] : kNoBlock;

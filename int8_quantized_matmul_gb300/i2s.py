@@ -703,13 +703,18 @@ class _Kv8Call:
     current device. Its tensors are kept alive, not copied."""
 
     def _bind(self, name, device, *args):
-        self._name, self._fn, self._args, self._index = name, getattr(_L, name), args, device.index
-        self._cuda = _torch().cuda
+        torch = _torch()
+        self._name, self._fn, self._index = name, getattr(_L, name), device.index
+        # structures as references made once, the stream as the number torch keeps
+        self._args = tuple(ctypes.byref(x) if isinstance(x, ctypes.Structure) else x for x in args)
+        self._hold = args
+        self._device, self._stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
 
     def __call__(self):
-        if self._cuda.current_device() != self._index:
-            raise ValueError(f"{self._name}: its tensors are on cuda:{self._index}, not on the current device")
-        rc = self._fn(*self._args, self._cuda.current_stream().cuda_stream)
+        index = self._index
+        if self._device() != index:
+            raise ValueError(f"{self._name}: its tensors are on cuda:{index}, not on the current device")
+        rc = self._fn(*self._args, self._stream(index))
         if rc != 0:
             raise I2SError(self._name, rc)
 

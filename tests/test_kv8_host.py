@@ -78,6 +78,13 @@ def test_cache_and_batch_refusals(i2s, name):
         assert getattr(c, name)() == c.E[want], (part, field, value)
 
 
+@pytest.mark.parametrize("name", ["write", "read", "attend"])
+def test_blocks_are_counted_in_32_bits(i2s, name):
+    c = Call(i2s)
+    c.batch.seqs, c.batch.table_width = 1000, (1 << 35) // (1000 * 2 * 64) + 1
+    assert getattr(c, name)() == c.E["I2S_E_BAD_SHAPE"]
+
+
 @pytest.mark.parametrize("name,inputs,outputs", [("write", "kv", ""), ("read", "", "kv"), ("attend", ["q"], ["out"])])
 def test_row_tensor_refusals(i2s, name, inputs, outputs):
     for t in list(inputs) + list(outputs):
