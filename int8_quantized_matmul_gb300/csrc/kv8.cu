@@ -1,6 +1,7 @@
 // The 8-bit KV cache (include/i2s.h, "8-bit KV cache"): the C ABI of the kv8_*
 // calls, the quantizing write, the read, and the norm-and-rotation pass.
 
+#include <algorithm>
 #include <cmath>
 #include <cstring>
 
@@ -13,84 +14,122 @@ namespace i2s {
 
 namespace {
 
+// Where N consecutive rows of a batch lie. N is 16 for batches of few rows per
+// sequence, whose units are many per row; for long ones 64, since what finding
+// them takes (three loads that wait for each other) is then spread over more.
+template <int N>
+struct RowPlaces {
+    int seq[N];     // -1: no row, or a position before the first token
+    int pos[N];
+    int left[N];    // rows of the sequence from this one on
+    int start[32];  // the row starts of the sequence of the first row and the 31 after it
+};
+
+// Filled by a CTA of THREADS threads, all of which take part. The sequence of
+// row0 is found by counting the row starts up to it, a load per thread for all
+// at once (a search would wait for one after the other); the others from there.
+template <int THREADS, int N>
+__device__ __forceinline__ void find_rows(const Kv8View& c, long long row0, RowPlaces<N>& p) {
+    const int tid = threadIdx.x;
+    int upto = 0;
+    for (int i0 = 0; i0 <= c.seqs; i0 += THREADS)
+        upto += __syncthreads_count(i0 + tid <= c.seqs && c.row_start[min(i0 + tid, c.seqs)] <= row0);
+    const int s0 = max(upto - 1, 0);
+    if (tid < 32) p.start[tid] = s0 + tid <= c.seqs ? c.row_start[s0 + tid] : 0x7fffffff;
+    __syncthreads();
+    if (tid < N) {
+        const long long row = row0 + tid;
+        int n = 0;
+        while (n < 31 && p.start[n + 1] <= row) ++n;
+        const int s = n == 31 ? kv8_seq_of_row(c, row) : s0 + n;
+        p.seq[tid] = -1;
+        if (upto > 0 && s >= 0 && s < c.seqs && row < c.rows) {
+            const Kv8Seq q = kv8_seq(c, s);
+            const long long i = row - q.row0, pos = (long long)q.len - q.n + i;
+            if (i >= 0 && i < q.n) {
+                if (pos < 0) atomicOr(c.status, kKvBadLength);
+                p.seq[tid] = pos < 0 ? -1 : s;
+                p.pos[tid] = (int)pos;
+                p.left[tid] = (int)(q.n - i);
+            }
+        }
+    }
+    __syncthreads();
+}
+
 // ---------------------------------------------------------------------------
 // Write. A unit is one (block, head, K or V) that the batch touches, one warp
 // each: it has every new value of the block and the block's old codes, so the
 // scale needs no exchange between warps and no atomics. Lane l holds values
 // VPL*l .. of each of the block's 16 tokens in registers, so the input is read
-// once: absolute maximum, then the codes.
+// once: absolute maximum, then the codes. Bytes bound it, and where there are
+// few the three loads that wait for each other (row, page, old scale).
 //
 // A unit belongs to the first row that the batch has in the block (its
-// leader); a CTA takes 16 consecutive rows, finds their leaders with one
-// search per row, and its warps share leaders x heads x {K, V} with those of
-// the same rows in the grid's second dimension.
+// leader); a CTA takes N consecutive rows, and its warps share leaders x heads
+// x {K, V} with those of the same rows in the grid's second dimension.
 // ---------------------------------------------------------------------------
-constexpr int kWriteWarps = 8;
+constexpr int kWriteWarps = 4;
 
-template <int DT, int D>
+template <int DT, int D, int N>
 __global__ void __launch_bounds__(kWriteWarps * 32) k_kv8_write(const __grid_constant__ Kv8View c, Kv8Rows k, Kv8Rows v) {
     using T = typename Kv8T<DT>::type;
     constexpr int VPL = D / 32;
-    __shared__ int s_seq[kKvBlock], s_pos[kKvBlock], s_count[kKvBlock];
-    __shared__ unsigned s_leaders;
+    __shared__ RowPlaces<N> s_rows;
+    __shared__ int s_lead[N], s_leaders;
+    pdl_wait();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const long long row0 = (long long)blockIdx.x * kKvBlock;
-    if (warp == 0) {
-        const long long row = row0 + lane;
-        bool leads = false;
-        if (lane < kKvBlock && row < c.rows) {
-            const int s = kv8_seq_of_row(c, row);
-            if (s >= 0) {
-                const Kv8Seq q = kv8_seq(c, s);
-                const long long i = row - q.row0;
-                const long long pos = (long long)q.len - q.n + i;
-                if (i >= 0 && i < q.n) {
-                    if (pos < 0) atomicOr(c.status, kKvBadLength);
-                    leads = pos >= 0 && (pos % kKvBlock == 0 || i == 0 || pos == 0);
-                    s_seq[lane] = s;
-                    s_pos[lane] = (int)pos;
-                    s_count[lane] = (int)min((long long)(kKvBlock - pos % kKvBlock), q.n - i);
-                }
+    const long long row0 = (long long)blockIdx.x * N;
+    find_rows<kWriteWarps * 32>(c, row0, s_rows);
+    if (warp == 0) {   // the leaders' rows, in order
+        int n = 0;
+#pragma unroll
+        for (int i0 = 0; i0 < N; i0 += 32) {
+            const int r = i0 + lane;
+            bool leads = false;
+            if (r < N && s_rows.seq[r] >= 0) {
+                const int s = s_rows.seq[r];
+                // the row before is not in its block: another sequence's, of a
+                // negative position, or (a CTA's first row) by where s starts
+                leads = s_rows.pos[r] % kKvBlock == 0 || (r > 0 ? s_rows.seq[r - 1] != s : c.row_start[s] >= row0);
             }
+            const unsigned m = __ballot_sync(0xffffffffu, leads);
+            if (leads) s_lead[n + __popc(m & ((1u << lane) - 1))] = r;
+            n += __popc(m);
         }
-        const unsigned m = __ballot_sync(0xffffffffu, leads);
-        if (lane == 0) s_leaders = m;
+        if (lane == 0) s_leaders = n;
     }
     __syncthreads();
-    const unsigned leaders = s_leaders;
     const int per = 2 * c.heads;   // units of a leader
-    const int units = __popc(leaders) * per;
+    const int units = s_leaders * per;
     for (int u = blockIdx.y * kWriteWarps + warp; u < units; u += gridDim.y * kWriteWarps) {
-        const int which = u & 1, head = (u % per) >> 1;
-        unsigned m = leaders;
-        for (int i = u / per; i > 0; --i) m &= m - 1;
-        const int r = __ffs(m) - 1;
-        const int pos = s_pos[r], first = pos % kKvBlock, count = s_count[r];
-        uint8_t* slab = kv8_slab(c, s_seq[r], pos, head);
-        if (slab == nullptr) continue;
+        const int which = u & 1, head = (u % per) >> 1, r = s_lead[u / per];
+        const int pos = s_rows.pos[r], first = pos % kKvBlock, count = min(kKvBlock - first, s_rows.left[r]);
         const Kv8Rows& x = which ? v : k;
         const T* src = static_cast<const T*>(x.data) + (row0 + r) * x.row_stride + head * x.head_stride + VPL * lane;
-        const int in_page = (pos - first) & ((1 << c.page_shift) - 1);   // the block's first token in its page
-        int8_t* codes = reinterpret_cast<int8_t*>(slab + kv8_code_off(c, which, in_page)) + VPL * lane;
-        float* scale_at = reinterpret_cast<float*>(slab + kv8_scale_off(c, which, in_page));
-
-        float val[kKvBlock][VPL];
-        unsigned top = 0;   // bits of |x| order as the values do, NaN above infinity
+        Kv8Vec<T, VPL> val[kKvBlock];   // on their way while the page is looked up
 #pragma unroll
         for (int i = 0; i < kKvBlock; ++i) {
             if (i < count) {
-                kv8_load<T, VPL>(src + i * x.row_stride, val[i]);
+                val[i] = *reinterpret_cast<const Kv8Vec<T, VPL>*>(src + i * x.row_stride);
             } else {
 #pragma unroll
-                for (int j = 0; j < VPL; ++j) val[i][j] = 0.0f;
+                for (int j = 0; j < VPL; ++j) val[i].v[j] = T(0.0f);
             }
         }
+        uint8_t* slab = kv8_slab(c, s_rows.seq[r], pos, head);
+        if (slab == nullptr) continue;
+        const int in_page = (pos - first) & ((1 << c.page_shift) - 1);   // the block's first token in its page
+        int8_t* codes = reinterpret_cast<int8_t*>(slab + kv8_code_off(c, which, in_page)) + VPL * lane;
+        float* scale_at = reinterpret_cast<float*>(slab + kv8_scale_off(c, which, in_page));
+        const float old = first ? *scale_at : 0.0f;
+
+        unsigned top = 0;   // bits of |x| order as the values do, NaN above infinity
 #pragma unroll
         for (int i = 0; i < kKvBlock; ++i)
 #pragma unroll
-            for (int j = 0; j < VPL; ++j) top = max(top, __float_as_uint(val[i][j]) & 0x7fffffffu);
+            for (int j = 0; j < VPL; ++j) top = max(top, __float_as_uint(kv8_f(val[i].v[j])) & 0x7fffffffu);
         top = __reduce_max_sync(0xffffffffu, top);
-        const float old = first ? *scale_at : 0.0f;
         float scale, inv;
         if (top >= 0x7f800000u || old != old) {
             scale = __uint_as_float(0x7fc00000u);
@@ -105,11 +144,12 @@ __global__ void __launch_bounds__(kWriteWarps * 32) k_kv8_write(const __grid_con
             if (i < count) {
                 Kv8Vec<int8_t, VPL> w;
 #pragma unroll
-                for (int j = 0; j < VPL; ++j) w.v[j] = inv == 0.0f ? 0 : (int8_t)quantize_one(val[i][j], inv);
+                for (int j = 0; j < VPL; ++j) w.v[j] = inv == 0.0f ? 0 : (int8_t)quantize_one(kv8_f(val[i].v[j]), inv);
                 *reinterpret_cast<Kv8Vec<int8_t, VPL>*>(codes + (first + i) * D) = w;
             }
         }
         if (first && inv != 0.0f && scale != old) {   // the older tokens' codes follow the grown scale
+#pragma unroll 4
             for (int i = 0; i < first; ++i) {
                 Kv8Vec<int8_t, VPL>* at = reinterpret_cast<Kv8Vec<int8_t, VPL>*>(codes + i * D);
                 Kv8Vec<int8_t, VPL> w = *at;
@@ -124,66 +164,71 @@ __global__ void __launch_bounds__(kWriteWarps * 32) k_kv8_write(const __grid_con
 }
 
 // ---------------------------------------------------------------------------
-// Read. A CTA takes 16 rows; one thread per row finds its page. Each thread
-// turns 4 codes at a time into values.
+// Read. A CTA takes N rows. A lane turns as many codes into values as 16 bytes
+// hold, a warp eight lines (a row's D codes of one head, K or V) at once.
 // ---------------------------------------------------------------------------
-constexpr int kReadThreads = 256;
+constexpr int kReadWarps = 8;
+constexpr int kReadBatch = 4;
 
-template <int DT, int D>
-__global__ void __launch_bounds__(kReadThreads) k_kv8_read(const __grid_constant__ Kv8View c, Kv8Rows k, Kv8Rows v) {
+template <int DT, int D, int N>
+__global__ void __launch_bounds__(kReadWarps * 32) k_kv8_read(const __grid_constant__ Kv8View c, Kv8Rows k, Kv8Rows v) {
     using T = typename Kv8T<DT>::type;
-    __shared__ const uint8_t* s_page[kKvBlock];   // the page's first slab; null: nothing to read
-    __shared__ int s_tok[kKvBlock];
-    const long long row0 = (long long)blockIdx.x * kKvBlock;
-    if (threadIdx.x < kKvBlock) {
-        const long long row = row0 + threadIdx.x;
-        const uint8_t* page = nullptr;
-        if (row < c.rows) {
-            const int s = kv8_seq_of_row(c, row);
-            if (s >= 0) {
-                const Kv8Seq q = kv8_seq(c, s);
-                const long long i = row - q.row0;
-                const long long pos = (long long)q.len - q.n + i;
-                if (i >= 0 && i < q.n && pos < 0) atomicOr(c.status, kKvBadLength);
-                if (i >= 0 && i < q.n && pos >= 0) {
-                    page = kv8_slab(c, s, (int)pos, 0);
-                    s_tok[threadIdx.x] = (int)pos & ((1 << c.page_shift) - 1);
-                }
-            }
-        }
-        s_page[threadIdx.x] = page;
+    constexpr int VPL = 16 / sizeof(T), LPL = D / VPL, LPW = 32 / LPL;   // lanes of a line, lines of a warp's load
+    __shared__ RowPlaces<N> s_rows;
+    __shared__ const uint8_t* s_page[N];   // the page's first slab; null: nothing to read
+    pdl_wait();
+    const long long row0 = (long long)blockIdx.x * N;
+    find_rows<kReadWarps * 32>(c, row0, s_rows);
+    if (threadIdx.x < N) {
+        const int r = threadIdx.x, s = s_rows.seq[r];
+        s_page[r] = s < 0 ? nullptr : kv8_slab(c, s, s_rows.pos[r], 0);
     }
     __syncthreads();
-    constexpr int Q = D / 4;   // quads of codes per (row, head, K or V)
-    const int per = 2 * c.heads * Q;
-    for (int u = blockIdx.y * kReadThreads + threadIdx.x; u < kKvBlock * per; u += gridDim.y * kReadThreads) {
-        const int r = u / per, rest = u - r * per;
-        const uint8_t* page = s_page[r];
-        if (page == nullptr) continue;
-        const int q4 = rest % Q, which = (rest / Q) & 1, head = rest / (2 * Q);
-        const uint8_t* slab = page + (long long)head * c.slab;
-        const int t = s_tok[r];
-        const float scale = *reinterpret_cast<const float*>(slab + kv8_scale_off(c, which, t));
-        const Kv8Vec<int8_t, 4> w =
-            *reinterpret_cast<const Kv8Vec<int8_t, 4>*>(slab + kv8_code_off(c, which, t) + 4 * q4);
-        float x[4];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane % LPL;
+    const int per = 2 * c.heads, lines = N * per, mask = (1 << c.page_shift) - 1;
+    const int step = kReadBatch * LPW;
+    for (int l0 = (blockIdx.y * kReadWarps + warp) * step; l0 < lines; l0 += gridDim.y * kReadWarps * step) {
+        Kv8Vec<int8_t, VPL> w[kReadBatch];
+        float scale[kReadBatch];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) x[j] = __fmul_rn(i8_to_float(w.v[j]), scale);
-        const Kv8Rows& o = which ? v : k;
-        kv8_store<T, 4>(static_cast<T*>(o.data) + (row0 + r) * o.row_stride + head * o.head_stride + 4 * q4, x);
+        for (int b = 0; b < kReadBatch; ++b) {
+            const int l = l0 + b * LPW + lane / LPL, r = l / per, h = l - r * per;
+            const uint8_t* page = l < lines ? s_page[r] : nullptr;
+            if (page != nullptr) {
+                const uint8_t* slab = page + (long long)(h >> 1) * c.slab;
+                const int t = s_rows.pos[r] & mask;
+                scale[b] = *reinterpret_cast<const float*>(slab + kv8_scale_off(c, h & 1, t));
+                w[b] = *reinterpret_cast<const Kv8Vec<int8_t, VPL>*>(slab + kv8_code_off(c, h & 1, t) + VPL * sub);
+            }
+        }
+#pragma unroll
+        for (int b = 0; b < kReadBatch; ++b) {
+            const int l = l0 + b * LPW + lane / LPL, r = l / per, h = l - r * per;
+            if (l >= lines || s_page[r] == nullptr) continue;
+            float x[VPL];
+#pragma unroll
+            for (int j = 0; j < VPL; ++j) x[j] = __fmul_rn(i8_to_float(w[b].v[j]), scale[b]);
+            const Kv8Rows& o = h & 1 ? v : k;
+            kv8_store<T, VPL>(static_cast<T*>(o.data) + (row0 + r) * o.row_stride + (h >> 1) * o.head_stride + VPL * sub, x);
+        }
     }
 }
 
 // ---------------------------------------------------------------------------
-// Norm and rotation. A CTA takes ROWS rows: its threads first compute the
-// cosines and sines of each row's angles once, shared by all the heads; then
-// one warp per (row, head) squares, normalises and turns, lane l holding VPL
-// consecutive values. position * turns (mod 2^64) is the angle in 2^-64 turns;
-// its upper 32 bits, signed, are the turn in [-1/2, 1/2), so sincospi sees at
-// most pi whatever the position.
+// Norm and rotation: each value is read once and written once, so bytes bound
+// it. A warp has one row: its lanes compute the cosines and sines of the row's
+// angles once, for all heads. position * turns (mod 2^64) is the angle in 2^-64
+// turns; its upper 32 bits, signed, are the turn in [-1/2, 1/2), so sincospi
+// sees at most pi whatever the position.
+//
+// A lane has VPL consecutive values (16 bytes) of a head, LPH lanes have a head,
+// a warp kRopeBatch loads at once, which is what keeps enough bytes on their
+// way. The partner of value d in a pair (d, d + rot/2) is in another lane, at a
+// whole number of lanes if rot/2 is a multiple of VPL; 16-bit rows with another
+// rot take 8 bytes per lane.
 // ---------------------------------------------------------------------------
-constexpr int kRopeWarps = 8;
-constexpr int kRopeRows = 4;
+constexpr int kRopeWarps = 4;
+constexpr int kRopeBatch = 4;
 
 struct Kv8RopeArgs {
     Kv8Rows q, q_out, k, k_out;
@@ -193,78 +238,106 @@ struct Kv8RopeArgs {
     const unsigned long long* turns;
     long long rows;
     int q_heads, k_heads, rot;
+    int heads_per_warp;
     float eps;
     bool next;   // pairs (2i, 2i + 1)
 };
 
-template <int DT, int D>
+template <int DT, int D, int VPL>
 __global__ void __launch_bounds__(kRopeWarps * 32) k_kv8_norm_rope(const __grid_constant__ Kv8RopeArgs a) {
     using T = typename Kv8T<DT>::type;
-    constexpr int VPL = D / 32;
-    __shared__ float2 s_cs[kRopeRows][D / 2];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const long long row0 = (long long)blockIdx.x * kRopeRows;
-    const int rows = (int)min((long long)kRopeRows, a.rows - row0);
-    const int half = a.rot >> 1;
-    for (int i = threadIdx.x; i < rows * half; i += kRopeWarps * 32) {
-        const int r = i / half, p = i - r * half;
-        const unsigned long long turn = (unsigned long long)(long long)a.positions[row0 + r] * a.turns[p];
-        const float x = __fmul_rn((float)(int)(turn >> 32), 0x1p-31f);   // twice the turn
-        float sn, cs;
-        sincospif(x, &sn, &cs);
-        s_cs[r][p] = make_float2(cs, sn);
-    }
-    __syncthreads();
-    const int heads = a.q_heads + a.k_heads;
-    for (int u = blockIdx.y * kRopeWarps + warp; u < rows * heads; u += gridDim.y * kRopeWarps) {
-        const int r = u / heads, h = u - r * heads;
-        const bool is_k = h >= a.q_heads;
-        const int head = is_k ? h - a.q_heads : h;
-        const Kv8Rows& in = is_k ? a.k : a.q;
-        const Kv8Rows& out = is_k ? a.k_out : a.q_out;
-        const float* gamma = is_k ? a.gamma_k : a.gamma_q;
-        float x[VPL];
-        kv8_load<T, VPL>(static_cast<const T*>(in.data) + (row0 + r) * in.row_stride + head * in.head_stride + VPL * lane, x);
-        if (gamma != nullptr) {
-            float ss = 0.0f;
+    constexpr int LPH = D / VPL, HPW = 32 / LPH;   // lanes of a head, heads of a warp's load
+    __shared__ float2 s_cs[kRopeWarps][D / 2];
+    pdl_wait();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane % LPH;
+    const long long row = (long long)blockIdx.x * kRopeWarps + warp;
+    if (row >= a.rows) return;
+    const int half = a.rot >> 1, d0 = VPL * sub;
+    const int h_end = min(a.q_heads + a.k_heads, (int)(blockIdx.y + 1) * a.heads_per_warp);
+    const bool turned = d0 < a.rot, low = d0 < half;
+    const int peer = (lane & ~(LPH - 1)) + (turned ? (low ? sub + half / VPL : sub - half / VPL) : sub);
+
+    // loads of the first heads, on their way while the angles are computed
+    Kv8Vec<T, VPL> raw[kRopeBatch];
+    auto fetch = [&](int h0) {
 #pragma unroll
-            for (int j = 0; j < VPL; ++j) ss = fmaf(x[j], x[j], ss);
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-            const float rs = __fdiv_rn(1.0f, __fsqrt_rn(ss * (1.0f / D) + a.eps));
-            float g[VPL];
-            kv8_load<float, VPL>(gamma + VPL * lane, g);
-#pragma unroll
-            for (int j = 0; j < VPL; ++j) x[j] = x[j] * rs * g[j];
+        for (int b = 0; b < kRopeBatch; ++b) {
+            const int h = min(h0 + b * HPW + lane / LPH, h_end - 1);
+            const bool is_k = h >= a.q_heads;
+            const Kv8Rows& in = is_k ? a.k : a.q;
+            raw[b] = *reinterpret_cast<const Kv8Vec<T, VPL>*>(static_cast<const T*>(in.data) + row * in.row_stride +
+                                                             (is_k ? h - a.q_heads : h) * in.head_stride + d0);
         }
-        const bool turned = VPL * lane < a.rot;
-        if (a.next) {
-            if (turned) {
+    };
+    const int h_lo = blockIdx.y * a.heads_per_warp;
+    fetch(h_lo);
+    if (half > 0) {
+        const unsigned long long pos = (unsigned long long)(long long)a.positions[row];
+        for (int p = lane; p < half; p += 32) {
+            const float x = __fmul_rn((float)(int)(pos * a.turns[p] >> 32), 0x1p-31f);   // twice the turn
+            float sn, cs;
+            sincospif(x, &sn, &cs);
+            s_cs[warp][p] = make_float2(cs, sn);
+        }
+        __syncwarp();
+    }
+    float2 t[VPL];   // of this lane's values; of its pairs where they are neighbours
 #pragma unroll
-                for (int j = 0; j < VPL; j += 2) {
-                    const float2 t = s_cs[r][(VPL * lane + j) >> 1];
-                    const float p = x[j], q = x[j + 1];
-                    x[j] = fmaf(p, t.x, -q * t.y);
-                    x[j + 1] = fmaf(q, t.x, p * t.y);
+    for (int j = 0; j < VPL; ++j) {
+        const int p = a.next ? (d0 + j) >> 1 : d0 + j - (low ? 0 : half);
+        t[j] = turned ? s_cs[warp][p] : make_float2(1.0f, 0.0f);
+    }
+    float gq[VPL], gk[VPL];
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) {
+        gq[j] = a.gamma_q != nullptr ? a.gamma_q[d0 + j] : 1.0f;
+        gk[j] = a.gamma_k != nullptr ? a.gamma_k[d0 + j] : 1.0f;
+    }
+    const bool norms = a.gamma_q != nullptr || a.gamma_k != nullptr;
+
+    for (int h0 = h_lo; h0 < h_end; h0 += kRopeBatch * HPW) {
+        if (h0 > h_lo) fetch(h0);
+#pragma unroll
+        for (int b = 0; b < kRopeBatch; ++b) {
+            const int h = h0 + b * HPW + lane / LPH;
+            const bool is_k = h >= a.q_heads;
+            float x[VPL];
+#pragma unroll
+            for (int j = 0; j < VPL; ++j) x[j] = kv8_f(raw[b].v[j]);
+            if (norms) {
+                float ss = 0.0f;
+#pragma unroll
+                for (int j = 0; j < VPL; ++j) ss = fmaf(x[j], x[j], ss);
+#pragma unroll
+                for (int o = LPH / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+                if (is_k ? a.gamma_k != nullptr : a.gamma_q != nullptr) {
+                    const float rs = __fdiv_rn(1.0f, __fsqrt_rn(ss * (1.0f / D) + a.eps));
+#pragma unroll
+                    for (int j = 0; j < VPL; ++j) x[j] = x[j] * rs * (is_k ? gk[j] : gq[j]);
                 }
             }
-        } else {
-            // the partner of value d is rot/2 further or nearer, in another lane
-            const bool low = VPL * lane < half;
-            const int step = half / VPL;
-            const int peer = turned ? (low ? lane + step : lane - step) : lane;
-            float y[VPL];
+            if (a.next) {
+                if (turned) {
 #pragma unroll
-            for (int j = 0; j < VPL; ++j) y[j] = __shfl_sync(0xffffffffu, x[j], peer);
-            if (turned) {
+                    for (int j = 0; j < VPL; j += 2) {
+                        const float p = x[j], q = x[j + 1];
+                        x[j] = fmaf(p, t[j].x, -q * t[j].y);
+                        x[j + 1] = fmaf(q, t[j].x, p * t[j].y);
+                    }
+                }
+            } else if (half > 0) {
 #pragma unroll
                 for (int j = 0; j < VPL; ++j) {
-                    const float2 t = s_cs[r][VPL * lane + j - (low ? 0 : half)];
-                    x[j] = fmaf(x[j], t.x, low ? -y[j] * t.y : y[j] * t.y);
+                    const float y = __shfl_sync(0xffffffffu, x[j], peer);
+                    if (turned) x[j] = fmaf(x[j], t[j].x, low ? -y * t[j].y : y * t[j].y);
                 }
             }
+            if (h < h_end) {
+                const Kv8Rows& out = is_k ? a.k_out : a.q_out;
+                kv8_store<T, VPL>(static_cast<T*>(out.data) + row * out.row_stride +
+                                      (is_k ? h - a.q_heads : h) * out.head_stride + d0, x);
+            }
         }
-        kv8_store<T, VPL>(static_cast<T*>(out.data) + (row0 + r) * out.row_stride + head * out.head_stride + VPL * lane, x);
     }
 }
 
@@ -364,6 +437,8 @@ Kv8Rows rows_of(const kv8_rows& t) { return {t.data, t.row_stride, t.head_stride
 
 int cuda_status(cudaError_t e) { return e == cudaSuccess ? I2S_OK : I2S_E_CUDA; }
 
+int clamp_grid(int64_t want) { return (int)(want < 1 ? 1 : want > 65535 ? 65535 : want); }
+
 // f<dtype, head_dim>() for the runtime values.
 template <template <int, int> class F, typename... A>
 void dispatch(int dt, int dim, A&&... args) {
@@ -378,26 +453,59 @@ void dispatch(int dt, int dim, A&&... args) {
     }
 }
 
+constexpr int kLongRows = 64;   // rows of a CTA for batches of at least 16 rows per sequence
+
 template <int DT, int D>
 struct GoWrite {
-    static void go(dim3 grid, cudaStream_t s, const Kv8View& c, const Kv8Rows& k, const Kv8Rows& v) {
-        k_kv8_write<DT, D><<<grid, kWriteWarps * 32, 0, s>>>(c, k, v);
+    template <int N>
+    static cudaError_t with(cudaStream_t s, const Kv8View& c, const Kv8Rows& k, const Kv8Rows& v) {
+        // Leaders expected among N rows: each row of a batch of single tokens,
+        // one in 16 of a long one. Single tokens' units get a warp each; of the
+        // long ones' a warp takes four.
+        const int leaders = N == kLongRows ? N / kKvBlock + 1 : std::min(N, N / c.max_rows + 1);
+        const int units = 2 * c.heads * leaders, each = N == kLongRows ? 4 : 1;
+        const dim3 grid((unsigned)((c.rows + N - 1) / N), clamp_grid((units + each * kWriteWarps - 1) / (each * kWriteWarps)));
+        return launch_pdl(k_kv8_write<DT, D, N>, grid, dim3(kWriteWarps * 32), 0, s, c, k, v);
+    }
+    static void go(cudaStream_t s, const Kv8View& c, const Kv8Rows& k, const Kv8Rows& v, cudaError_t& e) {
+        e = c.max_rows >= kKvBlock ? with<kLongRows>(s, c, k, v) : with<kKvBlock>(s, c, k, v);
     }
 };
 template <int DT, int D>
 struct GoRead {
-    static void go(dim3 grid, cudaStream_t s, const Kv8View& c, const Kv8Rows& k, const Kv8Rows& v) {
-        k_kv8_read<DT, D><<<grid, kReadThreads, 0, s>>>(c, k, v);
+    template <int N>
+    static cudaError_t with(cudaStream_t s, const Kv8View& c, const Kv8Rows& k, const Kv8Rows& v) {
+        // lines of a CTA's pass; of long batches a warp takes four passes
+        constexpr int lines = kReadWarps * kReadBatch * (32 / (D / (16 / (int)sizeof(typename Kv8T<DT>::type))));
+        const int each = N == kLongRows ? 4 : 1;
+        const dim3 grid((unsigned)((c.rows + N - 1) / N), clamp_grid((N * 2 * c.heads + each * lines - 1) / (each * lines)));
+        return launch_pdl(k_kv8_read<DT, D, N>, grid, dim3(kReadWarps * 32), 0, s, c, k, v);
+    }
+    static void go(cudaStream_t s, const Kv8View& c, const Kv8Rows& k, const Kv8Rows& v, cudaError_t& e) {
+        e = c.max_rows >= kKvBlock ? with<kLongRows>(s, c, k, v) : with<kKvBlock>(s, c, k, v);
     }
 };
 template <int DT, int D>
 struct GoRope {
-    static void go(dim3 grid, cudaStream_t s, const Kv8RopeArgs& a) {
-        k_kv8_norm_rope<DT, D><<<grid, kRopeWarps * 32, 0, s>>>(a);
+    template <int VPL>
+    static cudaError_t with(Kv8RopeArgs& a, cudaStream_t s) {
+        // Heads of a warp: all of a row's where there are rows enough to fill the
+        // GPU, one batch of loads where there are few.
+        const int heads = a.q_heads + a.k_heads, batch = kRopeBatch * (32 / (D / VPL));
+        const int64_t ctas = (a.rows + kRopeWarps - 1) / kRopeWarps;
+        int splits = 1;
+        while (splits * batch < heads && ctas * splits < 16 * 152) ++splits;
+        a.heads_per_warp = ((heads + splits - 1) / splits + batch - 1) / batch * batch;
+        const dim3 grid((unsigned)ctas, (unsigned)((heads + a.heads_per_warp - 1) / a.heads_per_warp));
+        return launch_pdl(k_kv8_norm_rope<DT, D, VPL>, grid, dim3(kRopeWarps * 32), 0, s, a);
+    }
+    static void go(Kv8RopeArgs& a, cudaStream_t s, cudaError_t& e) {
+        constexpr int kFull = DT == kKvF32 ? 4 : 8;
+        if (a.next || a.rot / 2 % kFull == 0) e = with<kFull>(a, s);
+        else e = with<4>(a, s);
     }
 };
 
-int clamp_grid(int64_t want) { return (int)(want < 1 ? 1 : want > 65535 ? 65535 : want); }
 
 }  // namespace
 }  // namespace i2s
@@ -423,13 +531,9 @@ int kv8_write(const kv8_cache* cache, const kv8_batch* batch, const kv8_rows* k,
         meets_batch(pool, *batch))
         return I2S_E_BAD_ARG;
     if ((r = check_current_device())) return r;
-    // Leaders expected among 16 rows: each row of a batch of single tokens, one
-    // or two of a long one.
-    const int leaders = c.max_rows >= kKvBlock ? 2 : min(kKvBlock, kKvBlock / c.max_rows + 1);
-    const dim3 grid((unsigned)((c.rows + kKvBlock - 1) / kKvBlock),
-                    clamp_grid((2 * c.heads * leaders + kWriteWarps - 1) / kWriteWarps));
-    dispatch<GoWrite>(k->dtype, c.dim, grid, stream, c, rows_of(*k), rows_of(*v));
-    return cuda_status(cudaGetLastError());
+    cudaError_t e = cudaSuccess;
+    dispatch<GoWrite>(k->dtype, c.dim, stream, c, rows_of(*k), rows_of(*v), e);
+    return cuda_status(e);
 }
 
 int kv8_read(const kv8_cache* cache, const kv8_batch* batch, const kv8_rows* k, const kv8_rows* v,
@@ -444,10 +548,9 @@ int kv8_read(const kv8_cache* cache, const kv8_batch* batch, const kv8_rows* k, 
     if (pool.meets(rk) || pool.meets(rv) || rk.meets(rv) || meets_batch(rk, *batch) || meets_batch(rv, *batch))
         return I2S_E_BAD_ARG;
     if ((r = check_current_device())) return r;
-    const int quads = kKvBlock * 2 * c.heads * (c.dim / 4);
-    const dim3 grid((unsigned)((c.rows + kKvBlock - 1) / kKvBlock), clamp_grid((quads + 4 * kReadThreads - 1) / (4 * kReadThreads)));
-    dispatch<GoRead>(k->dtype, c.dim, grid, stream, c, rows_of(*k), rows_of(*v));
-    return cuda_status(cudaGetLastError());
+    cudaError_t e = cudaSuccess;
+    dispatch<GoRead>(k->dtype, c.dim, stream, c, rows_of(*k), rows_of(*v), e);
+    return cuda_status(e);
 }
 
 int kv8_rope_turns_host(double base, int rot_dim, uint64_t* turns) {
@@ -510,10 +613,9 @@ int kv8_norm_rope(const kv8_rows* q, const kv8_rows* q_out, int q_heads, const f
     a.next = (flags & KV8_PAIRS_NEXT) != 0;
     int r = check_current_device();
     if (r) return r;
-    const int units = kRopeRows * (q_heads + k_heads);
-    const dim3 grid((unsigned)((rows + kRopeRows - 1) / kRopeRows), clamp_grid((units + 4 * kRopeWarps - 1) / (4 * kRopeWarps)));
-    dispatch<GoRope>(dt, head_dim, grid, stream, a);
-    return cuda_status(cudaGetLastError());
+    cudaError_t e = cudaSuccess;
+    dispatch<GoRope>(dt, head_dim, a, stream, e);
+    return cuda_status(e);
 }
 
 size_t kv8_attention_workspace(const kv8_cache* cache, const kv8_batch* batch, int q_heads) {
