@@ -71,6 +71,22 @@ __device__ __forceinline__ void find_rows(const Kv8View& c, long long row0, RowP
 // ---------------------------------------------------------------------------
 constexpr int kWriteWarps = 4;
 
+// The larger of the two, NaN if one is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+
+// round(x * inv), halfway cases away from zero, of a value no larger than the
+// scale's 127 (the product is below 127.0001, so nothing needs clamping). With
+// h = 0.5 - 2^-25, the largest float below one half, |v| + h rounded to nearest
+// reaches k + 1 exactly if |v| >= k + 1/2; the conversion then drops the rest.
+__device__ __forceinline__ int8_t code_of(float x, float inv) {
+    const float v = __fmul_rn(x, inv);
+    return (int8_t)__float2int_rz(__fadd_rn(v, copysignf(0x1.fffffep-2f, v)));
+}
+
 template <int DT, int D, int N>
 __global__ void __launch_bounds__(kWriteWarps * 32) k_kv8_write(const __grid_constant__ Kv8View c, Kv8Rows k, Kv8Rows v) {
     using T = typename Kv8T<DT>::type;
@@ -108,14 +124,13 @@ __global__ void __launch_bounds__(kWriteWarps * 32) k_kv8_write(const __grid_con
         const Kv8Rows& x = which ? v : k;
         const T* src = static_cast<const T*>(x.data) + (row0 + r) * x.row_stride + head * x.head_stride + VPL * lane;
         Kv8Vec<T, VPL> val[kKvBlock];   // on their way while the page is looked up
+        if (count == kKvBlock) {
 #pragma unroll
-        for (int i = 0; i < kKvBlock; ++i) {
-            if (i < count) {
-                val[i] = *reinterpret_cast<const Kv8Vec<T, VPL>*>(src + i * x.row_stride);
-            } else {
+            for (int i = 0; i < kKvBlock; ++i) val[i] = *reinterpret_cast<const Kv8Vec<T, VPL>*>(src + i * x.row_stride);
+        } else {   // rows past the last are copies of it
 #pragma unroll
-                for (int j = 0; j < VPL; ++j) val[i].v[j] = T(0.0f);
-            }
+            for (int i = 0; i < kKvBlock; ++i)
+                val[i] = *reinterpret_cast<const Kv8Vec<T, VPL>*>(src + min(i, count - 1) * x.row_stride);
         }
         uint8_t* slab = kv8_slab(c, s_rows.seq[r], pos, head);
         if (slab == nullptr) continue;
@@ -124,18 +139,19 @@ __global__ void __launch_bounds__(kWriteWarps * 32) k_kv8_write(const __grid_con
         float* scale_at = reinterpret_cast<float*>(slab + kv8_scale_off(c, which, in_page));
         const float old = first ? *scale_at : 0.0f;
 
-        unsigned top = 0;   // bits of |x| order as the values do, NaN above infinity
+        float top = 0.0f;   // NaN if a value is
 #pragma unroll
         for (int i = 0; i < kKvBlock; ++i)
 #pragma unroll
-            for (int j = 0; j < VPL; ++j) top = max(top, __float_as_uint(kv8_f(val[i].v[j])) & 0x7fffffffu);
-        top = __reduce_max_sync(0xffffffffu, top);
+            for (int j = 0; j < VPL; ++j) top = max_nan(top, fabsf(kv8_f(val[i].v[j])));
+        // the bits of what is not negative order as the values do, NaN above infinity
+        const unsigned bits = __reduce_max_sync(0xffffffffu, __float_as_uint(top) & 0x7fffffffu);
         float scale, inv;
-        if (top >= 0x7f800000u || old != old) {
+        if (bits >= 0x7f800000u || old != old) {
             scale = __uint_as_float(0x7fc00000u);
             inv = 0.0f;
         } else {
-            scale = fmaxf(__fdiv_rn(fmaxf(__uint_as_float(top), 1e-5f), 127.0f), old);
+            scale = fmaxf(__fdiv_rn(fmaxf(__uint_as_float(bits), 1e-5f), 127.0f), old);
             inv = __fdiv_rn(1.0f, scale);
         }
         __syncwarp();   // every lane has the old scale before it changes
@@ -144,7 +160,7 @@ __global__ void __launch_bounds__(kWriteWarps * 32) k_kv8_write(const __grid_con
             if (i < count) {
                 Kv8Vec<int8_t, VPL> w;
 #pragma unroll
-                for (int j = 0; j < VPL; ++j) w.v[j] = inv == 0.0f ? 0 : (int8_t)quantize_one(kv8_f(val[i].v[j]), inv);
+                for (int j = 0; j < VPL; ++j) w.v[j] = inv == 0.0f ? 0 : code_of(kv8_f(val[i].v[j]), inv);
                 *reinterpret_cast<Kv8Vec<int8_t, VPL>*>(codes + (first + i) * D) = w;
             }
         }
@@ -155,7 +171,7 @@ __global__ void __launch_bounds__(kWriteWarps * 32) k_kv8_write(const __grid_con
                 Kv8Vec<int8_t, VPL> w = *at;
 #pragma unroll
                 for (int j = 0; j < VPL; ++j)
-                    w.v[j] = (int8_t)quantize_one(__fmul_rn(i8_to_float(w.v[j]), old), inv);
+                    w.v[j] = code_of(__fmul_rn(i8_to_float(w.v[j]), old), inv);
                 *at = w;
             }
         }
@@ -165,51 +181,77 @@ __global__ void __launch_bounds__(kWriteWarps * 32) k_kv8_write(const __grid_con
 
 // ---------------------------------------------------------------------------
 // Read. A CTA takes N rows. A lane turns as many codes into values as 16 bytes
-// hold, a warp eight lines (a row's D codes of one head, K or V) at once.
+// hold; a warp has LPW lines (a row's D codes of one head, K or V) at once and
+// keeps them from row to row, kReadBatch rows on their way, so that what an
+// address takes per row is one addition to where the row's token lies.
 // ---------------------------------------------------------------------------
 constexpr int kReadWarps = 8;
 constexpr int kReadBatch = 4;
+
+// One code (byte SEL of w, 128 added) as a float: placed in the mantissa of 2^23.
+template <int SEL>
+__device__ __forceinline__ float code_to_float(uint32_t w) {
+    return __fsub_rn(__uint_as_float(__byte_perm(w, 0x4B000000u, 0x7540 | SEL)), 8388736.0f);
+}
 
 template <int DT, int D, int N>
 __global__ void __launch_bounds__(kReadWarps * 32) k_kv8_read(const __grid_constant__ Kv8View c, Kv8Rows k, Kv8Rows v) {
     using T = typename Kv8T<DT>::type;
     constexpr int VPL = 16 / sizeof(T), LPL = D / VPL, LPW = 32 / LPL;   // lanes of a line, lines of a warp's load
     __shared__ RowPlaces<N> s_rows;
-    __shared__ const uint8_t* s_page[N];   // the page's first slab; null: nothing to read
+    __shared__ const uint8_t* s_codes[N];   // the token's K codes of the page's first head; null: nothing to read
+    __shared__ int s_scale[N];              // from there to its K scale
     pdl_wait();
     const long long row0 = (long long)blockIdx.x * N;
     find_rows<kReadWarps * 32>(c, row0, s_rows);
     if (threadIdx.x < N) {
-        const int r = threadIdx.x, s = s_rows.seq[r];
-        s_page[r] = s < 0 ? nullptr : kv8_slab(c, s, s_rows.pos[r], 0);
+        const int r = threadIdx.x, s = s_rows.seq[r], t = s_rows.pos[r] & ((1 << c.page_shift) - 1);
+        const uint8_t* page = s < 0 ? nullptr : kv8_slab(c, s, s_rows.pos[r], 0);
+        s_codes[r] = page == nullptr ? nullptr : page + kv8_code_off(c, 0, t);
+        s_scale[r] = kv8_scale_off(c, 0, t) - kv8_code_off(c, 0, t);
     }
     __syncthreads();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane % LPL;
-    const int per = 2 * c.heads, lines = N * per, mask = (1 << c.page_shift) - 1;
-    const int step = kReadBatch * LPW;
-    for (int l0 = (blockIdx.y * kReadWarps + warp) * step; l0 < lines; l0 += gridDim.y * kReadWarps * step) {
-        Kv8Vec<int8_t, VPL> w[kReadBatch];
-        float scale[kReadBatch];
+    const int lane = threadIdx.x & 31, sub = lane % LPL;
+    const int lines = 2 * c.heads, groups = (lines + LPW - 1) / LPW;
+    const int warp = blockIdx.y * kReadWarps + (threadIdx.x >> 5), warps = gridDim.y * kReadWarps;
+    // warps share the groups of lines; where there are more of them, the rows too
+    const int share = max(warps / groups, 1);
+    for (int job = warp; job < groups * share; job += warps) {
+        const int h = job % groups * LPW + lane / LPL, which = h & 1;
+        const bool mine = h < lines;
+        const int code_off = (h >> 1) * c.slab + (which * c.dim << c.page_shift) + VPL * sub;
+        const int scale_off = (h >> 1) * c.slab + (which << c.page_shift) / kKvBlock * 4;
+        const Kv8Rows& o = which ? v : k;
+        T* out = static_cast<T*>(o.data) + row0 * o.row_stride + (h >> 1) * o.head_stride + VPL * sub;
+        for (int r0 = job / groups; r0 < N; r0 += kReadBatch * share) {
+            uint32_t w[kReadBatch][VPL / 4];
+            float scale[kReadBatch];
+            bool there[kReadBatch];
 #pragma unroll
-        for (int b = 0; b < kReadBatch; ++b) {
-            const int l = l0 + b * LPW + lane / LPL, r = l / per, h = l - r * per;
-            const uint8_t* page = l < lines ? s_page[r] : nullptr;
-            if (page != nullptr) {
-                const uint8_t* slab = page + (long long)(h >> 1) * c.slab;
-                const int t = s_rows.pos[r] & mask;
-                scale[b] = *reinterpret_cast<const float*>(slab + kv8_scale_off(c, h & 1, t));
-                w[b] = *reinterpret_cast<const Kv8Vec<int8_t, VPL>*>(slab + kv8_code_off(c, h & 1, t) + VPL * sub);
+            for (int b = 0; b < kReadBatch; ++b) {
+                const int r = r0 + b * share;
+                const uint8_t* at = r < N ? s_codes[r] : nullptr;
+                there[b] = mine && at != nullptr;
+                if (there[b]) {
+                    scale[b] = *reinterpret_cast<const float*>(at + s_scale[r] + scale_off);
+                    const Kv8Vec<uint32_t, VPL / 4> x = *reinterpret_cast<const Kv8Vec<uint32_t, VPL / 4>*>(at + code_off);
+#pragma unroll
+                    for (int i = 0; i < VPL / 4; ++i) w[b][i] = x.v[i] ^ 0x80808080u;
+                }
             }
-        }
 #pragma unroll
-        for (int b = 0; b < kReadBatch; ++b) {
-            const int l = l0 + b * LPW + lane / LPL, r = l / per, h = l - r * per;
-            if (l >= lines || s_page[r] == nullptr) continue;
-            float x[VPL];
+            for (int b = 0; b < kReadBatch; ++b) {
+                if (!there[b]) continue;
+                float x[VPL];
 #pragma unroll
-            for (int j = 0; j < VPL; ++j) x[j] = __fmul_rn(i8_to_float(w[b].v[j]), scale[b]);
-            const Kv8Rows& o = h & 1 ? v : k;
-            kv8_store<T, VPL>(static_cast<T*>(o.data) + (row0 + r) * o.row_stride + (h >> 1) * o.head_stride + VPL * sub, x);
+                for (int i = 0; i < VPL / 4; ++i) {
+                    x[4 * i] = __fmul_rn(code_to_float<0>(w[b][i]), scale[b]);
+                    x[4 * i + 1] = __fmul_rn(code_to_float<1>(w[b][i]), scale[b]);
+                    x[4 * i + 2] = __fmul_rn(code_to_float<2>(w[b][i]), scale[b]);
+                    x[4 * i + 3] = __fmul_rn(code_to_float<3>(w[b][i]), scale[b]);
+                }
+                kv8_store<T, VPL>(out + (r0 + b * share) * o.row_stride, x);
+            }
         }
     }
 }
@@ -461,9 +503,9 @@ struct GoWrite {
     static cudaError_t with(cudaStream_t s, const Kv8View& c, const Kv8Rows& k, const Kv8Rows& v) {
         // Leaders expected among N rows: each row of a batch of single tokens,
         // one in 16 of a long one. Single tokens' units get a warp each; of the
-        // long ones' a warp takes four.
+        // long ones' a warp takes two.
         const int leaders = N == kLongRows ? N / kKvBlock + 1 : std::min(N, N / c.max_rows + 1);
-        const int units = 2 * c.heads * leaders, each = N == kLongRows ? 4 : 1;
+        const int units = 2 * c.heads * leaders, each = N == kLongRows ? 2 : 1;
         const dim3 grid((unsigned)((c.rows + N - 1) / N), clamp_grid((units + each * kWriteWarps - 1) / (each * kWriteWarps)));
         return launch_pdl(k_kv8_write<DT, D, N>, grid, dim3(kWriteWarps * 32), 0, s, c, k, v);
     }
@@ -475,10 +517,11 @@ template <int DT, int D>
 struct GoRead {
     template <int N>
     static cudaError_t with(cudaStream_t s, const Kv8View& c, const Kv8Rows& k, const Kv8Rows& v) {
-        // lines of a CTA's pass; of long batches a warp takes four passes
-        constexpr int lines = kReadWarps * kReadBatch * (32 / (D / (16 / (int)sizeof(typename Kv8T<DT>::type))));
-        const int each = N == kLongRows ? 4 : 1;
-        const dim3 grid((unsigned)((c.rows + N - 1) / N), clamp_grid((N * 2 * c.heads + each * lines - 1) / (each * lines)));
+        // A warp takes four batches of rows of its lines (long batches), or one.
+        constexpr int LPW = 32 / (D / (16 / (int)sizeof(typename Kv8T<DT>::type)));
+        constexpr int passes = N == kLongRows ? 4 : 1;
+        const int64_t jobs = (int64_t)((2 * c.heads + LPW - 1) / LPW) * (N / (passes * kReadBatch));
+        const dim3 grid((unsigned)((c.rows + N - 1) / N), clamp_grid((jobs + kReadWarps - 1) / kReadWarps));
         return launch_pdl(k_kv8_read<DT, D, N>, grid, dim3(kReadWarps * 32), 0, s, c, k, v);
     }
     static void go(cudaStream_t s, const Kv8View& c, const Kv8Rows& k, const Kv8Rows& v, cudaError_t& e) {
