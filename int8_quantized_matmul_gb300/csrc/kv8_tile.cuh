@@ -318,8 +318,8 @@ __global__ void __launch_bounds__(kvt::kThreads, 1)
     Shared& S = *reinterpret_cast<Shared*>(sRaw + kStages * kOp / 2);
 
     const Kv8View& c = a.c;
-    // (the shuffle tells the compiler that a warp's index is the same in all its lanes)
-    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+    // (the reduction tells the compiler that a warp's index is the same in all its lanes)
+    const int tid = threadIdx.x, warp = (int)__reduce_max_sync(0xffffffffu, (unsigned)tid >> 5), lane = tid & 31;
     const int group = a.q_heads / c.heads;
     constexpr int kRowsItem = MT * kTileQ;
 
@@ -730,8 +730,9 @@ __global__ void __launch_bounds__(kvt::kThreads, 1)
             const uint32_t lead = lane == 0;
             const int me = warp - kIssueWarp;
             const int qt = MT == 2 ? me : 0;
-            const int n = __shfl_sync(0xffffffffu, steps_of(qt), 0);
-            const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+            // (reductions over the warp: their results are in uniform registers)
+            const int n = (int)__reduce_max_sync(0xffffffffu, (unsigned)steps_of(qt));
+            const uint32_t tm = __reduce_max_sync(0xffffffffu, tmem);
             constexpr uint32_t idesc_qk = tc::idesc_f16_f32(kTileQ, kTileKv);
             constexpr uint32_t idesc_pv = tc::idesc_f16_f32(kTileQ, D) | kTransposeB;
             const uint32_t to_ = tm + kColO + (uint32_t)(qt * D);
