@@ -26,13 +26,14 @@
 // 9e-6 of O was measured. For F32 rows O is therefore moved every kChain tiles
 // into a running sum that is added to with rounding (1e-6).
 //
-// Two shapes, each with two warpgroups of softmax threads, one thread per row
-// (TMEM lane), that run out of step, so that one's work fills the other's waits
-// and the MMAs of one's tile run during the other's softmax. MT = 2 (16-bit
-// rows, where there are enough of them): two query tiles share each converted
-// tile of the cache, a warpgroup each. MT = 1: the warpgroups take the tiles of
-// the cache by turns; the running maximum goes from one to the other through
-// shared memory, between the maximum and the weights of a tile.
+// Two shapes, with two warpgroups of softmax threads, one thread per row (TMEM
+// lane). MT = 2 (16-bit rows, where there are enough of them): two query tiles,
+// a warpgroup each, share each converted tile of the cache; one's softmax runs
+// while the other's MMAs do. MT = 1: one query tile, two S buffers; the
+// warpgroups take half of a tile's columns each and exchange their maxima, and
+// have the next tile's S ready while this one's P V and the S after it are
+// computed. (A tile for each warpgroup by turns: the way from S to the next S in
+// the same buffer is then longer than two tiles' MMAs, 4100 cycles per tile.)
 //
 // Roles (16 warps, one CTA per SM):
 //   warps 0-3, 4-7  softmax; they also stage Q, rescale O and write the output
@@ -86,12 +87,14 @@ __host__ __device__ constexpr int operand_bytes() { return kTileKv * D * 2; }
 struct Shared {
     uint64_t full[kSlots], empty[kSlots], cfull[kConsts], bfull[kConsts];
     uint64_t q_ready[2], s_full[2], p_ready[2][2], pv_done[2], drained[2], m_ready[2], l_ready;
-    float4 cst[kConsts][kBlocks];   // K scale, log2 of the V scale, its inverse
+    float2 cst[kConsts][kBlocks];   // K scale, log2 of the V scale
+    float inv[kConsts][kBlocks];    // inverse of the V scale
     const uint8_t* block[kConsts][kBlocks];   // K codes of a tile's blocks, null where there is none
-    float rows[3 * kTileQ];   // each row's factor (of MT tiles), then for MT = 1 its maximum after the even and the odd tiles
+    // MT = 1: the largest logits of a row's two halves, [step & 1][half][row].
+    // Before that, where the odd steps' will be: each row's factor.
+    float rows[2][2][kTileQ];
     uint32_t tmem;
     int abort;
-    int scan[kThreads / 32];
     int item[2];   // sequence, first row of the item in it
 };
 
@@ -150,7 +153,7 @@ __device__ __forceinline__ void hide(uint32_t (&v)[32], int lo, int hi) {
 
 // The largest logit (with the V scale's log2) of 32 columns of S.
 template <bool MASKED>
-__device__ __forceinline__ float piece_top(uint32_t (&v)[32], float mul, const float4* cst, int lo, int hi) {
+__device__ __forceinline__ float piece_top(uint32_t (&v)[32], float mul, const float2* cst, int lo, int hi) {
     if (MASKED) hide(v, lo, hi);
     float top = -INFINITY;
 #pragma unroll
@@ -161,7 +164,7 @@ __device__ __forceinline__ float piece_top(uint32_t (&v)[32], float mul, const f
             t0 = max3(t0, __uint_as_float(v[i]), __uint_as_float(v[i + 1]));
             t1 = max3(t1, __uint_as_float(v[i + 2]), __uint_as_float(v[i + 3]));
         }
-        const float2 k = *reinterpret_cast<const float2*>(&cst[b]);
+        const float2 k = cst[b];
         // a zero scale times -infinity would be NaN, which the maximum ignores
         top = fmaxf(top, fmaf(fmaxf(t0, t1), mul * k.x, k.y));
     }
@@ -170,11 +173,11 @@ __device__ __forceinline__ float piece_top(uint32_t (&v)[32], float mul, const f
 
 // The weights of 32 columns, as f16 (parts), and their share of l.
 template <bool MASKED, int PARTS>
-__device__ __forceinline__ void piece_weights(uint32_t (&v)[32], float mul, float sub, const float4* cst, int lo, int hi,
-                                              float& l, uint32_t (&hi16)[16], uint32_t (&lo16)[16]) {
+__device__ __forceinline__ void piece_weights(uint32_t (&v)[32], float mul, float sub, const float2* cst, const float* inv,
+                                              int lo, int hi, float& l, uint32_t (&hi16)[16], uint32_t (&lo16)[16]) {
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
-        const float4 k = cst[b];
+        const float2 k = cst[b];
         const float xm = mul * k.x, add = k.y - sub;
         float2 sum = make_float2(0.0f, 0.0f);
 #pragma unroll
@@ -196,13 +199,13 @@ __device__ __forceinline__ void piece_weights(uint32_t (&v)[32], float mul, floa
                 lo16[i / 2] = kvd::pack2(rest.x, rest.y);
             }
         }
-        l = fmaf(sum.x + sum.y, k.z, l);
+        l = fmaf(sum.x + sum.y, inv[b], l);
     }
 }
 
 // One tile of S at `ts` (128 columns of the thread's row): its largest logit.
 template <bool MASKED>
-__device__ __forceinline__ float tile_top(uint32_t ts, float mul, const float4* cst, int lo, int hi) {
+__device__ __forceinline__ float tile_top(uint32_t ts, float mul, const float2* cst, int lo, int hi) {
     uint32_t a[32], b[32];
     float top = -INFINITY;
     tc::tmem_ld_32x32b_x32(ts, a);
@@ -221,8 +224,8 @@ __device__ __forceinline__ float tile_top(uint32_t ts, float mul, const float4* 
 
 // The tile's weights in place of its S; each half of them is handed on as soon as it is there.
 template <bool MASKED, int PARTS>
-__device__ __forceinline__ void tile_weights(uint32_t ts, float mul, float sub, const float4* cst, int lo, int hi, float& l,
-                                             uint64_t* ready) {
+__device__ __forceinline__ void tile_weights(uint32_t ts, float mul, float sub, const float2* cst, const float* inv, int lo,
+                                             int hi, float& l, uint64_t* ready) {
     uint32_t a[32], b[32], hi16[16], lo16[16];
     auto store = [&](uint32_t at) {
         tc::tmem_st_32x32b_x16(at, hi16);
@@ -236,19 +239,19 @@ __device__ __forceinline__ void tile_weights(uint32_t ts, float mul, float sub, 
     tc::tmem_ld_32x32b_x32(ts, a);
     tc::tmem_ld_wait();
     tc::tmem_ld_32x32b_x32(ts + 32u, b);
-    piece_weights<MASKED, PARTS>(a, mul, sub, cst, lo, hi, l, hi16, lo16);
+    piece_weights<MASKED, PARTS>(a, mul, sub, cst, inv, lo, hi, l, hi16, lo16);
     store(ts);
     tc::tmem_ld_wait();
     tc::tmem_ld_32x32b_x32(ts + 64u, a);
-    piece_weights<MASKED, PARTS>(b, mul, sub, cst + 2, lo - 32, hi - 32, l, hi16, lo16);
+    piece_weights<MASKED, PARTS>(b, mul, sub, cst + 2, inv + 2, lo - 32, hi - 32, l, hi16, lo16);
     store(ts + 32u);
     tc::tmem_ld_wait();
     hand_on(0);
     tc::tmem_ld_32x32b_x32(ts + 96u, b);
-    piece_weights<MASKED, PARTS>(a, mul, sub, cst + 4, lo - 64, hi - 64, l, hi16, lo16);
+    piece_weights<MASKED, PARTS>(a, mul, sub, cst + 4, inv + 4, lo - 64, hi - 64, l, hi16, lo16);
     store(ts + 64u);
     tc::tmem_ld_wait();
-    piece_weights<MASKED, PARTS>(b, mul, sub, cst + 6, lo - 96, hi - 96, l, hi16, lo16);
+    piece_weights<MASKED, PARTS>(b, mul, sub, cst + 6, inv + 6, lo - 96, hi - 96, l, hi16, lo16);
     store(ts + 96u);
     hand_on(1);
 }
@@ -323,6 +326,7 @@ __global__ void __launch_bounds__(kvt::kThreads, 1)
     const int group = a.q_heads / c.heads;
     constexpr int kRowsItem = MT * kTileQ;
 
+    int* const scan = reinterpret_cast<int*>(S.rows);   // until the barrier below
     // The item: heads vary fastest, the last rows of the last sequence come
     // first (under a causal mask they see the most).
     {
@@ -338,12 +342,12 @@ __global__ void __launch_bounds__(kvt::kThreads, 1)
             const int v = __shfl_up_sync(0xffffffffu, upto, o);
             if (lane >= o) upto += v;
         }
-        if (lane == 31) S.scan[warp] = upto;
+        if (lane == 31) scan[warp] = upto;
         __syncthreads();
         int base = upto - mine, all = 0;
         for (int w = 0; w < kThreads / 32; ++w) {
-            if (w < warp) base += S.scan[w];
-            all += S.scan[w];
+            if (w < warp) base += scan[w];
+            all += scan[w];
         }
         const int at = all - 1 - (int)(blockIdx.x / c.heads);
         if (at < 0) return;   // uniform: every thread has the same `all`
@@ -374,7 +378,7 @@ __global__ void __launch_bounds__(kvt::kThreads, 1)
             tc::mbar_init(&S.p_ready[i][1], 128);
             tc::mbar_init(&S.pv_done[i], 1);
             tc::mbar_init(&S.drained[i], 1);
-            tc::mbar_init(&S.m_ready[i], 128);
+            tc::mbar_init(&S.m_ready[i], 256);
         }
         tc::mbar_init(&S.l_ready, 256);
         S.abort = 0;
@@ -463,7 +467,7 @@ __global__ void __launch_bounds__(kvt::kThreads, 1)
                     float up, down;
                     kvd::row_scale(top, up, down);
                     // mul is not negative, so the largest S of a block is the largest logit
-                    if (lane == 0) S.rows[qt * kTileQ + rr] = down * (fabsf(a.scale) * 1.44269504088896340736f);
+                    if (lane == 0) S.rows[1][qt][rr] = down * (fabsf(a.scale) * 1.44269504088896340736f);
                     if (a.scale < 0.0f) up = -up;
                     uint32_t hi[VPL / 2], lo[VPL / 2];
 #pragma unroll
@@ -502,37 +506,42 @@ __global__ void __launch_bounds__(kvt::kThreads, 1)
             return ok;
         };
         float mul = 0.0f;
-        if (n > 0 && wait(&S.q_ready[qt], 0)) mul = S.rows[qt * kTileQ + r];
-        float* const s_m = &S.rows[kTileQ];   // [step & 1][row] (MT = 1)
+        if (n > 0 && wait(&S.q_ready[qt], 0)) mul = S.rows[1][qt][r];
+        constexpr int OC = MT == 2 ? D : D / 2;   // columns of O that a thread has
         float m = -INFINITY, l = 0.0f, m_run = -INFINITY;
-        for (int j = h; ok && j < n; j += 3 - MT) {
+        for (int j = 0; ok && j < n; ++j) {
             const int cs = j % kConsts;
             const int bf = MT == 2 ? qt : j & 1, ph = MT == 2 ? j & 1 : (j >> 1) & 1;
             if (!wait(&S.cfull[cs], (j / kConsts) & 1) || !wait(&S.s_full[bf], ph)) break;
             tc::tc_fence_after();
-            const uint32_t ts = tmem + lanes + (uint32_t)(bf * kTileKv);
+            const uint32_t ts = tmem + lanes + (uint32_t)(bf * kTileKv + h * 64);
             const int tok = (from + j) * kTileKv;
             const bool masked = tok < all_lo || tok + kTileKv > all_hi;   // for some row of the warp
-            const int lo = see_lo - tok, hi = see_hi - tok;
-            const float top = masked ? tile_top<true>(ts, mul, S.cst[cs], lo, hi) : tile_top<false>(ts, mul, S.cst[cs], lo, hi);
-            float before = m;
-            if (MT == 1 && j > 0) {   // the maximum up to the tile before, of the other warpgroup
-                if (!wait(&S.m_ready[bf ^ 1], ((j - 1) >> 1) & 1)) break;
-                before = s_m[(bf ^ 1) * kTileQ + r];
-                if (before != m) l *= m == -INFINITY ? 0.0f : ex2(m - before);
+            const int lo = see_lo - tok - 64 * h, hi = see_hi - tok - 64 * h;
+            const float2* cst = &S.cst[cs][4 * h];
+            uint32_t xa[32], xb[32];   // MT = 1: the thread's 64 columns
+            float top;
+            if (MT == 2) {
+                top = masked ? tile_top<true>(ts, mul, cst, lo, hi) : tile_top<false>(ts, mul, cst, lo, hi);
+            } else {
+                tc::tmem_ld_32x32b_x32(ts, xa);
+                tc::tmem_ld_32x32b_x32(ts + 32u, xb);
+                tc::tmem_ld_wait();
+                top = masked ? fmaxf(piece_top<true>(xa, mul, cst, lo, hi), piece_top<true>(xb, mul, cst + 2, lo - 32, hi - 32))
+                             : fmaxf(piece_top<false>(xa, mul, cst, lo, hi), piece_top<false>(xb, mul, cst + 2, lo - 32, hi - 32));
+                S.rows[bf][h][r] = top;
+                tc::mbar_arrive(&S.m_ready[bf]);
+                if (!wait(&S.m_ready[bf], ph)) break;
+                top = fmaxf(top, S.rows[bf][h ^ 1][r]);
             }
-            const bool grown = __any_sync(0xffffffffu, top > before + kSlack);
+            const bool grown = __any_sync(0xffffffffu, top > m + kSlack);
             const bool flush = kChained && j > 0 && j % kChain == 0;
             float keep = 1.0f;
-            m = before;
             if (grown) {
-                m = fmaxf(before, top);
-                keep = m == -INFINITY ? 1.0f : ex2(before - m);
+                const float nm = fmaxf(m, top);
+                keep = nm == -INFINITY ? 1.0f : ex2(m - nm);
+                m = nm;
                 l *= keep;
-            }
-            if (MT == 1) {
-                s_m[bf * kTileQ + r] = m;
-                tc::mbar_arrive(&S.m_ready[bf]);
             }
             if ((grown && j > 0) || flush) {
                 // O holds the tiles before this one; with two S buffers their MMAs may still run
@@ -540,61 +549,67 @@ __global__ void __launch_bounds__(kvt::kThreads, 1)
                     if (!wait(&S.pv_done[(j - 1) & 1], ((j - 1) >> 1) & 1)) break;
                     tc::tc_fence_after();
                 }
+                const uint32_t at = to_ + (uint32_t)(h * OC), run_at = tr + (uint32_t)(h * OC);
                 if (flush) {
                     const bool first = j == kChain;
                     const float keep_run = m == -INFINITY ? 1.0f : ex2(m_run - m);
                     m_run = m;
 #pragma unroll 1
-                    for (int ch = 0; ch < D / 32; ++ch) {
-                        uint32_t o[32], v[32];
-                        tc::tmem_ld_32x32b_x32(to_ + 32u * ch, o);
-                        if (!first) tc::tmem_ld_32x32b_x32(tr + 32u * ch, v);
+                    for (int ch = 0; ch < OC / 16; ++ch) {
+                        uint32_t o[16], v[16];
+                        tc::tmem_ld_32x32b_x16(at + 16u * ch, o);
+                        if (!first) tc::tmem_ld_32x32b_x16(run_at + 16u * ch, v);
                         tc::tmem_ld_wait();
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) {
+                        for (int i = 0; i < 16; ++i) {
                             const float y = __uint_as_float(o[i]) * keep;
                             v[i] = __float_as_uint(first ? y : fmaf(__uint_as_float(v[i]), keep_run, y));
                         }
-                        tc::tmem_st_32x32b_x32(tr + 32u * ch, v);
+                        tc::tmem_st_32x32b_x16(run_at + 16u * ch, v);
                     }
                 } else {
 #pragma unroll 1
-                    for (int ch = 0; ch < D / 32; ++ch) {
-                        uint32_t v[32];
-                        tc::tmem_ld_32x32b_x32(to_ + 32u * ch, v);
+                    for (int ch = 0; ch < OC / 16; ++ch) {
+                        uint32_t v[16];
+                        tc::tmem_ld_32x32b_x16(at + 16u * ch, v);
                         tc::tmem_ld_wait();
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * keep);
-                        tc::tmem_st_32x32b_x32(to_ + 32u * ch, v);
+                        for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * keep);
+                        tc::tmem_st_32x32b_x16(at + 16u * ch, v);
                     }
                 }
             }
             const float sub = m == -INFINITY ? 0.0f : m - kBias;
-            if (masked) tile_weights<true, PARTS>(ts, mul, sub, S.cst[cs], lo, hi, l, S.p_ready[bf]);
-            else tile_weights<false, PARTS>(ts, mul, sub, S.cst[cs], lo, hi, l, S.p_ready[bf]);
+            const float* inv = &S.inv[cs][4 * h];
+            if (MT == 2) {
+                if (masked) tile_weights<true, PARTS>(ts, mul, sub, cst, inv, lo, hi, l, S.p_ready[bf]);
+                else tile_weights<false, PARTS>(ts, mul, sub, cst, inv, lo, hi, l, S.p_ready[bf]);
+            } else {
+                uint32_t hi16[16], lo16[16];
+                if (masked) piece_weights<true, PARTS>(xa, mul, sub, cst, inv, lo, hi, l, hi16, lo16);
+                else piece_weights<false, PARTS>(xa, mul, sub, cst, inv, lo, hi, l, hi16, lo16);
+                tc::tmem_st_32x32b_x16(ts, hi16);
+                if (PARTS == 2) tc::tmem_st_32x32b_x16(ts + 16u, lo16);
+                if (masked) piece_weights<true, PARTS>(xb, mul, sub, cst + 2, inv + 2, lo - 32, hi - 32, l, hi16, lo16);
+                else piece_weights<false, PARTS>(xb, mul, sub, cst + 2, inv + 2, lo - 32, hi - 32, l, hi16, lo16);
+                tc::tmem_st_32x32b_x16(ts + 32u, hi16);
+                if (PARTS == 2) tc::tmem_st_32x32b_x16(ts + 48u, lo16);
+                tc::tmem_st_wait();
+                tc::tc_fence_before();
+                tc::mbar_arrive(&S.p_ready[bf][h]);
+            }
         }
         if (ok && n > 0) {
             const int last = n - 1;
-            if (wait(&S.pv_done[MT == 2 ? qt : last & 1], MT == 2 ? last & 1 : (last >> 1) & 1) && MT == 1 &&
-                wait(&S.m_ready[last & 1], (last >> 1) & 1)) {
-                // the maximum of all tiles, l of both warpgroups, and what the
-                // running sum refers to (the first warpgroup moves O), through
-                // the memory of Q, which nothing reads any more
+            if (wait(&S.pv_done[MT == 2 ? qt : last & 1], MT == 2 ? last & 1 : (last >> 1) & 1) && MT == 1) {
+                // l of both halves, through the memory of Q, which nothing reads any more
                 float* const ex = reinterpret_cast<float*>(sQ);
-                const float all = s_m[(last & 1) * kTileQ + r];
-                if (all != m) l *= m == -INFINITY ? 0.0f : ex2(m - all);
-                m = all;
                 ex[h * kTileQ + r] = l;
-                if (h == 0) ex[2 * kTileQ + r] = m_run;
                 tc::mbar_arrive(&S.l_ready);
-                if (wait(&S.l_ready, 0)) {
-                    l += ex[(h ^ 1) * kTileQ + r];
-                    m_run = ex[2 * kTileQ + r];
-                }
+                if (wait(&S.l_ready, 0)) l += ex[(h ^ 1) * kTileQ + r];
             }
             tc::tc_fence_after();
         }
-        constexpr int OC = MT == 2 ? D : D / 2;   // columns of O that a thread writes
         if (ok) {
             const int ti = row / group, hh = head * group + row - ti * group;
             const long long grow = sq.row0 + ti;
@@ -861,8 +876,8 @@ __global__ void __launch_bounds__(kvt::kThreads, 1)
                 if (lane < kBlocks) {
                     const float k = sc0.x, v = sc0.y;
                     // NaN weights make l NaN for the rows that see the block; the others add 0 * 1
-                    S.cst[j % kConsts][lane] = v < 0.0f ? make_float4(0.0f, -INFINITY, 0.0f, 0.0f)
-                                                        : make_float4(k, log2f(v), v == v ? __fdiv_rn(1.0f, v) : 1.0f, 0.0f);
+                    S.cst[j % kConsts][lane] = v < 0.0f ? make_float2(0.0f, -INFINITY) : make_float2(k, log2f(v));
+                    S.inv[j % kConsts][lane] = v < 0.0f ? 0.0f : v == v ? __fdiv_rn(1.0f, v) : 1.0f;
                 }
                 tc::mbar_arrive(&S.cfull[j % kConsts]);
                 sc0 = sc1;
