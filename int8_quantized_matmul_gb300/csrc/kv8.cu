@@ -285,8 +285,8 @@ struct Kv8RopeArgs {
     bool next;   // pairs (2i, 2i + 1)
 };
 
-template <int DT, int D, int VPL>
-__global__ void __launch_bounds__(kRopeWarps * 32) k_kv8_norm_rope(const __grid_constant__ Kv8RopeArgs a) {
+template <int DT, int D, int VPL, bool NORM>
+__global__ void __launch_bounds__(kRopeWarps * 32, DT == kKvF32 ? 9 : 1) k_kv8_norm_rope(const __grid_constant__ Kv8RopeArgs a) {
     using T = typename Kv8T<DT>::type;
     constexpr int LPH = D / VPL, HPW = 32 / LPH;   // lanes of a head, heads of a warp's load
     __shared__ float2 s_cs[kRopeWarps][D / 2];
@@ -332,10 +332,9 @@ __global__ void __launch_bounds__(kRopeWarps * 32) k_kv8_norm_rope(const __grid_
     float gq[VPL], gk[VPL];
 #pragma unroll
     for (int j = 0; j < VPL; ++j) {
-        gq[j] = a.gamma_q != nullptr ? a.gamma_q[d0 + j] : 1.0f;
-        gk[j] = a.gamma_k != nullptr ? a.gamma_k[d0 + j] : 1.0f;
+        gq[j] = NORM && a.gamma_q != nullptr ? a.gamma_q[d0 + j] : 1.0f;
+        gk[j] = NORM && a.gamma_k != nullptr ? a.gamma_k[d0 + j] : 1.0f;
     }
-    const bool norms = a.gamma_q != nullptr || a.gamma_k != nullptr;
 
     for (int h0 = h_lo; h0 < h_end; h0 += kRopeBatch * HPW) {
         if (h0 > h_lo) fetch(h0);
@@ -346,7 +345,7 @@ __global__ void __launch_bounds__(kRopeWarps * 32) k_kv8_norm_rope(const __grid_
             float x[VPL];
 #pragma unroll
             for (int j = 0; j < VPL; ++j) x[j] = kv8_f(raw[b].v[j]);
-            if (norms) {
+            if (NORM) {
                 float ss = 0.0f;
 #pragma unroll
                 for (int j = 0; j < VPL; ++j) ss = fmaf(x[j], x[j], ss);
@@ -540,7 +539,9 @@ struct GoRope {
         while (splits * batch < heads && ctas * splits < 16 * 152) ++splits;
         a.heads_per_warp = ((heads + splits - 1) / splits + batch - 1) / batch * batch;
         const dim3 grid((unsigned)ctas, (unsigned)((heads + a.heads_per_warp - 1) / a.heads_per_warp));
-        return launch_pdl(k_kv8_norm_rope<DT, D, VPL>, grid, dim3(kRopeWarps * 32), 0, s, a);
+        if (a.gamma_q != nullptr || a.gamma_k != nullptr)
+            return launch_pdl(k_kv8_norm_rope<DT, D, VPL, true>, grid, dim3(kRopeWarps * 32), 0, s, a);
+        return launch_pdl(k_kv8_norm_rope<DT, D, VPL, false>, grid, dim3(kRopeWarps * 32), 0, s, a);
     }
     static void go(Kv8RopeArgs& a, cudaStream_t s, cudaError_t& e) {
         constexpr int kFull = DT == kKvF32 ? 4 : 8;
