@@ -602,17 +602,18 @@ int w8a8_mul_mat_grouped(const w8a8_problem* probs, int count, int64_t M, void* 
  * tokens concerned are cut to what is valid, so nothing outside the pool, the
  * table or the row tensors is touched. kv8_read_status reports the word.
  * Sequences may share pages that they only read; a block that a kv8_write
- * writes must belong to one sequence of its batch.
+ * writes must stand at one place of its batch's table.
  *
  * Row tensors. kv8_rows: element (row, head, d) at data[row*row_stride +
  * head*head_stride + d], strides in elements, of KV8_F32, KV8_F16 or KV8_BF16;
  * data 16-byte aligned and both strides a multiple of 16 bytes (so a slice of
- * a fused q/k/v projection works). Strides are not negative, and an output's
- * elements are distinct.
+ * a fused q/k/v projection works). Strides are not negative, a tensor reaches
+ * over less than 2^40 elements, an output's elements are distinct, and two
+ * outputs may be slices of one row.
  *
  * Limits: head_dim 64 or 128, 1 <= heads <= 1024, 1 <= seqs <= KV8_MAX_SEQS,
  * 1 <= max_rows <= rows < 2^31, table_width*page_tokens < 2^31,
- * seqs*heads*table_width*page_tokens < 2^35. Errors of every call: BAD_SHAPE, NULL_PTR, MISALIGNED, BAD_ARG (an unknown dtype or flag, or
+ * seqs*heads*table_width*page_tokens < 2^34. Errors of every call: BAD_SHAPE, NULL_PTR, MISALIGNED, BAD_ARG (an unknown dtype or flag, or
  * an output that overlaps another operand), UNSUPPORTED_DEVICE, CUDA.
  * ------------------------------------------------------------------------- */
 #define KV8_BLOCK 16
@@ -702,8 +703,10 @@ int kv8_norm_rope(const kv8_rows* q, const kv8_rows* q_out, int q_heads, const f
  * over the sequence's tokens j < kv_len[s], of KV head h / (q_heads / heads).
  * With KV8_CAUSAL only j <= the row's position, and with window > 0 (KV8_CAUSAL
  * only) j > position - window. A row that sees no token has a zero output.
- * Softmax statistics and sums are binary32; F32 queries and probabilities
- * enter the tensor cores as two f16 parts each, 16-bit ones as one.
+ * Softmax statistics and sums are binary32; F32 queries and the weights of F32
+ * rows enter the tensor cores as two f16 parts each (22 bits). Scales are
+ * taken to be as kv8_write makes them: not negative, V's from 2^-40 to 2^86, or
+ * NaN, which makes the rows that see the block NaN and no others.
  * q, out    rows x q_heads x head_dim, one dtype; q_heads a multiple of
  *           cache->heads, at most 64 times it. out overlaps no other operand.
  * lse       device F32 [rows x q_heads] or NULL: log(sum_j exp(softmax_scale *

@@ -401,13 +401,27 @@ Range rows_range(const kv8_rows& t, int64_t rows, int heads, int dim) {
     return bytes_at(t.data, (size_t)n * dtype_size(t.dtype));
 }
 
-constexpr int64_t kMaxStride = (int64_t)1 << 40;
+constexpr int64_t kMaxStride = (int64_t)1 << 40;   // elements, and of a whole tensor
+
+// Whether two outputs share no element: apart, or rows of one inside the gaps
+// between the rows of the other (slices of a fused row).
+bool apart(const kv8_rows& a, int a_heads, const kv8_rows& b, int b_heads, int64_t rows, int dim) {
+    const Range ra = rows_range(a, rows, a_heads, dim), rb = rows_range(b, rows, b_heads, dim);
+    if (!ra.meets(rb)) return true;
+    if (a.row_stride != b.row_stride || a.dtype != b.dtype) return false;
+    const int64_t pitch = a.row_stride * dtype_size(a.dtype);
+    const int64_t wa = ((a_heads - 1) * a.head_stride + dim) * dtype_size(a.dtype);
+    const int64_t wb = ((b_heads - 1) * b.head_stride + dim) * dtype_size(b.dtype);
+    const int64_t off = (int64_t)(rb.lo - ra.lo);   // b's first row after a's first
+    return off >= 0 ? off >= wa && off + wb <= pitch : -off >= wb && -off + wa <= pitch;
+}
 
 int check_rows(const kv8_rows* t, int64_t rows, int heads, int dim, bool output) {
     if (!t || !t->data) return I2S_E_NULL_PTR;
     if (t->dtype < kKvF32 || t->dtype > kKvBf16) return I2S_E_BAD_ARG;
     if (t->row_stride < 0 || t->head_stride < 0 || t->row_stride > kMaxStride || t->head_stride > kMaxStride)
         return I2S_E_BAD_SHAPE;
+    if ((__int128)(rows - 1) * t->row_stride + (__int128)(heads - 1) * t->head_stride > kMaxStride) return I2S_E_BAD_SHAPE;
     const int64_t unit = 16 / dtype_size(t->dtype);
     if (!aligned16(t->data) || t->row_stride % unit || t->head_stride % unit) return I2S_E_MISALIGNED;
     if (output) {
@@ -437,8 +451,9 @@ int check_sizes(const kv8_cache& c, const kv8_batch& b, Kv8View& w) {
         b.max_rows > b.rows)
         return I2S_E_BAD_SHAPE;
     if (b.table_width < 1 || b.table_width >= ((int64_t)1 << 31) / c.page_tokens) return I2S_E_BAD_SHAPE;
-    // blocks of all sequences and heads are counted in 32 bits
-    if (b.table_width * (c.page_tokens / kKvBlock) >= ((int64_t)1 << 31) / ((int64_t)b.seqs * c.heads)) return I2S_E_BAD_SHAPE;
+    // blocks of all sequences and heads, and a few places more for each pair of
+    // those, are counted in 32 bits
+    if (b.table_width * (c.page_tokens / kKvBlock) >= ((int64_t)1 << 30) / ((int64_t)b.seqs * c.heads)) return I2S_E_BAD_SHAPE;
     w.n_pages = c.n_pages;
     w.rows = b.rows;
     w.width = b.table_width;
@@ -589,7 +604,7 @@ int kv8_read(const kv8_cache* cache, const kv8_batch* batch, const kv8_rows* k, 
     if ((r = check_rows(k, c.rows, c.heads, c.dim, true)) || (r = check_rows(v, c.rows, c.heads, c.dim, true))) return r;
     if (k->dtype != v->dtype) return I2S_E_BAD_ARG;
     const Range rk = rows_range(*k, c.rows, c.heads, c.dim), rv = rows_range(*v, c.rows, c.heads, c.dim);
-    if (pool.meets(rk) || pool.meets(rv) || rk.meets(rv) || meets_batch(rk, *batch) || meets_batch(rv, *batch))
+    if (pool.meets(rk) || pool.meets(rv) || !apart(*k, c.heads, *v, c.heads, c.rows, c.dim) || meets_batch(rk, *batch) || meets_batch(rv, *batch))
         return I2S_E_BAD_ARG;
     if ((r = check_current_device())) return r;
     cudaError_t e = cudaSuccess;
@@ -638,11 +653,20 @@ int kv8_norm_rope(const kv8_rows* q, const kv8_rows* q_out, int q_heads, const f
     }
     if (((uintptr_t)gamma_q & 15) || ((uintptr_t)gamma_k & 15) || ((uintptr_t)positions & 3) || ((uintptr_t)turns & 7))
         return I2S_E_MISALIGNED;
+    for (int t = 0; t < 2; ++t) {
+        const Range small[4] = {bytes_at(gamma_q, gamma_q ? 4 * (size_t)head_dim : 0),
+                                bytes_at(gamma_k, gamma_k ? 4 * (size_t)head_dim : 0),
+                                bytes_at(positions, rot_dim ? 4 * (size_t)rows : 0),
+                                bytes_at(turns, rot_dim ? 4 * (size_t)rot_dim : 0)};
+        for (const Range& r : small)
+            if (heads[t] && r.lo < r.hi && ro[t].meets(r)) return I2S_E_BAD_ARG;
+    }
+    if (heads[0] && heads[1] && !apart(*q_out, q_heads, *k_out, k_heads, rows, head_dim)) return I2S_E_BAD_ARG;
     if (!(same[0] && same[1])) {
         for (int t = 0; t < 2; ++t) {
             if (heads[t] == 0) continue;
             if (ro[t].meets(ri[t])) return I2S_E_BAD_ARG;
-            if (heads[1 - t] && (ro[t].meets(ri[1 - t]) || ro[t].meets(ro[1 - t]))) return I2S_E_BAD_ARG;
+            if (heads[1 - t] && ro[t].meets(ri[1 - t])) return I2S_E_BAD_ARG;
         }
     }
     if (q_heads) a.q = rows_of(*q), a.q_out = rows_of(*q_out), a.gamma_q = gamma_q;

@@ -53,6 +53,8 @@ constexpr int kCtasPerSm = 3;
 constexpr int kMaxCtas = 152 * kCtasPerSm;   // two or three times as many, each with less: 2 to 13 % slower (64 sequences)
 constexpr int kStart = 14;            // blocks that an item's start counts for
 constexpr int kGrain = kStart + 2 * kWarps;   // places (of the order below) that a CTA takes at least: below, a join costs more than it saves
+constexpr int kPartBlocks = 256;     // of a part: a warp sums at most 64 blocks (1024 tokens) in its accumulators,
+                                     // which the tensor core cuts off at 2^-24 of the sum at each step
 constexpr float kBias = 8.0f;
 constexpr float kSlack = 6.0f;       // m follows the maximum only when it grows by more
 constexpr int kNoBlock = -0x7fffffff - 1;    // in the place of a page: past the part's blocks
@@ -164,7 +166,9 @@ __global__ void __launch_bounds__(kvd::kThreads, kvd::kCtasPerSm)
     __shared__ volatile struct {
         long long row0;
         int seq, head, item_x, b_at, blocks, count, rows, x, x_seq;
+        int first, more;   // the CTA's first block of the item; whether it has more of it after the part
     } s_part;
+    __shared__ float s_so_far[2][2][kRows];   // maxima and l of an item's parts before, by turns
     __shared__ float s_m[kWarps][kRows], s_l[kWarps][kRows];
 
     const Kv8View& c = a.c;
@@ -221,8 +225,10 @@ __global__ void __launch_bounds__(kvd::kThreads, kvd::kCtasPerSm)
     const uint32_t ring = smem_addr(smem) + warp * kRing;
     uint8_t* ring_p = smem + warp * kRing;
 
+    bool resumes = false;   // the part goes on with the item of the one before
+    int turn = 0;
     while (x < x_end) {
-        // The part of [x, x_end) that lies in one item.
+        // The part of [x, x_end) that lies in one item, or the first kPartBlocks of it.
         Kv8Seq sq = kv8_seq(c, s);
         Span sp = span_of(a, sq);
         while (s + 1 < c.seqs && x >= x_seq + sp.cost() * c.heads) {
@@ -234,19 +240,20 @@ __global__ void __launch_bounds__(kvd::kThreads, kvd::kCtasPerSm)
         const int cost = sp.cost(), blocks = sp.hi - sp.lo;
         const int head = (x - x_seq) / cost;
         const int item_x = x_seq + head * cost;
-        const int b_at = max(x - item_x - kStart, 0), count = min(cost, x_end - item_x) - kStart - b_at;
-        const int x_next = min(item_x + cost, x_end);
-        if (count <= 0) {   // only places before the blocks
-            x = x_next;
+        const int b_at = max(x - item_x - kStart, 0), left = min(cost, x_end - item_x) - kStart - b_at;
+        if (left <= 0) {   // only places before the blocks
+            x = min(item_x + cost, x_end);
             continue;
         }
+        const int count = min(left, kPartBlocks);
         const int b_lo = sp.lo + b_at, rows = min(sq.n * group, kRows);
         // What only the join and the next part need waits in shared memory: the
         // registers are the accumulators'.
         if (tid == 0) {
             s_part.seq = s, s_part.head = head, s_part.item_x = item_x, s_part.b_at = b_at, s_part.blocks = blocks;
             s_part.count = count, s_part.rows = rows, s_part.row0 = sq.row0;
-            s_part.x = x_next, s_part.x_seq = x_seq;
+            s_part.x = item_x + kStart + b_at + count, s_part.x_seq = x_seq, s_part.more = left > count;
+            if (!resumes) s_part.first = b_at;
         }
 
         // Query row g of the item, on its way while the pages are looked up.
@@ -485,8 +492,8 @@ __global__ void __launch_bounds__(kvd::kThreads, kvd::kCtasPerSm)
             s_l[warp][g] = l;
         }
         __syncthreads();
-        const bool whole = s_part.count == s_part.blocks;
-        float* slot = slots + (long long)(2 * cta + (s_part.b_at == 0 ? 1 : 0)) * slot_floats<D>();
+        const bool some_more = s_part.more, whole = s_part.first == 0 && s_part.b_at + s_part.count == s_part.blocks;
+        float* slot = slots + (long long)(2 * cta + (s_part.first == 0 ? 1 : 0)) * slot_floats<D>();
         for (int i = tid; i < s_part.rows * (D / 4); i += kThreads) {
             const int r = i / (D / 4), q4 = i % (D / 4);
             float top = s_m[0][r];
@@ -506,6 +513,19 @@ __global__ void __launch_bounds__(kvd::kThreads, kvd::kCtasPerSm)
                 sum.x = fmaf(v.x, k, sum.x), sum.y = fmaf(v.y, k, sum.y);
                 sum.z = fmaf(v.z, k, sum.z), sum.w = fmaf(v.w, k, sum.w);
                 total = fmaf(lw, k, total);
+            }
+            if (resumes) {   // and what the item's parts before have left in the slot
+                const float pm = s_so_far[turn ^ 1][0][r], nm = fmaxf(pm, top);
+                const float k0 = pm == -INFINITY ? 0.0f : ex2(pm - nm), k1 = top == -INFINITY ? 0.0f : ex2(top - nm);
+                const float4 v = *reinterpret_cast<const float4*>(slot + r * D + 4 * q4);
+                sum.x = fmaf(v.x, k0, sum.x * k1), sum.y = fmaf(v.y, k0, sum.y * k1);
+                sum.z = fmaf(v.z, k0, sum.z * k1), sum.w = fmaf(v.w, k0, sum.w * k1);
+                total = fmaf(s_so_far[turn ^ 1][1][r], k0, total * k1);
+                top = nm;
+            }
+            if (q4 == 0 && some_more) {
+                s_so_far[turn][0][r] = top;
+                s_so_far[turn][1][r] = total;
             }
             if (whole) {
                 const float inv = total == 0.0f ? 0.0f : __fdiv_rn(1.0f, total);
@@ -533,6 +553,8 @@ __global__ void __launch_bounds__(kvd::kThreads, kvd::kCtasPerSm)
         s = s_part.seq;
         x = s_part.x;
         x_seq = s_part.x_seq;
+        resumes = some_more;
+        turn ^= 1;
         __syncthreads();
     }
 }

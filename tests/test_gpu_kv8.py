@@ -154,6 +154,28 @@ def test_read_is_the_codes_times_the_scales(i2s, case, layout, dtype):
     assert st.batch.status() == 0
 
 
+def test_many_sequences_in_the_rows_of_one_block(i2s):
+    """More sequence starts than a CTA looks at at once, empty sequences among them, beside long ones."""
+    news = [1] * 50 + [0] * 40 + [1, 0, 2] * 20 + [70] + [0, 1] * 30 + [16, 33]
+    lens = [n + (7 * i) % 41 for i, n in enumerate(news)]
+    st = Setup(i2s, 2, 64, 16, lens, news, seed=8, pad_rows=7)
+    rng = np.random.default_rng(9)
+    k, kf = rows_tensor(rng, st.rows, 2, 64, "f32", std=2.0)
+    v, vf = rows_tensor(rng, st.rows, 2, 64, "f32", std=2.0)
+    i2s.kv8_write(st.cache, st.batch, k, v)
+    ref.write(st.pool, st.table, lens, st.row_start, kf, vf)
+    same_bits(st.pool_now(), st.pool.bytes())
+    kv = torch.full((st.rows, 4, 64), 3.0, device="cuda")   # read back into slices of one row
+    i2s.kv8_read(st.cache, st.batch, kv[:, :2], kv[:, 2:])
+    for which in (0, 1):
+        want = np.full((st.rows, 2, 64), 3.0, np.float32)
+        for s, n in enumerate(news):
+            x, _ = ref.cached(st.pool, st.table, s, lens[s], which)
+            want[st.row_start[s]:st.row_start[s + 1]] = x[lens[s] - n:].astype(np.float32)
+        same_bits(kv[:, 2 * which:2 * which + 2].cpu().numpy(), want)
+    assert st.batch.status() == 0
+
+
 def test_tokens_appended_one_by_one_match_the_definition(i2s):
     """40 single-token appends: every block grows through all its fill levels."""
     kv, dim, page, total = 2, 128, 32, 40
@@ -467,6 +489,67 @@ def test_attention_replayed_from_a_graph_after_the_lengths_change(i2s, new):
         torch.cuda.synchronize()
         assert torch.equal(one.out, two.out)
         compare_attention(st, qf, "f32", True, 0, 128 ** -0.5, one.out, lse, one.out.cpu().numpy())
+
+
+@pytest.mark.parametrize("news", [1, 3, 9])
+def test_attention_of_thousands_of_sequences(i2s, news):
+    """More sequences than a CTA has threads, in every kernel's own count of them."""
+    seqs = 1500
+    lens = [news + (13 * i) % 60 for i in range(seqs)]
+    lens[700], lens[1499] = 900, 2000
+    st = Setup(i2s, 1, 64, 16, lens, [news if i % 7 else 0 for i in range(seqs)], seed=news)
+    q, qf = rows_tensor(np.random.default_rng(1), st.rows, 2, 64, "f32")
+    check_attention(i2s, st, q, qf, "f32")
+    assert st.batch.status() == 0
+
+
+@pytest.mark.parametrize("new", [1, 130])
+def test_attention_over_many_tokens_stays_exact(i2s, new):
+    """Long sums: of 20000 tokens, within the bound that does not grow as fast as they do."""
+    st = Setup(i2s, 1, 128, 64, [20000], [new], seed=3)
+    q, qf = rows_tensor(np.random.default_rng(1), st.rows, 1 if new > 1 else 2, 128, "f32")
+    out = i2s.kv8_attention(st.cache, st.batch, q).cpu().numpy().astype(np.float64)
+    want = ref.attention(st.pool, st.table, st.lens, st.row_start, qf, float(np.float32(128 ** -0.5)), True, 0)[0]
+    # 22-bit operands; a chain of at most 512 tokens (64 tensor-core steps, each cut below 2^-23 of the sum): 2^-17
+    assert np.linalg.norm(out - want) <= 2.0 ** -17 * np.linalg.norm(want)
+
+
+def test_attention_of_shares_longer_than_one_accumulation(i2s):
+    """So many tokens that a CTA's share of an item exceeds the 256 blocks it sums at once: sequences that read the same
+    32768 tokens, 8 x 8 x 2048 blocks over 456 CTAs. Against 64 bits for the first and the last sequence."""
+    heads, dim, seqs, n = 8, 64, 8, 32768
+    st = Setup(i2s, heads, dim, 256, [n], [1], seed=77)
+    table = st.batch.page_table.expand(seqs, -1).contiguous()
+    starts = torch.arange(seqs + 1, dtype=torch.int32, device="cuda")
+    lens = [n - 3 * i for i in range(seqs)]
+    batch = i2s.Kv8Batch(starts, torch.tensor(lens, dtype=torch.int32, device="cuda"), table, rows=seqs, max_rows=1)
+    q, qf = rows_tensor(np.random.default_rng(5), seqs, heads, dim, "f32")
+    out = i2s.kv8_attention(st.cache, batch, q).cpu().numpy().astype(np.float64)
+    assert batch.status() == 0
+    for s in (0, seqs - 1):
+        want = ref.attention(st.pool, st.table, [lens[s]], [0, 1], qf[s:s + 1], float(np.float32(dim ** -0.5)), True, 0)[0]
+        assert np.linalg.norm(out[s] - want[0]) <= 2.0 ** -17 * np.linalg.norm(want)
+
+
+def test_attention_on_two_streams_at_once(i2s):
+    calls, wants = [], []
+    for new, seed in ((1, 41), (40, 42)):
+        st = Setup(i2s, 2, 128, 32, [3000, 500], [new, new], seed=seed)
+        q, qf = rows_tensor(np.random.default_rng(seed), st.rows, 4, 128, "f32")
+        call = i2s.Kv8Attention(st.cache, st.batch, q)
+        call()
+        calls.append(call)
+        wants.append(call.out.clone())
+    streams = [torch.cuda.Stream() for _ in calls]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for call, stream in zip(calls, streams):
+            with torch.cuda.stream(stream):
+                call.out.fill_(-1.0)
+                call()
+    torch.cuda.synchronize()
+    for call, want in zip(calls, wants):
+        assert torch.equal(call.out, want)
 
 
 def test_attention_is_the_same_every_time(i2s):

@@ -81,7 +81,7 @@ def test_cache_and_batch_refusals(i2s, name):
 @pytest.mark.parametrize("name", ["write", "read", "attend"])
 def test_blocks_are_counted_in_32_bits(i2s, name):
     c = Call(i2s)
-    c.batch.seqs, c.batch.table_width = 1000, (1 << 35) // (1000 * 2 * 64) + 1
+    c.batch.seqs, c.batch.table_width = 1000, (1 << 34) // (1000 * 2 * 64) + 1
     assert getattr(c, name)() == c.E["I2S_E_BAD_SHAPE"]
 
 
@@ -89,7 +89,8 @@ def test_blocks_are_counted_in_32_bits(i2s, name):
 def test_row_tensor_refusals(i2s, name, inputs, outputs):
     for t in list(inputs) + list(outputs):
         for want, field, value in (("I2S_E_NULL_PTR", "data", None), ("I2S_E_MISALIGNED", "data", 20 * A + 8),
-                                   ("I2S_E_BAD_SHAPE", "row_stride", -256), ("I2S_E_MISALIGNED", "head_stride", 130),
+                                   ("I2S_E_BAD_SHAPE", "row_stride", -256), ("I2S_E_BAD_SHAPE", "row_stride", 1 << 38),
+                                   ("I2S_E_MISALIGNED", "head_stride", 130),
                                    ("I2S_E_BAD_ARG", "dtype", 3), ("I2S_E_BAD_ARG", "dtype", -1)):
             c = Call(i2s)
             setattr(getattr(c, t), field, value)
@@ -123,6 +124,14 @@ def test_overlaps_are_refused(i2s):
     c = Call(i2s)
     c.cache.pages = 5 * A - 1024   # the pool over the status word
     assert c.write() == c.E["I2S_E_BAD_ARG"]
+
+
+def test_read_outputs_may_be_slices_of_one_row(i2s):
+    for off, ok in ((256, True), (128, False), (384, False), (-256, True)):
+        c = Call(i2s)
+        c.k = i2s.kv8_rows(8 * A, 512, 128, 0)
+        c.v = i2s.kv8_rows(8 * A + 4 * off, 512, 128, 0)
+        assert (c.read() == c.E["I2S_E_BAD_ARG"]) == (not ok), off
 
 
 def test_attention_refusals(i2s):
@@ -168,8 +177,16 @@ def test_norm_rope_refusals(i2s):
                      ("I2S_E_BAD_ARG", {"q_out": rows(A + 64, 768, 128, 0)}),          # over its input, not in place
                      ("I2S_E_BAD_ARG", {"q_out": rows(3 * A, 768, 128, 0)}),           # over the other input
                      ("I2S_E_BAD_ARG", {"q_out": rows(4 * A, 768, 128, 0)}),           # over the other output
-                     ("I2S_E_BAD_ARG", {"q_out": rows(2 * A, 128, 128, 0)})):          # onto itself
+                     ("I2S_E_BAD_ARG", {"q_out": rows(2 * A, 128, 128, 0)}),           # onto itself
+                     ("I2S_E_BAD_ARG", {"gq": 2 * A + 16}), ("I2S_E_BAD_ARG", {"pos": 4 * A + 64}),
+                     ("I2S_E_BAD_ARG", {"turns": 2 * A})):                             # over a small operand
         assert call(**kw) == E[want], kw
+    # in place in fused rows: slices of one row, but not the same or crossing ones
+    fused = rows(A, 1280, 128, 0)
+    for off, ok in ((768, True), (640, False), (0, False), (1152, False)):
+        k = rows(A + 4 * off, 1280, 128, 0)
+        got = call(q=fused, q_out=fused, k=k, k_out=k)
+        assert (got == E["I2S_E_BAD_ARG"]) == (not ok), off
 
 
 def test_rope_turns(i2s):
