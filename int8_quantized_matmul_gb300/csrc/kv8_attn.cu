@@ -76,8 +76,7 @@ static cudaError_t launch_tile(const Kv8AttnArgs& a, const TileCut& t, const Kv8
     static std::atomic<unsigned long long> ready{0};   // a bit per device
     const cudaError_t e = allow_smem(k_kv8_tile<DT, D, MT>, bytes, ready);
     if (e != cudaSuccess) return e;
-    k_kv8_tile<DT, D, MT><<<dim3((unsigned)t.items, (unsigned)t.splits), kvt::kThreads, bytes, s>>>(a, parts);
-    return cudaGetLastError();
+    return launch_pdl(k_kv8_tile<DT, D, MT>, dim3((unsigned)t.items, (unsigned)t.splits), dim3(kvt::kThreads), bytes, s, a, parts);
 }
 
 template <int DT, int D>
@@ -89,8 +88,7 @@ static cudaError_t launch_decode(const Kv8AttnArgs& a, void* ws, cudaStream_t s)
     cudaError_t e = allow_smem(k_kv8_decode<DT, D>, bytes, ready);
     if (e != cudaSuccess) return e;
     const int ctas = std::min(kvd::kMaxCtas, kvd::kCtasPerSm * device_sm_count());
-    k_kv8_decode<DT, D><<<ctas, kvd::kThreads, bytes, s>>>(a, slots, plan);
-    e = cudaGetLastError();
+    e = launch_pdl(k_kv8_decode<DT, D>, dim3((unsigned)ctas), dim3(kvd::kThreads), bytes, s, a, slots, plan);
     if (e != cudaSuccess) return e;
     const dim3 grid((unsigned)(a.c.seqs * a.c.heads), (unsigned)(a.c.max_rows * (a.q_heads / a.c.heads)));
     const bool many = (a.c.width << a.c.page_shift) >= 64 * kvd::kGrain * kKvBlock;   // parts an item may have

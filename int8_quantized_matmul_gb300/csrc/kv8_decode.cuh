@@ -175,6 +175,8 @@ __global__ void __launch_bounds__(kvd::kThreads, kvd::kCtasPerSm)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const int group = a.q_heads / c.heads;
 
+    pdl_wait();
+
     // This CTA's range of blocks: the block counts of all sequences summed,
     // each thread a run of them.
     const int per = (c.seqs + kThreads - 1) / kThreads;

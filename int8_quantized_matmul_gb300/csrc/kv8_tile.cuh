@@ -86,7 +86,7 @@ __host__ __device__ constexpr int operand_bytes() { return kTileKv * D * 2; }
 
 struct Shared {
     uint64_t full[kSlots], empty[kSlots], cfull[kConsts], bfull[kConsts];
-    uint64_t q_ready[2], s_full[2], p_ready[2][2], pv_done[2], drained[2], m_ready[2], l_ready;
+    uint64_t q_ready[2], s_full[2], p_ready[2][2], pv_done[2], drained[2], m_ready[2][4], l_ready;
     float2 cst[kConsts][kBlocks];   // K scale, log2 of the V scale
     float inv[kConsts][kBlocks];    // inverse of the V scale
     const uint8_t* block[kConsts][kBlocks];   // K codes of a tile's blocks, null where there is none
@@ -325,6 +325,7 @@ __global__ void __launch_bounds__(kvt::kThreads, 1)
     const int tid = threadIdx.x, warp = (int)__reduce_max_sync(0xffffffffu, (unsigned)tid >> 5), lane = tid & 31;
     const int group = a.q_heads / c.heads;
     constexpr int kRowsItem = MT * kTileQ;
+    pdl_wait();
 
     int* const scan = reinterpret_cast<int*>(S.rows);   // until the barrier below
     // The item: heads vary fastest, the last rows of the last sequence come
@@ -378,7 +379,7 @@ __global__ void __launch_bounds__(kvt::kThreads, 1)
             tc::mbar_init(&S.p_ready[i][1], 128);
             tc::mbar_init(&S.pv_done[i], 1);
             tc::mbar_init(&S.drained[i], 1);
-            tc::mbar_init(&S.m_ready[i], 256);
+            for (int w = 0; w < 4; ++w) tc::mbar_init(&S.m_ready[i][w], 64);   // the two warps that share 32 rows
         }
         tc::mbar_init(&S.l_ready, 256);
         S.abort = 0;
@@ -530,8 +531,8 @@ __global__ void __launch_bounds__(kvt::kThreads, 1)
                 top = masked ? fmaxf(piece_top<true>(xa, mul, cst, lo, hi), piece_top<true>(xb, mul, cst + 2, lo - 32, hi - 32))
                              : fmaxf(piece_top<false>(xa, mul, cst, lo, hi), piece_top<false>(xb, mul, cst + 2, lo - 32, hi - 32));
                 S.rows[bf][h][r] = top;
-                tc::mbar_arrive(&S.m_ready[bf]);
-                if (!wait(&S.m_ready[bf], ph)) break;
+                tc::mbar_arrive(&S.m_ready[bf][warp & 3]);
+                if (!wait(&S.m_ready[bf][warp & 3], ph)) break;
                 top = fmaxf(top, S.rows[bf][h ^ 1][r]);
             }
             const bool grown = __any_sync(0xffffffffu, top > m + kSlack);
