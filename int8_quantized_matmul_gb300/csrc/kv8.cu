@@ -286,7 +286,7 @@ struct Kv8RopeArgs {
 };
 
 template <int DT, int D, int VPL, bool NORM>
-__global__ void __launch_bounds__(kRopeWarps * 32, DT == kKvF32 ? 9 : 1) k_kv8_norm_rope(const __grid_constant__ Kv8RopeArgs a) {
+__global__ void __launch_bounds__(kRopeWarps * 32, DT == kKvF32 ? 9 : 6) k_kv8_norm_rope(const __grid_constant__ Kv8RopeArgs a) {
     using T = typename Kv8T<DT>::type;
     constexpr int LPH = D / VPL, HPW = 32 / LPH;   // lanes of a head, heads of a warp's load
     __shared__ float2 s_cs[kRopeWarps][D / 2];
@@ -299,16 +299,19 @@ __global__ void __launch_bounds__(kRopeWarps * 32, DT == kKvF32 ? 9 : 1) k_kv8_n
     const bool turned = d0 < a.rot, low = d0 < half;
     const int peer = (lane & ~(LPH - 1)) + (turned ? (low ? sub + half / VPL : sub - half / VPL) : sub);
 
+    // Where head h of this lane's values would lie in each tensor: K's heads count on from Q's.
+    const T* const q_at = static_cast<const T*>(a.q.data) + row * a.q.row_stride + d0;
+    const T* const k_at = static_cast<const T*>(a.k.data) + row * a.k.row_stride - a.q_heads * a.k.head_stride + d0;
+    T* const q_to = static_cast<T*>(a.q_out.data) + row * a.q_out.row_stride + d0;
+    T* const k_to = static_cast<T*>(a.k_out.data) + row * a.k_out.row_stride - a.q_heads * a.k_out.head_stride + d0;
     // loads of the first heads, on their way while the angles are computed
     Kv8Vec<T, VPL> raw[kRopeBatch];
     auto fetch = [&](int h0) {
 #pragma unroll
         for (int b = 0; b < kRopeBatch; ++b) {
             const int h = min(h0 + b * HPW + lane / LPH, h_end - 1);
-            const bool is_k = h >= a.q_heads;
-            const Kv8Rows& in = is_k ? a.k : a.q;
-            raw[b] = *reinterpret_cast<const Kv8Vec<T, VPL>*>(static_cast<const T*>(in.data) + row * in.row_stride +
-                                                             (is_k ? h - a.q_heads : h) * in.head_stride + d0);
+            raw[b] = *reinterpret_cast<const Kv8Vec<T, VPL>*>(h >= a.q_heads ? k_at + h * a.k.head_stride
+                                                                             : q_at + h * a.q.head_stride);
         }
     };
     const int h_lo = blockIdx.y * a.heads_per_warp;
@@ -352,7 +355,7 @@ __global__ void __launch_bounds__(kRopeWarps * 32, DT == kKvF32 ? 9 : 1) k_kv8_n
 #pragma unroll
                 for (int o = LPH / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
                 if (is_k ? a.gamma_k != nullptr : a.gamma_q != nullptr) {
-                    const float rs = __fdiv_rn(1.0f, __fsqrt_rn(ss * (1.0f / D) + a.eps));
+                    const float rs = rsqrtf(fmaf(ss, 1.0f / D, a.eps));
 #pragma unroll
                     for (int j = 0; j < VPL; ++j) x[j] = x[j] * rs * (is_k ? gk[j] : gq[j]);
                 }
@@ -374,9 +377,7 @@ __global__ void __launch_bounds__(kRopeWarps * 32, DT == kKvF32 ? 9 : 1) k_kv8_n
                 }
             }
             if (h < h_end) {
-                const Kv8Rows& out = is_k ? a.k_out : a.q_out;
-                kv8_store<T, VPL>(static_cast<T*>(out.data) + row * out.row_stride +
-                                      (is_k ? h - a.q_heads : h) * out.head_stride + d0, x);
+                kv8_store<T, VPL>(is_k ? k_to + h * a.k_out.head_stride : q_to + h * a.q_out.head_stride, x);
             }
         }
     }

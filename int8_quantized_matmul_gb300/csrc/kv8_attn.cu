@@ -92,7 +92,7 @@ static cudaError_t launch_decode(const Kv8AttnArgs& a, void* ws, cudaStream_t s)
     if (e != cudaSuccess) return e;
     const dim3 grid((unsigned)(a.c.seqs * a.c.heads), (unsigned)(a.c.max_rows * (a.q_heads / a.c.heads)));
     const bool many = (a.c.width << a.c.page_shift) >= 64 * kvd::kGrain * kKvBlock;   // parts an item may have
-    const int warps = many && (long long)grid.x * grid.y <= 4 * kSms ? kJoinWarps : kJoinWarps / 4;
+    const int warps = many && (long long)grid.x * grid.y <= 4 * kSms ? kJoinWarps : kJoinWarps / 8;
     return launch_pdl(k_kv8_join<DT, D>, grid, dim3(warps * 32), 0, s, a, slots, plan);
 }
 
