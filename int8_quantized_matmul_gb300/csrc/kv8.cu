@@ -68,6 +68,10 @@ __device__ __forceinline__ void find_rows(const Kv8View& c, long long row0, RowP
 // A unit belongs to the first row that the batch has in the block (its
 // leader); a CTA takes N consecutive rows, and its warps share leaders x heads
 // x {K, V} with those of the same rows in the grid's second dimension.
+//
+// Measured (one GB300): 9001 rows of 8 heads of 128, 16 bits, 55 MB: 16 us in a
+// stream with the read after it, 21 us under a cold cache, its issue slots half
+// taken (9 operations per value); 64 single tokens 4.9 us, a launch's latency.
 // ---------------------------------------------------------------------------
 constexpr int kWriteWarps = 4;
 
@@ -183,7 +187,10 @@ __global__ void __launch_bounds__(kWriteWarps * 32) k_kv8_write(const __grid_con
 // Read. A CTA takes N rows. A lane turns as many codes into values as 16 bytes
 // hold; a warp has LPW lines (a row's D codes of one head, K or V) at once and
 // keeps them from row to row, kReadBatch rows on their way, so that what an
-// address takes per row is one addition to where the row's token lies.
+// address takes per row is one addition to where the row's token lies. (With an
+// address of its own for each line: 30 us instead of 15.)
+//
+// Measured: the rows written above read back, 55 MB: 15 us, 3.7 TB/s.
 // ---------------------------------------------------------------------------
 constexpr int kReadWarps = 8;
 constexpr int kReadBatch = 4;
@@ -268,6 +275,10 @@ __global__ void __launch_bounds__(kReadWarps * 32) k_kv8_read(const __grid_const
 // way. The partner of value d in a pair (d, d + rot/2) is in another lane, at a
 // whole number of lanes if rot/2 is a multiple of VPL; 16-bit rows with another
 // rot take 8 bytes per lane.
+//
+// Measured: 8000 rows of 24 heads of 128, F32, 197 MB: 34.3 us, 5.7 TB/s (86 % of
+// a copy); 5003 16-bit rows of 36 heads, half of each turned, 92 MB: 18.2 us, 5.1
+// TB/s; 8 rows 4.3 us, the call. Loads in flight per warp 2/3/4/6: 43/40/39/41 us.
 // ---------------------------------------------------------------------------
 constexpr int kRopeWarps = 4;
 constexpr int kRopeBatch = 4;

@@ -31,12 +31,19 @@
 // for two codes) and subtracting 1152.
 //
 // Work split. The blocks of all items, item by item, are cut into equal
-// contiguous ranges, one per CTA, so ragged lengths leave no SM idle; kRounds
-// times as many CTAs as fit at once, so the SMs that memory serves faster take
-// more of them. The four warps of a CTA take the blocks of a range
-// in turn, two at a time, each with its own ring filled by cp.async a pair ahead
-// and its own running maximum, and join through shared memory. An item cut between
-// CTAs leaves its parts (O, m, l in F32) in the workspace for k_kv8_join.
+// contiguous ranges, one per CTA, so ragged lengths leave no SM idle. The four
+// warps of a CTA take the blocks of a range in turn, two at a time, each with
+// its own ring filled by cp.async a pair ahead and its own running maximum, and
+// join through shared memory. An item cut between CTAs leaves its parts (O, m, l
+// in F32) in the workspace for k_kv8_join.
+//
+// Measured (one GB300): 64 sequences of 500 to 4100 tokens, 16 heads over 8 of
+// 128, F32, 315 MB: 64.9 us, 4.9 TB/s, 73 % of a copy's rate; of those the kernel
+// takes 60, the rest is the join. What bounds it: starting an item (3 us of loads
+// that wait for each other) and instructions, 51 % of the issue slots with three
+// warps per scheduler (of 467 per block about 220 turn codes into f16 operands).
+// One token over 131001 tokens, 12 heads over 2, bf16, 67 MB: 24.5 us, a third of
+// it the join of 228 parts. One token over 75 tokens: 6.8 us, two launches.
 #pragma once
 
 #include "kv8.cuh"
