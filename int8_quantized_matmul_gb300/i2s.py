@@ -705,8 +705,9 @@ class _Kv8Call:
     def _bind(self, name, device, *args):
         torch = _torch()
         self._name, self._fn, self._index = name, getattr(_L, name), device.index
-        # structures as references made once, the stream as the number torch keeps
-        self._args = tuple(ctypes.byref(x) if isinstance(x, ctypes.Structure) else x for x in args)
+        # structures as references and numbers as C values, made once; the stream as the number torch keeps
+        self._args = tuple(ctypes.byref(x) if isinstance(x, ctypes.Structure) else x if x is None else t(x)
+                           for x, t in zip(args, self._fn.argtypes))
         self._hold = args
         self._device, self._stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
 
