@@ -708,7 +708,8 @@ int kv8_norm_rope(const kv8_rows* q, const kv8_rows* q_out, int q_heads, const f
  * taken to be as kv8_write makes them: not negative, V's from 2^-40 to 2^86, or
  * NaN, which makes the rows that see the block NaN and no others.
  * q, out    rows x q_heads x head_dim, one dtype; q_heads a multiple of
- *           cache->heads, at most 64 times it. out overlaps no other operand.
+ *           cache->heads, at most 64 times it, and max_rows * q_heads / heads
+ *           below 2^30. out overlaps no other operand.
  * lse       device F32 [rows x q_heads] or NULL: log(sum_j exp(softmax_scale *
  *           q . K_j)), -infinity for a row that sees no token.
  * ws        device workspace of at least kv8_attention_workspace() bytes, 256-byte

@@ -495,6 +495,12 @@ int check_batch(const kv8_cache* c, const kv8_batch* b, Kv8View& w, Range& pool)
     return I2S_OK;
 }
 
+// A sequence's query rows for one KV head are counted in 32 bits.
+bool q_heads_ok(int q_heads, const Kv8View& c) {
+    return q_heads >= 1 && q_heads % c.heads == 0 && q_heads / c.heads <= 64 &&
+           (int64_t)c.max_rows * (q_heads / c.heads) < (int64_t)1 << 30;
+}
+
 // What a batch's operators only read besides the pool and the row tensors.
 bool meets_batch(const Range& r, const kv8_batch& b) {
     return r.meets(bytes_at(b.row_start, 4 * ((size_t)b.seqs + 1))) || r.meets(bytes_at(b.kv_len, 4 * (size_t)b.seqs)) ||
@@ -700,8 +706,7 @@ int kv8_norm_rope(const kv8_rows* q, const kv8_rows* q_out, int q_heads, const f
 
 size_t kv8_attention_workspace(const kv8_cache* cache, const kv8_batch* batch, int q_heads) {
     Kv8View c;
-    if (!cache || !batch || check_sizes(*cache, *batch, c) != I2S_OK) return 0;
-    if (q_heads < 1 || q_heads % c.heads || q_heads / c.heads > 64) return 0;
+    if (!cache || !batch || check_sizes(*cache, *batch, c) != I2S_OK || !q_heads_ok(q_heads, c)) return 0;
     return kv8_attention_ws(c, q_heads);
 }
 
@@ -713,7 +718,7 @@ int kv8_attention(const kv8_cache* cache, const kv8_batch* batch, const kv8_rows
     int r = check_batch(cache, batch, a.c, pool);
     if (r) return r;
     if (!ws) return I2S_E_NULL_PTR;
-    if (q_heads < 1 || q_heads % a.c.heads || q_heads / a.c.heads > 64) return I2S_E_BAD_SHAPE;
+    if (!q_heads_ok(q_heads, a.c)) return I2S_E_BAD_SHAPE;
     if ((r = check_rows(q, a.c.rows, q_heads, a.c.dim, false)) || (r = check_rows(out, a.c.rows, q_heads, a.c.dim, true)))
         return r;
     if (q->dtype != out->dtype || (flags & ~KV8_CAUSAL) || window < 0 || (window && !(flags & KV8_CAUSAL)) ||
@@ -742,12 +747,14 @@ int kv8_attention(const kv8_cache* cache, const kv8_batch* batch, const kv8_rows
 
 int kv8_read_status(int32_t* status, int32_t* bits, i2s_stream_t stream) {
     if (!status) return I2S_E_NULL_PTR;
-    if (cudaStreamSynchronize(stream) != cudaSuccess) return I2S_E_CUDA;
+    // on `stream`, so that the calls queued there later find the word cleared
     int32_t word = 0;
-    if (cudaMemcpy(&word, status, 4, cudaMemcpyDeviceToHost) != cudaSuccess) return I2S_E_CUDA;
+    if (cudaMemcpyAsync(&word, status, 4, cudaMemcpyDeviceToHost, stream) != cudaSuccess ||
+        cudaStreamSynchronize(stream) != cudaSuccess)
+        return I2S_E_CUDA;
     if (bits) *bits = word;
     if (word == 0) return I2S_OK;
-    if (cudaMemset(status, 0, 4) != cudaSuccess) return I2S_E_CUDA;
+    if (cudaMemsetAsync(status, 0, 4, stream) != cudaSuccess) return I2S_E_CUDA;
     return (word & KV8_TIMEOUT) ? I2S_E_DEVICE_TIMEOUT : I2S_E_BAD_ARG;
 }
 

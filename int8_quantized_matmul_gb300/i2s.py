@@ -759,6 +759,8 @@ class Kv8Batch:
         self.row_start, self.kv_len, self.page_table = row_start, kv_len, page_table
         self.seqs, self.rows, self.device = seqs, int(rows), page_table.device
         self.max_rows = int(max_rows if max_rows is not None else rows)
+        if not (-2 ** 31 <= self.max_rows < 2 ** 31 and -2 ** 63 <= self.rows < 2 ** 63):
+            raise ValueError("rows or max_rows out of range")
         self.word = torch.zeros(1, dtype=torch.int32, device=page_table.device)
         self.struct = kv8_batch(_dptr(row_start), _dptr(kv_len), _dptr(page_table), _dptr(self.word), self.rows, width,
                                 seqs, self.max_rows)
@@ -840,6 +842,8 @@ class Kv8Attention(_Kv8Call):
         if out is None:
             out = torch.empty(tuple(q.shape), dtype=q.dtype, device=q.device)
         qr, orows = (_kv8_same(cache, t, batch.rows, heads, name) for name, t in (("q", q), ("out", out)))
+        if not -2 ** 31 <= int(window) < 2 ** 31:
+            raise ValueError("window out of range")
         if lse is not None and (lse.dtype != torch.float32 or tuple(lse.shape) != (batch.rows, heads) or
                                 lse.device != cache.device):
             raise ValueError(f"lse: expected float32 {(batch.rows, heads)} on {cache.device}")

@@ -616,3 +616,29 @@ def test_projections_norm_rope_write_attention_together(i2s, new):
     assert (kept - k).abs().max().item() <= 1.01 * step
     want = i2s.w8a8_mul_mat_packed(wo, bo, hidden, qh * dim, out.view(M, -1))[0]
     assert torch.equal(y, want)
+
+
+def test_window_that_a_c_integer_does_not_hold_is_refused(i2s):
+    st = Setup(i2s, 2, 64, 16, [20], [1], seed=23)
+    q = torch.zeros((1, 4, 64), device="cuda")
+    for window in (1 << 32, -(1 << 32)):
+        with pytest.raises(ValueError, match="out of range"):
+            i2s.Kv8Attention(st.cache, st.batch, q, window=window)
+    i2s.Kv8Attention(st.cache, st.batch, q, window=(1 << 31) - 1)()
+    assert st.batch.status() == 0
+
+
+def test_status_is_read_and_cleared_in_the_order_of_its_stream(i2s):
+    st = Setup(i2s, 2, 64, 16, [40], [1], seed=24)
+    q = torch.zeros((1, 4, 64), device="cuda")
+    call = i2s.Kv8Attention(st.cache, st.batch, q)
+    st.batch.page_table[0, 1] = -1
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        for _ in range(20):   # each call's bit is there, none of an earlier one's, none cleared late
+            call()
+            assert st.batch.status() == i2s.KV8_BAD_PAGE
+            call()
+            assert st.batch.status() == i2s.KV8_BAD_PAGE
+            assert st.batch.status() == 0

@@ -226,3 +226,20 @@ def test_reference_quantizer_and_round_trip():
     ref.write(pool, [[0, 1]], [20], [0, 20], x, x)   # at once: half a step
     back, _ = ref.cached(pool, [[0, 1]], 0, 20, 0)
     assert np.abs(back[:16] - x[:16]).max() <= 0.5001 * np.abs(x[:16]).max() / 127
+
+
+def test_query_rows_of_a_head_are_counted_in_32_bits(i2s):
+    c = Call(i2s)
+    c.batch.rows, c.q_heads = 1 << 25, 128
+    c.batch.max_rows = (1 << 24) - 1
+    assert c.need() > 0
+    c.batch.max_rows = 1 << 24   # times 64 query heads: 2^30
+    assert c.need() == 0 and c.attend() == c.E["I2S_E_BAD_SHAPE"]
+
+
+def test_sizes_that_a_c_integer_does_not_hold_are_refused(i2s):
+    torch = pytest.importorskip("torch")
+    starts, lens, table = (torch.zeros(n, dtype=torch.int32) for n in (3, 2, 8))
+    for kw in ({"rows": 10, "max_rows": (1 << 32) + 4}, {"rows": (1 << 64) + 10, "max_rows": 4}):
+        with pytest.raises(ValueError, match="out of range"):
+            i2s.Kv8Batch(starts, lens, table.view(2, 4), **kw)
