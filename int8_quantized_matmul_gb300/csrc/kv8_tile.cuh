@@ -24,7 +24,9 @@
 // Accumulation. The tensor core cuts each MMA's sum off below 2^-24 of the
 // accumulator, always towards zero, so a long chain loses: over 4000 tokens
 // 9e-6 of O was measured. For F32 rows O is therefore moved every kChain tiles
-// into a running sum that is added to with rounding (1e-6).
+// into a running sum that is added to with rounding: 7.5e-7 over 8000 tokens,
+// where plain F32 is off by 1.4e-6. The weights are made before that, while the
+// P V that it waits for runs (8000-token prompt: 461 us, the other way 472).
 //
 // Two shapes, with two warpgroups of softmax threads, one thread per row (TMEM
 // lane). MT = 2 (16-bit rows, where there are enough of them): two query tiles,
@@ -54,13 +56,14 @@
 // turns. Every wait is bounded; one that runs out sets KV8_TIMEOUT.
 //
 // Measured (one GB300): an 8000-token causal prompt, 16 heads over 8 of 128, F32
-// rows: 445 us, 589 TFLOP/s of 4 D per visible pair, 1.2 PFLOP/s of MMAs with the
-// second parts (31 and 61 % of the bf16 rate measured). Per tile of 128 x 128 it
-// takes 3400 cycles: from S to the maxima 800, to the weights 1600, P V after the
-// last of them 1000, Q K^T of the next but one 1250. Chunks of prompts with bf16
-// rows: 180 us, 3250 cycles per step of two query tiles, of which the 32 MMAs
-// (128 x 128 x 16, K and Q from shared memory) take 2600. 512 tokens of 12 heads
-// over 2: 16.8 us; 1 to 6 drafted tokens of 16 sequences, window 2048: 22.6 us.
+// rows: 461 us, 568 TFLOP/s of 4 D per visible pair, 1.1 PFLOP/s of MMAs with the
+// second parts (30 and 59 % of the bf16 rate measured). Per tile of 128 x 128 it
+// takes 3500 cycles (3400 if O moved every four tiles): from S to the maxima 800,
+// to the weights 1600, P V after the last of them 1000, Q K^T of the next but one
+// 1250. Chunks of prompts with bf16 rows: 180 us, 3250 cycles per step of two query
+// tiles, of which the 32 MMAs (128 x 128 x 16, K and Q from shared memory) take
+// 2600. 512 tokens of 12 heads over 2: 16.8 us; 1 to 6 drafted tokens of 16
+// sequences, window 2048: 22.8 us.
 #pragma once
 
 #include "kv8_decode.cuh"
@@ -79,7 +82,10 @@ constexpr int kIssueWarp = 12;
 constexpr float kBias = 8.0f;
 constexpr float kSlack = 6.0f;
 constexpr long long kWait = 2000000000LL;
-constexpr int kChain = 4;            // tiles summed in one accumulator (F32 rows)
+// Tiles summed in one accumulator (F32 rows). An 8000-token prompt takes 461, 439
+// and 439 us with 2, 3 and 4; over 70 batches of mixed sizes the error is at most
+// 1.4, 1.6 and over 1.6 times that of plain F32.
+constexpr int kChain = 2;
 constexpr int kSlots = 4;            // operands of the ring: K of a tile takes the place of K two tiles before,
                                      // free since that tile's S, not that of a V, free only after its weights
 constexpr int kStages = 2;           // int8 operands on their way: K and V of a tile
@@ -553,6 +559,19 @@ __global__ void __launch_bounds__(kvt::kThreads, 1)
                 m = nm;
                 l *= keep;
             }
+            const float sub = m == -INFINITY ? 0.0f : m - kBias;
+            const float* inv = &S.inv[cs][4 * h];
+            uint32_t wa[2][16], wb[2][16];   // MT = 1: the weights, made while the P V before this one runs
+            if (MT == 1) {
+                if (masked) piece_weights<true, PARTS>(xa, mul, sub, cst, inv, lo, hi, l, wa[0], wa[1]);
+                else piece_weights<false, PARTS>(xa, mul, sub, cst, inv, lo, hi, l, wa[0], wa[1]);
+                if (masked) piece_weights<true, PARTS>(xb, mul, sub, cst + 2, inv + 2, lo - 32, hi - 32, l, wb[0], wb[1]);
+                else piece_weights<false, PARTS>(xb, mul, sub, cst + 2, inv + 2, lo - 32, hi - 32, l, wb[0], wb[1]);
+                tc::tmem_st_32x32b_x16(ts, wa[0]);
+                if (PARTS == 2) tc::tmem_st_32x32b_x16(ts + 16u, wa[1]);
+                tc::tmem_st_32x32b_x16(ts + 32u, wb[0]);
+                if (PARTS == 2) tc::tmem_st_32x32b_x16(ts + 48u, wb[1]);
+            }
             if ((grown && j > 0) || flush) {
                 // O holds the tiles before this one; with two S buffers their MMAs may still run
                 if (MT == 1) {
@@ -589,21 +608,10 @@ __global__ void __launch_bounds__(kvt::kThreads, 1)
                     }
                 }
             }
-            const float sub = m == -INFINITY ? 0.0f : m - kBias;
-            const float* inv = &S.inv[cs][4 * h];
             if (MT == 2) {
                 if (masked) tile_weights<true, PARTS>(ts, mul, sub, cst, inv, lo, hi, l, S.p_ready[bf]);
                 else tile_weights<false, PARTS>(ts, mul, sub, cst, inv, lo, hi, l, S.p_ready[bf]);
             } else {
-                uint32_t hi16[16], lo16[16];
-                if (masked) piece_weights<true, PARTS>(xa, mul, sub, cst, inv, lo, hi, l, hi16, lo16);
-                else piece_weights<false, PARTS>(xa, mul, sub, cst, inv, lo, hi, l, hi16, lo16);
-                tc::tmem_st_32x32b_x16(ts, hi16);
-                if (PARTS == 2) tc::tmem_st_32x32b_x16(ts + 16u, lo16);
-                if (masked) piece_weights<true, PARTS>(xb, mul, sub, cst + 2, inv + 2, lo - 32, hi - 32, l, hi16, lo16);
-                else piece_weights<false, PARTS>(xb, mul, sub, cst + 2, inv + 2, lo - 32, hi - 32, l, hi16, lo16);
-                tc::tmem_st_32x32b_x16(ts + 32u, hi16);
-                if (PARTS == 2) tc::tmem_st_32x32b_x16(ts + 48u, lo16);
                 tc::tmem_st_wait();
                 tc::tc_fence_before();
                 tc::mbar_arrive(&S.p_ready[bf][h]);

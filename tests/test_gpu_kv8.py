@@ -642,3 +642,22 @@ def test_status_is_read_and_cleared_in_the_order_of_its_stream(i2s):
             call()
             assert st.batch.status() == i2s.KV8_BAD_PAGE
             assert st.batch.status() == 0
+
+
+@pytest.mark.parametrize("dim,group", [(64, 8), (128, 7), (128, 1)])
+def test_f32_sums_of_one_sign_lose_little(i2s, dim, group):
+    """Values of one sign, weights nearly alike: what a tensor core cuts off is always of that sign too, on average
+    2^-24 of the sum (a unit in the last place is between 2^-24 and 2^-23 of it, and half of one is lost) at each of the
+    32 steps (16 of two parts) of the 256 tokens summed at a time, when the sum is on average half of what it will be:
+    32 * 2^-24 / 2 = 9.5e-7. Logits below 0.1 * 4, weights and the other sums add less than 2^-23 by their norm."""
+    lens, news = [700, 990, 512], [60, 75, 47]
+    st = Setup(i2s, 2, dim, 64, lens, news, seed=41)
+    st.pool.codes[:, :, 1] = np.maximum(np.abs(st.pool.codes[:, :, 1]), 1)
+    st.data.view(-1).copy_(torch.from_numpy(st.pool.bytes()))
+    rng = np.random.default_rng(5)
+    q, qf = rows_tensor(rng, st.rows, 2 * group, dim, "f32", std=0.1)
+    got = i2s.kv8_attention(st.cache, st.batch, q).cpu().numpy()
+    assert st.batch.status() == 0
+    want = ref.attention(st.pool, st.table, lens, st.row_start, qf, dim ** -0.5, True, 0)[0]
+    off = np.linalg.norm(got - want) / np.linalg.norm(want)
+    assert off <= 32 * 2.0 ** -25 + 2.0 ** -23, off
