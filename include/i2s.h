@@ -704,7 +704,9 @@ int kv8_norm_rope(const kv8_rows* q, const kv8_rows* q_out, int q_heads, const f
  * With KV8_CAUSAL only j <= the row's position, and with window > 0 (KV8_CAUSAL
  * only) j > position - window. A row that sees no token has a zero output.
  * Softmax statistics and sums are binary32; F32 queries and the weights of F32
- * rows enter the tensor cores as two f16 parts each (22 bits). Scales are
+ * rows enter the tensor cores as two f16 parts each (22 bits). The sums of
+ * 16-bit rows may lose 2e-9 of themselves for each token seen, less than the
+ * rounding of the output up to 200000 tokens. Scales are
  * taken to be as kv8_write makes them: not negative, V's from 2^-40 to 2^86, or
  * NaN, which makes the rows that see the block NaN and no others.
  * q, out    rows x q_heads x head_dim, one dtype; q_heads a multiple of
