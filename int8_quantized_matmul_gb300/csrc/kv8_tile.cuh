@@ -801,10 +801,16 @@ __global__ void __launch_bounds__(kvt::kThreads, 1)
                 const uint64_t vd = sdesc_sw128_mnmajor(tc::smem_u32(sKV + slot * kOp));
                 const uint32_t ts = tm + (uint32_t)(bf * kTileKv);
                 const bool first = kChained ? j % kChain == 0 : j == 0;
+                // With one query tile each warpgroup scales or moves its own half of O's columns before it hands on its
+                // weights, and every MMA writes all of them: none starts before both have.
+                if (MT == 1 && (!wait(&S.p_ready[bf][0], ph) || !wait(&S.p_ready[bf][1], ph))) return false;
+                if (MT == 1) tc::tc_fence_after();
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
-                    if (!wait(&S.p_ready[bf][half], ph)) return false;
-                    tc::tc_fence_after();
+                    if (MT == 2) {   // a half as soon as it is there: the thread that made it has scaled all of its row of O
+                        if (!wait(&S.p_ready[bf][half], ph)) return false;
+                        tc::tc_fence_after();
+                    }
 #pragma unroll
                     for (int pt = PARTS - 1; pt >= 0; --pt)
 #pragma unroll

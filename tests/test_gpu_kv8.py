@@ -661,3 +661,33 @@ def test_f32_sums_of_one_sign_lose_little(i2s, dim, group):
     want = ref.attention(st.pool, st.table, lens, st.row_start, qf, dim ** -0.5, True, 0)[0]
     off = np.linalg.norm(got - want) / np.linalg.norm(want)
     assert off <= 32 * 2.0 ** -25 + 2.0 ** -23, off
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_sums_moved_while_the_maxima_grow(i2s, dim, dtype):
+    """Logits that grow along the cache at another rate in each row, so O is scaled and moved at nearly every one of 16
+    tiles: right, and the same bits every time. Two warpgroups share a query tile here (F32 rows always do, 16-bit rows
+    where there are fewer than 152 pairs of tiles: 4 heads x 16)."""
+    kv, group, n = 4, 2, 2048
+    st = Setup(i2s, kv, dim, 64, [n], [n], seed=dim)
+    rng = np.random.default_rng(8)
+    sign = np.where(rng.random(dim) < 0.5, -1, 1)
+    for b in range(n // 16):   # keys along one direction, longer and longer
+        p, sub = st.table[0][b * 16 // 64], b * 16 % 64 // 16
+        at = slice(sub * 16, sub * 16 + 16)
+        st.pool.codes[p, :, 0, at] = np.clip(100 * sign + rng.normal(0, 10, (kv, 16, dim)), -127, 127).astype(np.int8)
+        st.pool.scales[p, :, 0, sub] = 1e-4 * (b + 1)
+    st.data.view(-1).copy_(torch.from_numpy(st.pool.bytes()))
+    st.pool = ref.Pool(st.pool.bytes(), kv, dim, 64)
+    # a row's logits reach 0 to 80 (115 in powers of two): up to 7 a tile, past the slack of 6
+    x = rng.random((n, kv * group, 1)) * sign * (80 / (dim * 100 * 1e-4 * 128) * dim ** 0.5) + rng.normal(0, 0.05, (n, kv * group, dim))
+    q = torch.from_numpy(x.astype(np.float32)).to(DTYPES[dtype]).cuda()
+    check_attention(i2s, st, q, q.float().cpu().numpy(), dtype)
+    assert st.batch.status() == 0
+    call = i2s.Kv8Attention(st.cache, st.batch, q)
+    call()
+    first = call.out.clone()
+    for _ in range(30):
+        call()
+        assert torch.equal(first, call.out)
