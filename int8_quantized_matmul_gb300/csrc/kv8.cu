@@ -43,10 +43,10 @@ __device__ __forceinline__ void find_rows(const Kv8View& c, long long row0, RowP
         while (n < 31 && p.start[n + 1] <= row) ++n;
         const int s = n == 31 ? kv8_seq_of_row(c, row) : s0 + n;
         p.seq[tid] = -1;
-        if (upto > 0 && s >= 0 && s < c.seqs && row < c.rows) {
+        if (s >= 0 && s < c.seqs && row < c.rows) {
             const Kv8Seq q = kv8_seq(c, s);
             const long long i = row - q.row0, pos = (long long)q.len - q.n + i;
-            if (i >= 0 && i < q.n) {
+            if (i >= 0 && i < q.n) {   // not a row before the first sequence's, whose s is 0
                 if (pos < 0) atomicOr(c.status, kKvBadLength);
                 p.seq[tid] = pos < 0 ? -1 : s;
                 p.pos[tid] = (int)pos;

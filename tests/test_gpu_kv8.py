@@ -691,3 +691,37 @@ def test_sums_moved_while_the_maxima_grow(i2s, dim, dtype):
     for _ in range(30):
         call()
         assert torch.equal(first, call.out)
+
+
+@pytest.mark.parametrize("news", [[3, 1, 15], [40, 0, 100], [1] * 40])
+@pytest.mark.parametrize("lead", [1, 5, 17, 70])
+def test_a_batch_whose_first_row_is_not_row_0(i2s, lead, news):
+    """row_start[0] > 0, as a slice of a larger batch's row starts has it: the rows before belong to no sequence, those
+    behind are written, read and attended with as if they began at 0. Batches of few rows per sequence and of many."""
+    kv, dim = 2, 64
+    lens = [n + (11 * i) % 37 for i, n in enumerate(news)]
+    st = Setup(i2s, kv, dim, 32, lens, news, seed=lead, pad_rows=3)
+    rng = np.random.default_rng(lead)
+    starts, rows = st.row_start + np.int32(lead), st.rows + lead
+    batch = i2s.Kv8Batch(torch.from_numpy(starts).cuda(), st.batch.kv_len, st.batch.page_table, rows=rows,
+                         max_rows=max(news))
+    k, kf = rows_tensor(rng, rows, kv, dim, "f32", std=2.0)
+    v, vf = rows_tensor(rng, rows, kv, dim, "f32", std=2.0)
+    i2s.kv8_write(st.cache, batch, k, v)
+    ref.write(st.pool, st.table, lens, starts, kf, vf)
+    same_bits(st.pool_now(), st.pool.bytes())
+    back = [torch.full((rows, kv, dim), 3.0, device="cuda") for _ in range(2)]
+    i2s.kv8_read(st.cache, batch, *back)
+    for which in (0, 1):
+        want = np.full((rows, kv, dim), 3.0, np.float32)
+        for s, n in enumerate(news):
+            x, _ = ref.cached(st.pool, st.table, s, lens[s], which)
+            want[starts[s]:starts[s + 1]] = x[lens[s] - n:].astype(np.float32)
+        same_bits(back[which].cpu().numpy(), want)
+    q, qf = rows_tensor(rng, rows, 4, dim, "f32")
+    out, lse = torch.full((rows, 4, dim), 7.0, device="cuda"), torch.full((rows, 4), 99.0, device="cuda")
+    i2s.kv8_attention(st.cache, batch, q, out=out, lse=lse)
+    assert (out[:lead] == 7.0).all() and (lse[:lead] == 99.0).all()
+    compare_attention(st, qf[lead:], "f32", True, 0, dim ** -0.5, out[lead:], lse[lead:],
+                      np.full((st.rows, 4, dim), 7.0, np.float32))
+    assert batch.status() == 0
