@@ -704,9 +704,16 @@ int kv8_norm_rope(const kv8_rows* q, const kv8_rows* q_out, int q_heads, const f
  * With KV8_CAUSAL only j <= the row's position, and with window > 0 (KV8_CAUSAL
  * only) j > position - window. A row that sees no token has a zero output.
  * Softmax statistics and sums are binary32; F32 queries and the weights of F32
- * rows enter the tensor cores as two f16 parts each (22 bits). The sums of
- * 16-bit rows may lose 2e-9 of themselves for each token seen, less than the
- * rounding of the output up to 200000 tokens. Scales are
+ * rows enter the tensor cores as two f16 parts each (22 bits). 16-bit queries
+ * are exact there; the weights of 16-bit rows have two parts where max_rows *
+ * q_heads / heads is at most 8 and are rounded once to f16 where it is more.
+ * The tensor cores cut their sums off, always towards zero: about 2e-7 of the
+ * sum for each 16 tokens added to it. Partial sums of at most 1024 tokens (256
+ * of F32 rows where max_rows * q_heads / heads is above 8) are then added with
+ * rounding; measured for F32 rows: 1e-6, or 9e-6 behind a first token that has
+ * nearly all the weight. Many 16-bit rows over at most 8192 (f16) or 65536 (bf16)
+ * tokens (of the table, or window + max_rows) are summed at once, which loses
+ * less than half of the least half step of the output. Scales are
  * taken to be as kv8_write makes them: not negative, V's from 2^-40 to 2^86, or
  * NaN, which makes the rows that see the block NaN and no others.
  * q, out    rows x q_heads x head_dim, one dtype; q_heads a multiple of

@@ -19,10 +19,13 @@ static bool is_decode(int heads, int q_heads, int max_rows) {
 static size_t plan_bytes(int heads, int seqs) { return ((size_t)heads * seqs * sizeof(Kv8Plan) + 255) / 256 * 256; }
 
 // How the tile kernel cuts its work. Two query tiles per CTA read the cache half
-// as often and overlap each other's softmax and MMAs, but leave SMs idle where
-// there are too few of them; so do long caches under few rows, whose tiles are
-// then split between CTAs (as many as fill the SMs, four tiles of the cache at least each: with two, 512
-// tokens under 12 heads of 2 took 21.4 us, unsplit 18.5).
+// as often and overlap each other's softmax and MMAs (chunks of prompts, 16-bit:
+// 181 us, with one 203), but leave SMs idle where there are too few of them, and
+// lose too much over a long cache, whose length the host knows from the window or
+// the table's width. Long caches under few rows leave SMs idle too: their tiles
+// are then split between CTAs (as many as fill the SMs, four tiles of the cache
+// at least each: with two, 512 tokens under 12 heads of 2 took 21.4 us, unsplit
+// 18.5).
 struct TileCut {
     int query_tiles;   // of a CTA
     int items;         // grid: heads times a bound on the row tiles
@@ -34,11 +37,11 @@ static TileCut tile_cut(int dtype, int heads, int q_heads, int seqs, int max_row
     const long long rows_head = rows * (q_heads / heads);
     const int some = (int)std::min<long long>(seqs, rows);   // sequences that may have rows
     TileCut t;
-    t.query_tiles = dtype != kKvF32 && heads * ((rows_head + 255) / 256) >= kSms ? 2 : 1;
+    if (window) tokens = std::min<long long>(tokens, (long long)window + max_rows);
+    t.query_tiles = dtype != kKvF32 && heads * ((rows_head + 255) / 256) >= kSms && tokens <= kvt::longest(dtype) ? 2 : 1;
     const int per = t.query_tiles * kvt::kTileQ;
     t.items = (int)(heads * (rows_head / per + some));
     const long long likely = heads * std::max<long long>((rows_head + per - 1) / per, some);
-    if (window) tokens = std::min<long long>(tokens, (long long)window + max_rows);
     const long long tiles = (tokens + kvt::kTileKv - 1) / kvt::kTileKv;
     t.splits = (int)std::max<long long>(1, std::min<long long>(kSms / likely, tiles / 4));
     return t;
@@ -49,8 +52,8 @@ static size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 size_t kv8_attention_ws(const Kv8View& c, int q_heads) {
     if (is_decode(c.heads, q_heads, c.max_rows))
         return plan_bytes(c.heads, c.seqs) + (size_t)2 * kvd::kMaxCtas * kvd::kRows * (c.dim + 2) * sizeof(float);
-    size_t need = 256;   // for either dtype
-    for (int dtype : {kKvF32, kKvF16}) {
+    size_t need = 256;   // for every dtype
+    for (int dtype : {kKvF32, kKvF16, kKvBf16}) {
         const TileCut t = tile_cut(dtype, c.heads, q_heads, c.seqs, c.max_rows, c.rows, c.width << c.page_shift, 0);
         const size_t units = (size_t)t.splits * c.rows * q_heads;
         if (t.splits > 1) need = std::max(need, up256(units * c.dim * sizeof(float)) + 2 * up256(units * sizeof(float)));

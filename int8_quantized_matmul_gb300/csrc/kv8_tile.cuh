@@ -21,14 +21,18 @@
 // one part after the scaling (f16's 11 bits hold bf16's 8), and their weights
 // are rounded once to f16, 2^-12, below the half step of the output.
 //
-// Accumulation. The tensor core cuts each MMA's sum off below 2^-24 of the
-// accumulator, always towards zero, so a long chain loses: over 4000 tokens
-// 9e-6 of O was measured. For F32 rows O is therefore moved every kChain tiles
-// into a running sum that is added to with rounding: 7.5e-7 over 8000 tokens,
-// where plain F32 is off by 1.4e-6. The weights are made before that, while the
-// P V that it waits for runs (8000-token prompt: 461 us, the other way 472). 16-bit
-// rows keep one chain: 2e-9 a token, 3e-4 over 131000, below their half step (f16's
-// is 5e-4), and the second query tile has the columns.
+// Accumulation. The tensor core cuts off what it adds, always towards zero: with
+// values of one sign a step of 16 tokens loses 1.8e-7 of the sum as it then is,
+// 2.5 units of its last place (as if each of the 16 products lost half of a
+// quarter unit and the sum half of one; five units would be the most). A long
+// chain therefore loses, the more so if its first tokens have most of the weight.
+// With one query tile O is moved every kChain tiles into a running sum that is
+// added to with rounding: F32 rows 7.5e-7 over 8000 tokens, where plain F32 is
+// off by 1.4e-6 (5.5e-6 and 3.7e-6 behind a token of 2^16 times the others'
+// weight). The weights are made before that, while the P V that it waits for
+// runs (8000-token prompt: 459 us, the other way 472). Two query tiles leave no
+// columns for such a sum, so they are taken only for caches over which the one
+// chain loses at most half of the least half step of the rows' type: longest().
 //
 // Two shapes, with two warpgroups of softmax threads, one thread per row (TMEM
 // lane). MT = 2 (16-bit rows, where there are enough of them): two query tiles,
@@ -49,7 +53,7 @@
 //   warp 14         looks up the pages and the scales of the tiles to come
 // TMEM (512 columns): S (2 x 128 columns of f32), overwritten in place by the
 // weights (32 columns of S become 16 of high and 16 of low parts), and O (MT x D,
-// for F32 rows and the running sum). K is the K-major operand [token][d]; V with
+// for MT = 1 and the running sum). K is the K-major operand [token][d]; V with
 // the same bytes is the MN-major operand.
 //
 // A slot of the ring holds K or V of one tile, in the order K0 V0 K1 V1 ...
@@ -84,10 +88,13 @@ constexpr int kIssueWarp = 12;
 constexpr float kBias = 8.0f;
 constexpr float kSlack = 6.0f;
 constexpr long long kWait = 2000000000LL;
-// Tiles summed in one accumulator (F32 rows). An 8000-token prompt takes 461, 439
+// Tiles summed in one accumulator, where there is a running sum. F32 rows: an 8000-token prompt takes 459, 439
 // and 439 us with 2, 3 and 4; over 70 batches of mixed sizes the error is at most
-// 1.4, 1.6 and over 1.6 times that of plain F32.
-constexpr int kChain = 2;
+// 1.4, 1.6 and over 1.6 times that of plain F32. 16-bit rows: 64 steps lose 1.5e-5, a sixteenth of f16's least half step.
+constexpr int kChainF32 = 2, kChain16 = 8;
+// Tokens that 16-bit rows may sum in one accumulator: 2^-22 of the sum for each 16, up to half of the least half step
+// (2^-12 f16, 2^-9 bf16).
+constexpr long long longest(int dtype) { return dtype == kKvF16 ? 8192 : 65536; }
 constexpr int kSlots = 4;            // operands of the ring: K of a tile takes the place of K two tiles before,
                                      // free since that tile's S, not that of a V, free only after its weights
 constexpr int kStages = 2;           // int8 operands on their way: K and V of a tile
@@ -328,7 +335,8 @@ __global__ void __launch_bounds__(kvt::kThreads, 1)
     using T = typename Kv8T<DT>::type;
     constexpr int PARTS = DT == kKvF32 ? 2 : 1;
     static_assert(MT == 1 || PARTS == 1, "F32 rows need the columns of the second tile for their running sum");
-    constexpr bool kChained = PARTS == 2;
+    constexpr bool kChained = MT == 1;
+    constexpr int kChain = PARTS == 2 ? kChainF32 : kChain16;
     constexpr int kOp = operand_bytes<D>();
     constexpr int kKSteps = D / 16, kVSteps = kTileKv / 16;
     extern __shared__ __align__(1024) uint8_t smem_tile[];

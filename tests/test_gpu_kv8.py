@@ -725,3 +725,43 @@ def test_a_batch_whose_first_row_is_not_row_0(i2s, lead, news):
     compare_attention(st, qf[lead:], "f32", True, 0, dim ** -0.5, out[lead:], lse[lead:],
                       np.full((st.rows, 4, dim), 7.0, np.float32))
     assert batch.status() == 0
+
+
+@pytest.mark.parametrize("n,new,group,kv", [(32768, 320, 4, 8), (16000, 512, 5, 16), (8192, 512, 5, 16)])
+def test_f16_sums_behind_a_heavy_first_token_lose_little(i2s, n, new, group, kv):
+    """Values of one sign, and a first token with 2^16 times the weight of each of the others: the sum has most of its
+    size from the start, so whatever the tensor core cuts off later, always towards zero, is cut from all of it. A step
+    of 16 tokens aligns 16 products with the sum and cuts each at a quarter of the sum's unit, and the new sum at one:
+    on average 16 / 8 + 1 / 2 = 2.5 units, of at most 2^-23 of the sum. With one query tile in a CTA (the first case has
+    too few for two, the second too many tokens for f16) the sums are moved every 1024 tokens, and of the later chains
+    each is small: 64 steps. The third has two (16 heads x 10 pairs, 8192 tokens), whose sums are not moved: 512 steps.
+    The mean of the relative errors shows it below the rounding of the outputs, at most 2^-11 each, 5 standard deviations
+    of whose mean over 655360 and more outputs are below 2e-6; the weights' rounding (f16) averages out over the tokens
+    likewise, the first one's weight is a power of two. What is left is rounding in F32: together below 2^-17."""
+    dim = 64
+    st = Setup(i2s, kv, dim, 64, [n], [new], seed=n)
+    rng = np.random.default_rng(6)
+    pages = st.table[0][st.table[0] >= 0]
+    st.pool.codes[:, :, 1] = rng.integers(40, 128, st.pool.codes[:, :, 1].shape)
+    st.pool.codes[:, :, 0] = rng.integers(-3, 4, st.pool.codes[:, :, 0].shape)
+    st.pool.scales[pages] = 0.01
+    first = st.pool.codes[pages[0], :, 0]
+    first[:, 0] = 110
+    st.pool.codes[pages[0], :, 0] = first
+    st.data.view(-1).copy_(torch.from_numpy(st.pool.bytes()))
+    x = 16 * np.log(2.0) * dim ** 0.5 / (dim * 110 * 0.01) + rng.normal(0, 0.02, (new, kv * group, dim))
+    q = torch.from_numpy(x).to(torch.float16).cuda()
+    got = i2s.kv8_attention(st.cache, st.batch, q).double()
+    assert st.batch.status() == 0
+    off = 0.0
+    pos = torch.arange(n - new, n, device="cuda")[:, None]
+    for h in range(kv):
+        k, v = (torch.from_numpy(np.ascontiguousarray(
+            st.pool.codes[pages, h, which].reshape(-1, dim)[:n])).cuda().double() * np.float64(np.float32(0.01)) for which in (0, 1))
+        for g in range(h * group, h * group + group):
+            score = q[:, g].double() @ k.T * np.float64(np.float32(dim ** -0.5))
+            score = score.masked_fill_(torch.arange(n, device="cuda") > pos, float("-inf"))
+            want = torch.softmax(score, -1) @ v
+            off += ((got[:, g] - want) / want).mean().item() / (kv * group)
+    steps = 512 if n == 8192 else 64
+    assert abs(off) <= steps * 2.5 * 2.0 ** -23 + 2.0 ** -17, off
