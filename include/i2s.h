@@ -714,8 +714,10 @@ int kv8_norm_rope(const kv8_rows* q, const kv8_rows* q_out, int q_heads, const f
  * nearly all the weight. Many 16-bit rows over at most 8192 (f16) or 65536 (bf16)
  * tokens (of the table, or window + max_rows) are summed at once, which loses
  * less than half of the least half step of the output. Scales are
- * taken to be as kv8_write makes them: not negative, V's from 2^-40 to 2^86, or
- * NaN, which makes the rows that see the block NaN and no others.
+ * taken to be not negative, as kv8_write makes them, and V's at least 2^-40.
+ * One that is NaN, and a V scale of 2^87 or more (kv8_write makes those of values
+ * from 127 * 2^87 on), makes the rows that see its block NaN and no others; their
+ * lse may be NaN with them.
  * q, out    rows x q_heads x head_dim, one dtype; q_heads a multiple of
  *           cache->heads, at most 64 times it, and max_rows * q_heads / heads
  *           below 2^30. out overlaps no other operand.

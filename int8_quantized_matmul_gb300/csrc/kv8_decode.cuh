@@ -65,7 +65,10 @@ constexpr int kPartBlocks = 256;     // of a part: a warp sums at most 64 blocks
 constexpr float kBias = 8.0f;
 constexpr float kSlack = 6.0f;       // m follows the maximum only when it grows by more
 constexpr int kNoBlock = -0x7fffffff - 1;    // in the place of a page: past the part's blocks
+// V scales: below 2^87 their exponents lie within 126 of each other, so that the share of l of a block with a small scale
+// does not vanish beside the weights of one with a large scale (ex2 ends at 2^-126). From there on a scale is NaN.
 constexpr int kExpLo = -40, kExpHi = 86;
+constexpr float kScaleEnd = 0x1p87f;
 
 template <int D>
 __host__ __device__ constexpr int block_bytes() { return 2 * kKvBlock * D + 16; }   // codes, the two scales
@@ -404,7 +407,7 @@ __global__ void __launch_bounds__(kvd::kThreads, kvd::kCtasPerSm)
                     const float2 kv = *reinterpret_cast<const float2*>(st + b * kBlk + 2 * kKvBlock * D);   // the two scales
                     const int e = min(max((int)(__float_as_uint(kv.y) >> 23 & 255) - 127, kExpLo), kExpHi);
                     un[b] = __int_as_float((127 - e) << 23);
-                    f[b] = kv.y * un[b];
+                    f[b] = kv.y < kScaleEnd ? kv.y * un[b] : __int_as_float(0x7fc00000);
                     const float xm = mul * kv.x, ef = (float)e;
 #pragma unroll
                     for (int j = 0; j < 4; ++j)

@@ -889,6 +889,7 @@ __global__ void __launch_bounds__(kvt::kThreads, 1)
                         sc.x = *reinterpret_cast<const float*>(slab + kv8_scale_off(c, 0, tok));
                         sc.y = *reinterpret_cast<const float*>(slab + kv8_scale_off(c, 1, tok));
                         if (sc.y < 0x1p-40f) sc.y = 0x1p-40f;   // a scale that no written block has (0 among them)
+                        if (sc.y >= kvd::kScaleEnd) sc.y = __int_as_float(0x7fc00000);
                     } else if (page != kNoBlock) {
                         atomicOr(c.status, kKvBadPage);
                     }

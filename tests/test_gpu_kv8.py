@@ -765,3 +765,21 @@ def test_f16_sums_behind_a_heavy_first_token_lose_little(i2s, n, new, group, kv)
             off += ((got[:, g] - want) / want).mean().item() / (kv * group)
     steps = 512 if n == 8192 else 64
     assert abs(off) <= steps * 2.5 * 2.0 ** -23 + 2.0 ** -17, off
+
+
+@pytest.mark.parametrize("new", [2, 40])
+def test_value_scales_up_to_2_87_are_used_and_larger_ones_are_nan(i2s, new):
+    """Scales just below 2^87 give right rows in both kernels; from 2^87 on (values from 127 * 2^87, which kv8_write stores) the
+    rows that see the block are NaN, and no others."""
+    st = Setup(i2s, 1, 128, 64, [100], [new], seed=5)
+    first = 100 - new   # row 0 sees tokens 31..first, row 1 32..first + 1
+    page = st.table[0][0]
+    q, qf = rows_tensor(np.random.default_rng(1), st.rows, 2, 128, "f32")
+    st.pool.scales[page, 0, 1, 1] = np.float32(1.99 * 2.0 ** 86)   # tokens 16..31
+    st.data.view(-1).copy_(torch.from_numpy(st.pool.bytes()))
+    check_attention(i2s, st, q, qf, "f32", window=first - 31 + 1)
+    for size in (2.0 ** 87, 1.5 * 2.0 ** 100, 2.0 ** 121):
+        st.pool.scales[page, 0, 1, 1] = np.float32(size)
+        st.data.view(-1).copy_(torch.from_numpy(st.pool.bytes()))
+        out = i2s.kv8_attention(st.cache, st.batch, q, window=first - 31 + 1)
+        assert out[0].isnan().all() and out[1:].isfinite().all()
