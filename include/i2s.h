@@ -726,8 +726,12 @@ int kv8_norm_rope(const kv8_rows* q, const kv8_rows* q_out, int q_heads, const f
  * ws        device workspace of at least kv8_attention_workspace() bytes, 256-byte
  *           aligned, not preserved; calls sharing one are ordered on one stream.
  * More errors: WORKSPACE_TOO_SMALL, BAD_ARG for a window without KV8_CAUSAL or
- * a softmax_scale that is not finite. */
+ * a softmax_scale that is not finite. Rows whose kernel gave up a wait
+ * (KV8_TIMEOUT, after about a second) are NaN. KV8_TEST_STALL is for tests only:
+ * where the tile kernel runs (max_rows * q_heads / heads above 8), its threads
+ * wait for something that never comes, and give up. */
 #define KV8_CAUSAL 1u
+#define KV8_TEST_STALL 0x80000000u
 size_t kv8_attention_workspace(const kv8_cache* cache, const kv8_batch* batch, int q_heads);
 int kv8_attention(const kv8_cache* cache, const kv8_batch* batch, const kv8_rows* q, int q_heads, const kv8_rows* out,
                   float softmax_scale, unsigned flags, int window, float* lse, void* ws, size_t ws_bytes,

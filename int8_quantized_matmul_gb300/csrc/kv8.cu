@@ -721,7 +721,7 @@ int kv8_attention(const kv8_cache* cache, const kv8_batch* batch, const kv8_rows
     if (!q_heads_ok(q_heads, a.c)) return I2S_E_BAD_SHAPE;
     if ((r = check_rows(q, a.c.rows, q_heads, a.c.dim, false)) || (r = check_rows(out, a.c.rows, q_heads, a.c.dim, true)))
         return r;
-    if (q->dtype != out->dtype || (flags & ~KV8_CAUSAL) || window < 0 || (window && !(flags & KV8_CAUSAL)) ||
+    if (q->dtype != out->dtype || (flags & ~(KV8_CAUSAL | KV8_TEST_STALL)) || window < 0 || (window && !(flags & KV8_CAUSAL)) ||
         !std::isfinite(softmax_scale))
         return I2S_E_BAD_ARG;
     if (((uintptr_t)ws & 255) || ((uintptr_t)lse & 3)) return I2S_E_MISALIGNED;
@@ -742,6 +742,7 @@ int kv8_attention(const kv8_cache* cache, const kv8_batch* batch, const kv8_rows
     a.dtype = q->dtype;
     a.causal = (flags & KV8_CAUSAL) != 0;
     a.window = window;
+    a.test_stall = (flags & KV8_TEST_STALL) != 0;
     return cuda_status(launch_kv8_attention(a, ws, stream));
 }
 

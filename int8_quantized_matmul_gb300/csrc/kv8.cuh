@@ -134,6 +134,7 @@ struct Kv8AttnArgs {
     int q_heads, dtype;
     bool causal;
     int window;          // 0: none
+    bool test_stall;     // KV8_TEST_STALL
 };
 size_t kv8_attention_ws(const Kv8View& c, int q_heads);   // sizes only
 cudaError_t launch_kv8_attention(const Kv8AttnArgs& a, void* ws, cudaStream_t s);

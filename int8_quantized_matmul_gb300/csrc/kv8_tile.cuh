@@ -59,7 +59,10 @@
 // A slot of the ring holds K or V of one tile, in the order K0 V0 K1 V1 ...
 // full[] counts the 128 producer threads, empty[] the commits of the MMAs that
 // read it. Barriers that two steps could reach at once exist twice, used by
-// turns. Every wait is bounded; one that runs out sets KV8_TIMEOUT.
+// turns. Every wait is bounded; when one runs out its thread sets KV8_TIMEOUT and
+// the CTA's abort flag, every role leaves its loop, and rows that are not done
+// become NaN (also in a split's parts, so that the join cannot take what the
+// workspace held before).
 //
 // Measured (one GB300): an 8000-token causal prompt, 16 heads over 8 of 128, F32
 // rows: 461 us, 568 TFLOP/s of 4 D per visible pair, 1.1 PFLOP/s of MMAs with the
@@ -638,61 +641,64 @@ __global__ void __launch_bounds__(kvt::kThreads, 1)
             }
             tc::tc_fence_after();
         }
-        if (ok) {
-            const int ti = row / group, hh = head * group + row - ti * group;
-            const long long grow = sq.row0 + ti;
-            const bool split = gridDim.y > 1;
-            const long long part = ((long long)blockIdx.y * c.rows + grow) * a.q_heads + hh;
-            const float inv = split ? 1.0f : (l == 0.0f ? 0.0f : __fdiv_rn(1.0f, l));
-            const bool ran = kChained && n > kChain;
-            const float keep_run = m == -INFINITY ? 1.0f : ex2(m_run - m);
-            if (live && h == 0) {
-                if (split) {
-                    parts.m[part] = m;
-                    parts.l[part] = l;
-                } else if (a.lse != nullptr) {
-                    a.lse[grow * a.q_heads + hh] =
-                        l == 0.0f ? -INFINITY : (log2f(l) + (m - kBias)) * 0.69314718055994530942f;
-                }
+        if (!ok) {
+            __syncwarp();
+            tc::tmem_st_wait();   // what was stored is there before the memory is freed
+            m = -INFINITY, l = __int_as_float(0x7fc00000);
+        }
+        const int ti = row / group, hh = head * group + row - ti * group;
+        const long long grow = sq.row0 + ti;
+        const bool split = gridDim.y > 1;
+        const long long part = ((long long)blockIdx.y * c.rows + grow) * a.q_heads + hh;
+        const float inv = split ? 1.0f : (l == 0.0f ? 0.0f : __fdiv_rn(1.0f, l));
+        const bool ran = kChained && n > kChain;
+        const float keep_run = m == -INFINITY ? 1.0f : ex2(m_run - m);
+        if (live && h == 0) {
+            if (split) {
+                parts.m[part] = m;
+                parts.l[part] = l;
+            } else if (a.lse != nullptr) {
+                a.lse[grow * a.q_heads + hh] =
+                    l == 0.0f ? -INFINITY : (log2f(l) + (m - kBias)) * 0.69314718055994530942f;
             }
-            if (!split || n > 0) {
+        }
+        if (!split || n > 0) {   // (nothing is given up where n is 0)
 #pragma unroll 1
-                for (int ch = 0; ch < OC / 32; ++ch) {
-                    uint32_t v[32];
-                    if (n > 0) {
-                        tc::tmem_ld_32x32b_x32(to_ + (uint32_t)(h * OC + 32 * ch), v);
+            for (int ch = 0; ch < OC / 32; ++ch) {
+                uint32_t v[32];
+                if (ok && n > 0) {
+                    tc::tmem_ld_32x32b_x32(to_ + (uint32_t)(h * OC + 32 * ch), v);
+                    tc::tmem_ld_wait();
+                    if (ran) {
+                        uint32_t w[32];
+                        tc::tmem_ld_32x32b_x32(tr + (uint32_t)(h * OC + 32 * ch), w);
                         tc::tmem_ld_wait();
-                        if (ran) {
-                            uint32_t w[32];
-                            tc::tmem_ld_32x32b_x32(tr + (uint32_t)(h * OC + 32 * ch), w);
-                            tc::tmem_ld_wait();
 #pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                v[i] = __float_as_uint(fmaf(__uint_as_float(w[i]), keep_run, __uint_as_float(v[i])));
-                        }
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) v[i] = 0u;
+                        for (int i = 0; i < 32; ++i)
+                            v[i] = __float_as_uint(fmaf(__uint_as_float(w[i]), keep_run, __uint_as_float(v[i])));
                     }
-                    const int d0 = h * OC + 32 * ch;
-                    if (live && split) {
-                        float* dst = parts.o + part * D + d0;
+                } else {
 #pragma unroll
-                        for (int i = 0; i < 32; i += 4)
-                            *reinterpret_cast<uint4*>(dst + i) = make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-                    } else if (live) {
-                        T* dst = static_cast<T*>(a.out.data) + grow * a.out.row_stride + hh * a.out.head_stride + d0;
-                        constexpr int W = 16 / sizeof(T);
-#pragma unroll
-                        for (int i = 0; i < 32; i += W) {
-                            float y[W];
-#pragma unroll
-                            for (int k = 0; k < W; ++k) y[k] = __uint_as_float(v[i + k]) * inv;
-                            kv8_store<T, W>(dst + i, y);
-                        }
-                    }
-                    __syncwarp();
+                    for (int i = 0; i < 32; ++i) v[i] = ok ? 0u : 0x7fc00000u;
                 }
+                const int d0 = h * OC + 32 * ch;
+                if (live && split) {
+                    float* dst = parts.o + part * D + d0;
+#pragma unroll
+                    for (int i = 0; i < 32; i += 4)
+                        *reinterpret_cast<uint4*>(dst + i) = make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+                } else if (live) {
+                    T* dst = static_cast<T*>(a.out.data) + grow * a.out.row_stride + hh * a.out.head_stride + d0;
+                    constexpr int W = 16 / sizeof(T);
+#pragma unroll
+                    for (int i = 0; i < 32; i += W) {
+                        float y[W];
+#pragma unroll
+                        for (int k = 0; k < W; ++k) y[k] = __uint_as_float(v[i + k]) * inv;
+                        kv8_store<T, W>(dst + i, y);
+                    }
+                }
+                __syncwarp();
             }
         }
         tc::tc_fence_before();
@@ -901,7 +907,8 @@ __global__ void __launch_bounds__(kvt::kThreads, 1)
             int page0 = fetch_page(0), page1 = fetch_page(1), page2 = fetch_page(2);
             float2 sc0 = hand_block(0, page0), sc1 = hand_block(1, page1);
             bool ok = true;
-            for (int j = 0; ok && j < steps; ++j) {
+            // a test lets the others wait for scales that never come
+            for (int j = a.test_stall ? steps : 0; ok && j < steps; ++j) {
                 const int page3 = fetch_page(j + 3);
                 const int i = 2 * j;   // the scales of four tiles before are done with when K's slot is free
                 ok = tc::mbar_wait(&S.empty[i % kSlots], ((i / kSlots) & 1) ^ 1, abort_flag, kWait);

@@ -667,6 +667,7 @@ class W8A8Group:
 KV8_BLOCK = 16
 KV8_MAX_SEQS = 4096
 KV8_CAUSAL = 1
+KV8_TEST_STALL = 1 << 31   # tests only
 KV8_PAIRS_NEXT = 1
 KV8_TIMEOUT, KV8_BAD_ROWS, KV8_BAD_LENGTH, KV8_BAD_PAGE = 1, 2, 4, 8
 

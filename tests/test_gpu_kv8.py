@@ -21,6 +21,8 @@ attention: with A the largest sum |q||k| * scale that the row sees, a logit is
   sum p|v| with the largest |v|; plus half a step of the dtype.
 """
 
+import ctypes
+
 import numpy as np
 import pytest
 
@@ -783,3 +785,37 @@ def test_value_scales_up_to_2_87_are_used_and_larger_ones_are_nan(i2s, new):
         st.data.view(-1).copy_(torch.from_numpy(st.pool.bytes()))
         out = i2s.kv8_attention(st.cache, st.batch, q, window=first - 31 + 1)
         assert out[0].isnan().all() and out[1:].isfinite().all()
+
+
+@pytest.mark.parametrize("kv,group,lens,new,dtype", [
+    (1, 2, [3000], 40, "f32"),        # split along the cache, joined
+    (2, 6, [300, 130], 100, "f32"),   # a CTA for each query tile
+    (2, 6, [300, 130], 100, "bf16"),
+    (8, 8, [1000], 620, "bf16"),      # two query tiles in a CTA
+])
+def test_rows_of_a_kernel_that_gave_up_are_nan(i2s, kv, group, lens, new, dtype):
+    """Waits that nothing ends run out after about a second, with copies and products under way: the call ends, the status
+    says so, its rows are NaN whatever an earlier call left in the workspace, and the next call is right."""
+    st = Setup(i2s, kv, 64, 64, lens, [new] * len(lens), seed=19, pad_rows=2)
+    q, qf = rows_tensor(np.random.default_rng(3), st.rows, kv * group, 64, dtype)
+    lse = torch.zeros((st.rows, kv * group), device="cuda")
+    call = i2s.Kv8Attention(st.cache, st.batch, q, lse=lse)
+    call.out.fill_(7.0)
+    call()
+    assert st.batch.status() == 0
+    want, want_lse = call.out.clone(), lse.clone()
+    args = call._args
+    call._args = args[:6] + (ctypes.c_uint(i2s.KV8_CAUSAL | i2s.KV8_TEST_STALL),) + args[7:]
+    call()
+    with pytest.raises(i2s.I2SError) as e:
+        st.batch.check()
+    assert e.value.status == -6   # I2S_E_DEVICE_TIMEOUT
+    last = st.rows - 2
+    assert call.out[:last].isnan().all() and lse[:last].isnan().all()
+    assert torch.equal(call.out[last:], want[last:])
+    call._args = args
+    for _ in range(2):
+        call()
+        assert torch.equal(call.out, want) and torch.equal(lse, want_lse)
+        assert st.batch.status() == 0
+    compare_attention(st, qf, dtype, True, 0, 64 ** -0.5, call.out, None, call.out.float().cpu().numpy())
