@@ -698,6 +698,12 @@ def _kv8_same(cache, t, rows, heads, what):
     return _kv8_rows(t)
 
 
+def _kv8_here(cache, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != cache.device:
+            raise ValueError(f"{name}: on {t.device}, the cache is on {cache.device}")
+
+
 class _Kv8Call:
     """A call marshalled once, for repeated use and CUDA graph capture. It runs
     on torch's current stream of its tensors' device, which has to be the
@@ -785,6 +791,7 @@ class Kv8Write(_Kv8Call):
 
     def __init__(self, cache, batch, k, v):
         self._keep = (cache, batch, k, v)
+        _kv8_here(cache, batch=batch)
         kr, vr = (_kv8_same(cache, t, batch.rows, cache.heads, name) for name, t in (("k", k), ("v", v)))
         self._bind("kv8_write", cache.device, cache.struct, batch.struct, kr, vr)
 
@@ -794,6 +801,7 @@ class Kv8Read(_Kv8Call):
 
     def __init__(self, cache, batch, k, v):
         self._keep = (cache, batch, k, v)
+        _kv8_here(cache, batch=batch)
         kr, vr = (_kv8_same(cache, t, batch.rows, cache.heads, name) for name, t in (("k", k), ("v", v)))
         self._bind("kv8_read", cache.device, cache.struct, batch.struct, kr, vr)
 
@@ -839,6 +847,7 @@ class Kv8Attention(_Kv8Call):
 
     def __init__(self, cache, batch, q, out=None, scale=None, causal: bool = True, window: int = 0, lse=None, ws=None):
         torch = _torch()
+        _kv8_here(cache, batch=batch, ws=ws)
         heads = q.shape[1]
         if out is None:
             out = torch.empty(tuple(q.shape), dtype=q.dtype, device=q.device)

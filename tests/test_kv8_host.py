@@ -243,3 +243,19 @@ def test_sizes_that_a_c_integer_does_not_hold_are_refused(i2s):
     for kw in ({"rows": 10, "max_rows": (1 << 32) + 4}, {"rows": (1 << 64) + 10, "max_rows": 4}):
         with pytest.raises(ValueError, match="out of range"):
             i2s.Kv8Batch(starts, lens, table.view(2, 4), **kw)
+
+
+def test_a_batch_or_workspace_on_another_device_is_refused(i2s):
+    """Before any pointer is taken: the kernels would follow those of another device."""
+    torch = pytest.importorskip("torch")
+    from types import SimpleNamespace as Some
+    here, there = torch.device("cuda:0"), torch.device("cuda:1")
+    cache = Some(device=here, heads=2, head_dim=64)
+    for call in (i2s.Kv8Write, i2s.Kv8Read):
+        with pytest.raises(ValueError, match="batch: on cuda:1, the cache is on cuda:0"):
+            call(cache, Some(device=there, rows=1), None, None)
+    with pytest.raises(ValueError, match="batch: on cuda:1, the cache is on cuda:0"):
+        i2s.Kv8Attention(cache, Some(device=there, rows=1), None)
+    for ws in (there, torch.device("cpu")):
+        with pytest.raises(ValueError, match="ws: on "):
+            i2s.Kv8Attention(cache, Some(device=here, rows=1), None, ws=Some(device=ws))
