@@ -751,8 +751,8 @@ class Kv8Batch:
     (seqs + 1), kv_len (seqs) and page_table (seqs x table_width), int32 device
     tensors whose values may change between calls. rows: rows of the row
     tensors; max_rows: a bound on the rows of one sequence (default: rows).
-    status() is the kernels' word (KV8_BAD_*), cleared by reading it; check()
-    raises if it is not zero."""
+    status() is the kernels' word (KV8_BAD_*), read and cleared on the current
+    stream, as a call on the batch's device; check() raises if it is not zero."""
 
     def __init__(self, row_start, kv_len, page_table, rows: int, max_rows=None):
         torch = _torch()
@@ -773,6 +773,8 @@ class Kv8Batch:
                                 seqs, self.max_rows)
 
     def _read(self):
+        if _torch().cuda.current_device() != self.device.index:
+            raise ValueError(f"the batch is on {self.device}, not on the current device")
         bits = ctypes.c_int32(0)
         return int(_L.kv8_read_status(_dptr(self.word), ctypes.byref(bits), _stream())), bits.value
 

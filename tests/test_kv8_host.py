@@ -259,3 +259,14 @@ def test_a_batch_or_workspace_on_another_device_is_refused(i2s):
     for ws in (there, torch.device("cpu")):
         with pytest.raises(ValueError, match="ws: on "):
             i2s.Kv8Attention(cache, Some(device=here, rows=1), None, ws=Some(device=ws))
+
+
+def test_status_of_a_batch_on_another_device_is_refused(i2s, monkeypatch):
+    """The current stream is the current device's: the word would be read before the calls that set it."""
+    torch = pytest.importorskip("torch")
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    batch = i2s.Kv8Batch.__new__(i2s.Kv8Batch)
+    batch.device = torch.device("cuda:1")
+    for read in (batch.status, batch.check):
+        with pytest.raises(ValueError, match="not on the current device"):
+            read()
