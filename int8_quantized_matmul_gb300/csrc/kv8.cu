@@ -649,6 +649,9 @@ int kv8_norm_rope(const kv8_rows* q, const kv8_rows* q_out, int q_heads, const f
     if (rot_dim < 0 || rot_dim > head_dim || rot_dim % 8) return I2S_E_BAD_SHAPE;
     if (rot_dim > 0 && (!positions || !turns)) return I2S_E_NULL_PTR;
     if (!(eps >= 0.0f) || std::isinf(eps) || (flags & ~KV8_PAIRS_NEXT)) return I2S_E_BAD_ARG;
+    if (q_heads == 0) gamma_q = nullptr;   // what is ignored is not looked at
+    if (k_heads == 0) gamma_k = nullptr;
+    if (rot_dim == 0) positions = nullptr, turns = nullptr;
     Kv8RopeArgs a;
     std::memset(&a, 0, sizeof(a));
     const kv8_rows* in[2] = {q, k};

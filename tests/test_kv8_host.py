@@ -270,3 +270,17 @@ def test_status_of_a_batch_on_another_device_is_refused(i2s, monkeypatch):
     for read in (batch.status, batch.check):
         with pytest.raises(ValueError, match="not on the current device"):
             read()
+
+
+def test_norm_rope_does_not_look_at_arguments_it_ignores(i2s):
+    """The gamma of a tensor without heads, and positions and turns where nothing turns: any pointer will do."""
+    E = {v: k for k, v in i2s.STATUS.items()}
+    q, out = i2s.kv8_rows(A, 768, 128, 0), i2s.kv8_rows(2 * A, 768, 128, 0)
+
+    def call(gk=None, pos=20 * A, turns=21 * A, rot=128):
+        return i2s.lib.kv8_norm_rope(q, out, 6, None, None, None, 0, gk, 10, 128, 1e-6, pos, turns, rot, 0, None)
+    want = call()   # valid: ends at the device check where there is no GPU
+    assert want not in (E["I2S_E_MISALIGNED"], E["I2S_E_BAD_ARG"], E["I2S_E_NULL_PTR"])
+    for kw in ({"gk": 5 * A + 4}, {"gk": 2 * A}, {"rot": 0, "pos": 20 * A + 2}, {"rot": 0, "turns": 21 * A + 4},
+               {"rot": 0, "pos": 2 * A}):
+        assert call(**kw) == want, kw
