@@ -1,6 +1,8 @@
 import os
 import sys
 
+import pytest
+
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 if ROOT not in sys.path:
     sys.path.insert(0, ROOT)
@@ -8,3 +10,14 @@ if ROOT not in sys.path:
 
 def pytest_configure(config):
     config.addinivalue_line("markers", "gpu: needs a CUDA GPU (GB300, sm_103a)")
+
+
+def pytest_collection_modifyitems(config, items):
+    """test_kv8_host.py passes made-up addresses, some of them in calls that are valid: where there is a GPU those
+    would be launched, so the file runs only where there is none."""
+    here = [item for item in items if item.path.name == "test_kv8_host.py"]
+    if here:
+        import torch
+        if torch.cuda.is_available():
+            for item in here:
+                item.add_marker(pytest.mark.skip(reason="made-up addresses: only without a GPU"))
