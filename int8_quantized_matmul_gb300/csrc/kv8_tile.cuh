@@ -357,8 +357,11 @@ __global__ void __launch_bounds__(kvt::kThreads, 1)
 
     int* const scan = reinterpret_cast<int*>(S.rows);   // until the barrier below
     // The item: heads vary fastest, the last rows of the last sequence come
-    // first (under a causal mask they see the most).
+    // first (under a causal mask they see the most). Row starts that are not in
+    // order may count past 32 bits: an item that then is nobody's is (0, 0) once
+    // more, and one past its sequence's rows has no tiles.
     {
+        if (tid == 0) S.item[0] = S.item[1] = 0;
         const int per = (c.seqs + kThreads - 1) / kThreads;
         int mine = 0;
         for (int i = 0; i < per; ++i) {
@@ -436,7 +439,7 @@ __global__ void __launch_bounds__(kvt::kThreads, 1)
     int t_lo = 0;
     if (a.window) t_lo = (int)(max(0LL, (long long)sq.len - sq.n + row_lo / group - a.window + 1) / kTileKv);
     const int t_hi = (int)((last_seen(row_hi - 1) + kTileKv - 1) / kTileKv);
-    const int tiles = max(0, t_hi - t_lo);
+    const int tiles = row_lo < row_hi ? max(0, t_hi - t_lo) : 0;
     const int from = t_lo + (int)((long long)tiles * blockIdx.y / gridDim.y);
     const int to = t_lo + (int)((long long)tiles * (blockIdx.y + 1) / gridDim.y);
     const int steps = to - from;
