@@ -819,3 +819,27 @@ def test_rows_of_a_kernel_that_gave_up_are_nan(i2s, kv, group, lens, new, dtype)
         assert torch.equal(call.out, want) and torch.equal(lse, want_lse)
         assert st.batch.status() == 0
     compare_attention(st, qf, dtype, True, 0, 64 ** -0.5, call.out, None, call.out.float().cpu().numpy())
+
+
+def test_f32_sums_of_one_sign_over_many_tokens_lose_little(i2s):
+    """20000 tokens in one CTA (8 heads x 10 query tiles: no split), values of one sign: 78 sums of 256 tokens, each of
+    which loses on average 2.5 units, at most 2^-23 of it, at each of its 16 steps of high parts (the low parts have
+    either sign), when it is on average half of what it will be: 16 * 2.5 * 2^-24; the 78 additions to the running sum
+    round by at most 2^-24 of it, when it is on average half: 78 * 2^-25; operands of 22 bits and F32: 2^-22. In one
+    accumulator 1250 steps would lose 1.9e-4."""
+    kv, group, dim, n, new = 8, 4, 64, 20000, 320
+    st = Setup(i2s, kv, dim, 64, [n], [new], seed=12)
+    st.pool.codes[:, :, 1] = np.maximum(np.abs(st.pool.codes[:, :, 1]), 1)
+    st.data.view(-1).copy_(torch.from_numpy(st.pool.bytes()))
+    q, _ = rows_tensor(np.random.default_rng(5), new, kv * group, dim, "f32", std=0.1)
+    got = i2s.kv8_attention(st.cache, st.batch, q).double()
+    assert st.batch.status() == 0
+    pos = torch.arange(n - new, n, device="cuda")[:, None]
+    hidden = torch.arange(n, device="cuda") > pos
+    k, v = (torch.from_numpy(ref.cached(st.pool, st.table, 0, n, which)[0]).cuda() for which in (0, 1))
+    off = size = 0.0
+    for h in range(kv * group):
+        score = (q[:, h].double() @ k[:, h // group].T * np.float64(np.float32(dim ** -0.5))).masked_fill_(hidden, float("-inf"))
+        want = torch.softmax(score, -1) @ v[:, h // group]
+        off, size = off + (got[:, h] - want).square().sum().item(), size + want.square().sum().item()
+    assert (off / size) ** 0.5 <= 16 * 2.5 * 2.0 ** -24 + 78 * 2.0 ** -25 + 2.0 ** -22
