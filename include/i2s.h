@@ -611,10 +611,18 @@ int w8a8_mul_mat_grouped(const w8a8_problem* probs, int count, int64_t M, void* 
  * over less than 2^40 elements, an output's elements are distinct, and two
  * outputs may be slices of one row.
  *
+ * Speed. max_rows and table_width bound what the host cannot see, and choose
+ * kernels by it for the whole batch: kv8_attention takes its decode kernel where
+ * max_rows * q_heads / heads is at most 8, kv8_write and kv8_read their shapes for
+ * single tokens where max_rows is below 16, and few rows over a cache of many table
+ * entries are split along it. So give max_rows as it is, and sequences of single
+ * tokens a batch of their own rather than one with a prompt.
+ *
  * Limits: head_dim 64 or 128, 1 <= heads <= 1024, 1 <= seqs <= KV8_MAX_SEQS,
  * 1 <= max_rows <= rows < 2^31, table_width*page_tokens < 2^31,
- * seqs*heads*table_width*page_tokens < 2^34. Errors of every call: BAD_SHAPE, NULL_PTR, MISALIGNED, BAD_ARG (an unknown dtype or flag, or
- * an output that overlaps another operand), UNSUPPORTED_DEVICE, CUDA.
+ * seqs*heads*table_width*page_tokens < 2^34. Errors of every call: BAD_SHAPE,
+ * NULL_PTR, MISALIGNED, BAD_ARG (an unknown dtype or flag, or an output that
+ * overlaps another operand), UNSUPPORTED_DEVICE, CUDA.
  * ------------------------------------------------------------------------- */
 #define KV8_BLOCK 16
 #define KV8_MAX_SEQS 4096
@@ -663,7 +671,9 @@ size_t kv8_page_bytes(int heads, int head_dim, int page_tokens);
  * is clamp(round(x * (1/scale)), -127, 127), halfway cases away from zero, each
  * step one binary32 operation. An infinity or NaN among the values makes the
  * block's scale NaN and its new codes zero: it reads back as NaN, and stays so
- * until the block is written from its first token. Tokens at negative
+ * until the block is written from its first token. So it is after a rewind
+ * (drafted tokens taken back, kv_len smaller in a later batch): the block keeps
+ * the scale, or the NaN, that the rejected tokens gave it. Tokens at negative
  * positions (n > kv_len) are skipped (KV8_BAD_LENGTH), as are those of a bad page.
  * k and v have the same dtype. Writing the same tokens again changes nothing. */
 int kv8_write(const kv8_cache* cache, const kv8_batch* batch, const kv8_rows* k, const kv8_rows* v,

@@ -278,7 +278,8 @@ __global__ void __launch_bounds__(kReadWarps * 32) k_kv8_read(const __grid_const
 //
 // Measured: 8000 rows of 24 heads of 128, F32, 197 MB: 34.3 us, 5.7 TB/s (86 % of
 // a copy); 5003 16-bit rows of 36 heads, half of each turned, 92 MB: 18.2 us, 5.1
-// TB/s; 8 rows 3.9 us, the call. Loads in flight per warp 2/3/4/6: 43/40/39/41 us.
+// TB/s; 8 rows 3.9 us, the call. 16-bit rows with a norm have less: 8000 of 24 heads bf16 34.8 us (without it 18.6), f16
+// 27.0 (16.6), 60 bytes of a thread's state spilled. Loads in flight per warp 2/3/4/6: 43/40/39/41 us.
 // ---------------------------------------------------------------------------
 constexpr int kRopeWarps = 4;
 constexpr int kRopeBatch = 4;

@@ -25,7 +25,7 @@ static size_t plan_bytes(int heads, int seqs) { return ((size_t)heads * seqs * s
 // the table's width. Long caches under few rows leave SMs idle too: their tiles
 // are then split between CTAs (as many as fill the SMs, four tiles of the cache
 // at least each: with two, 512 tokens under 12 heads of 2 took 21.4 us, unsplit
-// 18.5).
+// 18.5; later in three, as under a wider table, 20.4 and 17.0).
 struct TileCut {
     int query_tiles;   // of a CTA
     int items;         // grid: heads times a bound on the row tiles

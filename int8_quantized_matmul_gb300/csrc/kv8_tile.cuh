@@ -30,7 +30,7 @@
 // added to with rounding: F32 rows 7.5e-7 over 8000 tokens, where plain F32 is
 // off by 1.4e-6 (5.5e-6 and 3.7e-6 behind a token of 2^16 times the others'
 // weight). The weights are made before that, while the P V that it waits for
-// runs (8000-token prompt: 459 us, the other way 472). Two query tiles leave no
+// runs (8000-token prompt: 461 us, the other way 472). Two query tiles leave no
 // columns for such a sum, so they are taken only for caches over which the one
 // chain loses at most half of the least half step of the rows' type: longest().
 //
@@ -69,10 +69,10 @@
 // second parts (30 and 59 % of the bf16 rate measured). Per tile of 128 x 128 it
 // takes 3500 cycles (3400 if O moved every four tiles): from S to the maxima 800,
 // to the weights 1600, P V after the last of them 1000, Q K^T of the next but one
-// 1250. Chunks of prompts with bf16 rows: 180 us, 3250 cycles per step of two query
+// 1250. Chunks of prompts with bf16 rows: 181 us, 3250 cycles per step of two query
 // tiles, of which the 32 MMAs (128 x 128 x 16, K and Q from shared memory) take
-// 2600. 512 tokens of 12 heads over 2: 16.8 us; 1 to 6 drafted tokens of 16
-// sequences, window 2048: 22.8 us.
+// 2600. 512 tokens of 12 heads over 2: 17.0 us (20.4 under a table of 16384: it is then split
+// in three); 1 to 6 drafted tokens of 16 sequences, window 2048: 22.8 us. 12 to 40 bytes of a thread's state are spilled.
 #pragma once
 
 #include "kv8_decode.cuh"
@@ -91,7 +91,7 @@ constexpr int kIssueWarp = 12;
 constexpr float kBias = 8.0f;
 constexpr float kSlack = 6.0f;
 constexpr long long kWait = 2000000000LL;
-// Tiles summed in one accumulator, where there is a running sum. F32 rows: an 8000-token prompt takes 459, 439
+// Tiles summed in one accumulator, where there is a running sum. F32 rows: an 8000-token prompt takes 461, 439
 // and 439 us with 2, 3 and 4; over 70 batches of mixed sizes the error is at most
 // 1.4, 1.6 and over 1.6 times that of plain F32. 16-bit rows: 64 steps lose 1.5e-5, a sixteenth of f16's least half step.
 constexpr int kChainF32 = 2, kChain16 = 8;

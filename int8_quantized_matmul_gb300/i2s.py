@@ -707,7 +707,9 @@ def _kv8_here(cache, **tensors):
 class _Kv8Call:
     """A call marshalled once, for repeated use and CUDA graph capture. It runs
     on torch's current stream of its tensors' device, which has to be the
-    current device. Its tensors are kept alive, not copied."""
+    current device. Its tensors, those that it makes among them, are kept alive
+    with it, not copied: keep it until its calls on other streams than the one it
+    was made on are done."""
 
     def _bind(self, name, device, *args):
         torch = _torch()
@@ -750,7 +752,8 @@ class Kv8Batch:
     """Which rows belong to which sequence, and where its tokens lie: row_start
     (seqs + 1), kv_len (seqs) and page_table (seqs x table_width), int32 device
     tensors whose values may change between calls. rows: rows of the row
-    tensors; max_rows: a bound on the rows of one sequence (default: rows).
+    tensors; max_rows: a bound on the rows of one sequence (default: rows), by
+    which the kernels are chosen: give it, at least for single tokens.
     status() is the kernels' word (KV8_BAD_*), read and cleared on the current
     stream, as a call on the batch's device; check() raises if it is not zero."""
 
