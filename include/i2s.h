@@ -591,8 +591,9 @@ int w8a8_mul_mat_grouped(const w8a8_problem* probs, int count, int64_t M, void* 
  * Batch. `rows` rows of new tokens, sequence by sequence: sequence s has the
  * n = row_start[s+1] - row_start[s] rows from row_start[s], n >= 0, and row i
  * of them is the token at position kv_len[s] - n + i, so kv_len[s] counts the
- * batch's own tokens. Rows at and past row_start[seqs] belong to no sequence:
- * no operator reads them or writes their outputs.
+ * batch's own tokens. Rows before row_start[0] and from row_start[seqs] on
+ * belong to no sequence: no operator of a batch reads them or writes their
+ * outputs.
  * row_start (seqs + 1), kv_len (seqs) and page_table are device int32, read by
  * the kernels, so a captured graph may be replayed after they change. The
  * kernels check them: a row_start that decreases or leaves [0, rows], a
@@ -722,12 +723,12 @@ int kv8_norm_rope(const kv8_rows* q, const kv8_rows* q_out, int q_heads, const f
  * of F32 rows where max_rows * q_heads / heads is above 8) are then added with
  * rounding; measured for F32 rows: 1e-6, or 9e-6 behind a first token that has
  * nearly all the weight. Many 16-bit rows over at most 8192 (f16) or 65536 (bf16)
- * tokens (of the table, or window + max_rows) are summed at once, which loses
- * less than half of the least half step of the output. Scales are
- * taken to be not negative, as kv8_write makes them, and V's at least 2^-40.
- * One that is NaN, and a V scale of 2^87 or more (kv8_write makes those of values
- * from 127 * 2^87 on), makes the rows that see its block NaN and no others; their
- * lse may be NaN with them.
+ * tokens (of the table, or window + max_rows) are summed at once, which with
+ * values of one sign loses about half of the least half step of the output.
+ * Scales are taken to be not negative, as kv8_write makes them, and V's at
+ * least 2^-40. One that is NaN, and a V scale of 2^87 or more (kv8_write makes
+ * those of values from 127 * 2^87 on), makes the rows that see its block NaN and
+ * no others; their lse may be NaN with them.
  * q, out    rows x q_heads x head_dim, one dtype; q_heads a multiple of
  *           cache->heads, at most 64 times it, and max_rows * q_heads / heads
  *           below 2^30. out overlaps no other operand.

@@ -95,7 +95,7 @@ constexpr long long kWait = 2000000000LL;
 // and 439 us with 2, 3 and 4; over 70 batches of mixed sizes the error is at most
 // 1.4, 1.6 and over 1.6 times that of plain F32. 16-bit rows: 64 steps lose 1.5e-5, a sixteenth of f16's least half step.
 constexpr int kChainF32 = 2, kChain16 = 8;
-// Tokens that 16-bit rows may sum in one accumulator: 2^-22 of the sum for each 16, up to half of the least half step
+// Tokens that 16-bit rows may sum in one accumulator: about 2^-22 of the sum lost for each 16, up to half of the least half step
 // (2^-12 f16, 2^-9 bf16).
 constexpr long long longest(int dtype) { return dtype == kKvF16 ? 8192 : 65536; }
 constexpr int kSlots = 4;            // operands of the ring: K of a tile takes the place of K two tiles before,

@@ -843,3 +843,25 @@ def test_f32_sums_of_one_sign_over_many_tokens_lose_little(i2s):
         want = torch.softmax(score, -1) @ v[:, h // group]
         off, size = off + (got[:, h] - want).square().sum().item(), size + want.square().sum().item()
     assert (off / size) ** 0.5 <= 16 * 2.5 * 2.0 ** -24 + 78 * 2.0 ** -25 + 2.0 ** -22
+
+
+@pytest.mark.parametrize("dtype,dim", [("f16", 64), ("bf16", 128)])
+def test_attention_of_16_bit_rows_split_along_a_long_cache(i2s, dtype, dim):
+    """10 query tiles in all: 15 CTAs share the cache of each, 10 tiles of it or more, so each moves its sums once before
+    its part is joined with the others'."""
+    st = Setup(i2s, 2, dim, 64, [20000], [320], seed=27)
+    q, qf = rows_tensor(np.random.default_rng(28), st.rows, 4, dim, dtype, std=1.5)
+    check_attention(i2s, st, q, qf, dtype)
+    assert st.batch.status() == 0
+
+
+def test_two_query_tiles_in_a_cta_give_the_same_bits_every_time(i2s):
+    st = Setup(i2s, 8, 128, 64, [1500, 900, 700], [800, 650, 700], seed=29)
+    q, _ = rows_tensor(np.random.default_rng(30), st.rows, 24, 128, "bf16", std=1.5)
+    call = i2s.Kv8Attention(st.cache, st.batch, q)
+    call()
+    first = call.out.clone()
+    for _ in range(20):
+        call.out.zero_()
+        call()
+        assert torch.equal(first, call.out)
