@@ -721,8 +721,9 @@ int kv8_norm_rope(const kv8_rows* q, const kv8_rows* q_out, int q_heads, const f
  * The tensor cores cut their sums off, always towards zero: about 2e-7 of the
  * sum for each 16 tokens added to it. Partial sums of at most 1024 tokens (256
  * of F32 rows where max_rows * q_heads / heads is above 8) are then added with
- * rounding; measured for F32 rows: 1e-6, or 9e-6 behind a first token that has
- * nearly all the weight. Many 16-bit rows over at most 8192 (f16) or 65536 (bf16)
+ * rounding. Measured for F32 rows and values of one sign: 1.4e-6 and, where
+ * max_rows * q_heads / heads is at most 8, 1.8e-6; behind a first token that has
+ * most of the weight 5.5e-6 and 1.6e-5. Many 16-bit rows over at most 8192 (f16) or 65536 (bf16)
  * tokens (of the table, or window + max_rows) are summed at once, which with
  * values of one sign loses about half of the least half step of the output.
  * Scales are taken to be not negative, as kv8_write makes them, and V's at
