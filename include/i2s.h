@@ -755,6 +755,137 @@ int kv8_attention(const kv8_cache* cache, const kv8_batch* batch, const kv8_rows
 int kv8_read_status(int32_t* status, int32_t* bits, i2s_stream_t stream);
 
 /* ---------------------------------------------------------------------------
+ * Rows that have weights of their own: a router, matrix products grouped by
+ * expert, and low-rank adapters beside a shared projection.
+ *
+ * Plan. `items` items, each of one owner (an expert, an adapter) or of none,
+ * sorted by owner: owner o's are list[start[o]] .. list[start[o + 1] - 1], in
+ * ascending order; start[0] = 0 and start[owners] counts the items that have an
+ * owner; list holds no more than those (entries from there on are not written).
+ * Both are device int32 (owners + 1 and items of them), made by route_plan_build or
+ * route_topk, or by the caller, and read by the kernels, so a captured graph may
+ * be replayed after they change. Starts that decrease or leave [0, items] are
+ * cut to what is in order, and entries outside [0, items) are left out, so nothing outside
+ * the row tensors is touched. An item may stand in a list once.
+ *
+ * Row tensors. i2s_rows: element (row, i) at data[row*stride + i], stride in elements,
+ * of I2S_F32, I2S_F16 or I2S_BF16 (the values of KV8_F32 and so on). Where a call
+ * says "vector rows", data and the stride are multiples of 16 bytes; else of one
+ * element. Strides are not negative, a tensor reaches over at most 2^40 elements, and an
+ * output's rows do not reach into each other.
+ *
+ * Errors of every call: BAD_SHAPE, NULL_PTR, MISALIGNED, BAD_ARG (an unknown
+ * dtype or flag, or an output that overlaps another operand),
+ * WORKSPACE_TOO_SMALL, UNSUPPORTED_DEVICE, CUDA. A workspace is 256-byte
+ * aligned, not preserved, and calls sharing one are ordered on one stream.
+ * ------------------------------------------------------------------------- */
+#define ROUTE_MAX_OWNERS 1024
+#define ROUTE_MAX_ITEMS 134217728   /* 2^27 */
+#define ROUTE_MAX_CHOSEN 16
+enum { I2S_F32 = 0, I2S_F16 = 1, I2S_BF16 = 2 };
+
+typedef struct route_plan {
+    int32_t* start;
+    int32_t* list;
+    int64_t items;
+    int owners;
+} route_plan;
+
+typedef struct i2s_rows {
+    void* data;
+    int64_t stride;
+    int dtype;
+} i2s_rows;
+
+/* The plan of items whose owners are given: owner is device int32 [items]; a
+ * value outside [0, owners) means none. */
+size_t route_plan_workspace(int64_t items, int owners);
+int route_plan_build(const int32_t* owner, const route_plan* plan, void* ws, size_t ws_bytes, i2s_stream_t stream);
+
+/* A router: of each row's `experts` logits (i2s_rows, rows x experts) the k
+ * largest logit + bias[e] (bias: device F32 [experts] or NULL; one binary32 sum), in falling
+ * order, equal ones by index. Item row*k + j is the row's j-th choice, expert[row*k + j]
+ * (device int32) its expert and weight[row*k + j] (device F32) its weight: factor times
+ *   exp(l - m) / sum_e exp(l_e - m), the softmax over all the row's logits (without the
+ *       bias), or with ROUTE_NORM over those of the chosen;
+ *   1 / (1 + exp(-l)) with ROUTE_SIGMOID, and with ROUTE_NORM that divided by
+ *       the sum over the chosen (zero where that sum is zero).
+ * A score of -infinity or NaN (a masked expert's) is never chosen, and such
+ * logits add nothing to a softmax: where fewer than k are left, the items behind them have the
+ * expert -1 and the weight 0. A logit of +infinity makes the weights of its row's softmax
+ * NaN. Sums are binary32.
+ * plan: items rows*k, owners `experts`; start and list are written as by
+ * route_plan_build from expert. NULL for none.
+ * 1 <= experts <= ROUTE_MAX_OWNERS, 1 <= k <= min(experts, ROUTE_MAX_CHOSEN),
+ * rows*k <= ROUTE_MAX_ITEMS. The workspace's size is route_plan_workspace(rows*k, experts);
+ * without a plan none is needed (NULL). factor is finite. */
+#define ROUTE_SIGMOID 1u
+#define ROUTE_NORM 2u
+int route_topk(const i2s_rows* logits, int64_t rows, int experts, int k, const float* bias, float factor, unsigned flags,
+               int32_t* expert, float* weight, const route_plan* plan, void* ws, size_t ws_bytes, i2s_stream_t stream);
+
+/* Matrix products grouped by expert over W8A8 weights ([P4] Implementation for the arithmetic of
+ * one): item i of expert e takes row i / x_group of x (quantized per row as w8a8_mul_mat does) and
+ *   d[i][n] = aScale * bscale[e][n] * (float)sum_k q[k] * wq[e][n][k],
+ * left to right, the dot in exact integers. Then
+ *   weight NULL, y_group 1: row i of y is d[i], or with W8A8_SWIGLU the N/2 values
+ *       g / (1 + exp(-g)) * u, g = d[i][n], u = d[i][n + N/2]. Rows of items without
+ *       an expert are left as they were.
+ *   weight (device F32 [items]): row t of y is the sum over j of weight[t*y_group + j] *
+ *       d[t*y_group + j], j ascending, each step a binary32 operation. Items without an expert add nothing,
+ *       a row without any is zero.
+ * Results are rounded once to y's dtype. An infinity or NaN in a row of x makes
+ * what it gives NaN, and nothing else.
+ * w      wq: device int8, experts x N x K, 16-byte aligned (w8a8_quantize_weights
+ *        of each expert's N x K, or of all (experts*N) x K at once); bscale: device F32, experts x N.
+ * plan   owners = experts; items a multiple of x_group and of y_group (a token's k choices share
+ *        a row of x: x_group = k; they are summed: y_group = k).
+ * x      vector rows, items/x_group x K. y: items/y_group x N (or N/2).
+ * ws     device workspace of w8a8_mul_mat_experts_workspace() bytes; its first word is the status
+ *        word that i2s_read_status reads (a wait that ran out; y is then incomplete).
+ * Requirements: K % 16 == 0, K <= 65536, experts*N < 2^31, experts <= ROUTE_MAX_OWNERS; N % 32 == 0
+ * with W8A8_SWIGLU, which takes no weight. W8A8_TEST_STALL is for tests only: products never come, waits run out. */
+#define W8A8_SWIGLU 1u
+#define W8A8_TEST_STALL 0x80000000u
+typedef struct w8a8_experts {
+    const int8_t* wq;
+    const float* bscale;
+    int64_t N;
+    int64_t K;
+    int experts;
+} w8a8_experts;
+size_t w8a8_mul_mat_experts_workspace(const w8a8_experts* w, const route_plan* plan, int x_group, int y_group,
+                                      unsigned flags);
+int w8a8_mul_mat_experts(const w8a8_experts* w, const route_plan* plan, const i2s_rows* x, int x_group, const i2s_rows* y,
+                         const float* weight, int y_group, unsigned flags, void* ws, size_t ws_bytes, i2s_stream_t stream);
+
+/* Low-rank adapters beside a shared projection: for row r of owner a in the plan (items = rows)
+ *   out[r] = base[r] + scale[a] * (B_a (A_a x[r])),
+ * rounded once to out's dtype. Rows of no adapter are left as they were, in out. out may be
+ * base itself (then y += ..., as beside i2s_mul_mat), or overlaps no operand.
+ * Sums are binary32; F32 rows and the inner vector A_a x enter the tensor cores as bf16 parts
+ * (three of F32 rows, together exact; of the inner vector three with F32 rows, else two).
+ * a      A: device, adapters x rank x K; B: device, adapters x N x rank; both of a->dtype (I2S_F16 or
+ *        I2S_BF16), 16-byte aligned. scale: device F32 [adapters] or NULL for 1.
+ * x      vector rows, rows x K; base, out: rows x N. One dtype: I2S_F32 or I2S_BF16 with adapters of
+ *        I2S_BF16, I2S_F16 with adapters of I2S_F16.
+ * Requirements: rank a multiple of 8, at most 128; K % 8 == 0, K <= 65536; 1 <= N <= 2^24;
+ * adapters <= ROUTE_MAX_OWNERS. Adapters of smaller rank are padded with zeros. */
+typedef struct lora_adapters {
+    const void* A;
+    const void* B;
+    const float* scale;
+    int64_t K;
+    int64_t N;
+    int rank;
+    int adapters;
+    int dtype;
+} lora_adapters;
+size_t lora_add_workspace(const lora_adapters* a, const route_plan* plan);
+int lora_add(const lora_adapters* a, const route_plan* plan, const i2s_rows* x, const i2s_rows* base, const i2s_rows* out,
+             void* ws, size_t ws_bytes, i2s_stream_t stream);
+
+/* ---------------------------------------------------------------------------
  * Device status. Kernels with bounded waits (the tensor-core pipelines) never
  * trap: when a wait runs out they record a code in the status word at the
  * start of the workspace and exit. Every i2s_mul_mat* call clears the word in

@@ -2,8 +2,8 @@
 
 Each translation unit under csrc/ is compiled by nvcc in parallel, then linked
 into int8_quantized_matmul_gb300/_lib/libi2s.so with the CUDA runtime linked
-statically and only the i2s_* / i8s_* / w8a8_* / kv8_* symbols exported (so the library's own
-runtime never interposes on another copy loaded in the same process).
+statically and only the i2s_* / i8s_* / w8a8_* / kv8_* / route_* / lora_* symbols
+exported (so the library's own runtime never interposes on another copy loaded in the same process).
 """
 
 from __future__ import annotations
@@ -20,7 +20,8 @@ LIB = os.path.join(LIBDIR, "libi2s.so")
 BUILD = os.path.join(HERE, "_build")
 
 SOURCES = ["abi.cu", "quant.cu", "gemv_tc.cu", "gemm_tc.cu", "i8s.cu", "i8s_tc.cu", "i8s_elt.cu",
-           "noalloc.cu", "kv8.cu", "kv8_attn.cu"]
+           "noalloc.cu", "kv8.cu", "kv8_attn.cu", "route.cu", "experts.cu",
+           "lora.cu"]
 NVCC = os.environ.get("NVCC", "nvcc")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-fmad=false", "-Xcompiler", "-fPIC,-fvisibility=hidden",

@@ -1,0 +1,786 @@
+// Matrix products grouped by expert over W8A8 weights (include/i2s.h,
+// w8a8_mul_mat_experts).
+//
+// Mathematics. Item i has a row of x and an expert e: with q the row's int8
+// codes (scale a) and w the expert's (scale b[n] per channel),
+//   d[i][n] = (a * b[n]) * (float)(sum_k q[k] * w[n][k]),
+// the sum exact in integers; then optionally silu(gate) * up over the two halves
+// of the channels, or the weighted sum of the items of a y row, item by item.
+// sm_103a has no integer tcgen05 MMA: codes are f16 integers, products at most
+// 128 * 127, so the f32 sums of 1024 positions stay below 2^24 and are exact. A
+// row of at most 1024 positions needs no more; of two such sums, exact both, one
+// f32 addition gives (float) of their sum; more are added in int32.
+//
+// Three launches: rows quantized to f16 codes; the products; the weighted sum.
+//
+// The product kernel. An item's weights are one expert's, so items come sorted
+// by expert (the plan), and a work unit is (expert, 128 channels, up to ROWS of
+// its items). The channels are the M of the MMA and the rows its N, which may be
+// any multiple of 16: ragged experts cost what they have. Units run over an expert's
+// row tiles first, then its channels, so that neighbouring CTAs read the
+// same weights at the same time: HBM gives them once.
+//
+// Weights stay one byte in memory and in the ring that TMA fills (128 channels x
+// 128 positions); converter warps, one thread per channel, turn them into f16 and
+// put them into tensor memory, from where the MMA takes its A operand. The rows
+// are gathered by TMA (gather4: four rows of the quantized x by their index), so
+// a row that eight experts read is neither copied nor laid out eight times.
+//
+// SWIGLU: a unit's 128 channels are 64 gate and the 64 up channels of the same
+// index, in blocks of 16 and 16 (a five-dimensional box of the weights as they lie): a
+// gate and its up value are then 16 lanes apart in the same warp, and every lane
+// finishes one of two neighbouring rows after one exchange.
+//
+// Roles (512 threads): warps 0-3 epilogue, 4-11 converters (two groups taking
+// stages by turns), 12 weights, 13 gathered rows, 14 MMAs. TMEM: two accumulators
+// of ROWS columns, then a ring of 64-column operands. Waits are bounded; one that runs
+// out sets the status word at the start of the workspace and the CTA's abort
+// flag, roles leave their loops, and what they issued is drained.
+
+#include <algorithm>
+#include <atomic>
+#include <cstring>
+
+#include "common.cuh"
+#include "internal.h"
+#include "owned.cuh"
+#include "tc.cuh"
+
+namespace i2s {
+
+namespace {
+
+namespace xp {
+
+constexpr int kThreads = 512;
+constexpr int kConvWarp = 4, kWeightWarp = 12, kRowWarp = 13, kMmaWarp = 14;
+constexpr int kChannels = 128;
+constexpr int kStep = 128;                      // positions of a stage
+constexpr int kChunkSteps = kI8sChunkK / kStep; // stages of an exact f32 sum
+constexpr int kWStage = kChannels * kStep;      // bytes of a stage's weights
+constexpr int kOpCols = kStep / 2;              // TMEM columns of a stage's weights in f16
+constexpr int kMaxSlots = 6, kMaxWSlots = 10;
+constexpr long long kWait = 2000000000LL;
+// Registers of a thread after the split (of the 128 at launch): epilogue,
+// converters, the others. 128 * 208 + 256 * 104 + 128 * 56 <= 512 * 128.
+constexpr int kRegsEpilogue = 208, kRegsConvert = 104, kRegsIssue = 56;
+
+template <int ROWS>
+struct Shape {
+    // Few rows per expert: the weights' bytes count, and get the shared memory.
+    // Many: the gathered rows do.
+    static constexpr int kSlots = ROWS == 32 ? 6 : 4;      // operands: gathered rows, and weights in TMEM
+    static constexpr int kWSlots = ROWS == 32 ? 10 : 5;    // weights as bytes
+    static constexpr int kAtom = ROWS * 128;               // 64 positions of the rows
+    static constexpr int kRowStage = 2 * kAtom;
+    static constexpr uint32_t kOp0 = 2 * ROWS;             // first TMEM column of the operands
+    static_assert(kOp0 + kSlots * kOpCols <= 512 && kSlots % 2 == 0, "TMEM, and each slot one converter group's");
+    static_assert(kSlots <= kMaxSlots && kWSlots <= kMaxWSlots, "barriers");
+};
+
+struct Shared {
+    uint64_t wfull[kMaxWSlots], wempty[kMaxWSlots];
+    uint64_t afull[kMaxSlots], bfull[kMaxSlots], empty[kMaxSlots];
+    uint64_t dfull[2], dempty[2], done;
+    uint32_t tmem;
+    int abort;
+    struct Row {
+        long long off;   // of the row in y; negative: none
+        float scale;
+        int pad;
+    } row[4][128];   // of each epilogue warp
+    int begin[kMaxOwners + 1], tile0[kMaxOwners + 1];
+};
+
+template <int ROWS>
+constexpr int smem_bytes() {
+    return Shape<ROWS>::kSlots * Shape<ROWS>::kRowStage + Shape<ROWS>::kWSlots * kWStage + (int)sizeof(Shared);
+}
+
+template <int N>
+__device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+
+// For a warp whose control flow is uniform; `lead` is not zero in one lane.
+__device__ __forceinline__ void mma(uint32_t lead, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n"
+        ".reg .pred p, q;\n"
+        "setp.ne.b32 p, %4, 0;\n"
+        "setp.ne.b32 q, %5, 0;\n"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n"
+        "}\n" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(lead)
+        : "memory");
+}
+__device__ __forceinline__ void commit(uint32_t lead, uint64_t* bar) {
+    asm volatile(
+        "{\n"
+        ".reg .pred q;\n"
+        "setp.ne.b32 q, %1, 0;\n"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n"
+        "}\n" ::"r"(tc::smem_u32(bar)), "r"(lead)
+        : "memory");
+}
+__device__ __forceinline__ void load_weights(void* dst, const CUtensorMap* map, int k, int n, int e, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+            tc::smem_u32(dst)),
+        "l"(map), "r"(k), "r"(n), "r"(e), "r"(tc::smem_u32(bar))
+        : "memory");
+}
+// 16 channels x (gate, up) x four blocks of 16.
+__device__ __forceinline__ void load_pairs(void* dst, const CUtensorMap* map, int k, int block, int e, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %3, %4, %5}], "
+        "[%6];" ::"r"(tc::smem_u32(dst)),
+        "l"(map), "r"(k), "r"(0), "r"(block), "r"(e), "r"(tc::smem_u32(bar))
+        : "memory");
+}
+__device__ __forceinline__ void gather_rows(void* dst, const CUtensorMap* map, int k, const int (&r)[4], uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, "
+        "%4, %5, %6}], [%7];" ::"r"(tc::smem_u32(dst)),
+        "l"(map), "r"(k), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(tc::smem_u32(bar))
+        : "memory");
+}
+
+// Codes 0, 1 (SEL 0x4140) or 2, 3 (0x4342) of four biased by 128, as f16:
+// the byte in the mantissa of 1024, less 1152.
+template <int SEL>
+__device__ __forceinline__ uint32_t codes2(uint32_t x) {
+    const uint32_t m = __byte_perm(x, 0x64646464u, SEL);
+    const __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&m), __half2half2(__ushort_as_half((unsigned short)0x6480)));
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+}  // namespace xp
+
+struct ExpertArgs {
+    CUtensorMap wmap, xmap;
+    PlanView plan;
+    const float* bscale;
+    const float* ascale;    // workspace, one per x row
+    void* y;                // y, or the workspace's F32 rows that are then weighted
+    long long y_stride;
+    int y_dtype;
+    int x_group, N, K, tiles_n;
+    uint8_t* used;          // workspace: items that have an expert, or null
+    uint32_t* status;
+    bool test_stall;
+};
+
+template <int ROWS, bool SWIGLU>
+__global__ void __launch_bounds__(xp::kThreads, 1) k_experts(const __grid_constant__ ExpertArgs a) {
+    using namespace xp;
+    using S_ = Shape<ROWS>;
+    extern __shared__ __align__(1024) uint8_t smem_xp[];
+    uint8_t* sRows = smem_xp;
+    uint8_t* sW = sRows + S_::kSlots * S_::kRowStage;
+    Shared& S = *reinterpret_cast<Shared*>(sW + S_::kWSlots * kWStage);
+    const int tid = threadIdx.x, warp = (int)__reduce_max_sync(0xffffffffu, (unsigned)tid >> 5), lane = tid & 31;
+    volatile int* abort_flag = &S.abort;
+    auto fail = [&] {
+        *abort_flag = 1;
+        atomicOr(a.status, 1u);
+    };
+
+    if (warp == kMmaWarp) {
+        if (lane == 0) {
+            for (int i = 0; i < S_::kWSlots; ++i) {
+                tc::mbar_init(&S.wfull[i], 1);
+                tc::mbar_init(&S.wempty[i], 4);
+            }
+            for (int i = 0; i < S_::kSlots; ++i) {
+                tc::mbar_init(&S.afull[i], 4);
+                tc::mbar_init(&S.bfull[i], 1);
+                tc::mbar_init(&S.empty[i], 1);
+            }
+            for (int i = 0; i < 2; ++i) {
+                tc::mbar_init(&S.dfull[i], 1);
+                tc::mbar_init(&S.dempty[i], 4);
+            }
+            tc::mbar_init(&S.done, 1);
+            S.abort = 0;
+            tc::fence_mbar_init();
+        }
+        __syncwarp();
+        tc::tmem_alloc(&S.tmem, 512);
+        tc::tmem_relinquish();
+    }
+    // The plan and the weights come from launches before the one that quantizes
+    // the rows, which began after those were complete: they are read before
+    // pdl_wait, while the rows are quantized.
+    if (warp == kWeightWarp) plan_tiles(a.plan, ROWS, S.begin, S.tile0, lane);
+    tc::tc_fence_before();
+    __syncthreads();
+    tc::tc_fence_after();
+    const uint32_t tmem = S.tmem;
+    const int units = S.tile0[a.plan.owners] * a.tiles_n;
+    const int steps = (a.K + kStep - 1) / kStep;
+
+    struct Unit {
+        int e, n0, first, rows;   // expert, first channel (tile index * 128), first place in the list, rows
+    };
+    auto unit_at = [&](int u) {
+        Unit t;
+        t.e = owner_of_tile(S.tile0, a.plan.owners, u / a.tiles_n);
+        const int tiles = S.tile0[t.e + 1] - S.tile0[t.e];
+        const int r = u - S.tile0[t.e] * a.tiles_n;
+        t.n0 = r / tiles * kChannels;
+        // rows spread evenly over the expert's row tiles
+        const int all = S.begin[t.e + 1] - S.begin[t.e], at = r % tiles;
+        const int lo = (int)((long long)all * at / tiles), hi = (int)((long long)all * (at + 1) / tiles);
+        t.first = S.begin[t.e] + lo;
+        t.rows = hi - lo;
+        return t;
+    };
+
+    if (warp < kConvWarp) {
+        // ---------------------------------------------------------- epilogue
+        regs_up<kRegsEpilogue>();
+        pdl_wait();
+        const uint32_t lanes = (uint32_t)(warp * 32) << 16;
+        const int chunks = (steps + kChunkSteps - 1) / kChunkSteps;
+        int chunk_at = 0;
+        bool ok = true;
+        for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
+            const Unit t = unit_at(u);
+            // each warp looks its rows up for itself
+            __syncwarp();
+            for (int i = lane; i < t.rows; i += 32) {
+                const int item = __ldcg(a.plan.list + t.first + i);
+                Shared::Row row = {-1, 0.0f, 0};
+                if (item >= 0 && item < a.plan.items) {
+                    row.off = item * a.y_stride;
+                    row.scale = __ldcg(a.ascale + item / a.x_group);
+                    if (a.used != nullptr && t.n0 == 0 && warp == 0) a.used[item] = 1;
+                }
+                S.row[warp][i] = row;
+            }
+            __syncwarp();
+            const int r = warp * 32 + lane;   // channel of the unit
+            // SWIGLU: lane's channel 16 * warp + lane % 16 of 64, gate or up
+            const int half = a.N >> 1;
+            const int n = SWIGLU ? (t.n0 >> 1) + warp * 16 + (lane & 15) : t.n0 + r;
+            const bool live = n < (SWIGLU ? half : a.N);
+            const float b = live ? __ldg(a.bscale + (long long)t.e * a.N + n + (SWIGLU && lane >= 16 ? half : 0)) : 0.0f;
+            float sum[ROWS];
+            for (int c = 0; c < chunks; ++c, ++chunk_at) {
+                const int buf = chunk_at & 1;
+                if (!tc::mbar_wait(&S.dfull[buf], (uint32_t)(chunk_at >> 1) & 1, abort_flag, kWait)) { fail(); ok = false; }
+                ok = __all_sync(0xffffffffu, ok) != 0;
+                if (!ok) break;
+                tc::tc_fence_after();
+#pragma unroll
+                for (int p = 0; p < ROWS / 32; ++p) {
+                    if (32 * p < t.rows) {
+                        uint32_t v[32];
+                        tc::tmem_ld_32x32b_x32(tmem + lanes + (uint32_t)(buf * ROWS + 32 * p), v);
+                        tc::tmem_ld_wait();
+                        if (chunks <= 2) {
+                            if (c == 0) {
+#pragma unroll
+                                for (int i = 0; i < 32; ++i) sum[32 * p + i] = __uint_as_float(v[i]);
+                            } else {
+#pragma unroll
+                                for (int i = 0; i < 32; ++i) sum[32 * p + i] = __fadd_rn(sum[32 * p + i], __uint_as_float(v[i]));
+                            }
+                        } else {   // int32 in the same registers
+                            if (c == 0) {
+#pragma unroll
+                                for (int i = 0; i < 32; ++i) sum[32 * p + i] = __int_as_float(__float2int_rn(__uint_as_float(v[i])));
+                            } else {
+#pragma unroll
+                                for (int i = 0; i < 32; ++i)
+                                    sum[32 * p + i] = __int_as_float(__float_as_int(sum[32 * p + i]) + __float2int_rn(__uint_as_float(v[i])));
+                            }
+                        }
+                    }
+                }
+                tc::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&S.dempty[buf]);
+            }
+            if (!ok) break;
+#pragma unroll
+            for (int p = 0; p < ROWS / 32; ++p) {
+                if (32 * p < t.rows) {
+                    if (chunks > 2) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) sum[32 * p + i] = __int2float_rn(__float_as_int(sum[32 * p + i]));
+                    }
+                    if (SWIGLU) {
+#pragma unroll
+                        for (int i = 0; i < 32; i += 2) {
+                            const Shared::Row r0 = S.row[warp][32 * p + i], r1 = S.row[warp][32 * p + i + 1];
+                            const float d0 = __fmul_rn(__fmul_rn(r0.scale, b), sum[32 * p + i]);
+                            const float d1 = __fmul_rn(__fmul_rn(r1.scale, b), sum[32 * p + i + 1]);
+                            // the lower half warp finishes row i, the upper row i + 1
+                            const float other = __shfl_xor_sync(0xffffffffu, lane < 16 ? d1 : d0, 16);
+                            const float g = lane < 16 ? d0 : other, up = lane < 16 ? other : d1;
+                            const float h = __fmul_rn(__fdiv_rn(g, __fadd_rn(1.0f, expf(-g))), up);
+                            const long long off = lane < 16 ? r0.off : r1.off;
+                            if (live && 32 * p + i + (lane >> 4) < t.rows && off >= 0) put_as(a.y, a.y_dtype, off + n, h);
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            const Shared::Row r0 = S.row[warp][32 * p + i];
+                            const float d = __fmul_rn(__fmul_rn(r0.scale, b), sum[32 * p + i]);
+                            if (live && 32 * p + i < t.rows && r0.off >= 0) put_as(a.y, a.y_dtype, r0.off + n, d);
+                        }
+                    }
+                }
+            }
+        }
+    } else if (warp < kWeightWarp) {
+        // -------------------------------------------------------- converters
+        regs_down<kRegsConvert>();
+        const int group = (warp - kConvWarp) >> 2, q = warp & 3, r = q * 32 + lane;
+        const uint32_t lanes = (uint32_t)(q * 32) << 16;
+        int at = 0;   // stage of this CTA
+        bool ok = true;
+        for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
+            for (int k = 0; k < steps; ++k, ++at) {
+                if ((at & 1) != group) continue;
+                const int ws = at % S_::kWSlots, slot = at % S_::kSlots;
+                if (!tc::mbar_wait(&S.wfull[ws], (uint32_t)(at / S_::kWSlots) & 1, abort_flag, kWait)) { fail(); ok = false; }
+                ok = __all_sync(0xffffffffu, ok) != 0;
+                if (!ok) break;
+                uint4 x[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    x[j] = *reinterpret_cast<const uint4*>(sW + ws * kWStage + r * 128 + ((j ^ (r & 7)) << 4));
+                // (nothing but these reads uses the slot: it is free once they are done)
+                uint32_t h[32];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const uint32_t w[4] = {x[j].x ^ 0x80808080u, x[j].y ^ 0x80808080u, x[j].z ^ 0x80808080u, x[j].w ^ 0x80808080u};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        h[8 * j + 2 * i] = codes2<0x4140>(w[i]);
+                        h[8 * j + 2 * i + 1] = codes2<0x4342>(w[i]);
+                    }
+                }
+                if (!tc::mbar_wait(&S.empty[slot], ((uint32_t)(at / S_::kSlots) & 1) ^ 1, abort_flag, kWait)) { fail(); ok = false; }
+                ok = __all_sync(0xffffffffu, ok) != 0;
+                if (!ok) break;
+                tc::tc_fence_after();
+                const uint32_t dst = tmem + lanes + S_::kOp0 + (uint32_t)(slot * kOpCols);
+                tc::tmem_st_32x32b_x32(dst, h);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const uint4 y = x[4 + j];
+                    const uint32_t w[4] = {y.x ^ 0x80808080u, y.y ^ 0x80808080u, y.z ^ 0x80808080u, y.w ^ 0x80808080u};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        h[8 * j + 2 * i] = codes2<0x4140>(w[i]);
+                        h[8 * j + 2 * i + 1] = codes2<0x4342>(w[i]);
+                    }
+                }
+                tc::tmem_st_32x32b_x32(dst + 32, h);
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&S.wempty[ws]);
+                tc::tmem_st_wait();
+                tc::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&S.afull[slot]);
+            }
+        }
+    } else {
+        regs_down<kRegsIssue>();
+        if (warp == kWeightWarp) {
+            // ------------------------------------------------------- weights
+            if (lane == 0) {
+                int at = 0;
+                bool ok = true;
+                for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
+                    const Unit t = unit_at(u);
+                    for (int k = 0; k < steps; ++k, ++at) {
+                        const int ws = at % S_::kWSlots;
+                        if (!tc::mbar_wait(&S.wempty[ws], ((uint32_t)(at / S_::kWSlots) & 1) ^ 1, abort_flag, kWait)) {
+                            fail();
+                            ok = false;
+                            break;
+                        }
+                        tc::mbar_arrive_expect_tx(&S.wfull[ws], kWStage);
+                        uint8_t* dst = sW + ws * kWStage;
+                        if (SWIGLU) load_pairs(dst, &a.wmap, k * kStep, t.n0 / 32, t.e, &S.wfull[ws]);
+                        else load_weights(dst, &a.wmap, k * kStep, t.n0, t.e, &S.wfull[ws]);
+                    }
+                }
+                // every copy has landed before the CTA leaves
+                for (int i = max(0, at - S_::kWSlots); i < at; ++i)
+                    tc::mbar_wait_drain(&S.wfull[i % S_::kWSlots], (uint32_t)(i / S_::kWSlots) & 1, kWait / 8);
+            }
+        } else if (warp == kRowWarp) {
+            // -------------------------------------------------- gathered rows
+            pdl_wait();
+            const int x_rows = a.plan.items / a.x_group;
+            int at = 0;
+            bool ok = true;
+            // lane l gathers rows 4l .. 4l + 3 of the unit; places behind its last row get the last row again
+            auto rows_of = [&](int u, int (&r)[4], int& groups) {
+                groups = 0;
+                if (u >= units) return;
+                const Unit t = unit_at(u);
+                groups = (t.rows + 3) / 4;
+                if (lane >= groups) return;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int item = __ldcg(a.plan.list + t.first + min(4 * lane + i, t.rows - 1));
+                    r[i] = min(max(item / a.x_group, 0), x_rows - 1);
+                }
+            };
+            int r[4], groups;
+            rows_of(blockIdx.x, r, groups);
+            for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
+                int next[4], next_groups;
+                rows_of(u + gridDim.x, next, next_groups);
+                for (int k = 0; k < steps; ++k, ++at) {
+                    const int slot = at % S_::kSlots;
+                    if (!tc::mbar_wait(&S.empty[slot], ((uint32_t)(at / S_::kSlots) & 1) ^ 1, abort_flag, kWait)) { fail(); ok = false; }
+                    ok = __all_sync(0xffffffffu, ok) != 0;
+                    if (!ok) break;
+                    // the second half of the stage is left out where the row ends in the first
+                    const bool both = k * kStep + 64 < a.K;
+                    if (lane == 0) tc::mbar_arrive_expect_tx(&S.bfull[slot], (uint32_t)groups * (both ? 1024u : 512u));
+                    __syncwarp();
+                    if (lane < groups) {
+                        uint8_t* dst = sRows + slot * S_::kRowStage + lane * 512;
+                        gather_rows(dst, &a.xmap, k * kStep, r, &S.bfull[slot]);
+                        if (both) gather_rows(dst + S_::kAtom, &a.xmap, k * kStep + 64, r, &S.bfull[slot]);
+                    }
+                    __syncwarp();
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) r[i] = next[i];
+                groups = next_groups;
+            }
+            for (int i = max(0, at - S_::kSlots); i < at; ++i)
+                tc::mbar_wait_drain(&S.bfull[i % S_::kSlots], (uint32_t)(i / S_::kSlots) & 1, kWait / 8);
+        } else if (warp == kMmaWarp) {
+            // ---------------------------------------------------------- MMAs
+            const uint32_t lead = lane == 0;
+            const uint32_t tm = __reduce_max_sync(0xffffffffu, tmem);
+            int at = 0, chunk_at = 0;
+            bool ok = true;
+            auto wait = [&](uint64_t* bar, uint32_t parity) {
+                const bool got = tc::mbar_wait(bar, parity, abort_flag, kWait);
+                return __all_sync(0xffffffffu, got) != 0;
+            };
+            // a test lets the others wait for products that never come
+            for (int u = a.test_stall ? units : blockIdx.x; ok && u < units; u += gridDim.x) {
+                const Unit t = unit_at(u);
+                const int rows = (int)__reduce_max_sync(0xffffffffu, (unsigned)t.rows);
+                const uint32_t idesc = tc::idesc_f16_f32(kChannels, (rows + 15) / 16 * 16);
+                for (int k = 0; ok && k < steps; ++k, ++at) {
+                    const int slot = at % S_::kSlots, buf = chunk_at & 1;
+                    const uint32_t phase = (uint32_t)(at / S_::kSlots) & 1;
+                    if (k % kChunkSteps == 0) {
+                        ok = wait(&S.dempty[buf], ((uint32_t)(chunk_at >> 1) & 1) ^ 1);
+                    }
+                    ok = ok && wait(&S.bfull[slot], phase) && wait(&S.afull[slot], phase);
+                    if (!ok) break;
+                    tc::tc_fence_after();
+                    const uint64_t bd = tc::sdesc_sw128_kmajor(tc::smem_u32(sRows + slot * S_::kRowStage));
+                    const uint32_t d = tm + (uint32_t)(buf * ROWS), op = tm + S_::kOp0 + (uint32_t)(slot * kOpCols);
+                    const int left = (a.K - k * kStep + 15) / 16;   // 16-position MMAs that are left of the rows
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        if (j < left)
+                            mma(lead, d, op + 8u * j, bd + (uint64_t)((j >> 2) * (S_::kAtom >> 4) + 2 * (j & 3)), idesc,
+                                k % kChunkSteps != 0 || j > 0);
+                    commit(lead, &S.empty[slot]);
+                    if (k % kChunkSteps == kChunkSteps - 1 || k == steps - 1) {
+                        commit(lead, &S.dfull[buf]);
+                        ++chunk_at;
+                    }
+                }
+            }
+            if (!ok) fail();
+            commit(lead, &S.done);
+            tc::mbar_wait_drain(&S.done, 0, kWait / 8);
+        }
+        __syncwarp();
+    }
+    tc::tc_fence_before();
+    __syncthreads();
+    tc::tc_fence_after();
+    if (warp == kMmaWarp) tc::tmem_dealloc(tmem, 512);
+}
+
+// ---------------------------------------------------------------------------
+// Rows of x as f16 codes and a scale: amax floored at 1e-9, scale = amax/127,
+// q = clamp(round(x * (127/amax)), -127, 127), halves away from zero (as every
+// W8A8 call). A row with an infinity or NaN gets the scale NaN and codes of zero: its
+// outputs are NaN, and no others. TPR threads per row, four values at a time,
+// kept in registers up to kKeep * 4 of them per thread, beyond that read again.
+// ---------------------------------------------------------------------------
+constexpr int kRowThreads = 256, kKeep = 8;
+
+template <int DT, int TPR>
+__global__ void __launch_bounds__(kRowThreads) k_expert_rows(RowsView x, int rows, int K, __half* q, float* ascale,
+                                                             uint8_t* used, int items, uint32_t* status) {
+    using T = typename RowT<DT>::type;
+    struct alignas(sizeof(T) * 4) V4 { T v[4]; };
+    constexpr int kRowsPer = kRowThreads / TPR;
+    __shared__ float s_max[kRowThreads / 32];
+    pdl_wait();
+    pdl_launch_next();
+    if (blockIdx.x == 0 && threadIdx.x == 0) *status = 0u;
+    if (used != nullptr)
+        for (int i = blockIdx.x * kRowThreads + threadIdx.x; i < (items + 3) / 4; i += gridDim.x * kRowThreads)
+            reinterpret_cast<uint32_t*>(used)[i] = 0u;
+    const int part = threadIdx.x % TPR;
+    const int row = blockIdx.x * kRowsPer + threadIdx.x / TPR;
+    const bool here = row < rows;
+    const V4* from = reinterpret_cast<const V4*>(static_cast<const T*>(x.data) + (here ? row * x.stride : 0));
+    const int n4 = here ? K / 4 : 0;
+    V4 keep[kKeep];
+    float mx = 0.0f;
+    bool finite = true;
+    auto look = [&](const V4& w) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float v = fabsf(to_f32(w.v[j]));
+            mx = fmaxf(mx, v);
+            finite = finite && v <= 3.402823466e38f;   // false for an infinity and for NaN
+        }
+    };
+#pragma unroll
+    for (int i = 0; i < kKeep; ++i)
+        if (part + i * TPR < n4) keep[i] = from[part + i * TPR];
+#pragma unroll
+    for (int i = 0; i < kKeep; ++i)
+        if (part + i * TPR < n4) look(keep[i]);
+    for (int i = part + kKeep * TPR; i < n4; i += TPR) look(from[i]);
+    if (!finite) mx = INFINITY;
+    mx = warp_max(mx);
+    if (TPR > 32) {
+        if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = mx;
+        __syncthreads();
+        const int w0 = threadIdx.x / TPR * (TPR / 32);
+        mx = s_max[w0];
+#pragma unroll
+        for (int i = 1; i < TPR / 32; ++i) mx = fmaxf(mx, s_max[w0 + i]);
+    }
+    if (!here) return;
+    finite = mx != INFINITY;
+    mx = fmaxf(mx, 1e-9f);
+    const float inv = finite ? __fdiv_rn(127.0f, mx) : 0.0f;
+    if (part == 0) ascale[row] = finite ? __fdiv_rn(mx, 127.0f) : __int_as_float(0x7fc00000);
+    uint2* to = reinterpret_cast<uint2*>(q + (long long)row * K);
+    auto put = [&](int i, const V4& w) {
+        uint32_t c[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            // (with the scale NaN every code is that of zero, whatever NaN times zero clamps to)
+            const float v0 = finite ? to_f32(w.v[2 * j]) : 0.0f, v1 = finite ? to_f32(w.v[2 * j + 1]) : 0.0f;
+            const __half2 h = __floats2half2_rn(small_int_to_float(quantize_one(v0, inv)), small_int_to_float(quantize_one(v1, inv)));
+            c[j] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+        to[i] = make_uint2(c[0], c[1]);
+    };
+#pragma unroll
+    for (int i = 0; i < kKeep; ++i)
+        if (part + i * TPR < n4) put(part + i * TPR, keep[i]);
+    for (int i = part + kKeep * TPR; i < n4; i += TPR) put(i, from[i]);
+}
+
+// y[t][n] = sum_j weight[t][j] * d[t * group + j][n], j ascending, each product
+// and sum rounded once; items without an expert add nothing.
+__global__ void __launch_bounds__(256) k_expert_sum(const float* __restrict__ d, const float* __restrict__ weight,
+                                                    const uint8_t* __restrict__ used, int group, int N, long long rows, void* y,
+                                                    long long y_stride, int y_dtype) {
+    pdl_wait();
+    const bool four = N % 4 == 0;   // the F32 rows are then read 16 bytes at a time
+    const int per = four ? N / 4 : N;
+    for (long long i = blockIdx.x * 256LL + threadIdx.x; i < rows * per; i += gridDim.x * 256LL) {
+        const long long t = i / per;
+        const int n = (int)(i - t * per) * (four ? 4 : 1);
+        float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        for (int j = 0; j < group; ++j) {
+            const long long item = t * group + j;
+            if (!used[item]) continue;
+            const float w = weight[item];
+            if (four) {
+                const float4 v = *reinterpret_cast<const float4*>(d + item * N + n);
+                s[0] = __fadd_rn(s[0], __fmul_rn(w, v.x));
+                s[1] = __fadd_rn(s[1], __fmul_rn(w, v.y));
+                s[2] = __fadd_rn(s[2], __fmul_rn(w, v.z));
+                s[3] = __fadd_rn(s[3], __fmul_rn(w, v.w));
+            } else {
+                s[0] = __fadd_rn(s[0], __fmul_rn(w, d[item * N + n]));
+            }
+        }
+        for (int j = 0; j < (four ? 4 : 1); ++j) put_as(y, y_dtype, t * y_stride + n + j, s[j]);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Host side
+// ---------------------------------------------------------------------------
+struct Layout {
+    size_t ascale, q, used, d, total;
+};
+
+Layout layout_of(int64_t items, int64_t x_rows, int64_t N, int64_t K) {
+    Layout l;
+    l.ascale = 256;   // the status word before it
+    l.q = l.ascale + up_256((size_t)x_rows * 4);
+    l.used = l.q + up_256((size_t)x_rows * K * 2);
+    l.d = l.used + up_256((size_t)items);
+    l.total = l.d + up_256((size_t)items * N * 4);
+    return l;
+}
+
+int check_sizes(const w8a8_experts* w, const route_plan* plan, int x_group, int y_group, bool swiglu) {
+    if (!w) return I2S_E_NULL_PTR;
+    const int r = check_plan_sizes(plan);
+    if (r) return r;
+    if (w->experts < 1 || w->experts > kMaxOwners || w->N < 1 || w->K < 16 || w->K % 16 || w->K > 65536 ||
+        w->N >= ((int64_t)1 << 31) / w->experts)
+        return I2S_E_BAD_SHAPE;
+    if (swiglu && w->N % 32) return I2S_E_BAD_SHAPE;
+    if (plan->owners != w->experts || x_group < 1 || y_group < 1 || plan->items % x_group || plan->items % y_group)
+        return I2S_E_BAD_SHAPE;
+    if (plan->items > kMaxReach / w->N || plan->items > kMaxReach / w->K || w->N * w->experts > kMaxReach / w->K)
+        return I2S_E_BAD_SHAPE;
+    return I2S_OK;
+}
+
+template <int ROWS, bool SWIGLU>
+cudaError_t launch_product(const ExpertArgs& a, int grid, cudaStream_t s) {
+    constexpr int bytes = xp::smem_bytes<ROWS>();
+    static_assert(bytes <= 232448, "shared memory");
+    static std::atomic<unsigned long long> ready{0};   // a bit per device
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (!(ready.load(std::memory_order_acquire) >> (dev & 63) & 1)) {
+        e = cudaFuncSetAttribute(k_experts<ROWS, SWIGLU>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e != cudaSuccess) return e;
+        ready.fetch_or(1ull << (dev & 63), std::memory_order_release);
+    }
+    return launch_pdl(k_experts<ROWS, SWIGLU>, dim3((unsigned)grid), dim3(xp::kThreads), bytes, s, a);
+}
+
+template <int DT>
+cudaError_t launch_rows(const RowsView& x, int rows, int K, __half* q, float* ascale, uint8_t* used, int items,
+                        uint32_t* status, cudaStream_t s) {
+    auto go = [&](auto kernel, int per) {
+        return launch_pdl(kernel, dim3((unsigned)((rows + per - 1) / per)), dim3(kRowThreads), 0, s, x, rows, K, q, ascale, used,
+                          items, status);
+    };
+    // the fewest threads that hold a row
+    if (K <= 32 * 4 * kKeep) return go(k_expert_rows<DT, 32>, kRowThreads / 32);
+    if (K <= 64 * 4 * kKeep) return go(k_expert_rows<DT, 64>, kRowThreads / 64);
+    return go(k_expert_rows<DT, kRowThreads>, 1);
+}
+
+}  // namespace
+}  // namespace i2s
+
+using namespace i2s;
+
+#pragma GCC visibility push(default)
+extern "C" {
+
+size_t w8a8_mul_mat_experts_workspace(const w8a8_experts* w, const route_plan* plan, int x_group, int y_group,
+                                      unsigned flags) {
+    if ((flags & ~(W8A8_SWIGLU | W8A8_TEST_STALL)) || check_sizes(w, plan, x_group, y_group, (flags & W8A8_SWIGLU) != 0)) return 0;
+    return layout_of(plan->items, plan->items / x_group, w->N, w->K).total;
+}
+
+int w8a8_mul_mat_experts(const w8a8_experts* w, const route_plan* plan, const i2s_rows* x, int x_group, const i2s_rows* y,
+                         const float* weight, int y_group, unsigned flags, void* ws, size_t ws_bytes, i2s_stream_t stream) {
+    const bool swiglu = (flags & W8A8_SWIGLU) != 0;
+    int r = check_sizes(w, plan, x_group, y_group, swiglu);
+    if (r) return r;
+    if ((r = check_plan(plan))) return r;
+    if (!w->wq || !w->bscale || !ws) return I2S_E_NULL_PTR;
+    if ((flags & ~(W8A8_SWIGLU | W8A8_TEST_STALL)) || (swiglu && weight) || (!weight && y_group != 1)) return I2S_E_BAD_ARG;
+    const int64_t items = plan->items, x_rows = items / x_group, y_rows = items / y_group;
+    const int64_t out = swiglu ? w->N / 2 : w->N;
+    if ((r = check_row_tensor(x, x_rows, w->K, true, false)) || (r = check_row_tensor(y, y_rows, out, false, true))) return r;
+    if (((uintptr_t)w->wq & 15) || ((uintptr_t)w->bscale & 3) || ((uintptr_t)weight & 3) || ((uintptr_t)ws & 255))
+        return I2S_E_MISALIGNED;
+    const Layout l = layout_of(items, x_rows, w->N, w->K);
+    const size_t need = l.total;
+    if (ws_bytes < need) return I2S_E_WORKSPACE_TOO_SMALL;
+    const Span sw = span_of(w->wq, (size_t)w->experts * w->N * w->K), sb = span_of(w->bscale, (size_t)w->experts * w->N * 4);
+    const Span sx = rows_span(*x, x_rows, w->K), sy = rows_span(*y, y_rows, out), ss = span_of(ws, need);
+    const Span sg = span_of(weight, weight ? (size_t)items * 4 : 0);
+    for (const Span& o : {sy, ss})
+        if (o.meets(sw) || o.meets(sb) || o.meets(sx) || o.meets(sg) || meets_plan(o, *plan)) return I2S_E_BAD_ARG;
+    if (sy.meets(ss)) return I2S_E_BAD_ARG;
+    if ((r = check_current_device())) return r;
+
+    uint8_t* base = static_cast<uint8_t*>(ws);
+    uint32_t* status = reinterpret_cast<uint32_t*>(base);
+    float* ascale = reinterpret_cast<float*>(base + l.ascale);
+    __half* q = reinterpret_cast<__half*>(base + l.q);
+    uint8_t* used = weight ? base + l.used : nullptr;
+    float* d = reinterpret_cast<float*>(base + l.d);
+
+    ExpertArgs a;
+    std::memset(&a, 0, sizeof(a));
+    const cuuint64_t N = (cuuint64_t)w->N, K = (cuuint64_t)w->K, E = (cuuint64_t)w->experts;
+    bool mapped;
+    if (swiglu) {
+        // (position, channel of a block, gate or up, block, expert)
+        const cuuint64_t dims[5] = {K, 16, 2, N / 32, E}, strides[4] = {K, N / 2 * K, 16 * K, N * K};
+        const cuuint32_t box[5] = {xp::kStep, 16, 2, 4, 1};
+        mapped = encode_tensor_map(&a.wmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, 5, w->wq, dims, strides, box);
+    } else {
+        const cuuint64_t dims[3] = {K, N, E}, strides[2] = {K, N * K};
+        const cuuint32_t box[3] = {xp::kStep, xp::kChannels, 1};
+        mapped = encode_tensor_map(&a.wmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, w->wq, dims, strides, box);
+    }
+    const cuuint64_t xdims[2] = {K, (cuuint64_t)x_rows}, xstrides[1] = {K * 2};
+    const cuuint32_t xbox[2] = {64, 1};
+    if (!mapped || !encode_tensor_map(&a.xmap, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, q, xdims, xstrides, xbox)) return I2S_E_CUDA;
+    a.plan = plan_view(*plan);
+    a.bscale = w->bscale;
+    a.ascale = ascale;
+    a.y = weight ? d : y->data;
+    a.y_stride = weight ? w->N : y->stride;
+    a.y_dtype = weight ? kF32 : y->dtype;
+    a.x_group = x_group;
+    a.N = (int)w->N;
+    a.K = (int)w->K;
+    a.tiles_n = (int)((w->N + xp::kChannels - 1) / xp::kChannels);
+    a.used = used;
+    a.status = status;
+    a.test_stall = (flags & W8A8_TEST_STALL) != 0;
+
+    const RowsView xv = {x->data, x->stride};
+    cudaError_t e;
+    if (x->dtype == kF32) e = launch_rows<kF32>(xv, (int)x_rows, a.K, q, ascale, used, (int)items, status, stream);
+    else if (x->dtype == kF16) e = launch_rows<kF16>(xv, (int)x_rows, a.K, q, ascale, used, (int)items, status, stream);
+    else e = launch_rows<kBf16>(xv, (int)x_rows, a.K, q, ascale, used, (int)items, status, stream);
+    if (e != cudaSuccess) return I2S_E_CUDA;
+
+    // Row tiles there may be: no more than one per expert and one per `rows` items.
+    const bool few = items <= 16 * (int64_t)w->experts;
+    const int rows = few ? 32 : 128;
+    const int64_t units = (std::min<int64_t>(items, w->experts) + items / rows) * a.tiles_n;
+    const int grid = (int)std::min<int64_t>(units, device_sm_count());
+    if (few) e = swiglu ? launch_product<32, true>(a, grid, stream) : launch_product<32, false>(a, grid, stream);
+    else e = swiglu ? launch_product<128, true>(a, grid, stream) : launch_product<128, false>(a, grid, stream);
+    if (e != cudaSuccess) return I2S_E_CUDA;
+    if (weight) {
+        const int64_t blocks = (y_rows * ((w->N % 4 == 0 ? w->N / 4 : w->N)) + 255) / 256;
+        e = launch_pdl(k_expert_sum, dim3((unsigned)std::min<int64_t>(blocks, 152 * 64)), dim3(256), 0, stream,
+                       static_cast<const float*>(d), weight, static_cast<const uint8_t*>(used), y_group, a.N, (long long)y_rows,
+                       y->data, (long long)y->stride, y->dtype);
+        if (e != cudaSuccess) return I2S_E_CUDA;
+    }
+    return I2S_OK;
+}
+
+}  // extern "C"
+#pragma GCC visibility pop

@@ -661,6 +661,17 @@ bool make_u8_operand_map(CUtensorMap* map, const void* base, int rows, int row_b
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// A tensor map in the 128-byte swizzle, zero fill beyond the extents.
+bool encode_tensor_map(CUtensorMap* map, CUtensorMapDataType type, int rank, const void* base, const cuuint64_t* dims,
+                       const cuuint64_t* strides, const cuuint32_t* box) {
+    EncodeTiledFn enc = encode_fn();
+    if (!enc || rank > 5) return false;
+    std::memset(map, 0, sizeof(*map));
+    const cuuint32_t unit[5] = {1, 1, 1, 1, 1};
+    return enc(map, type, (cuuint32_t)rank, const_cast<void*>(base), dims, strides, box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // Per device: 1 + the number of CTA pairs that can be resident at once (0:
 // not yet configured). Clusters must fit inside a GPC, so on a part whose
 // GPCs have odd SM counts this is below half the SM count, and a persistent

@@ -177,6 +177,8 @@ static_assert(sizeof(QuantArgs) <= 32764, "QuantArgs exceeds the kernel paramete
 bool make_f16_operand_map(CUtensorMap* map, const void* base, int rows, int K, int box_rows);
 // rows x row_bytes uint8 matrix, box {128 bytes, box_rows}, 128-byte swizzle
 bool make_u8_operand_map(CUtensorMap* map, const void* base, int rows, int row_bytes, int box_rows);
+bool encode_tensor_map(CUtensorMap* map, CUtensorMapDataType type, int rank, const void* base, const cuuint64_t* dims,
+                       const cuuint64_t* strides, const cuuint32_t* box);
 cudaError_t launch_gemm_tc(const TcArgs& a, int grid, cudaStream_t s);
 int gemm_tc_max_pairs();   // CTA pairs of the GEMM that fit on the device at once
 cudaError_t launch_gemv_tc(const TcArgs& a, int grid, cudaStream_t s);

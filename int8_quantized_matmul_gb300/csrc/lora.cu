@@ -1,0 +1,507 @@
+// Low-rank adapters of many requests beside a shared projection (include/i2s.h,
+// lora_add).
+//
+// Mathematics. Rows sorted by adapter a (the plan): t = A_a x over K, then
+// out = base + scale_a * (B_a t) over the rank. Two launches, since every value of t
+// needs all of K: k_lora_inner writes partial sums of t (K split between CTAs where rows are
+// few), k_lora_outer adds them in order and finishes.
+//
+// Precision. 16-bit operands go to the tensor cores as they are. F32 rows of x,
+// and then t, are cut into three parts of 8 bits that bf16 holds (high bits first, each cut
+// and each remainder exact), all 24 bits. With 16-bit rows t has two parts, rounded: 18 bits in bf16,
+// and 22 in f16 after a row is scaled by a power of two into its range. Small parts are
+// multiplied first.
+//
+// Both bound by memory: x, base and out pass once. The MMAs (m16n8k16) take their
+// operands straight from 16-byte loads of neighbouring values: which position of K (or
+// of the rank) an MMA's index stands for is free as long as both operands agree, so thread c
+// of a group of four has 8 neighbours of 32, of which the first MMA takes
+// the first four and the second the others. The outer product's columns are spread the same way,
+// so that a thread writes 8 neighbours.
+
+#include <algorithm>
+#include <atomic>
+
+#include "common.cuh"
+#include "internal.h"
+#include "owned.cuh"
+
+namespace i2s {
+
+namespace {
+
+constexpr int kThreads = 256, kWarps = 8;
+constexpr int kInnerRows = 32;    // rows of a CTA of the inner product
+constexpr int kOuterRows = 64, kOuterCols = 256;
+constexpr int kMaxRank = 128, kMaxSplits = 16;
+
+struct LoraArgs {
+    PlanView plan;
+    const void *A, *B;
+    const float* scale;
+    RowsView x, base, out;
+    float* t;          // workspace: [split][place in the list][rank]
+    int K, N, rank, splits, k_per;   // positions of K of a split
+    bool vec;          // base and out allow 16-byte accesses
+};
+
+// D += A B, f32 sums of f16 or bf16 products.
+template <bool F16>
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    if (F16)
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// The upper halves of two words: two values cut to bf16.
+__device__ __forceinline__ uint32_t upper2(float lo, float hi) {
+    return __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x7632);
+}
+__device__ __forceinline__ float cut(float x) { return __uint_as_float(__float_as_uint(x) & 0xffff0000u); }
+
+// Two values as PARTS bf16 pairs, high bits first.
+template <int PARTS>
+__device__ __forceinline__ void split2(float a, float b, uint32_t (&p)[PARTS]) {
+#pragma unroll
+    for (int i = 0; i < PARTS; ++i) {
+        p[i] = upper2(a, b);
+        if (i + 1 < PARTS) {
+            a = __fsub_rn(a, cut(a));
+            b = __fsub_rn(b, cut(b));
+        }
+    }
+}
+
+template <int DT>
+struct Kind {
+    static constexpr bool kF16Mma = DT == kF16;
+    static constexpr int kXParts = DT == kF32 ? 3 : 1;
+    static constexpr int kTParts = DT == kF32 ? 3 : 2;
+};
+
+// 8 neighbouring values of a row of x, as the operands of two MMAs: [part][4 pairs].
+template <int DT>
+__device__ __forceinline__ void load_x(const void* row, int k, bool in, uint4 (&w)[DT == kF32 ? 2 : 1]) {
+    constexpr int kWords = DT == kF32 ? 2 : 1;
+    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const typename RowT<DT>::type*>(row) + k);
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) w[i] = in ? __ldg(p + i) : make_uint4(0u, 0u, 0u, 0u);
+}
+template <int DT>
+__device__ __forceinline__ void parts_x(const uint4 (&w)[DT == kF32 ? 2 : 1], uint32_t (&p)[Kind<DT>::kXParts][4]) {
+    if constexpr (DT == kF32) {
+        const uint32_t v[8] = {w[0].x, w[0].y, w[0].z, w[0].w, w[1].x, w[1].y, w[1].z, w[1].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint32_t q[3];
+            split2<3>(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]), q);
+            p[0][i] = q[0];
+            p[1][i] = q[1];
+            p[2][i] = q[2];
+        }
+    } else {
+        p[0][0] = w[0].x;
+        p[0][1] = w[0].y;
+        p[0][2] = w[0].z;
+        p[0][3] = w[0].w;
+    }
+}
+
+struct alignas(16) Places {   // 16-byte accesses go to what follows it
+    int begin[kMaxOwners + 1], tile0[kMaxOwners + 1];
+};
+static_assert(sizeof(Places) % 16 == 0, "alignment of what follows");
+
+// t of up to kInnerRows rows of one adapter, over one split of K, for up to
+// 8 * NT of its rank. The warps take chunks of 32 positions by turns, and their
+// sums are added in shared memory, warp by warp.
+template <int DT, int NT>
+__global__ void __launch_bounds__(kThreads) k_lora_inner(const __grid_constant__ LoraArgs a) {
+    using W = Kind<DT>;
+    constexpr int kMt = kInnerRows / 16, kWords = DT == kF32 ? 2 : 1;
+    extern __shared__ __align__(16) uint8_t smem_in[];
+    Places& P = *reinterpret_cast<Places*>(smem_in);
+    float* sum = reinterpret_cast<float*>(smem_in + sizeof(Places));   // [warp][row][8 * NT]
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
+    pdl_wait();
+    if (warp == 0) plan_tiles(a.plan, kInnerRows, P.begin, P.tile0, lane);
+    __syncthreads();
+    const int tiles = P.tile0[a.plan.owners];
+    if ((int)blockIdx.x >= tiles) return;
+    const int o = owner_of_tile(P.tile0, a.plan.owners, blockIdx.x);
+    const int first = P.begin[o] + ((int)blockIdx.x - P.tile0[o]) * kInnerRows;
+    const int rows = min(kInnerRows, P.begin[o + 1] - first);
+    const int rank0 = blockIdx.z * 8 * NT;   // of the adapter's rank
+    const int k_lo = blockIdx.y * a.k_per, k_hi = min(a.K, k_lo + a.k_per);
+    using T = typename RowT<DT>::type;
+
+    // rows g, g + 8, ... of the tile; behind the last the last again
+    const T* xr[2 * kMt];
+#pragma unroll
+    for (int i = 0; i < 2 * kMt; ++i) {
+        const int item = __ldcg(a.plan.list + first + min(g + 8 * i, rows - 1));
+        xr[i] = static_cast<const T*>(a.x.data) + min(max(item, 0), a.plan.items - 1) * a.x.stride;
+    }
+    const uint16_t* A = static_cast<const uint16_t*>(a.A) + ((long long)o * a.rank + rank0) * a.K;
+    const bool two = rows > 16;   // both m16 tiles
+    float acc[kMt][NT][4] = {};
+    uint4 xw[2 * kMt][kWords], bw[NT];
+    auto load = [&](int k) {
+        const bool in = k < k_hi;
+#pragma unroll
+        for (int i = 0; i < 2 * kMt; ++i)
+            if (i < 2 || two) load_x<DT>(xr[i], k, in, xw[i]);
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+            bw[n] = in && rank0 + 8 * n < a.rank ? __ldg(reinterpret_cast<const uint4*>(A + (long long)(8 * n + g) * a.K + k))
+                                                 : make_uint4(0u, 0u, 0u, 0u);
+    };
+    int k = k_lo + warp * 32 + 8 * c;
+    load(k);
+    for (int k0 = k_lo + warp * 32; k0 < k_hi; k0 += kWarps * 32) {
+        uint32_t ap[2 * kMt][W::kXParts][4];
+        uint4 b[NT];
+#pragma unroll
+        for (int i = 0; i < 2 * kMt; ++i) parts_x<DT>(xw[i], ap[i]);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) b[n] = bw[n];
+        k += kWarps * 32;
+        load(k);
+#pragma unroll
+        for (int p = W::kXParts - 1; p >= 0; --p)
+#pragma unroll
+            for (int m = 0; m < kMt; ++m) {
+                if (m > 0 && !two) break;
+                const uint32_t a0[4] = {ap[2 * m][p][0], ap[2 * m + 1][p][0], ap[2 * m][p][1], ap[2 * m + 1][p][1]};
+                const uint32_t a1[4] = {ap[2 * m][p][2], ap[2 * m + 1][p][2], ap[2 * m][p][3], ap[2 * m + 1][p][3]};
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    mma16816<W::kF16Mma>(acc[m][n], a0, b[n].x, b[n].y);
+                    mma16816<W::kF16Mma>(acc[m][n], a1, b[n].z, b[n].w);
+                }
+            }
+    }
+    constexpr int kRow = 8 * NT;
+#pragma unroll
+    for (int m = 0; m < kMt; ++m)
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            float* at = sum + ((warp * kInnerRows + 16 * m + g) * kRow + 8 * n + 2 * c);
+            *reinterpret_cast<float2*>(at) = make_float2(acc[m][n][0], acc[m][n][1]);
+            *reinterpret_cast<float2*>(at + 8 * kRow) = make_float2(acc[m][n][2], acc[m][n][3]);
+        }
+    __syncthreads();
+    float* to = a.t + ((long long)blockIdx.y * a.plan.items + first) * a.rank + rank0;
+    for (int i = tid; i < rows * kRow; i += kThreads) {
+        const int row = i / kRow, n = i - row * kRow;
+        if (rank0 + n >= a.rank) continue;
+        float s = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) s = __fadd_rn(s, sum[(w * kInnerRows + row) * kRow + n]);
+        to[(long long)row * a.rank + n] = s;
+    }
+}
+
+// out of up to kOuterRows rows of one adapter, for kOuterCols columns: a warp has
+// 32 of them, with B in registers, and takes 16 rows at a time. KK: chunks of 32 of the rank.
+template <int DT, int KK>
+__global__ void __launch_bounds__(kThreads) k_lora_outer(const __grid_constant__ LoraArgs a) {
+    using W = Kind<DT>;
+    using T = typename RowT<DT>::type;
+    constexpr int kPitch = 32 * KK + 8;   // of a row of t's parts: rows 16 bytes apart in the banks
+    extern __shared__ __align__(16) uint8_t smem_out[];
+    Places& P = *reinterpret_cast<Places*>(smem_out);
+    uint16_t* tp = reinterpret_cast<uint16_t*>(smem_out + sizeof(Places));   // [part][row][kPitch]
+    __shared__ float s_mul[kOuterRows];      // what a row's sums are multiplied with
+    __shared__ int s_item[kOuterRows];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
+    pdl_wait();
+    if (warp == 0) plan_tiles(a.plan, kOuterRows, P.begin, P.tile0, lane);
+    __syncthreads();
+    const int tiles = P.tile0[a.plan.owners];
+    if ((int)blockIdx.x >= tiles) return;
+    const int o = owner_of_tile(P.tile0, a.plan.owners, blockIdx.x);
+    const int first = P.begin[o] + ((int)blockIdx.x - P.tile0[o]) * kOuterRows;
+    const int rows = min(kOuterRows, P.begin[o + 1] - first);
+    const int n0 = blockIdx.y * kOuterCols + warp * 32;
+
+    // B: column j of MMA tile i of the warp is n0 + 8 * (j / 2) + 2 * i + j % 2
+    uint4 b[4][KK];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int n = n0 + 8 * (g >> 1) + 2 * i + (g & 1);
+        const uint16_t* from = static_cast<const uint16_t*>(a.B) + ((long long)o * a.N + n) * a.rank + 8 * c;
+#pragma unroll
+        for (int k = 0; k < KK; ++k)
+            b[i][k] = n < a.N && 32 * k + 8 * c < a.rank ? __ldg(reinterpret_cast<const uint4*>(from + 32 * k)) : make_uint4(0u, 0u, 0u, 0u);
+    }
+    const float scale = a.scale != nullptr ? __ldg(a.scale + o) : 1.0f;
+    // t of the rows in parts, 8 lanes or more to a row
+    constexpr int kLanes = 8 * KK > 32 ? 32 : 8 * KK;   // of a row, 4 values each
+    static_assert(kLanes * 4 == 32 * KK, "a row's values");
+    for (int r = tid / kLanes; r < (rows + 15) / 16 * 16; r += kThreads / kLanes) {
+        const int q = 4 * (tid % kLanes);
+        float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        if (r < rows && q < a.rank) {
+            const float* from = a.t + (long long)(first + r) * a.rank + q;
+            for (int s = 0; s < a.splits; ++s) {
+                const float4 w = __ldcg(reinterpret_cast<const float4*>(from + (long long)s * a.plan.items * a.rank));
+                v[0] = __fadd_rn(v[0], w.x);
+                v[1] = __fadd_rn(v[1], w.y);
+                v[2] = __fadd_rn(v[2], w.z);
+                v[3] = __fadd_rn(v[3], w.w);
+            }
+        }
+        float mul = scale;
+        uint32_t p[W::kTParts][2];
+        if constexpr (DT == kF16) {
+            float m = fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));
+#pragma unroll
+            for (int s = 1; s < kLanes; s <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, s));
+            // the largest value to 2^13 .. 2^14; infinities stay what they are
+            const int e = min(max((int)(__float_as_uint(m) >> 23) - 127, -100), 127);
+            const float by = __int_as_float((127 + 13 - e > 254 ? 254 : 127 + 13 - e) << 23);
+            mul = __fmul_rn(mul, __int_as_float((254 - (int)(__float_as_uint(by) >> 23)) << 23));
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const float x = __fmul_rn(v[2 * i], by), y = __fmul_rn(v[2 * i + 1], by);
+                const __half2 h = __floats2half2_rn(x, y);
+                const float2 f = __half22float2(h);
+                const __half2 l = __floats2half2_rn(__fsub_rn(x, f.x), __fsub_rn(y, f.y));
+                p[0][i] = *reinterpret_cast<const uint32_t*>(&h);
+                p[1][i] = *reinterpret_cast<const uint32_t*>(&l);
+            }
+        } else if constexpr (DT == kBf16) {   // rounded, 18 bits
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+                const float2 f = __bfloat1622float2(h);
+                const __nv_bfloat162 l = __floats2bfloat162_rn(__fsub_rn(v[2 * i], f.x), __fsub_rn(v[2 * i + 1], f.y));
+                p[0][i] = *reinterpret_cast<const uint32_t*>(&h);
+                p[1][i] = *reinterpret_cast<const uint32_t*>(&l);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                uint32_t w[W::kTParts];
+                split2<W::kTParts>(v[2 * i], v[2 * i + 1], w);
+#pragma unroll
+                for (int j = 0; j < W::kTParts; ++j) p[j][i] = w[j];
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < W::kTParts; ++j)
+            *reinterpret_cast<uint2*>(tp + (j * kOuterRows + r) * kPitch + q) = make_uint2(p[j][0], p[j][1]);
+        if (q == 0) {
+            s_mul[r] = mul;
+            const int item = r < rows ? __ldcg(a.plan.list + first + r) : -1;
+            s_item[r] = item >= 0 && item < a.plan.items ? item : -1;
+        }
+    }
+    __syncthreads();
+    if (n0 >= a.N) return;
+    const int n = n0 + 8 * c;
+    const bool vec = a.vec && n + 8 <= a.N;
+    for (int m = 0; m < rows; m += 16) {
+        // base of rows m + g and m + g + 8, columns n .. n + 7
+        float y[2][8];
+        int item[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            item[h] = s_item[m + g + 8 * h];
+            if (item[h] < 0) continue;
+            const T* from = static_cast<const T*>(a.base.data) + item[h] * a.base.stride + n;
+            if (vec) {
+                struct alignas(16) V { T v[16 / sizeof(T)]; };
+                constexpr int kPer = 16 / sizeof(T);
+#pragma unroll
+                for (int i = 0; i < 8 / kPer; ++i) {
+                    const V w = *reinterpret_cast<const V*>(from + kPer * i);
+#pragma unroll
+                    for (int j = 0; j < kPer; ++j) y[h][kPer * i + j] = to_f32(w.v[j]);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) y[h][i] = n + i < a.N ? to_f32(from[i]) : 0.0f;
+            }
+        }
+        float acc[4][4] = {};
+#pragma unroll
+        for (int p = W::kTParts - 1; p >= 0; --p)
+#pragma unroll
+            for (int k = 0; k < KK; ++k) {
+                const uint16_t* from = tp + (p * kOuterRows + m + g) * kPitch + 32 * k + 8 * c;
+                const uint4 lo = *reinterpret_cast<const uint4*>(from), hi = *reinterpret_cast<const uint4*>(from + 8 * kPitch);
+                const uint32_t a0[4] = {lo.x, hi.x, lo.y, hi.y}, a1[4] = {lo.z, hi.z, lo.w, hi.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    mma16816<W::kF16Mma>(acc[i], a0, b[i][k].x, b[i][k].y);
+                    mma16816<W::kF16Mma>(acc[i], a1, b[i][k].z, b[i][k].w);
+                }
+            }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            if (item[h] < 0) continue;
+            const float mul = s_mul[m + g + 8 * h];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                y[h][2 * i] = fmaf(mul, acc[i][2 * h], y[h][2 * i]);
+                y[h][2 * i + 1] = fmaf(mul, acc[i][2 * h + 1], y[h][2 * i + 1]);
+            }
+            T* to = static_cast<T*>(a.out.data) + item[h] * a.out.stride + n;
+            if (vec) {
+                struct alignas(16) V { T v[16 / sizeof(T)]; };
+                constexpr int kPer = 16 / sizeof(T);
+#pragma unroll
+                for (int i = 0; i < 8 / kPer; ++i) {
+                    V w;
+#pragma unroll
+                    for (int j = 0; j < kPer; ++j) put_as(w.v, DT, j, y[h][kPer * i + j]);
+                    *reinterpret_cast<V*>(to + kPer * i) = w;
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (n + i < a.N) put_as(to, DT, i, y[h][i]);
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Host side
+// ---------------------------------------------------------------------------
+template <typename K>
+cudaError_t allow_smem(K kernel, int bytes, std::atomic<unsigned long long>& ready) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || (ready.load(std::memory_order_acquire) >> (dev & 63) & 1)) return e;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) ready.fetch_or(1ull << (dev & 63), std::memory_order_release);
+    return e;
+}
+
+// Row tiles there may be: no more than one per adapter and one per `rows` items.
+int64_t most_tiles(const PlanView& p, int rows) { return std::min(p.items, p.owners) + p.items / rows; }
+
+// How K is split: into multiples of the warps' 256 positions, as far as it takes
+// to have two CTAs per SM.
+int inner_splits(int64_t items, int owners, int K, int groups) {
+    const int64_t likely = std::max<int64_t>(std::min<int64_t>(items, owners), items / kInnerRows) * groups;
+    const int64_t most = (K + kWarps * 32 - 1) / (kWarps * 32);
+    return (int)std::max<int64_t>(1, std::min<int64_t>({2 * 152 / likely, most, (int64_t)kMaxSplits}));
+}
+
+int rank_tiles(int rank) { return rank <= 8 ? 1 : rank <= 16 ? 2 : rank <= 32 ? 4 : 8; }   // of 8, of a CTA
+
+template <int DT, int NT>
+cudaError_t launch_inner(const LoraArgs& a, cudaStream_t s) {
+    constexpr int bytes = (int)sizeof(Places) + kWarps * kInnerRows * 8 * NT * 4;
+    static std::atomic<unsigned long long> ready{0};   // a bit per device
+    const cudaError_t e = allow_smem(k_lora_inner<DT, NT>, bytes, ready);
+    if (e != cudaSuccess) return e;
+    const dim3 grid((unsigned)most_tiles(a.plan, kInnerRows), (unsigned)a.splits, (unsigned)((a.rank + 8 * NT - 1) / (8 * NT)));
+    return launch_pdl(k_lora_inner<DT, NT>, grid, dim3(kThreads), bytes, s, a);
+}
+
+template <int DT, int KK>
+cudaError_t launch_outer(const LoraArgs& a, cudaStream_t s) {
+    constexpr int bytes = (int)sizeof(Places) + Kind<DT>::kTParts * kOuterRows * (32 * KK + 8) * 2;
+    static std::atomic<unsigned long long> ready{0};
+    const cudaError_t e = allow_smem(k_lora_outer<DT, KK>, bytes, ready);
+    if (e != cudaSuccess) return e;
+    const dim3 grid((unsigned)most_tiles(a.plan, kOuterRows), (unsigned)((a.N + kOuterCols - 1) / kOuterCols));
+    return launch_pdl(k_lora_outer<DT, KK>, grid, dim3(kThreads), bytes, s, a);
+}
+
+template <int DT>
+cudaError_t launch_lora(const LoraArgs& a, cudaStream_t s) {
+    const int nt = rank_tiles(a.rank);
+    cudaError_t e = nt == 1 ? launch_inner<DT, 1>(a, s) : nt == 2 ? launch_inner<DT, 2>(a, s)
+                  : nt == 4 ? launch_inner<DT, 4>(a, s) : launch_inner<DT, 8>(a, s);
+    if (e != cudaSuccess) return e;
+    if (a.rank <= 32) return launch_outer<DT, 1>(a, s);
+    if (a.rank <= 64) return launch_outer<DT, 2>(a, s);
+    return launch_outer<DT, 4>(a, s);
+}
+
+int check_adapters(const lora_adapters* a, const route_plan* plan) {
+    if (!a) return I2S_E_NULL_PTR;
+    const int r = check_plan_sizes(plan);
+    if (r) return r;
+    if (a->adapters < 1 || a->adapters > kMaxOwners || plan->owners != a->adapters || a->rank < 8 || a->rank > kMaxRank ||
+        a->rank % 8 || a->K < 8 || a->K % 8 || a->K > 65536 || a->N < 1 || a->N > (1 << 24))
+        return I2S_E_BAD_SHAPE;
+    return I2S_OK;
+}
+
+}  // namespace
+}  // namespace i2s
+
+using namespace i2s;
+
+#pragma GCC visibility push(default)
+extern "C" {
+
+size_t lora_add_workspace(const lora_adapters* a, const route_plan* plan) {
+    if (check_adapters(a, plan)) return 0;
+    const int splits = inner_splits(plan->items, plan->owners, (int)a->K, (a->rank + 63) / 64);
+    return up_256((size_t)splits * plan->items * a->rank * 4);
+}
+
+int lora_add(const lora_adapters* a, const route_plan* plan, const i2s_rows* x, const i2s_rows* base, const i2s_rows* out,
+             void* ws, size_t ws_bytes, i2s_stream_t stream) {
+    int r = check_adapters(a, plan);
+    if (r) return r;
+    if ((r = check_plan(plan))) return r;
+    if (!a->A || !a->B || !ws) return I2S_E_NULL_PTR;
+    const int64_t rows = plan->items;
+    if ((r = check_row_tensor(x, rows, a->K, true, false)) || (r = check_row_tensor(base, rows, a->N, false, false)) ||
+        (r = check_row_tensor(out, rows, a->N, false, true)))
+        return r;
+    if (x->dtype != base->dtype || x->dtype != out->dtype || a->dtype != (x->dtype == kF16 ? kF16 : kBf16)) return I2S_E_BAD_ARG;
+    if (((uintptr_t)a->A & 15) || ((uintptr_t)a->B & 15) || ((uintptr_t)a->scale & 3) || ((uintptr_t)ws & 255))
+        return I2S_E_MISALIGNED;
+    const size_t need = lora_add_workspace(a, plan);
+    if (ws_bytes < need) return I2S_E_WORKSPACE_TOO_SMALL;
+    const Span sa = span_of(a->A, (size_t)a->adapters * a->rank * a->K * 2), sb = span_of(a->B, (size_t)a->adapters * a->N * a->rank * 2);
+    const Span sc = span_of(a->scale, a->scale ? (size_t)a->adapters * 4 : 0), sx = rows_span(*x, rows, a->K);
+    const Span sbase = rows_span(*base, rows, a->N), so = rows_span(*out, rows, a->N), sw = span_of(ws, need);
+    for (const Span& t : {so, sw})
+        if (t.meets(sa) || t.meets(sb) || t.meets(sc) || t.meets(sx) || meets_plan(t, *plan)) return I2S_E_BAD_ARG;
+    const bool same = out->data == base->data && (rows == 1 || out->stride == base->stride);
+    if (sw.meets(sbase) || sw.meets(so) || (!same && so.meets(sbase))) return I2S_E_BAD_ARG;
+    if ((r = check_current_device())) return r;
+
+    LoraArgs p;
+    p.plan = plan_view(*plan);
+    p.A = a->A;
+    p.B = a->B;
+    p.scale = a->scale;
+    p.x = {x->data, x->stride};
+    p.base = {base->data, base->stride};
+    p.out = {out->data, out->stride};
+    p.t = static_cast<float*>(ws);
+    p.K = (int)a->K;
+    p.N = (int)a->N;
+    p.rank = a->rank;
+    p.splits = inner_splits(rows, p.plan.owners, p.K, (a->rank + 63) / 64);
+    p.k_per = ((p.K + p.splits - 1) / p.splits + kWarps * 32 - 1) / (kWarps * 32) * (kWarps * 32);
+    p.splits = (p.K + p.k_per - 1) / p.k_per;   // none empty
+    const int size = dtype_bytes(x->dtype);
+    p.vec = !(((uintptr_t)base->data | (uintptr_t)out->data) & 15) &&
+            (rows == 1 || (base->stride * size % 16 == 0 && out->stride * size % 16 == 0));
+    cudaError_t e;
+    if (x->dtype == kF32) e = launch_lora<kF32>(p, stream);
+    else if (x->dtype == kF16) e = launch_lora<kF16>(p, stream);
+    else e = launch_lora<kBf16>(p, stream);
+    return e == cudaSuccess ? I2S_OK : I2S_E_CUDA;
+}
+
+}  // extern "C"
+#pragma GCC visibility pop

@@ -60,6 +60,24 @@ class kv8_rows(ctypes.Structure):
     _fields_ = [("data", _p), ("row_stride", _i64), ("head_stride", _i64), ("dtype", _int)]
 
 
+class route_plan_t(ctypes.Structure):
+    _fields_ = [("start", _p), ("list", _p), ("items", _i64), ("owners", _int)]
+
+
+class i2s_rows(ctypes.Structure):
+    _fields_ = [("data", _p), ("stride", _i64), ("dtype", _int)]
+
+
+class w8a8_experts(ctypes.Structure):
+    _fields_ = [("wq", _p), ("bscale", _p), ("N", _i64), ("K", _i64), ("experts", _int)]
+
+
+class lora_adapters(ctypes.Structure):
+    _fields_ = [("A", _p), ("B", _p), ("scale", _p), ("K", _i64), ("N", _i64), ("rank", _int), ("adapters", _int),
+                ("dtype", _int)]
+
+
+_plan_p, _row_p, _experts_p, _lora_p = (ctypes.POINTER(t) for t in (route_plan_t, i2s_rows, w8a8_experts, lora_adapters))
 _cache_p, _batch_p, _rows_p = (ctypes.POINTER(t) for t in (kv8_cache, kv8_batch, kv8_rows))
 
 _SIGS = {
@@ -126,6 +144,13 @@ _SIGS = {
     "kv8_attention_workspace": (_sz, [_cache_p, _batch_p, _int]),
     "kv8_attention": (_int, [_cache_p, _batch_p, _rows_p, _int, _rows_p, _f32, ctypes.c_uint, _int, _p, _p, _sz, _p]),
     "kv8_read_status": (_int, [_p, ctypes.POINTER(ctypes.c_int32), _p]),
+    "route_plan_workspace": (_sz, [_i64, _int]),
+    "route_plan_build": (_int, [_p, _plan_p, _p, _sz, _p]),
+    "route_topk": (_int, [_row_p, _i64, _int, _int, _p, _f32, ctypes.c_uint, _p, _p, _plan_p, _p, _sz, _p]),
+    "w8a8_mul_mat_experts_workspace": (_sz, [_experts_p, _plan_p, _int, _int, ctypes.c_uint]),
+    "w8a8_mul_mat_experts": (_int, [_experts_p, _plan_p, _row_p, _int, _row_p, _p, _int, ctypes.c_uint, _p, _sz, _p]),
+    "lora_add_workspace": (_sz, [_lora_p, _plan_p]),
+    "lora_add": (_int, [_lora_p, _plan_p, _row_p, _row_p, _row_p, _p, _sz, _p]),
 }
 for _name, (_res, _args) in _SIGS.items():
     _fn = getattr(_L, _name)
@@ -906,6 +931,213 @@ def kv8_norm_rope(q, k, positions=None, turns=None, **kw):
 def kv8_attention(cache, batch, q, **kw):
     """Attention of q over the cache; arguments as Kv8Attention."""
     call = Kv8Attention(cache, batch, q, **kw)
+    call()
+    return call.out
+
+
+# -- rows that have weights of their own --------------------------------------------
+
+ROUTE_MAX_OWNERS, ROUTE_MAX_ITEMS, ROUTE_MAX_CHOSEN = 1024, 1 << 27, 16
+ROUTE_SIGMOID, ROUTE_NORM = 1, 2
+W8A8_SWIGLU = 1
+W8A8_TEST_STALL = 1 << 31   # tests only
+
+
+def _row_tensor(t, rows, width, device, what):
+    """i2s_rows of a rows x width CUDA tensor with contiguous rows (which may be strided, as slices are)."""
+    torch = _torch()
+    dtypes = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
+    if t.device != device or t.dim() != 2 or tuple(t.shape) != (rows, width) or (width > 1 and t.stride(1) != 1):
+        raise ValueError(f"{what}: expected {(rows, width)} with contiguous rows on {device}, got {tuple(t.shape)} on {t.device}")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{what}: expected float32, float16 or bfloat16, got {t.dtype}")
+    return i2s_rows(t.data_ptr(), t.stride(0), dtypes[t.dtype])
+
+
+def _values(t, dtype, n, device, what):
+    """The pointer of n contiguous values, or None."""
+    if t is None:
+        return None
+    if t.dtype != dtype or t.numel() != n or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{what}: expected {n} contiguous values of {dtype} on {device}")
+    return t.data_ptr()
+
+
+def _cuda_device(device):
+    torch = _torch()
+    device = torch.device(device)
+    if device.type != "cuda":
+        raise ValueError("expected a CUDA tensor")
+    return torch.device("cuda", torch.cuda.current_device() if device.index is None else device.index)
+
+
+def _int_arg(value, what, bits=31):
+    value = int(value)
+    if not -(1 << bits) <= value < 1 << bits:
+        raise ValueError(f"{what} out of range")
+    return value
+
+
+class RoutePlan:
+    """Items sorted by owner: owner o's are list[start[o]:start[o + 1]]. int32
+    device tensors of owners + 1 and items, made if not given; a RouteBuild or RouteTopk
+    fills them, or the caller."""
+
+    def __init__(self, items: int, owners: int, start=None, list=None, device="cuda"):
+        torch = _torch()
+        self.device = _cuda_device(start.device if start is not None else list.device if list is not None else device)
+        self.items, self.owners = _int_arg(items, "items", 63), _int_arg(owners, "owners")
+        if not (1 <= self.items <= ROUTE_MAX_ITEMS and 1 <= self.owners <= ROUTE_MAX_OWNERS):
+            raise I2SError("route_plan", -1)
+        self.start = start if start is not None else torch.zeros(self.owners + 1, dtype=torch.int32, device=self.device)
+        self.list = list if list is not None else torch.zeros(self.items, dtype=torch.int32, device=self.device)
+        self.struct = route_plan_t(_values(self.start, torch.int32, self.owners + 1, self.device, "start"),
+                                   _values(self.list, torch.int32, self.items, self.device, "list"), self.items, self.owners)
+
+
+def _on(device, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name}: on {t.device}, not on {device}")
+
+
+class RouteBuild(_Kv8Call):
+    """route_plan_build: the plan of the items whose owners are given (int32
+    device tensor; a value outside [0, owners) means none)."""
+
+    def __init__(self, owner, owners: int, plan=None, ws=None):
+        device = _cuda_device(owner.device)
+        self.plan = plan if plan is not None else RoutePlan(owner.numel(), owners, device=device)
+        _on(device, plan=self.plan, ws=ws)
+        if self.plan.owners != owners:
+            raise ValueError("the plan is of other owners")
+        self.ws = ws if ws is not None else _ws(_L.route_plan_workspace(self.plan.items, owners), device)
+        self._keep = owner
+        self._bind("route_plan_build", device, _values(owner, _torch().int32, self.plan.items, device, "owner"),
+                   self.plan.struct, _dptr(self.ws), self.ws.numel())
+
+
+class RouteTopk(_Kv8Call):
+    """route_topk: the k largest of each row's logits (rows x experts) with their
+    weights, in `expert` and `weight` (rows x k), and the plan of the items row*k + j.
+    bias: F32 [experts], added for the choice alone; plan=False for none."""
+
+    def __init__(self, logits, k: int, bias=None, factor: float = 1.0, sigmoid: bool = False, norm: bool = False,
+                 expert=None, weight=None, plan=None, ws=None):
+        torch = _torch()
+        if logits.dim() != 2:
+            raise ValueError("logits: expected rows x experts")
+        device, (rows, experts), k = _cuda_device(logits.device), logits.shape, _int_arg(k, "k")
+        if not 1 <= k <= min(experts, ROUTE_MAX_CHOSEN) or rows < 1 or rows * k > ROUTE_MAX_ITEMS:
+            raise I2SError("route_topk", -1)
+        if plan is None:
+            plan = RoutePlan(rows * k, experts, device=device)
+        self.expert = expert if expert is not None else torch.empty((rows, k), dtype=torch.int32, device=device)
+        self.weight = weight if weight is not None else torch.empty((rows, k), dtype=torch.float32, device=device)
+        self.plan = plan or None
+        _on(device, plan=self.plan, ws=ws)
+        if self.plan is not None and ws is None:
+            ws = _ws(_L.route_plan_workspace(rows * k, experts), device)
+        self.ws, self._keep = ws, (logits, bias)
+        self._bind("route_topk", device, _row_tensor(logits, rows, experts, device, "logits"), rows, experts, k,
+                   _values(bias, torch.float32, experts, device, "bias"), float(factor),
+                   (ROUTE_SIGMOID if sigmoid else 0) | (ROUTE_NORM if norm else 0),
+                   _values(self.expert, torch.int32, rows * k, device, "expert"),
+                   _values(self.weight, torch.float32, rows * k, device, "weight"),
+                   self.plan.struct if self.plan is not None else None, _dptr(ws), ws.numel() if ws is not None else 0)
+
+
+class W8A8Experts(_Kv8Call):
+    """w8a8_mul_mat_experts: wq (experts x N x K int8), bscale (experts x N F32), a
+    plan over the items, x (items/x_group x K). out has a row per item of N values (swiglu: N/2),
+    or with weight (rows x k, F32) a row for each of weight's, the weighted
+    sum of its k items."""
+
+    def __init__(self, wq, bscale, plan, x, out=None, x_group: int = 1, swiglu: bool = False, weight=None, ws=None,
+                 test_stall: bool = False):
+        torch = _torch()
+        if wq.dim() != 3 or x.dim() != 2:
+            raise ValueError("wq: expected experts x N x K, x: rows x K")
+        device, (experts, N, K), x_group = _cuda_device(wq.device), wq.shape, _int_arg(x_group, "x_group")
+        _on(device, plan=plan, ws=ws)
+        y_group = 1
+        if weight is not None:
+            if weight.dim() != 2 or weight.shape[1] < 1:
+                raise ValueError("weight: expected rows x k")
+            y_group = weight.shape[1]
+        flags = (W8A8_SWIGLU if swiglu else 0) | (W8A8_TEST_STALL if test_stall else 0)
+        w = w8a8_experts(_values(wq, torch.int8, experts * N * K, device, "wq"),
+                         _values(bscale, torch.float32, experts * N, device, "bscale"), N, K, experts)
+        need = int(_L.w8a8_mul_mat_experts_workspace(w, plan.struct, x_group, y_group, flags))
+        if need == 0:
+            raise I2SError("w8a8_mul_mat_experts_workspace", -1)
+        rows, width = plan.items // y_group, N // 2 if swiglu else N
+        if out is None:
+            # rows of items without an expert are not written
+            out = torch.zeros((rows, width), dtype=x.dtype, device=device)
+        self.out, self.ws = out, ws if ws is not None else _ws(need, device)
+        self._keep = (wq, bscale, plan, x, weight)
+        self._bind("w8a8_mul_mat_experts", device, w, plan.struct,
+                   _row_tensor(x, plan.items // x_group, K, device, "x"), x_group,
+                   _row_tensor(out, rows, width, device, "out"), _values(weight, torch.float32, plan.items, device, "weight"),
+                   y_group, flags, _dptr(self.ws), self.ws.numel())
+
+    def check(self):
+        """Raises if a wait of the latest call ran out; waits for the current stream."""
+        _check("w8a8_mul_mat_experts", read_status(self.ws))
+
+
+class LoraAdd(_Kv8Call):
+    """lora_add: out = base + scale[a] * B[a] (A[a] x) for the rows of each adapter
+    a in the plan (items = rows). A: adapters x rank x K, B: adapters x N x rank, float16 or
+    bfloat16; scale: F32 [adapters] or None. out may be base (the default), in place."""
+
+    def __init__(self, A, B, plan, x, base, out=None, scale=None, ws=None):
+        torch = _torch()
+        if A.dim() != 3 or B.dim() != 3:
+            raise ValueError("A: expected adapters x rank x K, B: adapters x N x rank")
+        device, (adapters, rank, K), N = _cuda_device(A.device), A.shape, B.shape[1]
+        if tuple(B.shape) != (adapters, N, rank) or A.dtype != B.dtype or A.dtype not in (torch.float16, torch.bfloat16):
+            raise ValueError("A and B: expected adapters x rank x K and adapters x N x rank of float16 or bfloat16")
+        _on(device, plan=plan, ws=ws)
+        half = A.dtype
+        a = lora_adapters(_values(A, half, adapters * rank * K, device, "A"), _values(B, half, adapters * N * rank, device, "B"),
+                          _values(scale, torch.float32, adapters, device, "scale"), K, N, rank, adapters,
+                          1 if half == torch.float16 else 2)
+        need = int(_L.lora_add_workspace(a, plan.struct))
+        if need == 0:
+            raise I2SError("lora_add_workspace", -1)
+        self.out, self.ws = base if out is None else out, ws if ws is not None else _ws(need, device)
+        self._keep = (A, B, plan, x, base, scale)
+        self._bind("lora_add", device, a, plan.struct, _row_tensor(x, plan.items, K, device, "x"),
+                   _row_tensor(base, plan.items, N, device, "base"), _row_tensor(self.out, plan.items, N, device, "out"),
+                   _dptr(self.ws), self.ws.numel())
+
+
+def route_plan(owner, owners: int, **kw):
+    """The plan of the items whose owners are given; arguments as RouteBuild."""
+    call = RouteBuild(owner, owners, **kw)
+    call()
+    return call.plan
+
+
+def route_topk(logits, k: int, **kw):
+    """(expert, weight, plan) of each row; arguments as RouteTopk."""
+    call = RouteTopk(logits, k, **kw)
+    call()
+    return call.expert, call.weight, call.plan
+
+
+def w8a8_mul_mat_experts(wq, bscale, plan, x, **kw):
+    """Products grouped by expert; arguments as W8A8Experts."""
+    call = W8A8Experts(wq, bscale, plan, x, **kw)
+    call()
+    return call.out
+
+
+def lora_add(A, B, plan, x, base, **kw):
+    """base plus each row's adapter; arguments as LoraAdd."""
+    call = LoraAdd(A, B, plan, x, base, **kw)
     call()
     return call.out
 
