@@ -23,8 +23,9 @@
 // Weights stay one byte in memory and in the ring that TMA fills (128 channels x
 // 128 positions); converter warps, one thread per channel, turn them into f16 and
 // put them into tensor memory, from where the MMA takes its A operand. The rows
-// are gathered by TMA (gather4: four rows of the quantized x by their index), so
-// a row that eight experts read is neither copied nor laid out eight times.
+// are quantized into the plan's order, a row that eight experts read eight times, so that TMA
+// loads a tile of neighbours. (Gathered by their index instead, four to a copy, a stage
+// of 128 rows took 4000 cycles: 857 us for 4096 rows of 8 of 128 experts.)
 //
 // SWIGLU: a unit's 128 channels are 64 gate and the 64 up channels of the same
 // index, in blocks of 16 and 16 (a five-dimensional box of the weights as they lie): a
@@ -32,7 +33,7 @@
 // finishes one of two neighbouring rows after one exchange.
 //
 // Roles (512 threads): warps 0-3 epilogue, 4-11 converters (two groups taking
-// stages by turns), 12 weights, 13 gathered rows, 14 MMAs. TMEM: two accumulators
+// stages by turns), 12 weights, 13 rows, 14 MMAs. TMEM: two accumulators
 // of ROWS columns, then a ring of 64-column operands. Waits are bounded; one that runs
 // out sets the status word at the start of the workspace and the CTA's abort
 // flag, roles leave their loops, and what they issued is drained.
@@ -68,9 +69,10 @@ constexpr int kRegsEpilogue = 208, kRegsConvert = 104, kRegsIssue = 56;
 template <int ROWS>
 struct Shape {
     // Few rows per expert: the weights' bytes count, and get the shared memory.
-    // Many: the gathered rows do.
-    static constexpr int kSlots = ROWS == 32 ? 6 : 4;      // operands: gathered rows, and weights in TMEM
+    // Many: the rows do.
+    static constexpr int kSlots = ROWS == 32 ? 6 : 4;      // operands: rows, and weights in TMEM
     static constexpr int kWSlots = ROWS == 32 ? 10 : 5;    // weights as bytes
+    static constexpr int kBox = ROWS == 32 ? 16 : 32;      // rows of a copy
     static constexpr int kAtom = ROWS * 128;               // 64 positions of the rows
     static constexpr int kRowStage = 2 * kAtom;
     static constexpr uint32_t kOp0 = 2 * ROWS;             // first TMEM column of the operands
@@ -138,14 +140,6 @@ __device__ __forceinline__ void load_pairs(void* dst, const CUtensorMap* map, in
         "l"(map), "r"(k), "r"(0), "r"(block), "r"(e), "r"(tc::smem_u32(bar))
         : "memory");
 }
-__device__ __forceinline__ void gather_rows(void* dst, const CUtensorMap* map, int k, const int (&r)[4], uint64_t* bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, "
-        "%4, %5, %6}], [%7];" ::"r"(tc::smem_u32(dst)),
-        "l"(map), "r"(k), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(tc::smem_u32(bar))
-        : "memory");
-}
-
 // Codes 0, 1 (SEL 0x4140) or 2, 3 (0x4342) of four biased by 128, as f16:
 // the byte in the mantissa of 1024, less 1152.
 template <int SEL>
@@ -155,17 +149,40 @@ __device__ __forceinline__ uint32_t codes2(uint32_t x) {
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// x / (1 + exp(-x)); the reciprocal within one unit of its last place, and without the branches of
+// the exact quotient, around which nothing else would be scheduled.
+__device__ __forceinline__ float silu(float x) {
+    float r;
+    asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(__fadd_rn(1.0f, expf(-x))));
+    return __fmul_rn(x, r);
+}
+
+__device__ __forceinline__ void put(float* p, float v) { *p = v; }
+__device__ __forceinline__ void put(__half* p, float v) { *p = __float2half_rn(v); }
+__device__ __forceinline__ void put(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+
+// Values of up to 32 rows, channel n, of which `left` are the unit's. PAIRS: v[i] is of row i + mine, i even.
+template <typename T, bool PAIRS>
+__device__ __forceinline__ void store_rows(void* y, const Shared::Row* row, const float* v, int left, int mine, int n) {
+    T* to = static_cast<T*>(y) + n;
+#pragma unroll
+    for (int i = 0; i < 32; i += PAIRS ? 2 : 1) {
+        const long long off = row[i + (PAIRS ? mine : 0)].off;
+        if (i + mine < left && off >= 0) put(to + off, v[i]);
+    }
+}
+
 }  // namespace xp
 
 struct ExpertArgs {
     CUtensorMap wmap, xmap;
     PlanView plan;
     const float* bscale;
-    const float* ascale;    // workspace, one per x row
+    const float* ascale;    // workspace, one per place of the list, as the codes
     void* y;                // y, or the workspace's F32 rows that are then weighted
     long long y_stride;
     int y_dtype;
-    int x_group, N, K, tiles_n;
+    int N, K, tiles_n;
     uint8_t* used;          // workspace: items that have an expert, or null
     uint32_t* status;
     bool test_stall;
@@ -254,7 +271,7 @@ __global__ void __launch_bounds__(xp::kThreads, 1) k_experts(const __grid_consta
                 Shared::Row row = {-1, 0.0f, 0};
                 if (item >= 0 && item < a.plan.items) {
                     row.off = item * a.y_stride;
-                    row.scale = __ldcg(a.ascale + item / a.x_group);
+                    row.scale = __ldcg(a.ascale + t.first + i);
                     if (a.used != nullptr && t.n0 == 0 && warp == 0) a.used[item] = 1;
                 }
                 S.row[warp][i] = row;
@@ -304,34 +321,32 @@ __global__ void __launch_bounds__(xp::kThreads, 1) k_experts(const __grid_consta
                 if (lane == 0) tc::mbar_arrive(&S.dempty[buf]);
             }
             if (!ok) break;
+            const int mine = SWIGLU ? lane >> 4 : 0;
 #pragma unroll
             for (int p = 0; p < ROWS / 32; ++p) {
                 if (32 * p < t.rows) {
+                    float* v = sum + 32 * p;
                     if (chunks > 2) {
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) sum[32 * p + i] = __int2float_rn(__float_as_int(sum[32 * p + i]));
+                        for (int i = 0; i < 32; ++i) v[i] = __int2float_rn(__float_as_int(v[i]));
                     }
+                    const Shared::Row* row = S.row[warp] + 32 * p;
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v[i] = __fmul_rn(__fmul_rn(row[i].scale, b), v[i]);
                     if (SWIGLU) {
+                        // the lower half warp finishes row i, the upper row i + 1
 #pragma unroll
                         for (int i = 0; i < 32; i += 2) {
-                            const Shared::Row r0 = S.row[warp][32 * p + i], r1 = S.row[warp][32 * p + i + 1];
-                            const float d0 = __fmul_rn(__fmul_rn(r0.scale, b), sum[32 * p + i]);
-                            const float d1 = __fmul_rn(__fmul_rn(r1.scale, b), sum[32 * p + i + 1]);
-                            // the lower half warp finishes row i, the upper row i + 1
-                            const float other = __shfl_xor_sync(0xffffffffu, lane < 16 ? d1 : d0, 16);
-                            const float g = lane < 16 ? d0 : other, up = lane < 16 ? other : d1;
-                            const float h = __fmul_rn(__fdiv_rn(g, __fadd_rn(1.0f, expf(-g))), up);
-                            const long long off = lane < 16 ? r0.off : r1.off;
-                            if (live && 32 * p + i + (lane >> 4) < t.rows && off >= 0) put_as(a.y, a.y_dtype, off + n, h);
-                        }
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            const Shared::Row r0 = S.row[warp][32 * p + i];
-                            const float d = __fmul_rn(__fmul_rn(r0.scale, b), sum[32 * p + i]);
-                            if (live && 32 * p + i < t.rows && r0.off >= 0) put_as(a.y, a.y_dtype, r0.off + n, d);
+                            const float other = __shfl_xor_sync(0xffffffffu, mine ? v[i] : v[i + 1], 16);
+                            const float g = mine ? other : v[i], up = mine ? v[i + 1] : other;
+                            v[i] = __fmul_rn(silu(g), up);
                         }
                     }
+                    // (no value's computation hangs on another's store: the chains run side by side)
+                    const int left = live ? t.rows - 32 * p : 0;
+                    if (a.y_dtype == kF32) store_rows<float, SWIGLU>(a.y, row, v, left, mine, n);
+                    else if (a.y_dtype == kF16) store_rows<__half, SWIGLU>(a.y, row, v, left, mine, n);
+                    else store_rows<__nv_bfloat16, SWIGLU>(a.y, row, v, left, mine, n);
                 }
             }
         }
@@ -416,51 +431,35 @@ __global__ void __launch_bounds__(xp::kThreads, 1) k_experts(const __grid_consta
                     tc::mbar_wait_drain(&S.wfull[i % S_::kWSlots], (uint32_t)(i / S_::kWSlots) & 1, kWait / 8);
             }
         } else if (warp == kRowWarp) {
-            // -------------------------------------------------- gathered rows
-            pdl_wait();
-            const int x_rows = a.plan.items / a.x_group;
-            int at = 0;
-            bool ok = true;
-            // lane l gathers rows 4l .. 4l + 3 of the unit; places behind its last row get the last row again
-            auto rows_of = [&](int u, int (&r)[4], int& groups) {
-                groups = 0;
-                if (u >= units) return;
-                const Unit t = unit_at(u);
-                groups = (t.rows + 3) / 4;
-                if (lane >= groups) return;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int item = __ldcg(a.plan.list + t.first + min(4 * lane + i, t.rows - 1));
-                    r[i] = min(max(item / a.x_group, 0), x_rows - 1);
-                }
-            };
-            int r[4], groups;
-            rows_of(blockIdx.x, r, groups);
-            for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
-                int next[4], next_groups;
-                rows_of(u + gridDim.x, next, next_groups);
-                for (int k = 0; k < steps; ++k, ++at) {
-                    const int slot = at % S_::kSlots;
-                    if (!tc::mbar_wait(&S.empty[slot], ((uint32_t)(at / S_::kSlots) & 1) ^ 1, abort_flag, kWait)) { fail(); ok = false; }
-                    ok = __all_sync(0xffffffffu, ok) != 0;
-                    if (!ok) break;
-                    // the second half of the stage is left out where the row ends in the first
-                    const bool both = k * kStep + 64 < a.K;
-                    if (lane == 0) tc::mbar_arrive_expect_tx(&S.bfull[slot], (uint32_t)groups * (both ? 1024u : 512u));
-                    __syncwarp();
-                    if (lane < groups) {
-                        uint8_t* dst = sRows + slot * S_::kRowStage + lane * 512;
-                        gather_rows(dst, &a.xmap, k * kStep, r, &S.bfull[slot]);
-                        if (both) gather_rows(dst + S_::kAtom, &a.xmap, k * kStep + 64, r, &S.bfull[slot]);
+            // ---------------------------------------------------------- rows
+            if (lane == 0) {
+                pdl_wait();
+                int at = 0;
+                bool ok = true;
+                for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
+                    const Unit t = unit_at(u);
+                    const int boxes = (t.rows + S_::kBox - 1) / S_::kBox;
+                    for (int k = 0; k < steps; ++k, ++at) {
+                        const int slot = at % S_::kSlots;
+                        if (!tc::mbar_wait(&S.empty[slot], ((uint32_t)(at / S_::kSlots) & 1) ^ 1, abort_flag, kWait)) {
+                            fail();
+                            ok = false;
+                            break;
+                        }
+                        // the second half of the stage is left out where the row ends in the first
+                        const bool both = k * kStep + 64 < a.K;
+                        tc::mbar_arrive_expect_tx(&S.bfull[slot], (uint32_t)(boxes * S_::kBox * (both ? 256 : 128)));
+                        uint8_t* dst = sRows + slot * S_::kRowStage;
+                        for (int i = 0; i < boxes; ++i) {
+                            const int row = t.first + i * S_::kBox;
+                            tc::tma_load_2d(dst + i * S_::kBox * 128, &a.xmap, k * kStep, row, &S.bfull[slot]);
+                            if (both) tc::tma_load_2d(dst + S_::kAtom + i * S_::kBox * 128, &a.xmap, k * kStep + 64, row, &S.bfull[slot]);
+                        }
                     }
-                    __syncwarp();
                 }
-#pragma unroll
-                for (int i = 0; i < 4; ++i) r[i] = next[i];
-                groups = next_groups;
+                for (int i = max(0, at - S_::kSlots); i < at; ++i)
+                    tc::mbar_wait_drain(&S.bfull[i % S_::kSlots], (uint32_t)(i / S_::kSlots) & 1, kWait / 8);
             }
-            for (int i = max(0, at - S_::kSlots); i < at; ++i)
-                tc::mbar_wait_drain(&S.bfull[i % S_::kSlots], (uint32_t)(i / S_::kSlots) & 1, kWait / 8);
         } else if (warp == kMmaWarp) {
             // ---------------------------------------------------------- MMAs
             const uint32_t lead = lane == 0;
@@ -513,7 +512,7 @@ __global__ void __launch_bounds__(xp::kThreads, 1) k_experts(const __grid_consta
 }
 
 // ---------------------------------------------------------------------------
-// Rows of x as f16 codes and a scale: amax floored at 1e-9, scale = amax/127,
+// The rows of x as f16 codes and a scale, in the plan's order: amax floored at 1e-9, scale = amax/127,
 // q = clamp(round(x * (127/amax)), -127, 127), halves away from zero (as every
 // W8A8 call). A row with an infinity or NaN gets the scale NaN and codes of zero: its
 // outputs are NaN, and no others. TPR threads per row, four values at a time,
@@ -522,8 +521,8 @@ __global__ void __launch_bounds__(xp::kThreads, 1) k_experts(const __grid_consta
 constexpr int kRowThreads = 256, kKeep = 8;
 
 template <int DT, int TPR>
-__global__ void __launch_bounds__(kRowThreads) k_expert_rows(RowsView x, int rows, int K, __half* q, float* ascale,
-                                                             uint8_t* used, int items, uint32_t* status) {
+__global__ void __launch_bounds__(kRowThreads) k_expert_rows(RowsView x, PlanView plan, int x_group, int K, __half* q,
+                                                             float* ascale, uint8_t* used, uint32_t* status) {
     using T = typename RowT<DT>::type;
     struct alignas(sizeof(T) * 4) V4 { T v[4]; };
     constexpr int kRowsPer = kRowThreads / TPR;
@@ -532,12 +531,15 @@ __global__ void __launch_bounds__(kRowThreads) k_expert_rows(RowsView x, int row
     pdl_launch_next();
     if (blockIdx.x == 0 && threadIdx.x == 0) *status = 0u;
     if (used != nullptr)
-        for (int i = blockIdx.x * kRowThreads + threadIdx.x; i < (items + 3) / 4; i += gridDim.x * kRowThreads)
+        for (int i = blockIdx.x * kRowThreads + threadIdx.x; i < (plan.items + 3) / 4; i += gridDim.x * kRowThreads)
             reinterpret_cast<uint32_t*>(used)[i] = 0u;
     const int part = threadIdx.x % TPR;
-    const int row = blockIdx.x * kRowsPer + threadIdx.x / TPR;
-    const bool here = row < rows;
-    const V4* from = reinterpret_cast<const V4*>(static_cast<const T*>(x.data) + (here ? row * x.stride : 0));
+    const int place = blockIdx.x * kRowsPer + threadIdx.x / TPR;
+    int item = place < plan_end(plan) ? __ldcg(plan.list + place) : -1;
+    if (item >= plan.items) item = -1;
+    const bool here = item >= 0;
+    const long long row = here ? item / x_group : 0;
+    const V4* from = reinterpret_cast<const V4*>(static_cast<const T*>(x.data) + row * x.stride);
     const int n4 = here ? K / 4 : 0;
     V4 keep[kKeep];
     float mx = 0.0f;
@@ -571,8 +573,8 @@ __global__ void __launch_bounds__(kRowThreads) k_expert_rows(RowsView x, int row
     finite = mx != INFINITY;
     mx = fmaxf(mx, 1e-9f);
     const float inv = finite ? __fdiv_rn(127.0f, mx) : 0.0f;
-    if (part == 0) ascale[row] = finite ? __fdiv_rn(mx, 127.0f) : __int_as_float(0x7fc00000);
-    uint2* to = reinterpret_cast<uint2*>(q + (long long)row * K);
+    if (part == 0) ascale[place] = finite ? __fdiv_rn(mx, 127.0f) : __int_as_float(0x7fc00000);
+    uint2* to = reinterpret_cast<uint2*>(q + (long long)place * K);
     auto put = [&](int i, const V4& w) {
         uint32_t c[2];
 #pragma unroll
@@ -627,11 +629,11 @@ struct Layout {
     size_t ascale, q, used, d, total;
 };
 
-Layout layout_of(int64_t items, int64_t x_rows, int64_t N, int64_t K) {
+Layout layout_of(int64_t items, int64_t N, int64_t K) {
     Layout l;
     l.ascale = 256;   // the status word before it
-    l.q = l.ascale + up_256((size_t)x_rows * 4);
-    l.used = l.q + up_256((size_t)x_rows * K * 2);
+    l.q = l.ascale + up_256((size_t)items * 4);
+    l.used = l.q + up_256((size_t)items * K * 2);
     l.d = l.used + up_256((size_t)items);
     l.total = l.d + up_256((size_t)items * N * 4);
     return l;
@@ -669,11 +671,11 @@ cudaError_t launch_product(const ExpertArgs& a, int grid, cudaStream_t s) {
 }
 
 template <int DT>
-cudaError_t launch_rows(const RowsView& x, int rows, int K, __half* q, float* ascale, uint8_t* used, int items,
+cudaError_t launch_rows(const RowsView& x, const PlanView& plan, int x_group, int K, __half* q, float* ascale, uint8_t* used,
                         uint32_t* status, cudaStream_t s) {
     auto go = [&](auto kernel, int per) {
-        return launch_pdl(kernel, dim3((unsigned)((rows + per - 1) / per)), dim3(kRowThreads), 0, s, x, rows, K, q, ascale, used,
-                          items, status);
+        return launch_pdl(kernel, dim3((unsigned)((plan.items + per - 1) / per)), dim3(kRowThreads), 0, s, x, plan, x_group, K, q,
+                          ascale, used, status);
     };
     // the fewest threads that hold a row
     if (K <= 32 * 4 * kKeep) return go(k_expert_rows<DT, 32>, kRowThreads / 32);
@@ -692,7 +694,7 @@ extern "C" {
 size_t w8a8_mul_mat_experts_workspace(const w8a8_experts* w, const route_plan* plan, int x_group, int y_group,
                                       unsigned flags) {
     if ((flags & ~(W8A8_SWIGLU | W8A8_TEST_STALL)) || check_sizes(w, plan, x_group, y_group, (flags & W8A8_SWIGLU) != 0)) return 0;
-    return layout_of(plan->items, plan->items / x_group, w->N, w->K).total;
+    return layout_of(plan->items, w->N, w->K).total;
 }
 
 int w8a8_mul_mat_experts(const w8a8_experts* w, const route_plan* plan, const i2s_rows* x, int x_group, const i2s_rows* y,
@@ -708,7 +710,7 @@ int w8a8_mul_mat_experts(const w8a8_experts* w, const route_plan* plan, const i2
     if ((r = check_row_tensor(x, x_rows, w->K, true, false)) || (r = check_row_tensor(y, y_rows, out, false, true))) return r;
     if (((uintptr_t)w->wq & 15) || ((uintptr_t)w->bscale & 3) || ((uintptr_t)weight & 3) || ((uintptr_t)ws & 255))
         return I2S_E_MISALIGNED;
-    const Layout l = layout_of(items, x_rows, w->N, w->K);
+    const Layout l = layout_of(items, w->N, w->K);
     const size_t need = l.total;
     if (ws_bytes < need) return I2S_E_WORKSPACE_TOO_SMALL;
     const Span sw = span_of(w->wq, (size_t)w->experts * w->N * w->K), sb = span_of(w->bscale, (size_t)w->experts * w->N * 4);
@@ -740,8 +742,11 @@ int w8a8_mul_mat_experts(const w8a8_experts* w, const route_plan* plan, const i2
         const cuuint32_t box[3] = {xp::kStep, xp::kChannels, 1};
         mapped = encode_tensor_map(&a.wmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, w->wq, dims, strides, box);
     }
-    const cuuint64_t xdims[2] = {K, (cuuint64_t)x_rows}, xstrides[1] = {K * 2};
-    const cuuint32_t xbox[2] = {64, 1};
+    // Row tiles there may be: no more than one per expert and one per `rows` items.
+    const bool few = items <= 16 * (int64_t)w->experts;
+    const int rows = few ? 32 : 128;
+    const cuuint64_t xdims[2] = {K, (cuuint64_t)items}, xstrides[1] = {K * 2};
+    const cuuint32_t xbox[2] = {64, (cuuint32_t)(few ? xp::Shape<32>::kBox : xp::Shape<128>::kBox)};
     if (!mapped || !encode_tensor_map(&a.xmap, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, q, xdims, xstrides, xbox)) return I2S_E_CUDA;
     a.plan = plan_view(*plan);
     a.bscale = w->bscale;
@@ -749,7 +754,6 @@ int w8a8_mul_mat_experts(const w8a8_experts* w, const route_plan* plan, const i2
     a.y = weight ? d : y->data;
     a.y_stride = weight ? w->N : y->stride;
     a.y_dtype = weight ? kF32 : y->dtype;
-    a.x_group = x_group;
     a.N = (int)w->N;
     a.K = (int)w->K;
     a.tiles_n = (int)((w->N + xp::kChannels - 1) / xp::kChannels);
@@ -759,14 +763,11 @@ int w8a8_mul_mat_experts(const w8a8_experts* w, const route_plan* plan, const i2
 
     const RowsView xv = {x->data, x->stride};
     cudaError_t e;
-    if (x->dtype == kF32) e = launch_rows<kF32>(xv, (int)x_rows, a.K, q, ascale, used, (int)items, status, stream);
-    else if (x->dtype == kF16) e = launch_rows<kF16>(xv, (int)x_rows, a.K, q, ascale, used, (int)items, status, stream);
-    else e = launch_rows<kBf16>(xv, (int)x_rows, a.K, q, ascale, used, (int)items, status, stream);
+    if (x->dtype == kF32) e = launch_rows<kF32>(xv, a.plan, x_group, a.K, q, ascale, used, status, stream);
+    else if (x->dtype == kF16) e = launch_rows<kF16>(xv, a.plan, x_group, a.K, q, ascale, used, status, stream);
+    else e = launch_rows<kBf16>(xv, a.plan, x_group, a.K, q, ascale, used, status, stream);
     if (e != cudaSuccess) return I2S_E_CUDA;
 
-    // Row tiles there may be: no more than one per expert and one per `rows` items.
-    const bool few = items <= 16 * (int64_t)w->experts;
-    const int rows = few ? 32 : 128;
     const int64_t units = (std::min<int64_t>(items, w->experts) + items / rows) * a.tiles_n;
     const int grid = (int)std::min<int64_t>(units, device_sm_count());
     if (few) e = swiglu ? launch_product<32, true>(a, grid, stream) : launch_product<32, false>(a, grid, stream);

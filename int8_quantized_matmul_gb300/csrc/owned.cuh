@@ -52,16 +52,20 @@ __device__ __forceinline__ float get_as(const void* data, int dt, long long at) 
     return __bfloat162float(static_cast<const __nv_bfloat16*>(data)[at]);
 }
 
+// The places of the list that are in use.
+__device__ __forceinline__ int plan_end(const PlanView& p) { return min(max(__ldcg(p.start + p.owners), 0), p.items); }
+
 // One warp fills begin[0 .. owners] and tile0[0 .. owners]: owner o's items are
 // list[begin[o] .. begin[o + 1]), cut into tiles of `rows`, and tile0 counts the
 // tiles of the owners before o. Whatever the starts hold, begin is in order and
-// within [0, items].
+// within [0, plan_end].
 __device__ __forceinline__ void plan_tiles(const PlanView& p, int rows, int* begin, int* tile0, int lane) {
     int most = 0;
+    const int end = plan_end(p);
     for (int i0 = 0; i0 <= p.owners; i0 += 32) {
         const int i = i0 + lane;
         int v = i <= p.owners ? __ldcg(p.start + i) : 0;
-        v = min(max(v, most), p.items);
+        v = min(max(v, most), end);
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int u = __shfl_up_sync(0xffffffffu, v, o);
