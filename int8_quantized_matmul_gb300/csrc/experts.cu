@@ -33,7 +33,8 @@
 // finishes one of two neighbouring rows after one exchange.
 //
 // Roles (512 threads): warps 0-3 epilogue, 4-11 converters (two groups taking
-// stages by turns), 12 weights, 13 rows, 14 MMAs. TMEM: two accumulators
+// stages by turns), 12 weights, 13 rows, 14 and 15 MMAs (stages by
+// turns into the same accumulator: sums of integers do not depend on the order). TMEM: two accumulators
 // of ROWS columns, then a ring of 64-column operands. Waits are bounded; one that runs
 // out sets the status word at the start of the workspace and the CTA's abort
 // flag, roles leave their loops, and what they issued is drained.
@@ -55,12 +56,15 @@ namespace xp {
 
 constexpr int kThreads = 512;
 constexpr int kConvWarp = 4, kWeightWarp = 12, kRowWarp = 13, kMmaWarp = 14;
+constexpr int kIssuers = 2;                     // warps that issue MMAs, stages by turns
 constexpr int kChannels = 128;
 constexpr int kStep = 128;                      // positions of a stage
 constexpr int kChunkSteps = kI8sChunkK / kStep; // stages of an exact f32 sum
 constexpr int kWStage = kChannels * kStep;      // bytes of a stage's weights
 constexpr int kOpCols = kStep / 2;              // TMEM columns of a stage's weights in f16
 constexpr int kMaxSlots = 6, kMaxWSlots = 10;
+constexpr int kUnitSlots = 8;                   // units handed out ahead
+constexpr int kUnitReaders = 15;                // warps that are told of each: all but the one that takes them
 constexpr long long kWait = 2000000000LL;
 // Registers of a thread after the split (of the 128 at launch): epilogue,
 // converters, the others. 128 * 208 + 256 * 104 + 128 * 56 <= 512 * 128.
@@ -82,8 +86,10 @@ struct Shape {
 
 struct Shared {
     uint64_t wfull[kMaxWSlots], wempty[kMaxWSlots];
-    uint64_t afull[kMaxSlots], bfull[kMaxSlots], empty[kMaxSlots];
-    uint64_t dfull[2], dempty[2], done;
+    uint64_t full[kMaxSlots], empty[kMaxSlots];
+    uint64_t dfull[2], dempty[2], done[kIssuers];
+    uint64_t ufull[kUnitSlots], uempty[kUnitSlots];
+    int unit[kUnitSlots];
     uint32_t tmem;
     int abort;
     struct Row {
@@ -105,15 +111,15 @@ template <int N>
 __device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 
 // For a warp whose control flow is uniform; `lead` is not zero in one lane.
-__device__ __forceinline__ void mma(uint32_t lead, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+__device__ __forceinline__ void mma(uint32_t lead, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc) {
     asm volatile(
         "{\n"
         ".reg .pred p, q;\n"
-        "setp.ne.b32 p, %4, 0;\n"
-        "setp.ne.b32 q, %5, 0;\n"
+        "setp.eq.b32 p, 0, 0;\n"
+        "setp.ne.b32 q, %4, 0;\n"
         "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n"
         "}\n" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(lead)
+        "r"(a), "l"(b), "r"(idesc), "r"(lead)
         : "memory");
 }
 __device__ __forceinline__ void commit(uint32_t lead, uint64_t* bar) {
@@ -184,6 +190,7 @@ struct ExpertArgs {
     int y_dtype;
     int N, K, tiles_n;
     uint8_t* used;          // workspace: items that have an expert, or null
+    int* taken;             // workspace: units that CTAs have taken beyond their first
     uint32_t* status;
     bool test_stall;
 };
@@ -210,15 +217,18 @@ __global__ void __launch_bounds__(xp::kThreads, 1) k_experts(const __grid_consta
                 tc::mbar_init(&S.wempty[i], 4);
             }
             for (int i = 0; i < S_::kSlots; ++i) {
-                tc::mbar_init(&S.afull[i], 4);
-                tc::mbar_init(&S.bfull[i], 1);
+                tc::mbar_init(&S.full[i], 5);   // four converter warps, and the rows' bytes
                 tc::mbar_init(&S.empty[i], 1);
             }
             for (int i = 0; i < 2; ++i) {
-                tc::mbar_init(&S.dfull[i], 1);
+                tc::mbar_init(&S.dfull[i], kIssuers);
                 tc::mbar_init(&S.dempty[i], 4);
             }
-            tc::mbar_init(&S.done, 1);
+            for (int i = 0; i < kUnitSlots; ++i) {
+                tc::mbar_init(&S.ufull[i], 1);
+                tc::mbar_init(&S.uempty[i], kUnitReaders);
+            }
+            for (int i = 0; i < kIssuers; ++i) tc::mbar_init(&S.done[i], 1);
             S.abort = 0;
             tc::fence_mbar_init();
         }
@@ -234,6 +244,13 @@ __global__ void __launch_bounds__(xp::kThreads, 1) k_experts(const __grid_consta
     __syncthreads();
     tc::tc_fence_after();
     const uint32_t tmem = S.tmem;
+    if (warp < kConvWarp) {   // every MMA accumulates: the accumulators start at zero, and are left so when they are read
+        for (int i = 0; i < 2 * ROWS; i += 32) tc::tmem_st_zero_32x32b_x32(tmem + ((uint32_t)(warp * 32) << 16) + (uint32_t)i);
+        tc::tmem_st_wait();
+        tc::tc_fence_before();
+    }
+    __syncthreads();
+    tc::tc_fence_after();
     const int units = S.tile0[a.plan.owners] * a.tiles_n;
     const int steps = (a.K + kStep - 1) / kStep;
 
@@ -254,6 +271,19 @@ __global__ void __launch_bounds__(xp::kThreads, 1) k_experts(const __grid_consta
         return t;
     };
 
+    // The seq-th unit of this CTA, for one lane (`one`) or a whole warp of a reader; past the last, or where a wait ran out,
+    // one that is not there.
+    auto unit_told = [&](int seq, bool one) {
+        const int i = seq % kUnitSlots;
+        bool got = tc::mbar_wait(&S.ufull[i], (uint32_t)(seq / kUnitSlots) & 1, abort_flag, kWait);
+        if (!got) fail();
+        if (!one) got = __all_sync(0xffffffffu, got) != 0;
+        const int u = got ? *const_cast<volatile int*>(&S.unit[i]) : 0x7fffffff;
+        if (!one) __syncwarp();
+        if (one || lane == 0) tc::mbar_arrive(&S.uempty[i]);
+        return u;
+    };
+
     if (warp < kConvWarp) {
         // ---------------------------------------------------------- epilogue
         regs_up<kRegsEpilogue>();
@@ -262,7 +292,9 @@ __global__ void __launch_bounds__(xp::kThreads, 1) k_experts(const __grid_consta
         const int chunks = (steps + kChunkSteps - 1) / kChunkSteps;
         int chunk_at = 0;
         bool ok = true;
-        for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
+        for (int seq = 0; ok; ++seq) {
+            const int u = unit_told(seq, false);
+            if (u >= units) break;
             const Unit t = unit_at(u);
             // each warp looks its rows up for itself
             __syncwarp();
@@ -296,6 +328,7 @@ __global__ void __launch_bounds__(xp::kThreads, 1) k_experts(const __grid_consta
                         uint32_t v[32];
                         tc::tmem_ld_32x32b_x32(tmem + lanes + (uint32_t)(buf * ROWS + 32 * p), v);
                         tc::tmem_ld_wait();
+                        tc::tmem_st_zero_32x32b_x32(tmem + lanes + (uint32_t)(buf * ROWS + 32 * p));
                         if (chunks <= 2) {
                             if (c == 0) {
 #pragma unroll
@@ -316,6 +349,7 @@ __global__ void __launch_bounds__(xp::kThreads, 1) k_experts(const __grid_consta
                         }
                     }
                 }
+                tc::tmem_st_wait();
                 tc::tc_fence_before();
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive(&S.dempty[buf]);
@@ -357,7 +391,8 @@ __global__ void __launch_bounds__(xp::kThreads, 1) k_experts(const __grid_consta
         const uint32_t lanes = (uint32_t)(q * 32) << 16;
         int at = 0;   // stage of this CTA
         bool ok = true;
-        for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
+        for (int seq = 0; ok; ++seq) {
+            if (unit_told(seq, false) >= units) break;
             for (int k = 0; k < steps; ++k, ++at) {
                 if ((at & 1) != group) continue;
                 const int ws = at % S_::kWSlots, slot = at % S_::kSlots;
@@ -401,17 +436,24 @@ __global__ void __launch_bounds__(xp::kThreads, 1) k_experts(const __grid_consta
                 tc::tmem_st_wait();
                 tc::tc_fence_before();
                 __syncwarp();
-                if (lane == 0) tc::mbar_arrive(&S.afull[slot]);
+                if (lane == 0) tc::mbar_arrive(&S.full[slot]);
             }
         }
     } else {
         regs_down<kRegsIssue>();
         if (warp == kWeightWarp) {
-            // ------------------------------------------------------- weights
+            // ------------------------------------- weights, and who does which unit
             if (lane == 0) {
                 int at = 0;
                 bool ok = true;
-                for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
+                int u = blockIdx.x;
+                for (int seq = 0; ok; ++seq) {
+                    const int i = seq % kUnitSlots;
+                    ok = tc::mbar_wait(&S.uempty[i], ((uint32_t)(seq / kUnitSlots) & 1) ^ 1, abort_flag, kWait);
+                    if (!ok) fail();
+                    S.unit[i] = u;
+                    tc::mbar_arrive(&S.ufull[i]);
+                    if (!ok || u >= units) break;
                     const Unit t = unit_at(u);
                     for (int k = 0; k < steps; ++k, ++at) {
                         const int ws = at % S_::kWSlots;
@@ -425,6 +467,9 @@ __global__ void __launch_bounds__(xp::kThreads, 1) k_experts(const __grid_consta
                         if (SWIGLU) load_pairs(dst, &a.wmap, k * kStep, t.n0 / 32, t.e, &S.wfull[ws]);
                         else load_weights(dst, &a.wmap, k * kStep, t.n0, t.e, &S.wfull[ws]);
                     }
+                    // the first unit of each CTA is its own; the launch before clears the counter of the others
+                    if (seq == 0) pdl_wait();
+                    u = (int)gridDim.x + atomicAdd(a.taken, 1);
                 }
                 // every copy has landed before the CTA leaves
                 for (int i = max(0, at - S_::kWSlots); i < at; ++i)
@@ -436,7 +481,9 @@ __global__ void __launch_bounds__(xp::kThreads, 1) k_experts(const __grid_consta
                 pdl_wait();
                 int at = 0;
                 bool ok = true;
-                for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
+                for (int seq = 0; ok; ++seq) {
+                    const int u = unit_told(seq, true);
+                    if (u >= units) break;
                     const Unit t = unit_at(u);
                     const int boxes = (t.rows + S_::kBox - 1) / S_::kBox;
                     for (int k = 0; k < steps; ++k, ++at) {
@@ -448,60 +495,67 @@ __global__ void __launch_bounds__(xp::kThreads, 1) k_experts(const __grid_consta
                         }
                         // the second half of the stage is left out where the row ends in the first
                         const bool both = k * kStep + 64 < a.K;
-                        tc::mbar_arrive_expect_tx(&S.bfull[slot], (uint32_t)(boxes * S_::kBox * (both ? 256 : 128)));
+                        tc::mbar_arrive_expect_tx(&S.full[slot], (uint32_t)(boxes * S_::kBox * (both ? 256 : 128)));
                         uint8_t* dst = sRows + slot * S_::kRowStage;
                         for (int i = 0; i < boxes; ++i) {
                             const int row = t.first + i * S_::kBox;
-                            tc::tma_load_2d(dst + i * S_::kBox * 128, &a.xmap, k * kStep, row, &S.bfull[slot]);
-                            if (both) tc::tma_load_2d(dst + S_::kAtom + i * S_::kBox * 128, &a.xmap, k * kStep + 64, row, &S.bfull[slot]);
+                            tc::tma_load_2d(dst + i * S_::kBox * 128, &a.xmap, k * kStep, row, &S.full[slot]);
+                            if (both) tc::tma_load_2d(dst + S_::kAtom + i * S_::kBox * 128, &a.xmap, k * kStep + 64, row, &S.full[slot]);
                         }
                     }
                 }
                 for (int i = max(0, at - S_::kSlots); i < at; ++i)
-                    tc::mbar_wait_drain(&S.bfull[i % S_::kSlots], (uint32_t)(i / S_::kSlots) & 1, kWait / 8);
+                    tc::mbar_wait_drain(&S.full[i % S_::kSlots], (uint32_t)(i / S_::kSlots) & 1, kWait / 8);
             }
-        } else if (warp == kMmaWarp) {
+        } else {
             // ---------------------------------------------------------- MMAs
+            // (reductions over the warp: their results, and so the branches, are uniform)
             const uint32_t lead = lane == 0;
+            const int me = warp - kMmaWarp;
             const uint32_t tm = __reduce_max_sync(0xffffffffu, tmem);
+            const int end = (int)__reduce_max_sync(0xffffffffu, (unsigned)units);
             int at = 0, chunk_at = 0;
             bool ok = true;
             auto wait = [&](uint64_t* bar, uint32_t parity) {
-                const bool got = tc::mbar_wait(bar, parity, abort_flag, kWait);
+                const bool got = tc::mbar_wait_spin(bar, parity, abort_flag, kWait);
                 return __all_sync(0xffffffffu, got) != 0;
             };
             // a test lets the others wait for products that never come
-            for (int u = a.test_stall ? units : blockIdx.x; ok && u < units; u += gridDim.x) {
+            for (int seq = 0; ok && !a.test_stall; ++seq) {
+                const int u = (int)__reduce_max_sync(0xffffffffu, (unsigned)unit_told(seq, false));
+                if (u >= end) break;
                 const Unit t = unit_at(u);
                 const int rows = (int)__reduce_max_sync(0xffffffffu, (unsigned)t.rows);
                 const uint32_t idesc = tc::idesc_f16_f32(kChannels, (rows + 15) / 16 * 16);
-                for (int k = 0; ok && k < steps; ++k, ++at) {
-                    const int slot = at % S_::kSlots, buf = chunk_at & 1;
-                    const uint32_t phase = (uint32_t)(at / S_::kSlots) & 1;
-                    if (k % kChunkSteps == 0) {
-                        ok = wait(&S.dempty[buf], ((uint32_t)(chunk_at >> 1) & 1) ^ 1);
-                    }
-                    ok = ok && wait(&S.bfull[slot], phase) && wait(&S.afull[slot], phase);
-                    if (!ok) break;
-                    tc::tc_fence_after();
-                    const uint64_t bd = tc::sdesc_sw128_kmajor(tc::smem_u32(sRows + slot * S_::kRowStage));
-                    const uint32_t d = tm + (uint32_t)(buf * ROWS), op = tm + S_::kOp0 + (uint32_t)(slot * kOpCols);
-                    const int left = (a.K - k * kStep + 15) / 16;   // 16-position MMAs that are left of the rows
+                for (int k0 = 0; ok && k0 < steps; k0 += kChunkSteps, ++chunk_at) {
+                    const int buf = chunk_at & 1, k1 = min(steps, k0 + kChunkSteps);
+                    const uint32_t d = tm + (uint32_t)(buf * ROWS);
+                    ok = wait(&S.dempty[buf], ((uint32_t)(chunk_at >> 1) & 1) ^ 1);
+                    for (int k = k0; ok && k < k1; ++k, ++at) {
+                        if (at % kIssuers != me) continue;
+                        const int slot = at % S_::kSlots;
+                        ok = wait(&S.full[slot], (uint32_t)(at / S_::kSlots) & 1);
+                        if (!ok) break;
+                        tc::tc_fence_after();
+                        const uint64_t bd = tc::sdesc_sw128_kmajor(tc::smem_u32(sRows + slot * S_::kRowStage));
+                        const uint32_t op = tm + S_::kOp0 + (uint32_t)(slot * kOpCols);
+                        const int left = (a.K - k * kStep + 15) / 16;   // 16-position MMAs that are left of the rows
+                        if (left >= 8) {
 #pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        if (j < left)
-                            mma(lead, d, op + 8u * j, bd + (uint64_t)((j >> 2) * (S_::kAtom >> 4) + 2 * (j & 3)), idesc,
-                                k % kChunkSteps != 0 || j > 0);
-                    commit(lead, &S.empty[slot]);
-                    if (k % kChunkSteps == kChunkSteps - 1 || k == steps - 1) {
-                        commit(lead, &S.dfull[buf]);
-                        ++chunk_at;
+                            for (int j = 0; j < 8; ++j)
+                                mma(lead, d, op + 8u * j, bd + (uint64_t)((j >> 2) * (S_::kAtom >> 4) + 2 * (j & 3)), idesc);
+                        } else {
+                            for (int j = 0; j < left; ++j)
+                                mma(lead, d, op + 8u * j, bd + (uint64_t)((j >> 2) * (S_::kAtom >> 4) + 2 * (j & 3)), idesc);
+                        }
+                        commit(lead, &S.empty[slot]);
                     }
+                    commit(lead, &S.dfull[buf]);
                 }
             }
             if (!ok) fail();
-            commit(lead, &S.done);
-            tc::mbar_wait_drain(&S.done, 0, kWait / 8);
+            commit(lead, &S.done[me]);
+            tc::mbar_wait_drain(&S.done[me], 0, kWait / 8);
         }
         __syncwarp();
     }
@@ -529,7 +583,7 @@ __global__ void __launch_bounds__(kRowThreads) k_expert_rows(RowsView x, PlanVie
     __shared__ float s_max[kRowThreads / 32];
     pdl_wait();
     pdl_launch_next();
-    if (blockIdx.x == 0 && threadIdx.x == 0) *status = 0u;
+    if (blockIdx.x == 0 && threadIdx.x == 0) status[0] = status[1] = 0u;   // and the units taken
     if (used != nullptr)
         for (int i = blockIdx.x * kRowThreads + threadIdx.x; i < (plan.items + 3) / 4; i += gridDim.x * kRowThreads)
             reinterpret_cast<uint32_t*>(used)[i] = 0u;
@@ -631,7 +685,7 @@ struct Layout {
 
 Layout layout_of(int64_t items, int64_t N, int64_t K) {
     Layout l;
-    l.ascale = 256;   // the status word before it
+    l.ascale = 256;   // the status word and the counter before it
     l.q = l.ascale + up_256((size_t)items * 4);
     l.used = l.q + up_256((size_t)items * K * 2);
     l.d = l.used + up_256((size_t)items);
@@ -759,6 +813,7 @@ int w8a8_mul_mat_experts(const w8a8_experts* w, const route_plan* plan, const i2
     a.tiles_n = (int)((w->N + xp::kChannels - 1) / xp::kChannels);
     a.used = used;
     a.status = status;
+    a.taken = reinterpret_cast<int*>(status + 1);
     a.test_stall = (flags & W8A8_TEST_STALL) != 0;
 
     const RowsView xv = {x->data, x->stride};
