@@ -32,8 +32,8 @@
 // gate and its up value are then 16 lanes apart in the same warp, and every lane
 // finishes one of two neighbouring rows after one exchange.
 //
-// Roles (512 threads): warps 0-3 epilogue, 4-11 converters (two groups taking
-// stages by turns), 12 weights, 13 rows, 14 and 15 MMAs (stages by
+// Roles (640 threads): warps 0-7 epilogue (each half of the columns), 8-15 converters (two groups taking
+// stages by turns), 16 weights, 17 rows, 18 and 19 MMAs (stages by
 // turns into the same accumulator: sums of integers do not depend on the order). TMEM: two accumulators
 // of ROWS columns, then a ring of 64-column operands. Waits are bounded; one that runs
 // out sets the status word at the start of the workspace and the CTA's abort
@@ -54,8 +54,8 @@ namespace {
 
 namespace xp {
 
-constexpr int kThreads = 512;
-constexpr int kConvWarp = 4, kWeightWarp = 12, kRowWarp = 13, kMmaWarp = 14;
+constexpr int kThreads = 640;
+constexpr int kConvWarp = 8, kWeightWarp = 16, kRowWarp = 17, kMmaWarp = 18;
 constexpr int kIssuers = 2;                     // warps that issue MMAs, stages by turns
 constexpr int kChannels = 128;
 constexpr int kStep = 128;                      // positions of a stage
@@ -64,11 +64,11 @@ constexpr int kWStage = kChannels * kStep;      // bytes of a stage's weights
 constexpr int kOpCols = kStep / 2;              // TMEM columns of a stage's weights in f16
 constexpr int kMaxSlots = 6, kMaxWSlots = 10;
 constexpr int kUnitSlots = 8;                   // units handed out ahead
-constexpr int kUnitReaders = 15;                // warps that are told of each: all but the one that takes them
+constexpr int kUnitReaders = 19;                // warps that are told of each: all but the one that takes them
 constexpr long long kWait = 2000000000LL;
-// Registers of a thread after the split (of the 128 at launch): epilogue,
-// converters, the others. 128 * 208 + 256 * 104 + 128 * 56 <= 512 * 128.
-constexpr int kRegsEpilogue = 208, kRegsConvert = 104, kRegsIssue = 56;
+// Registers of a thread after the split (of the 96 at launch): epilogue,
+// converters, the others. 256 * 120 + 256 * 88 + 128 * 56 <= 640 * 96.
+constexpr int kRegsEpilogue = 120, kRegsConvert = 88, kRegsIssue = 56;
 
 template <int ROWS>
 struct Shape {
@@ -76,7 +76,6 @@ struct Shape {
     // Many: the rows do.
     static constexpr int kSlots = ROWS == 32 ? 6 : 4;      // operands: rows, and weights in TMEM
     static constexpr int kWSlots = ROWS == 32 ? 10 : 5;    // weights as bytes
-    static constexpr int kBox = ROWS == 32 ? 16 : 32;      // rows of a copy
     static constexpr int kAtom = ROWS * 128;               // 64 positions of the rows
     static constexpr int kRowStage = 2 * kAtom;
     static constexpr uint32_t kOp0 = 2 * ROWS;             // first TMEM column of the operands
@@ -84,19 +83,24 @@ struct Shape {
     static_assert(kSlots <= kMaxSlots && kWSlots <= kMaxWSlots, "barriers");
 };
 
+// Up to ROWS items of an expert and 128 channels; rows is 0 where there are no more units.
+struct Unit {
+    int e, n0, first, rows;   // expert, first channel, first place in the list, rows
+};
+
 struct Shared {
     uint64_t wfull[kMaxWSlots], wempty[kMaxWSlots];
     uint64_t full[kMaxSlots], empty[kMaxSlots];
     uint64_t dfull[2], dempty[2], done[kIssuers];
     uint64_t ufull[kUnitSlots], uempty[kUnitSlots];
-    int unit[kUnitSlots];
+    Unit unit[kUnitSlots];
     uint32_t tmem;
     int abort;
     struct Row {
         long long off;   // of the row in y; negative: none
         float scale;
         int pad;
-    } row[4][128];   // of each epilogue warp
+    } row[8][64];   // of each epilogue warp
     int begin[kMaxOwners + 1], tile0[kMaxOwners + 1];
 };
 
@@ -146,6 +150,26 @@ __device__ __forceinline__ void load_pairs(void* dst, const CUtensorMap* map, in
         "l"(map), "r"(k), "r"(0), "r"(block), "r"(e), "r"(tc::smem_u32(bar))
         : "memory");
 }
+__device__ __forceinline__ void load_rows(uint32_t lead, uint32_t dst, const CUtensorMap* map, int k, int row, uint32_t bar) {
+    asm volatile(
+        "{\n"
+        ".reg .pred q;\n"
+        "setp.ne.b32 q, %5, 0;\n"
+        "@q cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];\n"
+        "}\n" ::"r"(dst),
+        "l"(map), "r"(k), "r"(row), "r"(bar), "r"(lead)
+        : "memory");
+}
+__device__ __forceinline__ void expect_bytes(uint32_t lead, uint32_t bar, uint32_t bytes) {
+    asm volatile(
+        "{\n"
+        ".reg .pred q;\n"
+        "setp.ne.b32 q, %2, 0;\n"
+        "@q mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n"
+        "}\n" ::"r"(bar), "r"(bytes), "r"(lead)
+        : "memory");
+}
+
 // Codes 0, 1 (SEL 0x4140) or 2, 3 (0x4342) of four biased by 128, as f16:
 // the byte in the mantissa of 1024, less 1152.
 template <int SEL>
@@ -167,21 +191,21 @@ __device__ __forceinline__ void put(float* p, float v) { *p = v; }
 __device__ __forceinline__ void put(__half* p, float v) { *p = __float2half_rn(v); }
 __device__ __forceinline__ void put(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 
-// Values of up to 32 rows, channel n, of which `left` are the unit's. PAIRS: v[i] is of row i + mine, i even.
+// Values of 16 rows, channel n. PAIRS: v[i] is of row i + mine, i even.
 template <typename T, bool PAIRS>
-__device__ __forceinline__ void store_rows(void* y, const Shared::Row* row, const float* v, int left, int mine, int n) {
+__device__ __forceinline__ void store_rows(void* y, const Shared::Row* row, const float (&v)[16], int mine, int n) {
     T* to = static_cast<T*>(y) + n;
 #pragma unroll
-    for (int i = 0; i < 32; i += PAIRS ? 2 : 1) {
+    for (int i = 0; i < 16; i += PAIRS ? 2 : 1) {
         const long long off = row[i + (PAIRS ? mine : 0)].off;
-        if (i + mine < left && off >= 0) put(to + off, v[i]);
+        if (off >= 0) put(to + off, v[i]);
     }
 }
 
 }  // namespace xp
 
 struct ExpertArgs {
-    CUtensorMap wmap, xmap;
+    CUtensorMap wmap, xmap[3];   // rows in boxes of ROWS, ROWS / 2, ROWS / 4
     PlanView plan;
     const float* bscale;
     const float* ascale;    // workspace, one per place of the list, as the codes
@@ -222,7 +246,7 @@ __global__ void __launch_bounds__(xp::kThreads, 1) k_experts(const __grid_consta
             }
             for (int i = 0; i < 2; ++i) {
                 tc::mbar_init(&S.dfull[i], kIssuers);
-                tc::mbar_init(&S.dempty[i], 4);
+                tc::mbar_init(&S.dempty[i], 8);
             }
             for (int i = 0; i < kUnitSlots; ++i) {
                 tc::mbar_init(&S.ufull[i], 1);
@@ -245,7 +269,8 @@ __global__ void __launch_bounds__(xp::kThreads, 1) k_experts(const __grid_consta
     tc::tc_fence_after();
     const uint32_t tmem = S.tmem;
     if (warp < kConvWarp) {   // every MMA accumulates: the accumulators start at zero, and are left so when they are read
-        for (int i = 0; i < 2 * ROWS; i += 32) tc::tmem_st_zero_32x32b_x32(tmem + ((uint32_t)(warp * 32) << 16) + (uint32_t)i);
+        for (int i = 32 * (warp >> 2); i < 2 * ROWS; i += 64)
+            tc::tmem_st_zero_32x32b_x32(tmem + ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)i);
         tc::tmem_st_wait();
         tc::tc_fence_before();
     }
@@ -254,135 +279,138 @@ __global__ void __launch_bounds__(xp::kThreads, 1) k_experts(const __grid_consta
     const int units = S.tile0[a.plan.owners] * a.tiles_n;
     const int steps = (a.K + kStep - 1) / kStep;
 
-    struct Unit {
-        int e, n0, first, rows;   // expert, first channel (tile index * 128), first place in the list, rows
-    };
     auto unit_at = [&](int u) {
-        Unit t;
-        t.e = owner_of_tile(S.tile0, a.plan.owners, u / a.tiles_n);
+        Unit t = {0, 0, 0, 0};
+        if (u >= units) return t;
+        const int tile = u / a.tiles_n;
+        t.e = owner_of_tile(S.tile0, a.plan.owners, tile);
         const int tiles = S.tile0[t.e + 1] - S.tile0[t.e];
-        const int r = u - S.tile0[t.e] * a.tiles_n;
-        t.n0 = r / tiles * kChannels;
+        const int r = u - S.tile0[t.e] * a.tiles_n, n = r / tiles, at = r - n * tiles;
+        t.n0 = n * kChannels;
         // rows spread evenly over the expert's row tiles
-        const int all = S.begin[t.e + 1] - S.begin[t.e], at = r % tiles;
-        const int lo = (int)((long long)all * at / tiles), hi = (int)((long long)all * (at + 1) / tiles);
-        t.first = S.begin[t.e] + lo;
-        t.rows = hi - lo;
+        const int all = S.begin[t.e + 1] - S.begin[t.e], each = all / tiles, more = all - each * tiles;
+        t.first = S.begin[t.e] + at * each + min(at, more);
+        t.rows = each + (at < more);
         return t;
     };
-
-    // The seq-th unit of this CTA, for one lane (`one`) or a whole warp of a reader; past the last, or where a wait ran out,
-    // one that is not there.
-    auto unit_told = [&](int seq, bool one) {
+    // The seq-th unit of this CTA, for a whole warp; where the wait ran out, one that is not there.
+    auto unit_told = [&](int seq) {
         const int i = seq % kUnitSlots;
         bool got = tc::mbar_wait(&S.ufull[i], (uint32_t)(seq / kUnitSlots) & 1, abort_flag, kWait);
         if (!got) fail();
-        if (!one) got = __all_sync(0xffffffffu, got) != 0;
-        const int u = got ? *const_cast<volatile int*>(&S.unit[i]) : 0x7fffffff;
-        if (!one) __syncwarp();
-        if (one || lane == 0) tc::mbar_arrive(&S.uempty[i]);
-        return u;
+        got = __all_sync(0xffffffffu, got) != 0;
+        Unit t = {0, 0, 0, 0};
+        if (got) t = *reinterpret_cast<const Unit*>(&S.unit[i]);
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&S.uempty[i]);
+        return t;
     };
 
     if (warp < kConvWarp) {
         // ---------------------------------------------------------- epilogue
         regs_up<kRegsEpilogue>();
         pdl_wait();
-        const uint32_t lanes = (uint32_t)(warp * 32) << 16;
+        const int q = warp & 3;
+        const bool upper = warp >= 4;                 // of the unit's columns (rows)
+        const int mine = SWIGLU ? lane >> 4 : 0;      // SWIGLU: which of two neighbouring rows this lane finishes
+        const int half = a.N >> 1;
+        Shared::Row* const row = S.row[warp];
+        constexpr int kPieces = ROWS / 32;            // of 16 columns, that a warp may have
         const int chunks = (steps + kChunkSteps - 1) / kChunkSteps;
         int chunk_at = 0;
         bool ok = true;
         for (int seq = 0; ok; ++seq) {
-            const int u = unit_told(seq, false);
-            if (u >= units) break;
-            const Unit t = unit_at(u);
+            const Unit t = unit_told(seq);
+            if (t.rows == 0) break;
+            const int all = (t.rows + 15) >> 4, low = (all + 1) >> 1;
+            const int c0 = upper ? 16 * low : 0, pieces = upper ? all - low : low;
             // each warp looks its rows up for itself
-            __syncwarp();
-            for (int i = lane; i < t.rows; i += 32) {
-                const int item = __ldcg(a.plan.list + t.first + i);
-                Shared::Row row = {-1, 0.0f, 0};
+            for (int i = lane; i < 16 * pieces; i += 32) {
+                const int place = t.first + c0 + i;
+                const int item = c0 + i < t.rows ? __ldcg(a.plan.list + place) : -1;
+                Shared::Row r = {-1, 0.0f, 0};
                 if (item >= 0 && item < a.plan.items) {
-                    row.off = item * a.y_stride;
-                    row.scale = __ldcg(a.ascale + t.first + i);
-                    if (a.used != nullptr && t.n0 == 0 && warp == 0) a.used[item] = 1;
+                    r.off = item * a.y_stride;
+                    r.scale = __ldcg(a.ascale + place);
+                    if (a.used != nullptr && t.n0 == 0 && q == 0) a.used[item] = 1;
                 }
-                S.row[warp][i] = row;
+                row[i] = r;
             }
-            __syncwarp();
-            const int r = warp * 32 + lane;   // channel of the unit
-            // SWIGLU: lane's channel 16 * warp + lane % 16 of 64, gate or up
-            const int half = a.N >> 1;
-            const int n = SWIGLU ? (t.n0 >> 1) + warp * 16 + (lane & 15) : t.n0 + r;
+            // SWIGLU: the lane's channel is 16 * q + lane % 16 of the unit's 64, gate or up
+            const int n = SWIGLU ? (t.n0 >> 1) + q * 16 + (lane & 15) : t.n0 + q * 32 + lane;
             const bool live = n < (SWIGLU ? half : a.N);
             const float b = live ? __ldg(a.bscale + (long long)t.e * a.N + n + (SWIGLU && lane >= 16 ? half : 0)) : 0.0f;
-            float sum[ROWS];
+            __syncwarp();
+            float sum[kPieces][16];   // of the chunks before the last: f32 where there is one, else int32
             for (int c = 0; c < chunks; ++c, ++chunk_at) {
                 const int buf = chunk_at & 1;
+                const uint32_t d = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * ROWS + c0);
                 if (!tc::mbar_wait(&S.dfull[buf], (uint32_t)(chunk_at >> 1) & 1, abort_flag, kWait)) { fail(); ok = false; }
                 ok = __all_sync(0xffffffffu, ok) != 0;
                 if (!ok) break;
                 tc::tc_fence_after();
+                if (chunks > 1) {
 #pragma unroll
-                for (int p = 0; p < ROWS / 32; ++p) {
-                    if (32 * p < t.rows) {
-                        uint32_t v[32];
-                        tc::tmem_ld_32x32b_x32(tmem + lanes + (uint32_t)(buf * ROWS + 32 * p), v);
+                    for (int p = 0; p < kPieces; ++p) {
+                        if (p >= pieces) continue;
+                        uint32_t v[16];
+                        tc::tmem_ld_32x32b_x16(d + 16u * p, v);
                         tc::tmem_ld_wait();
-                        tc::tmem_st_zero_32x32b_x32(tmem + lanes + (uint32_t)(buf * ROWS + 32 * p));
-                        if (chunks <= 2) {
-                            if (c == 0) {
+                        if (c < chunks - 1) tc::tmem_st_zero_32x32b_x16(d + 16u * p);
+                        if (chunks == 2) {
 #pragma unroll
-                                for (int i = 0; i < 32; ++i) sum[32 * p + i] = __uint_as_float(v[i]);
-                            } else {
+                            for (int i = 0; i < 16; ++i)
+                                sum[p][i] = c == 0 ? __uint_as_float(v[i]) : __fadd_rn(sum[p][i], __uint_as_float(v[i]));
+                        } else {
 #pragma unroll
-                                for (int i = 0; i < 32; ++i) sum[32 * p + i] = __fadd_rn(sum[32 * p + i], __uint_as_float(v[i]));
-                            }
-                        } else {   // int32 in the same registers
-                            if (c == 0) {
-#pragma unroll
-                                for (int i = 0; i < 32; ++i) sum[32 * p + i] = __int_as_float(__float2int_rn(__uint_as_float(v[i])));
-                            } else {
-#pragma unroll
-                                for (int i = 0; i < 32; ++i)
-                                    sum[32 * p + i] = __int_as_float(__float_as_int(sum[32 * p + i]) + __float2int_rn(__uint_as_float(v[i])));
+                            for (int i = 0; i < 16; ++i) {
+                                const int s = __float2int_rn(__uint_as_float(v[i]));
+                                sum[p][i] = __int_as_float(c == 0 ? s : __float_as_int(sum[p][i]) + s);
                             }
                         }
+                        if (c == chunks - 1) {   // the whole sum takes the last chunk's place
+#pragma unroll
+                            for (int i = 0; i < 16; ++i)
+                                v[i] = __float_as_uint(chunks == 2 ? sum[p][i] : __int2float_rn(__float_as_int(sum[p][i])));
+                            tc::tmem_st_32x32b_x16(d + 16u * p, v);
+                        }
                     }
+                    tc::tmem_st_wait();
                 }
-                tc::tmem_st_wait();
+                if (c == chunks - 1) {
+                    // (not unrolled: code that runs once per unit comes from memory again each time)
+#pragma unroll 1
+                    for (int p = 0; p < pieces; ++p) {
+                        uint32_t w[16];
+                        tc::tmem_ld_32x32b_x16(d + 16u * p, w);
+                        tc::tmem_ld_wait();
+                        tc::tmem_st_zero_32x32b_x16(d + 16u * p);
+                        float v[16];
+                        const Shared::Row* r = row + 16 * p;
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) v[i] = __fmul_rn(__fmul_rn(r[i].scale, b), __uint_as_float(w[i]));
+                        if (SWIGLU) {
+#pragma unroll
+                            for (int i = 0; i < 16; i += 2) {
+                                const float other = __shfl_xor_sync(0xffffffffu, mine ? v[i] : v[i + 1], 16);
+                                const float g = mine ? other : v[i], up = mine ? v[i + 1] : other;
+                                v[i] = __fmul_rn(silu(g), up);
+                            }
+                        }
+                        // (no value's computation hangs on another's store: the chains run side by side)
+                        if (live) {
+                            if (a.y_dtype == kF32) store_rows<float, SWIGLU>(a.y, r, v, mine, n);
+                            else if (a.y_dtype == kF16) store_rows<__half, SWIGLU>(a.y, r, v, mine, n);
+                            else store_rows<__nv_bfloat16, SWIGLU>(a.y, r, v, mine, n);
+                        }
+                    }
+                    tc::tmem_st_wait();
+                }
                 tc::tc_fence_before();
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive(&S.dempty[buf]);
             }
-            if (!ok) break;
-            const int mine = SWIGLU ? lane >> 4 : 0;
-#pragma unroll
-            for (int p = 0; p < ROWS / 32; ++p) {
-                if (32 * p < t.rows) {
-                    float* v = sum + 32 * p;
-                    if (chunks > 2) {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) v[i] = __int2float_rn(__float_as_int(v[i]));
-                    }
-                    const Shared::Row* row = S.row[warp] + 32 * p;
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) v[i] = __fmul_rn(__fmul_rn(row[i].scale, b), v[i]);
-                    if (SWIGLU) {
-                        // the lower half warp finishes row i, the upper row i + 1
-#pragma unroll
-                        for (int i = 0; i < 32; i += 2) {
-                            const float other = __shfl_xor_sync(0xffffffffu, mine ? v[i] : v[i + 1], 16);
-                            const float g = mine ? other : v[i], up = mine ? v[i + 1] : other;
-                            v[i] = __fmul_rn(silu(g), up);
-                        }
-                    }
-                    // (no value's computation hangs on another's store: the chains run side by side)
-                    const int left = live ? t.rows - 32 * p : 0;
-                    if (a.y_dtype == kF32) store_rows<float, SWIGLU>(a.y, row, v, left, mine, n);
-                    else if (a.y_dtype == kF16) store_rows<__half, SWIGLU>(a.y, row, v, left, mine, n);
-                    else store_rows<__nv_bfloat16, SWIGLU>(a.y, row, v, left, mine, n);
-                }
-            }
+            __syncwarp();
         }
     } else if (warp < kWeightWarp) {
         // -------------------------------------------------------- converters
@@ -392,7 +420,7 @@ __global__ void __launch_bounds__(xp::kThreads, 1) k_experts(const __grid_consta
         int at = 0;   // stage of this CTA
         bool ok = true;
         for (int seq = 0; ok; ++seq) {
-            if (unit_told(seq, false) >= units) break;
+            if (unit_told(seq).rows == 0) break;
             for (int k = 0; k < steps; ++k, ++at) {
                 if ((at & 1) != group) continue;
                 const int ws = at % S_::kWSlots, slot = at % S_::kSlots;
@@ -446,15 +474,14 @@ __global__ void __launch_bounds__(xp::kThreads, 1) k_experts(const __grid_consta
             if (lane == 0) {
                 int at = 0;
                 bool ok = true;
-                int u = blockIdx.x;
+                Unit t = unit_at(blockIdx.x);
                 for (int seq = 0; ok; ++seq) {
                     const int i = seq % kUnitSlots;
                     ok = tc::mbar_wait(&S.uempty[i], ((uint32_t)(seq / kUnitSlots) & 1) ^ 1, abort_flag, kWait);
                     if (!ok) fail();
-                    S.unit[i] = u;
+                    S.unit[i] = t;
                     tc::mbar_arrive(&S.ufull[i]);
-                    if (!ok || u >= units) break;
-                    const Unit t = unit_at(u);
+                    if (!ok || t.rows == 0) break;
                     for (int k = 0; k < steps; ++k, ++at) {
                         const int ws = at % S_::kWSlots;
                         if (!tc::mbar_wait(&S.wempty[ws], ((uint32_t)(at / S_::kWSlots) & 1) ^ 1, abort_flag, kWait)) {
@@ -469,7 +496,7 @@ __global__ void __launch_bounds__(xp::kThreads, 1) k_experts(const __grid_consta
                     }
                     // the first unit of each CTA is its own; the launch before clears the counter of the others
                     if (seq == 0) pdl_wait();
-                    u = (int)gridDim.x + atomicAdd(a.taken, 1);
+                    t = unit_at((int)gridDim.x + atomicAdd(a.taken, 1));
                 }
                 // every copy has landed before the CTA leaves
                 for (int i = max(0, at - S_::kWSlots); i < at; ++i)
@@ -477,43 +504,46 @@ __global__ void __launch_bounds__(xp::kThreads, 1) k_experts(const __grid_consta
             }
         } else if (warp == kRowWarp) {
             // ---------------------------------------------------------- rows
-            if (lane == 0) {
-                pdl_wait();
-                int at = 0;
-                bool ok = true;
-                for (int seq = 0; ok; ++seq) {
-                    const int u = unit_told(seq, true);
-                    if (u >= units) break;
-                    const Unit t = unit_at(u);
-                    const int boxes = (t.rows + S_::kBox - 1) / S_::kBox;
-                    for (int k = 0; k < steps; ++k, ++at) {
-                        const int slot = at % S_::kSlots;
-                        if (!tc::mbar_wait(&S.empty[slot], ((uint32_t)(at / S_::kSlots) & 1) ^ 1, abort_flag, kWait)) {
-                            fail();
-                            ok = false;
-                            break;
-                        }
-                        // the second half of the stage is left out where the row ends in the first
-                        const bool both = k * kStep + 64 < a.K;
-                        tc::mbar_arrive_expect_tx(&S.full[slot], (uint32_t)(boxes * S_::kBox * (both ? 256 : 128)));
-                        uint8_t* dst = sRows + slot * S_::kRowStage;
-                        for (int i = 0; i < boxes; ++i) {
-                            const int row = t.first + i * S_::kBox;
-                            tc::tma_load_2d(dst + i * S_::kBox * 128, &a.xmap, k * kStep, row, &S.full[slot]);
-                            if (both) tc::tma_load_2d(dst + S_::kAtom + i * S_::kBox * 128, &a.xmap, k * kStep + 64, row, &S.full[slot]);
-                        }
+            // (uniform like the MMA warps: a copy issued in a branch of one lane takes 150 cycles)
+            const uint32_t lead = lane == 0;
+            pdl_wait();
+            int at = 0;
+            bool ok = true;
+            for (int seq = 0; ok; ++seq) {
+                const Unit t = unit_told(seq);
+                const int rows = (int)__reduce_max_sync(0xffffffffu, (unsigned)t.rows);
+                const int first = (int)__reduce_max_sync(0xffffffffu, (unsigned)t.first);
+                if (rows == 0) break;
+                // one box of ROWS, ROWS / 2 or ROWS / 4 rows, or the two smaller ones
+                const int some = rows > 3 * ROWS / 4 ? 0 : rows > ROWS / 4 ? 1 : 2;
+                const bool two = some == 1 && rows > ROWS / 2;
+                const uint32_t loaded = (uint32_t)(ROWS >> some) + (two ? ROWS / 4 : 0);
+                for (int k = 0; k < steps; ++k, ++at) {
+                    const int slot = at % S_::kSlots;
+                    const bool got = tc::mbar_wait_spin(&S.empty[slot], ((uint32_t)(at / S_::kSlots) & 1) ^ 1, abort_flag, kWait);
+                    if (!got) fail();
+                    ok = __all_sync(0xffffffffu, got) != 0;
+                    if (!ok) break;
+                    // the second half of the stage is left out where the row ends in the first
+                    const bool both = k * kStep + 64 < a.K;
+                    const uint32_t bar = tc::smem_u32(&S.full[slot]), dst = tc::smem_u32(sRows + slot * S_::kRowStage);
+                    expect_bytes(lead, bar, loaded * (both ? 256 : 128));
+                    load_rows(lead, dst, &a.xmap[some], k * kStep, first, bar);
+                    if (both) load_rows(lead, dst + S_::kAtom, &a.xmap[some], k * kStep + 64, first, bar);
+                    if (two) {
+                        load_rows(lead, dst + ROWS / 2 * 128, &a.xmap[2], k * kStep, first + ROWS / 2, bar);
+                        if (both) load_rows(lead, dst + S_::kAtom + ROWS / 2 * 128, &a.xmap[2], k * kStep + 64, first + ROWS / 2, bar);
                     }
                 }
-                for (int i = max(0, at - S_::kSlots); i < at; ++i)
-                    tc::mbar_wait_drain(&S.full[i % S_::kSlots], (uint32_t)(i / S_::kSlots) & 1, kWait / 8);
             }
+            for (int i = max(0, at - S_::kSlots); i < at; ++i)
+                tc::mbar_wait_drain(&S.full[i % S_::kSlots], (uint32_t)(i / S_::kSlots) & 1, kWait / 8);
         } else {
             // ---------------------------------------------------------- MMAs
             // (reductions over the warp: their results, and so the branches, are uniform)
             const uint32_t lead = lane == 0;
             const int me = warp - kMmaWarp;
             const uint32_t tm = __reduce_max_sync(0xffffffffu, tmem);
-            const int end = (int)__reduce_max_sync(0xffffffffu, (unsigned)units);
             int at = 0, chunk_at = 0;
             bool ok = true;
             auto wait = [&](uint64_t* bar, uint32_t parity) {
@@ -522,10 +552,8 @@ __global__ void __launch_bounds__(xp::kThreads, 1) k_experts(const __grid_consta
             };
             // a test lets the others wait for products that never come
             for (int seq = 0; ok && !a.test_stall; ++seq) {
-                const int u = (int)__reduce_max_sync(0xffffffffu, (unsigned)unit_told(seq, false));
-                if (u >= end) break;
-                const Unit t = unit_at(u);
-                const int rows = (int)__reduce_max_sync(0xffffffffu, (unsigned)t.rows);
+                const int rows = (int)__reduce_max_sync(0xffffffffu, (unsigned)unit_told(seq).rows);
+                if (rows == 0) break;
                 const uint32_t idesc = tc::idesc_f16_f32(kChannels, (rows + 15) / 16 * 16);
                 for (int k0 = 0; ok && k0 < steps; k0 += kChunkSteps, ++chunk_at) {
                     const int buf = chunk_at & 1, k1 = min(steps, k0 + kChunkSteps);
@@ -800,8 +828,11 @@ int w8a8_mul_mat_experts(const w8a8_experts* w, const route_plan* plan, const i2
     const bool few = items <= 16 * (int64_t)w->experts;
     const int rows = few ? 32 : 128;
     const cuuint64_t xdims[2] = {K, (cuuint64_t)items}, xstrides[1] = {K * 2};
-    const cuuint32_t xbox[2] = {64, (cuuint32_t)(few ? xp::Shape<32>::kBox : xp::Shape<128>::kBox)};
-    if (!mapped || !encode_tensor_map(&a.xmap, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, q, xdims, xstrides, xbox)) return I2S_E_CUDA;
+    for (int i = 0; i < 3; ++i) {
+        const cuuint32_t xbox[2] = {64, (cuuint32_t)(rows >> i)};
+        mapped = mapped && encode_tensor_map(&a.xmap[i], CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, q, xdims, xstrides, xbox);
+    }
+    if (!mapped) return I2S_E_CUDA;
     a.plan = plan_view(*plan);
     a.bscale = w->bscale;
     a.ascale = ascale;
