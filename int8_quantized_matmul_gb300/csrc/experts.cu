@@ -97,9 +97,8 @@ struct Shared {
     uint32_t tmem;
     int abort;
     struct Row {
-        long long off;   // of the row in y; negative: none
+        int item;   // negative: none
         float scale;
-        int pad;
     } row[8][64];   // of each epilogue warp
     int begin[kMaxOwners + 1], tile0[kMaxOwners + 1];
 };
@@ -113,6 +112,12 @@ template <int N>
 __device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N>
 __device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+
+// Arrives without waiting for this thread's earlier stores to be performed (a release does): for barriers that hand
+// back what was read, tensor memory (after tcgen05.wait) or values that are in registers by then.
+__device__ __forceinline__ void arrive_relaxed(uint64_t* bar) {
+    asm volatile("mbarrier.arrive.relaxed.cta.shared::cta.b64 _, [%0];" ::"r"(tc::smem_u32(bar)) : "memory");
+}
 
 // For a warp whose control flow is uniform; `lead` is not zero in one lane.
 __device__ __forceinline__ void mma(uint32_t lead, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc) {
@@ -191,15 +196,12 @@ __device__ __forceinline__ void put(float* p, float v) { *p = v; }
 __device__ __forceinline__ void put(__half* p, float v) { *p = __float2half_rn(v); }
 __device__ __forceinline__ void put(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 
-// Values of 16 rows, channel n. PAIRS: v[i] is of row i + mine, i even.
-template <typename T, bool PAIRS>
-__device__ __forceinline__ void store_rows(void* y, const Shared::Row* row, const float (&v)[16], int mine, int n) {
-    T* to = static_cast<T*>(y) + n;
+// Values of one channel of N items, where there is one.
+template <typename T, int N>
+__device__ __forceinline__ void store_rows(T* y, long long stride, const int (&item)[N], const float (&v)[N]) {
 #pragma unroll
-    for (int i = 0; i < 16; i += PAIRS ? 2 : 1) {
-        const long long off = row[i + (PAIRS ? mine : 0)].off;
-        if (off >= 0) put(to + off, v[i]);
-    }
+    for (int i = 0; i < N; ++i)
+        if (item[i] >= 0) put(y + item[i] * stride, v[i]);
 }
 
 }  // namespace xp
@@ -302,7 +304,7 @@ __global__ void __launch_bounds__(xp::kThreads, 1) k_experts(const __grid_consta
         Unit t = {0, 0, 0, 0};
         if (got) t = *reinterpret_cast<const Unit*>(&S.unit[i]);
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&S.uempty[i]);
+        if (lane == 0) arrive_relaxed(&S.uempty[i]);
         return t;
     };
 
@@ -328,9 +330,9 @@ __global__ void __launch_bounds__(xp::kThreads, 1) k_experts(const __grid_consta
             for (int i = lane; i < 16 * pieces; i += 32) {
                 const int place = t.first + c0 + i;
                 const int item = c0 + i < t.rows ? __ldcg(a.plan.list + place) : -1;
-                Shared::Row r = {-1, 0.0f, 0};
+                Shared::Row r = {-1, 0.0f};
                 if (item >= 0 && item < a.plan.items) {
-                    r.off = item * a.y_stride;
+                    r.item = item;
                     r.scale = __ldcg(a.ascale + place);
                     if (a.used != nullptr && t.n0 == 0 && q == 0) a.used[item] = 1;
                 }
@@ -342,75 +344,101 @@ __global__ void __launch_bounds__(xp::kThreads, 1) k_experts(const __grid_consta
             const float b = live ? __ldg(a.bscale + (long long)t.e * a.N + n + (SWIGLU && lane >= 16 ? half : 0)) : 0.0f;
             __syncwarp();
             float sum[kPieces][16];   // of the chunks before the last: f32 where there is one, else int32
-            for (int c = 0; c < chunks; ++c, ++chunk_at) {
-                const int buf = chunk_at & 1;
-                const uint32_t d = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * ROWS + c0);
-                if (!tc::mbar_wait(&S.dfull[buf], (uint32_t)(chunk_at >> 1) & 1, abort_flag, kWait)) { fail(); ok = false; }
+            // the accumulator of the next chunk, from this warp's first column on
+            auto next_chunk = [&] {
+                if (!tc::mbar_wait(&S.dfull[chunk_at & 1], (uint32_t)(chunk_at >> 1) & 1, abort_flag, kWait)) { fail(); ok = false; }
                 ok = __all_sync(0xffffffffu, ok) != 0;
-                if (!ok) break;
                 tc::tc_fence_after();
-                if (chunks > 1) {
-#pragma unroll
-                    for (int p = 0; p < kPieces; ++p) {
-                        if (p >= pieces) continue;
-                        uint32_t v[16];
-                        tc::tmem_ld_32x32b_x16(d + 16u * p, v);
-                        tc::tmem_ld_wait();
-                        if (c < chunks - 1) tc::tmem_st_zero_32x32b_x16(d + 16u * p);
-                        if (chunks == 2) {
-#pragma unroll
-                            for (int i = 0; i < 16; ++i)
-                                sum[p][i] = c == 0 ? __uint_as_float(v[i]) : __fadd_rn(sum[p][i], __uint_as_float(v[i]));
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) {
-                                const int s = __float2int_rn(__uint_as_float(v[i]));
-                                sum[p][i] = __int_as_float(c == 0 ? s : __float_as_int(sum[p][i]) + s);
-                            }
-                        }
-                        if (c == chunks - 1) {   // the whole sum takes the last chunk's place
-#pragma unroll
-                            for (int i = 0; i < 16; ++i)
-                                v[i] = __float_as_uint(chunks == 2 ? sum[p][i] : __int2float_rn(__float_as_int(sum[p][i])));
-                            tc::tmem_st_32x32b_x16(d + 16u * p, v);
-                        }
-                    }
-                    tc::tmem_st_wait();
-                }
-                if (c == chunks - 1) {
-                    // (not unrolled: code that runs once per unit comes from memory again each time)
-#pragma unroll 1
-                    for (int p = 0; p < pieces; ++p) {
-                        uint32_t w[16];
-                        tc::tmem_ld_32x32b_x16(d + 16u * p, w);
-                        tc::tmem_ld_wait();
-                        tc::tmem_st_zero_32x32b_x16(d + 16u * p);
-                        float v[16];
-                        const Shared::Row* r = row + 16 * p;
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) v[i] = __fmul_rn(__fmul_rn(r[i].scale, b), __uint_as_float(w[i]));
-                        if (SWIGLU) {
-#pragma unroll
-                            for (int i = 0; i < 16; i += 2) {
-                                const float other = __shfl_xor_sync(0xffffffffu, mine ? v[i] : v[i + 1], 16);
-                                const float g = mine ? other : v[i], up = mine ? v[i + 1] : other;
-                                v[i] = __fmul_rn(silu(g), up);
-                            }
-                        }
-                        // (no value's computation hangs on another's store: the chains run side by side)
-                        if (live) {
-                            if (a.y_dtype == kF32) store_rows<float, SWIGLU>(a.y, r, v, mine, n);
-                            else if (a.y_dtype == kF16) store_rows<__half, SWIGLU>(a.y, r, v, mine, n);
-                            else store_rows<__nv_bfloat16, SWIGLU>(a.y, r, v, mine, n);
-                        }
-                    }
-                    tc::tmem_st_wait();
-                }
+                return tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)((chunk_at & 1) * ROWS + c0);
+            };
+            auto hand_back = [&] {
+                tc::tmem_st_wait();
                 tc::tc_fence_before();
                 __syncwarp();
-                if (lane == 0) tc::mbar_arrive(&S.dempty[buf]);
+                if (lane == 0) arrive_relaxed(&S.dempty[chunk_at & 1]);
+                ++chunk_at;
+            };
+            for (int c = 0; ok && c < chunks - 1; ++c) {
+                const uint32_t d = next_chunk();
+                if (!ok) break;
+#pragma unroll
+                for (int p = 0; p < kPieces; ++p) {
+                    if (p >= pieces) continue;
+                    uint32_t v[16];
+                    tc::tmem_ld_32x32b_x16(d + 16u * p, v);
+                    tc::tmem_ld_wait();
+                    tc::tmem_st_zero_32x32b_x16(d + 16u * p);
+                    if (chunks == 2) {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) sum[p][i] = __uint_as_float(v[i]);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const int s = __float2int_rn(__uint_as_float(v[i]));
+                            sum[p][i] = __int_as_float(c == 0 ? s : __float_as_int(sum[p][i]) + s);
+                        }
+                    }
+                }
+                hand_back();
             }
-            __syncwarp();
+            if (!ok) break;
+            const uint32_t d = next_chunk();
+            if (!ok) break;
+            if (chunks > 1) {   // the whole sum takes the last chunk's place
+#pragma unroll
+                for (int p = 0; p < kPieces; ++p) {
+                    if (p >= pieces) continue;
+                    uint32_t v[16];
+                    tc::tmem_ld_32x32b_x16(d + 16u * p, v);
+                    tc::tmem_ld_wait();
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const float x = __uint_as_float(v[i]);
+                        v[i] = __float_as_uint(chunks == 2 ? __fadd_rn(sum[p][i], x)
+                                                           : __int2float_rn(__float_as_int(sum[p][i]) + __float2int_rn(x)));
+                    }
+                    tc::tmem_st_32x32b_x16(d + 16u * p, v);
+                }
+                tc::tmem_st_wait();
+            }
+            // (not unrolled: code that runs once per unit comes from memory again each time)
+#pragma unroll 1
+            for (int p = 0; p < pieces; ++p) {
+                uint32_t w[16];
+                tc::tmem_ld_32x32b_x16(d + 16u * p, w);
+                tc::tmem_ld_wait();
+                tc::tmem_st_zero_32x32b_x16(d + 16u * p);
+                // All of the rows' places are read, and all values made, before the first is stored: a read of
+                // shared memory would not be moved ahead of a store (108 cycles for each row).
+                constexpr int kOut = SWIGLU ? 8 : 16;
+                float v[kOut];
+                int item[kOut];
+                const Shared::Row* r = row + 16 * p;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const float d0 = __fmul_rn(__fmul_rn(r[i].scale, b), __uint_as_float(w[i]));
+                    if (SWIGLU) w[i] = __float_as_uint(d0);
+                    else v[i] = d0;
+                }
+#pragma unroll
+                for (int i = 0; i < kOut; ++i) {
+                    item[i] = r[SWIGLU ? 2 * i + mine : i].item;
+                    if (!live) item[i] = -1;
+                }
+                if (SWIGLU) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float other = __shfl_xor_sync(0xffffffffu, __uint_as_float(mine ? w[2 * i] : w[2 * i + 1]), 16);
+                        const float own = __uint_as_float(mine ? w[2 * i + 1] : w[2 * i]);
+                        const float g = mine ? other : own, up = mine ? own : other;
+                        v[i] = __fmul_rn(silu(g), up);
+                    }
+                }
+                if (a.y_dtype == kF32) store_rows(static_cast<float*>(a.y) + n, a.y_stride, item, v);
+                else if (a.y_dtype == kF16) store_rows(static_cast<__half*>(a.y) + n, a.y_stride, item, v);
+                else store_rows(static_cast<__nv_bfloat16*>(a.y) + n, a.y_stride, item, v);
+            }
+            hand_back();
         }
     } else if (warp < kWeightWarp) {
         // -------------------------------------------------------- converters
