@@ -42,6 +42,7 @@ struct LoraArgs {
     RowsView x, base, out;
     float* t;          // workspace: [split][place in the list][rank]
     int K, N, rank, splits, k_per;   // positions of K of a split
+    int col_blocks;    // of kOuterCols columns, of a CTA of the outer product
     bool vec;          // base and out allow 16-byte accesses
 };
 
@@ -129,6 +130,7 @@ __global__ void __launch_bounds__(kThreads) k_lora_inner(const __grid_constant__
     float* sum = reinterpret_cast<float*>(smem_in + sizeof(Places));   // [warp][row][8 * NT]
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
     pdl_wait();
+    pdl_launch_next();
     if (warp == 0) plan_tiles(a.plan, kInnerRows, P.begin, P.tile0, lane);
     __syncthreads();
     const int tiles = P.tile0[a.plan.owners];
@@ -207,20 +209,163 @@ __global__ void __launch_bounds__(kThreads) k_lora_inner(const __grid_constant__
     }
 }
 
-// out of up to kOuterRows rows of one adapter, for kOuterCols columns: a warp has
-// 32 of them, with B in registers, and takes 16 rows at a time. KK: chunks of 32 of the rank.
-template <int DT, int KK>
-__global__ void __launch_bounds__(kThreads) k_lora_outer(const __grid_constant__ LoraArgs a) {
+__device__ __forceinline__ void copy16(void* dst, const void* src, bool in) {   // zeros where `in` is false
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src),
+                 "r"(in ? 16 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// The same for up to kTileRows rows where adapters have many: x and A come through
+// shared memory, kStages stages of 64 positions ahead, so that A is read once for
+// all of the rows and a warp holds no loads. Warp (m, h) has 16 rows and half of a stage's positions.
+// 16-byte piece j of a row lies at another place in neighbouring rows, so that the
+// eight lanes that read at once meet no bank twice.
+constexpr int kTileRows = 64, kStages = 4, kStageK = 64;
+
+template <int DT, int NT>
+struct TileShape {
+    static constexpr int kSize = DT == kF32 ? 4 : 2;
+    static constexpr int kXRow = kStageK * kSize, kARow = kStageK * 2;
+    static constexpr int kX = kTileRows * kXRow, kStage = kX + 8 * NT * kARow;
+    static constexpr int kBytes = (int)sizeof(Places) + kStages * kStage;
+};
+template <int ROW_BYTES>
+__device__ __forceinline__ int piece_at(int row, int j) {
+    if (ROW_BYTES == 256) return row * 256 + ((j ^ (row & 7)) << 4);
+    return row * 128 + ((j ^ ((row & 1) << 2 | (row >> 1 & 3))) << 4);
+}
+
+template <int DT, int NT>
+__global__ void __launch_bounds__(kThreads, 2) k_lora_inner_tile(const __grid_constant__ LoraArgs a) {
     using W = Kind<DT>;
     using T = typename RowT<DT>::type;
-    constexpr int kPitch = 32 * KK + 8;   // of a row of t's parts: rows 16 bytes apart in the banks
+    using C = TileShape<DT, NT>;
+    constexpr int kWords = DT == kF32 ? 2 : 1, kPieces = C::kXRow / 16;   // of a row of a stage
+    extern __shared__ __align__(16) uint8_t smem_ti[];
+    Places& P = *reinterpret_cast<Places*>(smem_ti);
+    uint8_t* ring = smem_ti + sizeof(Places);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
+    const int m = warp & 3, h = warp >> 2;
+    pdl_wait();
+    pdl_launch_next();
+    if (warp == 0) plan_tiles(a.plan, kTileRows, P.begin, P.tile0, lane);
+    __syncthreads();
+    if ((int)blockIdx.x >= P.tile0[a.plan.owners]) return;
+    const int o = owner_of_tile(P.tile0, a.plan.owners, blockIdx.x);
+    const int first = P.begin[o] + ((int)blockIdx.x - P.tile0[o]) * kTileRows;
+    const int rows = min(kTileRows, P.begin[o + 1] - first);
+    const int rank0 = blockIdx.z * 8 * NT;
+    const int k_lo = blockIdx.y * a.k_per, k_hi = min(a.K, k_lo + a.k_per);
+    const int steps = (k_hi - k_lo + kStageK - 1) / kStageK;
+
+    // this thread's pieces of each stage: piece pj of rows pr, pr + kThreads / kPieces, ...
+    constexpr int kPer = kTileRows * kPieces / kThreads;
+    const int pr = tid / kPieces, pj = tid % kPieces;
+    const T* from[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        const int item = __ldcg(a.plan.list + first + min(pr + i * (kThreads / kPieces), rows - 1));
+        from[i] = static_cast<const T*>(a.x.data) + min(max(item, 0), a.plan.items - 1) * a.x.stride + pj * (16 / C::kSize);
+    }
+    const uint16_t* A = static_cast<const uint16_t*>(a.A) + ((long long)o * a.rank + rank0) * a.K;
+    auto load = [&](int step) {
+        if (step < steps) {
+            uint8_t* at = ring + step % kStages * C::kStage;
+            const int k = k_lo + step * kStageK;
+            const bool in = k + pj * (16 / C::kSize) < k_hi;
+#pragma unroll
+            for (int i = 0; i < kPer; ++i)
+                copy16(at + piece_at<C::kXRow>(pr + i * (kThreads / kPieces), pj), in ? from[i] + k : from[i], in);
+            at += C::kX;
+            for (int i = tid; i < 8 * NT * 8; i += kThreads) {
+                const int r = i >> 3, j = i & 7;
+                const bool there = rank0 + r < a.rank && k + 8 * j < k_hi;
+                copy16(at + piece_at<C::kARow>(r, j), there ? A + (long long)r * a.K + k + 8 * j : A, there);
+            }
+        }
+        copies_commit();
+    };
+    float acc[NT][4] = {};
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) load(i);
+    for (int step = 0; step < steps; ++step) {
+        copies_wait<kStages - 2>();
+        __syncthreads();   // the stage is there for all, and the one before it is done with
+        load(step + kStages - 1);
+        if (16 * m >= rows) continue;
+        const uint8_t* at = ring + step % kStages * C::kStage;
+        uint32_t ap[2][W::kXParts][4];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            uint4 w[kWords];
+#pragma unroll
+            for (int j = 0; j < kWords; ++j)
+                w[j] = *reinterpret_cast<const uint4*>(at + piece_at<C::kXRow>(16 * m + g + 8 * i, (4 * h + c) * kWords + j));
+            parts_x<DT>(w, ap[i]);
+        }
+        uint4 b[NT];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) b[n] = *reinterpret_cast<const uint4*>(at + C::kX + piece_at<C::kARow>(8 * n + g, 4 * h + c));
+#pragma unroll
+        for (int p = W::kXParts - 1; p >= 0; --p) {
+            const uint32_t a0[4] = {ap[0][p][0], ap[1][p][0], ap[0][p][1], ap[1][p][1]};
+            const uint32_t a1[4] = {ap[0][p][2], ap[1][p][2], ap[0][p][3], ap[1][p][3]};
+#pragma unroll
+            for (int n = 0; n < NT; ++n) mma16816<W::kF16Mma>(acc[n], a0, b[n].x, b[n].y);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) mma16816<W::kF16Mma>(acc[n], a1, b[n].z, b[n].w);
+        }
+    }
+    copies_wait<0>();
+    __syncthreads();
+    // the two halves' sums
+    float* sum = reinterpret_cast<float*>(ring);   // [64][8 * NT]
+    constexpr int kRow = 8 * NT;
+    static_assert(kTileRows * kRow * 4 <= kStages * C::kStage, "sums");
+    if (h == 1)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                *reinterpret_cast<float2*>(sum + (16 * m + g + 8 * i) * kRow + 8 * n + 2 * c) = make_float2(acc[n][2 * i], acc[n][2 * i + 1]);
+    __syncthreads();
+    if (h == 1) return;
+    float* to = a.t + ((long long)blockIdx.y * a.plan.items + first) * a.rank + rank0;
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int row = 16 * m + g + 8 * i;
+            const float2 other = *reinterpret_cast<const float2*>(sum + row * kRow + 8 * n + 2 * c);
+            if (row < rows && rank0 + 8 * n < a.rank)
+                *reinterpret_cast<float2*>(to + (long long)row * a.rank + 8 * n + 2 * c) =
+                    make_float2(__fadd_rn(acc[n][2 * i], other.x), __fadd_rn(acc[n][2 * i + 1], other.y));
+        }
+}
+
+// Values from row to row of t's parts: 64 bytes more or less than a multiple of 128, so that
+// the eight lanes that read 16 bytes of two rows at once meet no bank twice.
+__host__ __device__ constexpr int pitch_of(int kk) { return 32 * (kk | 1); }
+
+// out of up to kOuterRows rows of one adapter, for a.col_blocks times kOuterCols
+// columns: a warp has 32 of each block's, with B in registers, and takes 16 rows at a
+// time, the base of the 16 after them already on its way. KK: chunks of 32 of the rank.
+template <int DT, int KK>
+__global__ void __launch_bounds__(kThreads, KK <= 2 ? 2 : 1) k_lora_outer(const __grid_constant__ LoraArgs a) {
+    using W = Kind<DT>;
+    using T = typename RowT<DT>::type;
+    constexpr int kPitch = pitch_of(KK);
     extern __shared__ __align__(16) uint8_t smem_out[];
     Places& P = *reinterpret_cast<Places*>(smem_out);
     uint16_t* tp = reinterpret_cast<uint16_t*>(smem_out + sizeof(Places));   // [part][row][kPitch]
     __shared__ float s_mul[kOuterRows];      // what a row's sums are multiplied with
     __shared__ int s_item[kOuterRows];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
-    pdl_wait();
+    // All but t is older than the inner product's launch, which began when what made it was complete: it is read before
+    // pdl_wait, while the inner product runs.
     if (warp == 0) plan_tiles(a.plan, kOuterRows, P.begin, P.tile0, lane);
     __syncthreads();
     const int tiles = P.tile0[a.plan.owners];
@@ -228,18 +373,44 @@ __global__ void __launch_bounds__(kThreads) k_lora_outer(const __grid_constant__
     const int o = owner_of_tile(P.tile0, a.plan.owners, blockIdx.x);
     const int first = P.begin[o] + ((int)blockIdx.x - P.tile0[o]) * kOuterRows;
     const int rows = min(kOuterRows, P.begin[o + 1] - first);
-    const int n0 = blockIdx.y * kOuterCols + warp * 32;
+    int n0 = blockIdx.y * a.col_blocks * kOuterCols + warp * 32;
+    const int n_end = min(a.N, (int)(blockIdx.y + 1) * a.col_blocks * kOuterCols);
 
     // B: column j of MMA tile i of the warp is n0 + 8 * (j / 2) + 2 * i + j % 2
     uint4 b[4][KK];
+    auto load_b = [&] {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int n = n0 + 8 * (g >> 1) + 2 * i + (g & 1);
-        const uint16_t* from = static_cast<const uint16_t*>(a.B) + ((long long)o * a.N + n) * a.rank + 8 * c;
+        for (int i = 0; i < 4; ++i) {
+            const int n = n0 + 8 * (g >> 1) + 2 * i + (g & 1);
+            const uint16_t* from = static_cast<const uint16_t*>(a.B) + ((long long)o * a.N + n) * a.rank + 8 * c;
 #pragma unroll
-        for (int k = 0; k < KK; ++k)
-            b[i][k] = n < a.N && 32 * k + 8 * c < a.rank ? __ldg(reinterpret_cast<const uint4*>(from + 32 * k)) : make_uint4(0u, 0u, 0u, 0u);
+            for (int k = 0; k < KK; ++k)
+                b[i][k] = n < a.N && 32 * k + 8 * c < a.rank ? __ldg(reinterpret_cast<const uint4*>(from + 32 * k)) : make_uint4(0u, 0u, 0u, 0u);
+        }
+    };
+    load_b();
+    if (tid < kOuterRows) {
+        const int item = tid < rows ? __ldcg(a.plan.list + first + tid) : -1;
+        s_item[tid] = item >= 0 && item < a.plan.items ? item : -1;
     }
+    __syncthreads();
+    // base of rows m + g and m + g + 8 of the tile, columns n .. n + 7, as they lie in memory
+    constexpr int kVecs = 8 * (int)sizeof(T) / 16;
+    auto load_base = [&](uint4 (&y)[2][kVecs], int at, int m) {
+        const int n = at + 8 * c;
+        if (at >= n_end || !(a.vec && n + 8 <= a.N)) return;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int item = s_item[m + g + 8 * h];
+            if (item < 0) continue;
+            const uint4* from = reinterpret_cast<const uint4*>(static_cast<const T*>(a.base.data) + item * a.base.stride + n);
+#pragma unroll
+            for (int i = 0; i < kVecs; ++i) y[h][i] = from[i];
+        }
+    };
+    uint4 next[2][kVecs] = {};
+    load_base(next, n0, 0);
+    pdl_wait();
     const float scale = a.scale != nullptr ? __ldg(a.scale + o) : 1.0f;
     // t of the rows in parts, 8 lanes or more to a row
     constexpr int kLanes = 8 * KK > 32 ? 32 : 8 * KK;   // of a row, 4 values each
@@ -249,6 +420,7 @@ __global__ void __launch_bounds__(kThreads) k_lora_outer(const __grid_constant__
         float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
         if (r < rows && q < a.rank) {
             const float* from = a.t + (long long)(first + r) * a.rank + q;
+#pragma unroll 4
             for (int s = 0; s < a.splits; ++s) {
                 const float4 w = __ldcg(reinterpret_cast<const float4*>(from + (long long)s * a.plan.items * a.rank));
                 v[0] = __fadd_rn(v[0], w.x);
@@ -299,77 +471,68 @@ __global__ void __launch_bounds__(kThreads) k_lora_outer(const __grid_constant__
             *reinterpret_cast<uint2*>(tp + (j * kOuterRows + r) * kPitch + q) = make_uint2(p[j][0], p[j][1]);
         if (q == 0) {
             s_mul[r] = mul;
-            const int item = r < rows ? __ldcg(a.plan.list + first + r) : -1;
-            s_item[r] = item >= 0 && item < a.plan.items ? item : -1;
         }
     }
     __syncthreads();
-    if (n0 >= a.N) return;
-    const int n = n0 + 8 * c;
-    const bool vec = a.vec && n + 8 <= a.N;
-    for (int m = 0; m < rows; m += 16) {
-        // base of rows m + g and m + g + 8, columns n .. n + 7
-        float y[2][8];
-        int item[2];
+    while (n0 < n_end) {
+        const int n = n0 + 8 * c;
+        const bool vec = a.vec && n + 8 <= a.N;
+        for (int m = 0; m < rows; m += 16) {
+            uint4 y[2][kVecs];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            item[h] = s_item[m + g + 8 * h];
-            if (item[h] < 0) continue;
-            const T* from = static_cast<const T*>(a.base.data) + item[h] * a.base.stride + n;
-            if (vec) {
-                struct alignas(16) V { T v[16 / sizeof(T)]; };
-                constexpr int kPer = 16 / sizeof(T);
+            for (int h = 0; h < 2; ++h)
 #pragma unroll
-                for (int i = 0; i < 8 / kPer; ++i) {
-                    const V w = *reinterpret_cast<const V*>(from + kPer * i);
+                for (int i = 0; i < kVecs; ++i) y[h][i] = next[h][i];
+            const bool more = m + 16 < rows;
+            load_base(next, more ? n0 : n0 + kOuterCols, more ? m + 16 : 0);
+            float acc[4][4] = {};
 #pragma unroll
-                    for (int j = 0; j < kPer; ++j) y[h][kPer * i + j] = to_f32(w.v[j]);
+            for (int p = W::kTParts - 1; p >= 0; --p)
+#pragma unroll
+                for (int k = 0; k < KK; ++k) {
+                    const uint16_t* from = tp + (p * kOuterRows + m + g) * kPitch + 32 * k + 8 * c;
+                    const uint4 lo = *reinterpret_cast<const uint4*>(from), hi = *reinterpret_cast<const uint4*>(from + 8 * kPitch);
+                    const uint32_t a0[4] = {lo.x, hi.x, lo.y, hi.y}, a1[4] = {lo.z, hi.z, lo.w, hi.w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        mma16816<W::kF16Mma>(acc[i], a0, b[i][k].x, b[i][k].y);
+                        mma16816<W::kF16Mma>(acc[i], a1, b[i][k].z, b[i][k].w);
+                    }
                 }
-            } else {
+            if (!more && n0 + kOuterCols < n_end) {   // B of the next block, while this one is finished
+                n0 += kOuterCols;
+                load_b();
+                n0 -= kOuterCols;
+            }
 #pragma unroll
-                for (int i = 0; i < 8; ++i) y[h][i] = n + i < a.N ? to_f32(from[i]) : 0.0f;
+            for (int h = 0; h < 2; ++h) {
+                const int item = s_item[m + g + 8 * h];
+                if (item < 0) continue;
+                const float mul = s_mul[m + g + 8 * h];
+                T* to = static_cast<T*>(a.out.data) + item * a.out.stride + n;
+                struct alignas(16) V { T v[16 / sizeof(T)]; };
+                constexpr int kPer = 16 / (int)sizeof(T);
+                if (vec) {
+#pragma unroll
+                    for (int i = 0; i < kVecs; ++i) {
+                        const V old = *reinterpret_cast<const V*>(&y[h][i]);
+                        V w;
+#pragma unroll
+                        for (int j = 0; j < kPer; ++j) {
+                            const int q = kPer * i + j;   // column of the thread's eight
+                            put_as(w.v, DT, j, fmaf(mul, acc[q >> 1][2 * h + (q & 1)], to_f32(old.v[j])));
+                        }
+                        *reinterpret_cast<V*>(to + kPer * i) = w;
+                    }
+                } else {
+                    const T* from = static_cast<const T*>(a.base.data) + item * a.base.stride + n;
+#pragma unroll
+                    for (int q = 0; q < 8; ++q)
+                        if (n + q < a.N) put_as(to, DT, q, fmaf(mul, acc[q >> 1][2 * h + (q & 1)], to_f32(from[q])));
+                }
             }
         }
-        float acc[4][4] = {};
-#pragma unroll
-        for (int p = W::kTParts - 1; p >= 0; --p)
-#pragma unroll
-            for (int k = 0; k < KK; ++k) {
-                const uint16_t* from = tp + (p * kOuterRows + m + g) * kPitch + 32 * k + 8 * c;
-                const uint4 lo = *reinterpret_cast<const uint4*>(from), hi = *reinterpret_cast<const uint4*>(from + 8 * kPitch);
-                const uint32_t a0[4] = {lo.x, hi.x, lo.y, hi.y}, a1[4] = {lo.z, hi.z, lo.w, hi.w};
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    mma16816<W::kF16Mma>(acc[i], a0, b[i][k].x, b[i][k].y);
-                    mma16816<W::kF16Mma>(acc[i], a1, b[i][k].z, b[i][k].w);
-                }
-            }
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            if (item[h] < 0) continue;
-            const float mul = s_mul[m + g + 8 * h];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                y[h][2 * i] = fmaf(mul, acc[i][2 * h], y[h][2 * i]);
-                y[h][2 * i + 1] = fmaf(mul, acc[i][2 * h + 1], y[h][2 * i + 1]);
-            }
-            T* to = static_cast<T*>(a.out.data) + item[h] * a.out.stride + n;
-            if (vec) {
-                struct alignas(16) V { T v[16 / sizeof(T)]; };
-                constexpr int kPer = 16 / sizeof(T);
-#pragma unroll
-                for (int i = 0; i < 8 / kPer; ++i) {
-                    V w;
-#pragma unroll
-                    for (int j = 0; j < kPer; ++j) put_as(w.v, DT, j, y[h][kPer * i + j]);
-                    *reinterpret_cast<V*>(to + kPer * i) = w;
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    if (n + i < a.N) put_as(to, DT, i, y[h][i]);
-            }
-        }
+        n0 += kOuterCols;
     }
 }
 
@@ -389,10 +552,14 @@ cudaError_t allow_smem(K kernel, int bytes, std::atomic<unsigned long long>& rea
 // Row tiles there may be: no more than one per adapter and one per `rows` items.
 int64_t most_tiles(const PlanView& p, int rows) { return std::min(p.items, p.owners) + p.items / rows; }
 
-// How K is split: into multiples of the warps' 256 positions, as far as it takes
-// to have two CTAs per SM.
+// Adapters with many rows go through tiles of kTileRows in shared memory.
+bool many_rows(int64_t items, int owners) { return items >= 32 * (int64_t)owners; }
+
+// How K is split: as far as it takes to have two CTAs per SM, into multiples of the warps' 256 positions (few rows)
+// or of 256 at least (tiles).
 int inner_splits(int64_t items, int owners, int K, int groups) {
-    const int64_t likely = std::max<int64_t>(std::min<int64_t>(items, owners), items / kInnerRows) * groups;
+    const int rows = many_rows(items, owners) ? kTileRows : kInnerRows;
+    const int64_t likely = std::max<int64_t>(std::min<int64_t>(items, owners), (items + rows - 1) / rows) * groups;
     const int64_t most = (K + kWarps * 32 - 1) / (kWarps * 32);
     return (int)std::max<int64_t>(1, std::min<int64_t>({2 * 152 / likely, most, (int64_t)kMaxSplits}));
 }
@@ -401,8 +568,16 @@ int rank_tiles(int rank) { return rank <= 8 ? 1 : rank <= 16 ? 2 : rank <= 32 ? 
 
 template <int DT, int NT>
 cudaError_t launch_inner(const LoraArgs& a, cudaStream_t s) {
+    if (many_rows(a.plan.items, a.plan.owners)) {
+        constexpr int bytes = TileShape<DT, NT>::kBytes;
+        static std::atomic<unsigned long long> ready{0};   // a bit per device
+        const cudaError_t e = allow_smem(k_lora_inner_tile<DT, NT>, bytes, ready);
+        if (e != cudaSuccess) return e;
+        const dim3 grid((unsigned)most_tiles(a.plan, kTileRows), (unsigned)a.splits, (unsigned)((a.rank + 8 * NT - 1) / (8 * NT)));
+        return launch_pdl(k_lora_inner_tile<DT, NT>, grid, dim3(kThreads), bytes, s, a);
+    }
     constexpr int bytes = (int)sizeof(Places) + kWarps * kInnerRows * 8 * NT * 4;
-    static std::atomic<unsigned long long> ready{0};   // a bit per device
+    static std::atomic<unsigned long long> ready{0};
     const cudaError_t e = allow_smem(k_lora_inner<DT, NT>, bytes, ready);
     if (e != cudaSuccess) return e;
     const dim3 grid((unsigned)most_tiles(a.plan, kInnerRows), (unsigned)a.splits, (unsigned)((a.rank + 8 * NT - 1) / (8 * NT)));
@@ -411,11 +586,11 @@ cudaError_t launch_inner(const LoraArgs& a, cudaStream_t s) {
 
 template <int DT, int KK>
 cudaError_t launch_outer(const LoraArgs& a, cudaStream_t s) {
-    constexpr int bytes = (int)sizeof(Places) + Kind<DT>::kTParts * kOuterRows * (32 * KK + 8) * 2;
+    constexpr int bytes = (int)sizeof(Places) + Kind<DT>::kTParts * kOuterRows * pitch_of(KK) * 2;
     static std::atomic<unsigned long long> ready{0};
     const cudaError_t e = allow_smem(k_lora_outer<DT, KK>, bytes, ready);
     if (e != cudaSuccess) return e;
-    const dim3 grid((unsigned)most_tiles(a.plan, kOuterRows), (unsigned)((a.N + kOuterCols - 1) / kOuterCols));
+    const dim3 grid((unsigned)most_tiles(a.plan, kOuterRows), (unsigned)((a.N + a.col_blocks * kOuterCols - 1) / (a.col_blocks * kOuterCols)));
     return launch_pdl(k_lora_outer<DT, KK>, grid, dim3(kThreads), bytes, s, a);
 }
 
@@ -493,6 +668,10 @@ int lora_add(const lora_adapters* a, const route_plan* plan, const i2s_rows* x, 
     p.splits = inner_splits(rows, p.plan.owners, p.K, (a->rank + 63) / 64);
     p.k_per = ((p.K + p.splits - 1) / p.splits + kWarps * 32 - 1) / (kWarps * 32) * (kWarps * 32);
     p.splits = (p.K + p.k_per - 1) / p.k_per;   // none empty
+    // as many columns to a CTA as leave two CTAs per SM, all that run at once
+    const int64_t tiles = std::max<int64_t>(std::min<int64_t>(rows, p.plan.owners), (rows + kOuterRows - 1) / kOuterRows);
+    const int64_t blocks = (p.N + kOuterCols - 1) / kOuterCols;
+    p.col_blocks = (int)std::max<int64_t>(1, (tiles * blocks + 2 * 152 - 1) / (2 * 152));
     const int size = dtype_bytes(x->dtype);
     p.vec = !(((uintptr_t)base->data | (uintptr_t)out->data) & 15) &&
             (rows == 1 || (base->stride * size % 16 == 0 && out->stride * size % 16 == 0));
