@@ -352,7 +352,14 @@ __host__ __device__ constexpr int pitch_of(int kk) { return 32 * (kk | 1); }
 
 // out of up to kOuterRows rows of one adapter, for a.col_blocks times kOuterCols
 // columns: a warp has 32 of each block's, with B in registers, and takes 16 rows at a
-// time, the base of the 16 after them already on its way. KK: chunks of 32 of the rank.
+// time. A thread's part of base comes through its own places in shared memory, kDepth - 1
+// steps ahead (as many bytes as keep DRAM busy, and no registers; with one step ahead in registers a
+// prompt of 8000 rows took 39 us, 5000 bf16 rows of 8960 columns 40). KK: chunks of 32 of the rank.
+constexpr int kRingBytes = 65536;
+template <int DT>
+__host__ __device__ constexpr int outer_vecs() { return 8 * (DT == kF32 ? 4 : 2) / 16; }   // 16-byte pieces of a thread's eight columns
+template <int DT>
+__host__ __device__ constexpr int outer_depth() { return kRingBytes / (2 * outer_vecs<DT>() * kThreads * 16); }
 template <int DT, int KK>
 __global__ void __launch_bounds__(kThreads, KK <= 2 ? 2 : 1) k_lora_outer(const __grid_constant__ LoraArgs a) {
     using W = Kind<DT>;
@@ -394,22 +401,30 @@ __global__ void __launch_bounds__(kThreads, KK <= 2 ? 2 : 1) k_lora_outer(const 
         s_item[tid] = item >= 0 && item < a.plan.items ? item : -1;
     }
     __syncthreads();
-    // base of rows m + g and m + g + 8 of the tile, columns n .. n + 7, as they lie in memory
-    constexpr int kVecs = 8 * (int)sizeof(T) / 16;
-    auto load_base = [&](uint4 (&y)[2][kVecs], int at, int m) {
-        const int n = at + 8 * c;
-        if (at >= n_end || !(a.vec && n + 8 <= a.N)) return;
+    // Steps of 16 rows, the rows of one block of columns after another. A step's base of rows
+    // m + g and m + g + 8, columns n .. n + 7, as they lie in memory.
+    constexpr int kVecs = outer_vecs<DT>(), kDepth = outer_depth<DT>();
+    uint4* ring = reinterpret_cast<uint4*>(smem_out + sizeof(Places) + W::kTParts * kOuterRows * kPitch * 2) + tid;
+    int ahead = 0, ahead_m = 0, ahead_n = n0 + 8 * c;   // the step to fetch next
+    auto fetch = [&] {
+        if (ahead_n - 8 * c < n_end && a.vec && ahead_n + 8 <= a.N) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int item = s_item[m + g + 8 * h];
-            if (item < 0) continue;
-            const uint4* from = reinterpret_cast<const uint4*>(static_cast<const T*>(a.base.data) + item * a.base.stride + n);
+            for (int h = 0; h < 2; ++h) {
+                const int item = s_item[ahead_m + g + 8 * h];
+                if (item < 0) continue;
+                const T* from = static_cast<const T*>(a.base.data) + item * a.base.stride + ahead_n;
 #pragma unroll
-            for (int i = 0; i < kVecs; ++i) y[h][i] = from[i];
+                for (int i = 0; i < kVecs; ++i)
+                    copy16(ring + ((ahead % kDepth * 2 + h) * kVecs + i) * kThreads, from + i * (16 / (int)sizeof(T)), true);
+            }
         }
+        copies_commit();
+        ++ahead;
+        ahead_m += 16;
+        if (ahead_m >= rows) ahead_m = 0, ahead_n += kOuterCols;
     };
-    uint4 next[2][kVecs] = {};
-    load_base(next, n0, 0);
+#pragma unroll
+    for (int i = 0; i < kDepth - 1; ++i) fetch();
     pdl_wait();
     const float scale = a.scale != nullptr ? __ldg(a.scale + o) : 1.0f;
     // t of the rows in parts, 8 lanes or more to a row
@@ -474,17 +489,12 @@ __global__ void __launch_bounds__(kThreads, KK <= 2 ? 2 : 1) k_lora_outer(const 
         }
     }
     __syncthreads();
+    int step = 0;
     while (n0 < n_end) {
         const int n = n0 + 8 * c;
         const bool vec = a.vec && n + 8 <= a.N;
-        for (int m = 0; m < rows; m += 16) {
-            uint4 y[2][kVecs];
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int i = 0; i < kVecs; ++i) y[h][i] = next[h][i];
-            const bool more = m + 16 < rows;
-            load_base(next, more ? n0 : n0 + kOuterCols, more ? m + 16 : 0);
+        for (int m = 0; m < rows; m += 16, ++step) {
+            fetch();
             float acc[4][4] = {};
 #pragma unroll
             for (int p = W::kTParts - 1; p >= 0; --p)
@@ -499,11 +509,12 @@ __global__ void __launch_bounds__(kThreads, KK <= 2 ? 2 : 1) k_lora_outer(const 
                         mma16816<W::kF16Mma>(acc[i], a1, b[i][k].z, b[i][k].w);
                     }
                 }
-            if (!more && n0 + kOuterCols < n_end) {   // B of the next block, while this one is finished
+            if (m + 16 >= rows && n0 + kOuterCols < n_end) {   // B of the next block, while this one is finished
                 n0 += kOuterCols;
                 load_b();
                 n0 -= kOuterCols;
             }
+            copies_wait<kDepth - 1>();
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int item = s_item[m + g + 8 * h];
@@ -515,7 +526,7 @@ __global__ void __launch_bounds__(kThreads, KK <= 2 ? 2 : 1) k_lora_outer(const 
                 if (vec) {
 #pragma unroll
                     for (int i = 0; i < kVecs; ++i) {
-                        const V old = *reinterpret_cast<const V*>(&y[h][i]);
+                        const V old = *reinterpret_cast<const V*>(ring + ((step % kDepth * 2 + h) * kVecs + i) * kThreads);
                         V w;
 #pragma unroll
                         for (int j = 0; j < kPer; ++j) {
@@ -534,6 +545,7 @@ __global__ void __launch_bounds__(kThreads, KK <= 2 ? 2 : 1) k_lora_outer(const 
         }
         n0 += kOuterCols;
     }
+    copies_wait<0>();
 }
 
 // ---------------------------------------------------------------------------
@@ -586,7 +598,7 @@ cudaError_t launch_inner(const LoraArgs& a, cudaStream_t s) {
 
 template <int DT, int KK>
 cudaError_t launch_outer(const LoraArgs& a, cudaStream_t s) {
-    constexpr int bytes = (int)sizeof(Places) + Kind<DT>::kTParts * kOuterRows * pitch_of(KK) * 2;
+    constexpr int bytes = (int)sizeof(Places) + Kind<DT>::kTParts * kOuterRows * pitch_of(KK) * 2 + kRingBytes;
     static std::atomic<unsigned long long> ready{0};
     const cudaError_t e = allow_smem(k_lora_outer<DT, KK>, bytes, ready);
     if (e != cudaSuccess) return e;
