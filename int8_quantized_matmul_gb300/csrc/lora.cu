@@ -42,7 +42,6 @@ struct LoraArgs {
     RowsView x, base, out;
     float* t;          // workspace: [split][place in the list][rank]
     int K, N, rank, splits, k_per;   // positions of K of a split
-    int col_blocks;    // of kOuterCols columns, of a CTA of the outer product
     bool vec;          // base and out allow 16-byte accesses
 };
 
@@ -214,200 +213,135 @@ __device__ __forceinline__ void copy16(void* dst, const void* src, bool in) {   
                  "r"(in ? 16 : 0)
                  : "memory");
 }
+__device__ __forceinline__ void store16(float* p, const float (&v)[4]) {
+    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+}
+__device__ __forceinline__ void store16(__half* p, const float (&v)[8]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __half2 h = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ void store16(__nv_bfloat16* p, const float (&v)[8]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
-
-// The same for up to kTileRows rows where adapters have many: x and A come through
-// shared memory, kStages stages of 64 positions ahead, so that A is read once for
-// all of the rows and a warp holds no loads. Warp (m, h) has 16 rows and half of a stage's positions.
-// 16-byte piece j of a row lies at another place in neighbouring rows, so that the
-// eight lanes that read at once meet no bank twice.
-constexpr int kTileRows = 64, kStages = 4, kStageK = 64;
-
-template <int DT, int NT>
-struct TileShape {
-    static constexpr int kSize = DT == kF32 ? 4 : 2;
-    static constexpr int kXRow = kStageK * kSize, kARow = kStageK * 2;
-    static constexpr int kX = kTileRows * kXRow, kStage = kX + 8 * NT * kARow;
-    static constexpr int kBytes = (int)sizeof(Places) + kStages * kStage;
-};
-template <int ROW_BYTES>
-__device__ __forceinline__ int piece_at(int row, int j) {
-    if (ROW_BYTES == 256) return row * 256 + ((j ^ (row & 7)) << 4);
-    return row * 128 + ((j ^ ((row & 1) << 2 | (row >> 1 & 3))) << 4);
-}
-
-template <int DT, int NT>
-__global__ void __launch_bounds__(kThreads, 2) k_lora_inner_tile(const __grid_constant__ LoraArgs a) {
-    using W = Kind<DT>;
-    using T = typename RowT<DT>::type;
-    using C = TileShape<DT, NT>;
-    constexpr int kWords = DT == kF32 ? 2 : 1, kPieces = C::kXRow / 16;   // of a row of a stage
-    extern __shared__ __align__(16) uint8_t smem_ti[];
-    Places& P = *reinterpret_cast<Places*>(smem_ti);
-    uint8_t* ring = smem_ti + sizeof(Places);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
-    const int m = warp & 3, h = warp >> 2;
-    pdl_wait();
-    pdl_launch_next();
-    if (warp == 0) plan_tiles(a.plan, kTileRows, P.begin, P.tile0, lane);
-    __syncthreads();
-    if ((int)blockIdx.x >= P.tile0[a.plan.owners]) return;
-    const int o = owner_of_tile(P.tile0, a.plan.owners, blockIdx.x);
-    const int first = P.begin[o] + ((int)blockIdx.x - P.tile0[o]) * kTileRows;
-    const int rows = min(kTileRows, P.begin[o + 1] - first);
-    const int rank0 = blockIdx.z * 8 * NT;
-    const int k_lo = blockIdx.y * a.k_per, k_hi = min(a.K, k_lo + a.k_per);
-    const int steps = (k_hi - k_lo + kStageK - 1) / kStageK;
-
-    // this thread's pieces of each stage: piece pj of rows pr, pr + kThreads / kPieces, ...
-    constexpr int kPer = kTileRows * kPieces / kThreads;
-    const int pr = tid / kPieces, pj = tid % kPieces;
-    const T* from[kPer];
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        const int item = __ldcg(a.plan.list + first + min(pr + i * (kThreads / kPieces), rows - 1));
-        from[i] = static_cast<const T*>(a.x.data) + min(max(item, 0), a.plan.items - 1) * a.x.stride + pj * (16 / C::kSize);
-    }
-    const uint16_t* A = static_cast<const uint16_t*>(a.A) + ((long long)o * a.rank + rank0) * a.K;
-    auto load = [&](int step) {
-        if (step < steps) {
-            uint8_t* at = ring + step % kStages * C::kStage;
-            const int k = k_lo + step * kStageK;
-            const bool in = k + pj * (16 / C::kSize) < k_hi;
-#pragma unroll
-            for (int i = 0; i < kPer; ++i)
-                copy16(at + piece_at<C::kXRow>(pr + i * (kThreads / kPieces), pj), in ? from[i] + k : from[i], in);
-            at += C::kX;
-            for (int i = tid; i < 8 * NT * 8; i += kThreads) {
-                const int r = i >> 3, j = i & 7;
-                const bool there = rank0 + r < a.rank && k + 8 * j < k_hi;
-                copy16(at + piece_at<C::kARow>(r, j), there ? A + (long long)r * a.K + k + 8 * j : A, there);
-            }
-        }
-        copies_commit();
-    };
-    float acc[NT][4] = {};
-#pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) load(i);
-    for (int step = 0; step < steps; ++step) {
-        copies_wait<kStages - 2>();
-        __syncthreads();   // the stage is there for all, and the one before it is done with
-        load(step + kStages - 1);
-        if (16 * m >= rows) continue;
-        const uint8_t* at = ring + step % kStages * C::kStage;
-        uint32_t ap[2][W::kXParts][4];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            uint4 w[kWords];
-#pragma unroll
-            for (int j = 0; j < kWords; ++j)
-                w[j] = *reinterpret_cast<const uint4*>(at + piece_at<C::kXRow>(16 * m + g + 8 * i, (4 * h + c) * kWords + j));
-            parts_x<DT>(w, ap[i]);
-        }
-        uint4 b[NT];
-#pragma unroll
-        for (int n = 0; n < NT; ++n) b[n] = *reinterpret_cast<const uint4*>(at + C::kX + piece_at<C::kARow>(8 * n + g, 4 * h + c));
-#pragma unroll
-        for (int p = W::kXParts - 1; p >= 0; --p) {
-            const uint32_t a0[4] = {ap[0][p][0], ap[1][p][0], ap[0][p][1], ap[1][p][1]};
-            const uint32_t a1[4] = {ap[0][p][2], ap[1][p][2], ap[0][p][3], ap[1][p][3]};
-#pragma unroll
-            for (int n = 0; n < NT; ++n) mma16816<W::kF16Mma>(acc[n], a0, b[n].x, b[n].y);
-#pragma unroll
-            for (int n = 0; n < NT; ++n) mma16816<W::kF16Mma>(acc[n], a1, b[n].z, b[n].w);
-        }
-    }
-    copies_wait<0>();
-    __syncthreads();
-    // the two halves' sums
-    float* sum = reinterpret_cast<float*>(ring);   // [64][8 * NT]
-    constexpr int kRow = 8 * NT;
-    static_assert(kTileRows * kRow * 4 <= kStages * C::kStage, "sums");
-    if (h == 1)
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-                *reinterpret_cast<float2*>(sum + (16 * m + g + 8 * i) * kRow + 8 * n + 2 * c) = make_float2(acc[n][2 * i], acc[n][2 * i + 1]);
-    __syncthreads();
-    if (h == 1) return;
-    float* to = a.t + ((long long)blockIdx.y * a.plan.items + first) * a.rank + rank0;
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int row = 16 * m + g + 8 * i;
-            const float2 other = *reinterpret_cast<const float2*>(sum + row * kRow + 8 * n + 2 * c);
-            if (row < rows && rank0 + 8 * n < a.rank)
-                *reinterpret_cast<float2*>(to + (long long)row * a.rank + 8 * n + 2 * c) =
-                    make_float2(__fadd_rn(acc[n][2 * i], other.x), __fadd_rn(acc[n][2 * i + 1], other.y));
-        }
-}
 
 // Values from row to row of t's parts: 64 bytes more or less than a multiple of 128, so that
 // the eight lanes that read 16 bytes of two rows at once meet no bank twice.
 __host__ __device__ constexpr int pitch_of(int kk) { return 32 * (kk | 1); }
 
-// out of up to kOuterRows rows of one adapter, for a.col_blocks times kOuterCols
-// columns: a warp has 32 of each block's, with B in registers, and takes 16 rows at a
-// time. A thread's part of base comes through its own places in shared memory, kDepth - 1
-// steps ahead (as many bytes as keep DRAM busy, and no registers; with one step ahead in registers a
-// prompt of 8000 rows took 39 us, 5000 bf16 rows of 8960 columns 40). KK: chunks of 32 of the rank.
+// Four neighbouring values of row r of t, from place q on, as parts in tp[part][ROWS][pitch_of(KK)], and what the row's sums
+// are to be multiplied with. 8 * KK neighbouring lanes have a row.
+template <int DT, int KK, int ROWS>
+__device__ __forceinline__ void put_t(uint16_t* tp, float* s_mul, int r, int q, const float (&v)[4], float scale) {
+    using W = Kind<DT>;
+    float mul = scale;
+    uint32_t p[W::kTParts][2];
+    if constexpr (DT == kF16) {
+        float m = fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));
+#pragma unroll
+        for (int s = 1; s < 8 * KK; s <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, s));
+        // the largest value to 2^13 .. 2^14; infinities stay what they are
+        const int e = min(max((int)(__float_as_uint(m) >> 23) - 127, -100), 127);
+        const float by = __int_as_float((127 + 13 - e) << 23);
+        mul = __fmul_rn(mul, __int_as_float((127 - 13 + e) << 23));
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const float x = __fmul_rn(v[2 * i], by), y = __fmul_rn(v[2 * i + 1], by);
+            const __half2 h = __floats2half2_rn(x, y);
+            const float2 f = __half22float2(h);
+            const __half2 l = __floats2half2_rn(__fsub_rn(x, f.x), __fsub_rn(y, f.y));
+            p[0][i] = *reinterpret_cast<const uint32_t*>(&h);
+            p[1][i] = *reinterpret_cast<const uint32_t*>(&l);
+        }
+    } else if constexpr (DT == kBf16) {   // rounded, 18 bits
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+            const float2 f = __bfloat1622float2(h);
+            const __nv_bfloat162 l = __floats2bfloat162_rn(__fsub_rn(v[2 * i], f.x), __fsub_rn(v[2 * i + 1], f.y));
+            p[0][i] = *reinterpret_cast<const uint32_t*>(&h);
+            p[1][i] = *reinterpret_cast<const uint32_t*>(&l);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            uint32_t w[W::kTParts];
+            split2<W::kTParts>(v[2 * i], v[2 * i + 1], w);
+#pragma unroll
+            for (int j = 0; j < W::kTParts; ++j) p[j][i] = w[j];
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < W::kTParts; ++j)
+        *reinterpret_cast<uint2*>(tp + (j * ROWS + r) * pitch_of(KK) + q) = make_uint2(p[j][0], p[j][1]);
+    if (q == 0) s_mul[r] = mul;
+}
+
+// The outer product of a tile of up to ROWS rows of adapter o, for columns from n0 on (a warp's
+// 32 of each block of kOuterCols) to n_end. A warp has its 32 columns of B in registers, and takes 16 rows
+// at a time. A thread's part of base comes through its own places in shared memory, kDepth - 1
+// steps ahead: as many bytes as keep DRAM busy, and no registers. KK: chunks of 32 of the rank.
 constexpr int kRingBytes = 65536;
-template <int DT>
-__host__ __device__ constexpr int outer_vecs() { return 8 * (DT == kF32 ? 4 : 2) / 16; }   // 16-byte pieces of a thread's eight columns
-template <int DT>
-__host__ __device__ constexpr int outer_depth() { return kRingBytes / (2 * outer_vecs<DT>() * kThreads * 16); }
-template <int DT, int KK>
-__global__ void __launch_bounds__(kThreads, KK <= 2 ? 2 : 1) k_lora_outer(const __grid_constant__ LoraArgs a) {
+
+template <int DT, int KK, int ROWS>
+struct Outer {
     using W = Kind<DT>;
     using T = typename RowT<DT>::type;
-    constexpr int kPitch = pitch_of(KK);
-    extern __shared__ __align__(16) uint8_t smem_out[];
-    Places& P = *reinterpret_cast<Places*>(smem_out);
-    uint16_t* tp = reinterpret_cast<uint16_t*>(smem_out + sizeof(Places));   // [part][row][kPitch]
-    __shared__ float s_mul[kOuterRows];      // what a row's sums are multiplied with
-    __shared__ int s_item[kOuterRows];
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
-    // All but t is older than the inner product's launch, which began when what made it was complete: it is read before
-    // pdl_wait, while the inner product runs.
-    if (warp == 0) plan_tiles(a.plan, kOuterRows, P.begin, P.tile0, lane);
-    __syncthreads();
-    const int tiles = P.tile0[a.plan.owners];
-    if ((int)blockIdx.x >= tiles) return;
-    const int o = owner_of_tile(P.tile0, a.plan.owners, blockIdx.x);
-    const int first = P.begin[o] + ((int)blockIdx.x - P.tile0[o]) * kOuterRows;
-    const int rows = min(kOuterRows, P.begin[o + 1] - first);
-    int n0 = blockIdx.y * a.col_blocks * kOuterCols + warp * 32;
-    const int n_end = min(a.N, (int)(blockIdx.y + 1) * a.col_blocks * kOuterCols);
+    static constexpr int kVecs = 8 * (int)sizeof(T) / 16;                      // 16-byte pieces of a thread's eight columns
+    static constexpr int kDepth = kRingBytes / (2 * kVecs * kThreads * 16);    // steps
+    static constexpr int kPitch = pitch_of(KK);
+    static constexpr int kTBytes = W::kTParts * ROWS * kPitch * 2;
 
-    // B: column j of MMA tile i of the warp is n0 + 8 * (j / 2) + 2 * i + j % 2
+    const LoraArgs& a;
+    const int o, rows, n_end;
+    const int* s_item;   // ROWS items; negative: none
+    uint4* ring;
+    const int g, c;
+    int n0;
     uint4 b[4][KK];
-    auto load_b = [&] {
+    int ahead = 0, ahead_m = 0, ahead_n;   // the step to fetch next
+
+    // Where in a warp's 32 columns stand the 16-byte pieces i of thread c, each whole sectors with its neighbours'
+    // (F32: 16 columns of four threads and then 16 more; 16 bits: all 32 at once), and
+    // column j of MMA tile i, so that thread c's results of the tiles are those pieces in order.
+    static constexpr int kPer = 16 / (int)sizeof(T);   // columns of a piece
+    __device__ __forceinline__ static int piece_col(int i, int c) { return 4 * kPer * i + kPer * c; }
+    __device__ __forceinline__ static int tile_col(int i, int j) {
+        const int q = 2 * i + (j & 1);   // of the thread's eight
+        return piece_col(q / kPer, j >> 1) + q % kPer;
+    }
+
+    __device__ __forceinline__ Outer(const LoraArgs& a, int o, int rows, int n0, int n_end, const int* s_item, uint4* ring)
+        : a(a), o(o), rows(rows), n_end(n_end), s_item(s_item), ring(ring + threadIdx.x), g((threadIdx.x & 31) >> 2),
+          c(threadIdx.x & 3), n0(n0), ahead_n(n0) {}
+
+    __device__ __forceinline__ void load_b(int at) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int n = n0 + 8 * (g >> 1) + 2 * i + (g & 1);
+            const int n = at + tile_col(i, g);
             const uint16_t* from = static_cast<const uint16_t*>(a.B) + ((long long)o * a.N + n) * a.rank + 8 * c;
 #pragma unroll
             for (int k = 0; k < KK; ++k)
-                b[i][k] = n < a.N && 32 * k + 8 * c < a.rank ? __ldg(reinterpret_cast<const uint4*>(from + 32 * k)) : make_uint4(0u, 0u, 0u, 0u);
+                b[i][k] = n < a.N && 32 * k + 8 * c < a.rank ? __ldg(reinterpret_cast<const uint4*>(from + 32 * k))
+                                                             : make_uint4(0u, 0u, 0u, 0u);
         }
-    };
-    load_b();
-    if (tid < kOuterRows) {
-        const int item = tid < rows ? __ldcg(a.plan.list + first + tid) : -1;
-        s_item[tid] = item >= 0 && item < a.plan.items ? item : -1;
     }
-    __syncthreads();
-    // Steps of 16 rows, the rows of one block of columns after another. A step's base of rows
-    // m + g and m + g + 8, columns n .. n + 7, as they lie in memory.
-    constexpr int kVecs = outer_vecs<DT>(), kDepth = outer_depth<DT>();
-    uint4* ring = reinterpret_cast<uint4*>(smem_out + sizeof(Places) + W::kTParts * kOuterRows * kPitch * 2) + tid;
-    int ahead = 0, ahead_m = 0, ahead_n = n0 + 8 * c;   // the step to fetch next
-    auto fetch = [&] {
-        if (ahead_n - 8 * c < n_end && a.vec && ahead_n + 8 <= a.N) {
+    // A step's base: rows m + g and m + g + 8 of the tile, this thread's pieces of them.
+    __device__ __forceinline__ void fetch() {
+        if (ahead_n < n_end && a.vec && ahead_n + 32 <= a.N) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int item = s_item[ahead_m + g + 8 * h];
@@ -415,137 +349,286 @@ __global__ void __launch_bounds__(kThreads, KK <= 2 ? 2 : 1) k_lora_outer(const 
                 const T* from = static_cast<const T*>(a.base.data) + item * a.base.stride + ahead_n;
 #pragma unroll
                 for (int i = 0; i < kVecs; ++i)
-                    copy16(ring + ((ahead % kDepth * 2 + h) * kVecs + i) * kThreads, from + i * (16 / (int)sizeof(T)), true);
+                    copy16(ring + ((ahead % kDepth * 2 + h) * kVecs + i) * kThreads, from + piece_col(i, c), true);
             }
         }
         copies_commit();
         ++ahead;
         ahead_m += 16;
         if (ahead_m >= rows) ahead_m = 0, ahead_n += kOuterCols;
-    };
-#pragma unroll
-    for (int i = 0; i < kDepth - 1; ++i) fetch();
-    pdl_wait();
-    const float scale = a.scale != nullptr ? __ldg(a.scale + o) : 1.0f;
-    // t of the rows in parts, 8 lanes or more to a row
-    constexpr int kLanes = 8 * KK > 32 ? 32 : 8 * KK;   // of a row, 4 values each
-    static_assert(kLanes * 4 == 32 * KK, "a row's values");
-    for (int r = tid / kLanes; r < (rows + 15) / 16 * 16; r += kThreads / kLanes) {
-        const int q = 4 * (tid % kLanes);
-        float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        if (r < rows && q < a.rank) {
-            const float* from = a.t + (long long)(first + r) * a.rank + q;
-#pragma unroll 4
-            for (int s = 0; s < a.splits; ++s) {
-                const float4 w = __ldcg(reinterpret_cast<const float4*>(from + (long long)s * a.plan.items * a.rank));
-                v[0] = __fadd_rn(v[0], w.x);
-                v[1] = __fadd_rn(v[1], w.y);
-                v[2] = __fadd_rn(v[2], w.z);
-                v[3] = __fadd_rn(v[3], w.w);
-            }
-        }
-        float mul = scale;
-        uint32_t p[W::kTParts][2];
-        if constexpr (DT == kF16) {
-            float m = fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));
-#pragma unroll
-            for (int s = 1; s < kLanes; s <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, s));
-            // the largest value to 2^13 .. 2^14; infinities stay what they are
-            const int e = min(max((int)(__float_as_uint(m) >> 23) - 127, -100), 127);
-            const float by = __int_as_float((127 + 13 - e > 254 ? 254 : 127 + 13 - e) << 23);
-            mul = __fmul_rn(mul, __int_as_float((254 - (int)(__float_as_uint(by) >> 23)) << 23));
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const float x = __fmul_rn(v[2 * i], by), y = __fmul_rn(v[2 * i + 1], by);
-                const __half2 h = __floats2half2_rn(x, y);
-                const float2 f = __half22float2(h);
-                const __half2 l = __floats2half2_rn(__fsub_rn(x, f.x), __fsub_rn(y, f.y));
-                p[0][i] = *reinterpret_cast<const uint32_t*>(&h);
-                p[1][i] = *reinterpret_cast<const uint32_t*>(&l);
-            }
-        } else if constexpr (DT == kBf16) {   // rounded, 18 bits
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-                const float2 f = __bfloat1622float2(h);
-                const __nv_bfloat162 l = __floats2bfloat162_rn(__fsub_rn(v[2 * i], f.x), __fsub_rn(v[2 * i + 1], f.y));
-                p[0][i] = *reinterpret_cast<const uint32_t*>(&h);
-                p[1][i] = *reinterpret_cast<const uint32_t*>(&l);
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                uint32_t w[W::kTParts];
-                split2<W::kTParts>(v[2 * i], v[2 * i + 1], w);
-#pragma unroll
-                for (int j = 0; j < W::kTParts; ++j) p[j][i] = w[j];
-            }
-        }
-#pragma unroll
-        for (int j = 0; j < W::kTParts; ++j)
-            *reinterpret_cast<uint2*>(tp + (j * kOuterRows + r) * kPitch + q) = make_uint2(p[j][0], p[j][1]);
-        if (q == 0) {
-            s_mul[r] = mul;
-        }
     }
-    __syncthreads();
-    int step = 0;
-    while (n0 < n_end) {
-        const int n = n0 + 8 * c;
-        const bool vec = a.vec && n + 8 <= a.N;
-        for (int m = 0; m < rows; m += 16, ++step) {
-            fetch();
-            float acc[4][4] = {};
+    __device__ __forceinline__ void start() {
+        load_b(n0);
 #pragma unroll
-            for (int p = W::kTParts - 1; p >= 0; --p)
+        for (int i = 0; i < kDepth - 1; ++i) fetch();
+    }
+    __device__ __forceinline__ void run(const uint16_t* tp, const float* s_mul) {
+        int step = 0;
+        while (n0 < n_end) {
+            const bool vec = a.vec && n0 + 32 <= a.N;
+            for (int m = 0; m < rows; m += 16, ++step) {
+                fetch();
+                float acc[4][4] = {};
 #pragma unroll
-                for (int k = 0; k < KK; ++k) {
-                    const uint16_t* from = tp + (p * kOuterRows + m + g) * kPitch + 32 * k + 8 * c;
-                    const uint4 lo = *reinterpret_cast<const uint4*>(from), hi = *reinterpret_cast<const uint4*>(from + 8 * kPitch);
-                    const uint32_t a0[4] = {lo.x, hi.x, lo.y, hi.y}, a1[4] = {lo.z, hi.z, lo.w, hi.w};
+                for (int p = W::kTParts - 1; p >= 0; --p)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        mma16816<W::kF16Mma>(acc[i], a0, b[i][k].x, b[i][k].y);
-                        mma16816<W::kF16Mma>(acc[i], a1, b[i][k].z, b[i][k].w);
-                    }
-                }
-            if (m + 16 >= rows && n0 + kOuterCols < n_end) {   // B of the next block, while this one is finished
-                n0 += kOuterCols;
-                load_b();
-                n0 -= kOuterCols;
-            }
-            copies_wait<kDepth - 1>();
+                    for (int k = 0; k < KK; ++k) {
+                        const uint16_t* from = tp + (p * ROWS + m + g) * kPitch + 32 * k + 8 * c;
+                        const uint4 lo = *reinterpret_cast<const uint4*>(from), hi = *reinterpret_cast<const uint4*>(from + 8 * kPitch);
+                        const uint32_t a0[4] = {lo.x, hi.x, lo.y, hi.y}, a1[4] = {lo.z, hi.z, lo.w, hi.w};
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int item = s_item[m + g + 8 * h];
-                if (item < 0) continue;
-                const float mul = s_mul[m + g + 8 * h];
-                T* to = static_cast<T*>(a.out.data) + item * a.out.stride + n;
-                struct alignas(16) V { T v[16 / sizeof(T)]; };
-                constexpr int kPer = 16 / (int)sizeof(T);
-                if (vec) {
-#pragma unroll
-                    for (int i = 0; i < kVecs; ++i) {
-                        const V old = *reinterpret_cast<const V*>(ring + ((step % kDepth * 2 + h) * kVecs + i) * kThreads);
-                        V w;
-#pragma unroll
-                        for (int j = 0; j < kPer; ++j) {
-                            const int q = kPer * i + j;   // column of the thread's eight
-                            put_as(w.v, DT, j, fmaf(mul, acc[q >> 1][2 * h + (q & 1)], to_f32(old.v[j])));
+                        for (int i = 0; i < 4; ++i) {
+                            mma16816<W::kF16Mma>(acc[i], a0, b[i][k].x, b[i][k].y);
+                            mma16816<W::kF16Mma>(acc[i], a1, b[i][k].z, b[i][k].w);
                         }
-                        *reinterpret_cast<V*>(to + kPer * i) = w;
                     }
-                } else {
-                    const T* from = static_cast<const T*>(a.base.data) + item * a.base.stride + n;
+                // B of the next block, while this one is finished
+                if (m + 16 >= rows && n0 + kOuterCols < n_end) load_b(n0 + kOuterCols);
+                copies_wait<kDepth - 1>();
 #pragma unroll
-                    for (int q = 0; q < 8; ++q)
-                        if (n + q < a.N) put_as(to, DT, q, fmaf(mul, acc[q >> 1][2 * h + (q & 1)], to_f32(from[q])));
+                for (int h = 0; h < 2; ++h) {
+                    const int item = s_item[m + g + 8 * h];
+                    if (item < 0) continue;
+                    const float mul = s_mul[m + g + 8 * h];
+                    T* to = static_cast<T*>(a.out.data) + item * a.out.stride + n0;
+                    struct alignas(16) V { T v[kPer]; };
+                    if (vec) {
+#pragma unroll
+                        for (int i = 0; i < kVecs; ++i) {
+                            const V old = *reinterpret_cast<const V*>(ring + ((step % kDepth * 2 + h) * kVecs + i) * kThreads);
+                            float v[kPer];
+#pragma unroll
+                            for (int j = 0; j < kPer; ++j) {
+                                const int q = kPer * i + j;   // column of the thread's eight
+                                v[j] = fmaf(mul, acc[q >> 1][2 * h + (q & 1)], to_f32(old.v[j]));
+                            }
+                            store16(to + piece_col(i, c), v);
+                        }
+                    } else {
+                        const T* from = static_cast<const T*>(a.base.data) + item * a.base.stride + n0;
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) {
+                            const int n = piece_col(q / kPer, c) + q % kPer;
+                            if (n0 + n < a.N) put_as(to, DT, n, fmaf(mul, acc[q >> 1][2 * h + (q & 1)], to_f32(from[n])));
+                        }
+                    }
                 }
+            }
+            n0 += kOuterCols;
+        }
+        copies_wait<0>();
+    }
+};
+
+// An item of the list, negative where it is none.
+__device__ __forceinline__ int item_at(const PlanView& p, int place) {
+    const int item = __ldcg(p.list + place);
+    return item < p.items ? item : -1;
+}
+
+// The outer product behind k_lora_inner. The tiles' blocks of columns, all tiles' one after the
+// other, are shared out evenly; a CTA's are cut by tile.
+template <int DT, int KK>
+__global__ void __launch_bounds__(kThreads, KK <= 2 ? 2 : 1) k_lora_outer(const __grid_constant__ LoraArgs a) {
+    using O = Outer<DT, KK, kOuterRows>;
+    extern __shared__ __align__(16) uint8_t smem_out[];
+    Places& P = *reinterpret_cast<Places*>(smem_out);
+    uint16_t* tp = reinterpret_cast<uint16_t*>(smem_out + sizeof(Places));
+    uint4* ring = reinterpret_cast<uint4*>(smem_out + sizeof(Places) + O::kTBytes);
+    __shared__ float s_mul[kOuterRows];
+    __shared__ int s_item[kOuterRows];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    // All but t is older than the inner product's launch, which began when what made it was complete: it is read before
+    // pdl_wait, while the inner product runs.
+    if (warp == 0) plan_tiles(a.plan, kOuterRows, P.begin, P.tile0, lane);
+    __syncthreads();
+    const int blocks = (a.N + kOuterCols - 1) / kOuterCols;
+    // (rows times columns are below 2^40: the blocks of all tiles below 2^28)
+    const int every = P.tile0[a.plan.owners] * blocks;
+    const int each = every / (int)gridDim.x, more = every - each * (int)gridDim.x, me = (int)blockIdx.x;
+    const int hi_unit = (me + 1) * each + min(me + 1, more);
+    bool waited = false;
+    for (int unit = me * each + min(me, more); unit < hi_unit;) {
+        const int tile = unit / blocks, block = unit - tile * blocks;
+        const int some = min(blocks - block, hi_unit - unit);
+        unit += some;
+        const int o = owner_of_tile(P.tile0, a.plan.owners, tile);
+        const int first = P.begin[o] + (tile - P.tile0[o]) * kOuterRows;
+        const int rows = min(kOuterRows, P.begin[o + 1] - first);
+        if (tid < kOuterRows) s_item[tid] = tid < rows ? item_at(a.plan, first + tid) : -1;
+        __syncthreads();   // and the tile before is done with
+        O outer(a, o, rows, block * kOuterCols + warp * 32, min(a.N, (block + some) * kOuterCols), s_item, ring);
+        outer.start();
+        if (!waited) pdl_wait();
+        waited = true;
+        const float scale = a.scale != nullptr ? __ldg(a.scale + o) : 1.0f;
+        constexpr int kLanes = 8 * KK;   // of a row, 4 values each
+        for (int r = tid / kLanes; r < (rows + 15) / 16 * 16; r += kThreads / kLanes) {
+            const int q = 4 * (tid % kLanes);
+            float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            if (r < rows && q < a.rank) {
+                const float* from = a.t + (long long)(first + r) * a.rank + q;
+#pragma unroll 4
+                for (int s = 0; s < a.splits; ++s) {
+                    const float4 w = __ldcg(reinterpret_cast<const float4*>(from + (long long)s * a.plan.items * a.rank));
+                    v[0] = __fadd_rn(v[0], w.x);
+                    v[1] = __fadd_rn(v[1], w.y);
+                    v[2] = __fadd_rn(v[2], w.z);
+                    v[3] = __fadd_rn(v[3], w.w);
+                }
+            }
+            put_t<DT, KK, kOuterRows>(tp, s_mul, r, q, v, scale);
+        }
+        __syncthreads();
+        outer.run(tp, s_mul);
+        __syncthreads();
+    }
+}
+
+// Both products of a tile of kBothRows rows in one CTA, where there are tiles enough to fill the GPU: t stays in shared memory, and
+// the only launch. The inner product's x and A come through shared memory,
+// stages of 64 positions ahead; warp (m, h) takes 16 rows and a quarter of a stage's
+// positions, one MMA of the first kind above (four neighbours of 16 to a thread of a group of four).
+// A piece of 16 bytes lies at another place in the next rows, so that the lanes that read at
+// once meet no bank twice.
+constexpr int kBothRows = 32, kStageK = 64;
+
+template <int DT, int KK>
+struct Both {
+    static constexpr int kSize = DT == kF32 ? 4 : 2;
+    static constexpr int kRank = 32 * KK;
+    static constexpr int kXRow = kStageK * kSize, kARow = kStageK * 2;
+    static constexpr int kX = kBothRows * kXRow, kStage = kX + kRank * kARow;
+    static constexpr int kStages = kRingBytes / kStage < 4 ? 4 : kRingBytes / kStage;
+    static constexpr int kRing = kStages * kStage > kRingBytes ? kStages * kStage : kRingBytes;   // then of the base, and of the sums
+    static constexpr int kBytes = (int)sizeof(Places) + Outer<DT, KK, kBothRows>::kTBytes + kRing;
+};
+template <int ROW_BYTES>
+__device__ __forceinline__ int piece_at(int row, int j) {
+    if (ROW_BYTES == 256) return row * 256 + ((j ^ (row & 1) << 2) << 4);
+    return row * 128 + ((j ^ (row & 3) << 1) << 4);
+}
+
+template <int DT, int KK>
+__global__ void __launch_bounds__(kThreads, KK <= 2 ? 2 : 1) k_lora_both(const __grid_constant__ LoraArgs a) {
+    using W = Kind<DT>;
+    using T = typename RowT<DT>::type;
+    using C = Both<DT, KK>;
+    using O = Outer<DT, KK, kBothRows>;
+    constexpr int kPieces = C::kXRow / 16, NT = 4 * KK;
+    extern __shared__ __align__(16) uint8_t smem_both[];
+    Places& P = *reinterpret_cast<Places*>(smem_both);
+    uint16_t* tp = reinterpret_cast<uint16_t*>(smem_both + sizeof(Places));
+    uint8_t* ring = smem_both + sizeof(Places) + O::kTBytes;
+    __shared__ float s_mul[kBothRows];
+    __shared__ int s_item[kBothRows];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
+    const int m = warp & 1, h = warp >> 1;
+    pdl_wait();
+    if (warp == 0) plan_tiles(a.plan, kBothRows, P.begin, P.tile0, lane);
+    __syncthreads();
+    if ((int)blockIdx.x >= P.tile0[a.plan.owners]) return;
+    const int o = owner_of_tile(P.tile0, a.plan.owners, blockIdx.x);
+    const int first = P.begin[o] + ((int)blockIdx.x - P.tile0[o]) * kBothRows;
+    const int rows = min(kBothRows, P.begin[o + 1] - first);
+    const int steps = (a.K + kStageK - 1) / kStageK;
+    if (tid < kBothRows) s_item[tid] = tid < rows ? item_at(a.plan, first + tid) : -1;
+
+    // this thread's pieces of each stage: piece pj of rows pr, pr + kThreads / kPieces, ...
+    constexpr int kPer = kBothRows * kPieces / kThreads;
+    const int pr = tid / kPieces, pj = tid % kPieces;
+    const T* from[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        const int item = max(item_at(a.plan, first + min(pr + i * (kThreads / kPieces), rows - 1)), 0);
+        from[i] = static_cast<const T*>(a.x.data) + item * a.x.stride + pj * (16 / C::kSize);
+    }
+    const uint16_t* A = static_cast<const uint16_t*>(a.A) + (long long)o * a.rank * a.K;
+    auto load = [&](int step) {
+        if (step < steps) {
+            uint8_t* at = ring + step % C::kStages * C::kStage;
+            const int k = step * kStageK;
+            const bool in = k + pj * (16 / C::kSize) < a.K;
+#pragma unroll
+            for (int i = 0; i < kPer; ++i)
+                copy16(at + piece_at<C::kXRow>(pr + i * (kThreads / kPieces), pj), in ? from[i] + k : from[i], in);
+            at += C::kX;
+#pragma unroll
+            for (int i = 0; i < KK; ++i) {
+                const int r = (tid >> 3) + 32 * i, j = tid & 7;
+                const bool there = r < a.rank && k + 8 * j < a.K;
+                copy16(at + piece_at<C::kARow>(r, j), there ? A + (long long)r * a.K + k + 8 * j : A, there);
             }
         }
-        n0 += kOuterCols;
+        copies_commit();
+    };
+    float acc[NT][4] = {};
+#pragma unroll
+    for (int i = 0; i < C::kStages - 1; ++i) load(i);
+    for (int step = 0; step < steps; ++step) {
+        copies_wait<C::kStages - 2>();
+        __syncthreads();   // the stage is there for all, and the one before it is done with
+        load(step + C::kStages - 1);
+        if (16 * m >= rows) continue;
+        const uint8_t* at = ring + step % C::kStages * C::kStage;
+        uint32_t ap[2][W::kXParts][2];   // [row g or g + 8][part][pair]
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int row = 16 * m + g + 8 * i;
+            if constexpr (DT == kF32) {
+                const float4 w = *reinterpret_cast<const float4*>(at + piece_at<256>(row, 4 * h + c));
+                uint32_t p0[3], p1[3];
+                split2<3>(w.x, w.y, p0);
+                split2<3>(w.z, w.w, p1);
+#pragma unroll
+                for (int p = 0; p < 3; ++p) ap[i][p][0] = p0[p], ap[i][p][1] = p1[p];
+            } else {
+                const uint2 w = *reinterpret_cast<const uint2*>(at + piece_at<128>(row, 2 * h + (c >> 1)) + 8 * (c & 1));
+                ap[i][0][0] = w.x;
+                ap[i][0][1] = w.y;
+            }
+        }
+        uint2 b[NT];
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+            b[n] = *reinterpret_cast<const uint2*>(at + C::kX + piece_at<128>(8 * n + g, 2 * h + (c >> 1)) + 8 * (c & 1));
+#pragma unroll
+        for (int p = W::kXParts - 1; p >= 0; --p) {
+            const uint32_t x[4] = {ap[0][p][0], ap[1][p][0], ap[0][p][1], ap[1][p][1]};
+#pragma unroll
+            for (int n = 0; n < NT; ++n) mma16816<W::kF16Mma>(acc[n], x, b[n].x, b[n].y);
+        }
     }
     copies_wait<0>();
+    __syncthreads();
+    float* sum = reinterpret_cast<float*>(ring);   // [quarter][row][32 * KK]
+    static_assert(4 * kBothRows * C::kRank * 4 <= C::kRing, "sums");
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            *reinterpret_cast<float2*>(sum + (h * kBothRows + 16 * m + g + 8 * i) * C::kRank + 8 * n + 2 * c) =
+                make_float2(acc[n][2 * i], acc[n][2 * i + 1]);
+    __syncthreads();
+    const float scale = a.scale != nullptr ? __ldg(a.scale + o) : 1.0f;
+    constexpr int kLanes = 8 * KK;
+    for (int r = tid / kLanes; r < kBothRows; r += kThreads / kLanes) {
+        const int q = 4 * (tid % kLanes);
+        float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float4 w = *reinterpret_cast<const float4*>(sum + (i * kBothRows + r) * C::kRank + q);
+            v[0] = __fadd_rn(v[0], w.x);
+            v[1] = __fadd_rn(v[1], w.y);
+            v[2] = __fadd_rn(v[2], w.z);
+            v[3] = __fadd_rn(v[3], w.w);
+        }
+        put_t<DT, KK, kBothRows>(tp, s_mul, r, q, v, scale);
+    }
+    __syncthreads();   // the sums' place is then the base's
+    O outer(a, o, rows, warp * 32, a.N, s_item, reinterpret_cast<uint4*>(ring));
+    outer.start();
+    outer.run(tp, s_mul);
 }
 
 // ---------------------------------------------------------------------------
@@ -564,14 +647,13 @@ cudaError_t allow_smem(K kernel, int bytes, std::atomic<unsigned long long>& rea
 // Row tiles there may be: no more than one per adapter and one per `rows` items.
 int64_t most_tiles(const PlanView& p, int rows) { return std::min(p.items, p.owners) + p.items / rows; }
 
-// Adapters with many rows go through tiles of kTileRows in shared memory.
-bool many_rows(int64_t items, int owners) { return items >= 32 * (int64_t)owners; }
+// Both products in one CTA per 32 rows, where such tiles fill the GPU.
+bool both_in_one(int64_t items, int owners) { return items >= 32 * (int64_t)owners && items >= 200 * kBothRows; }
 
-// How K is split: as far as it takes to have two CTAs per SM, into multiples of the warps' 256 positions (few rows)
-// or of 256 at least (tiles).
+// How K is split: into multiples of the warps' 256 positions, as far as it takes
+// to have two CTAs per SM.
 int inner_splits(int64_t items, int owners, int K, int groups) {
-    const int rows = many_rows(items, owners) ? kTileRows : kInnerRows;
-    const int64_t likely = std::max<int64_t>(std::min<int64_t>(items, owners), (items + rows - 1) / rows) * groups;
+    const int64_t likely = std::max<int64_t>(std::min<int64_t>(items, owners), items / kInnerRows) * groups;
     const int64_t most = (K + kWarps * 32 - 1) / (kWarps * 32);
     return (int)std::max<int64_t>(1, std::min<int64_t>({2 * 152 / likely, most, (int64_t)kMaxSplits}));
 }
@@ -580,16 +662,8 @@ int rank_tiles(int rank) { return rank <= 8 ? 1 : rank <= 16 ? 2 : rank <= 32 ? 
 
 template <int DT, int NT>
 cudaError_t launch_inner(const LoraArgs& a, cudaStream_t s) {
-    if (many_rows(a.plan.items, a.plan.owners)) {
-        constexpr int bytes = TileShape<DT, NT>::kBytes;
-        static std::atomic<unsigned long long> ready{0};   // a bit per device
-        const cudaError_t e = allow_smem(k_lora_inner_tile<DT, NT>, bytes, ready);
-        if (e != cudaSuccess) return e;
-        const dim3 grid((unsigned)most_tiles(a.plan, kTileRows), (unsigned)a.splits, (unsigned)((a.rank + 8 * NT - 1) / (8 * NT)));
-        return launch_pdl(k_lora_inner_tile<DT, NT>, grid, dim3(kThreads), bytes, s, a);
-    }
     constexpr int bytes = (int)sizeof(Places) + kWarps * kInnerRows * 8 * NT * 4;
-    static std::atomic<unsigned long long> ready{0};
+    static std::atomic<unsigned long long> ready{0};   // a bit per device
     const cudaError_t e = allow_smem(k_lora_inner<DT, NT>, bytes, ready);
     if (e != cudaSuccess) return e;
     const dim3 grid((unsigned)most_tiles(a.plan, kInnerRows), (unsigned)a.splits, (unsigned)((a.rank + 8 * NT - 1) / (8 * NT)));
@@ -598,16 +672,32 @@ cudaError_t launch_inner(const LoraArgs& a, cudaStream_t s) {
 
 template <int DT, int KK>
 cudaError_t launch_outer(const LoraArgs& a, cudaStream_t s) {
-    constexpr int bytes = (int)sizeof(Places) + Kind<DT>::kTParts * kOuterRows * pitch_of(KK) * 2 + kRingBytes;
+    constexpr int bytes = (int)sizeof(Places) + Outer<DT, KK, kOuterRows>::kTBytes + kRingBytes;
     static std::atomic<unsigned long long> ready{0};
     const cudaError_t e = allow_smem(k_lora_outer<DT, KK>, bytes, ready);
     if (e != cudaSuccess) return e;
-    const dim3 grid((unsigned)most_tiles(a.plan, kOuterRows), (unsigned)((a.N + a.col_blocks * kOuterCols - 1) / (a.col_blocks * kOuterCols)));
+    const int64_t units = most_tiles(a.plan, kOuterRows) * ((a.N + kOuterCols - 1) / kOuterCols);
+    const dim3 grid((unsigned)std::min<int64_t>(units, (KK <= 2 ? 2 : 1) * device_sm_count()));
     return launch_pdl(k_lora_outer<DT, KK>, grid, dim3(kThreads), bytes, s, a);
+}
+
+template <int DT, int KK>
+cudaError_t launch_both(const LoraArgs& a, cudaStream_t s) {
+    constexpr int bytes = Both<DT, KK>::kBytes;
+    static_assert(bytes <= 232448, "shared memory");
+    static std::atomic<unsigned long long> ready{0};
+    const cudaError_t e = allow_smem(k_lora_both<DT, KK>, bytes, ready);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(k_lora_both<DT, KK>, dim3((unsigned)most_tiles(a.plan, kBothRows)), dim3(kThreads), bytes, s, a);
 }
 
 template <int DT>
 cudaError_t launch_lora(const LoraArgs& a, cudaStream_t s) {
+    if (both_in_one(a.plan.items, a.plan.owners)) {
+        if (a.rank <= 32) return launch_both<DT, 1>(a, s);
+        if (a.rank <= 64) return launch_both<DT, 2>(a, s);
+        return launch_both<DT, 4>(a, s);
+    }
     const int nt = rank_tiles(a.rank);
     cudaError_t e = nt == 1 ? launch_inner<DT, 1>(a, s) : nt == 2 ? launch_inner<DT, 2>(a, s)
                   : nt == 4 ? launch_inner<DT, 4>(a, s) : launch_inner<DT, 8>(a, s);
@@ -637,6 +727,7 @@ extern "C" {
 
 size_t lora_add_workspace(const lora_adapters* a, const route_plan* plan) {
     if (check_adapters(a, plan)) return 0;
+    if (both_in_one(plan->items, plan->owners)) return 256;   // t stays in shared memory
     const int splits = inner_splits(plan->items, plan->owners, (int)a->K, (a->rank + 63) / 64);
     return up_256((size_t)splits * plan->items * a->rank * 4);
 }
@@ -680,10 +771,6 @@ int lora_add(const lora_adapters* a, const route_plan* plan, const i2s_rows* x, 
     p.splits = inner_splits(rows, p.plan.owners, p.K, (a->rank + 63) / 64);
     p.k_per = ((p.K + p.splits - 1) / p.splits + kWarps * 32 - 1) / (kWarps * 32) * (kWarps * 32);
     p.splits = (p.K + p.k_per - 1) / p.k_per;   // none empty
-    // as many columns to a CTA as leave two CTAs per SM, all that run at once
-    const int64_t tiles = std::max<int64_t>(std::min<int64_t>(rows, p.plan.owners), (rows + kOuterRows - 1) / kOuterRows);
-    const int64_t blocks = (p.N + kOuterCols - 1) / kOuterCols;
-    p.col_blocks = (int)std::max<int64_t>(1, (tiles * blocks + 2 * 152 - 1) / (2 * 152));
     const int size = dtype_bytes(x->dtype);
     p.vec = !(((uintptr_t)base->data | (uintptr_t)out->data) & 15) &&
             (rows == 1 || (base->stride * size % 16 == 0 && out->stride * size % 16 == 0));

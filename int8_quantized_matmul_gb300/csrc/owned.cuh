@@ -62,17 +62,23 @@ __device__ __forceinline__ int plan_end(const PlanView& p) { return min(max(__ld
 __device__ __forceinline__ void plan_tiles(const PlanView& p, int rows, int* begin, int* tile0, int lane) {
     int most = 0;
     const int end = plan_end(p);
-    for (int i0 = 0; i0 <= p.owners; i0 += 32) {
-        const int i = i0 + lane;
-        int v = i <= p.owners ? __ldcg(p.start + i) : 0;
-        v = min(max(v, most), end);
+    for (int i0 = 0; i0 <= p.owners; i0 += 128) {   // four loads at once
+        int v[4];
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int u = __shfl_up_sync(0xffffffffu, v, o);
-            if (lane >= o) v = max(v, u);
+        for (int j = 0; j < 4; ++j) v[j] = i0 + 32 * j + lane <= p.owners ? __ldcg(p.start + i0 + 32 * j + lane) : 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int i = i0 + 32 * j + lane;
+            if (i0 + 32 * j > p.owners) break;
+            int u = min(max(v[j], most), end);
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int w = __shfl_up_sync(0xffffffffu, u, o);
+                if (lane >= o) u = max(u, w);
+            }
+            if (i <= p.owners) begin[i] = u;
+            most = __shfl_sync(0xffffffffu, u, 31);
         }
-        if (i <= p.owners) begin[i] = v;
-        most = __shfl_sync(0xffffffffu, v, 31);
     }
     __syncwarp();
     int before = 0;

@@ -340,7 +340,8 @@ class Lora:
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("adapters,rank,N,K,rows", [(1, 8, 1, 8, 1), (1, 16, 100, 72, 1), (5, 24, 257, 520, 7), (3, 64, 64, 2048, 40),
                                                     (40, 32, 300, 1000, 64), (2, 128, 511, 264, 131), (4, 40, 33, 4104, 600),
-                                                    (300, 8, 40, 64, 500), (1, 104, 1000, 16, 65)])
+                                                    (300, 8, 40, 64, 500), (1, 104, 1000, 16, 65), (3, 16, 264, 72, 6500), (2, 64, 500, 136, 7001),
+                                                    (1, 128, 33, 520, 6407), (90, 8, 64, 2056, 6450)])
 def test_lora(i2s, dtype, adapters, rank, N, K, rows):
     c = Lora(adapters, rank, N, K, rows, dtype, seed=rank + K)
     plan = i2s.route_plan(c.owner.cuda(), adapters)
