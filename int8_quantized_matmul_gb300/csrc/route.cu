@@ -27,7 +27,7 @@ namespace i2s {
 namespace {
 
 constexpr int kThreads = 1024, kWarps = kThreads / 32;
-constexpr int kBlocks = 64;
+constexpr int kBlocks = 128;   // (8000 rows of 128 experts: 64 18.5 us, 128 12.9, 256 21.7, beyond one CTA per SM)
 constexpr int kCounters = 8192;   // of the sort: one per (warp, owner), so fewer warps sort where owners are many
 
 struct TopkArgs {
@@ -122,7 +122,7 @@ __host__ __device__ __forceinline__ int sort_warps(int owners) {
 
 struct SortShared {
     int count[kCounters];
-    int base[kMaxOwners];
+    int all[kMaxOwners], before[kMaxOwners];   // an owner's items, and those of them in the blocks before
     int scan[kWarps];
 };
 
@@ -160,6 +160,7 @@ __device__ void sort_block(const int* owner, int lo, int hi, const PlanView& p, 
     const int per = ((hi - lo + warps - 1) / warps + 31) / 32 * 32;   // items of a warp, neighbours
     const int w_lo = min(hi, lo + warp * per), w_hi = min(hi, w_lo + per);
     for (int i = tid; i < warps * p.owners; i += kThreads) S.count[i] = 0;
+    if (tid < p.owners) S.all[tid] = S.before[tid] = 0;
     __syncthreads();
     int* mine = S.count + warp * p.owners;
     if (warp < warps)
@@ -171,16 +172,28 @@ __device__ void sort_block(const int* owner, int lo, int hi, const PlanView& p, 
     // where the block's items of each owner begin: after all of the owners before,
     // and this owner's in the blocks before
     int all = 0, before = 0;
-    if (tid < p.owners) {
-        if (counts == nullptr) {
+    if (counts == nullptr) {
+        if (tid < p.owners)
             for (int w = 0; w < warps; ++w) all += S.count[w * p.owners + tid];
-        } else {
-#pragma unroll 16
-            for (int b = 0; b < blocks; ++b) {
-                const int n = __ldcg(counts + b * p.owners + tid);
+    } else {
+        // the blocks' counts, as many blocks at a time as the threads allow
+        const int parts = max(1, kThreads / p.owners), part = tid / p.owners, o = tid - part * p.owners;
+        if (part < parts) {
+#pragma unroll 8
+            for (int b = part; b < blocks; b += parts) {
+                const int n = __ldcg(counts + b * p.owners + o);
                 all += n;
                 if (b < me) before += n;
             }
+            if (parts > 1) {
+                atomicAdd(S.all + o, all);
+                atomicAdd(S.before + o, before);
+            }
+        }
+        if (parts > 1) {
+            __syncthreads();
+            all = tid < p.owners ? S.all[tid] : 0;
+            before = tid < p.owners ? S.before[tid] : 0;
         }
     }
     const int first = block_before(all, S.scan);
@@ -228,6 +241,7 @@ template <int DT, int VPL>
 __global__ void __launch_bounds__(kThreads) k_route_topk(TopkArgs a, int per, int* counts) {
     __shared__ int n[kMaxOwners];
     pdl_wait();
+    pdl_launch_next();
     const int lo = blockIdx.x * per, hi = min(a.rows, lo + per);
     if (counts != nullptr) {
         for (int i = threadIdx.x; i < a.experts; i += kThreads) n[i] = 0;
@@ -247,6 +261,7 @@ __global__ void __launch_bounds__(kThreads) k_route_topk(TopkArgs a, int per, in
 __global__ void __launch_bounds__(kThreads) k_plan_count(const int* __restrict__ owner, int items, int owners, int per, int* counts) {
     __shared__ int n[kMaxOwners];
     pdl_wait();
+    pdl_launch_next();
     for (int i = threadIdx.x; i < owners; i += kThreads) n[i] = 0;
     __syncthreads();
     const int lo = min(items, blockIdx.x * per), hi = min(items, lo + per);

@@ -210,7 +210,7 @@ def test_experts_few_rows(i2s, dtype, E, N, K, rows, k):
 
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("E,N,K,rows,k", [(2, 160, 80, 50, 2), (3, 129, 1040, 300, 1), (7, 256, 208, 900, 4), (1, 32, 32, 257, 1),
-                                          (4, 320, 3104, 130, 2)])
+                                          (4, 320, 3104, 130, 2), (6, 64, 2080, 700, 6), (9, 32, 1024, 1000, 9)])
 def test_experts_many_rows(i2s, dtype, E, N, K, rows, k):
     check_experts(i2s, Experts(E, N, K, rows, k, seed=N + K, none=0.05), dtype)
 
