@@ -76,8 +76,10 @@ struct Shape {
     // Many: the rows do.
     static constexpr int kSlots = ROWS == 32 ? 6 : 4;      // operands: rows, and weights in TMEM
     static constexpr int kWSlots = ROWS == 32 ? 10 : 5;    // weights as bytes
-    static constexpr int kAtom = ROWS * 128;               // 64 positions of the rows
-    static constexpr int kRowStage = 2 * kAtom;
+    // Rows come in one copy per stage, as two atoms of 64 positions, of one to four times kBox rows.
+    static constexpr int kBox = ROWS / 4;
+    __device__ static int boxes(int rows) { return (rows + kBox - 1) / kBox; }
+    static constexpr int kRowStage = ROWS * 256;
     static constexpr uint32_t kOp0 = 2 * ROWS;             // first TMEM column of the operands
     static_assert(kOp0 + kSlots * kOpCols <= 512 && kSlots % 2 == 0, "TMEM, and each slot one converter group's");
     static_assert(kSlots <= kMaxSlots && kWSlots <= kMaxWSlots, "barriers");
@@ -155,14 +157,15 @@ __device__ __forceinline__ void load_pairs(void* dst, const CUtensorMap* map, in
         "l"(map), "r"(k), "r"(0), "r"(block), "r"(e), "r"(tc::smem_u32(bar))
         : "memory");
 }
-__device__ __forceinline__ void load_rows(uint32_t lead, uint32_t dst, const CUtensorMap* map, int k, int row, uint32_t bar) {
+// Rows from `row` on, positions 64 * block and the 64 * (halves - 1) after them, as one or two atoms.
+__device__ __forceinline__ void load_rows(uint32_t lead, uint32_t dst, const CUtensorMap* map, int row, int block, uint32_t bar) {
     asm volatile(
         "{\n"
         ".reg .pred q;\n"
-        "setp.ne.b32 q, %5, 0;\n"
-        "@q cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];\n"
+        "setp.ne.b32 q, %6, 0;\n"
+        "@q cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];\n"
         "}\n" ::"r"(dst),
-        "l"(map), "r"(k), "r"(row), "r"(bar), "r"(lead)
+        "l"(map), "r"(0), "r"(row), "r"(block), "r"(bar), "r"(lead)
         : "memory");
 }
 __device__ __forceinline__ void expect_bytes(uint32_t lead, uint32_t bar, uint32_t bytes) {
@@ -207,7 +210,7 @@ __device__ __forceinline__ void store_rows(T* y, long long stride, const int (&i
 }  // namespace xp
 
 struct ExpertArgs {
-    CUtensorMap wmap, xmap[3];   // rows in boxes of ROWS, ROWS / 2, ROWS / 4
+    CUtensorMap wmap, xmap[4];   // rows in boxes of one to four times Shape::kBox
     PlanView plan;
     const float* bscale;
     const float* ascale;    // workspace, one per place of the list, as the codes
@@ -542,26 +545,17 @@ __global__ void __launch_bounds__(xp::kThreads, 1) k_experts(const __grid_consta
                 const int rows = (int)__reduce_max_sync(0xffffffffu, (unsigned)t.rows);
                 const int first = (int)__reduce_max_sync(0xffffffffu, (unsigned)t.first);
                 if (rows == 0) break;
-                // one box of ROWS, ROWS / 2 or ROWS / 4 rows, or the two smaller ones
-                const int some = rows > 3 * ROWS / 4 ? 0 : rows > ROWS / 4 ? 1 : 2;
-                const bool two = some == 1 && rows > ROWS / 2;
-                const uint32_t loaded = (uint32_t)(ROWS >> some) + (two ? ROWS / 4 : 0);
+                const int box = S_::boxes(rows);
                 for (int k = 0; k < steps; ++k, ++at) {
                     const int slot = at % S_::kSlots;
                     const bool got = tc::mbar_wait_spin(&S.empty[slot], ((uint32_t)(at / S_::kSlots) & 1) ^ 1, abort_flag, kWait);
                     if (!got) fail();
                     ok = __all_sync(0xffffffffu, got) != 0;
                     if (!ok) break;
-                    // the second half of the stage is left out where the row ends in the first
-                    const bool both = k * kStep + 64 < a.K;
+                    // (a block past the row's last is zeros, and no MMA reads it)
                     const uint32_t bar = tc::smem_u32(&S.full[slot]), dst = tc::smem_u32(sRows + slot * S_::kRowStage);
-                    expect_bytes(lead, bar, loaded * (both ? 256 : 128));
-                    load_rows(lead, dst, &a.xmap[some], k * kStep, first, bar);
-                    if (both) load_rows(lead, dst + S_::kAtom, &a.xmap[some], k * kStep + 64, first, bar);
-                    if (two) {
-                        load_rows(lead, dst + ROWS / 2 * 128, &a.xmap[2], k * kStep, first + ROWS / 2, bar);
-                        if (both) load_rows(lead, dst + S_::kAtom + ROWS / 2 * 128, &a.xmap[2], k * kStep + 64, first + ROWS / 2, bar);
-                    }
+                    expect_bytes(lead, bar, (uint32_t)box * (S_::kBox * 256));
+                    load_rows(lead, dst, &a.xmap[box - 1], first, 2 * k, bar);
                 }
             }
             for (int i = max(0, at - S_::kSlots); i < at; ++i)
@@ -582,6 +576,7 @@ __global__ void __launch_bounds__(xp::kThreads, 1) k_experts(const __grid_consta
             for (int seq = 0; ok && !a.test_stall; ++seq) {
                 const int rows = (int)__reduce_max_sync(0xffffffffu, (unsigned)unit_told(seq).rows);
                 if (rows == 0) break;
+                const uint32_t atom = (uint32_t)S_::boxes(rows) * (S_::kBox * 128);   // bytes
                 const uint32_t idesc = tc::idesc_f16_f32(kChannels, (rows + 15) / 16 * 16);
                 for (int k0 = 0; ok && k0 < steps; k0 += kChunkSteps, ++chunk_at) {
                     const int buf = chunk_at & 1, k1 = min(steps, k0 + kChunkSteps);
@@ -599,10 +594,10 @@ __global__ void __launch_bounds__(xp::kThreads, 1) k_experts(const __grid_consta
                         if (left >= 8) {
 #pragma unroll
                             for (int j = 0; j < 8; ++j)
-                                mma(lead, d, op + 8u * j, bd + (uint64_t)((j >> 2) * (S_::kAtom >> 4) + 2 * (j & 3)), idesc);
+                                mma(lead, d, op + 8u * j, bd + (uint64_t)((j >> 2) * (atom >> 4) + 2 * (j & 3)), idesc);
                         } else {
                             for (int j = 0; j < left; ++j)
-                                mma(lead, d, op + 8u * j, bd + (uint64_t)((j >> 2) * (S_::kAtom >> 4) + 2 * (j & 3)), idesc);
+                                mma(lead, d, op + 8u * j, bd + (uint64_t)((j >> 2) * (atom >> 4) + 2 * (j & 3)), idesc);
                         }
                         commit(lead, &S.empty[slot]);
                     }
@@ -917,10 +912,12 @@ int w8a8_mul_mat_experts(const w8a8_experts* w, const route_plan* plan, const i2
     // Row tiles there may be: no more than one per expert and one per `rows` items.
     const bool few = items <= 16 * (int64_t)w->experts;
     const int rows = few ? 32 : 128;
-    const cuuint64_t xdims[2] = {K, (cuuint64_t)items}, xstrides[1] = {K * 2};
-    for (int i = 0; i < 3; ++i) {
-        const cuuint32_t xbox[2] = {64, (cuuint32_t)(rows >> i)};
-        mapped = mapped && encode_tensor_map(&a.xmap[i], CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, q, xdims, xstrides, xbox);
+    // (position of a block of 64, row, block): the last block may reach into the next row, or past the last into
+    // the workspace behind it; no MMA reads that
+    const cuuint64_t xdims[3] = {64, (cuuint64_t)items, (K + 63) / 64}, xstrides[2] = {K * 2, 128};
+    for (int i = 0; i < 4; ++i) {
+        const cuuint32_t xbox[3] = {64, (cuuint32_t)(rows / 4 * (i + 1)), 2};
+        mapped = mapped && encode_tensor_map(&a.xmap[i], CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, q, xdims, xstrides, xbox);
     }
     if (!mapped) return I2S_E_CUDA;
     a.plan = plan_view(*plan);
