@@ -315,6 +315,7 @@ __global__ void __launch_bounds__(xp::kThreads, 1) k_experts(const __grid_consta
         // ---------------------------------------------------------- epilogue
         regs_up<kRegsEpilogue>();
         pdl_wait();
+        pdl_launch_next();
         const int q = warp & 3;
         const bool upper = warp >= 4;                 // of the unit's columns (rows)
         const int mine = SWIGLU ? lane >> 4 : 0;      // SWIGLU: which of two neighbouring rows this lane finishes
@@ -750,32 +751,68 @@ __global__ void __launch_bounds__(kRowThreads) k_expert_rows(const __grid_consta
 }
 
 // y[t][n] = sum_j weight[t][j] * d[t * group + j][n], j ascending, each product
-// and sum rounded once; items without an expert add nothing.
+// and sum rounded once; items without an expert add nothing. V neighbouring values to a thread; eight items' loads at once.
+template <int V>
 __global__ void __launch_bounds__(256) k_expert_sum(const float* __restrict__ d, const float* __restrict__ weight,
-                                                    const uint8_t* __restrict__ used, int group, int N, long long rows, void* y,
-                                                    long long y_stride, int y_dtype) {
+                                                    const uint8_t* __restrict__ used, int group, int N, int rows, void* y,
+                                                    long long y_stride, int y_dtype, bool vec) {
+    const int per = N / V;
     pdl_wait();
-    const bool four = N % 4 == 0;   // the F32 rows are then read 16 bytes at a time
-    const int per = four ? N / 4 : N;
-    for (long long i = blockIdx.x * 256LL + threadIdx.x; i < rows * per; i += gridDim.x * 256LL) {
-        const long long t = i / per;
-        const int n = (int)(i - t * per) * (four ? 4 : 1);
-        float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        for (int j = 0; j < group; ++j) {
-            const long long item = t * group + j;
-            if (!used[item]) continue;
-            const float w = weight[item];
-            if (four) {
-                const float4 v = *reinterpret_cast<const float4*>(d + item * N + n);
-                s[0] = __fadd_rn(s[0], __fmul_rn(w, v.x));
-                s[1] = __fadd_rn(s[1], __fmul_rn(w, v.y));
-                s[2] = __fadd_rn(s[2], __fmul_rn(w, v.z));
-                s[3] = __fadd_rn(s[3], __fmul_rn(w, v.w));
-            } else {
-                s[0] = __fadd_rn(s[0], __fmul_rn(w, d[item * N + n]));
+    // a block's threads have neighbours of one row, or of a few
+    for (long long i = blockIdx.x * 256LL + threadIdx.x; i < (long long)rows * per; i += gridDim.x * 256LL) {
+        const int t = (int)(i / per);
+        const int n = (int)(i - (long long)t * per) * V;
+        float s[V] = {};
+        for (int j0 = 0; j0 < group; j0 += 8) {
+            float w[8], v[8][V];
+            bool in[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const long long item = (long long)t * group + j0 + j;
+                in[j] = j0 + j < group && used[item] != 0;
+                w[j] = j0 + j < group ? weight[item] : 0.0f;
             }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float* from = d + ((long long)t * group + j0 + j) * N + n;
+                if constexpr (V == 4) {
+                    const float4 x = in[j] ? *reinterpret_cast<const float4*>(from) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    v[j][0] = x.x;
+                    v[j][1] = x.y;
+                    v[j][2] = x.z;
+                    v[j][3] = x.w;
+                } else {
+                    v[j][0] = in[j] ? *from : 0.0f;
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+#pragma unroll
+                for (int q = 0; q < V; ++q)
+                    if (in[j]) s[q] = __fadd_rn(s[q], __fmul_rn(w[j], v[j][q]));
         }
-        for (int j = 0; j < (four ? 4 : 1); ++j) put_as(y, y_dtype, t * y_stride + n + j, s[j]);
+        const long long at = t * y_stride + n;
+        if (V == 4 && vec) {   // rows of y that allow accesses of four values
+            if (y_dtype == kF32) *reinterpret_cast<float4*>(static_cast<float*>(y) + at) = make_float4(s[0], s[V > 1 ? 1 : 0], s[V > 2 ? 2 : 0], s[V > 3 ? 3 : 0]);
+            else {
+                uint32_t h[2];
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    const float lo = s[V == 4 ? 2 * q : 0], hi = s[V == 4 ? 2 * q + 1 : 0];
+                    if (y_dtype == kF16) {
+                        const __half2 x = __floats2half2_rn(lo, hi);
+                        h[q] = *reinterpret_cast<const uint32_t*>(&x);
+                    } else {
+                        const __nv_bfloat162 x = __floats2bfloat162_rn(lo, hi);
+                        h[q] = *reinterpret_cast<const uint32_t*>(&x);
+                    }
+                }
+                *reinterpret_cast<uint2*>(static_cast<uint16_t*>(y) + at) = make_uint2(h[0], h[1]);
+            }
+        } else {
+#pragma unroll
+            for (int q = 0; q < V; ++q) put_as(y, y_dtype, at + q, s[q]);
+        }
     }
 }
 
@@ -947,10 +984,13 @@ int w8a8_mul_mat_experts(const w8a8_experts* w, const route_plan* plan, const i2
     else e = swiglu ? launch_product<128, true>(a, grid, stream) : launch_product<128, false>(a, grid, stream);
     if (e != cudaSuccess) return I2S_E_CUDA;
     if (weight) {
-        const int64_t blocks = (y_rows * ((w->N % 4 == 0 ? w->N / 4 : w->N)) + 255) / 256;
-        e = launch_pdl(k_expert_sum, dim3((unsigned)std::min<int64_t>(blocks, 152 * 64)), dim3(256), 0, stream,
-                       static_cast<const float*>(d), weight, static_cast<const uint8_t*>(used), y_group, a.N, (long long)y_rows,
-                       y->data, (long long)y->stride, y->dtype);
+        const bool four = w->N % 4 == 0;   // the F32 rows are then read 16 bytes at a time
+        const int size = dtype_bytes(y->dtype);
+        const bool vec = (uintptr_t)y->data % (4 * size) == 0 && (y_rows == 1 || y->stride % 4 == 0);
+        const int64_t blocks = (y_rows * (four ? w->N / 4 : w->N) + 255) / 256;
+        e = launch_pdl(four ? k_expert_sum<4> : k_expert_sum<1>, dim3((unsigned)std::min<int64_t>(blocks, 152 * 64)), dim3(256), 0,
+                       stream, static_cast<const float*>(d), weight, static_cast<const uint8_t*>(used), y_group, a.N, (int)y_rows,
+                       y->data, (long long)y->stride, y->dtype, vec);
         if (e != cudaSuccess) return I2S_E_CUDA;
     }
     return I2S_OK;
