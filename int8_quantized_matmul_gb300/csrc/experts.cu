@@ -75,13 +75,15 @@ struct Shape {
     // Few rows per expert: the weights' bytes count, and get the shared memory.
     // Many: the rows do.
     static constexpr int kSlots = ROWS == 32 ? 6 : 4;      // operands: rows, and weights in TMEM
-    static constexpr int kWSlots = ROWS == 32 ? 10 : 5;    // weights as bytes
+    static constexpr int kWSlots = ROWS == 32 ? 10 : 4;    // weights as bytes
     // Rows come in one copy per stage, as two atoms of 64 positions, of one to four times kBox rows.
     static constexpr int kBox = ROWS / 4;
     __device__ static int boxes(int rows) { return (rows + kBox - 1) / kBox; }
     static constexpr int kRowStage = ROWS * 256;
     static constexpr uint32_t kOp0 = 2 * ROWS;             // first TMEM column of the operands
-    static_assert(kOp0 + kSlots * kOpCols <= 512 && kSlots % 2 == 0, "TMEM, and each slot one converter group's");
+    // Each slot is always one converter group's and one issuer's: a parity wait passes for a phase two ahead, so one that
+    // has run ahead must not wait for a slot whose use before is the other's and has not come yet.
+    static_assert(kOp0 + kSlots * kOpCols <= 512 && kSlots % 2 == 0 && kWSlots % 2 == 0, "TMEM; slots");
     static_assert(kSlots <= kMaxSlots && kWSlots <= kMaxWSlots, "barriers");
 };
 

@@ -215,6 +215,25 @@ def test_experts_many_rows(i2s, dtype, E, N, K, rows, k):
     check_experts(i2s, Experts(E, N, K, rows, k, seed=N + K, none=0.05), dtype)
 
 
+@pytest.mark.parametrize("rows", [150, 500])
+def test_experts_weights_come_late(i2s, rows):
+    """Few rows for each of many weights, over many stages: the rings wait for weights that arrive in no order, and
+    two groups of warps take their stages by turns."""
+    c = Experts(24, 576, 4832, 1, 1, seed=rows)
+    rng = np.random.default_rng(rows)
+    c.rows, c.x, c.owner = rows, rng.normal(0, 1, (rows, 4832)).astype(np.float32), rng.integers(0, 24, rows).astype(np.int32)
+    w, b, plan = c.device(i2s)
+    calls = [i2s.W8A8Experts(w, b, plan, dev(c.x)) for _ in range(2)]
+    want = torch.from_numpy(ref.dots(c.wq, c.bscale, c.owner, c.x, 1)).cuda()
+    scratch = torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
+    for i in range(20):
+        scratch.fill_(i)   # the weights leave the cache
+        calls[i % 2].out.fill_(0)
+        calls[i % 2]()
+        assert torch.equal(calls[i % 2].out, want)
+    calls[0].check()
+
+
 def test_experts_ragged(i2s):
     """One expert has nearly all, some have one item, some none; more tiles than CTAs."""
     check_experts(i2s, Experts(40, 640, 272, 700, 2, seed=5, skew=[1000, 0, 0, 1, 30] + [0, 1, 2, 0, 5] * 7))
