@@ -881,7 +881,8 @@ cudaError_t launch_rows(const ExpertRowArgs& a, cudaStream_t s) {
 
 template <int DT>
 cudaError_t launch_quantize(const ExpertRowArgs& a, int* place, cudaStream_t s) {
-    // rows that several items read, and many of them
+    // Rows that several items read, and many of them (64 experts, 8 per row of 2048: a million values 37.8 us, by places
+    // 43.3; 8 million 61.0 and 61.5; 32 million 127.7 and 119.2, the products among them).
     if (a.x_group == 1 || (long long)a.plan.items * a.K < (1 << 23)) return launch_rows<DT, false>(a, s);
     const cudaError_t e = launch_pdl(k_expert_places, dim3((unsigned)std::min(152, (a.plan.items + 255) / 256)), dim3(256), 0, s,
                                      a.plan, place);
@@ -949,6 +950,8 @@ int w8a8_mul_mat_experts(const w8a8_experts* w, const route_plan* plan, const i2
         mapped = encode_tensor_map(&a.wmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, w->wq, dims, strides, box);
     }
     // Row tiles there may be: no more than one per expert and one per `rows` items.
+    // Few rows per expert take the shape for few (64 experts of 1536 x 2048, 8 items to an expert: 37.5 us, 42.7 in the other;
+    // 16: 43.7 and 45.8; 24: 48.7 and 47.9; 64: 83.2 and 61.5).
     const bool few = items <= 16 * (int64_t)w->experts;
     const int rows = few ? 32 : 128;
     // (position of a block of 64, row, block): the last block may reach into the next row, or past the last into

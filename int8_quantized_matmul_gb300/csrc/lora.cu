@@ -485,152 +485,6 @@ __global__ void __launch_bounds__(kThreads, KK <= 2 ? 2 : 1) k_lora_outer(const 
     }
 }
 
-// Both products of a tile of kBothRows rows in one CTA, where there are tiles enough to fill the GPU: t stays in shared memory, and
-// the only launch. The inner product's x and A come through shared memory,
-// stages of 64 positions ahead; warp (m, h) takes 16 rows and a quarter of a stage's
-// positions, one MMA of the first kind above (four neighbours of 16 to a thread of a group of four).
-// A piece of 16 bytes lies at another place in the next rows, so that the lanes that read at
-// once meet no bank twice.
-constexpr int kBothRows = 32, kStageK = 64;
-
-template <int DT, int KK>
-struct Both {
-    static constexpr int kSize = DT == kF32 ? 4 : 2;
-    static constexpr int kRank = 32 * KK;
-    static constexpr int kXRow = kStageK * kSize, kARow = kStageK * 2;
-    static constexpr int kX = kBothRows * kXRow, kStage = kX + kRank * kARow;
-    static constexpr int kStages = kRingBytes / kStage < 4 ? 4 : kRingBytes / kStage;
-    static constexpr int kRing = kStages * kStage > kRingBytes ? kStages * kStage : kRingBytes;   // then of the base, and of the sums
-    static constexpr int kBytes = (int)sizeof(Places) + Outer<DT, KK, kBothRows>::kTBytes + kRing;
-};
-template <int ROW_BYTES>
-__device__ __forceinline__ int piece_at(int row, int j) {
-    if (ROW_BYTES == 256) return row * 256 + ((j ^ (row & 1) << 2) << 4);
-    return row * 128 + ((j ^ (row & 3) << 1) << 4);
-}
-
-template <int DT, int KK>
-__global__ void __launch_bounds__(kThreads, KK <= 2 ? 2 : 1) k_lora_both(const __grid_constant__ LoraArgs a) {
-    using W = Kind<DT>;
-    using T = typename RowT<DT>::type;
-    using C = Both<DT, KK>;
-    using O = Outer<DT, KK, kBothRows>;
-    constexpr int kPieces = C::kXRow / 16, NT = 4 * KK;
-    extern __shared__ __align__(16) uint8_t smem_both[];
-    Places& P = *reinterpret_cast<Places*>(smem_both);
-    uint16_t* tp = reinterpret_cast<uint16_t*>(smem_both + sizeof(Places));
-    uint8_t* ring = smem_both + sizeof(Places) + O::kTBytes;
-    __shared__ float s_mul[kBothRows];
-    __shared__ int s_item[kBothRows];
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
-    const int m = warp & 1, h = warp >> 1;
-    pdl_wait();
-    if (warp == 0) plan_tiles(a.plan, kBothRows, P.begin, P.tile0, lane);
-    __syncthreads();
-    if ((int)blockIdx.x >= P.tile0[a.plan.owners]) return;
-    const int o = owner_of_tile(P.tile0, a.plan.owners, blockIdx.x);
-    const int first = P.begin[o] + ((int)blockIdx.x - P.tile0[o]) * kBothRows;
-    const int rows = min(kBothRows, P.begin[o + 1] - first);
-    const int steps = (a.K + kStageK - 1) / kStageK;
-    if (tid < kBothRows) s_item[tid] = tid < rows ? item_at(a.plan, first + tid) : -1;
-
-    // this thread's pieces of each stage: piece pj of rows pr, pr + kThreads / kPieces, ...
-    constexpr int kPer = kBothRows * kPieces / kThreads;
-    const int pr = tid / kPieces, pj = tid % kPieces;
-    const T* from[kPer];
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        const int item = max(item_at(a.plan, first + min(pr + i * (kThreads / kPieces), rows - 1)), 0);
-        from[i] = static_cast<const T*>(a.x.data) + item * a.x.stride + pj * (16 / C::kSize);
-    }
-    const uint16_t* A = static_cast<const uint16_t*>(a.A) + (long long)o * a.rank * a.K;
-    auto load = [&](int step) {
-        if (step < steps) {
-            uint8_t* at = ring + step % C::kStages * C::kStage;
-            const int k = step * kStageK;
-            const bool in = k + pj * (16 / C::kSize) < a.K;
-#pragma unroll
-            for (int i = 0; i < kPer; ++i)
-                copy16(at + piece_at<C::kXRow>(pr + i * (kThreads / kPieces), pj), in ? from[i] + k : from[i], in);
-            at += C::kX;
-#pragma unroll
-            for (int i = 0; i < KK; ++i) {
-                const int r = (tid >> 3) + 32 * i, j = tid & 7;
-                const bool there = r < a.rank && k + 8 * j < a.K;
-                copy16(at + piece_at<C::kARow>(r, j), there ? A + (long long)r * a.K + k + 8 * j : A, there);
-            }
-        }
-        copies_commit();
-    };
-    float acc[NT][4] = {};
-#pragma unroll
-    for (int i = 0; i < C::kStages - 1; ++i) load(i);
-    for (int step = 0; step < steps; ++step) {
-        copies_wait<C::kStages - 2>();
-        __syncthreads();   // the stage is there for all, and the one before it is done with
-        load(step + C::kStages - 1);
-        if (16 * m >= rows) continue;
-        const uint8_t* at = ring + step % C::kStages * C::kStage;
-        uint32_t ap[2][W::kXParts][2];   // [row g or g + 8][part][pair]
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int row = 16 * m + g + 8 * i;
-            if constexpr (DT == kF32) {
-                const float4 w = *reinterpret_cast<const float4*>(at + piece_at<256>(row, 4 * h + c));
-                uint32_t p0[3], p1[3];
-                split2<3>(w.x, w.y, p0);
-                split2<3>(w.z, w.w, p1);
-#pragma unroll
-                for (int p = 0; p < 3; ++p) ap[i][p][0] = p0[p], ap[i][p][1] = p1[p];
-            } else {
-                const uint2 w = *reinterpret_cast<const uint2*>(at + piece_at<128>(row, 2 * h + (c >> 1)) + 8 * (c & 1));
-                ap[i][0][0] = w.x;
-                ap[i][0][1] = w.y;
-            }
-        }
-        uint2 b[NT];
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-            b[n] = *reinterpret_cast<const uint2*>(at + C::kX + piece_at<128>(8 * n + g, 2 * h + (c >> 1)) + 8 * (c & 1));
-#pragma unroll
-        for (int p = W::kXParts - 1; p >= 0; --p) {
-            const uint32_t x[4] = {ap[0][p][0], ap[1][p][0], ap[0][p][1], ap[1][p][1]};
-#pragma unroll
-            for (int n = 0; n < NT; ++n) mma16816<W::kF16Mma>(acc[n], x, b[n].x, b[n].y);
-        }
-    }
-    copies_wait<0>();
-    __syncthreads();
-    float* sum = reinterpret_cast<float*>(ring);   // [quarter][row][32 * KK]
-    static_assert(4 * kBothRows * C::kRank * 4 <= C::kRing, "sums");
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-            *reinterpret_cast<float2*>(sum + (h * kBothRows + 16 * m + g + 8 * i) * C::kRank + 8 * n + 2 * c) =
-                make_float2(acc[n][2 * i], acc[n][2 * i + 1]);
-    __syncthreads();
-    const float scale = a.scale != nullptr ? __ldg(a.scale + o) : 1.0f;
-    constexpr int kLanes = 8 * KK;
-    for (int r = tid / kLanes; r < kBothRows; r += kThreads / kLanes) {
-        const int q = 4 * (tid % kLanes);
-        float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float4 w = *reinterpret_cast<const float4*>(sum + (i * kBothRows + r) * C::kRank + q);
-            v[0] = __fadd_rn(v[0], w.x);
-            v[1] = __fadd_rn(v[1], w.y);
-            v[2] = __fadd_rn(v[2], w.z);
-            v[3] = __fadd_rn(v[3], w.w);
-        }
-        put_t<DT, KK, kBothRows>(tp, s_mul, r, q, v, scale);
-    }
-    __syncthreads();   // the sums' place is then the base's
-    O outer(a, o, rows, warp * 32, a.N, s_item, reinterpret_cast<uint4*>(ring));
-    outer.start();
-    outer.run(tp, s_mul);
-}
-
 // ---------------------------------------------------------------------------
 // Host side
 // ---------------------------------------------------------------------------
@@ -646,9 +500,6 @@ cudaError_t allow_smem(K kernel, int bytes, std::atomic<unsigned long long>& rea
 
 // Row tiles there may be: no more than one per adapter and one per `rows` items.
 int64_t most_tiles(const PlanView& p, int rows) { return std::min(p.items, p.owners) + p.items / rows; }
-
-// Both products in one CTA per 32 rows, where such tiles fill the GPU.
-bool both_in_one(int64_t items, int owners) { return items >= 32 * (int64_t)owners && items >= 200 * kBothRows; }
 
 // How K is split: into multiples of the warps' 256 positions, as far as it takes
 // to have two CTAs per SM.
@@ -681,23 +532,8 @@ cudaError_t launch_outer(const LoraArgs& a, cudaStream_t s) {
     return launch_pdl(k_lora_outer<DT, KK>, grid, dim3(kThreads), bytes, s, a);
 }
 
-template <int DT, int KK>
-cudaError_t launch_both(const LoraArgs& a, cudaStream_t s) {
-    constexpr int bytes = Both<DT, KK>::kBytes;
-    static_assert(bytes <= 232448, "shared memory");
-    static std::atomic<unsigned long long> ready{0};
-    const cudaError_t e = allow_smem(k_lora_both<DT, KK>, bytes, ready);
-    if (e != cudaSuccess) return e;
-    return launch_pdl(k_lora_both<DT, KK>, dim3((unsigned)most_tiles(a.plan, kBothRows)), dim3(kThreads), bytes, s, a);
-}
-
 template <int DT>
 cudaError_t launch_lora(const LoraArgs& a, cudaStream_t s) {
-    if (both_in_one(a.plan.items, a.plan.owners)) {
-        if (a.rank <= 32) return launch_both<DT, 1>(a, s);
-        if (a.rank <= 64) return launch_both<DT, 2>(a, s);
-        return launch_both<DT, 4>(a, s);
-    }
     const int nt = rank_tiles(a.rank);
     cudaError_t e = nt == 1 ? launch_inner<DT, 1>(a, s) : nt == 2 ? launch_inner<DT, 2>(a, s)
                   : nt == 4 ? launch_inner<DT, 4>(a, s) : launch_inner<DT, 8>(a, s);
@@ -727,7 +563,6 @@ extern "C" {
 
 size_t lora_add_workspace(const lora_adapters* a, const route_plan* plan) {
     if (check_adapters(a, plan)) return 0;
-    if (both_in_one(plan->items, plan->owners)) return 256;   // t stays in shared memory
     const int splits = inner_splits(plan->items, plan->owners, (int)a->K, (a->rank + 63) / 64);
     return up_256((size_t)splits * plan->items * a->rank * 4);
 }
