@@ -773,7 +773,8 @@ int kv8_read_status(int32_t* status, int32_t* bits, i2s_stream_t stream);
  * of I2S_F32, I2S_F16 or I2S_BF16 (the values of KV8_F32 and so on). Where a call
  * says "vector rows", data and the stride are multiples of 16 bytes; else of one
  * element. Strides are not negative, a tensor reaches over at most 2^40 elements, and an
- * output's rows do not reach into each other.
+ * output's rows do not reach into each other. Overlaps are looked for from a tensor's first element to its last, gaps
+ * included.
  *
  * Errors of every call: BAD_SHAPE, NULL_PTR, MISALIGNED, BAD_ARG (an unknown
  * dtype or flag, or an output that overlaps another operand),

@@ -124,7 +124,7 @@ static_assert(sizeof(Places) % 16 == 0, "alignment of what follows");
 
 // t of up to kInnerRows rows of one adapter, over one split of K, for up to
 // 8 * NT of its rank (adapters of one rank are many tiles of few rows, so 32 rows at a time: A is then
-// read from L2 as often as x from DRAM at rank 64 in F32). The warps take chunks of 32 positions by turns, and their
+// read from L2 as often as x from DRAM at rank 64 in F32; 16 rows at a time with two CTAs per SM gave 71 us for 63). The warps take chunks of 32 positions by turns, and their
 // sums are added in shared memory, warp by warp.
 template <int DT, int NT>
 __global__ void __launch_bounds__(kThreads) k_lora_inner(const __grid_constant__ LoraArgs a) {
@@ -341,7 +341,7 @@ struct Outer {
             const uint16_t* from = static_cast<const uint16_t*>(a.B) + ((long long)o * a.N + n) * a.rank + 8 * c;
 #pragma unroll
             for (int k = 0; k < KK; ++k)
-                b[i][k] = n < a.N && 32 * k + 8 * c < a.rank ? __ldg(reinterpret_cast<const uint4*>(from + 32 * k))
+                b[i][k] = n < a.N && 32 * k + 8 * c < a.rank ? __ldcg(reinterpret_cast<const uint4*>(from + 32 * k))
                                                              : make_uint4(0u, 0u, 0u, 0u);
         }
     }
@@ -508,7 +508,8 @@ cudaError_t allow_smem(K kernel, int bytes, std::atomic<unsigned long long>& rea
 int64_t most_tiles(const PlanView& p, int rows) { return std::min(p.items, p.owners) + p.items / rows; }
 
 // How K is split: into multiples of the warps' 256 positions, as far as it takes
-// to have two CTAs per SM.
+// to have two CTAs per SM (64 rows of 40 adapters: unsplit 13.8 us, in four 10.4, in eight 14.5; 8000 rows: unsplit 63.7, in
+// two 73.9: a CTA's own start and end cost as much as 512 positions).
 int inner_splits(int64_t items, int owners, int K, int groups) {
     const int64_t likely = std::max<int64_t>(std::min<int64_t>(items, owners), items / kInnerRows) * groups;
     const int64_t most = (K + kWarps * 32 - 1) / (kWarps * 32);

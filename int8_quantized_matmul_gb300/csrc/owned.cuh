@@ -46,11 +46,6 @@ __device__ __forceinline__ void put_as(void* data, int dt, long long at, float v
     else if (dt == kF16) static_cast<__half*>(data)[at] = __float2half_rn(v);
     else static_cast<__nv_bfloat16*>(data)[at] = __float2bfloat16_rn(v);
 }
-__device__ __forceinline__ float get_as(const void* data, int dt, long long at) {
-    if (dt == kF32) return static_cast<const float*>(data)[at];
-    if (dt == kF16) return __half2float(static_cast<const __half*>(data)[at]);
-    return __bfloat162float(static_cast<const __nv_bfloat16*>(data)[at]);
-}
 
 // The places of the list that are in use.
 __device__ __forceinline__ int plan_end(const PlanView& p) { return min(max(__ldcg(p.start + p.owners), 0), p.items); }

@@ -283,9 +283,9 @@ __global__ void __launch_bounds__(kThreads) k_plan_sort(const int* owner, PlanVi
     sort_block(owner, lo, hi, p, start, list, counts, gridDim.x, blockIdx.x, S);
 }
 
-// Items that one CTA sorts by itself, and rows whose choices it makes too (8 of 128 experts: 32 rows 6.4 us, in two launches
+// Items that one CTA sorts by itself (2048 of 128 owners 5.3 us, in two launches 6.2; 4096 7.2 and 6.3), and rows whose choices it makes too (8 of 128 experts: 32 rows 6.4 us, in two launches
 // 8.1; 64 rows 9.0 and 8.0; 128 rows 14.4 and 8.4).
-constexpr int kOneItems = 4096, kOneRows = 48;
+constexpr int kOneItems = 2048, kOneRows = 48;
 
 template <int DT, int VPL>
 cudaError_t launch_topk(const TopkArgs& a, const PlanView& p, int* start, int* list, int* counts, cudaStream_t s) {
