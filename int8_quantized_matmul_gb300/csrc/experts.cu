@@ -630,15 +630,15 @@ __global__ void __launch_bounds__(xp::kThreads, 1) k_experts(const __grid_consta
 // The rows of x as f16 codes and a scale, in the plan's order: amax floored at 1e-9, scale = amax/127,
 // q = clamp(round(x * (127/amax)), -127, 127), halves away from zero (as every
 // W8A8 call). A row with an infinity or NaN gets the scale NaN and codes of zero: its
-// outputs are NaN, and no others. TPR threads per row, four values at a time,
-// kept in registers up to kKeep * 4 of them per thread, beyond that read again. Bound by memory: 3554 F32 rows of 8960
+// outputs are NaN, and no others. TPR threads per row, eight values at a time,
+// kept in registers up to kKeep * 8 of them per thread, beyond that read again. Bound by memory: 3554 F32 rows of 8960
 // (191 MB in and out) 32 us.
 //
 // COPIES false: a row for each place of the list. true, where several items read a row and there are many: each
 // row of x is quantized once and written to the places of its items, which k_expert_places has put
 // down (4096 bf16 rows of 2048, eight items each: 25 us instead of 62; the launch before it takes 3).
 // ---------------------------------------------------------------------------
-constexpr int kRowThreads = 256, kKeep = 8;
+constexpr int kRowThreads = 256, kKeep = 4;
 
 __global__ void __launch_bounds__(256) k_expert_places(PlanView plan, int* place) {
     pdl_wait();
@@ -664,7 +664,7 @@ struct ExpertRowArgs {
 template <int DT, int TPR, bool COPIES>
 __global__ void __launch_bounds__(kRowThreads) k_expert_rows(const __grid_constant__ ExpertRowArgs a) {
     using T = typename RowT<DT>::type;
-    struct alignas(sizeof(T) * 4) V4 { T v[4]; };
+    struct alignas(16) V8 { T v[8]; };
     constexpr int kRowsPer = kRowThreads / TPR;
     __shared__ float s_max[kRowThreads / 32];
     pdl_wait();
@@ -685,14 +685,14 @@ __global__ void __launch_bounds__(kRowThreads) k_expert_rows(const __grid_consta
         here = item >= 0 && item < a.plan.items;
         row = item / a.x_group;
     }
-    const V4* from = reinterpret_cast<const V4*>(static_cast<const T*>(a.x.data) + (here ? row * a.x.stride : 0));
-    const int n4 = here ? a.K / 4 : 0;
-    V4 keep[kKeep];
+    const V8* from = reinterpret_cast<const V8*>(static_cast<const T*>(a.x.data) + (here ? row * a.x.stride : 0));
+    const int n8 = here ? a.K / 8 : 0;
+    V8 keep[kKeep];
     float mx = 0.0f;
     bool finite = true;
-    auto look = [&](const V4& w) {
+    auto look = [&](const V8& w) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < 8; ++j) {
             const float v = fabsf(to_f32(w.v[j]));
             mx = fmaxf(mx, v);
             finite = finite && v <= 3.402823466e38f;   // false for an infinity and for NaN
@@ -700,11 +700,11 @@ __global__ void __launch_bounds__(kRowThreads) k_expert_rows(const __grid_consta
     };
 #pragma unroll
     for (int i = 0; i < kKeep; ++i)
-        if (part + i * TPR < n4) keep[i] = from[part + i * TPR];
+        if (part + i * TPR < n8) keep[i] = from[part + i * TPR];
 #pragma unroll
     for (int i = 0; i < kKeep; ++i)
-        if (part + i * TPR < n4) look(keep[i]);
-    for (int i = part + kKeep * TPR; i < n4; i += TPR) look(from[i]);
+        if (part + i * TPR < n8) look(keep[i]);
+    for (int i = part + kKeep * TPR; i < n8; i += TPR) look(from[i]);
     if (!finite) mx = INFINITY;
     mx = warp_max(mx);
     if (TPR > 32) {
@@ -720,21 +720,21 @@ __global__ void __launch_bounds__(kRowThreads) k_expert_rows(const __grid_consta
     mx = fmaxf(mx, 1e-9f);
     const float inv = finite ? __fdiv_rn(127.0f, mx) : 0.0f;
     const float scale = finite ? __fdiv_rn(mx, 127.0f) : __int_as_float(0x7fc00000);
-    auto codes = [&](const V4& w) {
-        uint32_t c[2];
+    auto codes = [&](const V8& w) {
+        uint32_t c[4];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
+        for (int j = 0; j < 4; ++j) {
             // (with the scale NaN every code is that of zero, whatever NaN times zero clamps to)
             const float v0 = finite ? to_f32(w.v[2 * j]) : 0.0f, v1 = finite ? to_f32(w.v[2 * j + 1]) : 0.0f;
             const __half2 h = __floats2half2_rn(small_int_to_float(quantize_one(v0, inv)), small_int_to_float(quantize_one(v1, inv)));
             c[j] = *reinterpret_cast<const uint32_t*>(&h);
         }
-        return make_uint2(c[0], c[1]);
+        return make_uint4(c[0], c[1], c[2], c[3]);
     };
     // the places that get this row, eight at a time
     for (int j0 = 0; j0 < (COPIES ? a.x_group : 1); j0 += 8) {
         constexpr int kAt = COPIES ? 8 : 1;
-        uint2* to[kAt];
+        uint4* to[kAt];
 #pragma unroll
         for (int j = 0; j < kAt; ++j) {
             int p = index;
@@ -744,19 +744,19 @@ __global__ void __launch_bounds__(kRowThreads) k_expert_rows(const __grid_consta
                 // an item without a place left what was there before: its place is another's, or none
                 if (p < 0 || p >= end || __ldcg(a.plan.list + p) != (int)item) p = -1;
             }
-            to[j] = p >= 0 ? reinterpret_cast<uint2*>(a.q + (long long)p * a.K) : nullptr;
+            to[j] = p >= 0 ? reinterpret_cast<uint4*>(a.q + (long long)p * a.K) : nullptr;
             if (p >= 0 && part == 0) a.ascale[p] = scale;
         }
-        auto put = [&](int i, const V4& w) {
-            const uint2 c = codes(w);
+        auto put = [&](int i, const V8& w) {
+            const uint4 c = codes(w);
 #pragma unroll
             for (int j = 0; j < kAt; ++j)
                 if (to[j] != nullptr) to[j][i] = c;
         };
 #pragma unroll
         for (int i = 0; i < kKeep; ++i)
-            if (part + i * TPR < n4) put(part + i * TPR, keep[i]);
-        for (int i = part + kKeep * TPR; i < n4; i += TPR) put(i, from[i]);
+            if (part + i * TPR < n8) put(part + i * TPR, keep[i]);
+        for (int i = part + kKeep * TPR; i < n8; i += TPR) put(i, from[i]);
     }
 }
 
@@ -882,8 +882,8 @@ cudaError_t launch_rows(const ExpertRowArgs& a, cudaStream_t s) {
         return launch_pdl(kernel, dim3((unsigned)((rows + per - 1) / per)), dim3(kRowThreads), 0, s, a);
     };
     // the fewest threads that hold a row
-    if (a.K <= 32 * 4 * kKeep) return go(k_expert_rows<DT, 32, COPIES>, kRowThreads / 32);
-    if (a.K <= 64 * 4 * kKeep) return go(k_expert_rows<DT, 64, COPIES>, kRowThreads / 64);
+    if (a.K <= 32 * 8 * kKeep) return go(k_expert_rows<DT, 32, COPIES>, kRowThreads / 32);
+    if (a.K <= 64 * 8 * kKeep) return go(k_expert_rows<DT, 64, COPIES>, kRowThreads / 64);
     return go(k_expert_rows<DT, kRowThreads, COPIES>, 1);
 }
 
