@@ -3,8 +3,8 @@
 //
 // Mathematics. Rows sorted by adapter a (the plan): t = A_a x over K, then
 // out = base + scale_a * (B_a t) over the rank. Two launches, since every value of t
-// needs all of K: k_lora_inner writes partial sums of t (K split between CTAs where rows are
-// few), k_lora_outer adds them in order and finishes.
+// needs all of K: k_lora_inner writes t, where rows are few in parts (K split between CTAs, which with many ranks are a
+// cluster and add theirs up), k_lora_outer adds parts in order and finishes.
 //
 // Precision. 16-bit operands go to the tensor cores as they are. F32 rows of x,
 // and then t, are cut into three parts of 8 bits that bf16 holds (high bits first, each cut
@@ -30,6 +30,7 @@
 #include "common.cuh"
 #include "internal.h"
 #include "owned.cuh"
+#include "tc.cuh"
 
 namespace i2s {
 
@@ -38,15 +39,16 @@ namespace {
 constexpr int kThreads = 256, kWarps = 8;
 constexpr int kInnerRows = 32;    // rows of a CTA of the inner product
 constexpr int kOuterRows = 64, kOuterCols = 256;
-constexpr int kMaxRank = 128, kMaxSplits = 16;
+constexpr int kMaxRank = 128, kMaxSplits = 8;   // a cluster has up to 8 CTAs
 
 struct LoraArgs {
     PlanView plan;
     const void *A, *B;
     const float* scale;
     RowsView x, base, out;
-    float* t;          // workspace: [split][place in the list][rank]
+    float* t;          // workspace: [part][place in the list][rank]
     int K, N, rank, splits, k_per;   // positions of K of a split
+    int parts;         // of t: splits, or 1 if they are joined
     bool vec;          // base and out allow 16-byte accesses
 };
 
@@ -203,15 +205,30 @@ __global__ void __launch_bounds__(kThreads) k_lora_inner(const __grid_constant__
             *reinterpret_cast<float2*>(at + 8 * kRow) = make_float2(acc[m][n][2], acc[m][n][3]);
         }
     __syncthreads();
-    float* to = a.t + ((long long)blockIdx.y * a.plan.items + first) * a.rank + rank0;
+    const bool joined = a.parts < a.splits;
+    float* to = a.t + ((joined ? 0LL : (long long)blockIdx.y) * a.plan.items + first) * a.rank + rank0;
+    float* part = sum + kWarps * kInnerRows * kRow;   // this CTA's sums, where the cluster has more
     for (int i = tid; i < rows * kRow; i += kThreads) {
         const int row = i / kRow, n = i - row * kRow;
-        if (rank0 + n >= a.rank) continue;
         float s = 0.0f;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) s = __fadd_rn(s, sum[(w * kInnerRows + row) * kRow + n]);
-        to[(long long)row * a.rank + n] = s;
+        if (joined) part[i] = s;
+        else if (rank0 + n < a.rank) to[(long long)row * a.rank + n] = s;
     }
+    if (!joined) return;
+    tc::cluster_sync();
+    for (int i = tid + kThreads * (int)blockIdx.y; i < rows * kRow; i += kThreads * a.splits) {
+        float s = 0.0f;
+        for (int c = 0; c < a.splits; ++c) {
+            float v;
+            asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(tc::smem_in_rank(part + i, (uint32_t)c)) : "memory");
+            s = __fadd_rn(s, v);
+        }
+        const int row = i / kRow, n = i - row * kRow;
+        if (rank0 + n < a.rank) to[(long long)row * a.rank + n] = s;
+    }
+    tc::cluster_sync();   // the others have read this CTA's sums
 }
 
 __device__ __forceinline__ void copy16(void* dst, const void* src, bool in) {   // zeros where `in` is false
@@ -475,7 +492,7 @@ __global__ void __launch_bounds__(kThreads, KK <= 2 ? 2 : 1) k_lora_outer(const 
             if (r < rows && q < a.rank) {
                 const float* from = a.t + (long long)(first + r) * a.rank + q;
 #pragma unroll 4
-                for (int s = 0; s < a.splits; ++s) {
+                for (int s = 0; s < a.parts; ++s) {
                     const float4 w = __ldcg(reinterpret_cast<const float4*>(from + (long long)s * a.plan.items * a.rank));
                     v[0] = __fadd_rn(v[0], w.x);
                     v[1] = __fadd_rn(v[1], w.y);
@@ -507,25 +524,43 @@ cudaError_t allow_smem(K kernel, int bytes, std::atomic<unsigned long long>& rea
 // Row tiles there may be: no more than one per adapter and one per `rows` items.
 int64_t most_tiles(const PlanView& p, int rows) { return std::min(p.items, p.owners) + p.items / rows; }
 
-// How K is split: into multiples of the warps' 256 positions, as far as it takes
-// to have two CTAs per SM (64 rows of 40 adapters: unsplit 13.8 us, in four 10.4, in eight 14.5; 8000 rows: unsplit 63.7, in
-// two 73.9: a CTA's own start and end cost as much as 512 positions).
-int inner_splits(int64_t items, int owners, int K, int groups) {
-    const int64_t likely = std::max<int64_t>(std::min<int64_t>(items, owners), items / kInnerRows) * groups;
+// How K is split: into multiples of the warps' 256 positions, as far as it takes to fill the GPU, with one CTA per SM
+// (many ranks: 250 registers) or two (64 rows of 40 adapters, rank 32: unsplit 13.8 us, in four 10.4, in eight 14.5; 8000
+// rows: unsplit 63.7, in two 73.9: a CTA's own start and end cost as much as 512 positions).
+int inner_splits(int64_t items, int owners, int K, int rank) {
+    const int64_t likely = std::max<int64_t>(std::min<int64_t>(items, owners), (items + kInnerRows - 1) / kInnerRows) * ((rank + 63) / 64);
     const int64_t most = (K + kWarps * 32 - 1) / (kWarps * 32);
-    return (int)std::max<int64_t>(1, std::min<int64_t>({2 * 152 / likely, most, (int64_t)kMaxSplits}));
+    return (int)std::max<int64_t>(1, std::min<int64_t>({(rank > 32 ? 152 : 2 * 152) / likely, most, (int64_t)kMaxSplits}));
 }
+// Whether the splits of a tile are a cluster, whose CTAs add their sums up among themselves, or each leaves its part of t to
+// the outer product, every CTA of which adds them. Few ranks: the cluster's barriers cost more (rank 16, one row:
+// 5.8 us, parts 5.2; rank 32, 64 rows of 40: 10.8 and 10.0). Many: the parts do (rank 128, 500 rows, 1536 x 8960:
+// 32.9 us and 47.0).
+bool joined_in_cluster(int rank) { return rank > 32; }
 
 int rank_tiles(int rank) { return rank <= 8 ? 1 : rank <= 16 ? 2 : rank <= 32 ? 4 : 8; }   // of 8, of a CTA
 
 template <int DT, int NT>
 cudaError_t launch_inner(const LoraArgs& a, cudaStream_t s) {
-    constexpr int bytes = (int)sizeof(Places) + kWarps * kInnerRows * 8 * NT * 4;
+    constexpr int bytes = (int)sizeof(Places) + (kWarps + 1) * kInnerRows * 8 * NT * 4;
     static std::atomic<unsigned long long> ready{0};   // a bit per device
     const cudaError_t e = allow_smem(k_lora_inner<DT, NT>, bytes, ready);
     if (e != cudaSuccess) return e;
     const dim3 grid((unsigned)most_tiles(a.plan, kInnerRows), (unsigned)a.splits, (unsigned)((a.rank + 8 * NT - 1) / (8 * NT)));
-    return launch_pdl(k_lora_inner<DT, NT>, grid, dim3(kThreads), bytes, s, a);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = bytes;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = attr[1].val.clusterDim.z = 1;
+    attr[1].val.clusterDim.y = (unsigned)a.splits;
+    cfg.attrs = attr;
+    cfg.numAttrs = a.parts < a.splits ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, k_lora_inner<DT, NT>, a);
 }
 
 template <int DT, int KK>
@@ -570,8 +605,8 @@ extern "C" {
 
 size_t lora_add_workspace(const lora_adapters* a, const route_plan* plan) {
     if (check_adapters(a, plan)) return 0;
-    const int splits = inner_splits(plan->items, plan->owners, (int)a->K, (a->rank + 63) / 64);
-    return up_256((size_t)splits * plan->items * a->rank * 4);
+    const int splits = inner_splits(plan->items, plan->owners, (int)a->K, a->rank);
+    return up_256((size_t)(joined_in_cluster(a->rank) ? 1 : splits) * plan->items * a->rank * 4);
 }
 
 int lora_add(const lora_adapters* a, const route_plan* plan, const i2s_rows* x, const i2s_rows* base, const i2s_rows* out,
@@ -610,9 +645,10 @@ int lora_add(const lora_adapters* a, const route_plan* plan, const i2s_rows* x, 
     p.K = (int)a->K;
     p.N = (int)a->N;
     p.rank = a->rank;
-    p.splits = inner_splits(rows, p.plan.owners, p.K, (a->rank + 63) / 64);
+    p.splits = inner_splits(rows, p.plan.owners, p.K, a->rank);
     p.k_per = ((p.K + p.splits - 1) / p.splits + kWarps * 32 - 1) / (kWarps * 32) * (kWarps * 32);
     p.splits = (p.K + p.k_per - 1) / p.k_per;   // none empty
+    p.parts = joined_in_cluster(a->rank) ? 1 : p.splits;
     const int size = dtype_bytes(x->dtype);
     p.vec = !(((uintptr_t)base->data | (uintptr_t)out->data) & 15) &&
             (rows == 1 || (base->stride * size % 16 == 0 && out->stride * size % 16 == 0));
