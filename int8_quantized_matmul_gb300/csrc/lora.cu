@@ -128,7 +128,9 @@ static_assert(sizeof(Places) % 16 == 0, "alignment of what follows");
 // 8 * NT of its rank (adapters of one rank are many tiles of few rows, so 32 rows at a time: A is then
 // read from L2 as often as x from DRAM at rank 64 in F32; 16 rows at a time with two CTAs per SM gave 71 us for 63). The warps take chunks of 32 positions by turns, and their
 // sums are added in shared memory, warp by warp.
-template <int DT, int NT>
+// JOIN: the splits of a tile are a cluster, which adds its CTAs' sums up (without it, in a kernel of its own: with both in one,
+// 8000 rows that need no join took 68.8 us for 63.4).
+template <int DT, int NT, bool JOIN>
 __global__ void __launch_bounds__(kThreads) k_lora_inner(const __grid_constant__ LoraArgs a) {
     using W = Kind<DT>;
     constexpr int kMt = kInnerRows / 16, kWords = DT == kF32 ? 2 : 1;
@@ -205,18 +207,17 @@ __global__ void __launch_bounds__(kThreads) k_lora_inner(const __grid_constant__
             *reinterpret_cast<float2*>(at + 8 * kRow) = make_float2(acc[m][n][2], acc[m][n][3]);
         }
     __syncthreads();
-    const bool joined = a.parts < a.splits;
-    float* to = a.t + ((joined ? 0LL : (long long)blockIdx.y) * a.plan.items + first) * a.rank + rank0;
+    float* to = a.t + ((JOIN ? 0LL : (long long)blockIdx.y) * a.plan.items + first) * a.rank + rank0;
     float* part = sum + kWarps * kInnerRows * kRow;   // this CTA's sums, where the cluster has more
     for (int i = tid; i < rows * kRow; i += kThreads) {
         const int row = i / kRow, n = i - row * kRow;
         float s = 0.0f;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) s = __fadd_rn(s, sum[(w * kInnerRows + row) * kRow + n]);
-        if (joined) part[i] = s;
+        if (JOIN) part[i] = s;
         else if (rank0 + n < a.rank) to[(long long)row * a.rank + n] = s;
     }
-    if (!joined) return;
+    if (!JOIN) return;
     tc::cluster_sync();
     for (int i = tid + kThreads * (int)blockIdx.y; i < rows * kRow; i += kThreads * a.splits) {
         float s = 0.0f;
@@ -536,15 +537,15 @@ int inner_splits(int64_t items, int owners, int K, int rank) {
 // the outer product, every CTA of which adds them. Few ranks: the cluster's barriers cost more (rank 16, one row:
 // 5.8 us, parts 5.2; rank 32, 64 rows of 40: 10.8 and 10.0). Many: the parts do (rank 128, 500 rows, 1536 x 8960:
 // 32.9 us and 47.0).
-bool joined_in_cluster(int rank) { return rank > 32; }
+bool joined_in_cluster(int rank) { return rank > 32; }   // (then the ranks of a CTA are 64: k_lora_inner<DT, 8, .>)
 
 int rank_tiles(int rank) { return rank <= 8 ? 1 : rank <= 16 ? 2 : rank <= 32 ? 4 : 8; }   // of 8, of a CTA
 
-template <int DT, int NT>
+template <int DT, int NT, bool JOIN = false>
 cudaError_t launch_inner(const LoraArgs& a, cudaStream_t s) {
-    constexpr int bytes = (int)sizeof(Places) + (kWarps + 1) * kInnerRows * 8 * NT * 4;
+    constexpr int bytes = (int)sizeof(Places) + (kWarps + (JOIN ? 1 : 0)) * kInnerRows * 8 * NT * 4;
     static std::atomic<unsigned long long> ready{0};   // a bit per device
-    const cudaError_t e = allow_smem(k_lora_inner<DT, NT>, bytes, ready);
+    const cudaError_t e = allow_smem(k_lora_inner<DT, NT, JOIN>, bytes, ready);
     if (e != cudaSuccess) return e;
     const dim3 grid((unsigned)most_tiles(a.plan, kInnerRows), (unsigned)a.splits, (unsigned)((a.rank + 8 * NT - 1) / (8 * NT)));
     cudaLaunchConfig_t cfg = {};
@@ -559,8 +560,8 @@ cudaError_t launch_inner(const LoraArgs& a, cudaStream_t s) {
     attr[1].val.clusterDim.x = attr[1].val.clusterDim.z = 1;
     attr[1].val.clusterDim.y = (unsigned)a.splits;
     cfg.attrs = attr;
-    cfg.numAttrs = a.parts < a.splits ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, k_lora_inner<DT, NT>, a);
+    cfg.numAttrs = JOIN ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, k_lora_inner<DT, NT, JOIN>, a);
 }
 
 template <int DT, int KK>
@@ -578,7 +579,8 @@ template <int DT>
 cudaError_t launch_lora(const LoraArgs& a, cudaStream_t s) {
     const int nt = rank_tiles(a.rank);
     cudaError_t e = nt == 1 ? launch_inner<DT, 1>(a, s) : nt == 2 ? launch_inner<DT, 2>(a, s)
-                  : nt == 4 ? launch_inner<DT, 4>(a, s) : launch_inner<DT, 8>(a, s);
+                  : nt == 4 ? launch_inner<DT, 4>(a, s)
+                  : a.parts < a.splits ? launch_inner<DT, 8, true>(a, s) : launch_inner<DT, 8>(a, s);
     if (e != cudaSuccess) return e;
     if (a.rank <= 32) return launch_outer<DT, 1>(a, s);
     if (a.rank <= 64) return launch_outer<DT, 2>(a, s);
