@@ -32,8 +32,8 @@
 // gate and its up value are then 16 lanes apart in the same warp, and every lane
 // finishes one of two neighbouring rows after one exchange.
 //
-// Measured (one GB300). Few rows per expert: 64 tokens over 8 of 128 experts, 1536 x 2048, 52-55 us, 6.5 TB/s of the weights
-// in use. Many: 4096 bf16 rows of the same 229 us (rows 36, products 187); 1777 F32 rows over 2 of 8, 1536 x 8960: 124 us (rows 32,
+// Measured (one GB300). Few rows per expert: 64 tokens over 8 of 128 experts, 1536 x 2048, 51-55 us, 289 MB of weights
+// in use. Many: 4096 bf16 rows of the same 224-229 us (rows 36, products 187); 1777 F32 rows over 2 of 8, 1536 x 8960: 123 us (rows 32,
 // products 84, sums 8), tensor pipe 51 % (66 % on the SMs with most units: 2.5 for each). A stage of 112 rows takes 800 to
 // 900 cycles for 450 of MMAs: shared memory moves about 740 cycles' worth (16 KB of weights in and out, 28 KB of rows in and
 // to the MMA), and without any one of rows, weights, TMEM stores, MMAs or stores of y it takes 94 % or more of the time. CTA
