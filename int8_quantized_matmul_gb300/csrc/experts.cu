@@ -33,7 +33,7 @@
 // finishes one of two neighbouring rows after one exchange.
 //
 // Measured (one GB300). Few rows per expert: 64 tokens over 8 of 128 experts, 1536 x 2048, 51-55 us, 289 MB of weights
-// in use. Many: 4096 bf16 rows of the same 224-229 us (rows 36, products 187); 1777 F32 rows over 2 of 8, 1536 x 8960: 123 us (rows 32,
+// in use. Many: 4096 bf16 rows of the same 220 us (rows 36, products 187); 1777 F32 rows over 2 of 8, 1536 x 8960: 123 us (rows 32,
 // products 84, sums 8), tensor pipe 51 % (66 % on the SMs with most units: 2.5 for each). A stage of 112 rows takes 800 to
 // 900 cycles for 450 of MMAs: shared memory moves about 740 cycles' worth (16 KB of weights in and out, 28 KB of rows in and
 // to the MMA), and without any one of rows, weights, TMEM stores, MMAs or stores of y it takes 94 % or more of the time. CTA
@@ -151,19 +151,26 @@ __device__ __forceinline__ void commit(uint32_t lead, uint64_t* bar) {
         "}\n" ::"r"(tc::smem_u32(bar)), "r"(lead)
         : "memory");
 }
-__device__ __forceinline__ void load_weights(void* dst, const CUtensorMap* map, int k, int n, int e, uint64_t* bar) {
+__device__ __forceinline__ void load_weights(uint32_t lead, uint32_t dst, const CUtensorMap* map, int k, int n, int e, uint32_t bar) {
     asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
-            tc::smem_u32(dst)),
-        "l"(map), "r"(k), "r"(n), "r"(e), "r"(tc::smem_u32(bar))
+        "{\n"
+        ".reg .pred q;\n"
+        "setp.ne.b32 q, %6, 0;\n"
+        "@q cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];\n"
+        "}\n" ::"r"(dst),
+        "l"(map), "r"(k), "r"(n), "r"(e), "r"(bar), "r"(lead)
         : "memory");
 }
 // 16 channels x (gate, up) x four blocks of 16.
-__device__ __forceinline__ void load_pairs(void* dst, const CUtensorMap* map, int k, int block, int e, uint64_t* bar) {
+__device__ __forceinline__ void load_pairs(uint32_t lead, uint32_t dst, const CUtensorMap* map, int k, int block, int e, uint32_t bar) {
     asm volatile(
-        "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %3, %4, %5}], "
-        "[%6];" ::"r"(tc::smem_u32(dst)),
-        "l"(map), "r"(k), "r"(0), "r"(block), "r"(e), "r"(tc::smem_u32(bar))
+        "{\n"
+        ".reg .pred q;\n"
+        "setp.ne.b32 q, %7, 0;\n"
+        "@q cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %3, %4, %5}], "
+        "[%6];\n"
+        "}\n" ::"r"(dst),
+        "l"(map), "r"(k), "r"(0), "r"(block), "r"(e), "r"(bar), "r"(lead)
         : "memory");
 }
 // Rows from `row` on, positions 64 * block and the 64 * (halves - 1) after them, as one or two atoms.
@@ -512,37 +519,48 @@ __global__ void __launch_bounds__(xp::kThreads, 1) k_experts(const __grid_consta
         regs_down<kRegsIssue>();
         if (warp == kWeightWarp) {
             // ------------------------------------- weights, and who does which unit
-            if (lane == 0) {
-                int at = 0;
-                bool ok = true;
-                Unit t = unit_at(blockIdx.x);
-                for (int seq = 0; ok; ++seq) {
-                    const int i = seq % kUnitSlots;
-                    ok = tc::mbar_wait(&S.uempty[i], ((uint32_t)(seq / kUnitSlots) & 1) ^ 1, abort_flag, kWait);
-                    if (!ok) fail();
+            // (uniform like the MMA warps: a copy issued in a branch of one lane takes 150 cycles)
+            const uint32_t lead = lane == 0;
+            int at = 0;
+            bool ok = true;
+            Unit t = unit_at(blockIdx.x);
+            for (int seq = 0; ok; ++seq) {
+                const int i = seq % kUnitSlots;
+                bool got = tc::mbar_wait(&S.uempty[i], ((uint32_t)(seq / kUnitSlots) & 1) ^ 1, abort_flag, kWait);
+                if (!got) fail();
+                ok = __all_sync(0xffffffffu, got) != 0;
+                if (lead) {
                     S.unit[i] = t;
                     tc::mbar_arrive(&S.ufull[i]);
-                    if (!ok || t.rows == 0) break;
-                    for (int k = 0; k < steps; ++k, ++at) {
-                        const int ws = at % S_::kWSlots;
-                        if (!tc::mbar_wait(&S.wempty[ws], ((uint32_t)(at / S_::kWSlots) & 1) ^ 1, abort_flag, kWait)) {
-                            fail();
-                            ok = false;
-                            break;
-                        }
-                        tc::mbar_arrive_expect_tx(&S.wfull[ws], kWStage);
-                        uint8_t* dst = sW + ws * kWStage;
-                        if (SWIGLU) load_pairs(dst, &a.wmap, k * kStep, t.n0 / 32, t.e, &S.wfull[ws]);
-                        else load_weights(dst, &a.wmap, k * kStep, t.n0, t.e, &S.wfull[ws]);
-                    }
-                    // the first unit of each CTA is its own; the launch before clears the counter of the others
-                    if (seq == 0) pdl_wait();
-                    t = unit_at((int)gridDim.x + atomicAdd(a.taken, 1));
                 }
-                // every copy has landed before the CTA leaves
-                for (int i = max(0, at - S_::kWSlots); i < at; ++i)
-                    tc::mbar_wait_drain(&S.wfull[i % S_::kWSlots], (uint32_t)(i / S_::kWSlots) & 1, kWait / 8);
+                const int rows = (int)__reduce_max_sync(0xffffffffu, (unsigned)t.rows);
+                if (!ok || rows == 0) break;
+                // The first unit of each CTA is its own; the launch before clears the counter of the others. The next is taken
+                // before this one's copies are issued: taken after them, it left the copies waiting for its answer (a
+                // step's down products, six stages to a unit, 36.8 us).
+                int taken = 0;
+                if (seq > 0 && lead) taken = atomicAdd(a.taken, 1);
+                const int n0 = (int)__reduce_max_sync(0xffffffffu, (unsigned)t.n0), e = (int)__reduce_max_sync(0xffffffffu, (unsigned)t.e);
+                for (int k = 0; k < steps; ++k, ++at) {
+                    const int ws = at % S_::kWSlots;
+                    got = tc::mbar_wait(&S.wempty[ws], ((uint32_t)(at / S_::kWSlots) & 1) ^ 1, abort_flag, kWait);
+                    if (!got) fail();
+                    ok = __all_sync(0xffffffffu, got) != 0;
+                    if (!ok) break;
+                    const uint32_t bar = tc::smem_u32(&S.wfull[ws]), dst = tc::smem_u32(sW + ws * kWStage);
+                    expect_bytes(lead, bar, kWStage);
+                    if (SWIGLU) load_pairs(lead, dst, &a.wmap, k * kStep, n0 / 32, e, bar);
+                    else load_weights(lead, dst, &a.wmap, k * kStep, n0, e, bar);
+                }
+                if (seq == 0) {
+                    pdl_wait();
+                    if (lead) taken = atomicAdd(a.taken, 1);
+                }
+                t = unit_at((int)gridDim.x + __shfl_sync(0xffffffffu, taken, 0));
             }
+            // every copy has landed before the CTA leaves
+            for (int i = max(0, at - S_::kWSlots); i < at; ++i)
+                tc::mbar_wait_drain(&S.wfull[i % S_::kWSlots], (uint32_t)(i / S_::kWSlots) & 1, kWait / 8);
         } else if (warp == kRowWarp) {
             // ---------------------------------------------------------- rows
             // (uniform like the MMA warps: a copy issued in a branch of one lane takes 150 cycles)
