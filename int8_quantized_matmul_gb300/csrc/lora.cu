@@ -507,6 +507,9 @@ __global__ void __launch_bounds__(kThreads, KK <= 2 ? 2 : 1) k_lora_outer(const 
         outer.run(tp, s_mul);
         __syncthreads();
     }
+    // Without a unit, too: the launch behind this one is ordered by this one's end alone, and the inner product
+    // may still be reading the plan.
+    if (!waited) pdl_wait();
 }
 
 // ---------------------------------------------------------------------------
