@@ -32,17 +32,17 @@
 // gate and its up value are then 16 lanes apart in the same warp, and every lane
 // finishes one of two neighbouring rows after one exchange.
 //
-// Measured (one GB300). Few rows per expert: 64 tokens over 8 of 128 experts, 1536 x 2048, 51-55 us, 289 MB of weights
-// in use. Many: 4096 bf16 rows of the same 220 us (rows 36, products 187); 1777 F32 rows over 2 of 8, 1536 x 8960: 123 us (rows 32,
-// products 84, sums 8), tensor pipe 51 % (66 % on the SMs with most units: 2.5 for each). A stage of 112 rows takes 800 to
-// 900 cycles for 450 of MMAs: shared memory moves about 740 cycles' worth (16 KB of weights in and out, 28 KB of rows in and
+// Measured (one GB300). Few rows per expert: 64 tokens over 8 of 128 experts, 1536 x 2048, 51-54 us, 289 MB of weights
+// in use. Many: 4096 bf16 rows of the same 228 us (rows 36, products 194); 1777 F32 rows over 2 of 8, 1536 x 8960: 127 us (rows 32,
+// products 88, sums 8), on the SMs with most units 2.5 for each. A stage of 112 rows takes 840 to
+// 940 cycles for 450 of MMAs: shared memory moves about 740 cycles' worth (16 KB of weights in and out, 28 KB of rows in and
 // to the MMA), and without any one of rows, weights, TMEM stores, MMAs or stores of y it takes 94 % or more of the time. CTA
 // pairs, which halve the rows' part, were slower (280 us).
 //
 // Roles (640 threads): warps 0-7 epilogue (each half of the columns), 8-15 converters (two groups taking
 // stages by turns), 16 weights, 17 rows, 18 and 19 MMAs (stages by
-// turns into the same accumulator: sums of integers do not depend on the order). TMEM: two accumulators
-// of ROWS columns, then a ring of 64-column operands. Waits are bounded; one that runs
+// turns; who adds to what is said at Shape::kTurns). TMEM: accumulators of ROWS columns for two chunks, then a ring of
+// 64-column operands. Waits are bounded; one that runs
 // out sets the status word at the start of the workspace and the CTA's abort
 // flag, roles leave their loops, and what they issued is drained.
 
@@ -63,15 +63,15 @@ namespace xp {
 
 constexpr int kThreads = 640;
 constexpr int kConvWarp = 8, kWeightWarp = 16, kRowWarp = 17, kMmaWarp = 18;
-constexpr int kIssuers = 2;                     // warps that issue MMAs, stages by turns
 constexpr int kChannels = 128;
 constexpr int kStep = 128;                      // positions of a stage
 constexpr int kChunkSteps = kI8sChunkK / kStep; // stages of an exact f32 sum
+constexpr int kIssuers = 2;                     // warps that issue MMAs, stages by turns
+constexpr int kUnitReaders = 19;                // warps that are told of each unit: all but the one that takes them
 constexpr int kWStage = kChannels * kStep;      // bytes of a stage's weights
 constexpr int kOpCols = kStep / 2;              // TMEM columns of a stage's weights in f16
 constexpr int kMaxSlots = 6, kMaxWSlots = 10;
 constexpr int kUnitSlots = 8;                   // units handed out ahead
-constexpr int kUnitReaders = 19;                // warps that are told of each: all but the one that takes them
 constexpr long long kWait = 2000000000LL;
 // Registers of a thread after the split (of the 96 at launch): epilogue,
 // converters, the others. 256 * 120 + 256 * 88 + 128 * 56 <= 640 * 96.
@@ -83,11 +83,18 @@ struct Shape {
     // Many: the rows do.
     static constexpr int kSlots = ROWS == 32 ? 6 : 4;      // operands: rows, and weights in TMEM
     static constexpr int kWSlots = ROWS == 32 ? 10 : 4;    // weights as bytes
+    // An accumulation reads what it adds to, and nothing orders the MMAs of two threads but a barrier between tcgen05
+    // fences. Few rows: each issuer has an accumulator of its own, and the epilogue adds the two (as fast as one for both).
+    // Many: TMEM has no room for that, and an issuer begins its stage when the other has issued the stage before
+    // (prompts 228 and 127 us; one issuer 248 and 139; an accumulator of each, taken into registers before the next chunk,
+    // 233 and 138; both into one without an order 221 and 124, exact in every comparison, but promised by nothing).
+    static constexpr bool kTurns = ROWS != 32;
+    static constexpr int kAcc = kTurns ? ROWS : kIssuers * ROWS;   // TMEM columns of a chunk's sums
     // Rows come in one copy per stage, as two atoms of 64 positions, of one to four times kBox rows.
     static constexpr int kBox = ROWS / 4;
     __device__ static int boxes(int rows) { return (rows + kBox - 1) / kBox; }
     static constexpr int kRowStage = ROWS * 256;
-    static constexpr uint32_t kOp0 = 2 * ROWS;             // first TMEM column of the operands
+    static constexpr uint32_t kOp0 = 2 * kAcc;             // first TMEM column of the operands
     // Each slot is always one converter group's and one issuer's: a parity wait passes for a phase two ahead, so one that
     // has run ahead must not wait for a slot whose use before is the other's and has not come yet.
     static_assert(kOp0 + kSlots * kOpCols <= 512 && kSlots % 2 == 0 && kWSlots % 2 == 0, "TMEM; slots");
@@ -102,7 +109,7 @@ struct Unit {
 struct Shared {
     uint64_t wfull[kMaxWSlots], wempty[kMaxWSlots];
     uint64_t full[kMaxSlots], empty[kMaxSlots];
-    uint64_t dfull[2], dempty[2], done[kIssuers];
+    uint64_t dfull[2], dempty[2], done[kIssuers], turn[kIssuers];
     uint64_t ufull[kUnitSlots], uempty[kUnitSlots];
     Unit unit[kUnitSlots];
     uint32_t tmem;
@@ -149,6 +156,16 @@ __device__ __forceinline__ void commit(uint32_t lead, uint64_t* bar) {
         "setp.ne.b32 q, %1, 0;\n"
         "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n"
         "}\n" ::"r"(tc::smem_u32(bar)), "r"(lead)
+        : "memory");
+}
+__device__ __forceinline__ void arrive_from(uint32_t lead, uint64_t* bar) {
+    asm volatile(
+        "{\n"
+        ".reg .pred q;\n"
+        "setp.ne.b32 q, %1, 0;\n"
+        "@q mbarrier.arrive.relaxed.cta.shared::cta.b64 _, [%0];\n"
+        "}\n" ::"r"(tc::smem_u32(bar)),
+        "r"(lead)
         : "memory");
 }
 __device__ __forceinline__ void load_weights(uint32_t lead, uint32_t dst, const CUtensorMap* map, int k, int n, int e, uint32_t bar) {
@@ -273,7 +290,7 @@ __global__ void __launch_bounds__(xp::kThreads, 1) k_experts(const __grid_consta
                 tc::mbar_init(&S.ufull[i], 1);
                 tc::mbar_init(&S.uempty[i], kUnitReaders);
             }
-            for (int i = 0; i < kIssuers; ++i) tc::mbar_init(&S.done[i], 1);
+            for (int i = 0; i < kIssuers; ++i) tc::mbar_init(&S.done[i], 1), tc::mbar_init(&S.turn[i], 1);
             S.abort = 0;
             tc::fence_mbar_init();
         }
@@ -290,7 +307,7 @@ __global__ void __launch_bounds__(xp::kThreads, 1) k_experts(const __grid_consta
     tc::tc_fence_after();
     const uint32_t tmem = S.tmem;
     if (warp < kConvWarp) {   // every MMA accumulates: the accumulators start at zero, and are left so when they are read
-        for (int i = 32 * (warp >> 2); i < 2 * ROWS; i += 64)
+        for (int i = 32 * (warp >> 2); i < 2 * S_::kAcc; i += 64)
             tc::tmem_st_zero_32x32b_x32(tmem + ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)i);
         tc::tmem_st_wait();
         tc::tc_fence_before();
@@ -369,7 +386,23 @@ __global__ void __launch_bounds__(xp::kThreads, 1) k_experts(const __grid_consta
                 if (!tc::mbar_wait(&S.dfull[chunk_at & 1], (uint32_t)(chunk_at >> 1) & 1, abort_flag, kWait)) { fail(); ok = false; }
                 ok = __all_sync(0xffffffffu, ok) != 0;
                 tc::tc_fence_after();
-                return tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)((chunk_at & 1) * ROWS + c0);
+                return tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)((chunk_at & 1) * S_::kAcc + c0);
+            };
+            // 16 columns of its sums, with two issuers both parts added (whole numbers, exact); they are left zero, the first
+            // part where `zero` says so
+            auto take = [&](uint32_t d, uint32_t (&v)[16], bool zero) {
+                tc::tmem_ld_32x32b_x16(d, v);
+                if constexpr (!S_::kTurns) {
+                    uint32_t u[16];
+                    tc::tmem_ld_32x32b_x16(d + ROWS, u);
+                    tc::tmem_ld_wait();
+                    tc::tmem_st_zero_32x32b_x16(d + ROWS);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__fadd_rn(__uint_as_float(v[i]), __uint_as_float(u[i])));
+                } else {
+                    tc::tmem_ld_wait();
+                }
+                if (zero) tc::tmem_st_zero_32x32b_x16(d);
             };
             auto hand_back = [&] {
                 tc::tmem_st_wait();
@@ -385,9 +418,7 @@ __global__ void __launch_bounds__(xp::kThreads, 1) k_experts(const __grid_consta
                 for (int p = 0; p < kPieces; ++p) {
                     if (p >= pieces) continue;
                     uint32_t v[16];
-                    tc::tmem_ld_32x32b_x16(d + 16u * p, v);
-                    tc::tmem_ld_wait();
-                    tc::tmem_st_zero_32x32b_x16(d + 16u * p);
+                    take(d + 16u * p, v, true);
                     if (chunks == 2) {
 #pragma unroll
                         for (int i = 0; i < 16; ++i) sum[p][i] = __uint_as_float(v[i]);
@@ -409,8 +440,7 @@ __global__ void __launch_bounds__(xp::kThreads, 1) k_experts(const __grid_consta
                 for (int p = 0; p < kPieces; ++p) {
                     if (p >= pieces) continue;
                     uint32_t v[16];
-                    tc::tmem_ld_32x32b_x16(d + 16u * p, v);
-                    tc::tmem_ld_wait();
+                    take(d + 16u * p, v, false);   // (stored to below: two stores to one place would have no order)
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
                         const float x = __uint_as_float(v[i]);
@@ -425,9 +455,7 @@ __global__ void __launch_bounds__(xp::kThreads, 1) k_experts(const __grid_consta
 #pragma unroll 1
             for (int p = 0; p < pieces; ++p) {
                 uint32_t w[16];
-                tc::tmem_ld_32x32b_x16(d + 16u * p, w);
-                tc::tmem_ld_wait();
-                tc::tmem_st_zero_32x32b_x16(d + 16u * p);
+                take(d + 16u * p, w, true);
                 // All of the rows' places are read, and all values made, before the first is stored: a read of
                 // shared memory would not be moved ahead of a store (108 cycles for each row).
                 constexpr int kOut = SWIGLU ? 8 : 16;
@@ -588,7 +616,7 @@ __global__ void __launch_bounds__(xp::kThreads, 1) k_experts(const __grid_consta
             }
             for (int i = max(0, at - S_::kSlots); i < at; ++i)
                 tc::mbar_wait_drain(&S.full[i % S_::kSlots], (uint32_t)(i / S_::kSlots) & 1, kWait / 8);
-        } else {
+        } else if (warp < kMmaWarp + kIssuers) {
             // ---------------------------------------------------------- MMAs
             // (reductions over the warp: their results, and so the branches, are uniform)
             const uint32_t lead = lane == 0;
@@ -608,17 +636,21 @@ __global__ void __launch_bounds__(xp::kThreads, 1) k_experts(const __grid_consta
                 const uint32_t idesc = tc::idesc_f16_f32(kChannels, (rows + 15) / 16 * 16);
                 for (int k0 = 0; ok && k0 < steps; k0 += kChunkSteps, ++chunk_at) {
                     const int buf = chunk_at & 1, k1 = min(steps, k0 + kChunkSteps);
-                    const uint32_t d = tm + (uint32_t)(buf * ROWS);
+                    const uint32_t d = tm + (uint32_t)(buf * S_::kAcc + (S_::kTurns ? 0 : me * ROWS));
                     ok = wait(&S.dempty[buf], ((uint32_t)(chunk_at >> 1) & 1) ^ 1);
                     for (int k = k0; ok && k < k1; ++k, ++at) {
                         if (at % kIssuers != me) continue;
                         const int slot = at % S_::kSlots;
-                        ok = wait(&S.full[slot], (uint32_t)(at / S_::kSlots) & 1);
-                        if (!ok) break;
-                        tc::tc_fence_after();
                         const uint64_t bd = tc::sdesc_sw128_kmajor(tc::smem_u32(sRows + slot * S_::kRowStage));
                         const uint32_t op = tm + S_::kOp0 + (uint32_t)(slot * kOpCols);
                         const int left = (a.K - k * kStep + 15) / 16;   // 16-position MMAs that are left of the rows
+                        // stage at - 1 is the other issuer's: the n-th handing over to issuer 1 is before its n-th stage, to issuer 0 after
+                        bool got = tc::mbar_wait_spin(&S.full[slot], (uint32_t)(at / S_::kSlots) & 1, abort_flag, kWait);
+                        if (S_::kTurns && at > 0)
+                            got = got && tc::mbar_wait_spin(&S.turn[me], (uint32_t)((at - 1) / kIssuers) & 1, abort_flag, kWait);
+                        ok = __all_sync(0xffffffffu, got) != 0;
+                        if (!ok) break;
+                        tc::tc_fence_after();
                         if (left >= 8) {
 #pragma unroll
                             for (int j = 0; j < 8; ++j)
@@ -626,6 +658,10 @@ __global__ void __launch_bounds__(xp::kThreads, 1) k_experts(const __grid_consta
                         } else {
                             for (int j = 0; j < left; ++j)
                                 mma(lead, d, op + 8u * j, bd + (uint64_t)((j >> 2) * (atom >> 4) + 2 * (j & 3)), idesc);
+                        }
+                        if (S_::kTurns) {
+                            tc::tc_fence_before();
+                            arrive_from(lead, &S.turn[me ^ 1]);
                         }
                         commit(lead, &S.empty[slot]);
                     }

@@ -73,3 +73,26 @@ def test_lora_plan_of_nobody_then_another(i2s, rank, graph):
                 at = own == a
                 want[at] = ((x[at].double() @ A[a].double().T) @ B[a].double().T).float()
             assert torch.equal(o, want), i
+
+
+# -- the two warps that issue an expert's MMAs --------------------------------------------------------
+
+@pytest.mark.parametrize("K", [16, 128, 144, 1024, 1152, 2176, 8976])
+@pytest.mark.parametrize("rows", [7, 250])
+def test_experts_stages_of_both_issuers(i2s, rows, K):
+    """One stage and many, odd and even counts, few rows (an accumulator for each issuer) and many (one, by turns): sums of
+    one sign as large as they come, and random ones, exact and the same in every call."""
+    E, N = 3, 520
+    rng = np.random.default_rng(K)
+    for extreme in (False, True):
+        wq = np.full((E, N, K), -128, np.int8) if extreme else rng.integers(-128, 128, (E, N, K)).astype(np.int8)
+        x = np.full((rows, K), 3.0, np.float32) if extreme else rng.normal(0, 1, (rows, K)).astype(np.float32)
+        bscale = np.exp(rng.normal(0, 0.3, (E, N))).astype(np.float32)
+        owner = rng.integers(0, E, rows).astype(np.int32)
+        want = torch.from_numpy(ref.dots(wq, bscale, owner, x, 1)).cuda()
+        call = i2s.W8A8Experts(dev(wq), dev(bscale), i2s.route_plan(dev(owner), E), dev(x))
+        for _ in range(8):
+            call.out.fill_(0)
+            call()
+            assert torch.equal(call.out, want)
+        call.check()
