@@ -805,17 +805,24 @@ size_t route_plan_workspace(int64_t items, int owners);
 int route_plan_build(const int32_t* owner, const route_plan* plan, void* ws, size_t ws_bytes, i2s_stream_t stream);
 
 /* A router: of each row's `experts` logits (i2s_rows, rows x experts) the k
- * largest logit + bias[e] (bias: device F32 [experts] or NULL; one binary32 sum), in falling
- * order, equal ones by index. Item row*k + j is the row's j-th choice, expert[row*k + j]
+ * largest scores, in falling order, equal ones by index. The score is a binary32 value, with a bias (device F32 [experts] or
+ * NULL) one binary32 sum:
+ *   logit + bias[e]: offsets and masks of logits;
+ *   with ROUTE_BIAS_SCORE p + bias[e], where p is what the expert counts for without a bias: the softmax over all the row's
+ *       logits, or with ROUTE_SIGMOID 1 / (1 + exp(-l)), in the steps of the weights below. THIS is the choice of routers that
+ *       are trained with a balancing bias (auxiliary-loss-free load balancing): logit + bias[e] chooses other experts there,
+ *       and nothing reports it. Two scores closer than the steps' roundings (about 2^-21 of p, more where a softmax has
+ *       many or far logits) may come in either order. Without a bias the flag changes nothing.
+ * The weights have no bias in either case. Item row*k + j is the row's j-th choice, expert[row*k + j]
  * (device int32) its expert and weight[row*k + j] (device F32) its weight: factor times
  *   exp(l - m) / sum_e exp(l_e - m), the softmax over all the row's logits (without the
  *       bias), or with ROUTE_NORM over those of the chosen;
  *   1 / (1 + exp(-l)) with ROUTE_SIGMOID, and with ROUTE_NORM that divided by
  *       the sum over the chosen (zero where that sum is zero).
- * A score of -infinity or NaN (a masked expert's) is never chosen, and such
+ * An expert whose score or logit + bias[e] is -infinity or NaN (a masked one) is never chosen, and such
  * logits add nothing to a softmax: where fewer than k are left, the items behind them have the
  * expert -1 and the weight 0. A logit of +infinity makes the weights of its row's softmax
- * NaN. Sums are binary32.
+ * NaN, and with ROUTE_BIAS_SCORE its scores: nothing is chosen. Sums are binary32.
  * plan: items rows*k, owners `experts`; start and list are written as by
  * route_plan_build from expert. NULL for none.
  * 1 <= experts <= ROUTE_MAX_OWNERS, 1 <= k <= min(experts, ROUTE_MAX_CHOSEN),
@@ -823,6 +830,7 @@ int route_plan_build(const int32_t* owner, const route_plan* plan, void* ws, siz
  * without a plan none is needed (NULL). factor is finite. */
 #define ROUTE_SIGMOID 1u
 #define ROUTE_NORM 2u
+#define ROUTE_BIAS_SCORE 8u
 int route_topk(const i2s_rows* logits, int64_t rows, int experts, int k, const float* bias, float factor, unsigned flags,
                int32_t* expert, float* weight, const route_plan* plan, void* ws, size_t ws_bytes, i2s_stream_t stream);
 

@@ -1,7 +1,8 @@
 // The router and the plans of rows sorted by owner (include/i2s.h, route_topk
 // and route_plan_build).
 //
-// Mathematics. A row's choices are the k largest scores (logit + bias), equal
+// Mathematics. A row's choices are the k largest scores (the logit, logit + bias, or
+// what weighs the expert, its sigmoid or its part of the softmax, + bias), equal
 // ones by index: the scores become integers of the same order, and k times the warp
 // takes the largest and of those the lowest index. Weights are a
 // softmax, over all logits or the chosen, or sigmoids.
@@ -50,8 +51,11 @@ __device__ __forceinline__ float warp_add(float v) {
     return v;
 }
 
+__device__ __forceinline__ float sigmoid_of(float x) { return __fdiv_rn(1.0f, __fadd_rn(1.0f, expf(-x))); }
+
 // One row by one warp; lane l looks at the experts l, l + 32, ... (VPL of them).
-template <int DT, int VPL>
+// SCORED: the bias, of which there is one, is added to the sigmoid or the softmax.
+template <int DT, int VPL, bool SCORED>
 __device__ __forceinline__ void topk_row(const TopkArgs& a, int row, int lane) {
     const typename RowT<DT>::type* x = static_cast<const typename RowT<DT>::type*>(a.logits) + row * a.stride;
     float l[VPL];
@@ -74,6 +78,26 @@ __device__ __forceinline__ void topk_row(const TopkArgs& a, int row, int lane) {
         if (!live) l[i] = -INFINITY;
         top = fmaxf(top, l[i]);
     }
+    float m, sum;   // of the softmax over all
+    auto softmax = [&] {
+        m = warp_max(top);
+        sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) sum += l[i] == -INFINITY ? 0.0f : expf(l[i] - m);
+        sum = warp_add(sum);
+    };
+    if constexpr (SCORED) {
+        if (!a.sigmoid) softmax();
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) {
+            const int e = lane + 32 * i;
+            if (key[i] == 0) continue;
+            const float p = a.sigmoid ? sigmoid_of(l[i]) : __fdiv_rn(expf(l[i] - m), sum);
+            const float s = __fadd_rn(__fadd_rn(p, a.bias[e]), 0.0f);
+            const uint32_t bits = __float_as_uint(s);
+            key[i] = s > -INFINITY ? ((bits >> 31) ? ~bits : bits | 0x80000000u) : 0u;
+        }
+    }
     int mine = -1;   // of lane j: the j-th choice
     for (int j = 0; j < a.k; ++j) {
         uint32_t best = 0;
@@ -94,21 +118,18 @@ __device__ __forceinline__ void topk_row(const TopkArgs& a, int row, int lane) {
     const float v = mine >= 0 ? to_f32(x[mine]) : -INFINITY;
     float w;
     if (a.sigmoid) {
-        w = mine >= 0 ? __fdiv_rn(1.0f, __fadd_rn(1.0f, expf(-v))) : 0.0f;
+        w = mine >= 0 ? sigmoid_of(v) : 0.0f;
         if (a.norm) {
-            const float sum = warp_add(w);
-            w = sum == 0.0f ? 0.0f : __fdiv_rn(w, sum);
+            const float all = warp_add(w);
+            w = all == 0.0f ? 0.0f : __fdiv_rn(w, all);
         }
     } else if (a.norm) {
-        const float m = warp_max(v);
-        w = mine >= 0 ? expf(v - m) : 0.0f;
+        const float best = warp_max(v);
+        w = mine >= 0 ? expf(v - best) : 0.0f;
         w = __fdiv_rn(w, warp_add(w));
     } else {
-        const float m = warp_max(top);
-        float sum = 0.0f;
-#pragma unroll
-        for (int i = 0; i < VPL; ++i) sum += l[i] == -INFINITY ? 0.0f : expf(l[i] - m);
-        w = __fdiv_rn(expf(v - m), warp_add(sum));
+        if constexpr (!SCORED) softmax();
+        w = __fdiv_rn(expf(v - m), sum);
     }
     if (lane < a.k) {
         a.expert[(long long)row * a.k + lane] = mine;
@@ -229,18 +250,18 @@ __device__ void sort_block(const int* owner, int lo, int hi, const PlanView& p, 
     }
 }
 
-template <int DT, int VPL>
+template <int DT, int VPL, bool SCORED>
 __global__ void __launch_bounds__(kThreads) k_route_one(TopkArgs a, PlanView p, int* start, int* list) {
     __shared__ SortShared S;
     pdl_wait();
-    for (int row = threadIdx.x >> 5; row < a.rows; row += kWarps) topk_row<DT, VPL>(a, row, threadIdx.x & 31);
+    for (int row = threadIdx.x >> 5; row < a.rows; row += kWarps) topk_row<DT, VPL, SCORED>(a, row, threadIdx.x & 31);
     if (start == nullptr) return;
     __syncthreads();   // this block's choices are then visible to it
     sort_block(a.expert, 0, a.rows * a.k, p, start, list, nullptr, 1, 0, S);
 }
 
 // Choices of `per` rows per block, and how many of them each expert has.
-template <int DT, int VPL>
+template <int DT, int VPL, bool SCORED>
 __global__ void __launch_bounds__(kThreads) k_route_topk(TopkArgs a, int per, int* counts) {
     __shared__ int n[kMaxOwners];
     pdl_wait();
@@ -250,7 +271,7 @@ __global__ void __launch_bounds__(kThreads) k_route_topk(TopkArgs a, int per, in
         for (int i = threadIdx.x; i < a.experts; i += kThreads) n[i] = 0;
         __syncthreads();
     }
-    for (int row = lo + (threadIdx.x >> 5); row < hi; row += kWarps) topk_row<DT, VPL>(a, row, threadIdx.x & 31);
+    for (int row = lo + (threadIdx.x >> 5); row < hi; row += kWarps) topk_row<DT, VPL, SCORED>(a, row, threadIdx.x & 31);
     if (counts == nullptr) return;
     __syncthreads();
     for (int i = lo * a.k + threadIdx.x; i < hi * a.k; i += kThreads) {
@@ -287,26 +308,32 @@ __global__ void __launch_bounds__(kThreads) k_plan_sort(const int* owner, PlanVi
 // 8.1; 64 rows 9.0 and 8.0; 128 rows 14.4 and 8.4).
 constexpr int kOneItems = 2048, kOneRows = 48;
 
-template <int DT, int VPL>
+template <int DT, int VPL, bool SCORED>
 cudaError_t launch_topk(const TopkArgs& a, const PlanView& p, int* start, int* list, int* counts, cudaStream_t s) {
     const int64_t items = (int64_t)a.rows * a.k;
     if (a.rows <= kOneRows && items <= kOneItems)
-        return launch_pdl(k_route_one<DT, VPL>, dim3(1), dim3(kThreads), 0, s, a, p, start, list);
+        return launch_pdl(k_route_one<DT, VPL, SCORED>, dim3(1), dim3(kThreads), 0, s, a, p, start, list);
     // without a plan the blocks need not be few
     const int most = start != nullptr ? kBlocks : 152 * 2;
     const int per = std::max(kWarps, (a.rows + most - 1) / most);
     const int blocks = (a.rows + per - 1) / per;
-    cudaError_t e = launch_pdl(k_route_topk<DT, VPL>, dim3((unsigned)blocks), dim3(kThreads), 0, s, a, per,
+    cudaError_t e = launch_pdl(k_route_topk<DT, VPL, SCORED>, dim3((unsigned)blocks), dim3(kThreads), 0, s, a, per,
                                start != nullptr ? counts : nullptr);
     if (e != cudaSuccess || start == nullptr) return e;
     return launch_pdl(k_plan_sort, dim3((unsigned)blocks), dim3(kThreads), 0, s, a.expert, p, per * a.k, start, list, counts);
 }
 
-template <int DT>
+template <int DT, bool SCORED>
 cudaError_t launch_dt(const TopkArgs& a, const PlanView& p, int* start, int* list, int* counts, cudaStream_t s) {
-    if (a.experts <= 128) return launch_topk<DT, 4>(a, p, start, list, counts, s);
-    if (a.experts <= 256) return launch_topk<DT, 8>(a, p, start, list, counts, s);
-    return launch_topk<DT, 32>(a, p, start, list, counts, s);
+    if (a.experts <= 128) return launch_topk<DT, 4, SCORED>(a, p, start, list, counts, s);
+    if (a.experts <= 256) return launch_topk<DT, 8, SCORED>(a, p, start, list, counts, s);
+    return launch_topk<DT, 32, SCORED>(a, p, start, list, counts, s);
+}
+template <bool SCORED>
+cudaError_t launch_route(int dt, const TopkArgs& a, const PlanView& p, int* start, int* list, int* counts, cudaStream_t s) {
+    if (dt == kF32) return launch_dt<kF32, SCORED>(a, p, start, list, counts, s);
+    if (dt == kF16) return launch_dt<kF16, SCORED>(a, p, start, list, counts, s);
+    return launch_dt<kBf16, SCORED>(a, p, start, list, counts, s);
 }
 
 }  // namespace
@@ -358,7 +385,7 @@ int route_topk(const i2s_rows* logits, int64_t rows, int experts, int k, const f
     if (!expert || !weight) return I2S_E_NULL_PTR;
     int r = check_row_tensor(logits, rows, experts, false, false);
     if (r) return r;
-    if ((flags & ~(ROUTE_SIGMOID | ROUTE_NORM)) || !std::isfinite(factor)) return I2S_E_BAD_ARG;
+    if ((flags & ~(ROUTE_SIGMOID | ROUTE_NORM | ROUTE_BIAS_SCORE)) || !std::isfinite(factor)) return I2S_E_BAD_ARG;
     if (((uintptr_t)bias & 3) || ((uintptr_t)expert & 3) || ((uintptr_t)weight & 3)) return I2S_E_MISALIGNED;
     const size_t items = (size_t)rows * k;
     const Span in[2] = {rows_span(*logits, rows, experts), span_of(bias, bias ? 4 * (size_t)experts : 0)};
@@ -386,10 +413,9 @@ int route_topk(const i2s_rows* logits, int64_t rows, int experts, int k, const f
                         (flags & ROUTE_SIGMOID) != 0, (flags & ROUTE_NORM) != 0};
     PlanView p = {nullptr, nullptr, (int)items, experts};
     int *start = plan ? plan->start : nullptr, *list = plan ? plan->list : nullptr, *counts = plan ? static_cast<int*>(ws) : nullptr;
-    cudaError_t e;
-    if (logits->dtype == kF32) e = launch_dt<kF32>(a, p, start, list, counts, stream);
-    else if (logits->dtype == kF16) e = launch_dt<kF16>(a, p, start, list, counts, stream);
-    else e = launch_dt<kBf16>(a, p, start, list, counts, stream);
+    const bool scored = bias != nullptr && (flags & ROUTE_BIAS_SCORE) != 0;
+    const cudaError_t e = scored ? launch_route<true>(logits->dtype, a, p, start, list, counts, stream)
+                                 : launch_route<false>(logits->dtype, a, p, start, list, counts, stream);
     return e == cudaSuccess ? I2S_OK : I2S_E_CUDA;
 }
 

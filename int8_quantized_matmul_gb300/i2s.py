@@ -938,7 +938,7 @@ def kv8_attention(cache, batch, q, **kw):
 # -- rows that have weights of their own --------------------------------------------
 
 ROUTE_MAX_OWNERS, ROUTE_MAX_ITEMS, ROUTE_MAX_CHOSEN = 1024, 1 << 27, 16
-ROUTE_SIGMOID, ROUTE_NORM = 1, 2
+ROUTE_SIGMOID, ROUTE_NORM, ROUTE_BIAS_SCORE = 1, 2, 8
 W8A8_SWIGLU = 1
 W8A8_TEST_STALL = 1 << 31   # tests only
 
@@ -1020,13 +1020,17 @@ class RouteBuild(_Kv8Call):
 class RouteTopk(_Kv8Call):
     """route_topk: the k largest of each row's logits (rows x experts) with their
     weights, in `expert` and `weight` (rows x k), and the plan of the items row*k + j.
-    bias: F32 [experts], added for the choice alone; plan=False for none."""
+    bias: F32 [experts], added for the choice alone, to the logits or with bias_on="score" to
+    their sigmoid or softmax: a router trained with a balancing bias wants "score".
+    plan=False for none."""
 
     def __init__(self, logits, k: int, bias=None, factor: float = 1.0, sigmoid: bool = False, norm: bool = False,
-                 expert=None, weight=None, plan=None, ws=None):
+                 expert=None, weight=None, plan=None, ws=None, bias_on: str = "logit"):
         torch = _torch()
         if logits.dim() != 2:
             raise ValueError("logits: expected rows x experts")
+        if bias_on not in ("logit", "score"):
+            raise ValueError(f"bias_on: expected logit or score, got {bias_on!r}")
         device, (rows, experts), k = _cuda_device(logits.device), logits.shape, _int_arg(k, "k")
         if not 1 <= k <= min(experts, ROUTE_MAX_CHOSEN) or rows < 1 or rows * k > ROUTE_MAX_ITEMS:
             raise I2SError("route_topk", -1)
@@ -1041,7 +1045,7 @@ class RouteTopk(_Kv8Call):
         self.ws, self._keep = ws, (logits, bias)
         self._bind("route_topk", device, _row_tensor(logits, rows, experts, device, "logits"), rows, experts, k,
                    _values(bias, torch.float32, experts, device, "bias"), float(factor),
-                   (ROUTE_SIGMOID if sigmoid else 0) | (ROUTE_NORM if norm else 0),
+                   (ROUTE_SIGMOID if sigmoid else 0) | (ROUTE_NORM if norm else 0) | (ROUTE_BIAS_SCORE if bias_on == "score" else 0),
                    _values(self.expert, torch.int32, rows * k, device, "expert"),
                    _values(self.weight, torch.float32, rows * k, device, "weight"),
                    self.plan.struct if self.plan is not None else None, _dptr(ws), ws.numel() if ws is not None else 0)

@@ -96,3 +96,112 @@ def test_experts_stages_of_both_issuers(i2s, rows, K):
             call()
             assert torch.equal(call.out, want)
         call.check()
+
+
+# -- choices by a biased score ------------------------------------------------------------------------
+
+EPS = 2.0 ** -24
+
+
+def scores(logits, bias, sigmoid):
+    """What the bias is added to in 64 bits, the score, how far binary32's steps may be off it, and which experts may be chosen.
+    The exponential is within 2 units (2^-22 of its value), its argument of a softmax rounded once (2^-24 of its size), a sum over
+    E values takes E/32 + 5 roundings, the sum with one, a quotient and the sum with the bias one each; below binary32's range
+    2^-126."""
+    with np.errstate(all="ignore"):
+        live = (logits > -np.inf) & (logits + bias > -np.inf)
+        if sigmoid:
+            p = 1 / (1 + np.exp(-logits))
+            err = p * (2.0 ** -22 + 2 * EPS)
+        else:
+            far = np.minimum(np.abs(logits - np.where(live, logits, -np.inf).max(1, keepdims=True)), 110)
+            e = np.where(live, np.exp(-far), 0)
+            total = e.sum(1, keepdims=True)
+            p = e / total
+            spread = (e * far).sum(1, keepdims=True) / total
+            err = p * ((far + spread) * EPS + 2 * 2.0 ** -22 + (logits.shape[1] / 32 + 7) * EPS)
+        score = p + bias
+        return score, err + np.abs(score) * EPS + 2.0 ** -126, live & (score > -np.inf)
+
+
+def check_scored(i2s, logits, k, bias, factor=1.0, sigmoid=False, norm=False):
+    call = i2s.RouteTopk(logits, k, bias=dev(bias), bias_on="score", factor=factor, sigmoid=sigmoid, norm=norm)
+    call.expert.fill_(77)
+    call()
+    values = logits.double().cpu().numpy()
+    got, weight = call.expert.cpu().numpy(), call.weight.double().cpu().numpy()
+    score, err, live = scores(values, bias.astype(np.float64), sigmoid)
+    rows, experts = values.shape
+    assert ((got >= 0).sum(1) == np.minimum(live.sum(1), k)).all()
+    left, at = live.copy(), np.arange(rows)
+    for j in range(k):
+        e, has = got[:, j], got[:, j] >= 0
+        assert (has | ~left.any(1)).all()
+        assert left[at[has], e[has]].all()   # live, and not chosen before
+        best = np.where(left, score - err, -np.inf).max(1)
+        assert (score[at[has], e[has]] + err[at[has], e[has]] >= best[has]).all()
+        left[at[has], e[has]] = False
+    # the weights are those of the chosen, without the bias
+    masked = np.where((values > -np.inf) & (values + bias > -np.inf), values, -np.inf)
+    v = np.where(got >= 0, np.take_along_axis(values, np.maximum(got, 0), 1), -np.inf)
+    with np.errstate(all="ignore"):
+        if sigmoid:
+            want = 1 / (1 + np.exp(-v))
+            want = want / want.sum(1, keepdims=True) if norm else want
+            size = 0
+        else:
+            base = v if norm else masked
+            top = base.max(1, keepdims=True)
+            want, size = np.exp(v - top) / np.exp(base - top).sum(1, keepdims=True), np.where(got >= 0, np.abs(v - top), 0)
+    want = np.where(got >= 0, want * factor, 0)
+    bound = 2 * (size + experts / 32 + k + 24) * EPS * np.abs(want) + 2.0 ** -126
+    assert (np.abs(weight - want) <= bound).all()
+    start, items = ref.plan(got.reshape(-1), experts)
+    assert call.plan.start.cpu().tolist() == start.tolist()
+    assert call.plan.list.cpu().tolist()[:len(items)] == items.tolist()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("rows,experts,k", [(1, 8, 2), (7, 33, 4), (48, 128, 8), (130, 60, 16), (300, 256, 8), (65, 1000, 16), (1003, 60, 4)])
+def test_route_by_biased_score(i2s, dtype, rows, experts, k):
+    rng = np.random.default_rng(rows + experts)
+    logits = dev(rng.normal(0, 2, (rows, experts)), dtype)
+    for scale in (0.3, 0.01):
+        bias = rng.normal(0, scale, experts).astype(np.float32)
+        for sigmoid in (False, True):
+            for norm in (False, True):
+                check_scored(i2s, logits, k, bias, 2.5 if norm else 1.0, sigmoid, norm)
+
+
+@pytest.mark.parametrize("sigmoid,logits,bias", [(True, [4.0, 1.0], [0.0, 0.5]), (False, [2.0, 1.0], [0.0, 0.5])])
+def test_route_where_the_two_choices_differ(i2s, sigmoid, logits, bias):
+    """By hand: sigmoid 0.982 + 0 and 0.731 + 0.5; softmax 0.731 + 0 and 0.269 + 0.5. The logits with the bias say the first
+    expert, the scores the second."""
+    x, b = dev(np.array([logits], np.float32)), dev(np.array(bias, np.float32))
+    by = {on: i2s.route_topk(x, 1, bias=b, bias_on=on, sigmoid=sigmoid) for on in ("logit", "score")}
+    assert by["logit"][0].tolist() == [[0]] and by["score"][0].tolist() == [[1]]
+    want = 1 / (1 + np.exp(-1.0)) if sigmoid else np.exp(1) / (np.exp(2) + np.exp(1))
+    assert abs(by["score"][1].item() - want) < 1e-6
+    assert by["score"][2].start.tolist() == [0, 0, 1]
+
+
+@pytest.mark.parametrize("rows", [6, 200])
+def test_route_by_biased_score_masks_and_ties(i2s, rows):
+    rng = np.random.default_rng(5)
+    x = rng.normal(0, 1, (rows, 40)).astype(np.float32)
+    x[0], x[1], x[2, 3:], x[3] = -np.inf, np.nan, -np.inf, 0.5
+    x[4] = np.linspace(-120, 120, 40)
+    bias = rng.normal(0, 0.2, 40).astype(np.float32)
+    bias[5], bias[6] = -np.inf, np.nan
+    for sigmoid in (False, True):
+        for norm in (False, True):
+            check_scored(i2s, dev(x), 4, bias, sigmoid=sigmoid, norm=norm)
+            zero = i2s.route_topk(dev(x), 4, bias=torch.zeros(40, device="cuda"), bias_on="score", sigmoid=sigmoid, norm=norm)
+            assert zero[0][3].tolist() == [0, 1, 2, 3]   # equal scores, by index
+            none = i2s.route_topk(dev(x), 4, bias_on="score", sigmoid=sigmoid, norm=norm)   # no bias: by the logits
+            assert torch.equal(none[0], i2s.route_topk(dev(x), 4, sigmoid=sigmoid, norm=norm)[0])
+    x[5, 7] = np.inf
+    e, w, _ = i2s.route_topk(dev(x), 4, bias=dev(bias), bias_on="score")
+    assert e[5].tolist() == [-1] * 4 and (w[5] == 0).all() and torch.isfinite(w).all()
+    e, w, _ = i2s.route_topk(dev(x), 4, bias=torch.zeros(40, device="cuda"), bias_on="score", sigmoid=True)
+    assert e[5, 0].item() == 7 and w[5, 0].item() == 1
