@@ -818,7 +818,7 @@ int route_plan_build(const int32_t* owner, const route_plan* plan, void* ws, siz
  *   exp(l - m) / sum_e exp(l_e - m), the softmax over all the row's logits (without the
  *       bias), or with ROUTE_NORM over those of the chosen;
  *   1 / (1 + exp(-l)) with ROUTE_SIGMOID, and with ROUTE_NORM that divided by
- *       the sum over the chosen (zero where that sum is zero).
+ *       the sum over the chosen (zero where all of them are zero in binary32, logits below about -104).
  * An expert whose score or logit + bias[e] is -infinity or NaN (a masked one) is never chosen, and such
  * logits add nothing to a softmax: where fewer than k are left, the items behind them have the
  * expert -1 and the weight 0. A logit of +infinity makes the weights of its row's softmax

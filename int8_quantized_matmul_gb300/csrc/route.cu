@@ -120,6 +120,13 @@ __device__ __forceinline__ void topk_row(const TopkArgs& a, int row, int lane) {
     if (a.sigmoid) {
         w = mine >= 0 ? sigmoid_of(v) : 0.0f;
         if (a.norm) {
+            // Far below zero exp(-v) leaves binary32's range (from -88.8 on) while the quotient of two sigmoids does not:
+            // all are then taken exp(-best) times as large, unless the best itself is zero in binary32.
+            if (__any_sync(0xffffffffu, mine >= 0 && v < -80.0f)) {
+                const float best = fminf(warp_max(v), 0.0f);
+                if (expf(best) == 0.0f) w = 0.0f;
+                else if (mine >= 0 && v < 0.0f) w = __fdiv_rn(expf(v - best), __fadd_rn(1.0f, expf(v)));
+            }
             const float all = warp_add(w);
             w = all == 0.0f ? 0.0f : __fdiv_rn(w, all);
         }

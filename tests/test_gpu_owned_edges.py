@@ -205,3 +205,24 @@ def test_route_by_biased_score_masks_and_ties(i2s, rows):
     assert e[5].tolist() == [-1] * 4 and (w[5] == 0).all() and torch.isfinite(w).all()
     e, w, _ = i2s.route_topk(dev(x), 4, bias=torch.zeros(40, device="cuda"), bias_on="score", sigmoid=True)
     assert e[5, 0].item() == 7 and w[5, 0].item() == 1
+
+
+@pytest.mark.parametrize("bias_on", ["logit", "score"])
+def test_route_sigmoids_far_below_zero(i2s, bias_on):
+    """Normed sigmoids of logits from which exp(-l) is beyond binary32: their quotients are ordinary numbers. By hand: chosen
+    -88 and -89.5 weigh 1 / (1 + exp(-1.5)) = 0.818 and 0.182; below -104 all are zero."""
+    x = torch.tensor([[-88.0, -89.5, -95.0], [-95.0, -95.0, -200.0], [-103.0, -102.0, -1000.0], [-60.0, -89.0, -120.0],
+                      [3.0, -89.0, -1.0], [-79.0, -81.0, -83.0], [0.0, -90.0, -90.0], [-200.0, -300.0, -float("inf")]], device="cuda")
+    for dtype, k, n in ((torch.float32, 2, 1), (torch.float32, 3, 40), (torch.bfloat16, 3, 1)):
+        rows = x.repeat(n, 1).to(dtype)
+        e, w, _ = i2s.route_topk(rows, k, sigmoid=True, norm=True, factor=2.0, bias=torch.zeros(3, device="cuda"), bias_on=bias_on)
+        v = rows.double().cpu().gather(1, e.long().clamp(min=0).cpu())
+        s = torch.where(e.cpu() >= 0, 1 / (1 + torch.exp(-v)), 0)
+        best = torch.where(e.cpu() >= 0, v, -1e30).max(1, keepdim=True).values.clamp(max=0)
+        zero = torch.exp(best).float() == 0   # in binary32
+        want = torch.where(zero, 0, 2 * s / s.sum(1, keepdim=True))
+        # the difference of two logits is rounded once, two exponentials within 2 units, three sums, two quotients
+        err = (w.double().cpu() - want).abs()
+        assert (err <= want * ((v - best).abs() * EPS + 2.0 ** -20) * 2 + 2.0 ** -126).all(), (err, want)
+    a, b = i2s.route_topk(x[:1], 2, sigmoid=True, norm=True)[1][0].tolist()
+    assert abs(a - 0.8175745) < 1e-6 and abs(b - 0.1824255) < 1e-6
