@@ -817,9 +817,8 @@ __global__ void __launch_bounds__(kRowThreads) k_expert_rows(const __grid_consta
 // y[t][n] = sum_j weight[t][j] * d[t * group + j][n], j ascending, each product
 // and sum rounded once; items without an expert add nothing. V neighbouring values to a thread; eight items' loads at once.
 template <int V>
-__global__ void __launch_bounds__(256) k_expert_sum(const float* __restrict__ d, const float* __restrict__ weight,
-                                                    const uint8_t* __restrict__ used, int group, int N, int rows, void* y,
-                                                    long long y_stride, int y_dtype, bool vec) {
+__global__ void __launch_bounds__(256) k_expert_sum(const float* d, const float* weight, const uint8_t* used, int group, int N,
+                                                    int rows, void* y, long long y_stride, int y_dtype, bool vec) {
     const int per = N / V;
     pdl_wait();
     // a block's threads have neighbours of one row, or of a few

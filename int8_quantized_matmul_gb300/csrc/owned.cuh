@@ -104,6 +104,9 @@ __device__ __forceinline__ int owner_of_tile(const int* tile0, int owners, int t
     return lo;
 }
 
+// What an earlier launch may have written is read by plain or L2 loads where its address is known before pdl_wait: a load of
+// data that is declared never to change (__ldg, __restrict__ of inputs) may be moved ahead of the wait.
+//
 // Starts the launches that wait on this one (their griddepcontrol.wait still
 // waits for all of it): their own set-up then runs beside this kernel.
 __device__ __forceinline__ void pdl_launch_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }

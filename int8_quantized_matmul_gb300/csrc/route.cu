@@ -70,7 +70,7 @@ __device__ __forceinline__ void topk_row(const TopkArgs& a, int row, int lane) {
     for (int i = 0; i < VPL; ++i) {
         const int e = lane + 32 * i;
         float s = l[i];
-        if (a.bias != nullptr && e < a.experts) s = __fadd_rn(s, __ldg(a.bias + e));
+        if (a.bias != nullptr && e < a.experts) s = __fadd_rn(s, a.bias[e]);
         s = __fadd_rn(s, 0.0f);   // one zero
         const uint32_t bits = __float_as_uint(s);
         const bool live = s > -INFINITY;   // not NaN either
@@ -289,7 +289,7 @@ __global__ void __launch_bounds__(kThreads) k_route_topk(TopkArgs a, int per, in
     for (int i = threadIdx.x; i < a.experts; i += kThreads) counts[blockIdx.x * a.experts + i] = n[i];
 }
 
-__global__ void __launch_bounds__(kThreads) k_plan_count(const int* __restrict__ owner, int items, int owners, int per, int* counts) {
+__global__ void __launch_bounds__(kThreads) k_plan_count(const int* owner, int items, int owners, int per, int* counts) {
     __shared__ int n[kMaxOwners];
     pdl_wait();
     pdl_launch_next();

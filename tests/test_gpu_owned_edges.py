@@ -226,3 +226,30 @@ def test_route_sigmoids_far_below_zero(i2s, bias_on):
         assert (err <= want * ((v - best).abs() * EPS + 2.0 ** -20) * 2 + 2.0 ** -126).all(), (err, want)
     a, b = i2s.route_topk(x[:1], 2, sigmoid=True, norm=True)[1][0].tolist()
     assert abs(a - 0.8175745) < 1e-6 and abs(b - 0.1824255) < 1e-6
+
+
+def test_router_sees_the_bias_and_the_weights_of_the_launch_before(i2s):
+    """A bias, owners and a sum's weights that are rewritten right before each call, many times without a wait between."""
+    n, rows, E, N, K = 60, 300, 24, 64, 64
+    rng = np.random.default_rng(1)
+    x, biases = torch.zeros((rows, E), device="cuda"), dev(rng.permuted(np.tile(np.arange(E, dtype=np.float32), (n, 1)), axis=1))
+    owners, gates = dev(rng.integers(0, E, (n, 5000)).astype(np.int32)), dev(rng.integers(1, 9, (n, rows, 1)).astype(np.float32))
+    bias, owner, gate = torch.empty(E, device="cuda"), torch.empty(5000, dtype=torch.int32, device="cuda"), torch.empty((rows, 1), device="cuda")
+    wq, bscale = torch.full((E, N, K), 1, dtype=torch.int8, device="cuda"), torch.ones((E, N), device="cuda")
+    ones = torch.ones((rows, K), device="cuda")
+    route, build = i2s.RouteTopk(x, 1, bias=bias), i2s.RouteBuild(owner, E)
+    total = i2s.W8A8Experts(wq, bscale, route.plan, ones, weight=gate)
+    unit = i2s.w8a8_mul_mat_experts(wq, bscale, i2s.route_plan(torch.zeros(rows, dtype=torch.int32, device="cuda"), E), ones)[0, 0]
+    seen = []
+    for i in range(n):
+        bias.copy_(biases[i])
+        owner.copy_(owners[i])
+        gate.copy_(gates[i])
+        route()
+        total()
+        build()
+        seen.append((route.expert.clone(), total.out.clone(), build.plan.start.clone()))
+    for i, (e, y, start) in enumerate(seen):
+        assert (e == biases[i].argmax()).all()
+        assert torch.equal(y, (gates[i] * unit).expand(rows, N))
+        assert start.diff().tolist() == torch.bincount(owners[i].long(), minlength=E).tolist()
