@@ -851,7 +851,8 @@ int route_topk(const i2s_rows* logits, int64_t rows, int experts, int k, const f
  * plan   owners = experts; items a multiple of x_group and of y_group (a token's k choices share
  *        a row of x: x_group = k; they are summed: y_group = k).
  * x      vector rows, items/x_group x K. y: items/y_group x N (or N/2).
- * ws     device workspace of w8a8_mul_mat_experts_workspace() bytes; its first word is the status
+ * ws     device workspace of w8a8_mul_mat_experts_workspace() bytes (without W8A8_SWIGLU enough for a weighted sum, items x N
+ *        F32 values, whether there is one or not); its first word is the status
  *        word that i2s_read_status reads (a wait that ran out; y is then incomplete).
  * Requirements: K % 16 == 0, K <= 65536, experts*N < 2^31, experts <= ROUTE_MAX_OWNERS; N % 32 == 0
  * with W8A8_SWIGLU, which takes no weight. W8A8_TEST_STALL is for tests only: products never come, waits run out. */

@@ -886,14 +886,15 @@ struct Layout {
     size_t ascale, q, used, place, d, total;
 };
 
-Layout layout_of(int64_t items, int64_t N, int64_t K) {
+// What the form may need: places of rows that several items read, F32 rows and who has some for a weighted sum.
+Layout layout_of(int64_t items, int64_t N, int64_t K, int x_group, bool swiglu) {
     Layout l;
     l.ascale = 256;   // the status word and the counter before it
     l.q = l.ascale + up_256((size_t)items * 4);
-    l.used = l.q + up_256((size_t)items * K * 2);
-    l.place = l.used + up_256((size_t)items);
-    l.d = l.place + up_256((size_t)items * 4);
-    l.total = l.d + up_256((size_t)items * N * 4);
+    l.place = l.q + up_256((size_t)items * K * 2 + 128);   // the last row's copy reaches up to 96 bytes behind it
+    l.used = l.place + (x_group > 1 ? up_256((size_t)items * 4) : 0);
+    l.d = l.used + (swiglu ? 0 : up_256((size_t)items));
+    l.total = l.d + (swiglu ? 0 : up_256((size_t)items * N * 4));
     return l;
 }
 
@@ -961,7 +962,7 @@ extern "C" {
 size_t w8a8_mul_mat_experts_workspace(const w8a8_experts* w, const route_plan* plan, int x_group, int y_group,
                                       unsigned flags) {
     if ((flags & ~(W8A8_SWIGLU | W8A8_TEST_STALL)) || check_sizes(w, plan, x_group, y_group, (flags & W8A8_SWIGLU) != 0)) return 0;
-    return layout_of(plan->items, w->N, w->K).total;
+    return layout_of(plan->items, w->N, w->K, x_group, (flags & W8A8_SWIGLU) != 0).total;
 }
 
 int w8a8_mul_mat_experts(const w8a8_experts* w, const route_plan* plan, const i2s_rows* x, int x_group, const i2s_rows* y,
@@ -977,7 +978,7 @@ int w8a8_mul_mat_experts(const w8a8_experts* w, const route_plan* plan, const i2
     if ((r = check_row_tensor(x, x_rows, w->K, true, false)) || (r = check_row_tensor(y, y_rows, out, false, true))) return r;
     if (((uintptr_t)w->wq & 15) || ((uintptr_t)w->bscale & 3) || ((uintptr_t)weight & 3) || ((uintptr_t)ws & 255))
         return I2S_E_MISALIGNED;
-    const Layout l = layout_of(items, w->N, w->K);
+    const Layout l = layout_of(items, w->N, w->K, x_group, swiglu);
     const size_t need = l.total;
     if (ws_bytes < need) return I2S_E_WORKSPACE_TOO_SMALL;
     const Span sw = span_of(w->wq, (size_t)w->experts * w->N * w->K), sb = span_of(w->bscale, (size_t)w->experts * w->N * 4);
@@ -1016,7 +1017,7 @@ int w8a8_mul_mat_experts(const w8a8_experts* w, const route_plan* plan, const i2
     const bool few = items <= 16 * (int64_t)w->experts;
     const int rows = few ? 32 : 128;
     // (position of a block of 64, row, block): the last block may reach into the next row, or past the last into
-    // the workspace behind it; no MMA reads that
+    // the bytes that layout_of leaves behind it; no MMA reads that
     const cuuint64_t xdims[3] = {64, (cuuint64_t)items, (K + 63) / 64}, xstrides[2] = {K * 2, 128};
     for (int i = 0; i < 4; ++i) {
         const cuuint32_t xbox[3] = {64, (cuuint32_t)(rows / 4 * (i + 1)), 2};

@@ -21,3 +21,19 @@ def test_flags_of_the_router(i2s):
     assert i2s.ROUTE_BIAS_SCORE == 8
     with pytest.raises(ValueError, match="bias_on"):
         i2s.RouteTopk(torch.zeros(4, 4), 2, bias_on="logits")
+
+
+@pytest.mark.parametrize("items,x_group,N,K", [(32768, 8, 1536, 2048), (20, 2, 64, 48), (1, 1, 32, 16), (256, 1, 4096, 1040)])
+def test_workspace_of_the_products_by_form(i2s, items, x_group, N, K):
+    """Codes of the rows with the 128 bytes behind the last that a copy may read, scales, and what the form needs besides: the
+    gate has no F32 rows, a row of its own per item no places."""
+    c = Call(i2s)
+    c.w.N, c.w.K, c.plan.items = N, K, items
+    need = lambda flags: c.L.w8a8_mul_mat_experts_workspace(c.w, c.plan, x_group, 1, flags)
+    least = 256 + items * (2 * K + 4) + 128 + (4 * items if x_group > 1 else 0)
+    assert least <= need(1) <= least + 3 * 256
+    more = items * (4 * N + 1)
+    assert least + more <= need(0) <= least + more + 5 * 256
+    c.x_group, c.ws_bytes, c.flags = x_group, need(1) - 1, 1
+    c.x.stride, c.y.stride = K, N
+    assert c.product() == c.E["I2S_E_WORKSPACE_TOO_SMALL"]
