@@ -5,6 +5,7 @@ import numpy as np
 import pytest
 
 from tests import owned_reference as ref
+from tests.test_gpu_guard import Guarded
 
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
@@ -253,3 +254,85 @@ def test_router_sees_the_bias_and_the_weights_of_the_launch_before(i2s):
         assert (e == biases[i].argmax()).all()
         assert torch.equal(y, (gates[i] * unit).expand(rows, N))
         assert start.diff().tolist() == torch.bincount(owners[i].long(), minlength=E).tolist()
+
+
+# -- guard bands around outputs and workspaces ---------------------------------------------------------
+
+@pytest.mark.parametrize("rows,experts,k", [(1, 8, 2), (48, 33, 4), (131, 60, 3), (700, 1000, 5), (2049, 128, 8)])
+def test_router_and_plans_stay_in_their_buffers(i2s, rows, experts, k):
+    rng = np.random.default_rng(rows)
+    logits = dev(rng.normal(0, 1, (rows, experts)).astype(np.float32))
+    logits[rows // 2, 1:] = -np.inf
+    items = rows * k
+    g = {"expert": Guarded(4 * items), "weight": Guarded(4 * items), "start": Guarded(4 * (experts + 1)), "list": Guarded(4 * items),
+         "ws": Guarded(i2s.lib.route_plan_workspace(items, experts))}
+    i32 = lambda n: g[n].buf.view(torch.int32)
+    plan = i2s.RoutePlan(items, experts, start=i32("start"), list=i32("list"))
+    for bias, bias_on in ((None, "logit"), (torch.zeros(experts, device="cuda"), "score")):
+        i2s.route_topk(logits, k, bias=bias, bias_on=bias_on, plan=plan, ws=g["ws"].buf, expert=i32("expert"), weight=g["weight"].f32(items))
+        owner = i32("expert").clone()
+        want = ref.plan(owner.cpu().numpy(), experts)
+        for _ in range(2):   # the router's plan, then that of its experts
+            assert plan.start.cpu().tolist() == want[0].tolist()
+            assert plan.list.cpu().tolist()[:len(want[1])] == want[1].tolist()
+            i2s.route_plan(owner, experts, plan=plan, ws=g["ws"].buf)
+        for name, buf in g.items():
+            buf.check(f"{name}, {rows} rows of {experts} experts")
+
+
+@pytest.mark.parametrize("rows,k,E,N,K", [(1, 2, 8, 64, 48), (70, 3, 5, 160, 1040), (9, 1, 3, 96, 16), (600, 4, 7, 288, 208),
+                                          (520, 8, 16, 64, 2064)])
+@pytest.mark.parametrize("form", ["plain", "up", "down", "rows"])
+def test_expert_products_stay_in_their_buffers(i2s, rows, k, E, N, K, form):
+    """up: gate and up; down: weighted sums of rows of their own; rows: weighted sums of shared rows. The workspace is as large as
+    the query says and no larger."""
+    rng = np.random.default_rng(N + K)
+    wq, bscale = rng.integers(-127, 128, (E, N, K)).astype(np.int8), np.exp(rng.normal(0, 0.3, (E, N))).astype(np.float32) * np.float32(1e-3)
+    owner = rng.integers(-1, E, rows * k).astype(np.int32)
+    x_group = 1 if form == "down" else k
+    x = rng.normal(0, 1, (rows * k // x_group, K)).astype(np.float32)
+    gate = rng.normal(0, 1, (rows, k)).astype(np.float32)
+    weighted = form in ("down", "rows")
+    plan = i2s.route_plan(dev(owner), E)
+    w, d = dev(wq), ref.dots(wq, bscale, owner, x, x_group)
+    struct = i2s.w8a8_experts(w.data_ptr(), w.data_ptr(), N, K, E)
+    ws = Guarded(i2s.lib.w8a8_mul_mat_experts_workspace(struct, plan.struct, x_group, k if weighted else 1, 1 if form == "up" else 0))
+    shape = (rows if weighted else rows * k, N // 2 if form == "up" else N)
+    y = Guarded(4 * shape[0] * shape[1])
+    y.buf.zero_()
+    ws.buf.fill_(0xff)   # whatever it holds before
+    out = i2s.w8a8_mul_mat_experts(w, dev(bscale), plan, dev(x), out=y.f32(*shape), x_group=x_group, swiglu=form == "up",
+                                   weight=dev(gate) if weighted else None, ws=ws.buf)
+    y.check("y")
+    ws.check("workspace")
+    got = out.cpu().numpy()
+    if form == "up":
+        want = np.where((owner >= 0)[:, None], ref.swiglu(d), 0)
+        assert (np.abs(got - want) <= 2.0 ** -20 * np.abs(want) + ref.swiglu_floor(d)).all()
+    else:
+        want = ref.weighted(d, owner, E, gate) if weighted else d
+        assert np.array_equal(got, want)
+
+
+@pytest.mark.parametrize("rows,adapters,rank,N,K", [(1, 1, 8, 33, 72), (64, 40, 32, 300, 520), (131, 3, 128, 511, 2056), (700, 5, 64, 264, 136)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.float16, torch.bfloat16])
+def test_adapters_stay_in_their_buffers(i2s, rows, adapters, rank, N, K, dtype):
+    rng = np.random.default_rng(rank)
+    half = torch.float16 if dtype == torch.float16 else torch.bfloat16
+    A, B = dev(rng.integers(-1, 2, (adapters, rank, K)), half), dev(rng.integers(-1, 2, (adapters, N, rank)), half)
+    x, base = dev(rng.integers(-1, 2, (rows, K)), dtype), dev(rng.integers(-8, 9, (rows, N)), dtype)
+    owner = dev(rng.integers(-1, adapters, rows).astype(np.int32))
+    plan = i2s.route_plan(owner, adapters)
+    struct = i2s.lora_adapters(A.data_ptr(), B.data_ptr(), None, K, N, rank, adapters, 1 if half == torch.float16 else 2)
+    ws, out = Guarded(i2s.lib.lora_add_workspace(struct, plan.struct)), Guarded(x.element_size() * rows * N)
+    y = out.buf.view(dtype).view(rows, N)
+    y.fill_(3)
+    ws.buf.fill_(0xff)
+    i2s.lora_add(A, B, plan, x, base, out=y, ws=ws.buf)
+    out.check("out")
+    ws.check("workspace")
+    for a in range(-1, adapters):
+        at = owner == a
+        # whole numbers: every sum is exact in 32 bits, and rounded once
+        want = base[at].double() + (x[at].double() @ A[a].double().T) @ B[a].double().T if a >= 0 else torch.full_like(y[at], 3).double()
+        assert torch.equal(y[at], want.float().to(dtype))
