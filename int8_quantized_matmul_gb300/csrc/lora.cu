@@ -183,19 +183,39 @@ __global__ void __launch_bounds__(kThreads) k_lora_inner(const __grid_constant__
         for (int n = 0; n < NT; ++n) b[n] = bw[n];
         k += kWarps * 32;
         load(k);
+        // F32 rows: a sum of its own for each 32 positions, small parts first, added to the others with rounding. The tensor
+        // core cuts off what it adds below the sum so far: six MMAs of a sum that lasts for all of K lose as many bits as K is
+        // long (3000 rows of 8960 of one sign, rank 64: 1.3e-5 of t, so 1.2e-7; plain binary32 1.2e-7; the 8000-row prompt takes
+        // 65.6 us for 64.3, rank 16 44.8 for 52.6). 16-bit rows: one pair of MMAs where F32 has three, and outputs whose half
+        // step is 2^-8 or 2^-11: a sum for all of K, which loses 6e-6 of 8960 values of one sign and 5e-5 of 65536 (3000 bf16
+        // rows of 8960, rank 64: 51 us, 59.5 with sums of their own).
+        constexpr bool kOwnSums = DT == kF32;
+        constexpr int kG = NT < 4 ? NT : 4;   // sums at a time, whose MMAs do not wait for each other
 #pragma unroll
-        for (int p = W::kXParts - 1; p >= 0; --p)
+        for (int m = 0; m < kMt; ++m) {
+            if (m > 0 && !two) break;
 #pragma unroll
-            for (int m = 0; m < kMt; ++m) {
-                if (m > 0 && !two) break;
-                const uint32_t a0[4] = {ap[2 * m][p][0], ap[2 * m + 1][p][0], ap[2 * m][p][1], ap[2 * m + 1][p][1]};
-                const uint32_t a1[4] = {ap[2 * m][p][2], ap[2 * m + 1][p][2], ap[2 * m][p][3], ap[2 * m + 1][p][3]};
+            for (int n0 = 0; n0 < NT; n0 += kG) {
+                float own[kG][4] = {};
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    mma16816<W::kF16Mma>(acc[m][n], a0, b[n].x, b[n].y);
-                    mma16816<W::kF16Mma>(acc[m][n], a1, b[n].z, b[n].w);
+                for (int p = W::kXParts - 1; p >= 0; --p) {
+                    const uint32_t a0[4] = {ap[2 * m][p][0], ap[2 * m + 1][p][0], ap[2 * m][p][1], ap[2 * m + 1][p][1]};
+                    const uint32_t a1[4] = {ap[2 * m][p][2], ap[2 * m + 1][p][2], ap[2 * m][p][3], ap[2 * m + 1][p][3]};
+#pragma unroll
+                    for (int n = 0; n < kG; ++n)
+                        mma16816<W::kF16Mma>(kOwnSums ? own[n] : acc[m][n0 + n], a0, b[n0 + n].x, b[n0 + n].y);
+#pragma unroll
+                    for (int n = 0; n < kG; ++n)
+                        mma16816<W::kF16Mma>(kOwnSums ? own[n] : acc[m][n0 + n], a1, b[n0 + n].z, b[n0 + n].w);
+                }
+                if (kOwnSums) {
+#pragma unroll
+                    for (int n = 0; n < kG; ++n)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) acc[m][n0 + n][i] = __fadd_rn(acc[m][n0 + n][i], own[n][i]);
                 }
             }
+        }
     }
     constexpr int kRow = 8 * NT;
 #pragma unroll

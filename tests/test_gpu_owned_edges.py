@@ -336,3 +336,27 @@ def test_adapters_stay_in_their_buffers(i2s, rows, adapters, rank, N, K, dtype):
         # whole numbers: every sum is exact in 32 bits, and rounded once
         want = base[at].double() + (x[at].double() @ A[a].double().T) @ B[a].double().T if a >= 0 else torch.full_like(y[at], 3).double()
         assert torch.equal(y[at], want.float().to(dtype))
+
+
+# -- an adapter's long sums --------------------------------------------------------------------------
+
+@pytest.mark.parametrize("rows,K,steps", [(3000, 2048, 8), (3000, 8960, 35), (64, 65536, 32)])
+@pytest.mark.parametrize("rank", [16, 64])
+def test_lora_long_sums_of_one_sign(i2s, rows, K, steps, rank):
+    """t over long K, all products positive, B picking one of t. Of 32 positions six MMAs cut off up to 5 units of 2^-24 each;
+    a warp then adds `steps` such sums, a CTA eight warps', up to eight CTAs theirs, each rounded: (30 + steps + 16) * 2^-24 of t.
+    One chain over all of K lost 1.2e-5 of the two longer ones."""
+    adapters, N = 4, 264
+    g = torch.Generator(device="cuda").manual_seed(K)
+    A = torch.rand(adapters, rank, K, device="cuda", generator=g).bfloat16()
+    x = torch.rand(rows, K, device="cuda", generator=g)
+    own = torch.randint(0, adapters, (rows,), device="cuda", generator=g, dtype=torch.int32)
+    B = torch.zeros(adapters, N, rank, device="cuda")
+    B[:, torch.arange(N), torch.arange(N) % rank] = 1
+    zero = torch.zeros(rows, N, device="cuda")
+    out = i2s.lora_add(A, B.bfloat16(), i2s.route_plan(own, adapters), x, zero, out=torch.empty_like(zero))
+    for a in range(adapters):
+        at = own == a
+        t = (x[at].double() @ A[a].double().T)[:, torch.arange(N) % rank]
+        err = (out[at].double() - t).abs() / t
+        assert err.max() <= (30 + steps + 16) * 2.0 ** -24, err.max().item() * 2 ** 24
