@@ -338,7 +338,58 @@ def test_adapters_stay_in_their_buffers(i2s, rows, adapters, rank, N, K, dtype):
         assert torch.equal(y[at], want.float().to(dtype))
 
 
-# -- an adapter's long sums --------------------------------------------------------------------------
+# -- what the parts of an adapter's F32 rows carry -----------------------------------------------------
+
+def full_values(rows, K, seed):
+    """F32 values with 24 bits each, of many sizes."""
+    rng = np.random.default_rng(seed)
+    m = rng.integers(1 << 23, 1 << 24, (rows, K)) | 1
+    return (m * np.exp2(rng.integers(-60, 30, (rows, K))) * rng.choice([-1, 1], (rows, K))).astype(np.float32)
+
+
+def three_bytes(rows, seed):
+    """Rows of three whole numbers of 8 bits each, 2^16 a + 2^8 b + c, whose sum has 24."""
+    rng = np.random.default_rng(seed)
+    v = rng.integers(128, 256, (rows, 3)) | 1
+    return (v * np.array([1 << 16, 1 << 8, 1]) * rng.choice([-1, 1], (rows, 1))).astype(np.float32)
+
+
+def in_parts(x, parts):
+    """The sum of a value's bf16 parts, high bits first, each cut off."""
+    left, total = x.astype(np.float32), np.zeros_like(x, np.float64)
+    for _ in range(parts):
+        part = (left.view(np.uint32) & np.uint32(0xffff0000)).view(np.float32)
+        total, left = total + part, (left - part).astype(np.float32)
+    return total
+
+
+@pytest.mark.parametrize("rank", [8, 32, 64, 128])
+@pytest.mark.parametrize("rows", [1, 50, 3000])
+def test_lora_rows_and_inner_vector_keep_24_bits(i2s, rank, rows):
+    """A and B pick one value each (a power of two): out is x's value bit for bit, through the parts of x and of the inner vector;
+    then a sum of three positions of 8 bits, which only the inner vector holds in 24."""
+    K, N, adapters = 520, 264, 3
+    rng = np.random.default_rng(rank + rows)
+    own = rng.integers(0, adapters, rows).astype(np.int32)
+    plan = i2s.route_plan(dev(own), adapters)
+    at = rng.integers(0, K, (adapters, rank))
+    A, B = np.zeros((adapters, rank, K), np.float32), np.zeros((adapters, N, rank), np.float32)
+    for a in range(adapters):
+        A[a, np.arange(rank), at[a]] = 4
+        B[a, np.arange(N), np.arange(N) % rank] = 0.5
+    x = full_values(rows, K, rank)
+    zero = torch.zeros((rows, N), device="cuda")
+    out = i2s.lora_add(dev(A).bfloat16(), dev(B).bfloat16(), plan, dev(x), zero, out=torch.empty_like(zero)).cpu().numpy()
+    want = 2 * x[np.arange(rows)[:, None], at[own][:, np.arange(N) % rank]]
+    assert np.array_equal(out, want)
+    for a in range(adapters):
+        A[a] = 0
+        A[a, :, 100:103] = 1
+    x = np.zeros((rows, K), np.float32)
+    x[:, 100:103] = three_bytes(rows, rank)
+    out = i2s.lora_add(dev(A).bfloat16(), dev(B).bfloat16(), plan, dev(x), zero, out=torch.empty_like(zero)).cpu().numpy()
+    assert np.array_equal(out, np.repeat(x.sum(1, keepdims=True) * np.float32(0.5), N, 1))
+
 
 @pytest.mark.parametrize("rows,K,steps", [(3000, 2048, 8), (3000, 8960, 35), (64, 65536, 32)])
 @pytest.mark.parametrize("rank", [16, 64])

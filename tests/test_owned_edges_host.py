@@ -2,9 +2,11 @@
 
 Addresses are made up: the file runs only where there is no GPU to launch on."""
 
+import numpy as np
 import pytest
 import torch
 
+from tests.test_gpu_owned_edges import full_values, in_parts, three_bytes
 from tests.test_owned_host import Call, i2s, refused  # noqa: F401 (a fixture)
 
 pytestmark = pytest.mark.skipif(torch.cuda.is_available(), reason="made-up addresses: only without a GPU")
@@ -37,3 +39,13 @@ def test_workspace_of_the_products_by_form(i2s, items, x_group, N, K):
     c.x_group, c.ws_bytes, c.flags = x_group, need(1) - 1, 1
     c.x.stride, c.y.stride = K, N
     assert c.product() == c.E["I2S_E_WORKSPACE_TOO_SMALL"]
+
+
+def test_values_that_show_a_missing_part(i2s):
+    """The rows of the test of 24 bits come out whole of three bf16 parts, and of two not one in a hundred does."""
+    x = full_values(300, 520, 1)
+    t = three_bytes(3000, 1).sum(1)
+    for v in (x, t):
+        assert np.array_equal(in_parts(v, 3), v.astype(np.float64))
+        assert (in_parts(v, 2) == v).mean() < 0.01
+    assert np.array_equal(in_parts(three_bytes(3000, 1), 1), three_bytes(3000, 1))   # the positions have 8 bits each
