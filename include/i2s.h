@@ -878,7 +878,9 @@ int w8a8_mul_mat_experts(const w8a8_experts* w, const route_plan* plan, const i2
  * exact, and are summed 32 positions at a time: 1.2e-7 to 1.8e-7 of B (A x), for K up to 65536, of one sign or of both. With
  * 16-bit rows the inner vector has two parts of their type (18 bits in bf16; 22 in f16, scaled by a power of two), and the
  * tensor cores cut its sums off towards zero: 6e-6 of 8960 values of one sign, 5e-5 of 65536, beside the half step of out,
- * 2^-8 in bf16 and 2^-11 in f16.
+ * 2^-8 in bf16 and 2^-11 in f16. An infinity or NaN in a row of x, or an inner product beyond the range, makes that row of
+ * out NaN (where the formula may have an infinity), and no other. F32 rows take bf16 adapters alone: adapters that were trained
+ * in f16 have to be rounded from 11 bits to 8 first.
  * a      A: device, adapters x rank x K; B: device, adapters x N x rank; both of a->dtype (I2S_F16 or
  *        I2S_BF16), 16-byte aligned. scale: device F32 [adapters] or NULL for 1.
  * x      vector rows, rows x K; base, out: rows x N. One dtype: I2S_F32 or I2S_BF16 with adapters of

@@ -297,7 +297,7 @@ __device__ __forceinline__ void put_t(uint16_t* tp, float* s_mul, int r, int q, 
         float m = fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));
 #pragma unroll
         for (int s = 1; s < 8 * KK; s <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, s));
-        // the largest value to 2^13 .. 2^14; infinities stay what they are
+        // the largest value to 2^13 .. 2^14 (an infinity becomes NaN with its second part, as in the other types)
         const int e = min(max((int)(__float_as_uint(m) >> 23) - 127, -100), 127);
         const float by = __int_as_float((127 + 13 - e) << 23);
         mul = __fmul_rn(mul, __int_as_float((127 - 13 + e) << 23));

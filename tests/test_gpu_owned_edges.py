@@ -411,3 +411,22 @@ def test_lora_long_sums_of_one_sign(i2s, rows, K, steps, rank):
         t = (x[at].double() @ A[a].double().T)[:, torch.arange(N) % rank]
         err = (out[at].double() - t).abs() / t
         assert err.max() <= (30 + steps + 16) * 2.0 ** -24, err.max().item() * 2 ** 24
+
+
+def test_lora_rows_that_are_not_finite_stay_alone(i2s):
+    """An infinity or NaN in a row of x, or an inner product beyond binary32, makes that row NaN, and no other."""
+    rows, K, N = 40, 64, 96
+    for dtype in (torch.float32, torch.float16, torch.bfloat16):
+        half = torch.float16 if dtype == torch.float16 else torch.bfloat16
+        A, B = torch.ones(2, 16, K, device="cuda").to(half), torch.ones(2, N, 16, device="cuda").to(half)
+        x = torch.ones(rows, K, device="cuda", dtype=dtype)
+        x[3, 5], x[20, 60], x[21, 0] = float("nan"), float("inf"), -float("inf")
+        bad = [3, 20, 21]
+        if dtype != torch.float16:
+            x[33] = torch.finfo(dtype).max
+            bad.append(33)
+        own = torch.arange(rows, device="cuda", dtype=torch.int32) % 2
+        out = i2s.lora_add(A, B, i2s.route_plan(own, 2), x, torch.zeros(rows, N, device="cuda", dtype=dtype))
+        fine = torch.ones(rows, dtype=torch.bool)
+        fine[bad] = False
+        assert (out.cpu()[fine] == 16 * K).all() and torch.isnan(out.cpu()[~fine]).all()
