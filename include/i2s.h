@@ -883,7 +883,7 @@ int w8a8_mul_mat_experts(const w8a8_experts* w, const route_plan* plan, const i2
  * in f16 have to be rounded from 11 bits to 8 first.
  * a      A: device, adapters x rank x K; B: device, adapters x N x rank; both of a->dtype (I2S_F16 or
  *        I2S_BF16), 16-byte aligned. scale: device F32 [adapters] or NULL for 1.
- * x      vector rows, rows x K; base, out: rows x N. One dtype: I2S_F32 or I2S_BF16 with adapters of
+ * x      vector rows, rows x K; base, out: rows x N, several times faster as vector rows. One dtype: I2S_F32 or I2S_BF16 with adapters of
  *        I2S_BF16, I2S_F16 with adapters of I2S_F16.
  * Requirements: rank a multiple of 8, at most 128; K % 8 == 0, K <= 65536; 1 <= N <= 2^24;
  * adapters <= ROUTE_MAX_OWNERS. Adapters of smaller rank are padded with zeros. */
