@@ -33,8 +33,8 @@
 // finishes one of two neighbouring rows after one exchange.
 //
 // Measured (one GB300). Few rows per expert: 64 tokens over 8 of 128 experts, 1536 x 2048, 51-54 us, 289 MB of weights
-// in use. Many: 4096 bf16 rows of the same 228 us (rows 36, products 194); 1777 F32 rows over 2 of 8, 1536 x 8960: 127 us (rows 32,
-// products 88, sums 8), on the SMs with most units 2.5 for each. A stage of 112 rows takes 840 to
+// in use. Many: 4096 bf16 rows of the same 228 us (rows 35, products 187); 1777 F32 rows over 2 of 8, 1536 x 8960: 127 us (rows 32,
+// products 90, sums 10, each alone), on the SMs with most units 2.5 for each. A stage of 112 rows takes 840 to
 // 940 cycles for 450 of MMAs: shared memory moves about 740 cycles' worth (16 KB of weights in and out, 28 KB of rows in and
 // to the MMA), and without any one of rows, weights, TMEM stores, MMAs or stores of y it takes 94 % or more of the time. CTA
 // pairs, which halve the rows' part, were slower (280 us).
@@ -690,7 +690,8 @@ __global__ void __launch_bounds__(xp::kThreads, 1) k_experts(const __grid_consta
 //
 // COPIES false: a row for each place of the list. true, where several items read a row and there are many: each
 // row of x is quantized once and written to the places of its items, which k_expert_places has put
-// down (4096 bf16 rows of 2048, eight items each: 25 us instead of 62; the launch before it takes 3).
+// down (4096 bf16 rows of 2048, eight items each: 35 us, and 3 the launch before it; the prompt of gate and up took 222 us
+// with it and 245 with a row for each place).
 // ---------------------------------------------------------------------------
 constexpr int kRowThreads = 256, kKeep = 4;
 

@@ -54,7 +54,10 @@
 // leader's accumulator barrier by a remote arrive. TMEM per CTA: two
 // accumulators of 128 columns (the epilogue of one tile overlaps the MMAs of
 // the next), the block scales (64 columns) and the A ring (6 x 32 columns).
-// The issuers all accumulate into the tile's accumulator.
+// The issuers all accumulate into the tile's accumulator. (That no update is lost is
+// what the hardware does, in every comparison with the oracle: PTX orders accumulating
+// MMAs of one thread, and of two with a barrier between tcgen05 fences, and
+// promises nothing about these.)
 //
 // K order: within a 128-position group, element 16w + 8t + 2i + h of the A
 // and B rows holds position 32s + 4w + i, where (t, h) = (0,0), (0,1), (1,0),

@@ -715,7 +715,10 @@ __global__ void __launch_bounds__(kThreadsGv, 2) k_i2s_gemv_tc(const __grid_cons
         // both into the segment's accumulator. Every MMA accumulates; the
         // epilogue zeroes an accumulator after reading it, and the sums are
         // exact integers, so the order in which the two streams land does not
-        // matter. A stage is free again once both issuers have committed.
+        // matter (that no update is lost is what the hardware does, in every
+        // comparison with the oracle; PTX orders accumulating MMAs of one thread, and
+        // of two with a barrier between tcgen05 fences, and promises nothing here).
+        // A stage is free again once both issuers have committed.
         // One wait per stage: a complete full_a implies the activation operand
         // has landed too (the converters waited for it before arriving). The
         // stage's MMAs (two per 128-position group) are unrolled.

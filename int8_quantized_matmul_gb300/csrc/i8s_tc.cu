@@ -38,7 +38,9 @@
 // same ring slot), all into the same accumulator.
 // Every MMA accumulates (the drain zeroes the accumulator after reading it);
 // the partial sums are exact integers, so the order in which the four
-// streams land does not matter.
+// streams land does not matter. (That no update is lost is what the hardware does, in every
+// comparison with the oracle: PTX orders accumulating MMAs of one thread, and of two
+// with a barrier between tcgen05 fences, and promises nothing about these.)
 //
 // Roles (416 threads per CTA): warps 0-7 drain and epilogue (warp w: TMEM
 // lanes 32(w%4)..+31 of the CTA's own TMEM, accumulator columns 80(w/4)..+79),

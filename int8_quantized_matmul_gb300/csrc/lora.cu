@@ -9,12 +9,13 @@
 // Precision. 16-bit operands go to the tensor cores as they are. F32 rows of x,
 // and then t, are cut into three parts of 8 bits that bf16 holds (high bits first, each cut
 // and each remainder exact), all 24 bits. With 16-bit rows t has two parts, rounded: 18 bits in bf16,
-// and 22 in f16 after a row is scaled by a power of two into its range. Small parts are
+// and 22 in f16 after a row is scaled by a power of two into its range: 2^-18 and 2^-22 of its absolute sum, a
+// thousandth of the half step that out is rounded by, and a third part would be half as many MMAs again. Small parts are
 // multiplied first.
 //
-// Measured (one GB300): 8000 F32 rows of 12 adapters, rank 64, 2048 x 2048: 63.4 us, of which the inner product 31 (10 of
-// DRAM and 10 of MMAs; 250 registers leave 8 warps per SM, and 262 CTAs are two waves) and the outer 34 (3.9 TB/s);
-// 5003 bf16 rows, rank 8, 8960 x 1536: 38 us; 64 rows of 40 adapters: 10.0 us, two launches, each with five loads that wait for
+// Measured (one GB300): 8000 F32 rows of 12 adapters, rank 64, 2048 x 2048: 64-66 us, of which the inner product 32 (10 of
+// DRAM and 10 of MMAs; 254 registers leave 8 warps per SM, and 262 CTAs are two waves) and the outer 34 (3.9 TB/s);
+// 5003 bf16 rows, rank 8, 8960 x 1536, three in ten without an adapter: 38-41 us, all with one 52; 64 rows of 40 adapters: 9.8 us, two launches, each with five loads that wait for
 // each other (starts, list, values). Both products in one CTA per 32 rows gave 61.9 us and was slower with fewer rows.
 //
 // Both are meant to be bound by memory: x, base and out pass once. The MMAs (m16n8k16) take their
