@@ -745,11 +745,13 @@ class _Kv8Call:
         self._hold = args
         self._device, self._stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
 
+    def _here(self):
+        if self._device() != self._index:
+            raise ValueError(f"{self._name}: its tensors are on cuda:{self._index}, not on the current device")
+
     def __call__(self):
-        index = self._index
-        if self._device() != index:
-            raise ValueError(f"{self._name}: its tensors are on cuda:{index}, not on the current device")
-        rc = self._fn(*self._args, self._stream(index))
+        self._here()
+        rc = self._fn(*self._args, self._stream(self._index))
         if rc != 0:
             raise I2SError(self._name, rc)
 
@@ -1087,7 +1089,8 @@ class W8A8Experts(_Kv8Call):
                    y_group, flags, _dptr(self.ws), self.ws.numel())
 
     def check(self):
-        """Raises if a wait of the latest call ran out; waits for the current stream."""
+        """Raises if a wait of the latest call ran out; waits for the current stream, as a call on the tensors' device."""
+        self._here()
         _check("w8a8_mul_mat_experts", read_status(self.ws))
 
 

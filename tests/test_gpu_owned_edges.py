@@ -430,3 +430,16 @@ def test_lora_rows_that_are_not_finite_stay_alone(i2s):
         fine = torch.ones(rows, dtype=torch.bool)
         fine[bad] = False
         assert (out.cpu()[fine] == 16 * K).all() and torch.isnan(out.cpu()[~fine]).all()
+
+
+def test_experts_status_on_another_device_is_refused(i2s):
+    """A check while another device is current would wait for that device's stream and read too early."""
+    wq, bscale = torch.ones((2, 32, 16), dtype=torch.int8, device="cuda"), torch.ones((2, 32), device="cuda")
+    plan = i2s.route_plan(torch.zeros(3, dtype=torch.int32, device="cuda"), 2)
+    call = i2s.W8A8Experts(wq, bscale, plan, torch.ones((3, 16), device="cuda"))
+    call()
+    call.check()
+    call._index += 1   # as if its tensors were on the next device
+    for use in (call, call.check):
+        with pytest.raises(ValueError, match="not on the current device"):
+            use()
