@@ -33,7 +33,7 @@
 // finishes one of two neighbouring rows after one exchange.
 //
 // Measured (one GB300). Few rows per expert: 64 tokens over 8 of 128 experts, 1536 x 2048, 51-54 us, 289 MB of weights
-// in use. Many: 4096 bf16 rows of the same 228 us (rows 35, products 187); 1777 F32 rows over 2 of 8, 1536 x 8960: 127 us (rows 32,
+// in use. Many: 4096 bf16 rows of the same 226-232 us (rows 35, products 187); 1777 F32 rows over 2 of 8, 1536 x 8960: 128 us (rows 32,
 // products 90, sums 10, each alone), on the SMs with most units 2.5 for each. A stage of 112 rows takes 840 to
 // 940 cycles for 450 of MMAs: shared memory moves about 740 cycles' worth (16 KB of weights in and out, 28 KB of rows in and
 // to the MMA), and without any one of rows, weights, TMEM stores, MMAs or stores of y it takes 94 % or more of the time. CTA
@@ -84,12 +84,15 @@ struct Shape {
     static constexpr int kSlots = ROWS == 32 ? 6 : 4;      // operands: rows, and weights in TMEM
     static constexpr int kWSlots = ROWS == 32 ? 10 : 4;    // weights as bytes
     // An accumulation reads what it adds to, and nothing orders the MMAs of two threads but a barrier between tcgen05
-    // fences. Few rows: each issuer has an accumulator of its own, and the epilogue adds the two (as fast as one for both).
-    // Many: TMEM has no room for that, and an issuer begins its stage when the other has issued the stage before
-    // (prompts 228 and 127 us; one issuer 248 and 139; an accumulator of each, taken into registers before the next chunk,
-    // 233 and 138; both into one without an order 221 and 124, exact in every comparison, but promised by nothing).
-    static constexpr bool kTurns = ROWS != 32;
-    static constexpr int kAcc = kTurns ? ROWS : kIssuers * ROWS;   // TMEM columns of a chunk's sums
+    // fences. Where the columns of a chunk's sums hold a unit's rows twice, each issuer has an accumulator of its own, and the
+    // epilogue adds the two. More rows: an issuer begins its stage when the other has issued the stage before. Both into one
+    // accumulator without an order is exact in every comparison, but promised by nothing; it took 52.7 us for 64 tokens of 8 of
+    // 128 (52.7 so), 10.9 for 41 of 3 of 4 experts, 2667 x 2000 (11.3; all by turns 12.2), 16.5 for 100 of 2 of 4, 2048 x 4096
+    // (19.2), prompts 214 and 124 (226 and 128; one issuer 248 and 139; an accumulator of each, taken into registers before the
+    // next chunk, 233 and 138).
+    static constexpr int kAcc = ROWS == 32 ? 64 : ROWS;    // TMEM columns of a chunk's sums
+    static constexpr bool kTurns = kAcc < 2 * ROWS;        // whether there are units with more
+    __device__ static bool own(int rows) { return !kTurns || rows <= kAcc / 2; }
     // Rows come in one copy per stage, as two atoms of 64 positions, of one to four times kBox rows.
     static constexpr int kBox = ROWS / 4;
     __device__ static int boxes(int rows) { return (rows + kBox - 1) / kBox; }
@@ -209,6 +212,26 @@ __device__ __forceinline__ void expect_bytes(uint32_t lead, uint32_t bar, uint32
         "@q mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n"
         "}\n" ::"r"(bar), "r"(bytes), "r"(lead)
         : "memory");
+}
+
+// Eight columns at b added to those at a and left zero (f32).
+__device__ __forceinline__ void add_columns8(uint32_t a, uint32_t b) {
+    uint32_t v[8], u[8];
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+                 : "r"(a)
+                 : "memory");
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7])
+                 : "r"(b)
+                 : "memory");
+    tc::tmem_ld_wait();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __float_as_uint(__fadd_rn(__uint_as_float(v[i]), __uint_as_float(u[i])));
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(a), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%1,%1,%1,%1,%1,%1,%1};" ::"r"(b), "r"(0u) : "memory");
 }
 
 // Codes 0, 1 (SEL 0x4140) or 2, 3 (0x4342) of four biased by 128, as f16:
@@ -386,17 +409,23 @@ __global__ void __launch_bounds__(xp::kThreads, 1) k_experts(const __grid_consta
                 if (!tc::mbar_wait(&S.dfull[chunk_at & 1], (uint32_t)(chunk_at >> 1) & 1, abort_flag, kWait)) { fail(); ok = false; }
                 ok = __all_sync(0xffffffffu, ok) != 0;
                 tc::tc_fence_after();
-                return tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)((chunk_at & 1) * S_::kAcc + c0);
+                const uint32_t d = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)((chunk_at & 1) * S_::kAcc + c0);
+                if (S_::kTurns && S_::own(t.rows) && ok) {   // the second issuer's to the first's, eight at a time (registers)
+#pragma unroll 1
+                    for (int i = 0; i < 16 * pieces; i += 8) add_columns8(d + (uint32_t)i, d + (uint32_t)(S_::kAcc / 2 + i));
+                    tc::tmem_st_wait();
+                }
+                return d;
             };
-            // 16 columns of its sums, with two issuers both parts added (whole numbers, exact); they are left zero, the first
-            // part where `zero` says so
+            // 16 columns of its sums, with few rows both issuers' added (whole numbers, exact); they are left zero, the first
+            // where `zero` says so
             auto take = [&](uint32_t d, uint32_t (&v)[16], bool zero) {
                 tc::tmem_ld_32x32b_x16(d, v);
                 if constexpr (!S_::kTurns) {
                     uint32_t u[16];
-                    tc::tmem_ld_32x32b_x16(d + ROWS, u);
+                    tc::tmem_ld_32x32b_x16(d + S_::kAcc / 2, u);
                     tc::tmem_ld_wait();
-                    tc::tmem_st_zero_32x32b_x16(d + ROWS);
+                    tc::tmem_st_zero_32x32b_x16(d + S_::kAcc / 2);
 #pragma unroll
                     for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__fadd_rn(__uint_as_float(v[i]), __uint_as_float(u[i])));
                 } else {
@@ -634,9 +663,10 @@ __global__ void __launch_bounds__(xp::kThreads, 1) k_experts(const __grid_consta
                 if (rows == 0) break;
                 const uint32_t atom = (uint32_t)S_::boxes(rows) * (S_::kBox * 128);   // bytes
                 const uint32_t idesc = tc::idesc_f16_f32(kChannels, (rows + 15) / 16 * 16);
+                const bool own = S_::own(rows);
                 for (int k0 = 0; ok && k0 < steps; k0 += kChunkSteps, ++chunk_at) {
                     const int buf = chunk_at & 1, k1 = min(steps, k0 + kChunkSteps);
-                    const uint32_t d = tm + (uint32_t)(buf * S_::kAcc + (S_::kTurns ? 0 : me * ROWS));
+                    const uint32_t d = tm + (uint32_t)(buf * S_::kAcc + (own ? me * (S_::kAcc / 2) : 0));
                     ok = wait(&S.dempty[buf], ((uint32_t)(chunk_at >> 1) & 1) ^ 1);
                     for (int k = k0; ok && k < k1; ++k, ++at) {
                         if (at % kIssuers != me) continue;
@@ -651,6 +681,7 @@ __global__ void __launch_bounds__(xp::kThreads, 1) k_experts(const __grid_consta
                         ok = __all_sync(0xffffffffu, got) != 0;
                         if (!ok) break;
                         tc::tc_fence_after();
+                        if (S_::kTurns && own) arrive_from(lead, &S.turn[me ^ 1]);
                         if (left >= 8) {
 #pragma unroll
                             for (int j = 0; j < 8; ++j)
@@ -659,7 +690,7 @@ __global__ void __launch_bounds__(xp::kThreads, 1) k_experts(const __grid_consta
                             for (int j = 0; j < left; ++j)
                                 mma(lead, d, op + 8u * j, bd + (uint64_t)((j >> 2) * (atom >> 4) + 2 * (j & 3)), idesc);
                         }
-                        if (S_::kTurns) {
+                        if (S_::kTurns && !own) {
                             tc::tc_fence_before();
                             arrive_from(lead, &S.turn[me ^ 1]);
                         }
