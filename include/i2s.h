@@ -811,8 +811,8 @@ int route_plan_build(const int32_t* owner, const route_plan* plan, void* ws, siz
  *   with ROUTE_BIAS_SCORE p + bias[e], where p is what the expert counts for without a bias: the softmax over all the row's
  *       logits, or with ROUTE_SIGMOID 1 / (1 + exp(-l)), in the steps of the weights below. THIS is the choice of routers that
  *       are trained with a balancing bias (auxiliary-loss-free load balancing): logit + bias[e] chooses other experts there,
- *       and nothing reports it. Two scores closer than the steps' roundings (about 2^-21 of p, more where a softmax has
- *       many or far logits) may come in either order. Without a bias the flag changes nothing.
+ *       and nothing reports it. Two scores closer than the steps' roundings (about 2^-20 of p, more where a softmax has
+ *       many or far logits, and 2^-24 of the scores) may come in either order. Without a bias the flag changes nothing.
  * The weights have no bias in either case. Item row*k + j is the row's j-th choice, expert[row*k + j]
  * (device int32) its expert and weight[row*k + j] (device F32) its weight: factor times
  *   exp(l - m) / sum_e exp(l_e - m), the softmax over all the row's logits (without the

@@ -1044,8 +1044,8 @@ int w8a8_mul_mat_experts(const w8a8_experts* w, const route_plan* plan, const i2
         mapped = encode_tensor_map(&a.wmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, w->wq, dims, strides, box);
     }
     // Row tiles there may be: no more than one per expert and one per `rows` items.
-    // Few rows per expert take the shape for few (64 experts of 1536 x 2048, 8 items to an expert: 37.5 us, 42.7 in the other;
-    // 16: 43.7 and 45.8; 24: 48.7 and 47.9; 64: 83.2 and 61.5).
+    // Few rows per expert take the shape for few (64 experts of 1536 x 2048, 8 items to an expert: 39.9 us, 43.0 in the other;
+    // 16: 42.8 and 44.9; 24: 47.0 and 46.6; 48: 63.5 and 55.5. 8 of 4096 x 1536: 16 14.1 and 14.8, 20 17.5 and 15.3).
     const bool few = items <= 16 * (int64_t)w->experts;
     const int rows = few ? 32 : 128;
     // (position of a block of 64, row, block): the last block may reach into the next row, or past the last into

@@ -443,3 +443,37 @@ def test_experts_status_on_another_device_is_refused(i2s):
     for use in (call, call.check):
         with pytest.raises(ValueError, match="not on the current device"):
             use()
+
+
+# -- rows whose places pass 32 bits --------------------------------------------------------------------
+
+def test_rows_far_apart(i2s):
+    """Row tensors that reach over more than 2^31 elements: slices of rows 32768 apart, the last of 70001 as right as the first."""
+    rows, far, E, N, K = 70001, 32768, 4, 32, 32
+    frames = [torch.empty((rows, far), dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    g = torch.Generator(device="cuda").manual_seed(3)
+    whole = lambda *shape, low, high: torch.randint(low, high, shape, device="cuda", generator=g).float()
+    logits, x, out = frames[0][:, 1024:1024 + E], frames[0][:, :K], frames[1][:, 64:64 + N]
+    logits.copy_(torch.rand((rows, E), device="cuda", generator=g).argsort(1))   # no two alike
+    expert, weight, plan = i2s.route_topk(logits, 2, norm=True)
+    own = logits.float().argmax(1)
+    assert torch.equal(expert[:, 0].long(), own) and (weight[:, 0] - 1 / (1 + np.exp(-1.0))).abs().max() < 1e-6
+    assert plan.start[-1] == 2 * rows
+    one = i2s.route_plan(expert[:, 0].contiguous(), E)
+    # experts: codes are the values where the largest of a row is 127
+    x.copy_(whole(rows, K, low=-100, high=101))
+    x[:, 0] = 127
+    wq, ones = whole(E, N, K, low=-2, high=3).to(torch.int8), torch.ones((E, N), device="cuda")
+    out.fill_(0)
+    i2s.w8a8_mul_mat_experts(wq, ones, one, x, out=out)
+    want = torch.einsum("rk,rnk->rn", x.float(), wq.float()[own])
+    assert torch.equal(out, want.bfloat16())
+    # adapters, in place
+    A, B = whole(E, 8, K, low=-1, high=2).bfloat16(), whole(E, N, 8, low=-1, high=2).bfloat16()
+    x.copy_(whole(rows, K, low=-2, high=3))
+    base = whole(rows, N, low=-9, high=10)
+    out.copy_(base)
+    i2s.lora_add(A, B, one, x, out)
+    t = torch.einsum("rk,rak->ra", x.float(), A.float()[own])
+    want = base + torch.einsum("ra,rna->rn", t, B.float()[own])
+    assert torch.equal(out, want.bfloat16())
